@@ -71,7 +71,8 @@ typedef enum zero_status {
 
 typedef enum zero_dtype {
   ZERO_FP16 = 0,     /* IEEE binary16 */
-  ZERO_BF16 = 1      /* bfloat16 */
+  ZERO_BF16 = 1,     /* bfloat16 */
+  ZERO_FP32 = 2      /* IEEE binary32, where a call says it takes it */
 } zero_dtype;
 
 typedef struct zero_opt_handle* zero_opt_t;

@@ -19,6 +19,7 @@ from . import _build
 
 FP16 = 0
 BF16 = 1
+FP32 = 2      # where a call says it takes it
 
 ZERO_OK, ZERO_EINVAL, ZERO_ERANGE, ZERO_ENOMEM, ZERO_ECUDA, ZERO_ENOTSUP = range(6)
 
@@ -90,6 +91,24 @@ class zero_opt_ckpt_info(ctypes.Structure):
                 ("real_len", _i64), ("scaler", zero_opt_scaler_state)]
 
 
+class zero_qk_config(ctypes.Structure):
+    _fields_ = [("q_heads", _i32), ("k_heads", _i32), ("head_dim", _i32), ("rotary_dim", _i32),
+                ("dtype", _i32), ("interleaved", _i32), ("gain_per_head", _i32),
+                ("reserved", _i32), ("eps", _f64)]
+
+
+class zero_qk_tensor(ctypes.Structure):
+    _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
+
+
+class zero_qk_buffers(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("n_pos", _i64), ("q", zero_qk_tensor), ("k", zero_qk_tensor),
+                ("q_out", zero_qk_tensor), ("k_out", zero_qk_tensor), ("dq", zero_qk_tensor),
+                ("dk", zero_qk_tensor), ("q_gain", _vp), ("k_gain", _vp), ("dq_gain", _vp),
+                ("dk_gain", _vp), ("cos", _vp), ("sin", _vp), ("positions", _vp),
+                ("positions64", _i32), ("reserved", _i32)]
+
+
 class ZeroOptError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         super().__init__(f"{where}: status {status}: {message}")
@@ -143,6 +162,11 @@ SIGNATURES = [
     ("zero_host_loss_scale", _i32, [_vp, _i32, _P(zero_opt_scaler_state)]),
     ("zero_host_set_loss_scale", _i32, [_vp, _i32, _P(zero_opt_scaler_state)]),
     ("zero_host_last_step", _i32, [_vp, _P(zero_opt_step_info)]),
+    ("zero_qk_create", _i32, [_P(zero_qk_config), _P(_vp)]),
+    ("zero_qk_destroy", _i32, [_vp]),
+    ("zero_qk_norm_rope", _i32, [_vp, _P(zero_qk_buffers), _vp]),
+    ("zero_qk_norm_rope_backward", _i32, [_vp, _P(zero_qk_buffers), _vp]),
+    ("zero_qk_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_opt_status_string", ctypes.c_char_p, [_i32]),
     ("zero_opt_last_error", ctypes.c_char_p, []),
 ]
@@ -603,3 +627,121 @@ def zero_host_last_step(h) -> zero_opt_step_info:
     out = zero_opt_step_info()
     _check(lib().zero_host_last_step(h, ctypes.byref(out)), "zero_host_last_step")
     return out
+
+
+# ---------------------------------------------------------------- query/key norm and rotation
+
+# Shapes a handle was made for, so that the binding can check tensors against them.
+_qk_configs = {}
+
+
+def make_qk_config(q_heads, k_heads, head_dim, rotary_dim=None, dtype=BF16, interleaved=False,
+                   eps=1e-6, gain_per_head=False) -> zero_qk_config:
+    """`rotary_dim` None: the whole head rotates.  `dtype` FP16, BF16 or FP32."""
+    return zero_qk_config(q_heads, k_heads, head_dim,
+                          head_dim if rotary_dim is None else rotary_dim, dtype,
+                          int(interleaved), int(gain_per_head), 0, eps)
+
+
+def zero_qk_create(cfg: zero_qk_config) -> int:
+    h = _vp()
+    _check(lib().zero_qk_create(ctypes.byref(cfg), ctypes.byref(h)), "zero_qk_create")
+    import torch
+    dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
+    _qk_configs[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
+                            bool(cfg.gain_per_head))
+    return h.value
+
+
+def zero_qk_destroy(h) -> None:
+    _qk_configs.pop(h, None)
+    _check(lib().zero_qk_destroy(h), "zero_qk_destroy")
+
+
+def _qk_bad(name, what):
+    raise ValueError(f"{name} must be {what}")
+
+
+def _qk_data(t, name, shape, dtype, device):
+    if t.dtype != dtype or t.shape != shape or t.device != device or \
+            (t.stride(2) != 1 and shape[2] > 1):
+        _qk_bad(name, f"a {dtype} tensor of {tuple(shape)} on {device} with contiguous heads")
+    return zero_qk_tensor(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _qk_gain(t, name, heads, dim, per_head, device):
+    import torch
+    shape = (heads, dim) if per_head else (dim,)
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
+        _qk_bad(name, f"a contiguous float32 tensor of {shape} on {device}")
+    return t.data_ptr()
+
+
+def _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions):
+    import torch
+    if h not in _qk_configs:
+        raise ValueError("not a handle of zero_qk_create")
+    hq, hk, dim, half, dtype, per_head = _qk_configs[h]
+    if not q.is_cuda or q.device.index != torch.cuda.current_device():
+        raise ValueError("q must be a CUDA tensor of the current device")
+    dev, n = q.device, q.shape[0]
+    b = zero_qk_buffers()
+    b.tokens = n
+    b.q = _qk_data(q, "q", (n, hq, dim), dtype, dev)
+    if hk:
+        b.k = _qk_data(k, "k", (n, hk, dim), dtype, dev)
+    if q_gain is not None:
+        b.q_gain = _qk_gain(q_gain, "q_gain", hq, dim, per_head, dev)
+    if k_gain is not None and hk:
+        b.k_gain = _qk_gain(k_gain, "k_gain", hk, dim, per_head, dev)
+    if half:
+        for name, t in (("cos", cos), ("sin", sin)):
+            if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != half or t.device != dev \
+                    or not t.is_contiguous():
+                _qk_bad(name, f"a contiguous float32 tensor of (positions, {half}) on {dev}")
+        if cos.shape != sin.shape:
+            raise ValueError("cos and sin must have the same shape")
+        b.n_pos, b.cos, b.sin = cos.shape[0], cos.data_ptr(), sin.data_ptr()
+    if positions.shape != (n,) or positions.device != dev or not positions.is_contiguous() or \
+            positions.dtype not in (torch.int64, torch.int32):
+        _qk_bad("positions", f"a contiguous int64 or int32 tensor of ({n},) on {dev}")
+    b.positions, b.positions64 = positions.data_ptr(), int(positions.dtype == torch.int64)
+    return b, (n, hq, dim), (n, hk, dim), dtype, dev, per_head
+
+
+def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions,
+                      stream=None) -> None:
+    """Normalise and rotate every head of `q` [tokens, q_heads, D] and `k` into
+    `q_out` and `k_out` (which may be `q` and `k`).  `k`, `k_out` are not looked
+    at by a handle with k_heads 0; a gain may be None (ones).  A token of
+    position -1 is padding and gets zeros."""
+    b, sq, sk, dtype, dev, _ = _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions)
+    b.q_out = _qk_data(q_out, "q_out", sq, dtype, dev)
+    if sk[1]:
+        b.k_out = _qk_data(k_out, "k_out", sk, dtype, dev)
+    _check(lib().zero_qk_norm_rope(h, ctypes.byref(b), _stream(stream)), "zero_qk_norm_rope")
+
+
+def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain, q_gain, k_gain,
+                               cos, sin, positions, stream=None) -> None:
+    """Gradients of `zero_qk_norm_rope`: from `dq_out`, `dk_out` and the
+    forward call's inputs into `dq`, `dk` (which may be `dq_out`, `dk_out`) and
+    the gains' float32 gradients (None: not wanted)."""
+    b, sq, sk, dtype, dev, per_head = _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions)
+    b.q_out = _qk_data(dq_out, "dq_out", sq, dtype, dev)
+    b.dq = _qk_data(dq, "dq", sq, dtype, dev)
+    if sk[1]:
+        b.k_out = _qk_data(dk_out, "dk_out", sk, dtype, dev)
+        b.dk = _qk_data(dk, "dk", sk, dtype, dev)
+        if dk_gain is not None:
+            b.dk_gain = _qk_gain(dk_gain, "dk_gain", sk[1], sk[2], per_head, dev)
+    if dq_gain is not None:
+        b.dq_gain = _qk_gain(dq_gain, "dq_gain", sq[1], sq[2], per_head, dev)
+    _check(lib().zero_qk_norm_rope_backward(h, ctypes.byref(b), _stream(stream)),
+           "zero_qk_norm_rope_backward")
+
+
+def zero_qk_launch_count(h) -> int:
+    out = _i64()
+    _check(lib().zero_qk_launch_count(h, ctypes.byref(out)), "zero_qk_launch_count")
+    return out.value

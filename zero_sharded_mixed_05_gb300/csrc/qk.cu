@@ -1,0 +1,548 @@
+// qk.cu -- each head's query and key normalised and rotated in one pass
+// (zero_qk.h), forward and backward.
+//
+// What bounds it: memory.  A row (one token's one head) is read once, its mean
+// square reduced in registers by a few lanes, and written once; the backward
+// pass reads the row and its output's gradient and writes the row's gradient.
+// Nothing else of size is moved: angles and gains are a few hundred bytes a
+// token and stay in L1.
+//
+// Layout: a row is owned by a group of lanes, each holding two vectors of V
+// numbers, chosen so that both members of every rotated pair are in the same
+// lane: without interleaving the vectors are V numbers of the first rotated
+// half and the V numbers they pair with; interleaved they are 2V numbers in a
+// row.  So the rotation needs no exchange between lanes, and a 16-byte load
+// per vector covers whole sectors.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <new>
+
+#include "host_util.h"
+#include "zero_qk.h"
+
+namespace {
+
+using zo::fail;
+
+constexpr int kQkThreads = 256;
+constexpr int kMaxDim = 512;
+
+struct Rows {
+  const char* in;      // x
+  const char* gout;    // backward: gradient of the result
+  char* out;           // forward: result; backward: dx
+  int64_t in_t, in_h, go_t, go_h, out_t, out_h;   // strides in elements
+  const float* gain;
+  int32_t heads;
+};
+
+struct QkArgs {
+  Rows r[2];           // queries, keys
+  const float* cos;
+  const float* sin;
+  const void* pos;
+  int64_t tokens, n_pos;
+  float* part;         // backward: [grid][rows a CTA][D] partial gain gradients
+  int32_t pos64, dim, rot, chunks, lanes, gain_per_head;
+  int32_t heads;       // of both
+  int32_t head_blocks; // CTAs side by side over the heads
+  int32_t reps;        // tokens a CTA takes at once when its heads are few
+  int32_t part_rows;   // rows of a CTA's partial: 2 (shared gains) or its heads
+  float eps, inv_dim;
+};
+
+template <typename T> struct Num;
+template <> struct Num<__half> {
+  static __device__ float get(__half x) { return __half2float(x); }
+  static __device__ __half put(float x) { return __float2half_rn(x); }
+};
+template <> struct Num<__nv_bfloat16> {
+  static __device__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+};
+template <> struct Num<float> {
+  static __device__ float get(float x) { return x; }
+  static __device__ float put(float x) { return x; }
+};
+
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const char* base, int64_t e) {
+  return *reinterpret_cast<const Vec<T, V>*>(reinterpret_cast<const T*>(base) + e);
+}
+
+// Where the two vectors of chunk c start.
+template <int V, bool kInter>
+__device__ __forceinline__ void places(const QkArgs& a, int c, int* p0, int* p1) {
+  if (kInter || c * 2 * V >= a.rot) {
+    *p0 = c * 2 * V;
+    *p1 = *p0 + V;
+  } else {
+    *p0 = c * V;
+    *p1 = a.rot / 2 + c * V;
+  }
+}
+
+__device__ __forceinline__ int64_t position(const QkArgs& a, int64_t t) {
+  return a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + t)
+                 : (int64_t)__ldg(static_cast<const int*>(a.pos) + t);
+}
+
+// The rotation of one chunk (dir +1) or its inverse (dir -1).  x holds the
+// chunk's two vectors one after the other.
+template <int V, bool kInter>
+__device__ __forceinline__ void turn(float* x, const float* cs, const float* sn, float dir) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int iu = kInter ? 2 * i : i, iv = kInter ? 2 * i + 1 : V + i;
+    const float u = x[iu], v = x[iv], s = dir * sn[i];
+    x[iu] = __fmaf_rn(u, cs[i], -__fmul_rn(v, s));
+    x[iv] = __fmaf_rn(v, cs[i], __fmul_rn(u, s));
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_f(const float* p, float* x) {
+  const Vec<float, (V < 4 ? V : 4)>* q = reinterpret_cast<const Vec<float, (V < 4 ? V : 4)>*>(p);
+#pragma unroll
+  for (int i = 0; i < V / (V < 4 ? V : 4); ++i) {
+    const Vec<float, (V < 4 ? V : 4)> y = q[i];
+#pragma unroll
+    for (int j = 0; j < (V < 4 ? V : 4); ++j) x[i * 4 + j] = y.v[j];
+  }
+}
+
+// V numbers a vector, C chunks a lane.  A group of a.lanes lanes owns one head
+// for the whole launch (its gain stays in registers) and walks the tokens.
+template <typename T, int V, int C, bool kInter, bool kBackward>
+__global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ QkArgs a) {
+  extern __shared__ float s_part[];
+  const int lanes = a.lanes, groups = kQkThreads / lanes;
+  const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  // the group's lanes of its warp: groups of one warp walk on by themselves
+  const unsigned mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u)
+                        << (threadIdx.x % 32 / lanes * lanes);
+  const int block = blockIdx.x % a.head_blocks;
+  const int per = min(groups, a.heads);       // heads side by side in a CTA
+  const int rep = group / per;
+  const int head = block * per + group % per;
+  const bool on = rep < a.reps && head < a.heads;
+  const int which = on && head >= a.r[0].heads ? 1 : 0;
+  const Rows& r = a.r[which];
+  const int h = head - (which ? a.r[0].heads : 0);
+  const int64_t slots = (int64_t)(gridDim.x / a.head_blocks) * a.reps;
+
+  float gain[C][2 * V], dgain[C][2 * V];
+  int p0[C], p1[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const int c = lane + j * lanes;
+    places<V, kInter>(a, min(c, a.chunks - 1), &p0[j], &p1[j]);
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) {
+      gain[j][i] = 1.0f;
+      dgain[j][i] = 0.0f;
+      if (on && r.gain && c < a.chunks)
+        gain[j][i] = __ldg(r.gain + (a.gain_per_head ? (int64_t)h * a.dim : 0) +
+                           (i < V ? p0[j] + i : p1[j] + i - V));
+    }
+  }
+
+  if (on)
+    for (int64_t t = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep; t < a.tokens; t += slots) {
+      const int64_t p = position(a, t);
+      const int64_t o_out = t * r.out_t + (int64_t)h * r.out_h;
+      if (p < 0 || (p >= a.n_pos && a.rot > 0)) {
+        // padding, or no angle for this position: no row and no table is read
+        const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          if (lane + j * lanes >= a.chunks) continue;
+          Vec<T, V> w;
+#pragma unroll
+          for (int i = 0; i < V; ++i) w.v[i] = fill;
+          *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p0[j]) = w;
+          *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p1[j]) = w;
+          if (kBackward && p >= 0)
+#pragma unroll
+            for (int i = 0; i < 2 * V; ++i) dgain[j][i] = __int_as_float(0x7fffffff);
+        }
+        continue;
+      }
+      const int64_t o_in = t * r.in_t + (int64_t)h * r.in_h;
+      float x[C][2 * V], g[C][2 * V], cs[C][V], sn[C][V];
+      float sq = 0.0f, dot = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int c = lane + j * lanes;
+        const bool live = c < a.chunks, turned = live && c * 2 * V < a.rot;
+        if (live) {
+          const Vec<T, V> u = load<T, V>(r.in, o_in + p0[j]), v = load<T, V>(r.in, o_in + p1[j]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            x[j][i] = Num<T>::get(u.v[i]);
+            x[j][V + i] = Num<T>::get(v.v[i]);
+          }
+          if (kBackward) {
+            const int64_t o_g = t * r.go_t + (int64_t)h * r.go_h;
+            const Vec<T, V> y = load<T, V>(r.gout, o_g + p0[j]), z = load<T, V>(r.gout, o_g + p1[j]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              g[j][i] = Num<T>::get(y.v[i]);
+              g[j][V + i] = Num<T>::get(z.v[i]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) x[j][i] = g[j][i] = 0.0f;
+        }
+        if (turned) {
+          load_f<V>(a.cos + p * (a.rot / 2) + c * V, cs[j]);
+          load_f<V>(a.sin + p * (a.rot / 2) + c * V, sn[j]);
+          if (kBackward) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          sq = __fmaf_rn(x[j][i], x[j][i], sq);
+          if (kBackward) dot = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), x[j][i], dot);
+        }
+      }
+      for (int o = lanes >> 1; o > 0; o >>= 1) {
+        sq = __fadd_rn(sq, __shfl_xor_sync(mask, sq, o));
+        if (kBackward) dot = __fadd_rn(dot, __shfl_xor_sync(mask, dot, o));
+      }
+      const float inv = rsqrtf(__fmaf_rn(sq, a.inv_dim, a.eps));
+      const float back = kBackward ? __fmul_rn(__fmul_rn(inv, __fmul_rn(inv, inv)),
+                                               __fmul_rn(dot, a.inv_dim)) : 0.0f;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int c = lane + j * lanes;
+        if (c >= a.chunks) continue;
+        float y[2 * V];
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) {
+          if (kBackward) {
+            dgain[j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[j][i]);
+            y[i] = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), inv, -__fmul_rn(x[j][i], back));
+          } else {
+            y[i] = __fmul_rn(__fmul_rn(x[j][i], inv), gain[j][i]);
+          }
+        }
+        if (!kBackward && c * 2 * V < a.rot) turn<V, kInter>(y, cs[j], sn[j], 1.0f);
+        Vec<T, V> u, v;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          u.v[i] = Num<T>::put(y[i]);
+          v.v[i] = Num<T>::put(y[V + i]);
+        }
+        *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p0[j]) = u;
+        *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p1[j]) = v;
+      }
+    }
+
+  if (kBackward && a.part) {
+    // The CTA's share of the gains' gradients: each group's sums to shared
+    // memory, then each column added over the groups of one gain in order.
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if (lane + j * lanes >= a.chunks) continue;
+#pragma unroll
+      for (int i = 0; i < 2 * V; ++i)
+        s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on ? dgain[j][i] : 0.0f;
+    }
+    __syncthreads();
+    float* to = a.part + (int64_t)blockIdx.x * a.part_rows * a.dim;
+    for (int e = threadIdx.x; e < a.part_rows * a.dim; e += kQkThreads) {
+      const int row = e / a.dim, d = e % a.dim;
+      float s = 0.0f;
+      for (int k = 0; k < groups; ++k) {
+        const int hd = block * per + k % per;
+        const int mine = a.gain_per_head ? k % per : (hd >= a.r[0].heads ? 1 : 0);
+        if (mine == row) s = __fadd_rn(s, s_part[k * a.dim + d]);
+      }
+      to[e] = s;
+    }
+  }
+}
+
+struct FoldArgs {
+  const float* part;
+  float* out[2];
+  int32_t grid, head_blocks, part_rows, per, dim, q_heads, heads, gain_per_head;
+};
+
+// Sums the CTAs' partial gain gradients in index order: 32 columns a CTA, 8
+// threads a column, each over every eighth partial.
+__global__ void __launch_bounds__(256) qk_fold_kernel(const FoldArgs a) {
+  __shared__ float s[8][33];
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
+  const int rows = a.gain_per_head ? a.heads : 2;
+  const int row = col / a.dim, d = col % a.dim;
+  float sum = 0.0f;
+  if (row < rows) {
+    const int step = a.gain_per_head ? a.head_blocks : 1;
+    const int first = a.gain_per_head ? row / a.per : 0;
+    const int local = a.gain_per_head ? row % a.per : row;
+    for (int c = first + part * step; c < a.grid; c += 8 * step)
+      sum = __fadd_rn(sum, a.part[((int64_t)c * a.part_rows + local) * a.dim + d]);
+  }
+  s[part][threadIdx.x % 32] = sum;
+  __syncthreads();
+  if (part == 0 && row < rows) {
+    for (int k = 1; k < 8; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
+    const int which = a.gain_per_head ? (row >= a.q_heads) : row;
+    const int at = a.gain_per_head ? row - (which ? a.q_heads : 0) : 0;
+    if (a.out[which]) a.out[which][(int64_t)at * a.dim + d] = sum;
+  }
+}
+
+bool fits(const void* p, int64_t s0, int64_t s1, int bytes, int esize) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && s0 * esize % bytes == 0 &&
+         s1 * esize % bytes == 0;
+}
+
+template <typename T, bool kInter, bool kBackward>
+const void* kernel_for(int v) {
+  if constexpr (sizeof(T) == 2)
+    if (v == 8) return (const void*)qk_kernel<T, 8, 1, kInter, kBackward>;
+  switch (v) {
+    case 4: return (const void*)qk_kernel<T, 4, 2, kInter, kBackward>;
+    case 2: return (const void*)qk_kernel<T, 2, 4, kInter, kBackward>;
+    default: return (const void*)qk_kernel<T, 1, 8, kInter, kBackward>;
+  }
+}
+
+template <typename T>
+const void* kernel_of(bool inter, bool backward, int v) {
+  if (inter) return backward ? kernel_for<T, true, true>(v) : kernel_for<T, true, false>(v);
+  return backward ? kernel_for<T, false, true>(v) : kernel_for<T, false, false>(v);
+}
+
+}  // namespace
+
+struct zero_qk_handle {
+  zero_qk_config cfg;
+  bool has_device = false;
+  int device = -1;
+  int sms = 0;
+  int max_grid = 0;
+  float* part = nullptr;
+  int64_t launches = 0;
+};
+
+namespace {
+
+zero_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(ZERO_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int elem_size(int32_t dtype) { return dtype == ZERO_FP32 ? 4 : 2; }
+
+zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backward) {
+  if (!h) return fail(ZERO_EINVAL, "handle is NULL");
+  if (!b) return fail(ZERO_EINVAL, "buffers are NULL");
+  const zero_qk_config& c = h->cfg;
+  if (b->tokens < 0 || b->n_pos < 0) return fail(ZERO_EINVAL, "tokens and n_pos must be >= 0");
+  const zero_qk_tensor* out[2] = {backward ? &b->dq : &b->q_out, backward ? &b->dk : &b->k_out};
+  const zero_qk_tensor* in[2] = {&b->q, &b->k};
+  const zero_qk_tensor* go[2] = {&b->q_out, &b->k_out};
+  if (b->tokens > 0) {
+    for (int w = 0; w < (c.k_heads > 0 ? 2 : 1); ++w)
+      if (!in[w]->data || !out[w]->data || (backward && !go[w]->data))
+        return fail(ZERO_EINVAL, "a %s tensor is NULL", w ? "key" : "query");
+    if (!b->positions) return fail(ZERO_EINVAL, "positions are NULL");
+    if (c.rotary_dim > 0 && b->n_pos > 0 && (!b->cos || !b->sin))
+      return fail(ZERO_EINVAL, "cos and sin must be non-NULL");
+  }
+  if (!h->has_device) return fail(ZERO_ECUDA, "no CUDA device for this handle");
+  int cur = -1;
+  cudaError_t e = cudaGetDevice(&cur);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (cur != h->device)
+    return fail(ZERO_ECUDA, "current device %d is not the handle's device %d", cur, h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* dgain[2] = {b->dq_gain, c.k_heads > 0 ? b->dk_gain : nullptr};
+  if (b->tokens == 0) {
+    for (int w = 0; backward && w < 2; ++w)
+      if (dgain[w]) {
+        const size_t rows = c.gain_per_head ? (size_t)(w ? c.k_heads : c.q_heads) : 1;
+        e = cudaMemsetAsync(dgain[w], 0, rows * c.head_dim * sizeof(float), s);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+      }
+    return ZERO_OK;
+  }
+
+  QkArgs a = {};
+  a.cos = b->cos;
+  a.sin = b->sin;
+  a.pos = b->positions;
+  a.pos64 = b->positions64;
+  a.tokens = b->tokens;
+  a.n_pos = b->n_pos;
+  a.dim = c.head_dim;
+  a.rot = c.rotary_dim;
+  a.gain_per_head = c.gain_per_head;
+  a.heads = c.q_heads + c.k_heads;
+  a.eps = (float)c.eps;
+  a.inv_dim = 1.0f / (float)c.head_dim;
+  const int es = elem_size(c.dtype);
+  // The widest vector that the head's halves, every address and every stride
+  // are multiples of: 16 bytes a load where all are, single numbers at worst.
+  int v = es == 2 ? 8 : 4;
+  for (; v > 1; v /= 2) {
+    bool ok = c.head_dim % (2 * v) == 0 && c.rotary_dim % (2 * v) == 0;
+    const int fb = std::min(v, 4) * 4;
+    ok = ok && (c.rotary_dim == 0 || (fits(b->cos, 0, 0, fb, 4) && fits(b->sin, 0, 0, fb, 4)));
+    for (int w = 0; ok && w < (c.k_heads > 0 ? 2 : 1); ++w) {
+      ok = fits(in[w]->data, in[w]->token_stride, in[w]->head_stride, v * es, es) &&
+           fits(out[w]->data, out[w]->token_stride, out[w]->head_stride, v * es, es);
+      if (backward)
+        ok = ok && fits(go[w]->data, go[w]->token_stride, go[w]->head_stride, v * es, es);
+    }
+    if (ok) break;
+  }
+  a.chunks = c.head_dim / (2 * v);
+  a.lanes = 1;
+  while (a.lanes < 32 && a.lanes < a.chunks) a.lanes *= 2;
+  for (int w = 0; w < 2; ++w) {
+    Rows& r = a.r[w];
+    r.heads = w ? c.k_heads : c.q_heads;
+    if (r.heads == 0) continue;
+    r.in = static_cast<const char*>(in[w]->data);
+    r.in_t = in[w]->token_stride;
+    r.in_h = in[w]->head_stride;
+    r.out = static_cast<char*>(out[w]->data);
+    r.out_t = out[w]->token_stride;
+    r.out_h = out[w]->head_stride;
+    if (backward) {
+      r.gout = static_cast<const char*>(go[w]->data);
+      r.go_t = go[w]->token_stride;
+      r.go_h = go[w]->head_stride;
+    }
+    r.gain = w ? b->k_gain : b->q_gain;
+  }
+  const int groups = kQkThreads / a.lanes, per = std::min(groups, a.heads);
+  a.head_blocks = (a.heads + per - 1) / per;
+  a.reps = std::max(1, groups / per);
+  a.part_rows = c.gain_per_head ? per : 2;
+  const bool want = backward && (dgain[0] || dgain[1]);
+  a.part = want ? h->part : nullptr;
+  const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, v)
+                   : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, v)
+                                          : kernel_of<float>(c.interleaved, backward, v);
+  const size_t smem = want ? (size_t)groups * c.head_dim * sizeof(float) : 0;
+  const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
+  int64_t grid = slots * a.head_blocks;
+  const int64_t most = std::max<int64_t>(1, h->max_grid / a.head_blocks) * a.head_blocks;
+  if (grid > most) grid = most;
+  void* params[] = {&a};
+  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kQkThreads), params, smem, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+  ++h->launches;
+  if (want) {
+    FoldArgs f = {};
+    f.part = h->part;
+    f.out[0] = dgain[0];
+    f.out[1] = dgain[1];
+    f.grid = (int)grid;
+    f.head_blocks = a.head_blocks;
+    f.part_rows = a.part_rows;
+    f.per = per;
+    f.dim = c.head_dim;
+    f.q_heads = c.q_heads;
+    f.heads = a.heads;
+    f.gain_per_head = c.gain_per_head;
+    const int64_t cols = (int64_t)(c.gain_per_head ? a.heads : 2) * c.head_dim;
+    void* fp[] = {&f};
+    e = cudaLaunchKernel((const void*)qk_fold_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256),
+                         fp, 0, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+    ++h->launches;
+  }
+  return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+zero_status zero_qk_create(const zero_qk_config* cfg, zero_qk_t* out) {
+  if (!out) return fail(ZERO_EINVAL, "out is NULL");
+  *out = nullptr;
+  if (!cfg) return fail(ZERO_EINVAL, "cfg is NULL");
+  if (cfg->q_heads < 1 || cfg->k_heads < 0 || (int64_t)cfg->q_heads + cfg->k_heads > 4096)
+    return fail(ZERO_EINVAL, "q_heads must be >= 1, k_heads >= 0 and both at most 4096 together");
+  if (cfg->head_dim < 2 || cfg->head_dim > kMaxDim || cfg->head_dim % 2)
+    return fail(ZERO_EINVAL, "head_dim must be even and in 2..%d", kMaxDim);
+  if (cfg->rotary_dim < 0 || cfg->rotary_dim > cfg->head_dim || cfg->rotary_dim % 2)
+    return fail(ZERO_EINVAL, "rotary_dim must be even and in 0..head_dim");
+  if (cfg->dtype != ZERO_FP16 && cfg->dtype != ZERO_BF16 && cfg->dtype != ZERO_FP32)
+    return fail(ZERO_EINVAL, "dtype must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
+  if ((cfg->interleaved | 1) != 1 || (cfg->gain_per_head | 1) != 1)
+    return fail(ZERO_EINVAL, "interleaved and gain_per_head must be 0 or 1");
+  if (!(cfg->eps >= 0.0)) return fail(ZERO_EINVAL, "eps must be >= 0");
+  zero_qk_handle* h = new (std::nothrow) zero_qk_handle;
+  if (!h) return fail(ZERO_ENOMEM, "handle allocation failed");
+  h->cfg = *cfg;
+  int count = 0;
+  if (cudaGetDeviceCount(&count) != cudaSuccess || count < 1) {
+    cudaGetLastError();
+    *out = h;
+    return ZERO_OK;
+  }
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess)
+    e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
+  h->max_grid = 4 * h->sms;
+  // partial gain gradients of every CTA of the largest grid: at most 256 rows
+  // of 2..512 numbers (a group of one lane owns a head of at most 16 numbers)
+  const int64_t rows = cfg->gain_per_head
+                           ? std::min<int64_t>(kQkThreads, (int64_t)cfg->q_heads + cfg->k_heads)
+                           : 2;
+  const int64_t blocks = std::max<int64_t>(h->max_grid, (int64_t)cfg->q_heads + cfg->k_heads);
+  if (e == cudaSuccess)
+    e = cudaMalloc(reinterpret_cast<void**>(&h->part),
+                   (size_t)(blocks * rows * cfg->head_dim) * sizeof(float));
+  if (e != cudaSuccess) {
+    delete h;
+    return e == cudaErrorMemoryAllocation ? fail(ZERO_ENOMEM, "workspace allocation failed")
+                                          : cuda_fail(e, "zero_qk_create");
+  }
+  h->has_device = true;
+  *out = h;
+  return ZERO_OK;
+}
+
+zero_status zero_qk_destroy(zero_qk_t h) {
+  if (!h) return ZERO_OK;
+  if (h->has_device) {
+    int prev = -1;
+    cudaGetDevice(&prev);
+    cudaSetDevice(h->device);
+    cudaDeviceSynchronize();
+    cudaFree(h->part);
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+  delete h;
+  return ZERO_OK;
+}
+
+zero_status zero_qk_norm_rope(zero_qk_t h, const zero_qk_buffers* b, void* stream) {
+  return run(h, b, stream, false);
+}
+
+zero_status zero_qk_norm_rope_backward(zero_qk_t h, const zero_qk_buffers* b, void* stream) {
+  return run(h, b, stream, true);
+}
+
+zero_status zero_qk_launch_count(zero_qk_t h, int64_t* launches) {
+  if (!h || !launches) return fail(ZERO_EINVAL, "NULL argument");
+  *launches = h->launches;
+  return ZERO_OK;
+}
+
+}  // extern "C"
