@@ -361,6 +361,12 @@ zero_status zero_opt_set_lr(zero_opt_t h, double lr);
  * `stream`. Errors: EINVAL, ECUDA. */
 zero_status zero_opt_last_step(zero_opt_t h, void* stream, zero_opt_step_info* out);
 
+/* Device address of the record that zero_opt_last_step reads, for kernels that
+ * go by this handle's decisions (zero_muon_step).  Valid for the life of the
+ * handle; each stepping call writes it on that call's stream.  Host only.
+ * Errors: EINVAL (NULL), ECUDA (no device). */
+zero_status zero_opt_decision(zero_opt_t h, const zero_opt_step_info** decision_dev);
+
 /* Timing hook: subsequent steps (and statistics calls) of this handle record
  * the caller's CUDA events (cudaEvent_t, created by the caller; each may be
  * NULL) on the step's stream: ev_start before pass 1, ev_mid between pass 1

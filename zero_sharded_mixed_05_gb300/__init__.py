@@ -91,6 +91,33 @@ class zero_opt_ckpt_info(ctypes.Structure):
                 ("real_len", _i64), ("scaler", zero_opt_scaler_state)]
 
 
+MUON_SCALE_ONE, MUON_SCALE_RMS, MUON_SCALE_ASPECT = range(3)
+MUON_MAX_STEPS = 16
+
+
+class zero_muon_config(ctypes.Structure):
+    _fields_ = [("grad_dtype", _i32), ("param_dtype", _i32), ("nesterov", _i32), ("steps", _i32),
+                ("scale_rule", _i32), ("reserved", _i32), ("lr", _f64), ("momentum", _f64),
+                ("weight_decay", _f64), ("eps", _f64), ("coef", _f64 * 3 * MUON_MAX_STEPS)]
+
+
+class zero_muon_shape(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("cols", _i64), ("batch", _i64)]
+
+
+class zero_muon_operand(ctypes.Structure):
+    _fields_ = [("src", _vp), ("dst", _vp), ("in_row", _i64), ("in_batch", _i64),
+                ("out_row", _i64), ("out_batch", _i64)]
+
+
+class zero_muon_matrix(ctypes.Structure):
+    _fields_ = [("grad", _vp), ("momentum", _vp), ("master", _vp), ("param16", _vp)]
+
+
+class zero_muon_info(ctypes.Structure):
+    _fields_ = [("skipped", _i32), ("fault", _i32)]
+
+
 class zero_qk_config(ctypes.Structure):
     _fields_ = [("q_heads", _i32), ("k_heads", _i32), ("head_dim", _i32), ("rotary_dim", _i32),
                 ("dtype", _i32), ("interleaved", _i32), ("gain_per_head", _i32),
@@ -162,6 +189,16 @@ SIGNATURES = [
     ("zero_host_loss_scale", _i32, [_vp, _i32, _P(zero_opt_scaler_state)]),
     ("zero_host_set_loss_scale", _i32, [_vp, _i32, _P(zero_opt_scaler_state)]),
     ("zero_host_last_step", _i32, [_vp, _P(zero_opt_step_info)]),
+    ("zero_opt_decision", _i32, [_vp, _P(_vp)]),
+    ("zero_muon_config_default", _i32, [_P(zero_muon_config)]),
+    ("zero_muon_create", _i32, [_P(zero_muon_config), _P(zero_muon_shape), _i32, _P(_vp)]),
+    ("zero_muon_destroy", _i32, [_vp]),
+    ("zero_muon_workspace_bytes", _i32, [_vp, _P(_i64)]),
+    ("zero_muon_set_lr", _i32, [_vp, _f64]),
+    ("zero_muon_orthogonalize", _i32, [_vp, _P(zero_muon_operand), _i32, _i32, _vp]),
+    ("zero_muon_step", _i32, [_vp, _P(zero_muon_matrix), _f64, _vp, _vp]),
+    ("zero_muon_last_step", _i32, [_vp, _vp, _P(zero_muon_info)]),
+    ("zero_muon_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_qk_create", _i32, [_P(zero_qk_config), _P(_vp)]),
     ("zero_qk_destroy", _i32, [_vp]),
     ("zero_qk_norm_rope", _i32, [_vp, _P(zero_qk_buffers), _vp]),
@@ -627,6 +664,135 @@ def zero_host_last_step(h) -> zero_opt_step_info:
     out = zero_opt_step_info()
     _check(lib().zero_host_last_step(h, ctypes.byref(out)), "zero_host_last_step")
     return out
+
+
+def zero_opt_decision(h) -> int:
+    """Device address of the handle's last decision (for `zero_muon_step`)."""
+    out = _vp()
+    _check(lib().zero_opt_decision(h, ctypes.byref(out)), "zero_opt_decision")
+    return out.value
+
+
+# ---------------------------------------------------------------- orthogonalised updates
+
+# Shapes a handle was made for, so that the binding can check tensors against them.
+_muon_shapes = {}
+
+
+def make_muon_config(grad_dtype=FP16, param_dtype=None, lr=2e-2, momentum=0.95, nesterov=True,
+                     weight_decay=0.0, steps=5, coefs=None, eps=1e-7,
+                     scale_rule=MUON_SCALE_ONE) -> zero_muon_config:
+    """`coefs`: (a, b, c) for every step, or a list of one triple a step."""
+    cfg = zero_muon_config()
+    _check(lib().zero_muon_config_default(ctypes.byref(cfg)), "zero_muon_config_default")
+    cfg.grad_dtype = grad_dtype
+    cfg.param_dtype = grad_dtype if param_dtype is None else param_dtype
+    cfg.lr, cfg.momentum, cfg.weight_decay, cfg.eps = lr, momentum, weight_decay, eps
+    cfg.nesterov, cfg.steps, cfg.scale_rule = int(nesterov), steps, scale_rule
+    if coefs is not None:
+        each = list(coefs) if hasattr(coefs[0], "__len__") else [coefs] * min(steps, MUON_MAX_STEPS)
+        if len(each) != steps:
+            raise ValueError(f"{len(each)} coefficient triples for {steps} steps")
+        for i, abc in enumerate(each[:MUON_MAX_STEPS]):
+            cfg.coef[i][:] = [float(c) for c in abc]
+    return cfg
+
+
+def zero_muon_create(cfg: zero_muon_config, shapes) -> int:
+    """Handle for matrices of `shapes`: (rows, cols) or (rows, cols, batch) each."""
+    full = [tuple(s) + (1,) * (3 - len(s)) for s in shapes]
+    arr = (zero_muon_shape * max(len(full), 1))(*full)
+    h = _vp()
+    _check(lib().zero_muon_create(ctypes.byref(cfg), arr, len(full), ctypes.byref(h)),
+           "zero_muon_create")
+    _muon_shapes[h.value] = full
+    return h.value
+
+
+def zero_muon_destroy(h) -> None:
+    _muon_shapes.pop(h, None)
+    _check(lib().zero_muon_destroy(h), "zero_muon_destroy")
+
+
+def zero_muon_workspace_bytes(h) -> int:
+    out = _i64()
+    _check(lib().zero_muon_workspace_bytes(h, ctypes.byref(out)), "zero_muon_workspace_bytes")
+    return out.value
+
+
+def zero_muon_set_lr(h, lr: float) -> None:
+    _check(lib().zero_muon_set_lr(h, lr), "zero_muon_set_lr")
+
+
+def zero_muon_orthogonalize(h, ins, outs, stream=None) -> None:
+    """The orthogonalised form of every matrix of `ins` into `outs`: one tensor
+    per shape of the handle, [rows, cols] or [batch, rows, cols], with
+    contiguous rows; all inputs of one dtype (float16, bfloat16 or float32),
+    all outputs of one."""
+    import torch
+    shapes = _muon_shapes.get(h)
+    if shapes is None:
+        raise ValueError("not a handle of zero_muon_create")
+    if len(ins) != len(shapes) or len(outs) != len(shapes):
+        raise ValueError(f"{len(shapes)} inputs and outputs are wanted")
+    codes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
+    dev = torch.cuda.current_device()
+    arr = (zero_muon_operand * max(len(shapes), 1))()
+    dtypes = []
+    for i, (rows, cols, batch) in enumerate(shapes):
+        at = []
+        for name, t, first in (("ins", ins[i], ins[0]), ("outs", outs[i], outs[0])):
+            if not t.is_cuda or t.device.index != dev or t.dtype != first.dtype \
+                    or t.dtype not in codes or t.shape[-2:] != (rows, cols) \
+                    or (t.stride(-1) != 1 and cols > 1) \
+                    or not (t.dim() == 3 and t.shape[0] == batch or t.dim() == 2 and batch == 1):
+                raise ValueError(f"{name}[{i}] must be a CUDA tensor of the current device with "
+                                 f"shape ({batch}, {rows}, {cols}), contiguous rows and the dtype "
+                                 "of the others")
+            at.append((t.stride(-2), t.stride(0) if t.dim() == 3 else 0))
+            dtypes.append(codes[t.dtype])
+        arr[i] = zero_muon_operand(ins[i].data_ptr(), outs[i].data_ptr(), *at[0], *at[1])
+    _check(lib().zero_muon_orthogonalize(h, arr, dtypes[0] if dtypes else FP16,
+                                         dtypes[1] if dtypes else FP16, _stream(stream)),
+           "zero_muon_orthogonalize")
+
+
+def make_muon_list(mats):
+    """Per-matrix list for `zero_muon_step`; each item is a dict with grad,
+    momentum, master (or None: param16 is the master) and param16, contiguous."""
+    arr = (zero_muon_matrix * max(len(mats), 1))()
+    for i, m in enumerate(mats):
+        for name in ("grad", "momentum", "master", "param16"):
+            t = m[name]
+            if hasattr(t, "is_contiguous") and not t.is_contiguous():
+                raise ValueError(f"item {i}: {name} must be contiguous")
+        arr[i] = zero_muon_matrix(_ptr(m["grad"]), _ptr(m["momentum"]), _ptr(m["master"]),
+                                  _ptr(m["param16"]))
+    return arr, len(mats), list(mats)
+
+
+def zero_muon_step(h, mats, grad_scale=1.0, decision=None, stream=None) -> None:
+    """Step of every matrix (`mats` from `make_muon_list`, one item per shape of
+    the handle).  `decision`: None, or the address from `zero_opt_decision`."""
+    arr, n, _ = mats
+    if n != len(_muon_shapes.get(h, ())):
+        raise ValueError(f"the list has {n} matrices, the handle "
+                         f"{len(_muon_shapes.get(h, ()))}")
+    _check(lib().zero_muon_step(h, arr, grad_scale, _ptr(decision), _stream(stream)),
+           "zero_muon_step")
+
+
+def zero_muon_last_step(h, stream=None) -> zero_muon_info:
+    out = zero_muon_info()
+    _check(lib().zero_muon_last_step(h, _stream(stream), ctypes.byref(out)),
+           "zero_muon_last_step")
+    return out
+
+
+def zero_muon_launch_count(h) -> int:
+    out = _i64()
+    _check(lib().zero_muon_launch_count(h, ctypes.byref(out)), "zero_muon_launch_count")
+    return out.value
 
 
 # ---------------------------------------------------------------- query/key norm and rotation

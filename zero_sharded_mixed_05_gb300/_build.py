@@ -12,10 +12,12 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, "zero_opt.cu"), os.path.join(CSRC, "ckpt.cpp"),
            os.path.join(CSRC, "noalloc.cu"), os.path.join(CSRC, "host_step.cpp"),
-           os.path.join(CSRC, "qk.cu")]
+           os.path.join(CSRC, "qk.cu"), os.path.join(CSRC, "muon.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "zero_opt_internal.h",
-                                                     "host_util.h", "decide_core.h", "host_cast.h")] + [
-    os.path.join(INCLUDE, f) for f in ("zero_opt.h", "zero_qk.h")]
+                                                     "host_util.h", "decide_core.h", "host_cast.h",
+                                                     "muon_kernels.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("zero_opt.h", "zero_qk.h",
+                                                                       "zero_muon.h")]
 LIB = os.path.join(PKG, "libzero_opt.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,352 @@
+// muon_kernels.cuh -- device side of the orthogonalised update (zero_muon.h).
+//
+// A call is three stages:
+//   muon_stats_kernel   reads the input (for the step: gradient and momentum,
+//                       and writes the new momentum) and finds |U|_F
+//   muon_start_kernel   writes X = U / (|U|_F + eps) into the workspace
+//   products            steps times  A = X X^T,  B = b A + c A A,  X <- a X + B X,
+//                       the last with the result's epilogue
+// The workspace holds every matrix in the orientation it came in: for a wide
+// matrix the products are X X^T and B X, for a tall one X^T X and X B.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "zero_muon.h"
+
+namespace zm {
+
+constexpr int kThreads = 256;
+constexpr int kMaxEntries = ZERO_MUON_MAX_SHAPES;
+constexpr int kVec = 8;                        // numbers of a vector in the first two stages
+constexpr int kChunk = kThreads * 8;           // vectors of a CTA
+
+struct Entry {
+  int32_t rows, cols, batch, k, l, tall;
+  int64_t ldx, ldk;          // elements from row to row of x and of a/b
+  float* x[2];               // [batch][rows][ldx], read and written in turn
+  float* a;                  // [batch][k][ldk]
+  float* b;
+  int32_t unit0;             // first matrix of the entry among all
+  int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
+  int32_t vpr;               // vectors a row
+  int64_t tile0;             // products: first tile, by the kind of product
+  float s;                   // scale_rule's factor
+};
+
+// What a call was given for one entry.
+struct Io {
+  const void* in;            // matrix, or gradient
+  float* mom;
+  float* master;
+  void* out;                 // result, or 16-bit parameters
+  int64_t in_row, in_batch, out_row, out_batch;
+};
+
+struct Workspace {
+  int32_t fault;
+  int32_t skipped;
+};
+
+struct Call {
+  const Entry* entries;
+  int32_t n, step;           // step: 1 zero_muon_step, 0 zero_muon_orthogonalize
+  Workspace* ws;
+  double* part;              // sums of squares, one a CTA of the first stage
+  unsigned* ticket;          // one a matrix, zero between calls
+  float* inv;                // 1 / (|U|_F + eps), one a matrix
+  const zero_opt_step_info* decision;
+  double eps;
+  float grad_scale, mu;
+  int32_t nesterov, in_type, out_type;
+  float decay, lr;           // 1 - lr * weight_decay; lr
+  Io io[kMaxEntries];
+};
+
+template <typename T> __device__ __forceinline__ float num(T x);
+template <> __device__ __forceinline__ float num(__half x) { return __half2float(x); }
+template <> __device__ __forceinline__ float num(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float num(float x) { return x; }
+template <typename T> __device__ __forceinline__ T as(float x);
+template <> __device__ __forceinline__ __half as(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 as(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ float as(float x) { return x; }
+
+__device__ __forceinline__ bool skipped(const Call& c) {
+  return c.decision && c.decision->skipped;
+}
+
+__device__ __forceinline__ float grad_factor(const Call& c) {
+  return c.decision ? __fmul_rn(c.grad_scale, c.decision->coef) : c.grad_scale;
+}
+
+// The entry whose CTAs of the first two stages include this one.
+__device__ __forceinline__ int entry_of_chunk(const Call& c) {
+  __shared__ int found;
+  for (int i = threadIdx.x; i < c.n; i += kThreads) {
+    const Entry& e = c.entries[i];
+    const int at = (int)blockIdx.x - e.chunk0;
+    if (at >= 0 && at < e.chunks * e.batch) found = i;
+  }
+  __syncthreads();
+  return found;
+}
+
+// Eight numbers of a row (fewer at its end, the rest zero) from p.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float* x) {
+  if (vec && n == kVec) {
+    if constexpr (sizeof(T) == 2) {
+      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      const T* t = reinterpret_cast<const T*>(&u);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[i] = num<T>(t[i]);
+    } else {
+      const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) x[i] = i < n ? num<T>(p[i]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ void store8(float* p, int n, bool vec, const float* x) {
+  if (vec && n == kVec) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      if (i < n) p[i] = x[i];
+  }
+}
+
+__device__ __forceinline__ bool aligned(const void* p, int64_t row, int64_t batch, int esize) {
+  const int64_t m = 16 / esize;
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && row % m == 0 && batch % m == 0;
+}
+
+// U of eight numbers for the step, from the gradient and the momentum; `mom`
+// holds the old momentum and gets the new one (kNew), or holds the new one.
+template <bool kNew>
+__device__ __forceinline__ void update_of(const Call& c, float f, const float* g, float* mom, float* u) {
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const float gi = __fmul_rn(g[i], f);
+    if (kNew) mom[i] = __fadd_rn(__fmul_rn(c.mu, mom[i]), gi);
+    u[i] = c.nesterov ? __fadd_rn(gi, __fmul_rn(c.mu, mom[i])) : mom[i];
+  }
+}
+
+// Stage 1.  Bound by memory: the step reads 2 + 4 bytes a number and writes 4.
+// Squares are added in binary32 within a thread's 64 numbers and in binary64
+// beyond; the last CTA of a matrix adds the CTAs' sums in index order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_constant__ Call c) {
+  __shared__ double red[kThreads / 32];
+  __shared__ int last;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    c.ws->fault = 0;
+    c.ws->skipped = skipped(c);
+  }
+  if (skipped(c)) return;
+  const int ei = entry_of_chunk(c);
+  const Entry& e = c.entries[ei];
+  const Io& io = c.io[ei];
+  const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
+  const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
+  const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
+  float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
+  const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
+  const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
+  const float f = grad_factor(c);
+  float sq = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < kChunk / kThreads; ++i) {
+    const uint32_t v = (uint32_t)chunk * kChunk + i * kThreads + threadIdx.x;
+    if (v >= vecs) break;
+    const uint32_t row = v / (uint32_t)e.vpr, col = (v - row * e.vpr) * kVec;
+    const int n = min(kVec, e.cols - (int)col);
+    float x[kVec], u[kVec];
+    load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
+    if (c.step) {
+      float m[kVec];
+      float* pm = mom + (int64_t)row * e.cols + col;
+      load8<float>(pm, n, vmom, m);
+      update_of<true>(c, f, x, m, u);
+      store8(pm, n, vmom, m);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) u[j] = x[j];
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) sq = __fmaf_rn(u[j], u[j], sq);
+  }
+  double d = sq;
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
+  __syncthreads();
+  const int unit = e.unit0 + b;
+  double* part = c.part + e.chunk0 + (int64_t)b * e.chunks;
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kThreads / 32; ++i) d += red[i];
+    part[chunk] = d;
+    __threadfence();
+    last = atomicAdd(&c.ticket[unit], 1u) == (unsigned)e.chunks - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  d = 0.0;
+  for (int i = threadIdx.x; i < e.chunks; i += kThreads) d += __ldcg(&part[i]);
+  for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  __syncthreads();
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < kThreads / 32; ++i) d += red[i];
+    c.inv[unit] = (float)(1.0 / (sqrt(d) + c.eps));
+    c.ticket[unit] = 0u;
+  }
+}
+
+// Stage 2.  Reads U's sources again (from L2 where they fit) and writes X.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ Call c) {
+  if (skipped(c)) return;
+  const int ei = entry_of_chunk(c);
+  const Entry& e = c.entries[ei];
+  const Io& io = c.io[ei];
+  const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
+  const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
+  const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
+  const float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
+  const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
+  const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
+  const float f = grad_factor(c), inv = c.inv[e.unit0 + b];
+  const int64_t base = (int64_t)b * e.rows * e.ldx;
+#pragma unroll 4
+  for (int i = 0; i < kChunk / kThreads; ++i) {
+    const uint32_t v = (uint32_t)chunk * kChunk + i * kThreads + threadIdx.x;
+    if (v >= vecs) break;
+    const uint32_t row = v / (uint32_t)e.vpr, col = (v - row * e.vpr) * kVec;
+    const int n = min(kVec, e.cols - (int)col);
+    float x[kVec], u[kVec];
+    load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
+    if (c.step) {
+      float m[kVec];
+      load8<float>(mom + (int64_t)row * e.cols + col, n, vmom, m);
+      update_of<false>(c, f, x, m, u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) u[j] = x[j];
+    }
+    // rows of the workspace are multiples of 16 numbers: the vector fits
+    float* to = e.x[0] + base + (int64_t)row * e.ldx + col;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) u[j] = __fmul_rn(u[j], inv);
+    store8(to, kVec, true, u);
+  }
+}
+
+// One number of the result: O itself, or the step with it.
+__device__ __forceinline__ void finish(const Call& c, const Entry& e, const Io& io, int b, int row,
+                                       int col, float o) {
+  if (!c.step) {
+    const int64_t at = (int64_t)b * io.out_batch + (int64_t)row * io.out_row + col;
+    if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[at] = as<__half>(o);
+    else if (c.out_type == ZERO_BF16) static_cast<__nv_bfloat16*>(io.out)[at] = as<__nv_bfloat16>(o);
+    else static_cast<float*>(io.out)[at] = o;
+    return;
+  }
+  const int64_t at = ((int64_t)b * e.rows + row) * e.cols + col;
+  float w;
+  if (io.master) w = io.master[at];
+  else if (c.out_type == ZERO_FP16) w = num<__half>(static_cast<__half*>(io.out)[at]);
+  else w = num<__nv_bfloat16>(static_cast<__nv_bfloat16*>(io.out)[at]);
+  w = __fmaf_rn(-__fmul_rn(c.lr, e.s), o, __fmul_rn(w, c.decay));
+  if (io.master) io.master[at] = w;
+  if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[at] = as<__half>(w);
+  else static_cast<__nv_bfloat16*>(io.out)[at] = as<__nv_bfloat16>(w);
+}
+
+// Stage 3, one product of every matrix: 64 x 64 tiles of binary32 sums.
+// which: 0 A = X X^T, 1 B = b A + c A A, 2 X <- a X + B X.
+__global__ void __launch_bounds__(kThreads) muon_product_kernel(const __grid_constant__ Call c,
+                                                                int which, int cur, int last,
+                                                                float ca, float cb, float cc) {
+  __shared__ float sa[16][65], sb[16][65];
+  if (skipped(c)) return;
+  int64_t t = blockIdx.x;
+  int ei = 0, tm = 0, tn = 0;
+  for (; ei < c.n; ++ei) {
+    const Entry& e = c.entries[ei];
+    const int m = which == 2 ? e.rows : e.k, n = which == 2 ? e.cols : e.k;
+    tm = (m + 63) / 64;
+    tn = (n + 63) / 64;
+    if (t < (int64_t)tm * tn * e.batch) break;
+    t -= (int64_t)tm * tn * e.batch;
+  }
+  if (ei == c.n) return;
+  const Entry& e = c.entries[ei];
+  const int b = (int)(t / (tm * tn)), m0 = (int)(t % (tm * tn)) / tn * 64,
+            n0 = (int)(t % (tm * tn)) % tn * 64;
+  const int M = which == 2 ? e.rows : e.k, N = which == 2 ? e.cols : e.k;
+  const int K = which == 0 ? e.l : e.k;
+  const float* x = e.x[cur] + (int64_t)b * e.rows * e.ldx;
+  const float* A = e.a + (int64_t)b * e.k * e.ldk;
+  const float* B = e.b + (int64_t)b * e.k * e.ldk;
+  // D[m][n] = sum over k of P(m, k) Q(n, k)
+  auto left = [&](int m, int k) -> float {
+    if (m >= M || k >= K) return 0.0f;
+    if (which == 0) return (e.tall ? x[(int64_t)k * e.ldx + m] : x[(int64_t)m * e.ldx + k]);
+    if (which == 1) return (A[(int64_t)m * e.ldk + k]);
+    return (e.tall ? x[(int64_t)m * e.ldx + k] : B[(int64_t)m * e.ldk + k]);
+  };
+  auto right = [&](int n, int k) -> float {
+    if (n >= N || k >= K) return 0.0f;
+    if (which == 0) return (e.tall ? x[(int64_t)k * e.ldx + n] : x[(int64_t)n * e.ldx + k]);
+    if (which == 1) return (A[(int64_t)n * e.ldk + k]);
+    return (e.tall ? B[(int64_t)n * e.ldk + k] : x[(int64_t)k * e.ldx + n]);
+  };
+  float acc[4][4] = {};
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  for (int k0 = 0; k0 < K; k0 += 16) {
+    for (int i = threadIdx.x; i < 64 * 16; i += kThreads) {
+      sa[i % 16][i / 16] = left(m0 + i / 16, k0 + i % 16);
+      sb[i % 16][i / 16] = right(n0 + i / 16, k0 + i % 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          acc[i][j] = __fmaf_rn(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
+    __syncthreads();
+  }
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) {
+      const int row = m0 + ty + 16 * i, col = n0 + tx + 16 * j;
+      if (row >= M || col >= N) continue;
+      const float d = acc[i][j];
+      const int64_t at = (int64_t)b * e.k * e.ldk + (int64_t)row * e.ldk + col;
+      if (which == 0) {
+        e.a[at] = d;
+      } else if (which == 1) {
+        e.b[at] = __fmaf_rn(cb, e.a[at], __fmul_rn(cc, d));
+      } else {
+        const int64_t ax = ((int64_t)b * e.rows + row) * e.ldx + col;
+        const float y = __fmaf_rn(ca, e.x[cur][ax], d);
+        if (last) finish(c, e, c.io[ei], b, row, col, y);
+        else e.x[cur ^ 1][ax] = y;
+      }
+    }
+}
+
+}  // namespace zm

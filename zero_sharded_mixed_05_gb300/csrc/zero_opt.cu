@@ -1155,6 +1155,15 @@ zero_status zero_opt_last_step(zero_opt_t h, void* stream, zero_opt_step_info* o
   return read_small(h, &h->ws->dec, sizeof(zero_opt_step_info), stream, out);
 }
 
+zero_status zero_opt_decision(zero_opt_t h, const zero_opt_step_info** decision_dev) {
+  if (!h) return fail(ZERO_EINVAL, "handle is NULL");
+  if (!decision_dev) return fail(ZERO_EINVAL, "decision_dev is NULL");
+  *decision_dev = nullptr;
+  if (!h->has_device) return fail(ZERO_ECUDA, "no CUDA device for this handle");
+  *decision_dev = reinterpret_cast<const zero_opt_step_info*>(&h->ws->dec);
+  return ZERO_OK;
+}
+
 zero_status zero_opt_save_shard(zero_opt_t h, int32_t rank, const float* master,
                                 const float* m, const float* v, void* stream,
                                 const char* path) {
