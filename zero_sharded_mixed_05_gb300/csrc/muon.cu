@@ -1,6 +1,6 @@
 // muon.cu -- host side of the orthogonalised update (zero_muon.h): checks,
 // the workspace and its layout, launches.
-#include "muon_kernels.cuh"
+#include "muon_products.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -32,7 +32,12 @@ struct zero_muon_handle {
   unsigned char* mem = nullptr;     // the whole workspace
   int64_t bytes = 0;
   zm::Call call = {};               // the fields that no call changes
+  const CUtensorMap* maps = nullptr;
+  const int32_t* starts = nullptr;
   int64_t chunks = 0;               // CTAs of the first two stages
+  int pair = 2;                     // CTAs a tile of the products
+  int grid = 0;                     // CTAs of the products
+  int smem = 0;
   int64_t launches = 0;
 };
 
@@ -75,33 +80,64 @@ zero_status launch(zero_muon_t h, const void* fn, int64_t grid, void** params, c
   return ZERO_OK;
 }
 
-template <typename T>
-zero_status run(zero_muon_t h, zm::Call& c, cudaStream_t s) {
-  if (c.n == 0) return ZERO_OK;
-  void* p[] = {&c};
-  zero_status st = launch(h, (const void*)zm::muon_stats_kernel<T>, h->chunks, p, s);
-  if (st == ZERO_OK) st = launch(h, (const void*)zm::muon_start_kernel<T>, h->chunks, p, s);
-  int64_t tiles[3] = {0, 0, 0};
-  for (const zm::Entry& e : h->entries) {
-    const int64_t k = (e.k + 63) / 64, m = (e.rows + 63) / 64, n = (e.cols + 63) / 64;
-    tiles[0] += k * k * e.batch;
-    tiles[2] += m * n * e.batch;
-  }
-  tiles[1] = tiles[0];
-  for (int i = 0; i < h->cfg.steps && st == ZERO_OK; ++i)
-    for (int which = 0; which < 3 && st == ZERO_OK; ++which) {
-      int cur = i % 2, last = i == h->cfg.steps - 1;
-      float a = (float)h->cfg.coef[i][0], b = (float)h->cfg.coef[i][1], cc = (float)h->cfg.coef[i][2];
-      void* q[] = {&c, &which, &cur, &last, &a, &b, &cc};
-      st = launch(h, (const void*)zm::muon_product_kernel, tiles[which], q, s);
-    }
-  return st;
+const void* products_kernel(int pair) {
+  return pair == 2 ? (const void*)zm::muon_products_kernel<2> : (const void*)zm::muon_products_kernel<1>;
 }
 
-zero_status run_typed(zero_muon_t h, zm::Call& c, cudaStream_t s) {
-  if (c.in_type == ZERO_FP16) return run<__half>(h, c, s);
-  if (c.in_type == ZERO_BF16) return run<__nv_bfloat16>(h, c, s);
-  return run<float>(h, c, s);
+// One cooperative launch (its CTAs wait for one another), in clusters of the pair.
+cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cudaStream_t s) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)h->grid);
+  lc.blockDim = dim3(zm::kProductThreads);
+  lc.dynamicSmemBytes = (size_t)h->smem;
+  lc.stream = s;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)h->pair;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  return lc;
+}
+
+template <typename T, int N>
+zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t s) {
+  zm::Start<N> start;
+  start.c = c;
+  std::copy(io, io + c.n, start.io);
+  void* p[] = {&start};
+  zero_status st = launch(h, (const void*)zm::muon_stats_kernel<T, N>, h->chunks, p, s);
+  if (st != ZERO_OK) return st;
+  void* q[] = {&start.c};
+  st = launch(h, (const void*)zm::muon_start_kernel<T>, h->chunks, q, s);
+  if (st != ZERO_OK) return st;
+  zm::Products pr = {};
+  pr.c = c;
+  pr.maps = h->maps;
+  pr.starts = h->starts;
+  pr.steps = h->cfg.steps;
+  for (int i = 0; i < pr.steps; ++i)
+    for (int j = 0; j < 3; ++j) pr.coef[i][j] = (float)h->cfg.coef[i][j];
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc = products_config(h, attr, s);
+  void* r[] = {&pr};
+  const cudaError_t e = cudaLaunchKernelExC(&lc, products_kernel(h->pair), r);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
+  ++h->launches;
+  return ZERO_OK;
+}
+
+template <typename T>
+zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t s) {
+  if (c.n == 0) return ZERO_OK;
+  return c.n <= 8 ? run<T, 8>(h, c, io, s) : run<T, zm::kMaxEntries>(h, c, io, s);
+}
+
+zero_status run_typed(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t s) {
+  if (c.in_type == ZERO_FP16) return run<__half>(h, c, io, s);
+  if (c.in_type == ZERO_BF16) return run<__nv_bfloat16>(h, c, io, s);
+  return run<float>(h, c, io, s);
 }
 
 zero_status check_device(zero_muon_t h) {
@@ -114,40 +150,100 @@ zero_status check_device(zero_muon_t h) {
   return ZERO_OK;
 }
 
-// Allocates the workspace and fills in the addresses.
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                CUtensorMapFloatOOBfill);
+
+// Map of a [batch][rows][cols] array of binary16 numbers read in boxes of
+// 64 x 64; what lies outside of it reads as zero.
+bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t cols, int64_t rows, int64_t batch,
+            int64_t ld) {
+  const cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t stride[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
+  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dim, stride, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Allocates the workspace, fills in the addresses and readies the products.
 cudaError_t place(zero_muon_t h) {
   Layout lay;
   const int64_t n = (int64_t)h->entries.size();
   int64_t units = 0;
   for (const zm::Entry& e : h->entries) units += e.batch;
   const int64_t ws = lay.take(sizeof(zm::Workspace)), table = lay.take(n * sizeof(zm::Entry));
+  const int64_t maps = lay.take(4 * n * sizeof(CUtensorMap)), starts = lay.take(2 * (n + 1) * 4);
+  const int64_t io = lay.take(n * sizeof(zm::Io));
   const int64_t part = lay.take(h->chunks * sizeof(double)), ticket = lay.take(units * 4),
-                inv = lay.take(units * 4);
+                inv = lay.take(units * 4), done = lay.take(units * 4);
   const int64_t cleared = lay.size;
   std::vector<int64_t> at;
   for (const zm::Entry& e : h->entries) {
-    const int64_t x = e.batch * (int64_t)e.rows * e.ldx * 4, a = e.batch * (int64_t)e.k * e.ldk * 4;
-    for (int64_t bytes : {x, x, a, a}) at.push_back(lay.take(bytes));
+    const int64_t x = e.batch * (int64_t)e.rows * e.ldx * 2, a = e.batch * (int64_t)e.k * e.ldk * 2;
+    for (int64_t bytes : {x, x, x, a, a, e.batch * e.ldk * 4}) at.push_back(lay.take(bytes));
   }
   h->bytes = lay.size;
+  std::vector<CUtensorMap> map(4 * n);
+  std::vector<int32_t> first(2 * (n + 1), 0);
   cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->mem), (size_t)h->bytes);
   if (e != cudaSuccess) return e;
+  void* sym = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &sym, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess) return cudaErrorSymbolNotFound;
+  const EncodeTiled fn = reinterpret_cast<EncodeTiled>(sym);
+  const int tile = 128 * h->pair;
   for (int64_t i = 0; i < n; ++i) {
     zm::Entry& en = h->entries[i];
-    en.x[0] = reinterpret_cast<float*>(h->mem + at[4 * i]);
-    en.x[1] = reinterpret_cast<float*>(h->mem + at[4 * i + 1]);
-    en.a = reinterpret_cast<float*>(h->mem + at[4 * i + 2]);
-    en.b = reinterpret_cast<float*>(h->mem + at[4 * i + 3]);
+    en.x[0] = reinterpret_cast<__half*>(h->mem + at[6 * i]);
+    en.x[1] = reinterpret_cast<__half*>(h->mem + at[6 * i + 1]);
+    en.lo = reinterpret_cast<__half*>(h->mem + at[6 * i + 2]);
+    en.a = reinterpret_cast<__half*>(h->mem + at[6 * i + 3]);
+    en.b = reinterpret_cast<__half*>(h->mem + at[6 * i + 4]);
+    en.diag = reinterpret_cast<float*>(h->mem + at[6 * i + 5]);
+    const bool ok = encode(fn, &map[4 * i], en.x[0], en.cols, en.rows, en.batch, en.ldx) &&
+                    encode(fn, &map[4 * i + 1], en.x[1], en.cols, en.rows, en.batch, en.ldx) &&
+                    encode(fn, &map[4 * i + 2], en.a, en.k, en.k, en.batch, en.ldk) &&
+                    encode(fn, &map[4 * i + 3], en.b, en.k, en.k, en.batch, en.ldk);
+    if (!ok) return cudaErrorInvalidValue;
+    const int64_t nk = (en.k + tile - 1) / tile, nr = (en.rows + tile - 1) / tile,
+                  nc = (en.cols + tile - 1) / tile;
+    first[i + 1] = (int32_t)(first[i] + en.batch * nk * (nk + 1) / 2);
+    first[n + 1 + i + 1] = (int32_t)(first[n + 1 + i] + en.batch * nr * nc);
   }
   e = cudaMemset(h->mem, 0, (size_t)cleared);
-  if (e == cudaSuccess && n > 0)
-    e = cudaMemcpy(h->mem + table, h->entries.data(), n * sizeof(zm::Entry), cudaMemcpyHostToDevice);
+  const auto copy = [&](int64_t to, const void* from, size_t bytes) {
+    if (e == cudaSuccess && bytes > 0)
+      e = cudaMemcpy(h->mem + to, from, bytes, cudaMemcpyHostToDevice);
+  };
+  copy(table, h->entries.data(), n * sizeof(zm::Entry));
+  copy(maps, map.data(), map.size() * sizeof(CUtensorMap));
+  copy(starts, first.data(), first.size() * sizeof(int32_t));
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   h->call.ws = reinterpret_cast<zm::Workspace*>(h->mem + ws);
   h->call.entries = reinterpret_cast<const zm::Entry*>(h->mem + table);
+  h->call.io = reinterpret_cast<zm::Io*>(h->mem + io);
   h->call.part = reinterpret_cast<double*>(h->mem + part);
   h->call.ticket = reinterpret_cast<unsigned*>(h->mem + ticket);
   h->call.inv = reinterpret_cast<float*>(h->mem + inv);
+  h->call.done = reinterpret_cast<uint32_t*>(h->mem + done);
+  h->maps = reinterpret_cast<const CUtensorMap*>(h->mem + maps);
+  h->starts = reinterpret_cast<const int32_t*>(h->mem + starts);
+  h->smem = zm::smem_bytes((int)n);
+  const void* kernel = products_kernel(h->pair);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, h->smem);
+  // as many pairs as can be on the device at once, and no more than tiles
+  h->grid = h->pair;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t lc = products_config(h, attr, nullptr);
+  int clusters = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc);
+  const int most = std::max(first[n], first[2 * n + 1]);
+  h->grid = h->pair * std::max(1, std::min(clusters, most));
   return e;
 }
 
@@ -207,23 +303,32 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
       e.tall = s.rows > s.cols;
       e.k = (int32_t)std::min(s.rows, s.cols);
       e.l = (int32_t)std::max(s.rows, s.cols);
-      e.ldx = (s.cols + 15) / 16 * 16;
-      e.ldk = (e.k + 15) / 16 * 16;
-      e.unit0 = (int32_t)units;
+      e.item = i;
+      e.ldx = (s.cols + 31) / 32 * 32;
+      e.ldk = (e.k + 31) / 32 * 32;
       e.vpr = (int32_t)((s.cols + zm::kVec - 1) / zm::kVec);
       e.chunks = (int32_t)(((int64_t)e.rows * e.vpr + zm::kChunk - 1) / zm::kChunk);
-      e.chunk0 = (int32_t)h->chunks;
       e.s = (float)(cfg->scale_rule == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt((double)e.l)
                     : cfg->scale_rule == ZERO_MUON_SCALE_ASPECT
                         ? std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols))
                         : 1.0);
-      units += s.batch;
-      h->chunks += (int64_t)e.chunks * s.batch;
-      if (units > INT32_MAX / 2 || h->chunks > INT32_MAX / 2) {
+      h->entries.push_back(e);
+    }
+    // the products' tiles go out from the deepest to the shallowest
+    std::stable_sort(h->entries.begin(), h->entries.end(), [](const zm::Entry& x, const zm::Entry& y) {
+      return x.k != y.k ? x.k > y.k : x.l > y.l;
+    });
+    double tiles = 0;
+    for (zm::Entry& e : h->entries) {
+      e.unit0 = (int32_t)units;
+      e.chunk0 = (int32_t)h->chunks;
+      units += e.batch;
+      h->chunks += (int64_t)e.chunks * e.batch;
+      tiles += (e.rows / 128 + 1.0) * (e.cols / 128 + 1.0) * e.batch;
+      if (units > INT32_MAX / 2 || h->chunks > INT32_MAX / 2 || tiles > INT32_MAX / 64) {
         delete h;
         return fail(ZERO_ERANGE, "too many matrices, or too large, for one handle");
       }
-      h->entries.push_back(e);
     }
   } catch (const std::bad_alloc&) {
     delete h;
@@ -295,27 +400,29 @@ zero_status zero_muon_orthogonalize(zero_muon_t h, const zero_muon_operand* item
     if (!dtype16(d) && d != ZERO_FP32)
       return fail(ZERO_EINVAL, "dtype must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
   zm::Call c = h->call;
+  zm::Io io[zm::kMaxEntries] = {};
   for (int i = 0; i < n; ++i) {
     const zero_muon_operand& t = items[i];
-    const zm::Entry& e = h->entries[i];
+    const zero_muon_shape& e = h->shapes[i];
     if (!t.in || !t.out) return fail(ZERO_EINVAL, "item %d: in and out must be non-NULL", i);
     if (t.in_row < 0 || t.in_batch < 0 || t.out_row < 0 || t.out_batch < 0)
       return fail(ZERO_EINVAL, "item %d: strides must be >= 0", i);
     if (e.rows > 1 && (t.in_row < e.cols || t.out_row < e.cols))
-      return fail(ZERO_EINVAL, "item %d: a row stride is below its %d columns", i, e.cols);
-    c.io[i].in = t.in;
-    c.io[i].out = t.out;
-    c.io[i].in_row = t.in_row;
-    c.io[i].in_batch = t.in_batch;
-    c.io[i].out_row = t.out_row;
-    c.io[i].out_batch = t.out_batch;
+      return fail(ZERO_EINVAL, "item %d: a row stride is below its %lld columns", i,
+                  (long long)e.cols);
+    io[i].in = t.in;
+    io[i].out = t.out;
+    io[i].in_row = t.in_row;
+    io[i].in_batch = t.in_batch;
+    io[i].out_row = t.out_row;
+    io[i].out_batch = t.out_batch;
   }
   const zero_status st = check_device(h);
   if (st != ZERO_OK) return st;
   c.step = 0;
   c.in_type = in_dtype;
   c.out_type = out_dtype;
-  return run_typed(h, c, static_cast<cudaStream_t>(stream));
+  return run_typed(h, c, io, static_cast<cudaStream_t>(stream));
 }
 
 zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double grad_scale,
@@ -325,17 +432,18 @@ zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double 
   if (n > 0 && !items) return fail(ZERO_EINVAL, "items is NULL");
   if (!std::isfinite(grad_scale)) return fail(ZERO_EINVAL, "grad_scale is not finite");
   zm::Call c = h->call;
+  zm::Io io[zm::kMaxEntries] = {};
   for (int i = 0; i < n; ++i) {
     const zero_muon_matrix& t = items[i];
-    const zm::Entry& e = h->entries[i];
+    const zero_muon_shape& e = h->shapes[i];
     if (!t.grad || !t.momentum || !t.param16)
       return fail(ZERO_EINVAL, "item %d: grad, momentum and param16 must be non-NULL", i);
-    c.io[i].in = t.grad;
-    c.io[i].mom = t.momentum;
-    c.io[i].master = t.master;
-    c.io[i].out = t.param16;
-    c.io[i].in_row = c.io[i].out_row = e.cols;
-    c.io[i].in_batch = c.io[i].out_batch = (int64_t)e.rows * e.cols;
+    io[i].in = t.grad;
+    io[i].mom = t.momentum;
+    io[i].master = t.master;
+    io[i].out = t.param16;
+    io[i].in_row = io[i].out_row = e.cols;
+    io[i].in_batch = io[i].out_batch = e.rows * e.cols;
   }
   const zero_status st = check_device(h);
   if (st != ZERO_OK) return st;
@@ -346,7 +454,7 @@ zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double 
   c.decision = decision;
   c.decay = (float)(1.0 - h->cfg.lr * h->cfg.weight_decay);
   c.lr = (float)h->cfg.lr;
-  return run_typed(h, c, static_cast<cudaStream_t>(stream));
+  return run_typed(h, c, io, static_cast<cudaStream_t>(stream));
 }
 
 zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out) {

@@ -3,9 +3,10 @@
 // A call is three stages:
 //   muon_stats_kernel   reads the input (for the step: gradient and momentum,
 //                       and writes the new momentum) and finds |U|_F
-//   muon_start_kernel   writes X = U / (|U|_F + eps) into the workspace
-//   products            steps times  A = X X^T,  B = b A + c A A,  X <- a X + B X,
-//                       the last with the result's epilogue
+//   muon_start_kernel   writes X = U / (|U|_F + eps), held as two binary16
+//                       numbers, into the workspace
+//   muon_products_kernel steps times  A = X X^T,  B = b A + c A A,  X <- a X + B X,
+//                       the last with the result's epilogue (muon_products.cuh)
 // The workspace holds every matrix in the orientation it came in: for a wide
 // matrix the products are X X^T and B X, for a tall one X^T X and X B.
 #pragma once
@@ -23,16 +24,23 @@ constexpr int kMaxEntries = ZERO_MUON_MAX_SHAPES;
 constexpr int kVec = 8;                        // numbers of a vector in the first two stages
 constexpr int kChunk = kThreads * 8;           // vectors of a CTA
 
+// X, A and B are held times 4096 (zero_muon.h); the second part of X times
+// 2^11 more, so that it is a normal number wherever the first is.
+constexpr float kScale = 4096.0f;
+constexpr float kLoScale = 2048.0f;
+
 struct Entry {
   int32_t rows, cols, batch, k, l, tall;
-  int64_t ldx, ldk;          // elements from row to row of x and of a/b
-  float* x[2];               // [batch][rows][ldx], read and written in turn
-  float* a;                  // [batch][k][ldk]
-  float* b;
+  int64_t ldx, ldk;          // elements from row to row of x/lo and of a/b
+  __half* x[2];              // [batch][rows][ldx], read and written in turn
+  __half* lo;
+  __half* a;                 // [batch][k][ldk]
+  __half* b;
+  float* diag;               // [batch][ldk]: A's diagonal
   int32_t unit0;             // first matrix of the entry among all
   int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
   int32_t vpr;               // vectors a row
-  int64_t tile0;             // products: first tile, by the kind of product
+  int32_t item;              // the caller's index
   float s;                   // scale_rule's factor
 };
 
@@ -62,7 +70,15 @@ struct Call {
   float grad_scale, mu;
   int32_t nesterov, in_type, out_type;
   float decay, lr;           // 1 - lr * weight_decay; lr
-  Io io[kMaxEntries];
+  uint32_t* done;            // finished tiles of each matrix
+  Io* io;                    // by the caller's index; stage 1 fills it in
+};
+
+// Stage 1's arguments: the caller's addresses travel with the launch (a large
+// argument costs microseconds, so a handle of few entries has a small one).
+template <int N> struct Start {
+  Call c;
+  Io io[N];
 };
 
 template <typename T> __device__ __forceinline__ float num(T x);
@@ -145,8 +161,9 @@ __device__ __forceinline__ void update_of(const Call& c, float f, const float* g
 // Stage 1.  Bound by memory: the step reads 2 + 4 bytes a number and writes 4.
 // Squares are added in binary32 within a thread's 64 numbers and in binary64
 // beyond; the last CTA of a matrix adds the CTAs' sums in index order.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_constant__ Call c) {
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_constant__ Start<N> s) {
+  const Call& c = s.c;
   __shared__ double red[kThreads / 32];
   __shared__ int last;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -154,9 +171,11 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     c.ws->skipped = skipped(c);
   }
   if (skipped(c)) return;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < c.n; i += kThreads) c.io[i] = s.io[i];
   const int ei = entry_of_chunk(c);
   const Entry& e = c.entries[ei];
-  const Io& io = c.io[ei];
+  const Io& io = s.io[e.item];
   const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
   const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
   const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
@@ -211,7 +230,18 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     for (int i = 1; i < kThreads / 32; ++i) d += red[i];
     c.inv[unit] = (float)(1.0 / (sqrt(d) + c.eps));
     c.ticket[unit] = 0u;
+    c.done[unit] = 0u;
   }
+}
+
+// x times kScale as a sum of two binary16 numbers, the second times kLoScale.
+__device__ __forceinline__ void split(float x, __half* hi, __half* lo) {
+  *hi = __float2half_rn(x);
+  *lo = __float2half_rn(__fmul_rn(__fadd_rn(x, -__half2float(*hi)), kLoScale));
+}
+
+__device__ __forceinline__ float joined(__half hi, __half lo) {
+  return __fmaf_rn(__half2float(lo), 1.0f / kLoScale, __half2float(hi));
 }
 
 // Stage 2.  Reads U's sources again (from L2 where they fit) and writes X.
@@ -220,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
   if (skipped(c)) return;
   const int ei = entry_of_chunk(c);
   const Entry& e = c.entries[ei];
-  const Io& io = c.io[ei];
+  const Io& io = c.io[e.item];
   const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
   const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
   const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
@@ -245,11 +275,13 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
 #pragma unroll
       for (int j = 0; j < kVec; ++j) u[j] = x[j];
     }
-    // rows of the workspace are multiples of 16 numbers: the vector fits
-    float* to = e.x[0] + base + (int64_t)row * e.ldx + col;
+    __align__(16) __half hi[kVec], lo[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) u[j] = __fmul_rn(u[j], inv);
-    store8(to, kVec, true, u);
+    for (int j = 0; j < kVec; ++j) split(__fmul_rn(__fmul_rn(u[j], inv), kScale), &hi[j], &lo[j]);
+    // rows of the workspace are multiples of 16 numbers: the vector fits
+    const int64_t to = base + (int64_t)row * e.ldx + col;
+    *reinterpret_cast<uint4*>(e.x[0] + to) = *reinterpret_cast<const uint4*>(hi);
+    *reinterpret_cast<uint4*>(e.lo + to) = *reinterpret_cast<const uint4*>(lo);
   }
 }
 
@@ -272,81 +304,6 @@ __device__ __forceinline__ void finish(const Call& c, const Entry& e, const Io& 
   if (io.master) io.master[at] = w;
   if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[at] = as<__half>(w);
   else static_cast<__nv_bfloat16*>(io.out)[at] = as<__nv_bfloat16>(w);
-}
-
-// Stage 3, one product of every matrix: 64 x 64 tiles of binary32 sums.
-// which: 0 A = X X^T, 1 B = b A + c A A, 2 X <- a X + B X.
-__global__ void __launch_bounds__(kThreads) muon_product_kernel(const __grid_constant__ Call c,
-                                                                int which, int cur, int last,
-                                                                float ca, float cb, float cc) {
-  __shared__ float sa[16][65], sb[16][65];
-  if (skipped(c)) return;
-  int64_t t = blockIdx.x;
-  int ei = 0, tm = 0, tn = 0;
-  for (; ei < c.n; ++ei) {
-    const Entry& e = c.entries[ei];
-    const int m = which == 2 ? e.rows : e.k, n = which == 2 ? e.cols : e.k;
-    tm = (m + 63) / 64;
-    tn = (n + 63) / 64;
-    if (t < (int64_t)tm * tn * e.batch) break;
-    t -= (int64_t)tm * tn * e.batch;
-  }
-  if (ei == c.n) return;
-  const Entry& e = c.entries[ei];
-  const int b = (int)(t / (tm * tn)), m0 = (int)(t % (tm * tn)) / tn * 64,
-            n0 = (int)(t % (tm * tn)) % tn * 64;
-  const int M = which == 2 ? e.rows : e.k, N = which == 2 ? e.cols : e.k;
-  const int K = which == 0 ? e.l : e.k;
-  const float* x = e.x[cur] + (int64_t)b * e.rows * e.ldx;
-  const float* A = e.a + (int64_t)b * e.k * e.ldk;
-  const float* B = e.b + (int64_t)b * e.k * e.ldk;
-  // D[m][n] = sum over k of P(m, k) Q(n, k)
-  auto left = [&](int m, int k) -> float {
-    if (m >= M || k >= K) return 0.0f;
-    if (which == 0) return (e.tall ? x[(int64_t)k * e.ldx + m] : x[(int64_t)m * e.ldx + k]);
-    if (which == 1) return (A[(int64_t)m * e.ldk + k]);
-    return (e.tall ? x[(int64_t)m * e.ldx + k] : B[(int64_t)m * e.ldk + k]);
-  };
-  auto right = [&](int n, int k) -> float {
-    if (n >= N || k >= K) return 0.0f;
-    if (which == 0) return (e.tall ? x[(int64_t)k * e.ldx + n] : x[(int64_t)n * e.ldx + k]);
-    if (which == 1) return (A[(int64_t)n * e.ldk + k]);
-    return (e.tall ? B[(int64_t)n * e.ldk + k] : x[(int64_t)k * e.ldx + n]);
-  };
-  float acc[4][4] = {};
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  for (int k0 = 0; k0 < K; k0 += 16) {
-    for (int i = threadIdx.x; i < 64 * 16; i += kThreads) {
-      sa[i % 16][i / 16] = left(m0 + i / 16, k0 + i % 16);
-      sb[i % 16][i / 16] = right(n0 + i / 16, k0 + i % 16);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __fmaf_rn(sa[k][ty + 16 * i], sb[k][tx + 16 * j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int row = m0 + ty + 16 * i, col = n0 + tx + 16 * j;
-      if (row >= M || col >= N) continue;
-      const float d = acc[i][j];
-      const int64_t at = (int64_t)b * e.k * e.ldk + (int64_t)row * e.ldk + col;
-      if (which == 0) {
-        e.a[at] = d;
-      } else if (which == 1) {
-        e.b[at] = __fmaf_rn(cb, e.a[at], __fmul_rn(cc, d));
-      } else {
-        const int64_t ax = ((int64_t)b * e.rows + row) * e.ldx + col;
-        const float y = __fmaf_rn(ca, e.x[cur][ax], d);
-        if (last) finish(c, e, c.io[ei], b, row, col, y);
-        else e.x[cur ^ 1][ax] = y;
-      }
-    }
 }
 
 }  // namespace zm
