@@ -797,7 +797,8 @@ def zero_muon_launch_count(h) -> int:
 
 # ---------------------------------------------------------------- query/key norm and rotation
 
-# Shapes a handle was made for, so that the binding can check tensors against them.
+# What a handle was made for, so that the binding can check tensors against it:
+# head counts, head_dim, rotary_dim / 2, dtype, gain_per_head.
 _qk_configs = {}
 
 
@@ -824,55 +825,65 @@ def zero_qk_destroy(h) -> None:
     _check(lib().zero_qk_destroy(h), "zero_qk_destroy")
 
 
-def _qk_bad(name, what):
-    raise ValueError(f"{name} must be {what}")
+def _qk_heads(t, name, n, heads, dim, dtype, dev):
+    """(address, token stride, head stride) of a [tokens, heads, D] tensor."""
+    if t.dtype is not dtype or t.shape != (n, heads, dim) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a {dtype} tensor of {(n, heads, dim)} on cuda:{dev}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    return t.data_ptr(), st, sh
 
 
-def _qk_data(t, name, shape, dtype, device):
-    if t.dtype != dtype or t.shape != shape or t.device != device or \
-            (t.stride(2) != 1 and shape[2] > 1):
-        _qk_bad(name, f"a {dtype} tensor of {tuple(shape)} on {device} with contiguous heads")
-    return zero_qk_tensor(t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _qk_gain(t, name, heads, dim, per_head, device):
+def _qk_gain(t, name, heads, dim, per_head, dev):
     import torch
     shape = (heads, dim) if per_head else (dim,)
-    if t.dtype != torch.float32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        _qk_bad(name, f"a contiguous float32 tensor of {shape} on {device}")
+    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != dev \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {shape} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions):
+def _qk_call(fn, h, ins, outs, grads, gains, dgains, cos, sin, positions, stream):
+    """Check the tensors against the handle and make the call.  ins, outs,
+    grads: (name, query tensor, key tensor); gains, dgains: (query's, key's)."""
     import torch
-    if h not in _qk_configs:
+    cfg = _qk_configs.get(h)
+    if cfg is None:
         raise ValueError("not a handle of zero_qk_create")
-    hq, hk, dim, half, dtype, per_head = _qk_configs[h]
-    if not q.is_cuda or q.device.index != torch.cuda.current_device():
+    hq, hk, dim, half, dtype, per_head = cfg
+    q = ins[1]
+    dev, n = q.get_device(), q.shape[0]
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("q must be a CUDA tensor of the current device")
-    dev, n = q.device, q.shape[0]
-    b = zero_qk_buffers()
-    b.tokens = n
-    b.q = _qk_data(q, "q", (n, hq, dim), dtype, dev)
-    if hk:
-        b.k = _qk_data(k, "k", (n, hk, dim), dtype, dev)
-    if q_gain is not None:
-        b.q_gain = _qk_gain(q_gain, "q_gain", hq, dim, per_head, dev)
-    if k_gain is not None and hk:
-        b.k_gain = _qk_gain(k_gain, "k_gain", hk, dim, per_head, dev)
+    at = []
+    for name, tq, tk in (ins, outs, grads):
+        at.append(zero_qk_tensor(*_qk_heads(tq, name % "q", n, hq, dim, dtype, dev))
+                  if tq is not None else zero_qk_tensor())
+        at.append(zero_qk_tensor(*_qk_heads(tk, name % "k", n, hk, dim, dtype, dev))
+                  if hk and tk is not None else zero_qk_tensor())
+    gain = [None if t is None or not heads else _qk_gain(t, name, heads, dim, per_head, dev)
+            for name, t, heads in (("q_gain", gains[0], hq), ("k_gain", gains[1], hk),
+                                   ("dq_gain", dgains[0], hq), ("dk_gain", dgains[1], hk))]
+    n_pos, pc, ps = 0, None, None
     if half:
         for name, t in (("cos", cos), ("sin", sin)):
-            if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != half or t.device != dev \
-                    or not t.is_contiguous():
-                _qk_bad(name, f"a contiguous float32 tensor of (positions, {half}) on {dev}")
-        if cos.shape != sin.shape:
+            if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != half \
+                    or t.get_device() != dev or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous float32 tensor of (positions, "
+                                 f"{half}) on cuda:{dev}")
+        n_pos, pc, ps = cos.shape[0], cos.data_ptr(), sin.data_ptr()
+        if sin.shape[0] != n_pos:
             raise ValueError("cos and sin must have the same shape")
-        b.n_pos, b.cos, b.sin = cos.shape[0], cos.data_ptr(), sin.data_ptr()
-    if positions.shape != (n,) or positions.device != dev or not positions.is_contiguous() or \
-            positions.dtype not in (torch.int64, torch.int32):
-        _qk_bad("positions", f"a contiguous int64 or int32 tensor of ({n},) on {dev}")
-    b.positions, b.positions64 = positions.data_ptr(), int(positions.dtype == torch.int64)
-    return b, (n, hq, dim), (n, hk, dim), dtype, dev, per_head
+    wide = positions.dtype is torch.int64
+    if positions.shape != (n,) or positions.get_device() != dev or not positions.is_contiguous() \
+            or not (wide or positions.dtype is torch.int32):
+        raise ValueError(f"positions must be a contiguous int64 or int32 tensor of ({n},) on "
+                         f"cuda:{dev}")
+    b = zero_qk_buffers(n, n_pos, *at, *gain, pc, ps, positions.data_ptr(), wide, 0)
+    if stream is None:
+        stream = torch.cuda.current_stream(dev).cuda_stream
+    _check(getattr(lib(), fn)(h, ctypes.byref(b), _stream(stream)), fn)
 
 
 def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions,
@@ -881,11 +892,8 @@ def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions
     `q_out` and `k_out` (which may be `q` and `k`).  `k`, `k_out` are not looked
     at by a handle with k_heads 0; a gain may be None (ones).  A token of
     position -1 is padding and gets zeros."""
-    b, sq, sk, dtype, dev, _ = _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions)
-    b.q_out = _qk_data(q_out, "q_out", sq, dtype, dev)
-    if sk[1]:
-        b.k_out = _qk_data(k_out, "k_out", sk, dtype, dev)
-    _check(lib().zero_qk_norm_rope(h, ctypes.byref(b), _stream(stream)), "zero_qk_norm_rope")
+    _qk_call("zero_qk_norm_rope", h, ("%s", q, k), ("%s_out", q_out, k_out), ("", None, None),
+             (q_gain, k_gain), (None, None), cos, sin, positions, stream)
 
 
 def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain, q_gain, k_gain,
@@ -893,18 +901,8 @@ def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain
     """Gradients of `zero_qk_norm_rope`: from `dq_out`, `dk_out` and the
     forward call's inputs into `dq`, `dk` (which may be `dq_out`, `dk_out`) and
     the gains' float32 gradients (None: not wanted)."""
-    b, sq, sk, dtype, dev, per_head = _qk_buffers(h, q, k, q_gain, k_gain, cos, sin, positions)
-    b.q_out = _qk_data(dq_out, "dq_out", sq, dtype, dev)
-    b.dq = _qk_data(dq, "dq", sq, dtype, dev)
-    if sk[1]:
-        b.k_out = _qk_data(dk_out, "dk_out", sk, dtype, dev)
-        b.dk = _qk_data(dk, "dk", sk, dtype, dev)
-        if dk_gain is not None:
-            b.dk_gain = _qk_gain(dk_gain, "dk_gain", sk[1], sk[2], per_head, dev)
-    if dq_gain is not None:
-        b.dq_gain = _qk_gain(dq_gain, "dq_gain", sq[1], sq[2], per_head, dev)
-    _check(lib().zero_qk_norm_rope_backward(h, ctypes.byref(b), _stream(stream)),
-           "zero_qk_norm_rope_backward")
+    _qk_call("zero_qk_norm_rope_backward", h, ("%s", q, k), ("d%s_out", dq_out, dk_out),
+             ("d%s", dq, dk), (q_gain, k_gain), (dq_gain, dk_gain), cos, sin, positions, stream)
 
 
 def zero_qk_launch_count(h) -> int:

@@ -378,40 +378,43 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int64_t total = (2ll * starts[p.c.n] + starts[2 * p.c.n + 1]) * p.steps;
   const int first = blockIdx.x / kPair, stride = gridDim.x / kPair;
 
-  if (warp == 0 && lane == 0) {
-    // ---- TMA
+  if (warp == 0) {
+    // ---- TMA.  The warp walks together; one lane issues.
     uint32_t s = 0, phase = 1;
     int64_t issued = 0;
     bool ok = true;
     for (int64_t index = first; ok && index < total; index += stride) {
       const Tile t = tile_at<kPair>(p, starts, index);
       const Entry& e = p.c.entries[t.entry];
-      if (t.need) {
-        ok = count_wait(p.c.done + t.unit, t.need, fault);
-        if (!ok) break;
-        fence_proxy_async();
-      }
+      const Side sa = side_of(e, t.which, 0), sb = side_of(e, t.which, 1);
       const CUtensorMap* map = p.maps + 4 * t.entry;
       const CUtensorMap* mx = map + (t.step & 1);
-      const Side sa = side_of(e, t.which, 0), sb = side_of(e, t.which, 1);
       const CUtensorMap* ma = sa == kSymmetric ? map + 1 + t.which : mx;
       const CUtensorMap* mb = sb == kSymmetric ? map + 1 + t.which : mx;
       const int am = t.i * kTile, bm = t.j * kTile;
       const int a0 = am + (int)rank * 128, b0 = bm + (int)rank * 128;
       const int depth = t.which == 0 ? e.l : e.k;
+      if (t.need) {
+        ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
+        if (!ok) break;
+        fence_proxy_async();
+      }
       for (int k0 = 0; k0 < depth; k0 += 64) {
-        ok = mbar_wait(empty + 8 * s, phase, fault);
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
         const uint32_t bar = kPair == 2 ? peer(full + 8 * s, 0) : full + 8 * s;
-        if (rank == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
         const uint32_t to = stages + s * kStageBytes;
         const bool xa = across<kPair>(sa, am, k0), xb = across<kPair>(sb, bm, k0);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          tma_load<kPair>(to + q * kBoxBytes, ma, bar, xa ? a0 + 64 * q : k0, xa ? k0 : a0 + 64 * q, t.b);
-          tma_load<kPair>(to + kOperandBytes + q * kBoxBytes, mb, bar, xb ? b0 + 64 * q : k0,
-                          xb ? k0 : b0 + 64 * q, t.b);
+        const int ax = xa ? a0 : k0, ay = xa ? k0 : a0, bx = xb ? b0 : k0, by = xb ? k0 : b0;
+        const int adx = xa ? 64 : 0, ady = 64 - adx, bdx = xb ? 64 : 0, bdy = 64 - bdx;
+        if (elected()) {
+          if (rank == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
+          tma_load<kPair>(to, ma, bar, ax, ay, t.b);
+          tma_load<kPair>(to + kBoxBytes, ma, bar, ax + adx, ay + ady, t.b);
+          tma_load<kPair>(to + kOperandBytes, mb, bar, bx, by, t.b);
+          tma_load<kPair>(to + kOperandBytes + kBoxBytes, mb, bar, bx + bdx, by + bdy, t.b);
         }
+        __syncwarp();
         ++issued;
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
@@ -419,24 +422,23 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // Every stage that was filled is released (or, after a fault, has at
     // least arrived) before the CTA may end.
     if (ok) {
-      for (int q = 0; q < kStages && q < issued; ++q) {
+      for (int q = 0; ok && q < kStages && q < issued; ++q) {
         ok = mbar_wait(empty + 8 * s, phase, fault);
-        if (!ok) break;
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
     }
-    if (!ok) {
+    if (!ok && rank == 0) {
       const uint64_t t0 = now_ns();
       const int held = (int)(issued < kStages ? issued : kStages);
-      for (int q = 0; rank == 0 && q < held; ++q) {
+      for (int q = 0; q < held; ++q) {
         const int64_t at = issued - held + q;
         while (!mbar_try(full + 8 * (uint32_t)(at % kStages), (uint32_t)(at / kStages) & 1) &&
                now_ns() - t0 < 1000000000ull) {
         }
       }
     }
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---- products
+  } else if (warp == 1 && rank == 0) {
+    // ---- products.  The warp walks together; one lane issues.
     uint32_t s = 0, phase = 0, acc = 0, acc_phase = 1;
     bool ok = true;
     for (int64_t index = first; ok && index < total; index += stride) {
@@ -445,31 +447,32 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const Side sa = side_of(e, t.which, 0), sb = side_of(e, t.which, 1);
       const int am = t.i * kTile, bm = t.j * kTile;
       const int depth = t.which == 0 ? e.l : e.k;
-      ok = mbar_wait(acc_empty + 8 * acc, acc_phase, fault);
+      ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * acc, acc_phase, fault));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kTile;
       for (int k0 = 0; k0 < depth; k0 += 64) {
-        ok = mbar_wait(full + 8 * s, phase, fault);
-        if (!ok) break;
-        tc_fence_after();
         const bool xa = across<kPair>(sa, am, k0), xb = across<kPair>(sb, bm, k0);
         const uint32_t idesc = instruction(kTile, kTile, xa, xb);
         const uint32_t at = stages + s * kStageBytes;
         const uint64_t da = operand(at, kBoxBytes), db = operand(at + kOperandBytes, kBoxBytes);
         // 16 deep: 32 bytes along a row, or 16 rows of 128 bytes
         const uint64_t ia = xa ? 16 * 128 >> 4 : 32 >> 4, ib = xb ? 16 * 128 >> 4 : 32 >> 4;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mma_f16<kPair>(d, da + q * ia, db + q * ib, idesc, k0 > 0 || q > 0);
-        mma_commit<kPair>(empty + 8 * s);
+        ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, phase, fault));
+        if (!ok) break;
+        tc_fence_after();
+        if (elected()) {
+          mma_f16_x4<kPair>(d, da, db, ia, ib, idesc, k0 > 0);
+          mma_commit<kPair>(empty + 8 * s);
+          if (k0 + 64 >= depth) mma_commit<kPair>(acc_full + 8 * acc);
+        }
+        __syncwarp();
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
-      if (!ok) break;
-      mma_commit<kPair>(acc_full + 8 * acc);
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
     if (!ok) {   // products in flight still read shared memory and write TMEM
-      mma_commit<kPair>(drain);
+      if (elected()) mma_commit<kPair>(drain);
       const uint64_t t0 = now_ns();
       while (!mbar_try(drain, 0) && now_ns() - t0 < 1000000000ull) {
       }

@@ -12,12 +12,17 @@
 // lane: without interleaving the vectors are V numbers of the first rotated
 // half and the V numbers they pair with; interleaved they are 2V numbers in a
 // row.  So the rotation needs no exchange between lanes, and a 16-byte load
-// per vector covers whole sectors.
+// per vector covers whole sectors.  A group owns R heads for the whole launch
+// and walks the tokens: the R rows of a token are loaded together, which puts
+// enough bytes in flight to cover memory's latency, share one read of the
+// token's angles, and keep their gains' gradients in registers to the end.
+// The next token's position is fetched ahead, since the angles wait for it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <mutex>
 #include <new>
 
 #include "host_util.h"
@@ -29,6 +34,7 @@ using zo::fail;
 
 constexpr int kQkThreads = 256;
 constexpr int kMaxDim = 512;
+constexpr int kMaxPerSm = 4;      // CTAs an SM: what the workspace has room for
 
 struct Rows {
   const char* in;      // x
@@ -48,8 +54,9 @@ struct QkArgs {
   float* part;         // backward: [grid][rows a CTA][D] partial gain gradients
   int32_t pos64, dim, rot, chunks, lanes, gain_per_head;
   int32_t heads;       // of both
+  int32_t per;         // groups a token in a CTA, each of R heads
   int32_t head_blocks; // CTAs side by side over the heads
-  int32_t reps;        // tokens a CTA takes at once when its heads are few
+  int32_t reps;        // tokens a CTA takes at once
   int32_t part_rows;   // rows of a CTA's partial: 2 (shared gains) or its heads
   float eps, inv_dim;
 };
@@ -70,9 +77,20 @@ template <> struct Num<float> {
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
 
+// A row is read once: past L1, which is left to the angles and gains.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const char* base, int64_t e) {
-  return *reinterpret_cast<const Vec<T, V>*>(reinterpret_cast<const T*>(base) + e);
+  const T* p = reinterpret_cast<const T*>(base) + e;
+  Vec<T, V> x;
+  if constexpr (sizeof(x) == 16) {
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    x = *reinterpret_cast<const Vec<T, V>*>(&u);
+  } else {
+    x = *reinterpret_cast<const Vec<T, V>*>(p);
+  }
+  return x;
 }
 
 // Where the two vectors of chunk c start.
@@ -116,95 +134,121 @@ __device__ __forceinline__ void load_f(const float* p, float* x) {
   }
 }
 
-// V numbers a vector, C chunks a lane.  A group of a.lanes lanes owns one head
-// for the whole launch (its gain stays in registers) and walks the tokens.
-template <typename T, int V, int C, bool kInter, bool kBackward>
-__global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ QkArgs a) {
+// V numbers a vector, C chunks a lane, R heads a group.
+template <typename T, int V, int C, int R, bool kInter, bool kBackward>
+__global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant__ QkArgs a) {
   extern __shared__ float s_part[];
-  const int lanes = a.lanes, groups = kQkThreads / lanes;
+  const int lanes = a.lanes;
   const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   // the group's lanes of its warp: groups of one warp walk on by themselves
   const unsigned mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u)
                         << (threadIdx.x % 32 / lanes * lanes);
   const int block = blockIdx.x % a.head_blocks;
-  const int per = min(groups, a.heads);       // heads side by side in a CTA
-  const int rep = group / per;
-  const int head = block * per + group % per;
-  const bool on = rep < a.reps && head < a.heads;
-  const int which = on && head >= a.r[0].heads ? 1 : 0;
-  const Rows& r = a.r[which];
-  const int h = head - (which ? a.r[0].heads : 0);
+  const int rep = group / a.per;
+  // head j of the group: adjacent groups take adjacent heads
+  const int head0 = block * a.per * R + group % a.per;
+  const bool on = rep < a.reps && head0 < a.heads;
   const int64_t slots = (int64_t)(gridDim.x / a.head_blocks) * a.reps;
-
-  float gain[C][2 * V], dgain[C][2 * V];
   int p0[C], p1[C];
 #pragma unroll
-  for (int j = 0; j < C; ++j) {
-    const int c = lane + j * lanes;
-    places<V, kInter>(a, min(c, a.chunks - 1), &p0[j], &p1[j]);
-#pragma unroll
-    for (int i = 0; i < 2 * V; ++i) {
-      gain[j][i] = 1.0f;
-      dgain[j][i] = 0.0f;
-      if (on && r.gain && c < a.chunks)
-        gain[j][i] = __ldg(r.gain + (a.gain_per_head ? (int64_t)h * a.dim : 0) +
-                           (i < V ? p0[j] + i : p1[j] + i - V));
-    }
-  }
+  for (int j = 0; j < C; ++j) places<V, kInter>(a, min(lane + j * lanes, a.chunks - 1), &p0[j], &p1[j]);
+  const auto which = [&](int r) { return head0 + r * a.per >= a.r[0].heads ? 1 : 0; };
+  const auto local = [&](int r) { return head0 + r * a.per - (which(r) ? a.r[0].heads : 0); };
 
-  if (on)
-    for (int64_t t = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep; t < a.tokens; t += slots) {
-      const int64_t p = position(a, t);
-      const int64_t o_out = t * r.out_t + (int64_t)h * r.out_h;
-      if (p < 0 || (p >= a.n_pos && a.rot > 0)) {
-        // padding, or no angle for this position: no row and no table is read
-        const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
+  float dgain[kBackward ? R : 1][C][2 * V];
+  if (kBackward)
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = 0.0f;
+
+  int64_t t = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep;
+  int64_t next = on && t < a.tokens ? position(a, t) : 0;
+  for (; on && t < a.tokens; t += slots) {
+    const int64_t p = next;
+    if (t + slots < a.tokens) next = position(a, t + slots);
+    if (p < 0 || (p >= a.n_pos && a.rot > 0)) {
+      // padding, or no angle for this position: no row and no table is read
+      const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (head0 + r * a.per >= a.heads) continue;
+        const Rows& w = a.r[which(r)];
+        T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
 #pragma unroll
         for (int j = 0; j < C; ++j) {
           if (lane + j * lanes >= a.chunks) continue;
-          Vec<T, V> w;
+          Vec<T, V> z;
 #pragma unroll
-          for (int i = 0; i < V; ++i) w.v[i] = fill;
-          *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p0[j]) = w;
-          *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p1[j]) = w;
+          for (int i = 0; i < V; ++i) z.v[i] = fill;
+          *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = z;
+          *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = z;
           if (kBackward && p >= 0)
 #pragma unroll
-            for (int i = 0; i < 2 * V; ++i) dgain[j][i] = __int_as_float(0x7fffffff);
+            for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = __int_as_float(0x7fffffff);
         }
-        continue;
       }
-      const int64_t o_in = t * r.in_t + (int64_t)h * r.in_h;
-      float x[C][2 * V], g[C][2 * V], cs[C][V], sn[C][V];
+      continue;
+    }
+    Vec<T, V> xr[R][C][2], gr[kBackward ? R : 1][C][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (head0 + r * a.per >= a.heads) continue;
+      const Rows& w = a.r[which(r)];
+      const int64_t o_in = t * w.in_t + (int64_t)local(r) * w.in_h;
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        if (lane + j * lanes >= a.chunks) continue;
+        xr[r][j][0] = load<T, V>(w.in, o_in + p0[j]);
+        xr[r][j][1] = load<T, V>(w.in, o_in + p1[j]);
+        if constexpr (kBackward) {
+          const int64_t o_g = t * w.go_t + (int64_t)local(r) * w.go_h;
+          gr[r][j][0] = load<T, V>(w.gout, o_g + p0[j]);
+          gr[r][j][1] = load<T, V>(w.gout, o_g + p1[j]);
+        }
+      }
+    }
+    float cs[C][V], sn[C][V];
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      const int c = lane + j * lanes;
+      if (c < a.chunks && c * 2 * V < a.rot) {
+        load_f<V>(a.cos + p * (a.rot / 2) + c * V, cs[j]);
+        load_f<V>(a.sin + p * (a.rot / 2) + c * V, sn[j]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (head0 + r * a.per >= a.heads) continue;
+      const Rows& w = a.r[which(r)];
+      float x[C][2 * V], g[C][2 * V], gain[C][2 * V];
       float sq = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         const int c = lane + j * lanes;
-        const bool live = c < a.chunks, turned = live && c * 2 * V < a.rot;
-        if (live) {
-          const Vec<T, V> u = load<T, V>(r.in, o_in + p0[j]), v = load<T, V>(r.in, o_in + p1[j]);
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            x[j][i] = Num<T>::get(u.v[i]);
-            x[j][V + i] = Num<T>::get(v.v[i]);
-          }
-          if (kBackward) {
-            const int64_t o_g = t * r.go_t + (int64_t)h * r.go_h;
-            const Vec<T, V> y = load<T, V>(r.gout, o_g + p0[j]), z = load<T, V>(r.gout, o_g + p1[j]);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-              g[j][i] = Num<T>::get(y.v[i]);
-              g[j][V + i] = Num<T>::get(z.v[i]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 2 * V; ++i) x[j][i] = g[j][i] = 0.0f;
+        for (int i = 0; i < 2 * V; ++i) {
+          gain[j][i] = 1.0f;
+          x[j][i] = g[j][i] = 0.0f;
         }
-        if (turned) {
-          load_f<V>(a.cos + p * (a.rot / 2) + c * V, cs[j]);
-          load_f<V>(a.sin + p * (a.rot / 2) + c * V, sn[j]);
-          if (kBackward) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
+        if (c >= a.chunks) continue;
+        if (w.gain) {
+          const float* gp = w.gain + (a.gain_per_head ? (int64_t)local(r) * a.dim : 0);
+          load_f<V>(gp + p0[j], gain[j]);
+          load_f<V>(gp + p1[j], gain[j] + V);
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          x[j][i] = Num<T>::get(xr[r][j][0].v[i]);
+          x[j][V + i] = Num<T>::get(xr[r][j][1].v[i]);
+          if constexpr (kBackward) {
+            g[j][i] = Num<T>::get(gr[r][j][0].v[i]);
+            g[j][V + i] = Num<T>::get(gr[r][j][1].v[i]);
+          }
+        }
+        if (kBackward && c * 2 * V < a.rot) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
           sq = __fmaf_rn(x[j][i], x[j][i], sq);
@@ -218,6 +262,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
       const float inv = rsqrtf(__fmaf_rn(sq, a.inv_dim, a.eps));
       const float back = kBackward ? __fmul_rn(__fmul_rn(inv, __fmul_rn(inv, inv)),
                                                __fmul_rn(dot, a.inv_dim)) : 0.0f;
+      T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
         const int c = lane + j * lanes;
@@ -225,8 +270,8 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
         float y[2 * V];
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) {
-          if (kBackward) {
-            dgain[j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[j][i]);
+          if constexpr (kBackward) {
+            dgain[r][j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[r][j][i]);
             y[i] = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), inv, -__fmul_rn(x[j][i], back));
           } else {
             y[i] = __fmul_rn(__fmul_rn(x[j][i], inv), gain[j][i]);
@@ -239,32 +284,42 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
           u.v[i] = Num<T>::put(y[i]);
           v.v[i] = Num<T>::put(y[V + i]);
         }
-        *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p0[j]) = u;
-        *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(r.out) + o_out + p1[j]) = v;
+        *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = u;
+        *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = v;
       }
     }
+  }
 
-  if (kBackward && a.part) {
-    // The CTA's share of the gains' gradients: each group's sums to shared
-    // memory, then each column added over the groups of one gain in order.
-#pragma unroll
-    for (int j = 0; j < C; ++j) {
-      if (lane + j * lanes >= a.chunks) continue;
-#pragma unroll
-      for (int i = 0; i < 2 * V; ++i)
-        s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on ? dgain[j][i] : 0.0f;
-    }
-    __syncthreads();
+  if constexpr (kBackward) {
+    if (!a.part) return;
+    // The CTA's share of the gains' gradients: a head a group at a time to
+    // shared memory, each column then added over the groups in order.
+    const int groups = kQkThreads / lanes;
     float* to = a.part + (int64_t)blockIdx.x * a.part_rows * a.dim;
-    for (int e = threadIdx.x; e < a.part_rows * a.dim; e += kQkThreads) {
-      const int row = e / a.dim, d = e % a.dim;
-      float s = 0.0f;
-      for (int k = 0; k < groups; ++k) {
-        const int hd = block * per + k % per;
-        const int mine = a.gain_per_head ? k % per : (hd >= a.r[0].heads ? 1 : 0);
-        if (mine == row) s = __fadd_rn(s, s_part[k * a.dim + d]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        if (lane + j * lanes >= a.chunks) continue;
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i)
+          s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on ? dgain[r][j][i] : 0.0f;
       }
-      to[e] = s;
+      __syncthreads();
+      // shared gains: two rows that grow with r; gains of a head: its own row
+      const int rows = a.gain_per_head ? a.per : 2;
+      for (int e = threadIdx.x; e < rows * a.dim; e += kQkThreads) {
+        const int row = e / a.dim, d = e % a.dim;
+        float s = 0.0f;
+        for (int k = 0; k < groups; ++k) {
+          const int hd = block * a.per * R + k % a.per + r * a.per;
+          const int mine = a.gain_per_head ? k % a.per : (hd >= a.r[0].heads ? 1 : 0);
+          if (mine == row && hd < a.heads) s = __fadd_rn(s, s_part[k * a.dim + d]);
+        }
+        if (a.gain_per_head) to[r * a.per * a.dim + e] = s;
+        else to[e] = r ? __fadd_rn(to[e], s) : s;
+      }
     }
   }
 }
@@ -306,20 +361,26 @@ bool fits(const void* p, int64_t s0, int64_t s1, int bytes, int esize) {
 }
 
 template <typename T, bool kInter, bool kBackward>
-const void* kernel_for(int v) {
+const void* kernel_for(int v, int r) {
   if constexpr (sizeof(T) == 2)
-    if (v == 8) return (const void*)qk_kernel<T, 8, 1, kInter, kBackward>;
+    if (v == 8) {
+      if constexpr (!kBackward)
+        if (r == 4) return (const void*)qk_kernel<T, 8, 1, 4, kInter, kBackward>;
+      if (r == 2) return (const void*)qk_kernel<T, 8, 1, 2, kInter, kBackward>;
+      return (const void*)qk_kernel<T, 8, 1, 1, kInter, kBackward>;
+    }
   switch (v) {
-    case 4: return (const void*)qk_kernel<T, 4, 2, kInter, kBackward>;
-    case 2: return (const void*)qk_kernel<T, 2, 4, kInter, kBackward>;
-    default: return (const void*)qk_kernel<T, 1, 8, kInter, kBackward>;
+    case 4: return r == 2 ? (const void*)qk_kernel<T, 4, 2, 2, kInter, kBackward>
+                          : (const void*)qk_kernel<T, 4, 2, 1, kInter, kBackward>;
+    case 2: return (const void*)qk_kernel<T, 2, 4, 1, kInter, kBackward>;
+    default: return (const void*)qk_kernel<T, 1, 8, 1, kInter, kBackward>;
   }
 }
 
 template <typename T>
-const void* kernel_of(bool inter, bool backward, int v) {
-  if (inter) return backward ? kernel_for<T, true, true>(v) : kernel_for<T, true, false>(v);
-  return backward ? kernel_for<T, false, true>(v) : kernel_for<T, false, false>(v);
+const void* kernel_of(bool inter, bool backward, int v, int r) {
+  if (inter) return backward ? kernel_for<T, true, true>(v, r) : kernel_for<T, true, false>(v, r);
+  return backward ? kernel_for<T, false, true>(v, r) : kernel_for<T, false, false>(v, r);
 }
 
 }  // namespace
@@ -329,9 +390,28 @@ struct zero_qk_handle {
   bool has_device = false;
   int device = -1;
   int sms = 0;
-  int max_grid = 0;
   float* part = nullptr;
   int64_t launches = 0;
+  std::mutex mu;
+  struct {
+    const void* fn;
+    int ctas;
+  } occ[16] = {};     // kernel -> CTAs an SM; a handle's type and pairing leave 13
+
+  // CTAs of a kernel that an SM holds at once, at most kMaxPerSm.
+  int resident(const void* fn, int smem) {
+    std::lock_guard<std::mutex> lock(mu);
+    for (auto& o : occ) {
+      if (o.fn == fn) return o.ctas;
+      if (o.fn) continue;
+      int n = 0;
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kQkThreads, smem) != cudaSuccess) n = 1;
+      o.ctas = std::max(1, std::min(n, kMaxPerSm));
+      o.fn = fn;
+      return o.ctas;
+    }
+    return 1;
+  }
 };
 
 namespace {
@@ -397,6 +477,7 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     bool ok = c.head_dim % (2 * v) == 0 && c.rotary_dim % (2 * v) == 0;
     const int fb = std::min(v, 4) * 4;
     ok = ok && (c.rotary_dim == 0 || (fits(b->cos, 0, 0, fb, 4) && fits(b->sin, 0, 0, fb, 4)));
+    ok = ok && fits(b->q_gain, 0, 0, fb, 4) && (c.k_heads == 0 || fits(b->k_gain, 0, 0, fb, 4));
     for (int w = 0; ok && w < (c.k_heads > 0 ? 2 : 1); ++w) {
       ok = fits(in[w]->data, in[w]->token_stride, in[w]->head_stride, v * es, es) &&
            fits(out[w]->data, out[w]->token_stride, out[w]->head_stride, v * es, es);
@@ -425,19 +506,29 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     }
     r.gain = w ? b->k_gain : b->q_gain;
   }
-  const int groups = kQkThreads / a.lanes, per = std::min(groups, a.heads);
-  a.head_blocks = (a.heads + per - 1) / per;
-  a.reps = std::max(1, groups / per);
-  a.part_rows = c.gain_per_head ? per : 2;
+  const int groups = kQkThreads / a.lanes;
+  const int es_vec = v * es;
+  // Heads a group: more rows in flight and fewer reads of the angles, as long
+  // as the heads divide and the tokens still fill the device.
+  int r = 1;
+  const int most_r = es_vec < 16 ? 1 : v == 8 ? (backward ? 2 : 4) : 2;
+  while (2 * r <= most_r && a.heads % (2 * r) == 0 &&
+         b->tokens * a.heads >= (int64_t)2 * r * groups * 2 * h->sms)
+    r *= 2;
+  a.per = std::min(groups, (a.heads + r - 1) / r);
+  a.head_blocks = (a.heads + a.per * r - 1) / (a.per * r);
+  a.reps = std::max(1, groups / a.per);
+  a.part_rows = c.gain_per_head ? a.per * r : 2;
   const bool want = backward && (dgain[0] || dgain[1]);
   a.part = want ? h->part : nullptr;
-  const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, v)
-                   : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, v)
-                                          : kernel_of<float>(c.interleaved, backward, v);
+  const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, v, r)
+                   : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, v, r)
+                                          : kernel_of<float>(c.interleaved, backward, v, r);
   const size_t smem = want ? (size_t)groups * c.head_dim * sizeof(float) : 0;
   const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
   int64_t grid = slots * a.head_blocks;
-  const int64_t most = std::max<int64_t>(1, h->max_grid / a.head_blocks) * a.head_blocks;
+  const int64_t resident = (int64_t)h->resident(fn, (int)smem) * h->sms;
+  const int64_t most = std::max<int64_t>(1, resident / a.head_blocks) * a.head_blocks;
   if (grid > most) grid = most;
   void* params[] = {&a};
   e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kQkThreads), params, smem, s);
@@ -451,7 +542,7 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     f.grid = (int)grid;
     f.head_blocks = a.head_blocks;
     f.part_rows = a.part_rows;
-    f.per = per;
+    f.per = a.per * r;
     f.dim = c.head_dim;
     f.q_heads = c.q_heads;
     f.heads = a.heads;
@@ -497,13 +588,12 @@ zero_status zero_qk_create(const zero_qk_config* cfg, zero_qk_t* out) {
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
-  h->max_grid = 4 * h->sms;
-  // partial gain gradients of every CTA of the largest grid: at most 256 rows
-  // of 2..512 numbers (a group of one lane owns a head of at most 16 numbers)
-  const int64_t rows = cfg->gain_per_head
-                           ? std::min<int64_t>(kQkThreads, (int64_t)cfg->q_heads + cfg->k_heads)
-                           : 2;
-  const int64_t blocks = std::max<int64_t>(h->max_grid, (int64_t)cfg->q_heads + cfg->k_heads);
+  // Partial gain gradients of every CTA of the largest grid.  A CTA's rows are
+  // two, or its heads: at most 256 groups (a group of one lane owns heads of
+  // at most 16 numbers), four heads each.
+  const int64_t heads = (int64_t)cfg->q_heads + cfg->k_heads;
+  const int64_t rows = cfg->gain_per_head ? std::min<int64_t>(4 * kQkThreads, heads + 4) : 2;
+  const int64_t blocks = std::max<int64_t>((int64_t)kMaxPerSm * h->sms, heads);
   if (e == cudaSuccess)
     e = cudaMalloc(reinterpret_cast<void**>(&h->part),
                    (size_t)(blocks * rows * cfg->head_dim) * sizeof(float));

@@ -19,6 +19,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// True in one lane of a warp that is here as a whole.  What it guards is
+// issued with operands that the compiler knows to be the warp's.
+__device__ __forceinline__ bool elected() {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -202,6 +210,16 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
 }
 __device__ __forceinline__ void tmem_load_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Four products, 64 deep: the descriptors' low words step by `ia` and `ib`.
+template <int kPair>
+__device__ __forceinline__ void mma_f16_x4(uint32_t d, uint64_t a, uint64_t b, uint64_t ia, uint64_t ib,
+                                           uint32_t idesc, uint32_t add) {
+  mma_f16<kPair>(d, a, b, idesc, add);
+  mma_f16<kPair>(d, a + ia, b + ib, idesc, 1);
+  mma_f16<kPair>(d, a + 2 * ia, b + 2 * ib, idesc, 1);
+  mma_f16<kPair>(d, a + 3 * ia, b + 3 * ib, idesc, 1);
 }
 
 // Shared-memory operand of a product: 128-byte rows swizzled over groups of
