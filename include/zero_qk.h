@@ -14,8 +14,8 @@
  *   dgain = sum over tokens (and heads, for a shared gain) of dy * x * r
  *   dx    = r * dy * gain - x * r^3 * mean(dy * gain * x)
  *
- * A token whose position is negative is padding: its inputs are not read, its
- * outputs and gradients are zero and it adds nothing to the gains' gradients.
+ * A token whose position is negative is padding: what its inputs hold (NaN
+ * and infinity included) is ignored, its outputs and gradients are zero and it adds nothing to the gains' gradients.
  * A position of n_pos or more has no angle: its rows come out as NaN.
  *
  * Arithmetic is binary32 throughout; results are rounded once, to the data's

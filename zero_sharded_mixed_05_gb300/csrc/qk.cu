@@ -13,10 +13,13 @@
 // half and the V numbers they pair with; interleaved they are 2V numbers in a
 // row.  So the rotation needs no exchange between lanes, and a 16-byte load
 // per vector covers whole sectors.  A group owns R heads for the whole launch
-// and walks the tokens: the R rows of a token are loaded together, which puts
-// enough bytes in flight to cover memory's latency, share one read of the
-// token's angles, and keep their gains' gradients in registers to the end.
-// The next token's position is fetched ahead, since the angles wait for it.
+// and walks the tokens: its R rows of a token share one read of the token's
+// angles, and their gains' gradients stay in registers to the end.
+//
+// 16-byte vectors come by cp.async into a ring of kRing tokens in shared memory
+// in which every thread reads only what it copied itself, so that bytes in
+// flight cost no registers and no barrier; narrower ones are loaded directly.
+// The angles of the next token are fetched while the rows are still on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -77,20 +80,16 @@ template <> struct Num<float> {
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
 
-// A row is read once: past L1, which is left to the angles and gains.
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load(const char* base, int64_t e) {
-  const T* p = reinterpret_cast<const T*>(base) + e;
-  Vec<T, V> x;
-  if constexpr (sizeof(x) == 16) {
-    uint4 u;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
-    x = *reinterpret_cast<const Vec<T, V>*>(&u);
-  } else {
-    x = *reinterpret_cast<const Vec<T, V>*>(p);
-  }
-  return x;
+  return *reinterpret_cast<const Vec<T, V>*>(reinterpret_cast<const T*>(base) + e);
+}
+
+// 16 bytes from global to shared memory, in the background.
+__device__ __forceinline__ void copy16(void* to, const char* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
 }
 
 // Where the two vectors of chunk c start.
@@ -134,10 +133,20 @@ __device__ __forceinline__ void load_f(const float* p, float* x) {
   }
 }
 
+constexpr int kRing = 3;
+
+// Bytes of a CTA's ring: R rows of C chunks of two vectors, for the row and
+// (backward) its gradient.
+constexpr int ring_bytes(int c, int r, bool backward) {
+  return kRing * kQkThreads * r * c * 2 * (backward ? 2 : 1) * 16;
+}
+
 // V numbers a vector, C chunks a lane, R heads a group.
 template <typename T, int V, int C, int R, bool kInter, bool kBackward>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant__ QkArgs a) {
-  extern __shared__ float s_part[];
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  constexpr bool kAsync = sizeof(T) * V == 16;
+  constexpr int kVecs = R * C * 2 * (kBackward ? 2 : 1);   // a thread's vectors of a token
   const int lanes = a.lanes;
   const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   // the group's lanes of its warp: groups of one warp walk on by themselves
@@ -145,15 +154,18 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
                         << (threadIdx.x % 32 / lanes * lanes);
   const int block = blockIdx.x % a.head_blocks;
   const int rep = group / a.per;
-  // head j of the group: adjacent groups take adjacent heads
+  // head r of the group: adjacent groups take adjacent heads
   const int head0 = block * a.per * R + group % a.per;
   const bool on = rep < a.reps && head0 < a.heads;
   const int64_t slots = (int64_t)(gridDim.x / a.head_blocks) * a.reps;
+  const int64_t first = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep;
   int p0[C], p1[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) places<V, kInter>(a, min(lane + j * lanes, a.chunks - 1), &p0[j], &p1[j]);
+  const auto has = [&](int r) { return R == 1 || head0 + r * a.per < a.heads; };
   const auto which = [&](int r) { return head0 + r * a.per >= a.r[0].heads ? 1 : 0; };
   const auto local = [&](int r) { return head0 + r * a.per - (which(r) ? a.r[0].heads : 0); };
+  const auto live = [&](int j) { return lane + j * lanes < a.chunks; };
 
   float dgain[kBackward ? R : 1][C][2 * V];
   if (kBackward)
@@ -164,53 +176,37 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = 0.0f;
 
-  int64_t t = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep;
-  int64_t next = on && t < a.tokens ? position(a, t) : 0;
-  for (; on && t < a.tokens; t += slots) {
-    const int64_t p = next;
-    if (t + slots < a.tokens) next = position(a, t + slots);
-    if (p < 0 || (p >= a.n_pos && a.rot > 0)) {
-      // padding, or no angle for this position: no row and no table is read
-      const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
+  // Starts the copies of token t into slot `at` of the ring.
+  const auto fetch = [&](int64_t t, int at) {
+    if constexpr (kAsync) {
+      if (t < a.tokens) {
+        unsigned char* to = s_raw + ((int64_t)at * kVecs * kQkThreads + threadIdx.x) * 16;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (head0 + r * a.per >= a.heads) continue;
-        const Rows& w = a.r[which(r)];
-        T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
+        for (int r = 0; r < R; ++r) {
+          if (!has(r)) continue;
+          const Rows& w = a.r[which(r)];
+          const char* in = w.in + (t * w.in_t + (int64_t)local(r) * w.in_h) * (int)sizeof(T);
+          const char* go = kBackward ? w.gout + (t * w.go_t + (int64_t)local(r) * w.go_h) * (int)sizeof(T) : nullptr;
 #pragma unroll
-        for (int j = 0; j < C; ++j) {
-          if (lane + j * lanes >= a.chunks) continue;
-          Vec<T, V> z;
-#pragma unroll
-          for (int i = 0; i < V; ++i) z.v[i] = fill;
-          *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = z;
-          *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = z;
-          if (kBackward && p >= 0)
-#pragma unroll
-            for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = __int_as_float(0x7fffffff);
+          for (int j = 0; j < C; ++j) {
+            if (!live(j)) continue;
+            constexpr int kStep = kQkThreads * 16;
+            const int n = (r * C + j) * (kBackward ? 4 : 2);
+            copy16(to + n * kStep, in + p0[j] * (int)sizeof(T));
+            copy16(to + (n + 1) * kStep, in + p1[j] * (int)sizeof(T));
+            if constexpr (kBackward) {
+              copy16(to + (n + 2) * kStep, go + p0[j] * (int)sizeof(T));
+              copy16(to + (n + 3) * kStep, go + p1[j] * (int)sizeof(T));
+            }
+          }
         }
       }
-      continue;
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    Vec<T, V> xr[R][C][2], gr[kBackward ? R : 1][C][2];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (head0 + r * a.per >= a.heads) continue;
-      const Rows& w = a.r[which(r)];
-      const int64_t o_in = t * w.in_t + (int64_t)local(r) * w.in_h;
-#pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if (lane + j * lanes >= a.chunks) continue;
-        xr[r][j][0] = load<T, V>(w.in, o_in + p0[j]);
-        xr[r][j][1] = load<T, V>(w.in, o_in + p1[j]);
-        if constexpr (kBackward) {
-          const int64_t o_g = t * w.go_t + (int64_t)local(r) * w.go_h;
-          gr[r][j][0] = load<T, V>(w.gout, o_g + p0[j]);
-          gr[r][j][1] = load<T, V>(w.gout, o_g + p1[j]);
-        }
-      }
-    }
-    float cs[C][V], sn[C][V];
+  };
+  float cs[C][V], sn[C][V];
+  const auto angles = [&](int64_t p) {
+    if (p < 0 || p >= a.n_pos) return;
 #pragma unroll
     for (int j = 0; j < C; ++j) {
       const int c = lane + j * lanes;
@@ -219,104 +215,163 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
         load_f<V>(a.sin + p * (a.rot / 2) + c * V, sn[j]);
       }
     }
+  };
+
+  if (on && first < a.tokens) {
+    int64_t p = position(a, first);
+    int64_t next = first + slots < a.tokens ? position(a, first + slots) : 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (head0 + r * a.per >= a.heads) continue;
-      const Rows& w = a.r[which(r)];
-      float x[C][2 * V], g[C][2 * V], gain[C][2 * V];
-      float sq = 0.0f, dot = 0.0f;
+    for (int k = 0; k < kRing - 1; ++k) fetch(first + k * slots, k);
+    angles(p);
+    int at = 0;
+    for (int64_t t = first; t < a.tokens; t += slots) {
+      fetch(t + (kRing - 1) * slots, at == 0 ? kRing - 1 : at - 1);
+      if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      // padding, or no angle for this position: a fill of the rows
+      const bool skip = p < 0 || (p >= a.n_pos && a.rot > 0);
+      float gain[C][2 * V];
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const int c = lane + j * lanes;
+      for (int r = 0; r < R; ++r) {
+        if (!has(r)) continue;
+        const Rows& w = a.r[which(r)];
+        T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
+        if (skip) {
+          const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          gain[j][i] = 1.0f;
-          x[j][i] = g[j][i] = 0.0f;
-        }
-        if (c >= a.chunks) continue;
-        if (w.gain) {
-          const float* gp = w.gain + (a.gain_per_head ? (int64_t)local(r) * a.dim : 0);
-          load_f<V>(gp + p0[j], gain[j]);
-          load_f<V>(gp + p1[j], gain[j] + V);
-        }
+          for (int j = 0; j < C; ++j) {
+            if (!live(j)) continue;
+            Vec<T, V> z;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          x[j][i] = Num<T>::get(xr[r][j][0].v[i]);
-          x[j][V + i] = Num<T>::get(xr[r][j][1].v[i]);
-          if constexpr (kBackward) {
-            g[j][i] = Num<T>::get(gr[r][j][0].v[i]);
-            g[j][V + i] = Num<T>::get(gr[r][j][1].v[i]);
+            for (int i = 0; i < V; ++i) z.v[i] = fill;
+            *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = z;
+            *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = z;
+            if (kBackward && p >= 0)
+#pragma unroll
+              for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = __int_as_float(0x7fffffff);
           }
+          continue;
         }
-        if (kBackward && c * 2 * V < a.rot) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
+        float x[C][2 * V], g[C][2 * V];
+        float sq = 0.0f, dot = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          sq = __fmaf_rn(x[j][i], x[j][i], sq);
-          if (kBackward) dot = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), x[j][i], dot);
-        }
-      }
-      for (int o = lanes >> 1; o > 0; o >>= 1) {
-        sq = __fadd_rn(sq, __shfl_xor_sync(mask, sq, o));
-        if (kBackward) dot = __fadd_rn(dot, __shfl_xor_sync(mask, dot, o));
-      }
-      const float inv = rsqrtf(__fmaf_rn(sq, a.inv_dim, a.eps));
-      const float back = kBackward ? __fmul_rn(__fmul_rn(inv, __fmul_rn(inv, inv)),
-                                               __fmul_rn(dot, a.inv_dim)) : 0.0f;
-      T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
+        for (int j = 0; j < C; ++j) {
+          const int c = lane + j * lanes;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        const int c = lane + j * lanes;
-        if (c >= a.chunks) continue;
-        float y[2 * V];
+          for (int i = 0; i < 2 * V; ++i) x[j][i] = g[j][i] = 0.0f;
+          if (c >= a.chunks) continue;
+          // a shared gain is loaded once a token and kind of row
+          if (r == 0 || a.gain_per_head || which(r) != which(r - 1)) {
+            if (w.gain) {
+              const float* gp = w.gain + (a.gain_per_head ? (int64_t)local(r) * a.dim : 0);
+              load_f<V>(gp + p0[j], gain[j]);
+              load_f<V>(gp + p1[j], gain[j] + V);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) {
-          if constexpr (kBackward) {
-            dgain[r][j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[r][j][i]);
-            y[i] = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), inv, -__fmul_rn(x[j][i], back));
+              for (int i = 0; i < 2 * V; ++i) gain[j][i] = 1.0f;
+            }
+          }
+          Vec<T, V> v[kBackward ? 4 : 2];
+          if constexpr (kAsync) {
+            const unsigned char* from =
+                s_raw + ((int64_t)(at * kVecs + (r * C + j) * (kBackward ? 4 : 2)) * kQkThreads + threadIdx.x) * 16;
+#pragma unroll
+            for (int k = 0; k < (kBackward ? 4 : 2); ++k)
+              v[k] = *reinterpret_cast<const Vec<T, V>*>(from + k * kQkThreads * 16);
           } else {
-            y[i] = __fmul_rn(__fmul_rn(x[j][i], inv), gain[j][i]);
+            const int64_t o_in = t * w.in_t + (int64_t)local(r) * w.in_h;
+            v[0] = load<T, V>(w.in, o_in + p0[j]);
+            v[1] = load<T, V>(w.in, o_in + p1[j]);
+            if constexpr (kBackward) {
+              const int64_t o_g = t * w.go_t + (int64_t)local(r) * w.go_h;
+              v[2] = load<T, V>(w.gout, o_g + p0[j]);
+              v[3] = load<T, V>(w.gout, o_g + p1[j]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            x[j][i] = Num<T>::get(v[0].v[i]);
+            x[j][V + i] = Num<T>::get(v[1].v[i]);
+            if constexpr (kBackward) {
+              g[j][i] = Num<T>::get(v[2].v[i]);
+              g[j][V + i] = Num<T>::get(v[3].v[i]);
+            }
+          }
+          if (kBackward && c * 2 * V < a.rot) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) {
+            sq = __fmaf_rn(x[j][i], x[j][i], sq);
+            if (kBackward) dot = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), x[j][i], dot);
           }
         }
-        if (!kBackward && c * 2 * V < a.rot) turn<V, kInter>(y, cs[j], sn[j], 1.0f);
-        Vec<T, V> u, v;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          u.v[i] = Num<T>::put(y[i]);
-          v.v[i] = Num<T>::put(y[V + i]);
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
+          sq = __fadd_rn(sq, __shfl_xor_sync(mask, sq, o));
+          if (kBackward) dot = __fadd_rn(dot, __shfl_xor_sync(mask, dot, o));
         }
-        *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = u;
-        *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = v;
+        const float inv = rsqrtf(__fmaf_rn(sq, a.inv_dim, a.eps));
+        const float back = kBackward ? __fmul_rn(__fmul_rn(inv, __fmul_rn(inv, inv)),
+                                                 __fmul_rn(dot, a.inv_dim)) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          const int c = lane + j * lanes;
+          if (c >= a.chunks) continue;
+          float y[2 * V];
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) {
+            if constexpr (kBackward) {
+              dgain[r][j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[r][j][i]);
+              y[i] = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), inv, -__fmul_rn(x[j][i], back));
+            } else {
+              y[i] = __fmul_rn(__fmul_rn(x[j][i], inv), gain[j][i]);
+            }
+          }
+          if (!kBackward && c * 2 * V < a.rot) turn<V, kInter>(y, cs[j], sn[j], 1.0f);
+          Vec<T, V> u, v;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            u.v[i] = Num<T>::put(y[i]);
+            v.v[i] = Num<T>::put(y[V + i]);
+          }
+          *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = u;
+          *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = v;
+        }
       }
+      p = next;
+      if (t + slots < a.tokens) angles(p);
+      if (t + 2 * slots < a.tokens) next = position(a, t + 2 * slots);
+      at = at == kRing - 1 ? 0 : at + 1;
     }
   }
 
   if constexpr (kBackward) {
     if (!a.part) return;
     // The CTA's share of the gains' gradients: a head a group at a time to
-    // shared memory, each column then added over the groups in order.
-    const int groups = kQkThreads / lanes;
+    // shared memory (over the ring, which is done with), each column then
+    // added over the groups in order.
+    if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+    float* s_part = reinterpret_cast<float*>(s_raw);
     float* to = a.part + (int64_t)blockIdx.x * a.part_rows * a.dim;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        if (lane + j * lanes >= a.chunks) continue;
+        if (!live(j)) continue;
 #pragma unroll
         for (int i = 0; i < 2 * V; ++i)
-          s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on ? dgain[r][j][i] : 0.0f;
+          s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on && has(r) ? dgain[r][j][i] : 0.0f;
       }
       __syncthreads();
-      // shared gains: two rows that grow with r; gains of a head: its own row
+      // shared gains: two rows, added to with every r; a head's gain: its row
       const int rows = a.gain_per_head ? a.per : 2;
+      const int h0 = block * a.per * R + r * a.per;
+      const int nq = min(max(a.r[0].heads - h0, 0), a.per);     // query heads among these
       for (int e = threadIdx.x; e < rows * a.dim; e += kQkThreads) {
         const int row = e / a.dim, d = e % a.dim;
+        const int lo = a.gain_per_head ? row : row ? nq : 0;
+        const int hi = a.gain_per_head ? row + 1 : row ? a.per : nq;
         float s = 0.0f;
-        for (int k = 0; k < groups; ++k) {
-          const int hd = block * a.per * R + k % a.per + r * a.per;
-          const int mine = a.gain_per_head ? k % a.per : (hd >= a.r[0].heads ? 1 : 0);
-          if (mine == row && hd < a.heads) s = __fadd_rn(s, s_part[k * a.dim + d]);
-        }
+        for (int q = 0; q < a.reps; ++q)
+          for (int k = lo; k < hi; ++k) s = __fadd_rn(s, s_part[(q * a.per + k) * a.dim + d]);
         if (a.gain_per_head) to[r * a.per * a.dim + e] = s;
         else to[e] = r ? __fadd_rn(to[e], s) : s;
       }
@@ -332,8 +387,9 @@ struct FoldArgs {
 
 // Sums the CTAs' partial gain gradients in index order: 32 columns a CTA, 8
 // threads a column, each over every eighth partial.
-__global__ void __launch_bounds__(256) qk_fold_kernel(const FoldArgs a) {
+__global__ void __launch_bounds__(256) qk_fold_kernel(const __grid_constant__ FoldArgs a) {
   __shared__ float s[8][33];
+  cudaGridDependencySynchronize();   // launched while the partials are still written
   const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
   const int rows = a.gain_per_head ? a.heads : 2;
   const int row = col / a.dim, d = col % a.dim;
@@ -342,8 +398,18 @@ __global__ void __launch_bounds__(256) qk_fold_kernel(const FoldArgs a) {
     const int step = a.gain_per_head ? a.head_blocks : 1;
     const int first = a.gain_per_head ? row / a.per : 0;
     const int local = a.gain_per_head ? row % a.per : row;
-    for (int c = first + part * step; c < a.grid; c += 8 * step)
-      sum = __fadd_rn(sum, a.part[((int64_t)c * a.part_rows + local) * a.dim + d]);
+    const int64_t one = (int64_t)a.part_rows * a.dim;
+    const float* at = a.part + (int64_t)local * a.dim + d;
+    int c = first + part * step;
+    for (; c + 56 * step < a.grid; c += 64 * step) {
+      float v[8];                // eight loads on their way at once
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = at[(c + 8 * k * step) * one];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = __fadd_rn(sum, v[k]);
+    }
+#pragma unroll 4
+    for (; c < a.grid; c += 8 * step) sum = __fadd_rn(sum, at[c * one]);
   }
   s[part][threadIdx.x % 32] = sum;
   __syncthreads();
@@ -370,8 +436,10 @@ const void* kernel_for(int v, int r) {
       return (const void*)qk_kernel<T, 8, 1, 1, kInter, kBackward>;
     }
   switch (v) {
-    case 4: return r == 2 ? (const void*)qk_kernel<T, 4, 2, 2, kInter, kBackward>
-                          : (const void*)qk_kernel<T, 4, 2, 1, kInter, kBackward>;
+    case 4:
+      if constexpr (sizeof(T) == 4 && !kBackward)
+        if (r == 2) return (const void*)qk_kernel<T, 4, 2, 2, kInter, kBackward>;
+      return (const void*)qk_kernel<T, 4, 2, 1, kInter, kBackward>;
     case 2: return (const void*)qk_kernel<T, 2, 4, 1, kInter, kBackward>;
     default: return (const void*)qk_kernel<T, 1, 8, 1, kInter, kBackward>;
   }
@@ -405,6 +473,7 @@ struct zero_qk_handle {
       if (o.fn == fn) return o.ctas;
       if (o.fn) continue;
       int n = 0;
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kQkThreads, smem) != cudaSuccess) n = 1;
       o.ctas = std::max(1, std::min(n, kMaxPerSm));
       o.fn = fn;
@@ -511,7 +580,7 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   // Heads a group: more rows in flight and fewer reads of the angles, as long
   // as the heads divide and the tokens still fill the device.
   int r = 1;
-  const int most_r = es_vec < 16 ? 1 : v == 8 ? (backward ? 2 : 4) : 2;
+  const int most_r = es_vec < 16 ? 1 : v == 8 ? (backward ? 2 : 4) : (backward ? 1 : 2);
   while (2 * r <= most_r && a.heads % (2 * r) == 0 &&
          b->tokens * a.heads >= (int64_t)2 * r * groups * 2 * h->sms)
     r *= 2;
@@ -524,7 +593,9 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, v, r)
                    : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, v, r)
                                           : kernel_of<float>(c.interleaved, backward, v, r);
-  const size_t smem = want ? (size_t)groups * c.head_dim * sizeof(float) : 0;
+  const int chunks_lane = v == 8 ? 1 : v == 4 ? 2 : v == 2 ? 4 : 8;
+  size_t smem = es_vec == 16 ? (size_t)ring_bytes(chunks_lane, r, backward) : 0;
+  if (want) smem = std::max(smem, (size_t)groups * c.head_dim * sizeof(float));
   const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
   int64_t grid = slots * a.head_blocks;
   const int64_t resident = (int64_t)h->resident(fn, (int)smem) * h->sms;
@@ -549,9 +620,17 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     f.gain_per_head = c.gain_per_head;
     const int64_t cols = (int64_t)(c.gain_per_head ? a.heads : 2) * c.head_dim;
     void* fp[] = {&f};
-    e = cudaLaunchKernel((const void*)qk_fold_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256),
-                         fp, 0, s);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)((cols + 31) / 32));
+    lc.blockDim = dim3(256);
+    lc.stream = s;
+    lc.attrs = &early;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelExC(&lc, (const void*)qk_fold_kernel, fp);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
     ++h->launches;
   }
   return ZERO_OK;
