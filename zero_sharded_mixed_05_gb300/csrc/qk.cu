@@ -37,7 +37,8 @@ using zo::fail;
 
 constexpr int kQkThreads = 256;
 constexpr int kMaxDim = 512;
-constexpr int kMaxPerSm = 4;      // CTAs an SM: what the workspace has room for
+constexpr int kMaxPerSm = 6;      // CTAs an SM: what the workspace has room for
+constexpr int kMaxSmem = 200 * 1024;
 
 struct Rows {
   const char* in;      // x
@@ -64,25 +65,72 @@ struct QkArgs {
   float eps, inv_dim;
 };
 
+// Two numbers of the data's type as binary32, and back with one rounding each.
 template <typename T> struct Num;
 template <> struct Num<__half> {
   static __device__ float get(__half x) { return __half2float(x); }
+  static __device__ float2 get2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
   static __device__ __half put(float x) { return __float2half_rn(x); }
+  static __device__ void put2(__half* p, float2 x) { *reinterpret_cast<__half2*>(p) = __float22half2_rn(x); }
 };
 template <> struct Num<__nv_bfloat16> {
   static __device__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ float2 get2(const __nv_bfloat16* p) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
   static __device__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
+  static __device__ void put2(__nv_bfloat16* p, float2 x) {
+    *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(x);
+  }
 };
 template <> struct Num<float> {
   static __device__ float get(float x) { return x; }
+  static __device__ float2 get2(const float* p) { return make_float2(p[0], p[1]); }
   static __device__ float put(float x) { return x; }
+  static __device__ void put2(float* p, float2 x) { p[0] = x.x; p[1] = x.y; }
 };
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T v[V]; };
 
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// A chunk: the lane's two vectors one after the other, as V pairs of numbers
+// for the two-wide binary32 instructions.
 template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load(const char* base, int64_t e) {
-  return *reinterpret_cast<const Vec<T, V>*>(reinterpret_cast<const T*>(base) + e);
+__device__ __forceinline__ void widen(const Vec<T, V>& u, const Vec<T, V>& v, float2* x) {
+  if constexpr (V == 1) {
+    x[0] = make_float2(Num<T>::get(u.v[0]), Num<T>::get(v.v[0]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      x[k] = Num<T>::get2(u.v + 2 * k);
+      x[V / 2 + k] = Num<T>::get2(v.v + 2 * k);
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void narrow(const float2* x, Vec<T, V>& u, Vec<T, V>& v) {
+  if constexpr (V == 1) {
+    u.v[0] = Num<T>::put(x[0].x);
+    v.v[0] = Num<T>::put(x[0].y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {
+      Num<T>::put2(u.v + 2 * k, x[k]);
+      Num<T>::put2(v.v + 2 * k, x[V / 2 + k]);
+    }
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load(const char* p, int e) {
+  return *reinterpret_cast<const Vec<T, V>*>(reinterpret_cast<const T*>(p) + e);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(char* p, int e, const Vec<T, V>& x) {
+  *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(p) + e) = x;
 }
 
 // 16 bytes from global to shared memory, in the background.
@@ -109,27 +157,34 @@ __device__ __forceinline__ int64_t position(const QkArgs& a, int64_t t) {
                  : (int64_t)__ldg(static_cast<const int*>(a.pos) + t);
 }
 
-// The rotation of one chunk (dir +1) or its inverse (dir -1).  x holds the
-// chunk's two vectors one after the other.
+// The rotation of one chunk, or with -sin its inverse.
 template <int V, bool kInter>
-__device__ __forceinline__ void turn(float* x, const float* cs, const float* sn, float dir) {
+__device__ __forceinline__ void turn(float2* x, const float* cs, const float* sn, bool inverse) {
+  if constexpr (kInter || V == 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int iu = kInter ? 2 * i : i, iv = kInter ? 2 * i + 1 : V + i;
-    const float u = x[iu], v = x[iv], s = dir * sn[i];
-    x[iu] = __fmaf_rn(u, cs[i], -__fmul_rn(v, s));
-    x[iv] = __fmaf_rn(v, cs[i], __fmul_rn(u, s));
+    for (int k = 0; k < V; ++k) {          // a pair (u, v) of its own angle
+      const float s = inverse ? -sn[k] : sn[k];
+      x[k] = __ffma2_rn(x[k], both(cs[k]), __fmul2_rn(make_float2(x[k].y, x[k].x), make_float2(-s, s)));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) {      // two u and their two v
+      const float2 u = x[k], v = x[V / 2 + k], c = make_float2(cs[2 * k], cs[2 * k + 1]);
+      const float2 s = inverse ? make_float2(-sn[2 * k], -sn[2 * k + 1]) : make_float2(sn[2 * k], sn[2 * k + 1]);
+      x[k] = __ffma2_rn(u, c, __fmul2_rn(v, make_float2(-s.x, -s.y)));
+      x[V / 2 + k] = __ffma2_rn(v, c, __fmul2_rn(u, s));
+    }
   }
 }
 
 template <int V>
 __device__ __forceinline__ void load_f(const float* p, float* x) {
-  const Vec<float, (V < 4 ? V : 4)>* q = reinterpret_cast<const Vec<float, (V < 4 ? V : 4)>*>(p);
+  constexpr int kW = V < 4 ? V : 4;
 #pragma unroll
-  for (int i = 0; i < V / (V < 4 ? V : 4); ++i) {
-    const Vec<float, (V < 4 ? V : 4)> y = q[i];
+  for (int i = 0; i < V / kW; ++i) {
+    const Vec<float, kW> y = reinterpret_cast<const Vec<float, kW>*>(p)[i];
 #pragma unroll
-    for (int j = 0; j < (V < 4 ? V : 4); ++j) x[i * 4 + j] = y.v[j];
+    for (int j = 0; j < kW; ++j) x[i * kW + j] = y.v[j];
   }
 }
 
@@ -137,16 +192,19 @@ constexpr int kRing = 3;
 
 // Bytes of a CTA's ring: R rows of C chunks of two vectors, for the row and
 // (backward) its gradient.
-constexpr int ring_bytes(int c, int r, bool backward) {
-  return kRing * kQkThreads * r * c * 2 * (backward ? 2 : 1) * 16;
+constexpr int ring_bytes(int threads, int c, int r, bool backward) {
+  return kRing * threads * r * c * 2 * (backward ? 2 : 1) * 16;
 }
 
-// V numbers a vector, C chunks a lane, R heads a group.
-template <typename T, int V, int C, int R, bool kInter, bool kBackward>
+// V numbers a vector, C chunks a lane, R heads a group (all queries or all
+// keys).  kSum: one sum of gain gradients a group (a shared gain) instead of
+// one a head.
+template <typename T, int V, int C, int R, bool kInter, bool kBackward, bool kSum>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant__ QkArgs a) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   constexpr bool kAsync = sizeof(T) * V == 16;
-  constexpr int kVecs = R * C * 2 * (kBackward ? 2 : 1);   // a thread's vectors of a token
+  constexpr int kEach = kBackward ? 4 : 2;                 // vectors of a chunk
+  constexpr int kSums = !kBackward ? 1 : kSum ? 1 : R;
   const int lanes = a.lanes;
   const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   // the group's lanes of its warp: groups of one warp walk on by themselves
@@ -154,52 +212,70 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
                         << (threadIdx.x % 32 / lanes * lanes);
   const int block = blockIdx.x % a.head_blocks;
   const int rep = group / a.per;
-  // head r of the group: adjacent groups take adjacent heads
-  const int head0 = block * a.per * R + group % a.per;
+  const int head0 = (block * a.per + group % a.per) * R;
   const bool on = rep < a.reps && head0 < a.heads;
   const int64_t slots = (int64_t)(gridDim.x / a.head_blocks) * a.reps;
   const int64_t first = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep;
+  const Rows& w = a.r[on && head0 >= a.r[0].heads ? 1 : 0];
+  const int local = head0 - (head0 >= a.r[0].heads ? a.r[0].heads : 0);
   int p0[C], p1[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) places<V, kInter>(a, min(lane + j * lanes, a.chunks - 1), &p0[j], &p1[j]);
-  const auto has = [&](int r) { return R == 1 || head0 + r * a.per < a.heads; };
-  const auto which = [&](int r) { return head0 + r * a.per >= a.r[0].heads ? 1 : 0; };
-  const auto local = [&](int r) { return head0 + r * a.per - (which(r) ? a.r[0].heads : 0); };
   const auto live = [&](int j) { return lane + j * lanes < a.chunks; };
 
-  float dgain[kBackward ? R : 1][C][2 * V];
+  float2 dgain[kSums][C][V];
   if (kBackward)
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < kSums; ++r)
 #pragma unroll
       for (int j = 0; j < C; ++j)
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = 0.0f;
-
-  // Starts the copies of token t into slot `at` of the ring.
-  const auto fetch = [&](int64_t t, int at) {
-    if constexpr (kAsync) {
-      if (t < a.tokens) {
-        unsigned char* to = s_raw + ((int64_t)at * kVecs * kQkThreads + threadIdx.x) * 16;
+        for (int i = 0; i < V; ++i) dgain[r][j][i] = both(0.0f);
+  float2 gain[C][V];
+  const auto load_gain = [&](int r) {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (!has(r)) continue;
-          const Rows& w = a.r[which(r)];
-          const char* in = w.in + (t * w.in_t + (int64_t)local(r) * w.in_h) * (int)sizeof(T);
-          const char* go = kBackward ? w.gout + (t * w.go_t + (int64_t)local(r) * w.go_h) * (int)sizeof(T) : nullptr;
+    for (int j = 0; j < C; ++j)
+      if (w.gain && live(j)) {
+        const float* gp = w.gain + (a.gain_per_head ? (int64_t)(local + r) * a.dim : 0);
+        widen<float, V>(load<float, V>(reinterpret_cast<const char*>(gp), p0[j]),
+                        load<float, V>(reinterpret_cast<const char*>(gp), p1[j]), gain[j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) gain[j][i] = both(1.0f);
+      }
+  };
+
+  // the group's rows of its next token, in bytes
+  constexpr int kS = (int)sizeof(T);
+  const char* in = w.in + (first * w.in_t + (int64_t)local * w.in_h) * kS;
+  const char* go = kBackward ? w.gout + (first * w.go_t + (int64_t)local * w.go_h) * kS : nullptr;
+  char* out = w.out + (first * w.out_t + (int64_t)local * w.out_h) * kS;
+  const int64_t in_t = slots * w.in_t * kS, in_h = w.in_h * kS;
+  const int64_t go_t = slots * w.go_t * kS, go_h = w.go_h * kS;
+  const int64_t out_t = slots * w.out_t * kS, out_h = w.out_h * kS;
+  const int step = blockDim.x * 16;                        // ring: from vector to vector
+  unsigned char* const mine = s_raw + threadIdx.x * 16;
+
+  // Starts the copies of a token's rows into slot `at` of the ring.
+  const auto fetch = [&](bool there, int at) {
+    if constexpr (kAsync) {
+      if (there) {
+        unsigned char* to = mine + at * (R * C * kEach) * step;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             if (!live(j)) continue;
-            constexpr int kStep = kQkThreads * 16;
-            const int n = (r * C + j) * (kBackward ? 4 : 2);
-            copy16(to + n * kStep, in + p0[j] * (int)sizeof(T));
-            copy16(to + (n + 1) * kStep, in + p1[j] * (int)sizeof(T));
+            const int n = (r * C + j) * kEach;
+            copy16(to + n * step, in + r * in_h + p0[j] * kS);
+            copy16(to + (n + 1) * step, in + r * in_h + p1[j] * kS);
             if constexpr (kBackward) {
-              copy16(to + (n + 2) * kStep, go + p0[j] * (int)sizeof(T));
-              copy16(to + (n + 3) * kStep, go + p1[j] * (int)sizeof(T));
+              copy16(to + (n + 2) * step, go + r * go_h + p0[j] * kS);
+              copy16(to + (n + 3) * step, go + r * go_h + p1[j] * kS);
             }
           }
-        }
+        in += in_t;
+        if (kBackward) go += go_t;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
@@ -221,120 +297,92 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
     int64_t p = position(a, first);
     int64_t next = first + slots < a.tokens ? position(a, first + slots) : 0;
 #pragma unroll
-    for (int k = 0; k < kRing - 1; ++k) fetch(first + k * slots, k);
+    for (int k = 0; k < kRing - 1; ++k) fetch(first + k * slots < a.tokens, k);
     angles(p);
+    if (!a.gain_per_head) load_gain(0);
     int at = 0;
     for (int64_t t = first; t < a.tokens; t += slots) {
-      fetch(t + (kRing - 1) * slots, at == 0 ? kRing - 1 : at - 1);
+      fetch(t + (kRing - 1) * slots < a.tokens, at == 0 ? kRing - 1 : at - 1);
       if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
       // padding, or no angle for this position: a fill of the rows
       const bool skip = p < 0 || (p >= a.n_pos && a.rot > 0);
-      float gain[C][2 * V];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        if (!has(r)) continue;
-        const Rows& w = a.r[which(r)];
-        T* out = reinterpret_cast<T*>(w.out) + t * w.out_t + (int64_t)local(r) * w.out_h;
         if (skip) {
-          const T fill = Num<T>::put(p < 0 ? 0.0f : __int_as_float(0x7fffffff));
+          const float f = p < 0 ? 0.0f : __int_as_float(0x7fffffff);
+          Vec<T, V> z;
+#pragma unroll
+          for (int i = 0; i < V; ++i) z.v[i] = Num<T>::put(f);
 #pragma unroll
           for (int j = 0; j < C; ++j) {
             if (!live(j)) continue;
-            Vec<T, V> z;
-#pragma unroll
-            for (int i = 0; i < V; ++i) z.v[i] = fill;
-            *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = z;
-            *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = z;
+            store<T, V>(out + r * out_h, p0[j], z);
+            store<T, V>(out + r * out_h, p1[j], z);
             if (kBackward && p >= 0)
 #pragma unroll
-              for (int i = 0; i < 2 * V; ++i) dgain[r][j][i] = __int_as_float(0x7fffffff);
+              for (int i = 0; i < V; ++i) dgain[kSum ? 0 : r][j][i] = both(f);
           }
           continue;
         }
-        float x[C][2 * V], g[C][2 * V];
-        float sq = 0.0f, dot = 0.0f;
+        if (a.gain_per_head) load_gain(r);
+        float2 x[C][V], g[C][V];
+        float2 sq = both(0.0f), dot = both(0.0f);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          const int c = lane + j * lanes;
+          if (!live(j)) continue;
+          const bool turned = (lane + j * lanes) * 2 * V < a.rot;
+          const unsigned char* from = mine + (at * (R * C * kEach) + (r * C + j) * kEach) * step;
+          const auto vec = [&](int k, const char* row, int e) {
+            if constexpr (kAsync) return *reinterpret_cast<const Vec<T, V>*>(from + k * step);
+            else return load<T, V>(row, e);
+          };
+          widen<T, V>(vec(0, in + r * in_h, p0[j]), vec(1, in + r * in_h, p1[j]), x[j]);
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) x[j][i] = g[j][i] = 0.0f;
-          if (c >= a.chunks) continue;
-          // a shared gain is loaded once a token and kind of row
-          if (r == 0 || a.gain_per_head || which(r) != which(r - 1)) {
-            if (w.gain) {
-              const float* gp = w.gain + (a.gain_per_head ? (int64_t)local(r) * a.dim : 0);
-              load_f<V>(gp + p0[j], gain[j]);
-              load_f<V>(gp + p1[j], gain[j] + V);
-            } else {
+          for (int i = 0; i < V; ++i) sq = __ffma2_rn(x[j][i], x[j][i], sq);
+          if constexpr (kBackward) {
+            widen<T, V>(vec(2, go + r * go_h, p0[j]), vec(3, go + r * go_h, p1[j]), g[j]);
+            if (turned) turn<V, kInter>(g[j], cs[j], sn[j], true);
 #pragma unroll
-              for (int i = 0; i < 2 * V; ++i) gain[j][i] = 1.0f;
-            }
-          }
-          Vec<T, V> v[kBackward ? 4 : 2];
-          if constexpr (kAsync) {
-            const unsigned char* from =
-                s_raw + ((int64_t)(at * kVecs + (r * C + j) * (kBackward ? 4 : 2)) * kQkThreads + threadIdx.x) * 16;
-#pragma unroll
-            for (int k = 0; k < (kBackward ? 4 : 2); ++k)
-              v[k] = *reinterpret_cast<const Vec<T, V>*>(from + k * kQkThreads * 16);
+            for (int i = 0; i < V; ++i) dot = __ffma2_rn(__fmul2_rn(g[j][i], gain[j][i]), x[j][i], dot);
           } else {
-            const int64_t o_in = t * w.in_t + (int64_t)local(r) * w.in_h;
-            v[0] = load<T, V>(w.in, o_in + p0[j]);
-            v[1] = load<T, V>(w.in, o_in + p1[j]);
-            if constexpr (kBackward) {
-              const int64_t o_g = t * w.go_t + (int64_t)local(r) * w.go_h;
-              v[2] = load<T, V>(w.gout, o_g + p0[j]);
-              v[3] = load<T, V>(w.gout, o_g + p1[j]);
-            }
-          }
+            // the rotation does not wait for the norm, which scales it as a whole
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            x[j][i] = Num<T>::get(v[0].v[i]);
-            x[j][V + i] = Num<T>::get(v[1].v[i]);
-            if constexpr (kBackward) {
-              g[j][i] = Num<T>::get(v[2].v[i]);
-              g[j][V + i] = Num<T>::get(v[3].v[i]);
-            }
-          }
-          if (kBackward && c * 2 * V < a.rot) turn<V, kInter>(g[j], cs[j], sn[j], -1.0f);
-#pragma unroll
-          for (int i = 0; i < 2 * V; ++i) {
-            sq = __fmaf_rn(x[j][i], x[j][i], sq);
-            if (kBackward) dot = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), x[j][i], dot);
+            for (int i = 0; i < V; ++i) x[j][i] = __fmul2_rn(x[j][i], gain[j][i]);
+            if (turned) turn<V, kInter>(x[j], cs[j], sn[j], false);
           }
         }
+        float sum = __fadd_rn(sq.x, sq.y), sum_dot = __fadd_rn(dot.x, dot.y);
         for (int o = lanes >> 1; o > 0; o >>= 1) {
-          sq = __fadd_rn(sq, __shfl_xor_sync(mask, sq, o));
-          if (kBackward) dot = __fadd_rn(dot, __shfl_xor_sync(mask, dot, o));
+          sum = __fadd_rn(sum, __shfl_xor_sync(mask, sum, o));
+          if (kBackward) sum_dot = __fadd_rn(sum_dot, __shfl_xor_sync(mask, sum_dot, o));
         }
-        const float inv = rsqrtf(__fmaf_rn(sq, a.inv_dim, a.eps));
-        const float back = kBackward ? __fmul_rn(__fmul_rn(inv, __fmul_rn(inv, inv)),
-                                                 __fmul_rn(dot, a.inv_dim)) : 0.0f;
+        const float inv = rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps));
+        const float2 inv2 = both(inv);
+        const float2 back = both(__fmul_rn(-__fmul_rn(inv, __fmul_rn(inv, inv)), __fmul_rn(sum_dot, a.inv_dim)));
 #pragma unroll
         for (int j = 0; j < C; ++j) {
-          const int c = lane + j * lanes;
-          if (c >= a.chunks) continue;
-          float y[2 * V];
-#pragma unroll
-          for (int i = 0; i < 2 * V; ++i) {
-            if constexpr (kBackward) {
-              dgain[r][j][i] = __fmaf_rn(g[j][i], __fmul_rn(x[j][i], inv), dgain[r][j][i]);
-              y[i] = __fmaf_rn(__fmul_rn(g[j][i], gain[j][i]), inv, -__fmul_rn(x[j][i], back));
-            } else {
-              y[i] = __fmul_rn(__fmul_rn(x[j][i], inv), gain[j][i]);
-            }
-          }
-          if (!kBackward && c * 2 * V < a.rot) turn<V, kInter>(y, cs[j], sn[j], 1.0f);
-          Vec<T, V> u, v;
+          if (!live(j)) continue;
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            u.v[i] = Num<T>::put(y[i]);
-            v.v[i] = Num<T>::put(y[V + i]);
+            if constexpr (kBackward) {
+              float2& d = dgain[kSum ? 0 : r][j][i];
+              d = __ffma2_rn(g[j][i], __fmul2_rn(x[j][i], inv2), d);
+              x[j][i] = __ffma2_rn(__fmul2_rn(g[j][i], gain[j][i]), inv2, __fmul2_rn(x[j][i], back));
+            } else {
+              x[j][i] = __fmul2_rn(x[j][i], inv2);
+            }
           }
-          *reinterpret_cast<Vec<T, V>*>(out + p0[j]) = u;
-          *reinterpret_cast<Vec<T, V>*>(out + p1[j]) = v;
+          Vec<T, V> u, v;
+          narrow<T, V>(x[j], u, v);
+          store<T, V>(out + r * out_h, p0[j], u);
+          store<T, V>(out + r * out_h, p1[j], v);
         }
       }
+      if (!kAsync) {
+        in += in_t;
+        if (kBackward) go += go_t;
+      }
+      out += out_t;
       p = next;
       if (t + slots < a.tokens) angles(p);
       if (t + 2 * slots < a.tokens) next = position(a, t + 2 * slots);
@@ -344,36 +392,45 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant
 
   if constexpr (kBackward) {
     if (!a.part) return;
-    // The CTA's share of the gains' gradients: a head a group at a time to
-    // shared memory (over the ring, which is done with), each column then
-    // added over the groups in order.
+    // The CTA's share of the gains' gradients: a group's sums to shared memory
+    // (over the ring, which is done with), each column then added over the
+    // groups in order.
     if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
     float* s_part = reinterpret_cast<float*>(s_raw);
     float* to = a.part + (int64_t)blockIdx.x * a.part_rows * a.dim;
+    // groups of queries among the CTA's
+    const int nq = min(max(a.r[0].heads / R - block * a.per, 0), a.per);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < kSums; ++r) {
       __syncthreads();
+      if (rep < a.reps)
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if (!live(j)) continue;
+        for (int j = 0; j < C; ++j) {
+          if (!live(j)) continue;
+          float* s = s_part + group * a.dim;
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i)
-          s_part[group * a.dim + (i < V ? p0[j] + i : p1[j] + i - V)] = on && has(r) ? dgain[r][j][i] : 0.0f;
-      }
+          for (int i = 0; i < V; ++i) {
+            const int e = 2 * i;                 // number e of the two vectors
+            const float2 d = on ? dgain[r][j][i] : both(0.0f);
+            if constexpr (V == 1) {
+              s[p0[j]] = d.x;
+              s[p1[j]] = d.y;
+            } else {
+              float* q = s + (e < V ? p0[j] + e : p1[j] + e - V);
+              q[0] = d.x;
+              q[1] = d.y;
+            }
+          }
+        }
       __syncthreads();
-      // shared gains: two rows, added to with every r; a head's gain: its row
-      const int rows = a.gain_per_head ? a.per : 2;
-      const int h0 = block * a.per * R + r * a.per;
-      const int nq = min(max(a.r[0].heads - h0, 0), a.per);     // query heads among these
-      for (int e = threadIdx.x; e < rows * a.dim; e += kQkThreads) {
+      const int rows = kSum ? 2 : a.per;
+      for (int e = threadIdx.x; e < rows * a.dim; e += blockDim.x) {
         const int row = e / a.dim, d = e % a.dim;
-        const int lo = a.gain_per_head ? row : row ? nq : 0;
-        const int hi = a.gain_per_head ? row + 1 : row ? a.per : nq;
+        const int lo = !kSum ? row : row ? nq : 0, hi = !kSum ? row + 1 : row ? a.per : nq;
         float s = 0.0f;
         for (int q = 0; q < a.reps; ++q)
           for (int k = lo; k < hi; ++k) s = __fadd_rn(s, s_part[(q * a.per + k) * a.dim + d]);
-        if (a.gain_per_head) to[r * a.per * a.dim + e] = s;
-        else to[e] = r ? __fadd_rn(to[e], s) : s;
+        to[kSum ? e : (row * R + r) * a.dim + d] = s;
       }
     }
   }
@@ -426,29 +483,34 @@ bool fits(const void* p, int64_t s0, int64_t s1, int bytes, int esize) {
          s1 * esize % bytes == 0;
 }
 
-template <typename T, bool kInter, bool kBackward>
+template <typename T, bool kInter, bool kBackward, bool kSum>
 const void* kernel_for(int v, int r) {
   if constexpr (sizeof(T) == 2)
     if (v == 8) {
       if constexpr (!kBackward)
-        if (r == 4) return (const void*)qk_kernel<T, 8, 1, 4, kInter, kBackward>;
-      if (r == 2) return (const void*)qk_kernel<T, 8, 1, 2, kInter, kBackward>;
-      return (const void*)qk_kernel<T, 8, 1, 1, kInter, kBackward>;
+        if (r == 4) return (const void*)qk_kernel<T, 8, 1, 4, kInter, kBackward, kSum>;
+      if (r == 2) return (const void*)qk_kernel<T, 8, 1, 2, kInter, kBackward, kSum>;
+      return (const void*)qk_kernel<T, 8, 1, 1, kInter, kBackward, kSum>;
     }
   switch (v) {
     case 4:
       if constexpr (sizeof(T) == 4 && !kBackward)
-        if (r == 2) return (const void*)qk_kernel<T, 4, 2, 2, kInter, kBackward>;
-      return (const void*)qk_kernel<T, 4, 2, 1, kInter, kBackward>;
-    case 2: return (const void*)qk_kernel<T, 2, 4, 1, kInter, kBackward>;
-    default: return (const void*)qk_kernel<T, 1, 8, 1, kInter, kBackward>;
+        if (r == 2) return (const void*)qk_kernel<T, 4, 2, 2, kInter, kBackward, kSum>;
+      return (const void*)qk_kernel<T, 4, 2, 1, kInter, kBackward, kSum>;
+    case 2: return (const void*)qk_kernel<T, 2, 4, 1, kInter, kBackward, kSum>;
+    default: return (const void*)qk_kernel<T, 1, 8, 1, kInter, kBackward, kSum>;
   }
 }
 
+template <typename T, bool kInter>
+const void* kernel_of(bool backward, bool sum, int v, int r) {
+  if (!backward) return kernel_for<T, kInter, false, false>(v, r);
+  return sum ? kernel_for<T, kInter, true, true>(v, r) : kernel_for<T, kInter, true, false>(v, r);
+}
+
 template <typename T>
-const void* kernel_of(bool inter, bool backward, int v, int r) {
-  if (inter) return backward ? kernel_for<T, true, true>(v, r) : kernel_for<T, true, false>(v, r);
-  return backward ? kernel_for<T, false, true>(v, r) : kernel_for<T, false, false>(v, r);
+const void* kernel_of(bool inter, bool backward, bool sum, int v, int r) {
+  return inter ? kernel_of<T, true>(backward, sum, v, r) : kernel_of<T, false>(backward, sum, v, r);
 }
 
 }  // namespace
@@ -463,23 +525,21 @@ struct zero_qk_handle {
   std::mutex mu;
   struct {
     const void* fn;
-    int ctas;
-  } occ[16] = {};     // kernel -> CTAs an SM; a handle's type and pairing leave 13
+    int threads, smem, ctas;
+  } occ[32] = {};     // launch shapes seen, oldest overwritten
+  int seen = 0;
 
   // CTAs of a kernel that an SM holds at once, at most kMaxPerSm.
-  int resident(const void* fn, int smem) {
+  int resident(const void* fn, int threads, int smem) {
     std::lock_guard<std::mutex> lock(mu);
-    for (auto& o : occ) {
-      if (o.fn == fn) return o.ctas;
-      if (o.fn) continue;
-      int n = 0;
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, kQkThreads, smem) != cudaSuccess) n = 1;
-      o.ctas = std::max(1, std::min(n, kMaxPerSm));
-      o.fn = fn;
-      return o.ctas;
-    }
-    return 1;
+    for (const auto& o : occ)
+      if (o.fn == fn && o.threads == threads && o.smem == smem) return o.ctas;
+    int n = 0;
+    if (smem > 48 * 1024) cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) n = 1;
+    n = std::max(1, std::min(n, kMaxPerSm));
+    occ[seen++ % 32] = {fn, threads, smem, n};
+    return n;
   }
 };
 
@@ -577,32 +637,36 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   }
   const int groups = kQkThreads / a.lanes;
   const int es_vec = v * es;
-  // Heads a group: more rows in flight and fewer reads of the angles, as long
-  // as the heads divide and the tokens still fill the device.
+  const bool want = backward && (dgain[0] || dgain[1]);
+  const bool sum = want && !c.gain_per_head;
+  // Heads a group: fewer reads of the angles and fewer bookkeeping
+  // instructions a row, as long as both head counts divide and the tokens
+  // still fill the device.  The ring sets the most: two CTAs an SM.
   int r = 1;
   const int most_r = es_vec < 16 ? 1 : v == 8 ? (backward ? 2 : 4) : (backward ? 1 : 2);
-  while (2 * r <= most_r && a.heads % (2 * r) == 0 &&
+  while (2 * r <= most_r && c.q_heads % (2 * r) == 0 && c.k_heads % (2 * r) == 0 &&
          b->tokens * a.heads >= (int64_t)2 * r * groups * 2 * h->sms)
     r *= 2;
-  a.per = std::min(groups, (a.heads + r - 1) / r);
-  a.head_blocks = (a.heads + a.per * r - 1) / (a.per * r);
-  a.reps = std::max(1, groups / a.per);
-  a.part_rows = c.gain_per_head ? a.per * r : 2;
-  const bool want = backward && (dgain[0] || dgain[1]);
+  a.per = std::min(groups, a.heads / r);
+  a.head_blocks = (a.heads / r + a.per - 1) / a.per;
+  a.reps = groups / a.per;
+  a.part_rows = sum ? 2 : a.per * r;
   a.part = want ? h->part : nullptr;
-  const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, v, r)
-                   : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, v, r)
-                                          : kernel_of<float>(c.interleaved, backward, v, r);
+  // no more threads than groups that have a head
+  const int threads = (a.per * a.reps * a.lanes + 31) / 32 * 32;
+  const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, sum, v, r)
+                   : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, sum, v, r)
+                                          : kernel_of<float>(c.interleaved, backward, sum, v, r);
   const int chunks_lane = v == 8 ? 1 : v == 4 ? 2 : v == 2 ? 4 : 8;
-  size_t smem = es_vec == 16 ? (size_t)ring_bytes(chunks_lane, r, backward) : 0;
-  if (want) smem = std::max(smem, (size_t)groups * c.head_dim * sizeof(float));
+  size_t smem = es_vec == 16 ? (size_t)ring_bytes(threads, chunks_lane, r, backward) : 0;
+  if (want) smem = std::max(smem, (size_t)a.per * a.reps * c.head_dim * sizeof(float));
   const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
   int64_t grid = slots * a.head_blocks;
-  const int64_t resident = (int64_t)h->resident(fn, (int)smem) * h->sms;
+  const int64_t resident = (int64_t)h->resident(fn, threads, (int)smem) * h->sms;
   const int64_t most = std::max<int64_t>(1, resident / a.head_blocks) * a.head_blocks;
   if (grid > most) grid = most;
   void* params[] = {&a};
-  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(kQkThreads), params, smem, s);
+  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), params, smem, s);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
   ++h->launches;
   if (want) {
@@ -669,9 +733,9 @@ zero_status zero_qk_create(const zero_qk_config* cfg, zero_qk_t* out) {
     e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   // Partial gain gradients of every CTA of the largest grid.  A CTA's rows are
   // two, or its heads: at most 256 groups (a group of one lane owns heads of
-  // at most 16 numbers), four heads each.
+  // at most 16 numbers), two heads each.
   const int64_t heads = (int64_t)cfg->q_heads + cfg->k_heads;
-  const int64_t rows = cfg->gain_per_head ? std::min<int64_t>(4 * kQkThreads, heads + 4) : 2;
+  const int64_t rows = cfg->gain_per_head ? std::min<int64_t>(2 * kQkThreads, heads) : 2;
   const int64_t blocks = std::max<int64_t>((int64_t)kMaxPerSm * h->sms, heads);
   if (e == cudaSuccess)
     e = cudaMalloc(reinterpret_cast<void**>(&h->part),
