@@ -46,10 +46,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = 32 * (4 + kEpiWarps);
 constexpr int kPatchCols = 16;
 constexpr int kPatchBytes = kEpiWarps * 32 * (kPatchCols + 1) * 4;
+constexpr int kDiagBytes = 256 * 4;
 
 struct Products {
   Call c;
-  const CUtensorMap* maps;   // four an entry: x[0], x[1], a, b
+  const CUtensorMap* maps;   // eight an entry: x[0], x[1], a, b in boxes of 128 rows
+                             // (depth along the rows), and the same in boxes of 64
   const int32_t* starts;     // [2][n + 1]: first tile of each entry, triangular and full
   int32_t steps;
   float coef[ZERO_MUON_MAX_STEPS][3];
@@ -61,7 +63,7 @@ struct Tile {
 };
 
 constexpr int smem_bytes(int n) {
-  return 1024 + kStages * kStageBytes + kPatchBytes + 256 + 2 * (n + 1) * 4;
+  return 1024 + kStages * kStageBytes + kPatchBytes + kDiagBytes + 256 + 2 * (n + 1) * 4;
 }
 
 template <int kPair>
@@ -220,115 +222,129 @@ __device__ __forceinline__ void result_row(const Products& p, const Entry& e, co
 }
 
 // One tile's epilogue: the warp's 32 rows of the accumulator, half its columns.
+// Whatever it reads besides is fetched while the products still run: the
+// diagonal's numbers of the tile's columns go to shared memory, and of each
+// 32 columns the operands are on their way while those before are worked on.
+// False: a wait ran out.
 template <int kPair>
-__device__ __forceinline__ void epilogue(const Products& p, const Tile& t, uint32_t acc, int warp, int lane,
-                                         uint32_t rank, float* patch, uint32_t empty_bar) {
+__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, uint32_t acc, uint32_t full_bar,
+                                         uint32_t phase, uint32_t empty_bar, int warp, int lane,
+                                         uint32_t rank, float* patch, float* cols) {
   constexpr int kTile = 128 * kPair, kCols = kTile / 2;
-  const Entry& e = p.c.entries[t.entry];
+  const Entry& en = p.c.entries[t.entry];
+  const int rows = en.rows, ncols = en.cols, k = en.k, tall = en.tall;
+  const int64_t ldx = en.ldx, ldk = en.ldk;
   const int quarter = warp % 4, part = warp / 4;
   const int row0 = t.i * kTile + (int)rank * 128 + quarter * 32, row = row0 + lane;
-  const int M = t.which == 2 ? e.rows : e.k, N = t.which == 2 ? e.cols : e.k;
+  const int M = t.which == 2 ? rows : k, N = t.which == 2 ? ncols : k;
   const float ca = p.coef[t.step][0], cb = p.coef[t.step][1], cc = p.coef[t.step][2];
   const bool last = t.step == p.steps - 1;
   const int cur = t.step & 1;
-  float* diag = e.diag + (int64_t)t.b * e.ldk;
+  const int col0 = t.j * kTile;
+  const int64_t at_k = ((int64_t)t.b * k + row) * ldk + col0, at_x = ((int64_t)t.b * rows + row) * ldx + col0;
+  float* diag = en.diag + (int64_t)t.b * ldk;
+  __half* const to = t.which == 0 ? en.a + at_k : t.which == 1 ? en.b + at_k : en.x[cur ^ 1] + at_x;
+  const __half* const from = t.which == 1 ? en.a + at_k : en.x[cur] + at_x;
+  __half* const lo_at = en.lo + at_x;
+  const bool in = row < M;
+
+  int ok = 1;
   float di = 0.0f;
-  if (row < M && (t.which == 1 || (t.which == 2 && !e.tall))) di = __ldcg(diag + row);
+  uint32_t hi[16], lo[16];
+  const auto fetch = [&](int c0) {
+    if (t.which == 0 || !in || col0 + c0 >= N) return;
+    load_row(from + c0, hi);
+    if (t.which == 2) load_row(lo_at + c0, lo);
+  };
+  if (t.which != 0) {
+    if (lane == 0) ok = count_wait(p.c.done + t.unit, t.need, &p.c.ws->fault);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (in && (t.which == 1 || !tall)) di = __ldcg(diag + row);
+    const int c = warp * 32 + lane;
+    if (c < kTile && col0 + c < N) {
+      const float d = __ldcg(diag + col0 + c);
+      // b A + c A A: c d_j; X: e_j of a tall matrix
+      cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
+    }
+    fetch(part * kCols);
+  }
+  if (lane == 0 && ok) ok = mbar_wait(full_bar, phase, &p.c.ws->fault);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // all eight warps go on or none: the count of finished tiles is of whole ones
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\n"
+      "barrier.red.and.pred q, 1, %2, p;\nselp.b32 %0, 1, 0, q;\n}"
+      : "=r"(ok)
+      : "r"(ok), "r"(32 * kEpiWarps)
+      : "memory");
+  if (!ok) return false;
+  tc_fence_after();
+
   const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16);
+  // the row's share of b A + c A A's factor, or e_i of a wide matrix
+  const float ei = t.which == 1 ? __fmaf_rn(cc, di, cb) : __fmul_rn(di, __fmaf_rn(cc, di, cb));
 #pragma unroll 1
   for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
-    const int col = t.j * kTile + c0;
-    if (col >= N || row0 >= M) break;
+    if (col0 + c0 >= N || row0 >= M) break;
     float v[32];
     tmem_load32(lanes + c0, v);
+    tmem_load_wait();
     if (t.which == 0) {
-      tmem_load_wait();
-      if (row < M) {
-        uint32_t h[16];
-        const int at = row - col;     // the diagonal's place in this row, if any
+      if (in) {
+        const int at = row - (col0 + c0);     // the diagonal's place in this row, if any
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          v[k] = __fmul_rn(v[k], 1.0f / kScale);
-          if (k == at) {
-            __stcg(diag + row, __fmul_rn(v[k], 1.0f / kScale));
-            v[k] = 0.0f;
+        for (int q = 0; q < 32; ++q) {
+          v[q] = __fmul_rn(v[q], 1.0f / kScale);
+          if (q == at) {
+            __stcg(diag + row, __fmul_rn(v[q], 1.0f / kScale));
+            v[q] = 0.0f;
           }
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) h[k] = pack(v[2 * k], v[2 * k + 1]);
+        for (int q = 0; q < 16; ++q) hi[q] = pack(v[2 * q], v[2 * q + 1]);
         // rows are multiples of 32 numbers: nothing of the next row is written
-        store_row(e.a + ((int64_t)t.b * e.k + row) * e.ldk + col, h);
+        store_row(to + c0, hi);
       }
     } else if (t.which == 1) {
-      uint32_t s[16];
-      if (row < M) load_row(e.a + ((int64_t)t.b * e.k + row) * e.ldk + col, s);
-      float dj[32];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 d4 = __ldcg(reinterpret_cast<const float4*>(diag + col) + q);
-        dj[4 * q] = d4.x; dj[4 * q + 1] = d4.y; dj[4 * q + 2] = d4.z; dj[4 * q + 3] = d4.w;
-      }
-      tmem_load_wait();
-      if (row < M) {
+      if (in) {
         uint32_t h[16];
+        const float scale = __fmul_rn(cc, 1.0f / kScale);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 f = unpack(s[k]);
-          const float x = __fmaf_rn(__fmaf_rn(cc, __fadd_rn(di, dj[2 * k]), cb), f.x,
-                                    __fmul_rn(cc * (1.0f / kScale), v[2 * k]));
-          const float y = __fmaf_rn(__fmaf_rn(cc, __fadd_rn(di, dj[2 * k + 1]), cb), f.y,
-                                    __fmul_rn(cc * (1.0f / kScale), v[2 * k + 1]));
-          h[k] = pack(x, y);
+        for (int q = 0; q < 16; ++q) {
+          const float2 f = unpack(hi[q]), d = reinterpret_cast<const float2*>(cols + c0)[q];
+          h[q] = pack(__fmaf_rn(__fadd_rn(ei, d.x), f.x, __fmul_rn(scale, v[2 * q])),
+                      __fmaf_rn(__fadd_rn(ei, d.y), f.y, __fmul_rn(scale, v[2 * q + 1])));
         }
-        store_row(e.b + ((int64_t)t.b * e.k + row) * e.ldk + col, h);
+        if (c0 + 32 < (part + 1) * kCols) fetch(c0 + 32);
+        store_row(to + c0, h);
       }
     } else {
-      const int64_t at = ((int64_t)t.b * e.rows + row) * e.ldx + col;
-      uint32_t hi[16], lo[16];
-      if (row < M) {
-        load_row(e.x[cur] + at, hi);
-        load_row(e.lo + at, lo);
-      } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0;
+      for (int q = 0; q < 16; ++q) {
+        const float2 h = unpack(hi[q]), l = unpack(lo[q]);
+        float2 d = make_float2(ei, ei);
+        if (tall) d = reinterpret_cast<const float2*>(cols + c0)[q];
+        v[2 * q] = __fmaf_rn(v[2 * q], 1.0f / kScale,
+                             __fmaf_rn(ca, __fmaf_rn(l.x, 1.0f / kLoScale, h.x), __fmul_rn(d.x, h.x)));
+        v[2 * q + 1] = __fmaf_rn(v[2 * q + 1], 1.0f / kScale,
+                                 __fmaf_rn(ca, __fmaf_rn(l.y, 1.0f / kLoScale, h.y), __fmul_rn(d.y, h.y)));
       }
-      const float ei = __fmul_rn(di, __fmaf_rn(cc, di, cb));
-      float dj[32];
-      if (e.tall) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 d4 = __ldcg(reinterpret_cast<const float4*>(diag + col) + q);
-          dj[4 * q] = d4.x; dj[4 * q + 1] = d4.y; dj[4 * q + 2] = d4.z; dj[4 * q + 3] = d4.w;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) dj[k] = __fmul_rn(dj[k], __fmaf_rn(cc, dj[k], cb));
-      } else {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) dj[k] = ei;
-      }
-      tmem_load_wait();
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const float2 h = unpack(hi[k]), l = unpack(lo[k]);
-        v[2 * k] = __fmaf_rn(v[2 * k], 1.0f / kScale,
-                             __fmaf_rn(ca, __fmaf_rn(l.x, 1.0f / kLoScale, h.x), __fmul_rn(dj[2 * k], h.x)));
-        v[2 * k + 1] = __fmaf_rn(v[2 * k + 1], 1.0f / kScale,
-                                 __fmaf_rn(ca, __fmaf_rn(l.y, 1.0f / kLoScale, h.y), __fmul_rn(dj[2 * k + 1], h.y)));
-      }
+      if (c0 + 32 < (part + 1) * kCols) fetch(c0 + 32);
       if (last) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = __fmul_rn(v[k], 1.0f / kScale);
-        result_row(p, e, p.c.io[e.item], t.b, row, row0, col, v, patch, lane);
-      } else if (row < M) {
+        for (int q = 0; q < 32; ++q) v[q] = __fmul_rn(v[q], 1.0f / kScale);
+        result_row(p, en, p.c.io[en.item], t.b, row, row0, col0 + c0, v, patch, lane);
+      } else if (in) {
+        uint32_t h[16], l[16];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          hi[k] = pack(v[2 * k], v[2 * k + 1]);
-          const float2 h = unpack(hi[k]);
-          lo[k] = pack(__fmul_rn(__fadd_rn(v[2 * k], -h.x), kLoScale),
-                       __fmul_rn(__fadd_rn(v[2 * k + 1], -h.y), kLoScale));
+        for (int q = 0; q < 16; ++q) {
+          h[q] = pack(v[2 * q], v[2 * q + 1]);
+          const float2 f = unpack(h[q]);
+          l[q] = pack(__fmul_rn(__fadd_rn(v[2 * q], -f.x), kLoScale),
+                      __fmul_rn(__fadd_rn(v[2 * q + 1], -f.y), kLoScale));
         }
-        store_row(e.x[cur ^ 1] + at, hi);
-        store_row(e.lo + at, lo);
+        store_row(to + c0, h);
+        store_row(lo_at + c0, l);
       }
     }
   }
@@ -336,6 +352,12 @@ __device__ __forceinline__ void epilogue(const Products& p, const Tile& t, uint3
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive_cluster(kPair == 2 ? peer(empty_bar, 0) : empty_bar);
+  // the tile is done when all its warps' writes are made
+  fence_proxy_async();
+  asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
+  if (warp == 0 && lane == 0)
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + t.unit) : "memory");
+  return true;
 }
 
 template <int kPair>
@@ -348,8 +370,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t stages = smem_u32(base);
   float* patches = reinterpret_cast<float*>(base + kStages * kStageBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kStages * kStageBytes + kPatchBytes);
-  int32_t* starts = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kPatchBytes + 256);
+  float* cols = reinterpret_cast<float*>(base + kStages * kStageBytes + kPatchBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kStages * kStageBytes + kPatchBytes + kDiagBytes);
+  int32_t* starts = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kPatchBytes + kDiagBytes + 256);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, tmem_at = drain + 8;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -378,21 +401,19 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int64_t total = (2ll * starts[p.c.n] + starts[2 * p.c.n + 1]) * p.steps;
   const int first = blockIdx.x / kPair, stride = gridDim.x / kPair;
 
-  if (warp == 0) {
-    // ---- TMA.  The warp walks together; one lane issues.
+  if (warp == 0 || warp == 3) {
+    // ---- TMA: warp 0 the first operand, warp 3 the second.  A warp walks
+    // together; one lane issues.
+    const int side = warp == 3;
     uint32_t s = 0, phase = 1;
     int64_t issued = 0;
     bool ok = true;
     for (int64_t index = first; ok && index < total; index += stride) {
       const Tile t = tile_at<kPair>(p, starts, index);
       const Entry& e = p.c.entries[t.entry];
-      const Side sa = side_of(e, t.which, 0), sb = side_of(e, t.which, 1);
-      const CUtensorMap* map = p.maps + 4 * t.entry;
-      const CUtensorMap* mx = map + (t.step & 1);
-      const CUtensorMap* ma = sa == kSymmetric ? map + 1 + t.which : mx;
-      const CUtensorMap* mb = sb == kSymmetric ? map + 1 + t.which : mx;
-      const int am = t.i * kTile, bm = t.j * kTile;
-      const int a0 = am + (int)rank * 128, b0 = bm + (int)rank * 128;
+      const Side how = side_of(e, t.which, side);
+      const CUtensorMap* map = p.maps + 8 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
+      const int m0 = (side ? t.j : t.i) * kTile, at = m0 + (int)rank * 128;
       const int depth = t.which == 0 ? e.l : e.k;
       if (t.need) {
         ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
@@ -403,16 +424,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
         const uint32_t bar = kPair == 2 ? peer(full + 8 * s, 0) : full + 8 * s;
-        const uint32_t to = stages + s * kStageBytes;
-        const bool xa = across<kPair>(sa, am, k0), xb = across<kPair>(sb, bm, k0);
-        const int ax = xa ? a0 : k0, ay = xa ? k0 : a0, bx = xb ? b0 : k0, by = xb ? k0 : b0;
-        const int adx = xa ? 64 : 0, ady = 64 - adx, bdx = xb ? 64 : 0, bdy = 64 - bdx;
+        const uint32_t to = stages + s * kStageBytes + side * kOperandBytes;
+        const bool x = across<kPair>(how, m0, k0);
         if (elected()) {
-          if (rank == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
-          tma_load<kPair>(to, ma, bar, ax, ay, t.b);
-          tma_load<kPair>(to + kBoxBytes, ma, bar, ax + adx, ay + ady, t.b);
-          tma_load<kPair>(to + kOperandBytes, mb, bar, bx, by, t.b);
-          tma_load<kPair>(to + kOperandBytes + kBoxBytes, mb, bar, bx + bdx, by + bdy, t.b);
+          if (rank == 0 && side == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
+          if (x) {
+            tma_load<kPair>(to, map + 4, bar, at, k0, t.b);
+            tma_load<kPair>(to + kBoxBytes, map + 4, bar, at + 64, k0, t.b);
+          } else {
+            tma_load<kPair>(to, map, bar, k0, at, t.b);
+          }
         }
         __syncwarp();
         ++issued;
@@ -427,7 +448,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
     }
-    if (!ok && rank == 0) {
+    if (!ok && rank == 0 && side == 0) {
       const uint64_t t0 = now_ns();
       const int held = (int)(issued < kStages ? issued : kStages);
       for (int q = 0; q < held; ++q) {
@@ -483,26 +504,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     float* patch = patches + (warp - 4) * 32 * (kPatchCols + 1);
     for (int64_t index = first; index < total; index += stride) {
       const Tile t = tile_at<kPair>(p, starts, index);
-      bool ok = true;
-      if (lane == 0) ok = mbar_wait(acc_full + 8 * acc, phase, fault);
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      // all eight warps go on or none: the count below is of whole tiles
-      int go;
-      asm volatile(
-          "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\n"
-          "barrier.red.and.pred q, 1, %2, p;\nselp.b32 %0, 1, 0, q;\n}"
-          : "=r"(go)
-          : "r"((int)ok), "r"(32 * kEpiWarps)
-          : "memory");
-      if (!go) break;
-      tc_fence_after();
-      epilogue<kPair>(p, t, tmem + acc * kTile, warp - 4, lane, rank, patch, acc_empty + 8 * acc);
-      fence_proxy_async();
-      asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
-      if (warp == 4 && lane == 0) {
-        __threadfence();
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + t.unit) : "memory");
-      }
+      if (!epilogue<kPair>(p, t, tmem + acc * kTile, acc_full + 8 * acc, phase, acc_empty + 8 * acc,
+                           warp - 4, lane, rank, patch, cols))
+        break;
       if (++acc == 2) { acc = 0; phase ^= 1; }
     }
   }
