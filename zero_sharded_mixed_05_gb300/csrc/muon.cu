@@ -156,12 +156,12 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 CUtensorMapFloatOOBfill);
 
 // Map of a [batch][rows][cols] array of binary16 numbers read in boxes of
-// `box_rows` x 64; what lies outside of it reads as zero.
-bool encode(EncodeTiled fn, CUtensorMap* map, int box_rows, __half* p, int64_t cols, int64_t rows,
-            int64_t batch, int64_t ld) {
+// 128 x 64; what lies outside of it reads as zero.
+bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t cols, int64_t rows, int64_t batch,
+            int64_t ld) {
   const cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t stride[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 128, 1}, step[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dim, stride, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -174,7 +174,7 @@ cudaError_t place(zero_muon_t h) {
   int64_t units = 0;
   for (const zm::Entry& e : h->entries) units += e.batch;
   const int64_t ws = lay.take(sizeof(zm::Workspace)), table = lay.take(n * sizeof(zm::Entry));
-  const int64_t maps = lay.take(8 * n * sizeof(CUtensorMap)), starts = lay.take(2 * (n + 1) * 4);
+  const int64_t maps = lay.take(4 * n * sizeof(CUtensorMap)), starts = lay.take(2 * (n + 1) * 4);
   const int64_t io = lay.take(n * sizeof(zm::Io));
   const int64_t part = lay.take(h->chunks * sizeof(double)), ticket = lay.take(units * 4),
                 inv = lay.take(units * 4), done = lay.take(units * 4);
@@ -185,7 +185,7 @@ cudaError_t place(zero_muon_t h) {
     for (int64_t bytes : {x, x, x, a, a, e.batch * e.ldk * 4}) at.push_back(lay.take(bytes));
   }
   h->bytes = lay.size;
-  std::vector<CUtensorMap> map(8 * n);
+  std::vector<CUtensorMap> map(4 * n);
   std::vector<int32_t> first(2 * (n + 1), 0);
   cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->mem), (size_t)h->bytes);
   if (e != cudaSuccess) return e;
@@ -204,15 +204,11 @@ cudaError_t place(zero_muon_t h) {
     en.a = reinterpret_cast<__half*>(h->mem + at[6 * i + 3]);
     en.b = reinterpret_cast<__half*>(h->mem + at[6 * i + 4]);
     en.diag = reinterpret_cast<float*>(h->mem + at[6 * i + 5]);
-    bool ok = true;
-    for (int j = 0; j < 2; ++j) {
-      CUtensorMap* m = &map[8 * i + 4 * j];
-      const int box = j ? 64 : 128;
-      ok = ok && encode(fn, m, box, en.x[0], en.cols, en.rows, en.batch, en.ldx) &&
-           encode(fn, m + 1, box, en.x[1], en.cols, en.rows, en.batch, en.ldx) &&
-           encode(fn, m + 2, box, en.a, en.k, en.k, en.batch, en.ldk) &&
-           encode(fn, m + 3, box, en.b, en.k, en.k, en.batch, en.ldk);
-    }
+    CUtensorMap* m = &map[4 * i];
+    const bool ok = encode(fn, m, en.x[0], en.cols, en.rows, en.batch, en.ldx) &&
+                    encode(fn, m + 1, en.x[1], en.cols, en.rows, en.batch, en.ldx) &&
+                    encode(fn, m + 2, en.a, en.k, en.k, en.batch, en.ldk) &&
+                    encode(fn, m + 3, en.b, en.k, en.k, en.batch, en.ldk);
     if (!ok) return cudaErrorInvalidValue;
     const int64_t nk = (en.k + tile - 1) / tile, nr = (en.rows + tile - 1) / tile,
                   nc = (en.cols + tile - 1) / tile;

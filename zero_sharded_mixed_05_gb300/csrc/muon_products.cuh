@@ -12,7 +12,7 @@
 // What bounds it: the tensor cores, for matrices of a few thousand; the
 // latency of fifteen dependent products for small ones.  Hence:
 // - one persistent CTA pair an SM pair, 256 x 256 tiles (cta_group::2: each CTA
-//   stages half of both operands, 32 KB a stage of depth 64, and holds half of
+//   stages half of both operands, 64 KB a stage of depth 128, and holds half of
 //   the tile's accumulators), or single CTAs with 128 x 128 tiles where 256
 //   would mostly be empty;
 // - TMA, products and epilogue run in warps of their own, through a ring of
@@ -31,6 +31,8 @@
 // and e H enters X's update in binary32.
 #pragma once
 
+#include <climits>
+
 #include "muon_kernels.cuh"
 #include "sm103.cuh"
 
@@ -38,9 +40,10 @@ namespace zm {
 
 using namespace sm103;
 
-constexpr int kStages = 6;
-constexpr int kBoxBytes = 64 * 64 * 2;
-constexpr int kOperandBytes = 2 * kBoxBytes;       // a CTA's 128 rows, 64 deep
+constexpr int kStages = 3;
+constexpr int kDepth = 128;                        // of a stage
+constexpr int kBoxBytes = 128 * 64 * 2;
+constexpr int kOperandBytes = 2 * kBoxBytes;       // a CTA's 128 rows (or columns) of it
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = 32 * (4 + kEpiWarps);
@@ -50,8 +53,7 @@ constexpr int kDiagBytes = 256 * 4;
 
 struct Products {
   Call c;
-  const CUtensorMap* maps;   // eight an entry: x[0], x[1], a, b in boxes of 128 rows
-                             // (depth along the rows), and the same in boxes of 64
+  const CUtensorMap* maps;   // four an entry: x[0], x[1], a, b
   const int32_t* starts;     // [2][n + 1]: first tile of each entry, triangular and full
   int32_t steps;
   float coef[ZERO_MUON_MAX_STEPS][3];
@@ -121,11 +123,16 @@ __device__ __forceinline__ Side side_of(const Entry& e, int which, int s) {
   return s == 0 ? kSymmetric : kAcross;
 }
 
+// The depth from which on the operand's numbers lie down the rows.
 template <int kPair>
-__device__ __forceinline__ bool across(Side s, int at, int k0) {
+__device__ __forceinline__ int across_from(Side s, int at) {
   constexpr int kTile = 128 * kPair;
-  return s == kAcross || (s == kSymmetric && k0 / kTile > at / kTile);
+  return s == kAcross ? 0 : s == kAlong ? INT_MAX : (at / kTile + 1) * kTile;
 }
+
+// What every lane holds alike, said so to the compiler: the issuing loops run
+// on the warp's uniform registers.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ uint32_t pack(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -375,7 +382,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   int32_t* starts = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kPatchBytes + kDiagBytes + 256);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, tmem_at = drain + 8;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t rank = kPair == 2 ? cluster_rank() : 0;
   int* fault = &p.c.ws->fault;
 
@@ -412,28 +419,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const Tile t = tile_at<kPair>(p, starts, index);
       const Entry& e = p.c.entries[t.entry];
       const Side how = side_of(e, t.which, side);
-      const CUtensorMap* map = p.maps + 8 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
-      const int m0 = (side ? t.j : t.i) * kTile, at = m0 + (int)rank * 128;
-      const int depth = t.which == 0 ? e.l : e.k;
+      const CUtensorMap* map = p.maps + 4 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
+      const int m0 = (side ? t.j : t.i) * kTile, at = uniform(m0 + (int)rank * 128);
+      const int depth = uniform(t.which == 0 ? e.l : e.k), turn = uniform(across_from<kPair>(how, m0));
+      const int b = uniform(t.b);
       if (t.need) {
         ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
         if (!ok) break;
         fence_proxy_async();
       }
-      for (int k0 = 0; k0 < depth; k0 += 64) {
+      for (int k0 = 0; k0 < depth; k0 += kDepth) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
         const uint32_t bar = kPair == 2 ? peer(full + 8 * s, 0) : full + 8 * s;
         const uint32_t to = stages + s * kStageBytes + side * kOperandBytes;
-        const bool x = across<kPair>(how, m0, k0);
+        const bool x = k0 >= turn;
         if (elected()) {
           if (rank == 0 && side == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
-          if (x) {
-            tma_load<kPair>(to, map + 4, bar, at, k0, t.b);
-            tma_load<kPair>(to + kBoxBytes, map + 4, bar, at + 64, k0, t.b);
-          } else {
-            tma_load<kPair>(to, map, bar, k0, at, t.b);
-          }
+          tma_load<kPair>(to, map, bar, x ? at : k0, x ? k0 : at, b);
+          tma_load<kPair>(to + kBoxBytes, map, bar, (x ? at : k0) + 64, x ? k0 : at, b);
         }
         __syncwarp();
         ++issued;
@@ -465,27 +469,30 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int64_t index = first; ok && index < total; index += stride) {
       const Tile t = tile_at<kPair>(p, starts, index);
       const Entry& e = p.c.entries[t.entry];
-      const Side sa = side_of(e, t.which, 0), sb = side_of(e, t.which, 1);
-      const int am = t.i * kTile, bm = t.j * kTile;
-      const int depth = t.which == 0 ? e.l : e.k;
+      const int ta = uniform(across_from<kPair>(side_of(e, t.which, 0), t.i * kTile));
+      const int tb = uniform(across_from<kPair>(side_of(e, t.which, 1), t.j * kTile));
+      const int depth = uniform(t.which == 0 ? e.l : e.k);
       ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * acc, acc_phase, fault));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kTile;
-      for (int k0 = 0; k0 < depth; k0 += 64) {
-        const bool xa = across<kPair>(sa, am, k0), xb = across<kPair>(sb, bm, k0);
+      for (int k0 = 0; k0 < depth; k0 += kDepth) {
+        const bool xa = k0 >= ta, xb = k0 >= tb;
         const uint32_t idesc = instruction(kTile, kTile, xa, xb);
         const uint32_t at = stages + s * kStageBytes;
         const uint64_t da = operand(at, kBoxBytes), db = operand(at + kOperandBytes, kBoxBytes);
-        // 16 deep: 32 bytes along a row, or 16 rows of 128 bytes
-        const uint64_t ia = xa ? 16 * 128 >> 4 : 32 >> 4, ib = xb ? 16 * 128 >> 4 : 32 >> 4;
         ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, phase, fault));
         if (!ok) break;
         tc_fence_after();
         if (elected()) {
-          mma_f16_x4<kPair>(d, da, db, ia, ib, idesc, k0 > 0);
+#pragma unroll
+          for (int q = 0; q < kDepth / 16; ++q) {
+            // 16 deep: 32 bytes along a row (four to a box), or 16 rows of 128 bytes
+            const uint32_t along = (q / 4 * kBoxBytes + q % 4 * 32) >> 4, down = q * 16 * 128 >> 4;
+            mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > 0 || q > 0);
+          }
           mma_commit<kPair>(empty + 8 * s);
-          if (k0 + 64 >= depth) mma_commit<kPair>(acc_full + 8 * acc);
+          if (k0 + kDepth >= depth) mma_commit<kPair>(acc_full + 8 * acc);
         }
         __syncwarp();
         if (++s == kStages) { s = 0; phase ^= 1; }

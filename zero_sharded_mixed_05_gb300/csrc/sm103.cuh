@@ -212,20 +212,10 @@ __device__ __forceinline__ void tmem_load_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Four products, 64 deep: the descriptors' low words step by `ia` and `ib`.
-template <int kPair>
-__device__ __forceinline__ void mma_f16_x4(uint32_t d, uint64_t a, uint64_t b, uint64_t ia, uint64_t ib,
-                                           uint32_t idesc, uint32_t add) {
-  mma_f16<kPair>(d, a, b, idesc, add);
-  mma_f16<kPair>(d, a + ia, b + ib, idesc, 1);
-  mma_f16<kPair>(d, a + 2 * ia, b + 2 * ib, idesc, 1);
-  mma_f16<kPair>(d, a + 3 * ia, b + 3 * ib, idesc, 1);
-}
-
 // Shared-memory operand of a product: 128-byte rows swizzled over groups of
-// eight (1024 bytes), stored as boxes of 64 x 64 numbers.  With the product's
-// depth along the rows' 128 bytes the groups follow at 1024 bytes; with the
-// depth down the rows, `box` is the distance of the next 64 numbers across.
+// eight (1024 bytes), stored as boxes of 128 rows of 64 numbers.  With the
+// product's depth along the rows' 128 bytes the groups follow at 1024 bytes;
+// with the depth down the rows, `box` is the distance of the next 64 numbers across.
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t box) {
   return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(box >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
