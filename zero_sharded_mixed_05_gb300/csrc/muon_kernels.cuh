@@ -3,8 +3,8 @@
 // A call is three stages:
 //   muon_stats_kernel   reads the input (for the step: gradient and momentum,
 //                       and writes the new momentum) and finds |U|_F
-//   muon_start_kernel   writes X = U / (|U|_F + eps), held as two binary16
-//                       numbers, into the workspace
+//   muon_start_kernel   writes X = U / (|U|_F + eps) into the workspace, in
+//                       binary16 for the products and in binary32
 //   muon_products_kernel steps times  A = X X^T,  B = b A + c A A,  X <- a X + B X,
 //                       the last with the result's epilogue (muon_products.cuh)
 // The workspace holds every matrix in the orientation it came in: for a wide
@@ -24,18 +24,18 @@ constexpr int kMaxEntries = ZERO_MUON_MAX_SHAPES;
 constexpr int kVec = 8;                        // numbers of a vector in the first two stages
 constexpr int kChunk = kThreads * 8;           // vectors of a CTA
 
-// X, A and B are held times 4096 (zero_muon.h); the second part of X times
-// 2^11 more, so that it is a normal number wherever the first is.
-constexpr float kScale = 4096.0f;
-constexpr float kLoScale = 2048.0f;
+// A and B are held times 4096 and X times 64, so that a product of X by itself
+// has A's scale (zero_muon.h).
+constexpr float kScale = 4096.0f, kScaleX = 64.0f;
 
 struct Entry {
   int32_t rows, cols, batch, k, l, tall;
-  int64_t ldx, ldk;          // elements from row to row of x/lo and of a/b
+  int64_t ldx, ldk;          // elements from row to row of x and of a/b
   __half* x[2];              // [batch][rows][ldx], read and written in turn
-  __half* lo;
+  float* x32;                // the same numbers in binary32, in blocks
   __half* a;                 // [batch][k][ldk]
   __half* b;
+  __half* a_blk;             // a in blocks
   float* diag;               // [batch][ldk]: A's diagonal
   int32_t unit0;             // first matrix of the entry among all
   int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
@@ -43,6 +43,20 @@ struct Entry {
   int32_t item;              // the caller's index
   float s;                   // scale_rule's factor
 };
+
+// Blocks of 32 x 32 numbers, for what only an epilogue reads and writes, where
+// a thread holds a row: 16-byte pieces of the 32 rows lie side by side, so
+// that a warp's access is whole lines (a row-major access by rows touches a
+// line a thread and was what bound the epilogue).  The place of the piece
+// with columns col.. of a row, in an array with `ld` columns (a multiple of
+// 32), counted from the matrix's first number.
+template <typename T>
+__device__ __forceinline__ int64_t block_at(int row, int col, int64_t ld) {
+  constexpr int kPiece = 16 / sizeof(T);
+  return ((int64_t)(row / 32) * (ld / 32) + col / 32) * 1024 + (col % 32) / kPiece * (32 * kPiece) +
+         row % 32 * kPiece;
+}
+__host__ __device__ inline int64_t block_size(int64_t rows, int64_t ld) { return (rows + 31) / 32 * 32 * ld; }
 
 // What a call was given for one entry.
 struct Io {
@@ -234,16 +248,6 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
   }
 }
 
-// x times kScale as a sum of two binary16 numbers, the second times kLoScale.
-__device__ __forceinline__ void split(float x, __half* hi, __half* lo) {
-  *hi = __float2half_rn(x);
-  *lo = __float2half_rn(__fmul_rn(__fadd_rn(x, -__half2float(*hi)), kLoScale));
-}
-
-__device__ __forceinline__ float joined(__half hi, __half lo) {
-  return __fmaf_rn(__half2float(lo), 1.0f / kLoScale, __half2float(hi));
-}
-
 // Stage 2.  Reads U's sources again (from L2 where they fit) and writes X.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ Call c) {
@@ -259,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
   const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
   const float f = grad_factor(c), inv = c.inv[e.unit0 + b];
   const int64_t base = (int64_t)b * e.rows * e.ldx;
+  float* x32 = e.x32 + (int64_t)b * block_size(e.rows, e.ldx);
 #pragma unroll 4
   for (int i = 0; i < kChunk / kThreads; ++i) {
     const uint32_t v = (uint32_t)chunk * kChunk + i * kThreads + threadIdx.x;
@@ -275,35 +280,53 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
 #pragma unroll
       for (int j = 0; j < kVec; ++j) u[j] = x[j];
     }
-    __align__(16) __half hi[kVec], lo[kVec];
+    __align__(16) __half h[kVec];
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) split(__fmul_rn(__fmul_rn(u[j], inv), kScale), &hi[j], &lo[j]);
-    // rows of the workspace are multiples of 16 numbers: the vector fits
-    const int64_t to = base + (int64_t)row * e.ldx + col;
-    *reinterpret_cast<uint4*>(e.x[0] + to) = *reinterpret_cast<const uint4*>(hi);
-    *reinterpret_cast<uint4*>(e.lo + to) = *reinterpret_cast<const uint4*>(lo);
+    for (int j = 0; j < kVec; ++j) {
+      u[j] = __fmul_rn(__fmul_rn(u[j], inv), kScaleX);
+      h[j] = __float2half_rn(u[j]);
+    }
+    // rows of the workspace are multiples of 32 numbers: the vector fits
+    *reinterpret_cast<uint4*>(e.x[0] + base + (int64_t)row * e.ldx + col) = *reinterpret_cast<const uint4*>(h);
+    float* blk = x32 + block_at<float>(row, col, e.ldx);
+    *reinterpret_cast<float4*>(blk) = make_float4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<float4*>(blk + 128) = make_float4(u[4], u[5], u[6], u[7]);
   }
 }
 
-// One number of the result: O itself, or the step with it.
-__device__ __forceinline__ void finish(const Call& c, const Entry& e, const Io& io, int b, int row,
-                                       int col, float o) {
+// R numbers of the result, every S-th row from `row` on: O itself, o(0).., or the
+// step with it.
+template <int R, int S, typename F>
+__device__ __forceinline__ void finish(const Call& c, const Entry& e, const Io& io, int b, int row, int col, F o) {
   if (!c.step) {
     const int64_t at = (int64_t)b * io.out_batch + (int64_t)row * io.out_row + col;
-    if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[at] = as<__half>(o);
-    else if (c.out_type == ZERO_BF16) static_cast<__nv_bfloat16*>(io.out)[at] = as<__nv_bfloat16>(o);
-    else static_cast<float*>(io.out)[at] = o;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t i = at + r * S * io.out_row;
+      if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[i] = as<__half>(o(r));
+      else if (c.out_type == ZERO_BF16) static_cast<__nv_bfloat16*>(io.out)[i] = as<__nv_bfloat16>(o(r));
+      else static_cast<float*>(io.out)[i] = o(r);
+    }
     return;
   }
   const int64_t at = ((int64_t)b * e.rows + row) * e.cols + col;
-  float w;
-  if (io.master) w = io.master[at];
-  else if (c.out_type == ZERO_FP16) w = num<__half>(static_cast<__half*>(io.out)[at]);
-  else w = num<__nv_bfloat16>(static_cast<__nv_bfloat16*>(io.out)[at]);
-  w = __fmaf_rn(-__fmul_rn(c.lr, e.s), o, __fmul_rn(w, c.decay));
-  if (io.master) io.master[at] = w;
-  if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[at] = as<__half>(w);
-  else static_cast<__nv_bfloat16*>(io.out)[at] = as<__nv_bfloat16>(w);
+  float w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = at + (int64_t)r * S * e.cols;
+    if (io.master) w[r] = io.master[i];
+    else if (c.out_type == ZERO_FP16) w[r] = num<__half>(static_cast<__half*>(io.out)[i]);
+    else w[r] = num<__nv_bfloat16>(static_cast<__nv_bfloat16*>(io.out)[i]);
+  }
+  const float step = -__fmul_rn(c.lr, e.s);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = at + (int64_t)r * S * e.cols;
+    w[r] = __fmaf_rn(step, o(r), __fmul_rn(w[r], c.decay));
+    if (io.master) io.master[i] = w[r];
+    if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[i] = as<__half>(w[r]);
+    else static_cast<__nv_bfloat16*>(io.out)[i] = as<__nv_bfloat16>(w[r]);
+  }
 }
 
 }  // namespace zm

@@ -1,6 +1,6 @@
 // muon_products.cuh -- all products of an orthogonalisation in one kernel.
 //
-// For every matrix and step, with H the first part of X (muon_kernels.cuh):
+// For every matrix and step, with H the binary16 rounding of X:
 //   which 0   A = H H^T (H^T H for a tall matrix)
 //   which 1   B = b A + c A A
 //   which 2   X <- a X + B H (a X + H B for a tall matrix); after the last
@@ -17,7 +17,8 @@
 //   would mostly be empty;
 // - TMA, products and epilogue run in warps of their own, through a ring of
 //   stages and two accumulators, so that a tile's epilogue is hidden behind
-//   the next tile's products;
+//   the next tile's products; the first TMA warp finds out what the next tile
+//   is and waits for what it needs, and tells the others by a ring of tiles;
 // - no launch between dependent products: the tiles of all products of all
 //   matrices form one list in which every tile comes after those that it
 //   needs, dealt out in turn; a tile waits for its matrix's count of finished
@@ -47,68 +48,100 @@ constexpr int kOperandBytes = 2 * kBoxBytes;       // a CTA's 128 rows (or colum
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;
 constexpr int kProductThreads = 32 * (4 + kEpiWarps);
-constexpr int kPatchCols = 16;
-constexpr int kPatchBytes = kEpiWarps * 32 * (kPatchCols + 1) * 4;
-constexpr int kDiagBytes = 256 * 4;
+constexpr int kPatchBytes = kEpiWarps * 2048;      // a warp's 32 rows of 64 bytes
+constexpr int kDiagBytes = 2 * 256 * 4;            // of two tiles
+constexpr int kSlots = 16;                         // tiles a CTA has in work: 3 stages, 2 accumulators,
+                                                   // 2 being counted; the rest is slack
 
 struct Products {
   Call c;
   const CUtensorMap* maps;   // four an entry: x[0], x[1], a, b
-  const int32_t* starts;     // [2][n + 1]: first tile of each entry, triangular and full
-  int32_t steps;
+  const struct Group* group;
+  const struct Stretch* stretch;
+  int64_t tiles;             // of all groups
+  int32_t groups, steps;
   float coef[ZERO_MUON_MAX_STEPS][3];
 };
 
+// A stretch of matrices of one entry.  The tiles go out group by group, a group
+// being stretches whose working set stays in L2 through all their products
+// (one after another; see muon.cu), and within a group product by product.
+struct Stretch {
+  int32_t entry, b0;                 // matrices b0.. of the entry
+  int32_t triangles, fulls;          // tiles of the group's stretches before this one
+};
+struct Group {
+  int64_t first;                     // tiles of the groups before
+  int32_t stretch0, stretches;
+  int32_t triangles, fulls;          // tiles of a product of the first two kinds, and of the third
+};
+
 struct Tile {
-  int entry, b, step, which, i, j, unit;
+  Entry e;
+  int entry, b, step, which, i, j, unit, depth;
   uint32_t need;             // finished CTA tiles of the matrix that it waits for
 };
 
-constexpr int smem_bytes(int n) {
-  return 1024 + kStages * kStageBytes + kPatchBytes + kDiagBytes + 256 + 2 * (n + 1) * 4;
-}
+constexpr int kProductSmem = kStages * kStageBytes + kPatchBytes + kDiagBytes + 256 + kSlots * (int)sizeof(Tile);
 
 template <int kPair>
-__device__ __forceinline__ Tile tile_at(const Products& p, const int32_t* starts, int64_t index) {
+__device__ __forceinline__ void tile_at(const Products& p, int64_t index, int lane, Tile* out) {
   constexpr int kTile = 128 * kPair;
-  const int n = p.c.n;
-  const int32_t *tri = starts, *full = starts + n + 1;
-  const int64_t per = 2ll * tri[n] + full[n];
-  Tile t;
-  t.step = (int)(index / per);
-  int r = (int)(index - t.step * per);
-  t.which = r < tri[n] ? 0 : r < 2 * tri[n] ? 1 : 2;
-  r -= t.which == 0 ? 0 : t.which == 1 ? tri[n] : 2 * tri[n];
-  const int32_t* at = t.which == 2 ? full : tri;
-  int lo = 0, hi = n;                      // the last entry that starts at or before r
+  int lo = 0, hi = p.groups;               // the last group that starts at or before it
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (at[mid] <= r) lo = mid; else hi = mid;
+    if (p.group[mid].first <= index) lo = mid; else hi = mid;
   }
-  t.entry = lo;
-  r -= at[lo];
-  const Entry& e = p.c.entries[lo];
-  const int nk = (e.k + kTile - 1) / kTile, nr = (e.rows + kTile - 1) / kTile,
-            nc = (e.cols + kTile - 1) / kTile;
+  const Group g = p.group[lo];
+  index -= g.first;
+  const int per = 2 * g.triangles + g.fulls;
+  const int step = (int)(index / per);
+  int r = (int)(index - (int64_t)step * per);
+  const int which = r < g.triangles ? 0 : r < 2 * g.triangles ? 1 : 2;
+  r -= which * g.triangles;
+  const Stretch* s = p.stretch + g.stretch0;
+  lo = 0, hi = g.stretches;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if ((which == 2 ? s[mid].fulls : s[mid].triangles) <= r) lo = mid; else hi = mid;
+  }
+  const Stretch st = s[lo];
+  r -= which == 2 ? st.fulls : st.triangles;
+  const Entry& from = p.c.entries[st.entry];
+  static_assert(sizeof(Entry) % 4 == 0 && sizeof(Entry) / 4 <= 64, "copied by one warp");
+  for (int w = lane; w < (int)sizeof(Entry) / 4; w += 32)
+    reinterpret_cast<uint32_t*>(&out->e)[w] = reinterpret_cast<const uint32_t*>(&from)[w];
+  __syncwarp();
+  const Entry& e = out->e;
+  const int nk = (e.k + kTile - 1) / kTile, nr = (e.rows + kTile - 1) / kTile, nc = (e.cols + kTile - 1) / kTile;
   const int ntri = nk * (nk + 1) / 2, nfull = nr * nc;
-  const int each = t.which == 2 ? nfull : ntri;
-  t.b = r / each;
-  r -= t.b * each;
-  t.unit = e.unit0 + t.b;
-  if (t.which == 2) {
+  const int each = which == 2 ? nfull : ntri;
+  const int b = st.b0 + r / each;
+  r %= each;
+  int i, j;
+  if (which == 2) {
     // the short side runs fastest: X streams by once, B stays in L2
-    t.i = e.tall ? r / nc : r % nr;
-    t.j = e.tall ? r % nc : r / nr;
+    i = e.tall ? r / nc : r % nr;
+    j = e.tall ? r % nc : r / nr;
   } else {
-    int i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
+    i = (int)((sqrtf(8.0f * (float)r + 1.0f) - 1.0f) * 0.5f);
     while ((i + 1) * (i + 2) / 2 <= r) ++i;
     while (i * (i + 1) / 2 > r) --i;
-    t.i = i;
-    t.j = r - i * (i + 1) / 2;
+    j = r - i * (i + 1) / 2;
   }
-  t.need = (uint32_t)kPair * ((uint32_t)t.step * (2 * ntri + nfull) +
-                              (t.which == 0 ? 0u : t.which == 1 ? (uint32_t)ntri : 2u * ntri));
-  return t;
+  if (lane == 0) {
+    out->entry = st.entry;
+    out->b = b;
+    out->step = step;
+    out->which = which;
+    out->i = i;
+    out->j = j;
+    out->unit = e.unit0 + b;
+    out->depth = which == 0 ? e.l : e.k;
+    out->need = (uint32_t)kPair * ((uint32_t)step * (2 * ntri + nfull) +
+                                   (which == 0 ? 0u : which == 1 ? (uint32_t)ntri : 2u * ntri));
+  }
+  __syncwarp();
 }
 
 // How one side of a product is read: rows `at`.. of a stored matrix with the
@@ -142,103 +175,61 @@ __device__ __forceinline__ float2 unpack(uint32_t u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
-// 32 binary16 numbers at a 32-byte address.
-__device__ __forceinline__ void load_row(const __half* p, uint32_t* v) {
-  load32(p, v);
-  load32(p + 16, v + 8);
-}
-__device__ __forceinline__ void store_row(__half* p, const uint32_t* v) {
-  store32(p, v);
-  store32(p + 16, v + 8);
+// The warp's shared memory: 32 rows of 64 bytes, the 16-byte pieces of a row in
+// an order of the row's own, so that neither rows nor pieces collide.
+__device__ __forceinline__ uint4* piece(float* patch, int row, int at) {
+  return reinterpret_cast<uint4*>(patch) + row * 4 + (at ^ (row / 2 & 3));
 }
 
-// The result of 32 numbers of a row a thread, columns col..col+31.
-__device__ __forceinline__ void result_row(const Products& p, const Entry& e, const Io& io, int b, int row,
-                                           int row0, int col, float* o, float* patch, int lane) {
-  const bool half_out = p.c.out_type != ZERO_FP32;
-  const int es = half_out ? 2 : 4;
-  const int n = min(32, e.cols - col);
-  const uintptr_t rows32 = (uintptr_t)(io.out_row * es) | (uintptr_t)(io.out_batch * es);
-  bool wide = ((reinterpret_cast<uintptr_t>(io.out) | rows32) & 31) == 0;
-  if (p.c.step && io.master)
-    wide = wide && ((reinterpret_cast<uintptr_t>(io.master) | ((uintptr_t)e.cols * 4)) & 31) == 0;
-  if (wide && n == 32) {
-    // whole sectors a thread
-    if (row >= e.rows) return;
-    const int64_t at = (int64_t)b * io.out_batch + (int64_t)row * io.out_row + col;
-    char* out = static_cast<char*>(io.out) + at * es;
-    if (p.c.step) {
-      const float step = -__fmul_rn(p.c.lr, e.s);
+// Writes the patch as 32 binary16 numbers of each of the rows row0.. to a
+// row-major array, columns col.., whole sectors at a time.
+__device__ __forceinline__ void flush(float* patch, __half* to, int64_t ld, int row0, int rows, int col, int lane) {
+  __syncwarp();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float w[8];
-        if (io.master) {
-          load32(io.master + at + 8 * q, reinterpret_cast<uint32_t*>(w));
-        } else {
-          const uint4 u = *reinterpret_cast<const uint4*>(out + 16 * q);
-          const uint32_t* h = reinterpret_cast<const uint32_t*>(&u);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = p.c.out_type == ZERO_FP16
-                                 ? unpack(h[k])
-                                 : make_float2(__uint_as_float(h[k] << 16), __uint_as_float(h[k] & 0xffff0000u));
-            w[2 * k] = f.x;
-            w[2 * k + 1] = f.y;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          w[k] = __fmaf_rn(step, o[8 * q + k], __fmul_rn(w[k], p.c.decay));
-          o[8 * q + k] = w[k];
-        }
-        if (io.master) store32(io.master + at + 8 * q, reinterpret_cast<const uint32_t*>(w));
-      }
-    }
-    if (!half_out) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) store32(out + 32 * q, reinterpret_cast<const uint32_t*>(o + 8 * q));
-    } else {
-      uint32_t h[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        if (p.c.out_type == ZERO_FP16) {
-          h[k] = pack(o[2 * k], o[2 * k + 1]);
-        } else {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * k], o[2 * k + 1]);
-          h[k] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-      }
-      store32(out, h);
-      store32(out + 32, h + 8);
-    }
-    return;
+  for (int q = 0; q < 4; ++q) {
+    const int r = q * 8 + lane / 4;
+    const uint4 v = *piece(patch, r, lane % 4);
+    if (row0 + r < rows) *reinterpret_cast<uint4*>(to + (int64_t)(row0 + r) * ld + col + lane % 4 * 8) = v;
   }
-  // any address: through shared memory, so that a warp writes along rows
-#pragma unroll
-  for (int c0 = 0; c0 < 32; c0 += kPatchCols) {
-#pragma unroll
-    for (int k = 0; k < kPatchCols; ++k) patch[lane * (kPatchCols + 1) + k] = o[c0 + k];
-    __syncwarp();
-    const int cc = c0 + lane % kPatchCols;
-    if (cc < n)
-      for (int r = lane / kPatchCols; r < 32; r += 32 / kPatchCols)
-        if (row0 + r < e.rows)
-          finish(p.c, e, io, b, row0 + r, col + cc, patch[r * (kPatchCols + 1) + lane % kPatchCols]);
-    __syncwarp();
-  }
+  __syncwarp();
 }
 
-// One tile's epilogue: the warp's 32 rows of the accumulator, half its columns.
-// Whatever it reads besides is fetched while the products still run: the
-// diagonal's numbers of the tile's columns go to shared memory, and of each
-// 32 columns the operands are on their way while those before are worked on.
-// False: a wait ran out.
+// The result of 32 x 16 numbers of X, in the patch as 32 rows: a warp reads and
+// writes along rows, at any address.
+__device__ __forceinline__ void result(const Products& p, const Entry& e, const Io& io, int b, int row0, int col,
+                                       float* patch, int lane) {
+  __syncwarp();
+  const int at = lane % 16;
+  if (col + at < e.cols) {
+    const auto value = [&](int r) {
+      return __fmul_rn(reinterpret_cast<const float*>(piece(patch, r, at / 4))[at % 4], 1.0f / kScaleX);
+    };
+    const int n = min(32, e.rows - row0);
+    int r = lane / 16;
+#pragma unroll 1
+    for (; r + 14 < n; r += 16)
+      finish<8, 2>(p.c, e, io, b, row0 + r, col + at, [&](int k) { return value(r + 2 * k); });
+#pragma unroll 1
+    for (; r < n; r += 2) finish<1, 2>(p.c, e, io, b, row0 + r, col + at, [&](int) { return value(r); });
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// One tile's epilogue: the warp's 32 rows of the accumulator, half its columns,
+// 16 at a time.  Whatever it reads besides is fetched while the products
+// still run: the diagonal's numbers of the tile's columns go to shared memory
+// (`cols`), and the next columns' numbers are on their way while those before
+// are worked on.  The loops are kept short: a small matrix runs each of them
+// once a tile, and straight code of 64 columns waited on instruction fetches
+// longer than it ran (64x64: 91 us).  False: a wait ran out.
 template <int kPair>
-__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, uint32_t acc, uint32_t full_bar,
-                                         uint32_t phase, uint32_t empty_bar, int warp, int lane,
-                                         uint32_t rank, float* patch, float* cols) {
+__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool ready, uint32_t acc, uint32_t full_bar,
+                                         uint32_t phase, uint32_t empty_bar, int warp, int lane, uint32_t rank,
+                                         float* patch, float* cols) {
   constexpr int kTile = 128 * kPair, kCols = kTile / 2;
-  const Entry& en = p.c.entries[t.entry];
+  const Entry& en = t.e;
   const int rows = en.rows, ncols = en.cols, k = en.k, tall = en.tall;
   const int64_t ldx = en.ldx, ldk = en.ldk;
   const int quarter = warp % 4, part = warp / 4;
@@ -246,34 +237,37 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, uint3
   const int M = t.which == 2 ? rows : k, N = t.which == 2 ? ncols : k;
   const float ca = p.coef[t.step][0], cb = p.coef[t.step][1], cc = p.coef[t.step][2];
   const bool last = t.step == p.steps - 1;
-  const int cur = t.step & 1;
-  const int col0 = t.j * kTile;
-  const int64_t at_k = ((int64_t)t.b * k + row) * ldk + col0, at_x = ((int64_t)t.b * rows + row) * ldx + col0;
-  float* diag = en.diag + (int64_t)t.b * ldk;
-  __half* const to = t.which == 0 ? en.a + at_k : t.which == 1 ? en.b + at_k : en.x[cur ^ 1] + at_x;
-  const __half* const from = t.which == 1 ? en.a + at_k : en.x[cur] + at_x;
-  __half* const lo_at = en.lo + at_x;
-  const bool in = row < M;
+  const int col0 = t.j * kTile, mine = col0 + part * kCols;   // the warp's first column
+  float* diag = en.diag + t.b * ldk;
+  // what a product reads and what only epilogues do
+  __half* const to = t.which == 0 ? en.a + t.b * k * ldk
+                     : t.which == 1 ? en.b + t.b * k * ldk : en.x[(t.step & 1) ^ 1] + t.b * rows * ldx;
+  const int64_t ld = t.which == 2 ? ldx : ldk;
+  uint4* const blk = reinterpret_cast<uint4*>(
+      t.which == 2 ? reinterpret_cast<char*>(en.x32 + t.b * block_size(rows, ldx) + block_at<float>(row, mine, ldx))
+                   : reinterpret_cast<char*>(en.a_blk + t.b * block_size(k, ldk) + block_at<__half>(row, mine, ldk)));
 
-  int ok = 1;
+  int ok = ready;
   float di = 0.0f;
-  uint32_t hi[16], lo[16];
-  const auto fetch = [&](int c0) {
-    if (t.which == 0 || !in || col0 + c0 >= N) return;
-    load_row(from + c0, hi);
-    if (t.which == 2) load_row(lo_at + c0, lo);
-  };
-  if (t.which != 0) {
-    if (lane == 0) ok = count_wait(p.c.done + t.unit, t.need, &p.c.ws->fault);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (in && (t.which == 1 || !tall)) di = __ldcg(diag + row);
-    const int c = warp * 32 + lane;
-    if (c < kTile && col0 + c < N) {
-      const float d = __ldcg(diag + col0 + c);
-      // b A + c A A: c d_j; X: e_j of a tall matrix
-      cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
+  uint4 old[4];
+  const auto fetch = [&](int c) {             // 16 columns from the warp's c on
+    if (row0 >= M || c >= kCols || mine + c >= N) return;
+    if (t.which == 1) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) old[q] = __ldcg(blk + c * 4 + q * 32);
+    } else if (t.which == 2) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) old[q] = __ldcg(blk + c * 8 + q * 32);
     }
-    fetch(part * kCols);
+  };
+  if (t.which != 0 && ok) {
+    fetch(0);
+    const int c = warp * 32 + lane;
+    float d = 0.0f;
+    if (c < kTile && col0 + c < N) d = __ldcg(diag + col0 + c);
+    if (row < M && (t.which == 1 || !tall)) di = __ldcg(diag + row);
+    // b A + c A A: c d_j; X: e_j of a tall matrix
+    if (c < kTile) cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
   }
   if (lane == 0 && ok) ok = mbar_wait(full_bar, phase, &p.c.ws->fault);
   ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -287,83 +281,73 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, uint3
   if (!ok) return false;
   tc_fence_after();
 
-  const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16) + part * kCols;
+  cols += part * kCols;
   // the row's share of b A + c A A's factor, or e_i of a wide matrix
   const float ei = t.which == 1 ? __fmaf_rn(cc, di, cb) : __fmul_rn(di, __fmaf_rn(cc, di, cb));
+  const int ncol = row0 < M ? min(kCols, N - mine) : 0;        // columns of the warp's there are
+  float next[16];
+  if (ncol > 0) tmem_load16(lanes, next);
 #pragma unroll 1
-  for (int c0 = part * kCols; c0 < (part + 1) * kCols; c0 += 32) {
-    if (col0 + c0 >= N || row0 >= M) break;
-    float v[32];
-    tmem_load32(lanes + c0, v);
+  for (int c = 0; c < ncol; c += 16) {
+    float v[16];
     tmem_load_wait();
+#pragma unroll
+    for (int q = 0; q < 16; ++q) v[q] = next[q];
+    if (c + 16 < ncol) tmem_load16(lanes + c + 16, next);
+    float2* y = reinterpret_cast<float2*>(v);
     if (t.which == 0) {
-      if (in) {
-        const int at = row - (col0 + c0);     // the diagonal's place in this row, if any
+      const int at = row - (mine + c);         // the diagonal's place, if in these columns
+      if (row0 < mine + c + 16 && row0 + 32 > mine + c) {
+        float d = 0.0f;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          v[q] = __fmul_rn(v[q], 1.0f / kScale);
-          if (q == at) {
-            __stcg(diag + row, __fmul_rn(v[q], 1.0f / kScale));
-            v[q] = 0.0f;
-          }
+        for (int q = 0; q < 16; ++q) {
+          d = q == at ? v[q] : d;
+          v[q] = q == at ? 0.0f : v[q];
         }
-#pragma unroll
-        for (int q = 0; q < 16; ++q) hi[q] = pack(v[2 * q], v[2 * q + 1]);
-        // rows are multiples of 32 numbers: nothing of the next row is written
-        store_row(to + c0, hi);
+        if (at >= 0 && at < 16 && row < M) __stcg(diag + row, __fmul_rn(d, 1.0f / kScale));
       }
     } else if (t.which == 1) {
-      if (in) {
-        uint32_t h[16];
-        const float scale = __fmul_rn(cc, 1.0f / kScale);
+      const float2 scale = both(__fmul_rn(cc, 1.0f / kScale)), e2 = both(ei);
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(old);
+      const float2* d = reinterpret_cast<const float2*>(cols + c);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float2 f = unpack(hi[q]), d = reinterpret_cast<const float2*>(cols + c0)[q];
-          h[q] = pack(__fmaf_rn(__fadd_rn(ei, d.x), f.x, __fmul_rn(scale, v[2 * q])),
-                      __fmaf_rn(__fadd_rn(ei, d.y), f.y, __fmul_rn(scale, v[2 * q + 1])));
-        }
-        if (c0 + 32 < (part + 1) * kCols) fetch(c0 + 32);
-        store_row(to + c0, h);
-      }
+      for (int q = 0; q < 8; ++q)
+        y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
+      fetch(c + 16);
     } else {
+      const float2* x = reinterpret_cast<const float2*>(old);
+      const float2* d = reinterpret_cast<const float2*>(cols + c);
+      const float2 ca2 = both(ca), down = both(1.0f / kScale), e2 = both(ei);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const float2 h = unpack(hi[q]), l = unpack(lo[q]);
-        float2 d = make_float2(ei, ei);
-        if (tall) d = reinterpret_cast<const float2*>(cols + c0)[q];
-        v[2 * q] = __fmaf_rn(v[2 * q], 1.0f / kScale,
-                             __fmaf_rn(ca, __fmaf_rn(l.x, 1.0f / kLoScale, h.x), __fmul_rn(d.x, h.x)));
-        v[2 * q + 1] = __fmaf_rn(v[2 * q + 1], 1.0f / kScale,
-                                 __fmaf_rn(ca, __fmaf_rn(l.y, 1.0f / kLoScale, h.y), __fmul_rn(d.y, h.y)));
-      }
-      if (c0 + 32 < (part + 1) * kCols) fetch(c0 + 32);
+      for (int q = 0; q < 8; ++q)
+        y[q] = __ffma2_rn(y[q], down,
+                          __ffma2_rn(ca2, x[q], __fmul2_rn(tall ? d[q] : e2, unpack(pack(x[q].x, x[q].y)))));
+      fetch(c + 16);
       if (last) {
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = __fmul_rn(v[q], 1.0f / kScale);
-        result_row(p, en, p.c.io[en.item], t.b, row, row0, col0 + c0, v, patch, lane);
-      } else if (in) {
-        uint32_t h[16], l[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          h[q] = pack(v[2 * q], v[2 * q + 1]);
-          const float2 f = unpack(h[q]);
-          l[q] = pack(__fmul_rn(__fadd_rn(v[2 * q], -f.x), kLoScale),
-                      __fmul_rn(__fadd_rn(v[2 * q + 1], -f.y), kLoScale));
-        }
-        store_row(to + c0, h);
-        store_row(lo_at + c0, l);
+        for (int q = 0; q < 4; ++q) *piece(patch, lane, q) = reinterpret_cast<const uint4*>(v)[q];
+        result(p, en, p.c.io[en.item], t.b, row0, mine + c, patch, lane);
+        continue;
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) blk[c * 8 + q * 32] = reinterpret_cast<const uint4*>(v)[q];
     }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float2* z = y + 4 * q;
+      const uint4 h = make_uint4(pack(z[0].x, z[0].y), pack(z[1].x, z[1].y), pack(z[2].x, z[2].y),
+                                 pack(z[3].x, z[3].y));
+      *piece(patch, lane, c / 8 % 4 + q) = h;
+      if (t.which == 0) blk[c * 4 + q * 32] = h;
+    }
+    // 32 columns are whole, or end here (a row has room for 32)
+    if (c % 32 || c + 16 >= ncol) flush(patch, to, ld, row0, M, mine + c / 32 * 32, lane);
   }
   // the accumulator may be written again once both CTAs have read it
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive_cluster(kPair == 2 ? peer(empty_bar, 0) : empty_bar);
-  // the tile is done when all its warps' writes are made
-  fence_proxy_async();
-  asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
-  if (warp == 0 && lane == 0)
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + t.unit) : "memory");
   return true;
 }
 
@@ -372,21 +356,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     muon_products_kernel(const __grid_constant__ Products p) {
   constexpr int kTile = 128 * kPair;
   constexpr uint32_t kTmemCols = 2 * kTile;
-  extern __shared__ unsigned char raw[];
+  extern __shared__ __align__(1024) unsigned char base[];
   if (skipped(p.c)) return;
-  unsigned char* base = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t stages = smem_u32(base);
   float* patches = reinterpret_cast<float*>(base + kStages * kStageBytes);
   float* cols = reinterpret_cast<float*>(base + kStages * kStageBytes + kPatchBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kStages * kStageBytes + kPatchBytes + kDiagBytes);
-  int32_t* starts = reinterpret_cast<int32_t*>(base + kStages * kStageBytes + kPatchBytes + kDiagBytes + 256);
-  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
-                 acc_empty = acc_full + 16, drain = acc_empty + 16, tmem_at = drain + 8;
+  unsigned char* small = base + kStages * kStageBytes + kPatchBytes + kDiagBytes;
+  Tile* slots = reinterpret_cast<Tile*>(small + 256);
+  const uint32_t full = smem_u32(small), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
+                 acc_empty = acc_full + 16, drain = acc_empty + 16, tmem_at = drain + 8,
+                 told = tmem_at + 4,       // tiles that are in the ring and whose needs are met
+                 counted = told + 4;       // tiles whose writes the counting warp has seen
+  volatile int* const stop = reinterpret_cast<volatile int*>(small + (counted - full) + 4);
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t rank = kPair == 2 ? cluster_rank() : 0;
   int* fault = &p.c.ws->fault;
 
-  for (int i = threadIdx.x; i < 2 * (p.c.n + 1); i += kProductThreads) starts[i] = p.starts[i];
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(full + 8 * s, 1);
@@ -397,6 +382,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(acc_empty + 8 * s, kPair * kEpiWarps);
     }
     mbar_init(drain, 1);
+    shared_set(told, 0);
+    shared_set(counted, 0);
+    *stop = 0;
     mbar_init_fence();
   }
   if (warp == 2) tmem_alloc<kPair>(tmem_at, kTmemCols);
@@ -404,40 +392,47 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __syncthreads();
   if (kPair == 2) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(base + (tmem_at - stages));
-  const int64_t total = (2ll * starts[p.c.n] + starts[2 * p.c.n + 1]) * p.steps;
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(small + (tmem_at - full));
   const int first = blockIdx.x / kPair, stride = gridDim.x / kPair;
+  const uint32_t mine = first < p.tiles ? (uint32_t)((p.tiles - first + stride - 1) / stride) : 0;   // tiles
 
   if (warp == 0 || warp == 3) {
     // ---- TMA: warp 0 the first operand, warp 3 the second.  A warp walks
     // together; one lane issues.
     const int side = warp == 3;
-    uint32_t s = 0, phase = 1;
-    int64_t issued = 0;
+    uint32_t s = 0, phase = 1, issued = 0;
     bool ok = true;
-    for (int64_t index = first; ok && index < total; index += stride) {
-      const Tile t = tile_at<kPair>(p, starts, index);
-      const Entry& e = p.c.entries[t.entry];
-      const Side how = side_of(e, t.which, side);
+    for (uint32_t n = 0; ok && n < mine; ++n) {
+      Tile& t = slots[n % kSlots];
+      if (side == 0) {
+        tile_at<kPair>(p, first + (int64_t)n * stride, lane, &t);
+        if (t.need) ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
+        if (!ok) break;
+        if (lane == 0) shared_set(told, n + 1);
+      } else {
+        ok = __all_sync(0xffffffffu, shared_wait(told, n + 1, fault));
+        if (!ok) break;
+      }
+      if (t.need) fence_proxy_async();
+      const Side how = side_of(t.e, t.which, side), other = side_of(t.e, t.which, side ^ 1);
       const CUtensorMap* map = p.maps + 4 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
       const int m0 = (side ? t.j : t.i) * kTile, at = uniform(m0 + (int)rank * 128);
-      const int depth = uniform(t.which == 0 ? e.l : e.k), turn = uniform(across_from<kPair>(how, m0));
-      const int b = uniform(t.b);
-      if (t.need) {
-        ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
-        if (!ok) break;
-        fence_proxy_async();
-      }
+      const int turn = uniform(across_from<kPair>(how, m0));
+      const int other_turn = uniform(across_from<kPair>(other, (side ? t.i : t.j) * kTile));
+      const int depth = uniform(t.depth), b = uniform(t.b);
       for (int k0 = 0; k0 < depth; k0 += kDepth) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
         const uint32_t bar = kPair == 2 ? peer(full + 8 * s, 0) : full + 8 * s;
         const uint32_t to = stages + s * kStageBytes + side * kOperandBytes;
         const bool x = k0 >= turn;
+        // a box along the rows that would lie beyond the depth is left out
+        const bool both = depth - k0 > 64;
         if (elected()) {
-          if (rank == 0 && side == 0) mbar_expect(full + 8 * s, kPair * kStageBytes);
+          if (rank == 0 && side == 0)
+            mbar_expect(full + 8 * s, kPair * kBoxBytes * (2 + (both || x) + (both || k0 >= other_turn)));
           tma_load<kPair>(to, map, bar, x ? at : k0, x ? k0 : at, b);
-          tma_load<kPair>(to + kBoxBytes, map, bar, (x ? at : k0) + 64, x ? k0 : at, b);
+          if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, (x ? at : k0) + 64, x ? k0 : at, b);
         }
         __syncwarp();
         ++issued;
@@ -447,18 +442,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // Every stage that was filled is released (or, after a fault, has at
     // least arrived) before the CTA may end.
     if (ok) {
-      for (int q = 0; ok && q < kStages && q < issued; ++q) {
+      for (uint32_t q = 0; ok && q < kStages && q < issued; ++q) {
         ok = mbar_wait(empty + 8 * s, phase, fault);
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
     }
     if (!ok && rank == 0 && side == 0) {
       const uint64_t t0 = now_ns();
-      const int held = (int)(issued < kStages ? issued : kStages);
-      for (int q = 0; q < held; ++q) {
-        const int64_t at = issued - held + q;
-        while (!mbar_try(full + 8 * (uint32_t)(at % kStages), (uint32_t)(at / kStages) & 1) &&
-               now_ns() - t0 < 1000000000ull) {
+      const uint32_t held = issued < kStages ? issued : kStages;
+      for (uint32_t at = issued - held; at < issued; ++at) {
+        while (!mbar_try(full + 8 * (at % kStages), at / kStages & 1) && now_ns() - t0 < 1000000000ull) {
         }
       }
     }
@@ -466,12 +459,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // ---- products.  The warp walks together; one lane issues.
     uint32_t s = 0, phase = 0, acc = 0, acc_phase = 1;
     bool ok = true;
-    for (int64_t index = first; ok && index < total; index += stride) {
-      const Tile t = tile_at<kPair>(p, starts, index);
-      const Entry& e = p.c.entries[t.entry];
-      const int ta = uniform(across_from<kPair>(side_of(e, t.which, 0), t.i * kTile));
-      const int tb = uniform(across_from<kPair>(side_of(e, t.which, 1), t.j * kTile));
-      const int depth = uniform(t.which == 0 ? e.l : e.k);
+    for (uint32_t n = 0; ok && n < mine; ++n) {
+      ok = __all_sync(0xffffffffu, shared_wait(told, n + 1, fault));
+      if (!ok) break;
+      const Tile& t = slots[n % kSlots];
+      const int ta = uniform(across_from<kPair>(side_of(t.e, t.which, 0), t.i * kTile));
+      const int tb = uniform(across_from<kPair>(side_of(t.e, t.which, 1), t.j * kTile));
+      const int depth = uniform(t.depth);
       ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * acc, acc_phase, fault));
       if (!ok) break;
       tc_fence_after();
@@ -485,12 +479,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elected()) {
+          const auto four = [&](int q0) {
 #pragma unroll
-          for (int q = 0; q < kDepth / 16; ++q) {
-            // 16 deep: 32 bytes along a row (four to a box), or 16 rows of 128 bytes
-            const uint32_t along = (q / 4 * kBoxBytes + q % 4 * 32) >> 4, down = q * 16 * 128 >> 4;
-            mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > 0 || q > 0);
-          }
+            for (int q = q0; q < q0 + 4; ++q) {
+              // 16 deep: 32 bytes along a row (four to a box), or 16 rows of 128 bytes
+              const uint32_t along = (q / 4 * kBoxBytes + q % 4 * 32) >> 4, down = q * 16 * 128 >> 4;
+              mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > 0 || q > 0);
+            }
+          };
+          four(0);
+          if (depth - k0 > 64) four(4);
           mma_commit<kPair>(empty + 8 * s);
           if (k0 + kDepth >= depth) mma_commit<kPair>(acc_full + 8 * acc);
         }
@@ -508,13 +506,31 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp >= 4) {
     // ---- epilogue
     uint32_t acc = 0, phase = 0;
-    float* patch = patches + (warp - 4) * 32 * (kPatchCols + 1);
-    for (int64_t index = first; index < total; index += stride) {
-      const Tile t = tile_at<kPair>(p, starts, index);
-      if (!epilogue<kPair>(p, t, tmem + acc * kTile, acc_full + 8 * acc, phase, acc_empty + 8 * acc,
-                           warp - 4, lane, rank, patch, cols))
-        break;
+    float* patch = patches + (warp - 4) * 512;
+    for (uint32_t n = 0; n < mine; ++n) {
+      // the tile before the last is counted: its barrier is free again
+      bool ok = shared_wait(told, n + 1, fault) && (n < 2 || shared_wait(counted, n - 1, fault));
+      ok = __all_sync(0xffffffffu, ok);
+      ok = epilogue<kPair>(p, slots[n % kSlots], ok, tmem + acc * kTile, acc_full + 8 * acc, phase,
+                           acc_empty + 8 * acc, warp - 4, lane, rank, patch, cols + acc * 256);
+      if (!ok) *stop = 1;
+      // the tile's writes are made: warp 2 counts it
+      asm volatile("barrier.arrive %0, %1;" ::"r"(2 + acc), "r"(32 * kEpiWarps + 32) : "memory");
+      if (!ok) break;
       if (++acc == 2) { acc = 0; phase ^= 1; }
+    }
+  } else if (warp == 2) {
+    // ---- count of finished tiles: waits for the epilogue's writes to be
+    // visible to the device, so that its warps need not
+    for (uint32_t n = 0; n < mine; ++n) {
+      asm volatile("barrier.sync %0, %1;" ::"r"(2 + n % 2), "r"(32 * kEpiWarps + 32) : "memory");
+      if (*stop) break;
+      if (lane == 0) {
+        const uint32_t unit = (uint32_t)slots[n % kSlots].unit;
+        shared_set(counted, n + 1);
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + unit) : "memory");
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();

@@ -59,9 +59,11 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
                : "memory");
 }
 
-// Arrive at a barrier of any CTA of the cluster (address from peer()).
+// Arrive at a barrier of any CTA of the cluster (address from peer()).  It
+// orders no memory but TMEM, by the fence before it: a release at the
+// cluster's scope would wait for all of the thread's writes.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
@@ -97,13 +99,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* fa
   }
 }
 
-// The same for a counter in global memory to reach `need`.
-__device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t need, int* fault) {
+// The same for a counter in global memory to reach `need`, and for one in this
+// CTA's shared memory.
+template <typename Load>
+__device__ __forceinline__ bool reach(Load load, uint32_t need, int* fault) {
   uint64_t t0 = 0;
   for (uint32_t n = 1;; ++n) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-    if (v >= need) return true;
+    if (load() >= need) return true;
     if (n % 64 == 0) {
       if (*(volatile int*)fault) return false;
       const uint64_t t = now_ns();
@@ -114,6 +116,23 @@ __device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t nee
       }
     }
   }
+}
+__device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t need, int* fault) {
+  return reach([=] {
+    uint32_t v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    return v;
+  }, need, fault);
+}
+__device__ __forceinline__ bool shared_wait(uint32_t counter, uint32_t need, int* fault) {
+  return reach([=] {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(counter) : "memory");
+    return v;
+  }, need, fault);
+}
+__device__ __forceinline__ void shared_set(uint32_t counter, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(counter), "r"(v) : "memory");
 }
 
 // Ordinary writes before it are seen by TMA reads that are ordered after it.
@@ -195,17 +214,14 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// 32 columns of the warp's 32 lanes of TMEM, a row a thread.
-__device__ __forceinline__ void tmem_load32(uint32_t addr, float* v) {
+// 16 columns of the warp's 32 lanes of TMEM, a row a thread.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
 __device__ __forceinline__ void tmem_load_wait() {
@@ -226,20 +242,6 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t box) {
 __device__ __forceinline__ uint32_t instruction(int m, int n, bool across_a, bool across_b) {
   return 1u << 4 | (uint32_t)across_a << 15 | (uint32_t)across_b << 16 | (uint32_t)(n >> 3) << 17 |
          (uint32_t)(m >> 4) << 24;
-}
-
-// ---- 32-byte accesses: a whole sector a thread
-
-__device__ __forceinline__ void load32(const void* p, uint32_t* v) {   // past L1
-  asm volatile("ld.relaxed.gpu.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-               : "l"(p)
-               : "memory");
-}
-__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
 }
 
 }  // namespace sm103
