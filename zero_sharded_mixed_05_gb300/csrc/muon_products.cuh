@@ -217,18 +217,19 @@ __device__ __forceinline__ void result(const Products& p, const Entry& e, const 
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// One tile's epilogue: the warp's 32 rows of the accumulator, half its columns,
-// 16 at a time.  Whatever it reads besides is fetched while the products
+// One tile's epilogue: the warp's 32 rows of the accumulator, every second 32 of
+// its columns, 16 at a time.  Whatever it reads besides is fetched while the products
 // still run: the diagonal's numbers of the tile's columns go to shared memory
 // (`cols`), and the next columns' numbers are on their way while those before
 // are worked on.  The loops are kept short: a small matrix runs each of them
 // once a tile, and straight code of 64 columns waited on instruction fetches
 // longer than it ran (64x64: 91 us).  False: a wait ran out.
 template <int kPair>
-__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool ready, uint32_t acc, uint32_t full_bar,
+__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool ready, uint32_t told, uint32_t number,
+                                         uint32_t acc, uint32_t full_bar,
                                          uint32_t phase, uint32_t empty_bar, int warp, int lane, uint32_t rank,
                                          float* patch, float* cols) {
-  constexpr int kTile = 128 * kPair, kCols = kTile / 2;
+  constexpr int kTile = 128 * kPair;
   const Entry& en = t.e;
   const int rows = en.rows, ncols = en.cols, k = en.k, tall = en.tall;
   const int64_t ldx = en.ldx, ldk = en.ldk;
@@ -237,21 +238,22 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   const int M = t.which == 2 ? rows : k, N = t.which == 2 ? ncols : k;
   const float ca = p.coef[t.step][0], cb = p.coef[t.step][1], cc = p.coef[t.step][2];
   const bool last = t.step == p.steps - 1;
-  const int col0 = t.j * kTile, mine = col0 + part * kCols;   // the warp's first column
+  const int col0 = t.j * kTile, ncol = row0 < M ? min(kTile, N - col0) : 0;
   float* diag = en.diag + t.b * ldk;
   // what a product reads and what only epilogues do
   __half* const to = t.which == 0 ? en.a + t.b * k * ldk
                      : t.which == 1 ? en.b + t.b * k * ldk : en.x[(t.step & 1) ^ 1] + t.b * rows * ldx;
   const int64_t ld = t.which == 2 ? ldx : ldk;
   uint4* const blk = reinterpret_cast<uint4*>(
-      t.which == 2 ? reinterpret_cast<char*>(en.x32 + t.b * block_size(rows, ldx) + block_at<float>(row, mine, ldx))
-                   : reinterpret_cast<char*>(en.a_blk + t.b * block_size(k, ldk) + block_at<__half>(row, mine, ldk)));
+      t.which == 2 ? reinterpret_cast<char*>(en.x32 + t.b * block_size(rows, ldx) + block_at<float>(row, col0, ldx))
+                   : reinterpret_cast<char*>(en.a_blk + t.b * block_size(k, ldk) + block_at<__half>(row, col0, ldk)));
 
   int ok = ready;
   float di = 0.0f;
   uint4 old[4];
-  const auto fetch = [&](int c) {             // 16 columns from the warp's c on
-    if (row0 >= M || c >= kCols || mine + c >= N) return;
+  const auto after = [](int c) { return c % 32 ? c + 48 : c + 16; };   // the warp's next 16 columns
+  const auto fetch = [&](int c) {
+    if (c >= ncol) return;
     if (t.which == 1) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) old[q] = __ldcg(blk + c * 4 + q * 32);
@@ -260,14 +262,17 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       for (int q = 0; q < 4; ++q) old[q] = __ldcg(blk + c * 8 + q * 32);
     }
   };
-  if (t.which != 0 && ok) {
-    fetch(0);
-    const int c = warp * 32 + lane;
-    float d = 0.0f;
-    if (c < kTile && col0 + c < N) d = __ldcg(diag + col0 + c);
-    if (row < M && (t.which == 1 || !tall)) di = __ldcg(diag + row);
-    // b A + c A A: c d_j; X: e_j of a tall matrix
-    if (c < kTile) cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
+  if (t.which != 0) {
+    ok = __all_sync(0xffffffffu, ok && shared_wait(told, number + 1, &p.c.ws->fault));
+    if (ok) {
+      fetch(part * 32);
+      const int c = warp * 32 + lane;
+      float d = 0.0f;
+      if (c < kTile && col0 + c < N) d = __ldcg(diag + col0 + c);
+      if (row < M && (t.which == 1 || !tall)) di = __ldcg(diag + row);
+      // b A + c A A: c d_j; X: e_j of a tall matrix
+      if (c < kTile) cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
+    }
   }
   if (lane == 0 && ok) ok = mbar_wait(full_bar, phase, &p.c.ws->fault);
   ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -281,24 +286,22 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   if (!ok) return false;
   tc_fence_after();
 
-  const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16) + part * kCols;
-  cols += part * kCols;
+  const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16);
   // the row's share of b A + c A A's factor, or e_i of a wide matrix
   const float ei = t.which == 1 ? __fmaf_rn(cc, di, cb) : __fmul_rn(di, __fmaf_rn(cc, di, cb));
-  const int ncol = row0 < M ? min(kCols, N - mine) : 0;        // columns of the warp's there are
   float next[16];
-  if (ncol > 0) tmem_load16(lanes, next);
+  if (part * 32 < ncol) tmem_load16(lanes + part * 32, next);
 #pragma unroll 1
-  for (int c = 0; c < ncol; c += 16) {
+  for (int c = part * 32; c < ncol; c = after(c)) {
     float v[16];
     tmem_load_wait();
 #pragma unroll
     for (int q = 0; q < 16; ++q) v[q] = next[q];
-    if (c + 16 < ncol) tmem_load16(lanes + c + 16, next);
+    if (after(c) < ncol) tmem_load16(lanes + after(c), next);
     float2* y = reinterpret_cast<float2*>(v);
     if (t.which == 0) {
-      const int at = row - (mine + c);         // the diagonal's place, if in these columns
-      if (row0 < mine + c + 16 && row0 + 32 > mine + c) {
+      const int at = row - (col0 + c);         // the diagonal's place, if in these columns
+      if (row0 < col0 + c + 16 && row0 + 32 > col0 + c) {
         float d = 0.0f;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -314,7 +317,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
-      fetch(c + 16);
+      fetch(after(c));
     } else {
       const float2* x = reinterpret_cast<const float2*>(old);
       const float2* d = reinterpret_cast<const float2*>(cols + c);
@@ -323,11 +326,11 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       for (int q = 0; q < 8; ++q)
         y[q] = __ffma2_rn(y[q], down,
                           __ffma2_rn(ca2, x[q], __fmul2_rn(tall ? d[q] : e2, unpack(pack(x[q].x, x[q].y)))));
-      fetch(c + 16);
+      fetch(after(c));
       if (last) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) *piece(patch, lane, q) = reinterpret_cast<const uint4*>(v)[q];
-        result(p, en, p.c.io[en.item], t.b, row0, mine + c, patch, lane);
+        result(p, en, p.c.io[en.item], t.b, row0, col0 + c, patch, lane);
         continue;
       }
 #pragma unroll
@@ -342,7 +345,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       if (t.which == 0) blk[c * 4 + q * 32] = h;
     }
     // 32 columns are whole, or end here (a row has room for 32)
-    if (c % 32 || c + 16 >= ncol) flush(patch, to, ld, row0, M, mine + c / 32 * 32, lane);
+    if (c % 32 || c + 16 >= ncol) flush(patch, to, ld, row0, M, col0 + c / 32 * 32, lane);
   }
   // the accumulator may be written again once both CTAs have read it
   tc_fence_before();
@@ -365,7 +368,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   Tile* slots = reinterpret_cast<Tile*>(small + 256);
   const uint32_t full = smem_u32(small), empty = full + 8 * kStages, acc_full = empty + 8 * kStages,
                  acc_empty = acc_full + 16, drain = acc_empty + 16, tmem_at = drain + 8,
-                 told = tmem_at + 4,       // tiles that are in the ring and whose needs are met
+                 known = tmem_at + 4,      // tiles that are in the ring
+                 told = known + 4,         // and whose needs are met
                  counted = told + 4;       // tiles whose writes the counting warp has seen
   volatile int* const stop = reinterpret_cast<volatile int*>(small + (counted - full) + 4);
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -382,6 +386,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(acc_empty + 8 * s, kPair * kEpiWarps);
     }
     mbar_init(drain, 1);
+    shared_set(known, 0);
     shared_set(told, 0);
     shared_set(counted, 0);
     *stop = 0;
@@ -406,20 +411,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       Tile& t = slots[n % kSlots];
       if (side == 0) {
         tile_at<kPair>(p, first + (int64_t)n * stride, lane, &t);
-        if (t.need) ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, t.need, fault));
-        if (!ok) break;
-        if (lane == 0) shared_set(told, n + 1);
+        if (lane == 0) shared_set(known, n + 1);
       } else {
-        ok = __all_sync(0xffffffffu, shared_wait(told, n + 1, fault));
+        ok = __all_sync(0xffffffffu, shared_wait(known, n + 1, fault));
         if (!ok) break;
       }
-      if (t.need) fence_proxy_async();
       const Side how = side_of(t.e, t.which, side), other = side_of(t.e, t.which, side ^ 1);
       const CUtensorMap* map = p.maps + 4 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
       const int m0 = (side ? t.j : t.i) * kTile, at = uniform(m0 + (int)rank * 128);
       const int turn = uniform(across_from<kPair>(how, m0));
       const int other_turn = uniform(across_from<kPair>(other, (side ? t.i : t.j) * kTile));
       const int depth = uniform(t.depth), b = uniform(t.b);
+      const uint32_t need = t.need;
+      // each waits for the device's count itself: a shared word between them
+      // would be one more step before the first load
+      if (need) {
+        ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, need, fault));
+        if (!ok) break;
+        fence_proxy_async();
+      }
       for (int k0 = 0; k0 < depth; k0 += kDepth) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
@@ -435,6 +445,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, (x ? at : k0) + 64, x ? k0 : at, b);
         }
         __syncwarp();
+        if (side == 0 && k0 == 0 && lane == 0) shared_set(told, n + 1);
         ++issued;
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
@@ -460,7 +471,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t s = 0, phase = 0, acc = 0, acc_phase = 1;
     bool ok = true;
     for (uint32_t n = 0; ok && n < mine; ++n) {
-      ok = __all_sync(0xffffffffu, shared_wait(told, n + 1, fault));
+      ok = __all_sync(0xffffffffu, shared_wait(known, n + 1, fault));
       if (!ok) break;
       const Tile& t = slots[n % kSlots];
       const int ta = uniform(across_from<kPair>(side_of(t.e, t.which, 0), t.i * kTile));
@@ -509,9 +520,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     float* patch = patches + (warp - 4) * 512;
     for (uint32_t n = 0; n < mine; ++n) {
       // the tile before the last is counted: its barrier is free again
-      bool ok = shared_wait(told, n + 1, fault) && (n < 2 || shared_wait(counted, n - 1, fault));
+      bool ok = shared_wait(known, n + 1, fault) && (n < 2 || shared_wait(counted, n - 1, fault));
       ok = __all_sync(0xffffffffu, ok);
-      ok = epilogue<kPair>(p, slots[n % kSlots], ok, tmem + acc * kTile, acc_full + 8 * acc, phase,
+      ok = epilogue<kPair>(p, slots[n % kSlots], ok, told, n, tmem + acc * kTile, acc_full + 8 * acc, phase,
                            acc_empty + 8 * acc, warp - 4, lane, rank, patch, cols + acc * 256);
       if (!ok) *stop = 1;
       // the tile's writes are made: warp 2 counts it
