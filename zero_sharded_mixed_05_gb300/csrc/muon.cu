@@ -36,6 +36,7 @@ struct zero_muon_handle {
   const zm::Group* group = nullptr;
   const zm::Stretch* stretch = nullptr;
   int64_t chunks = 0;               // CTAs of the first two stages
+  bool second = false;              // some matrix needs the second
   int pair = 2;                     // CTAs a tile of the products
   int grid = 0;                     // CTAs of the products
   int smem = 0;
@@ -75,10 +76,21 @@ struct Layout {
   }
 };
 
-zero_status launch(zero_muon_t h, const void* fn, int64_t grid, void** params, cudaStream_t s) {
-  const cudaError_t e =
-      cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(zm::kThreads), params, 0, s);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+// `early`: scheduled while the kernel before it still runs; it waits for that
+// kernel by itself.
+zero_status launch(zero_muon_t h, const void* fn, int64_t grid, void** params, cudaStream_t s,
+                   bool early = false) {
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid);
+  lc.blockDim = dim3(zm::kThreads);
+  lc.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelExC(&lc, fn, params);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
   ++h->launches;
   return ZERO_OK;
 }
@@ -112,9 +124,11 @@ zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t
   void* p[] = {&start};
   zero_status st = launch(h, (const void*)zm::muon_stats_kernel<T, N>, h->chunks, p, s);
   if (st != ZERO_OK) return st;
-  void* q[] = {&start.c};
-  st = launch(h, (const void*)zm::muon_start_kernel<T>, h->chunks, q, s);
-  if (st != ZERO_OK) return st;
+  if (h->second) {
+    void* q[] = {&start.c};
+    st = launch(h, (const void*)zm::muon_start_kernel<T>, h->chunks, q, s, true);
+    if (st != ZERO_OK) return st;
+  }
   zm::Products pr = {};
   pr.c = c;
   pr.maps = h->maps;
@@ -359,8 +373,8 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
       e.item = i;
       e.ldx = (s.cols + 31) / 32 * 32;
       e.ldk = (e.k + 31) / 32 * 32;
-      e.vpr = (int32_t)((s.cols + zm::kVec - 1) / zm::kVec);
-      e.chunks = (int32_t)(((int64_t)e.rows * e.vpr + zm::kChunk - 1) / zm::kChunk);
+      e.across = (int32_t)(e.ldx / 32);
+      e.chunks = (int32_t)(((s.rows + 31) / 32 * e.across + zm::kChunk - 1) / zm::kChunk);
       e.s = (float)(cfg->scale_rule == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt((double)e.l)
                     : cfg->scale_rule == ZERO_MUON_SCALE_ASPECT
                         ? std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols))
@@ -377,6 +391,7 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
       e.chunk0 = (int32_t)h->chunks;
       units += e.batch;
       h->chunks += (int64_t)e.chunks * e.batch;
+      h->second = h->second || e.chunks > 1;
       tiles += (e.rows / 128 + 1.0) * (e.cols / 128 + 1.0) * e.batch;
       if (units > INT32_MAX / 2 || h->chunks > INT32_MAX / 2 || tiles > INT32_MAX / 64) {
         delete h;

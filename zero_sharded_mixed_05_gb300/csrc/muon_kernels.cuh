@@ -21,8 +21,9 @@ namespace zm {
 
 constexpr int kThreads = 256;
 constexpr int kMaxEntries = ZERO_MUON_MAX_SHAPES;
-constexpr int kVec = 8;                        // numbers of a vector in the first two stages
-constexpr int kChunk = kThreads * 8;           // vectors of a CTA
+constexpr int kVec = 8;                        // numbers of a thread's vector in the first two stages
+constexpr int kPasses = 8;                     // vectors of a thread
+constexpr int kChunk = kThreads * kPasses * kVec / 1024;   // blocks of 32 x 32 numbers of a CTA
 
 // A and B are held times 4096 and X times 64, so that a product of X by itself
 // has A's scale (zero_muon.h).
@@ -39,7 +40,7 @@ struct Entry {
   float* diag;               // [batch][ldk]: A's diagonal
   int32_t unit0;             // first matrix of the entry among all
   int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
-  int32_t vpr;               // vectors a row
+  int32_t across;            // blocks of 32 columns
   int32_t item;              // the caller's index
   float s;                   // scale_rule's factor
 };
@@ -112,16 +113,31 @@ __device__ __forceinline__ float grad_factor(const Call& c) {
   return c.decision ? __fmul_rn(c.grad_scale, c.decision->coef) : c.grad_scale;
 }
 
-// The entry whose CTAs of the first two stages include this one.
-__device__ __forceinline__ int entry_of_chunk(const Call& c) {
+// What a CTA of the first two stages works on.  A warp's pass is 8 rows of a
+// block of 32 x 32: four threads a row, so that a row's 32 numbers are whole
+// sectors in every array, and so are the block's pieces of 8 rows.
+struct Part {
+  int entry, b, chunk;       // matrix b of the entry, CTA `chunk` of the matrix
+};
+__device__ __forceinline__ Part part_of(const Call& c, int cta) {
   __shared__ int found;
   for (int i = threadIdx.x; i < c.n; i += kThreads) {
     const Entry& e = c.entries[i];
-    const int at = (int)blockIdx.x - e.chunk0;
+    const int at = cta - e.chunk0;
     if (at >= 0 && at < e.chunks * e.batch) found = i;
   }
   __syncthreads();
-  return found;
+  const Entry& e = c.entries[found];
+  const int at = cta - e.chunk0;
+  return {found, at / e.chunks, at % e.chunks};
+}
+// Row and first column of a thread's vector of a pass; false: not in the matrix.
+__device__ __forceinline__ bool place(const Entry& e, int chunk, int pass, int* row, int* col) {
+  const int64_t blk = (int64_t)chunk * kChunk + pass / 4 * (kThreads / 32) + threadIdx.x / 32;
+  const int down = (int)(blk / e.across), right = (int)(blk - (int64_t)down * e.across);
+  *row = down * 32 + pass % 4 * 8 + threadIdx.x % 32 / 4;
+  *col = right * 32 + threadIdx.x % 4 * kVec;
+  return *row < e.rows && *col < e.cols;
 }
 
 // Eight numbers of a row (fewer at its end, the rest zero) from p.
@@ -172,9 +188,28 @@ __device__ __forceinline__ void update_of(const Call& c, float f, const float* g
   }
 }
 
+// Writes a vector of X: rounded for the products, and in binary32.
+__device__ __forceinline__ void put_x(const Entry& e, int b, int row, int col, const float* u, float inv) {
+  __align__(16) __half h[kVec];
+  float y[kVec];
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) {
+    y[j] = __fmul_rn(__fmul_rn(u[j], inv), kScaleX);
+    h[j] = __float2half_rn(y[j]);
+  }
+  // rows of the workspace are multiples of 32 numbers: the vector fits
+  *reinterpret_cast<uint4*>(e.x[0] + ((int64_t)b * e.rows + row) * e.ldx + col) = *reinterpret_cast<const uint4*>(h);
+  float* blk = e.x32 + (int64_t)b * block_size(e.rows, e.ldx) + block_at<float>(row, col, e.ldx);
+  *reinterpret_cast<float4*>(blk) = make_float4(y[0], y[1], y[2], y[3]);
+  *reinterpret_cast<float4*>(blk + 128) = make_float4(y[4], y[5], y[6], y[7]);
+}
+
+__device__ __forceinline__ float inverse(double squares, double eps) { return (float)(1.0 / (sqrt(squares) + eps)); }
+
 // Stage 1.  Bound by memory: the step reads 2 + 4 bytes a number and writes 4.
 // Squares are added in binary32 within a thread's 64 numbers and in binary64
-// beyond; the last CTA of a matrix adds the CTAs' sums in index order.
+// beyond; the last CTA of a matrix adds the CTAs' sums in index order.  Of a
+// matrix that one CTA holds the numbers are still there: it writes X at once.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_constant__ Start<N> s) {
   const Call& c = s.c;
@@ -187,23 +222,22 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
   if (skipped(c)) return;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < c.n; i += kThreads) c.io[i] = s.io[i];
-  const int ei = entry_of_chunk(c);
-  const Entry& e = c.entries[ei];
+  const Part part = part_of(c, blockIdx.x);
+  const Entry& e = c.entries[part.entry];
   const Io& io = s.io[e.item];
-  const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
-  const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
+  const int b = part.b;
   const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
   float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
   const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
   const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
   const float f = grad_factor(c);
+  const bool alone = e.chunks == 1;
   float sq = 0.0f;
 #pragma unroll 4
-  for (int i = 0; i < kChunk / kThreads; ++i) {
-    const uint32_t v = (uint32_t)chunk * kChunk + i * kThreads + threadIdx.x;
-    if (v >= vecs) break;
-    const uint32_t row = v / (uint32_t)e.vpr, col = (v - row * e.vpr) * kVec;
-    const int n = min(kVec, e.cols - (int)col);
+  for (int i = 0; i < kPasses; ++i) {
+    int row, col;
+    if (!place(e, part.chunk, i, &row, &col)) continue;
+    const int n = min(kVec, e.cols - col);
     float x[kVec], u[kVec];
     load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
     if (c.step) {
@@ -224,10 +258,34 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
   __syncthreads();
   const int unit = e.unit0 + b;
-  double* part = c.part + e.chunk0 + (int64_t)b * e.chunks;
+  if (alone) {
+    d = 0.0;
+    for (int i = 0; i < kThreads / 32; ++i) d += red[i];
+    const float inv = inverse(d, c.eps);
+    if (threadIdx.x == 0) c.done[unit] = 0u;
+#pragma unroll 2
+    for (int i = 0; i < kPasses; ++i) {      // again from L1 or L2
+      int row, col;
+      if (!place(e, 0, i, &row, &col)) continue;
+      const int n = min(kVec, e.cols - col);
+      float x[kVec], u[kVec];
+      load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
+      if (c.step) {
+        float m[kVec];
+        load8<float>(mom + (int64_t)row * e.cols + col, n, vmom, m);
+        update_of<false>(c, f, x, m, u);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) u[j] = x[j];
+      }
+      put_x(e, b, row, col, u, inv);
+    }
+    return;
+  }
+  double* sums = c.part + e.chunk0 + (int64_t)b * e.chunks;
   if (threadIdx.x == 0) {
     for (int i = 1; i < kThreads / 32; ++i) d += red[i];
-    part[chunk] = d;
+    sums[part.chunk] = d;
     __threadfence();
     last = atomicAdd(&c.ticket[unit], 1u) == (unsigned)e.chunks - 1;
   }
@@ -235,41 +293,41 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
   if (!last) return;
   __threadfence();
   d = 0.0;
-  for (int i = threadIdx.x; i < e.chunks; i += kThreads) d += __ldcg(&part[i]);
+  for (int i = threadIdx.x; i < e.chunks; i += kThreads) d += __ldcg(&sums[i]);
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   __syncthreads();
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < kThreads / 32; ++i) d += red[i];
-    c.inv[unit] = (float)(1.0 / (sqrt(d) + c.eps));
+    c.inv[unit] = inverse(d, c.eps);
     c.ticket[unit] = 0u;
     c.done[unit] = 0u;
   }
 }
 
-// Stage 2.  Reads U's sources again (from L2 where they fit) and writes X.
+// Stage 2.  Reads U's sources again and writes X.  From the last CTA's numbers
+// to the first's: stage 1 ended with the last, which L2 still holds, and the
+// products begin with the first.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ Call c) {
+  cudaGridDependencySynchronize();           // launched while stage 1 still runs
   if (skipped(c)) return;
-  const int ei = entry_of_chunk(c);
-  const Entry& e = c.entries[ei];
+  const Part part = part_of(c, gridDim.x - 1 - blockIdx.x);
+  const Entry& e = c.entries[part.entry];
+  if (e.chunks == 1) return;                 // stage 1 wrote it
   const Io& io = c.io[e.item];
-  const int at = (int)blockIdx.x - e.chunk0, b = at / e.chunks, chunk = at % e.chunks;
-  const uint32_t vecs = (uint32_t)e.rows * (uint32_t)e.vpr;
+  const int b = part.b;
   const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
   const float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
   const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
   const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
   const float f = grad_factor(c), inv = c.inv[e.unit0 + b];
-  const int64_t base = (int64_t)b * e.rows * e.ldx;
-  float* x32 = e.x32 + (int64_t)b * block_size(e.rows, e.ldx);
 #pragma unroll 4
-  for (int i = 0; i < kChunk / kThreads; ++i) {
-    const uint32_t v = (uint32_t)chunk * kChunk + i * kThreads + threadIdx.x;
-    if (v >= vecs) break;
-    const uint32_t row = v / (uint32_t)e.vpr, col = (v - row * e.vpr) * kVec;
-    const int n = min(kVec, e.cols - (int)col);
+  for (int i = 0; i < kPasses; ++i) {
+    int row, col;
+    if (!place(e, part.chunk, i, &row, &col)) continue;
+    const int n = min(kVec, e.cols - col);
     float x[kVec], u[kVec];
     load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
     if (c.step) {
@@ -280,17 +338,7 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
 #pragma unroll
       for (int j = 0; j < kVec; ++j) u[j] = x[j];
     }
-    __align__(16) __half h[kVec];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      u[j] = __fmul_rn(__fmul_rn(u[j], inv), kScaleX);
-      h[j] = __float2half_rn(u[j]);
-    }
-    // rows of the workspace are multiples of 32 numbers: the vector fits
-    *reinterpret_cast<uint4*>(e.x[0] + base + (int64_t)row * e.ldx + col) = *reinterpret_cast<const uint4*>(h);
-    float* blk = x32 + block_at<float>(row, col, e.ldx);
-    *reinterpret_cast<float4*>(blk) = make_float4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<float4*>(blk + 128) = make_float4(u[4], u[5], u[6], u[7]);
+    put_x(e, b, row, col, u, inv);
   }
 }
 
