@@ -28,10 +28,10 @@
  * b A + c A A are held times 4096, X times 64, which keeps them in
  * binary16's normal range for entries from 1.5e-8 (X: 1e-6) to 16 (a
  * coefficient set that takes singular values well beyond one, so that A or
- * b A + c A A pass 16, overflows to infinity and NaN).  X is kept in binary32 as
- * well: only the products take its rounding, not the term a X, so that the
- * many directions in which a gradient is small or zero are not filled with
- * rounding noise that p would blow up.  O is within about
+ * b A + c A A pass 16, overflows to infinity and NaN).  X is held as the sum of
+ * two binary16 numbers, of which the products take the first and the term a X
+ * both, so that the many directions in which a gradient is small or zero are
+ * not filled with rounding noise that p would blow up.  O is within about
  * 2e-3 (Frobenius, relative) of the definition in 64 bits.  Norms are summed
  * in binary32 and binary64 (numbers whose squares leave binary32's range,
  * beyond about 1e19 or below 1e-19, are outside what the norm can tell), M
@@ -117,7 +117,7 @@ typedef struct zero_muon_info {
 zero_status zero_muon_config_default(zero_muon_config* cfg);
 
 /* Make a handle for n shapes (n = 0..ZERO_MUON_MAX_SHAPES) and its workspace:
- * about 8 bytes per element of the matrices and 6 per element of the k x k
+ * about 6 bytes per element of the matrices and 4 per element of the k x k
  * products.  Errors: EINVAL (NULL pointers, a field outside its range),
  * ERANGE (n or a shape beyond the limits above), ENOMEM, ECUDA.  *out is NULL
  * on failure.  Without a CUDA device the handle is created and every

@@ -33,15 +33,13 @@ struct zero_muon_handle {
   int64_t bytes = 0;
   zm::Call call = {};               // the fields that no call changes
   const CUtensorMap* maps = nullptr;
-  const zm::Group* group = nullptr;
-  const zm::Stretch* stretch = nullptr;
+  const int32_t* starts = nullptr;
   int64_t chunks = 0;               // CTAs of the first two stages
   bool second = false;              // some matrix needs the second
   int pair = 2;                     // CTAs a tile of the products
   int grid = 0;                     // CTAs of the products
   int smem = 0;
-  int64_t tiles = 0;                // of all products
-  int32_t groups = 0;
+  int32_t triangles = 0, fulls = 0; // tiles of a product of the first two kinds, of the third
   int64_t launches = 0;
 };
 
@@ -132,10 +130,10 @@ zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t
   zm::Products pr = {};
   pr.c = c;
   pr.maps = h->maps;
-  pr.group = h->group;
-  pr.stretch = h->stretch;
-  pr.tiles = h->tiles;
-  pr.groups = h->groups;
+  pr.starts = h->starts;
+  pr.triangles = h->triangles;
+  pr.fulls = h->fulls;
+  pr.tiles = (2ll * h->triangles + h->fulls) * h->cfg.steps;
   pr.steps = h->cfg.steps;
   for (int i = 0; i < pr.steps; ++i)
     for (int j = 0; j < 3; ++j) pr.coef[i][j] = (float)h->cfg.coef[i][j];
@@ -175,57 +173,16 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                 CUtensorMapFloatOOBfill);
 
-// Map of a [batch][rows][cols] array of binary16 numbers read in boxes of
-// 128 x 64; what lies outside of it reads as zero.
-bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t cols, int64_t rows, int64_t batch,
-            int64_t ld) {
-  const cuuint64_t dim[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
-  const cuuint64_t stride[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
-  const cuuint32_t box[3] = {64, 128, 1}, step[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dim, stride, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+// Map of a matrix in blocks (muon_kernels.cuh), [batch] of them: runs of 32
+// rows of a piece, rows of blocks, pieces across, matrices.  A box is 128 rows
+// of eight pieces; what lies outside reads as zero.
+bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t rows, int64_t ld, int64_t batch) {
+  const cuuint64_t dim[4] = {256, (cuuint64_t)(rows + 31) / 32, (cuuint64_t)ld / 8, (cuuint64_t)batch};
+  const cuuint64_t stride[3] = {(cuuint64_t)ld * 64, 512, (cuuint64_t)zm::block_size(rows, ld) * 2};
+  const cuuint32_t box[4] = {256, 4, 8, 1}, step[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, p, dim, stride, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Cuts the matrices into groups that go through all their products one after
-// another.  A group takes matrices until their working set (X in binary32 and
-// twice in binary16, A three times) passes kGroupBytes, so that it stays in L2
-// between products, and until their tiles fill the device several times over,
-// so that the end of each product costs little.
-constexpr int64_t kGroupBytes = 64 << 20;
-constexpr int kGroupWaves = 4;
-
-void make_groups(zero_muon_t h, int clusters, std::vector<zm::Group>* groups, std::vector<zm::Stretch>* stretches) {
-  const int tile = 128 * h->pair;
-  zm::Group g = {};
-  int64_t bytes = 0, tiles = 0;
-  const auto close = [&] {
-    if (g.stretches == 0) return;
-    groups->push_back(g);
-    tiles += (int64_t)(2 * g.triangles + g.fulls) * h->cfg.steps;
-    g = {};
-    g.first = tiles;
-    g.stretch0 = (int32_t)stretches->size();
-    bytes = 0;
-  };
-  for (size_t i = 0; i < h->entries.size(); ++i) {
-    const zm::Entry& e = h->entries[i];
-    const int32_t nk = (e.k + tile - 1) / tile, nr = (e.rows + tile - 1) / tile, nc = (e.cols + tile - 1) / tile;
-    const int64_t each = (int64_t)e.rows * e.ldx * 8 + (int64_t)e.k * e.ldk * 6;
-    for (int32_t b = 0; b < e.batch; ++b) {
-      if (b == 0 || g.stretches == 0) {
-        stretches->push_back({(int32_t)i, b, g.triangles, g.fulls});
-        ++g.stretches;
-      }
-      g.triangles += nk * (nk + 1) / 2;
-      g.fulls += nr * nc;
-      bytes += each;
-      if (bytes >= kGroupBytes && g.triangles >= kGroupWaves * clusters) close();
-    }
-  }
-  close();
-  h->tiles = tiles;
-  h->groups = (int32_t)groups->size();
 }
 
 // Allocates the workspace, fills in the addresses and readies the products.
@@ -244,25 +201,28 @@ cudaError_t place(zero_muon_t h) {
   int clusters = 0;
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc);
   if (e != cudaSuccess) return e;
-  clusters = std::max(clusters, 1);
-  std::vector<zm::Group> groups;
-  std::vector<zm::Stretch> stretches;
-  make_groups(h, clusters, &groups, &stretches);
-  int64_t most = 1;
-  for (const zm::Group& g : groups) most = std::max<int64_t>(most, std::max(g.triangles, g.fulls));
-  h->grid = h->pair * (int)std::min<int64_t>(clusters, most);
+  const int tile = 128 * h->pair;
+  std::vector<int32_t> starts;
+  for (const zm::Entry& en : h->entries) {
+    const int32_t nk = (en.k + tile - 1) / tile;
+    starts.push_back(h->triangles);
+    h->triangles += en.batch * (nk * (nk + 1) / 2);
+  }
+  for (const zm::Entry& en : h->entries) {
+    starts.push_back(h->fulls);
+    h->fulls += en.batch * ((en.rows + tile - 1) / tile) * ((en.cols + tile - 1) / tile);
+  }
+  h->grid = h->pair * std::min(std::max(clusters, 1), std::max(1, std::max(h->triangles, h->fulls)));
   const int64_t ws = lay.take(sizeof(zm::Workspace)), table = lay.take(n * sizeof(zm::Entry));
   const int64_t maps = lay.take(4 * n * sizeof(CUtensorMap));
-  const int64_t io = lay.take(n * sizeof(zm::Io)), group = lay.take(groups.size() * sizeof(zm::Group)),
-                stretch = lay.take(stretches.size() * sizeof(zm::Stretch));
+  const int64_t io = lay.take(n * sizeof(zm::Io)), first = lay.take(starts.size() * sizeof(int32_t));
   const int64_t part = lay.take(h->chunks * sizeof(double)), ticket = lay.take(units * 4),
                 inv = lay.take(units * 4), done = lay.take(units * 4);
   const int64_t cleared = lay.size;
   std::vector<int64_t> at;
   for (const zm::Entry& e : h->entries) {
-    const int64_t x = e.batch * (int64_t)e.rows * e.ldx * 2, a = e.batch * (int64_t)e.k * e.ldk * 2;
-    const int64_t x32 = e.batch * zm::block_size(e.rows, e.ldx) * 4, blk = e.batch * zm::block_size(e.k, e.ldk) * 2;
-    for (int64_t bytes : {x, x, x32, a, a, blk, e.batch * e.ldk * 4}) at.push_back(lay.take(bytes));
+    const int64_t x = e.batch * zm::block_size(e.rows, e.ldx) * 2, a = e.batch * zm::block_size(e.k, e.ldk) * 2;
+    for (int64_t bytes : {x, x, x, a, a, e.batch * e.ldk * 4}) at.push_back(lay.take(bytes));
   }
   h->bytes = lay.size;
   std::vector<CUtensorMap> map(4 * n);
@@ -276,19 +236,17 @@ cudaError_t place(zero_muon_t h) {
   const EncodeTiled fn = reinterpret_cast<EncodeTiled>(sym);
   for (int64_t i = 0; i < n; ++i) {
     zm::Entry& en = h->entries[i];
-    const auto half = [&](int j) { return reinterpret_cast<__half*>(h->mem + at[7 * i + j]); };
+    const auto half = [&](int j) { return reinterpret_cast<__half*>(h->mem + at[6 * i + j]); };
     en.x[0] = half(0);
     en.x[1] = half(1);
-    en.x32 = reinterpret_cast<float*>(half(2));
+    en.lo = half(2);
     en.a = half(3);
     en.b = half(4);
-    en.a_blk = half(5);
-    en.diag = reinterpret_cast<float*>(half(6));
+    en.diag = reinterpret_cast<float*>(half(5));
     CUtensorMap* m = &map[4 * i];
-    const bool ok = encode(fn, m, en.x[0], en.cols, en.rows, en.batch, en.ldx) &&
-                    encode(fn, m + 1, en.x[1], en.cols, en.rows, en.batch, en.ldx) &&
-                    encode(fn, m + 2, en.a, en.k, en.k, en.batch, en.ldk) &&
-                    encode(fn, m + 3, en.b, en.k, en.k, en.batch, en.ldk);
+    const bool ok = encode(fn, m, en.x[0], en.rows, en.ldx, en.batch) &&
+                    encode(fn, m + 1, en.x[1], en.rows, en.ldx, en.batch) &&
+                    encode(fn, m + 2, en.a, en.k, en.ldk, en.batch) && encode(fn, m + 3, en.b, en.k, en.ldk, en.batch);
     if (!ok) return cudaErrorInvalidValue;
   }
   e = cudaMemset(h->mem, 0, (size_t)cleared);
@@ -298,8 +256,7 @@ cudaError_t place(zero_muon_t h) {
   };
   copy(table, h->entries.data(), n * sizeof(zm::Entry));
   copy(maps, map.data(), map.size() * sizeof(CUtensorMap));
-  copy(group, groups.data(), groups.size() * sizeof(zm::Group));
-  copy(stretch, stretches.data(), stretches.size() * sizeof(zm::Stretch));
+  copy(first, starts.data(), starts.size() * sizeof(int32_t));
   if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   h->call.ws = reinterpret_cast<zm::Workspace*>(h->mem + ws);
   h->call.entries = reinterpret_cast<const zm::Entry*>(h->mem + table);
@@ -309,8 +266,7 @@ cudaError_t place(zero_muon_t h) {
   h->call.inv = reinterpret_cast<float*>(h->mem + inv);
   h->call.done = reinterpret_cast<uint32_t*>(h->mem + done);
   h->maps = reinterpret_cast<const CUtensorMap*>(h->mem + maps);
-  h->group = reinterpret_cast<const zm::Group*>(h->mem + group);
-  h->stretch = reinterpret_cast<const zm::Stretch*>(h->mem + stretch);
+  h->starts = reinterpret_cast<const int32_t*>(h->mem + first);
   return e;
 }
 

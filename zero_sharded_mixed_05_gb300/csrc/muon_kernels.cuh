@@ -3,8 +3,8 @@
 // A call is three stages:
 //   muon_stats_kernel   reads the input (for the step: gradient and momentum,
 //                       and writes the new momentum) and finds |U|_F
-//   muon_start_kernel   writes X = U / (|U|_F + eps) into the workspace, in
-//                       binary16 for the products and in binary32
+//   muon_start_kernel   writes X = U / (|U|_F + eps), held as the sum of two
+//                       binary16 numbers, into the workspace
 //   muon_products_kernel steps times  A = X X^T,  B = b A + c A A,  X <- a X + B X,
 //                       the last with the result's epilogue (muon_products.cuh)
 // The workspace holds every matrix in the orientation it came in: for a wide
@@ -28,15 +28,17 @@ constexpr int kChunk = kThreads * kPasses * kVec / 1024;   // blocks of 32 x 32 
 // A and B are held times 4096 and X times 64, so that a product of X by itself
 // has A's scale (zero_muon.h).
 constexpr float kScale = 4096.0f, kScaleX = 64.0f;
+// The second part of X is held times 2^11 more, so that it is a normal number
+// wherever the first is.
+constexpr float kLoScale = 2048.0f;
 
 struct Entry {
   int32_t rows, cols, batch, k, l, tall;
-  int64_t ldx, ldk;          // elements from row to row of x and of a/b
-  __half* x[2];              // [batch][rows][ldx], read and written in turn
-  float* x32;                // the same numbers in binary32, in blocks
-  __half* a;                 // [batch][k][ldk]
+  int64_t ldx, ldk;          // columns of x and lo, and of a and b, to a multiple of 32
+  __half* x[2];              // [batch] blocks of X's first part, read and written in turn
+  __half* lo;                // and of its second
+  __half* a;                 // [batch] blocks of A and of b A + c A A
   __half* b;
-  __half* a_blk;             // a in blocks
   float* diag;               // [batch][ldk]: A's diagonal
   int32_t unit0;             // first matrix of the entry among all
   int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
@@ -45,17 +47,16 @@ struct Entry {
   float s;                   // scale_rule's factor
 };
 
-// Blocks of 32 x 32 numbers, for what only an epilogue reads and writes, where
-// a thread holds a row: 16-byte pieces of the 32 rows lie side by side, so
-// that a warp's access is whole lines (a row-major access by rows touches a
-// line a thread and was what bound the epilogue).  The place of the piece
-// with columns col.. of a row, in an array with `ld` columns (a multiple of
-// 32), counted from the matrix's first number.
-template <typename T>
-__device__ __forceinline__ int64_t block_at(int row, int col, int64_t ld) {
-  constexpr int kPiece = 16 / sizeof(T);
-  return ((int64_t)(row / 32) * (ld / 32) + col / 32) * 1024 + (col % 32) / kPiece * (32 * kPiece) +
-         row % 32 * kPiece;
+// Every matrix of the workspace is in blocks of 32 x 32 binary16 numbers: eight
+// columns of a row are a piece of 16 bytes, the pieces of the block's 32 rows
+// lie side by side, then the next eight columns'.  One layout serves all: an
+// epilogue thread that holds a row reads and writes whole lines together with
+// its warp (by rows of a row-major array it would touch a line a thread); eight
+// pieces are the tensor core's 8 x 16-byte core matrix, for the depth along
+// the rows as well as down them; and TMA brings 512 bytes a run.  What pads a
+// matrix to whole blocks is zero.
+__host__ __device__ inline int64_t block_at(int row, int col, int64_t ld) {
+  return (row / 32 * (ld / 32) + col / 32) * 1024 + col % 32 / 8 * 256 + row % 32 * 8;
 }
 __host__ __device__ inline int64_t block_size(int64_t rows, int64_t ld) { return (rows + 31) / 32 * 32 * ld; }
 
@@ -131,13 +132,13 @@ __device__ __forceinline__ Part part_of(const Call& c, int cta) {
   const int at = cta - e.chunk0;
   return {found, at / e.chunks, at % e.chunks};
 }
-// Row and first column of a thread's vector of a pass; false: not in the matrix.
+// Row and first column of a thread's vector of a pass; false: not in the blocks.
 __device__ __forceinline__ bool place(const Entry& e, int chunk, int pass, int* row, int* col) {
   const int64_t blk = (int64_t)chunk * kChunk + pass / 4 * (kThreads / 32) + threadIdx.x / 32;
   const int down = (int)(blk / e.across), right = (int)(blk - (int64_t)down * e.across);
   *row = down * 32 + pass % 4 * 8 + threadIdx.x % 32 / 4;
   *col = right * 32 + threadIdx.x % 4 * kVec;
-  return *row < e.rows && *col < e.cols;
+  return down * 32 < e.rows;
 }
 
 // Eight numbers of a row (fewer at its end, the rest zero) from p.
@@ -188,20 +189,23 @@ __device__ __forceinline__ void update_of(const Call& c, float f, const float* g
   }
 }
 
-// Writes a vector of X: rounded for the products, and in binary32.
+// x as the sum of two binary16 numbers, the second times kLoScale.
+__device__ __forceinline__ void split(float2 x, __half2* hi, __half2* lo) {
+  *hi = __float22half2_rn(x);
+  const float2 h = __half22float2(*hi);
+  *lo = __floats2half2_rn(__fmul_rn(__fadd_rn(x.x, -h.x), kLoScale), __fmul_rn(__fadd_rn(x.y, -h.y), kLoScale));
+}
+
+// Writes a vector of X.
 __device__ __forceinline__ void put_x(const Entry& e, int b, int row, int col, const float* u, float inv) {
-  __align__(16) __half h[kVec];
-  float y[kVec];
+  __align__(16) __half2 hi[kVec / 2], lo[kVec / 2];
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    y[j] = __fmul_rn(__fmul_rn(u[j], inv), kScaleX);
-    h[j] = __float2half_rn(y[j]);
-  }
-  // rows of the workspace are multiples of 32 numbers: the vector fits
-  *reinterpret_cast<uint4*>(e.x[0] + ((int64_t)b * e.rows + row) * e.ldx + col) = *reinterpret_cast<const uint4*>(h);
-  float* blk = e.x32 + (int64_t)b * block_size(e.rows, e.ldx) + block_at<float>(row, col, e.ldx);
-  *reinterpret_cast<float4*>(blk) = make_float4(y[0], y[1], y[2], y[3]);
-  *reinterpret_cast<float4*>(blk + 128) = make_float4(y[4], y[5], y[6], y[7]);
+  for (int j = 0; j < kVec / 2; ++j)
+    split(make_float2(__fmul_rn(__fmul_rn(u[2 * j], inv), kScaleX), __fmul_rn(__fmul_rn(u[2 * j + 1], inv), kScaleX)),
+          &hi[j], &lo[j]);
+  const int64_t at = (int64_t)b * block_size(e.rows, e.ldx) + block_at(row, col, e.ldx);
+  *reinterpret_cast<uint4*>(e.x[0] + at) = *reinterpret_cast<const uint4*>(hi);
+  *reinterpret_cast<uint4*>(e.lo + at) = *reinterpret_cast<const uint4*>(lo);
 }
 
 __device__ __forceinline__ float inverse(double squares, double eps) { return (float)(1.0 / (sqrt(squares) + eps)); }
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
   for (int i = 0; i < kPasses; ++i) {
     int row, col;
     if (!place(e, part.chunk, i, &row, &col)) continue;
-    const int n = min(kVec, e.cols - col);
+    const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
     float x[kVec], u[kVec];
     load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
     if (c.step) {
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     for (int i = 0; i < kPasses; ++i) {      // again from L1 or L2
       int row, col;
       if (!place(e, 0, i, &row, &col)) continue;
-      const int n = min(kVec, e.cols - col);
+      const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
       float x[kVec], u[kVec];
       load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
       if (c.step) {
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_const
   for (int i = 0; i < kPasses; ++i) {
     int row, col;
     if (!place(e, part.chunk, i, &row, &col)) continue;
-    const int n = min(kVec, e.cols - col);
+    const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
     float x[kVec], u[kVec];
     load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
     if (c.step) {

@@ -43,7 +43,8 @@ using namespace sm103;
 
 constexpr int kStages = 3;
 constexpr int kDepth = 128;                        // of a stage
-constexpr int kBoxBytes = 128 * 64 * 2;
+constexpr int kBoxBytes = 128 * 64 * 2;            // 128 rows of eight pieces of eight columns
+constexpr int kPieceBytes = 128 * 16;              // in shared memory: a piece's 128 rows side by side
 constexpr int kOperandBytes = 2 * kBoxBytes;       // a CTA's 128 rows (or columns) of it
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kEpiWarps = 8;
@@ -56,24 +57,11 @@ constexpr int kSlots = 16;                         // tiles a CTA has in work: 3
 struct Products {
   Call c;
   const CUtensorMap* maps;   // four an entry: x[0], x[1], a, b
-  const struct Group* group;
-  const struct Stretch* stretch;
-  int64_t tiles;             // of all groups
-  int32_t groups, steps;
+  const int32_t* starts;     // [2][n]: first tile of each entry in a product of the first two kinds, in the third
+  int64_t tiles;             // of all products
+  int32_t triangles, fulls;  // of a product of the first two kinds, of the third
+  int32_t steps;
   float coef[ZERO_MUON_MAX_STEPS][3];
-};
-
-// A stretch of matrices of one entry.  The tiles go out group by group, a group
-// being stretches whose working set stays in L2 through all their products
-// (one after another; see muon.cu), and within a group product by product.
-struct Stretch {
-  int32_t entry, b0;                 // matrices b0.. of the entry
-  int32_t triangles, fulls;          // tiles of the group's stretches before this one
-};
-struct Group {
-  int64_t first;                     // tiles of the groups before
-  int32_t stretch0, stretches;
-  int32_t triangles, fulls;          // tiles of a product of the first two kinds, and of the third
 };
 
 struct Tile {
@@ -87,27 +75,19 @@ constexpr int kProductSmem = kStages * kStageBytes + kPatchBytes + kDiagBytes + 
 template <int kPair>
 __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int lane, Tile* out) {
   constexpr int kTile = 128 * kPair;
-  int lo = 0, hi = p.groups;               // the last group that starts at or before it
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.group[mid].first <= index) lo = mid; else hi = mid;
-  }
-  const Group g = p.group[lo];
-  index -= g.first;
-  const int per = 2 * g.triangles + g.fulls;
+  const int per = 2 * p.triangles + p.fulls;
   const int step = (int)(index / per);
   int r = (int)(index - (int64_t)step * per);
-  const int which = r < g.triangles ? 0 : r < 2 * g.triangles ? 1 : 2;
-  r -= which * g.triangles;
-  const Stretch* s = p.stretch + g.stretch0;
-  lo = 0, hi = g.stretches;
+  const int which = r < p.triangles ? 0 : r < 2 * p.triangles ? 1 : 2;
+  r -= which * p.triangles;
+  const int32_t* at = p.starts + (which == 2 ? p.c.n : 0);
+  int lo = 0, hi = p.c.n;                  // the last entry that starts at or before r
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if ((which == 2 ? s[mid].fulls : s[mid].triangles) <= r) lo = mid; else hi = mid;
+    if (at[mid] <= r) lo = mid; else hi = mid;
   }
-  const Stretch st = s[lo];
-  r -= which == 2 ? st.fulls : st.triangles;
-  const Entry& from = p.c.entries[st.entry];
+  r -= at[lo];
+  const Entry& from = p.c.entries[lo];
   static_assert(sizeof(Entry) % 4 == 0 && sizeof(Entry) / 4 <= 64, "copied by one warp");
   for (int w = lane; w < (int)sizeof(Entry) / 4; w += 32)
     reinterpret_cast<uint32_t*>(&out->e)[w] = reinterpret_cast<const uint32_t*>(&from)[w];
@@ -116,7 +96,7 @@ __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int la
   const int nk = (e.k + kTile - 1) / kTile, nr = (e.rows + kTile - 1) / kTile, nc = (e.cols + kTile - 1) / kTile;
   const int ntri = nk * (nk + 1) / 2, nfull = nr * nc;
   const int each = which == 2 ? nfull : ntri;
-  const int b = st.b0 + r / each;
+  const int b = r / each;
   r %= each;
   int i, j;
   if (which == 2) {
@@ -130,7 +110,7 @@ __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int la
     j = r - i * (i + 1) / 2;
   }
   if (lane == 0) {
-    out->entry = st.entry;
+    out->entry = lo;
     out->b = b;
     out->step = step;
     out->which = which;
@@ -181,19 +161,6 @@ __device__ __forceinline__ uint4* piece(float* patch, int row, int at) {
   return reinterpret_cast<uint4*>(patch) + row * 4 + (at ^ (row / 2 & 3));
 }
 
-// Writes the patch as 32 binary16 numbers of each of the rows row0.. to a
-// row-major array, columns col.., whole sectors at a time.
-__device__ __forceinline__ void flush(float* patch, __half* to, int64_t ld, int row0, int rows, int col, int lane) {
-  __syncwarp();
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int r = q * 8 + lane / 4;
-    const uint4 v = *piece(patch, r, lane % 4);
-    if (row0 + r < rows) *reinterpret_cast<uint4*>(to + (int64_t)(row0 + r) * ld + col + lane % 4 * 8) = v;
-  }
-  __syncwarp();
-}
-
 // The result of 32 x 16 numbers of X, in the patch as 32 rows: a warp reads and
 // writes along rows, at any address.
 __device__ __forceinline__ void result(const Products& p, const Entry& e, const Io& io, int b, int row0, int col,
@@ -238,28 +205,25 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   const int M = t.which == 2 ? rows : k, N = t.which == 2 ? ncols : k;
   const float ca = p.coef[t.step][0], cb = p.coef[t.step][1], cc = p.coef[t.step][2];
   const bool last = t.step == p.steps - 1;
-  const int col0 = t.j * kTile, ncol = row0 < M ? min(kTile, N - col0) : 0;
-  float* diag = en.diag + t.b * ldk;
-  // what a product reads and what only epilogues do
-  __half* const to = t.which == 0 ? en.a + t.b * k * ldk
-                     : t.which == 1 ? en.b + t.b * k * ldk : en.x[(t.step & 1) ^ 1] + t.b * rows * ldx;
+  // columns of the tile, to whole blocks: padding is written too, as zeros
+  const int col0 = t.j * kTile, ncol = row0 < M ? min(kTile, (N + 31) / 32 * 32 - col0) : 0;
   const int64_t ld = t.which == 2 ? ldx : ldk;
-  uint4* const blk = reinterpret_cast<uint4*>(
-      t.which == 2 ? reinterpret_cast<char*>(en.x32 + t.b * block_size(rows, ldx) + block_at<float>(row, col0, ldx))
-                   : reinterpret_cast<char*>(en.a_blk + t.b * block_size(k, ldk) + block_at<__half>(row, col0, ldk)));
+  const int64_t at0 = t.b * block_size(M, ld) + block_at(row, col0, ld);
+  float* diag = en.diag + t.b * ldk;
+  uint4* const to = reinterpret_cast<uint4*>((t.which == 0 ? en.a : t.which == 1 ? en.b : en.x[(t.step & 1) ^ 1]) + at0);
+  const uint4* const from = reinterpret_cast<const uint4*>((t.which == 1 ? en.a : en.x[t.step & 1]) + at0);
+  uint4* const low = reinterpret_cast<uint4*>(en.lo + at0);
 
   int ok = ready;
   float di = 0.0f;
-  uint4 old[4];
+  uint4 hi[2], lo[2];
   const auto after = [](int c) { return c % 32 ? c + 48 : c + 16; };   // the warp's next 16 columns
   const auto fetch = [&](int c) {
-    if (c >= ncol) return;
-    if (t.which == 1) {
+    if (t.which == 0 || c >= ncol) return;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) old[q] = __ldcg(blk + c * 4 + q * 32);
-    } else if (t.which == 2) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) old[q] = __ldcg(blk + c * 8 + q * 32);
+    for (int q = 0; q < 2; ++q) {
+      hi[q] = __ldcg(from + c * 4 + q * 32);
+      if (t.which == 2) lo[q] = __ldcg(low + c * 4 + q * 32);
     }
   };
   if (t.which != 0) {
@@ -312,20 +276,22 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       }
     } else if (t.which == 1) {
       const float2 scale = both(__fmul_rn(cc, 1.0f / kScale)), e2 = both(ei);
-      const uint32_t* s = reinterpret_cast<const uint32_t*>(old);
+      const uint32_t* s = reinterpret_cast<const uint32_t*>(hi);
       const float2* d = reinterpret_cast<const float2*>(cols + c);
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
       fetch(after(c));
     } else {
-      const float2* x = reinterpret_cast<const float2*>(old);
+      const uint32_t *h = reinterpret_cast<const uint32_t*>(hi), *l = reinterpret_cast<const uint32_t*>(lo);
       const float2* d = reinterpret_cast<const float2*>(cols + c);
-      const float2 ca2 = both(ca), down = both(1.0f / kScale), e2 = both(ei);
+      const float2 ca2 = both(ca), down = both(1.0f / kScale), e2 = both(ei), low2 = both(1.0f / kLoScale);
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int q = 0; q < 8; ++q) {
+        const float2 x = unpack(h[q]);
         y[q] = __ffma2_rn(y[q], down,
-                          __ffma2_rn(ca2, x[q], __fmul2_rn(tall ? d[q] : e2, unpack(pack(x[q].x, x[q].y)))));
+                          __ffma2_rn(ca2, __ffma2_rn(unpack(l[q]), low2, x), __fmul2_rn(tall ? d[q] : e2, x)));
+      }
       fetch(after(c));
       if (last) {
 #pragma unroll
@@ -333,19 +299,20 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
         result(p, en, p.c.io[en.item], t.b, row0, col0 + c, patch, lane);
         continue;
       }
+      __align__(16) __half2 first[8], second[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) blk[c * 8 + q * 32] = reinterpret_cast<const uint4*>(v)[q];
+      for (int q = 0; q < 8; ++q) split(y[q], &first[q], &second[q]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        to[c * 4 + q * 32] = reinterpret_cast<const uint4*>(first)[q];
+        low[c * 4 + q * 32] = reinterpret_cast<const uint4*>(second)[q];
+      }
+      continue;
     }
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float2* z = y + 4 * q;
-      const uint4 h = make_uint4(pack(z[0].x, z[0].y), pack(z[1].x, z[1].y), pack(z[2].x, z[2].y),
-                                 pack(z[3].x, z[3].y));
-      *piece(patch, lane, c / 8 % 4 + q) = h;
-      if (t.which == 0) blk[c * 4 + q * 32] = h;
-    }
-    // 32 columns are whole, or end here (a row has room for 32)
-    if (c % 32 || c + 16 >= ncol) flush(patch, to, ld, row0, M, col0 + c / 32 * 32, lane);
+    for (int q = 0; q < 2; ++q)
+      to[c * 4 + q * 32] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
+                                      pack(y[4 * q + 2].x, y[4 * q + 2].y), pack(y[4 * q + 3].x, y[4 * q + 3].y));
   }
   // the accumulator may be written again once both CTAs have read it
   tc_fence_before();
@@ -441,8 +408,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (elected()) {
           if (rank == 0 && side == 0)
             mbar_expect(full + 8 * s, kPair * kBoxBytes * (2 + (both || x) + (both || k0 >= other_turn)));
-          tma_load<kPair>(to, map, bar, x ? at : k0, x ? k0 : at, b);
-          if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, (x ? at : k0) + 64, x ? k0 : at, b);
+          const int down = (x ? k0 : at) / 32, right = (x ? at : k0) / 8;   // rows of blocks, pieces
+          tma_load<kPair>(to, map, bar, 0, down, right, b);
+          if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, 0, down, right + 8, b);
         }
         __syncwarp();
         if (side == 0 && k0 == 0 && lane == 0) shared_set(told, n + 1);
@@ -485,7 +453,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const bool xa = k0 >= ta, xb = k0 >= tb;
         const uint32_t idesc = instruction(kTile, kTile, xa, xb);
         const uint32_t at = stages + s * kStageBytes;
-        const uint64_t da = operand(at, kBoxBytes), db = operand(at + kOperandBytes, kBoxBytes);
+        // core matrices: 128 bytes from eight rows to the next, kPieceBytes from piece to piece
+        const auto desc = [](uint32_t addr, bool x) {
+          return x ? operand(addr, 128, kPieceBytes) : operand(addr, kPieceBytes, 128);
+        };
+        const uint64_t da = desc(at, xa), db = desc(at + kOperandBytes, xb);
         ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, phase, fault));
         if (!ok) break;
         tc_fence_after();
@@ -493,8 +465,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           const auto four = [&](int q0) {
 #pragma unroll
             for (int q = q0; q < q0 + 4; ++q) {
-              // 16 deep: 32 bytes along a row (four to a box), or 16 rows of 128 bytes
-              const uint32_t along = (q / 4 * kBoxBytes + q % 4 * 32) >> 4, down = q * 16 * 128 >> 4;
+              // 16 deep: two pieces, or sixteen rows
+              const uint32_t along = q * 2 * kPieceBytes >> 4, down = q * 2 * 128 >> 4;
               mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > 0 || q > 0);
             }
           };

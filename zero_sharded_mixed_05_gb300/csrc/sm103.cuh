@@ -140,21 +140,21 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
-// ---- TMA: a tile of a [batch][rows][cols] array.  x must be a multiple of 16
+// ---- TMA: a box of an array of four dimensions.  x must be a multiple of 16
 // bytes.  With a pair the barrier may be the other CTA's.
 
 template <int kPair>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y,
-                                         int z) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                         int w) {
   if constexpr (kPair == 2)
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
         : "memory");
 }
 
@@ -228,13 +228,13 @@ __device__ __forceinline__ void tmem_load_wait() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory operand of a product: 128-byte rows swizzled over groups of
-// eight (1024 bytes), stored as boxes of 128 rows of 64 numbers.  With the
-// product's depth along the rows' 128 bytes the groups follow at 1024 bytes;
-// with the depth down the rows, `box` is the distance of the next 64 numbers across.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t box) {
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(box >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory operand of a product, not swizzled: core matrices of 8 rows of
+// 16 bytes, `deep` bytes from one to the next along the product's depth and
+// `wide` bytes across it.  Depth along the 16 bytes: the descriptor's leading
+// offset is the depth's; down the rows: the stride offset is.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+         (uint64_t)1 << 46;
 }
 
 // Instruction word: binary16 operands, binary32 accumulators; across_a /
