@@ -97,6 +97,33 @@ const void* products_kernel(int pair) {
   return pair == 2 ? (const void*)zm::muon_products_kernel<2> : (const void*)zm::muon_products_kernel<1>;
 }
 
+// Estimated cycles of one step's products with tiles of 128 * pair: full waves of
+// tiles at what a stage of depth 128 takes (measured: 740 cycles for a single
+// CTA's 128 x 128, 1060 for a pair's 256 x 256, whose tensor work alone is 512
+// and 1024), and a fixed part a product (from a tile's needs being met to its
+// count: 5500 and 7500).  Measured, singles against pairs: 768x768 x 12 174 and
+// 186 us, 2048x2048 215 and 241, 1536x1536 x 4 305 and 267, 4096x4096 1164 and 922.
+double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
+  const int tile = 128 * pair, slots = std::max(1, sms / pair);
+  double tiles[2] = {0, 0}, work[3] = {0, 0, 0};
+  for (const zm::Entry& e : entries) {
+    const double nk = (e.k + tile - 1) / tile;
+    const double tri = e.batch * nk * (nk + 1) / 2;
+    const double full = (double)e.batch * ((e.rows + tile - 1) / tile) * ((e.cols + tile - 1) / tile);
+    tiles[0] += tri;
+    tiles[1] += full;
+    work[0] += tri * ((e.l + 127) / 128);
+    work[1] += tri * ((e.k + 127) / 128);
+    work[2] += full * ((e.k + 127) / 128);
+  }
+  double cycles = 0;
+  for (int which = 0; which < 3; ++which) {
+    const double n = tiles[which == 2];
+    cycles += std::ceil(n / slots) * (work[which] / n) * (pair == 2 ? 1060 : 740) + (pair == 2 ? 7500 : 5500);
+  }
+  return cycles;
+}
+
 // One cooperative launch (its CTAs wait for one another), in clusters of the pair.
 cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cudaStream_t s) {
   cudaLaunchConfig_t lc = {};
@@ -189,6 +216,7 @@ bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t rows, int64_t l
 cudaError_t place(zero_muon_t h) {
   Layout lay;
   const int64_t n = (int64_t)h->entries.size();
+  h->pair = n > 0 && products_cost(h->entries, 1, h->sms) <= products_cost(h->entries, 2, h->sms) ? 1 : 2;
   int64_t units = 0;
   for (const zm::Entry& e : h->entries) units += e.batch;
   const void* kernel = products_kernel(h->pair);
