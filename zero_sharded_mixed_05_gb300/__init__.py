@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import _build
 
@@ -201,8 +202,8 @@ SIGNATURES = [
     ("zero_muon_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_qk_create", _i32, [_P(zero_qk_config), _P(_vp)]),
     ("zero_qk_destroy", _i32, [_vp]),
-    ("zero_qk_norm_rope", _i32, [_vp, _P(zero_qk_buffers), _vp]),
-    ("zero_qk_norm_rope_backward", _i32, [_vp, _P(zero_qk_buffers), _vp]),
+    ("zero_qk_norm_rope", _i32, [_vp, _vp, _vp]),
+    ("zero_qk_norm_rope_backward", _i32, [_vp, _vp, _vp]),
     ("zero_qk_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_opt_status_string", ctypes.c_char_p, [_i32]),
     ("zero_opt_last_error", ctypes.c_char_p, []),
@@ -251,6 +252,8 @@ def current_stream(device=None) -> int:
 
 
 def _stream(s):
+    if type(s) is int:
+        return s
     if s is None:
         import torch
         if torch.cuda.is_available():
@@ -797,9 +800,11 @@ def zero_muon_launch_count(h) -> int:
 
 # ---------------------------------------------------------------- query/key norm and rotation
 
-# What a handle was made for, so that the binding can check tensors against it:
-# head counts, head_dim, rotary_dim / 2, dtype, gain_per_head.
-_qk_configs = {}
+# What a handle was made for, so that the binding can check tensors against it
+# (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, device), and
+# memory for one call's zero_qk_buffers (calls on one handle are ordered).
+_qk_handles = {}
+_qk_pack = struct.Struct("=27qii").pack_into
 
 
 def make_qk_config(q_heads, k_heads, head_dim, rotary_dim=None, dtype=BF16, interleaved=False,
@@ -815,75 +820,83 @@ def zero_qk_create(cfg: zero_qk_config) -> int:
     _check(lib().zero_qk_create(ctypes.byref(cfg), ctypes.byref(h)), "zero_qk_create")
     import torch
     dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
-    _qk_configs[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
-                            bool(cfg.gain_per_head))
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    b = zero_qk_buffers()
+    _qk_handles[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
+                            bool(cfg.gain_per_head), dev, b, ctypes.addressof(b))
     return h.value
 
 
 def zero_qk_destroy(h) -> None:
-    _qk_configs.pop(h, None)
+    _qk_handles.pop(h, None)
     _check(lib().zero_qk_destroy(h), "zero_qk_destroy")
+
+
+def _qk_refuse(name, what):
+    raise ValueError(f"{name} must be {what}")
 
 
 def _qk_heads(t, name, n, heads, dim, dtype, dev):
     """(address, token stride, head stride) of a [tokens, heads, D] tensor."""
-    if t.dtype is not dtype or t.shape != (n, heads, dim) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a {dtype} tensor of {(n, heads, dim)} on cuda:{dev}")
-    st, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must have contiguous heads")
+    st, sh, sd = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if t.dtype is not dtype or t.shape != (n, heads, dim) or t.get_device() != dev or sd != 1:
+        _qk_refuse(name, f"a {dtype} tensor of {(n, heads, dim)} with contiguous heads on "
+                   f"cuda:{dev}")
     return t.data_ptr(), st, sh
 
 
-def _qk_gain(t, name, heads, dim, per_head, dev):
-    import torch
-    shape = (heads, dim) if per_head else (dim,)
-    if t.dtype is not torch.float32 or t.shape != shape or t.get_device() != dev \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {shape} on cuda:{dev}")
+def _qk_flat(t, name, shape, dtype, dev):
+    """Address of a contiguous tensor."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _qk_refuse(name, f"a contiguous {dtype} tensor of {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _qk_call(fn, h, ins, outs, grads, gains, dgains, cos, sin, positions, stream):
-    """Check the tensors against the handle and make the call.  ins, outs,
-    grads: (name, query tensor, key tensor); gains, dgains: (query's, key's)."""
+_NO_HEADS = (0, 0, 0)
+
+
+def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gain, cos, sin,
+             positions, stream):
+    """Check the tensors against the handle and make the call."""
     import torch
-    cfg = _qk_configs.get(h)
-    if cfg is None:
+    if h not in _qk_handles:
         raise ValueError("not a handle of zero_qk_create")
-    hq, hk, dim, half, dtype, per_head = cfg
-    q = ins[1]
-    dev, n = q.get_device(), q.shape[0]
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("q must be a CUDA tensor of the current device")
-    at = []
-    for name, tq, tk in (ins, outs, grads):
-        at.append(zero_qk_tensor(*_qk_heads(tq, name % "q", n, hq, dim, dtype, dev))
-                  if tq is not None else zero_qk_tensor())
-        at.append(zero_qk_tensor(*_qk_heads(tk, name % "k", n, hk, dim, dtype, dev))
-                  if hk and tk is not None else zero_qk_tensor())
-    gain = [None if t is None or not heads else _qk_gain(t, name, heads, dim, per_head, dev)
-            for name, t, heads in (("q_gain", gains[0], hq), ("k_gain", gains[1], hk),
-                                   ("dq_gain", dgains[0], hq), ("dk_gain", dgains[1], hk))]
-    n_pos, pc, ps = 0, None, None
+    hq, hk, dim, half, dtype, per_head, dev, b, at = _qk_handles[h]
+    n = q.shape[0]
+    f32 = torch.float32
+    tq = _qk_heads(q, "q", n, hq, dim, dtype, dev)
+    tqo = _qk_heads(qo, names[0], n, hq, dim, dtype, dev)
+    tdq = _NO_HEADS if dq is None else _qk_heads(dq, "dq", n, hq, dim, dtype, dev)
+    shape = (hq, dim) if per_head else (dim,)
+    gq = 0 if q_gain is None else _qk_flat(q_gain, "q_gain", shape, f32, dev)
+    dgq = 0 if dq_gain is None else _qk_flat(dq_gain, "dq_gain", shape, f32, dev)
+    tk = tko = tdk = _NO_HEADS
+    gk = dgk = 0
+    if hk:
+        tk = _qk_heads(k, "k", n, hk, dim, dtype, dev)
+        tko = _qk_heads(ko, names[1], n, hk, dim, dtype, dev)
+        if dk is not None:
+            tdk = _qk_heads(dk, "dk", n, hk, dim, dtype, dev)
+        if per_head:
+            shape = (hk, dim)
+        if k_gain is not None:
+            gk = _qk_flat(k_gain, "k_gain", shape, f32, dev)
+        if dk_gain is not None:
+            dgk = _qk_flat(dk_gain, "dk_gain", shape, f32, dev)
+    n_pos = pc = ps = 0
     if half:
-        for name, t in (("cos", cos), ("sin", sin)):
-            if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != half \
-                    or t.get_device() != dev or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous float32 tensor of (positions, "
-                                 f"{half}) on cuda:{dev}")
-        n_pos, pc, ps = cos.shape[0], cos.data_ptr(), sin.data_ptr()
-        if sin.shape[0] != n_pos:
-            raise ValueError("cos and sin must have the same shape")
+        n_pos = cos.shape[0]
+        table = (n_pos, half)
+        pc = _qk_flat(cos, "cos", table, f32, dev)
+        ps = _qk_flat(sin, "sin", table, f32, dev)
     wide = positions.dtype is torch.int64
-    if positions.shape != (n,) or positions.get_device() != dev or not positions.is_contiguous() \
-            or not (wide or positions.dtype is torch.int32):
-        raise ValueError(f"positions must be a contiguous int64 or int32 tensor of ({n},) on "
-                         f"cuda:{dev}")
-    b = zero_qk_buffers(n, n_pos, *at, *gain, pc, ps, positions.data_ptr(), wide, 0)
+    pp = _qk_flat(positions, "positions", (n,), torch.int64 if wide else torch.int32, dev)
+    _qk_pack(b, 0, n, n_pos, *tq, *tk, *tqo, *tko, *tdq, *tdk, gq, gk, dgq, dgk, pc, ps, pp, wide, 0)
     if stream is None:
-        stream = torch.cuda.current_stream(dev).cuda_stream
-    _check(getattr(lib(), fn)(h, ctypes.byref(b), _stream(stream)), fn)
+        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    status = fn(h, at, _stream(stream))
+    if status:
+        _check(status, fn.__name__)
 
 
 def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions,
@@ -892,8 +905,8 @@ def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions
     `q_out` and `k_out` (which may be `q` and `k`).  `k`, `k_out` are not looked
     at by a handle with k_heads 0; a gain may be None (ones).  A token of
     position -1 is padding and gets zeros."""
-    _qk_call("zero_qk_norm_rope", h, ("%s", q, k), ("%s_out", q_out, k_out), ("", None, None),
-             (q_gain, k_gain), (None, None), cos, sin, positions, stream)
+    _qk_call(lib().zero_qk_norm_rope, h, ("q_out", "k_out"), q, k, q_out, k_out, None, None, q_gain,
+             k_gain, None, None, cos, sin, positions, stream)
 
 
 def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain, q_gain, k_gain,
@@ -901,8 +914,8 @@ def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain
     """Gradients of `zero_qk_norm_rope`: from `dq_out`, `dk_out` and the
     forward call's inputs into `dq`, `dk` (which may be `dq_out`, `dk_out`) and
     the gains' float32 gradients (None: not wanted)."""
-    _qk_call("zero_qk_norm_rope_backward", h, ("%s", q, k), ("d%s_out", dq_out, dk_out),
-             ("d%s", dq, dk), (q_gain, k_gain), (dq_gain, dk_gain), cos, sin, positions, stream)
+    _qk_call(lib().zero_qk_norm_rope_backward, h, ("dq_out", "dk_out"), q, k, dq_out, dk_out, dq, dk,
+             q_gain, k_gain, dq_gain, dk_gain, cos, sin, positions, stream)
 
 
 def zero_qk_launch_count(h) -> int:

@@ -47,7 +47,7 @@ constexpr int kBoxBytes = 128 * 64 * 2;            // 128 rows of eight pieces o
 constexpr int kPieceBytes = 128 * 16;              // in shared memory: a piece's 128 rows side by side
 constexpr int kOperandBytes = 2 * kBoxBytes;       // a CTA's 128 rows (or columns) of it
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 12;
 constexpr int kProductThreads = 32 * (4 + kEpiWarps);
 constexpr int kPatchBytes = kEpiWarps * 2048;      // a warp's 32 rows of 64 bytes
 constexpr int kDiagBytes = 2 * 256 * 4;            // of two tiles
@@ -184,8 +184,8 @@ __device__ __forceinline__ void result(const Products& p, const Entry& e, const 
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// One tile's epilogue: the warp's 32 rows of the accumulator, every second 32 of
-// its columns, 16 at a time.  Whatever it reads besides is fetched while the products
+// One tile's epilogue: the warp's 32 rows of the accumulator, every third 16 of
+// its columns.  Whatever it reads besides is fetched while the products
 // still run: the diagonal's numbers of the tile's columns go to shared memory
 // (`cols`), and the next columns' numbers are on their way while those before
 // are worked on.  The loops are kept short: a small matrix runs each of them
@@ -217,7 +217,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   int ok = ready;
   float di = 0.0f;
   uint4 hi[2], lo[2];
-  const auto after = [](int c) { return c % 32 ? c + 48 : c + 16; };   // the warp's next 16 columns
+  constexpr int kNext = 16 * (kEpiWarps / 4);  // to the warp's next 16 columns
   const auto fetch = [&](int c) {
     if (t.which == 0 || c >= ncol) return;
 #pragma unroll
@@ -229,7 +229,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   if (t.which != 0) {
     ok = __all_sync(0xffffffffu, ok && shared_wait(told, number + 1, &p.c.ws->fault));
     if (ok) {
-      fetch(part * 32);
+      fetch(part * 16);
       const int c = warp * 32 + lane;
       float d = 0.0f;
       if (c < kTile && col0 + c < N) d = __ldcg(diag + col0 + c);
@@ -240,7 +240,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   }
   if (lane == 0 && ok) ok = mbar_wait(full_bar, phase, &p.c.ws->fault);
   ok = __shfl_sync(0xffffffffu, ok, 0);
-  // all eight warps go on or none: the count of finished tiles is of whole ones
+  // all its warps go on or none: the count of finished tiles is of whole ones
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.ne.b32 p, %1, 0;\n"
       "barrier.red.and.pred q, 1, %2, p;\nselp.b32 %0, 1, 0, q;\n}"
@@ -254,14 +254,14 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
   // the row's share of b A + c A A's factor, or e_i of a wide matrix
   const float ei = t.which == 1 ? __fmaf_rn(cc, di, cb) : __fmul_rn(di, __fmaf_rn(cc, di, cb));
   float next[16];
-  if (part * 32 < ncol) tmem_load16(lanes + part * 32, next);
+  if (part * 16 < ncol) tmem_load16(lanes + part * 16, next);
 #pragma unroll 1
-  for (int c = part * 32; c < ncol; c = after(c)) {
+  for (int c = part * 16; c < ncol; c += kNext) {
     float v[16];
     tmem_load_wait();
 #pragma unroll
     for (int q = 0; q < 16; ++q) v[q] = next[q];
-    if (after(c) < ncol) tmem_load16(lanes + after(c), next);
+    if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
     float2* y = reinterpret_cast<float2*>(v);
     if (t.which == 0) {
       const int at = row - (col0 + c);         // the diagonal's place, if in these columns
@@ -281,7 +281,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
 #pragma unroll
       for (int q = 0; q < 8; ++q)
         y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
-      fetch(after(c));
+      fetch(c + kNext);
     } else {
       const uint32_t *h = reinterpret_cast<const uint32_t*>(hi), *l = reinterpret_cast<const uint32_t*>(lo);
       const float2* d = reinterpret_cast<const float2*>(cols + c);
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
         y[q] = __ffma2_rn(y[q], down,
                           __ffma2_rn(ca2, __ffma2_rn(unpack(l[q]), low2, x), __fmul2_rn(tall ? d[q] : e2, x)));
       }
-      fetch(after(c));
+      fetch(c + kNext);
       if (last) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) *piece(patch, lane, q) = reinterpret_cast<const uint4*>(v)[q];

@@ -616,8 +616,9 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     if (ok) break;
   }
   a.chunks = c.head_dim / (2 * v);
+  const int chunks_lane = v == 8 ? 1 : v == 4 ? 2 : v == 2 ? 4 : 8;
   a.lanes = 1;
-  while (a.lanes < 32 && a.lanes < a.chunks) a.lanes *= 2;
+  while (a.lanes * chunks_lane < a.chunks) a.lanes *= 2;
   for (int w = 0; w < 2; ++w) {
     Rows& r = a.r[w];
     r.heads = w ? c.k_heads : c.q_heads;
@@ -657,7 +658,6 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   const void* fn = c.dtype == ZERO_FP16   ? kernel_of<__half>(c.interleaved, backward, sum, v, r)
                    : c.dtype == ZERO_BF16 ? kernel_of<__nv_bfloat16>(c.interleaved, backward, sum, v, r)
                                           : kernel_of<float>(c.interleaved, backward, sum, v, r);
-  const int chunks_lane = v == 8 ? 1 : v == 4 ? 2 : v == 2 ? 4 : 8;
   size_t smem = es_vec == 16 ? (size_t)ring_bytes(threads, chunks_lane, r, backward) : 0;
   if (want) smem = std::max(smem, (size_t)a.per * a.reps * c.head_dim * sizeof(float));
   const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
