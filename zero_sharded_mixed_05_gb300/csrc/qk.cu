@@ -188,7 +188,7 @@ __device__ __forceinline__ void load_f(const float* p, float* x) {
   }
 }
 
-constexpr int kRing = 3;
+constexpr int kRing = 2;
 
 // Bytes of a CTA's ring: R rows of C chunks of two vectors, for the row and
 // (backward) its gradient.
@@ -200,7 +200,7 @@ constexpr int ring_bytes(int threads, int c, int r, bool backward) {
 // keys).  kSum: one sum of gain gradients a group (a shared gain) instead of
 // one a head.
 template <typename T, int V, int C, int R, bool kInter, bool kBackward, bool kSum>
-__global__ void __launch_bounds__(kQkThreads, 2) qk_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const __grid_constant__ QkArgs a) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   constexpr bool kAsync = sizeof(T) * V == 16;
   constexpr int kEach = kBackward ? 4 : 2;                 // vectors of a chunk
@@ -489,7 +489,8 @@ const void* kernel_for(int v, int r) {
     if (v == 8) {
       if constexpr (!kBackward)
         if (r == 4) return (const void*)qk_kernel<T, 8, 1, 4, kInter, kBackward, kSum>;
-      if (r == 2) return (const void*)qk_kernel<T, 8, 1, 2, kInter, kBackward, kSum>;
+      if constexpr (!kBackward || kSum)
+        if (r == 2) return (const void*)qk_kernel<T, 8, 1, 2, kInter, kBackward, kSum>;
       return (const void*)qk_kernel<T, 8, 1, 1, kInter, kBackward, kSum>;
     }
   switch (v) {
@@ -639,12 +640,15 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   const int groups = kQkThreads / a.lanes;
   const int es_vec = v * es;
   const bool want = backward && (dgain[0] || dgain[1]);
-  const bool sum = want && !c.gain_per_head;
+  const bool sum = backward && !(want && c.gain_per_head);
   // Heads a group: fewer reads of the angles and fewer bookkeeping
   // instructions a row, as long as both head counts divide and the tokens
-  // still fill the device.  The ring sets the most: two CTAs an SM.
+  // still fill the device.  The most: what the ring and the registers leave two
+  // or three CTAs an SM for (16,384 tokens, 40 heads of 128: forward 59 us with
+  // four, 68 with two; backward 100 with two, 157 with one; with sums a head,
+  // 20 heads of 64, backward 46 with one, 52 with two).
   int r = 1;
-  const int most_r = es_vec < 16 ? 1 : v == 8 ? (backward ? 2 : 4) : (backward ? 1 : 2);
+  const int most_r = es_vec < 16 ? 1 : v == 8 ? (!backward ? 4 : sum ? 2 : 1) : (backward ? 1 : 2);
   while (2 * r <= most_r && c.q_heads % (2 * r) == 0 && c.k_heads % (2 * r) == 0 &&
          b->tokens * a.heads >= (int64_t)2 * r * groups * 2 * h->sms)
     r *= 2;
