@@ -150,6 +150,14 @@ zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double 
 /* What the last call did.  Synchronizes `stream`.  Errors: EINVAL, ECUDA. */
 zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out);
 
+/* Failure-detection test hook.  In the next call of this handle the tiles of
+ * every product but the first wait for counts that are never reached.  Their
+ * waits run out after their bound (two seconds), the kernel ends without
+ * writing results and zero_muon_last_step reports fault = 1.  Nothing hangs,
+ * the context stays usable and the next call is whole again.  Host only.
+ * Errors: EINVAL (NULL). */
+zero_status zero_muon_inject_wait_fault(zero_muon_t h);
+
 /* Kernels launched by this handle since creation. */
 zero_status zero_muon_launch_count(zero_muon_t h, int64_t* launches);
 

@@ -58,6 +58,7 @@ def test_null_arguments(z):
     assert L.zero_muon_step(None, None, 1.0, None, None) == z.ZERO_EINVAL
     assert L.zero_muon_last_step(None, None, None) == z.ZERO_EINVAL
     assert L.zero_muon_launch_count(None, None) == z.ZERO_EINVAL
+    assert L.zero_muon_inject_wait_fault(None) == z.ZERO_EINVAL
     assert L.zero_muon_destroy(None) == z.ZERO_OK
     assert L.zero_opt_decision(None, None) == z.ZERO_EINVAL
 

@@ -391,3 +391,24 @@ def test_binding_refuses(z):
             z.make_muon_list([dict(grad=a.T, momentum=a, master=a, param16=a)])
     finally:
         z.zero_muon_destroy(h)
+
+
+@pytest.mark.parametrize("shape", [(100, 60, 1), (1536, 1536, 4)], ids=str)
+def test_a_wait_that_runs_out_is_a_reported_fault(z, shape):
+    """With single CTAs' tiles and with pairs': the call ends by itself, says
+    so, writes no result, and the next one is whole."""
+    import torch
+    m, n, b = shape
+    g = torch.randn(b, m, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    h = z.zero_muon_create(z.make_muon_config(), [shape])
+    try:
+        out = torch.full_like(g, 7.0)
+        z.zero_muon_inject_wait_fault(h)
+        z.zero_muon_orthogonalize(h, [g], [out])
+        info = z.zero_muon_last_step(h)
+        assert (info.skipped, info.fault) == (0, 1) and (out == 7).all()
+        z.zero_muon_orthogonalize(h, [g], [out])
+        assert z.zero_muon_last_step(h).fault == 0
+        close(out, ortho64(g), "fp32")
+    finally:
+        z.zero_muon_destroy(h)

@@ -41,6 +41,7 @@ struct zero_muon_handle {
   int smem = 0;
   int32_t triangles = 0, fulls = 0; // tiles of a product of the first two kinds, of the third
   int64_t launches = 0;
+  uint32_t inject = 0;              // test hook, one call
 };
 
 namespace {
@@ -162,6 +163,8 @@ zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t
   pr.fulls = h->fulls;
   pr.tiles = (2ll * h->triangles + h->fulls) * h->cfg.steps;
   pr.steps = h->cfg.steps;
+  pr.inject = h->inject;
+  h->inject = 0;
   for (int i = 0; i < pr.steps; ++i)
     for (int j = 0; j < 3; ++j) pr.coef[i][j] = (float)h->cfg.coef[i][j];
   cudaLaunchAttribute attr[2];
@@ -520,6 +523,12 @@ zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out
   if (e != cudaSuccess) return cuda_fail(e, "zero_muon_last_step");
   out->skipped = w.skipped;
   out->fault = w.fault;
+  return ZERO_OK;
+}
+
+zero_status zero_muon_inject_wait_fault(zero_muon_t h) {
+  if (!h) return fail(ZERO_EINVAL, "handle is NULL");
+  h->inject = 1u << 30;
   return ZERO_OK;
 }
 

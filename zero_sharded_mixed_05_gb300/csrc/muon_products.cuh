@@ -61,6 +61,7 @@ struct Products {
   int64_t tiles;             // of all products
   int32_t triangles, fulls;  // of a product of the first two kinds, of the third
   int32_t steps;
+  uint32_t inject;           // test hook: added to what a tile waits for
   float coef[ZERO_MUON_MAX_STEPS][3];
 };
 
@@ -118,8 +119,9 @@ __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int la
     out->j = j;
     out->unit = e.unit0 + b;
     out->depth = which == 0 ? e.l : e.k;
-    out->need = (uint32_t)kPair * ((uint32_t)step * (2 * ntri + nfull) +
+    const uint32_t need = (uint32_t)kPair * ((uint32_t)step * (2 * ntri + nfull) +
                                    (which == 0 ? 0u : which == 1 ? (uint32_t)ntri : 2u * ntri));
+    out->need = need ? need + p.inject : 0u;
   }
   __syncwarp();
 }

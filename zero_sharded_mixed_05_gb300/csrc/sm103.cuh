@@ -78,10 +78,11 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr uint64_t kWaitNs = 10ull * 1000 * 1000 * 1000;
+constexpr uint64_t kWaitNs = 2ull * 1000 * 1000 * 1000;
 
-// Waits until the phase of `parity` has completed: true.  After ten seconds,
-// or when another thread has given up, sets *fault and gives up: false.
+// Waits until the phase of `parity` has completed: true.  After two seconds (a
+// tile takes milliseconds at most), or when another thread has given up, sets
+// *fault and gives up: false.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* fault) {
   if (mbar_try(bar, parity)) return true;
   uint64_t t0 = 0;
