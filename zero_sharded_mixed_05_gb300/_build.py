@@ -15,7 +15,7 @@ SOURCES = [os.path.join(CSRC, "zero_opt.cu"), os.path.join(CSRC, "ckpt.cpp"),
            os.path.join(CSRC, "qk.cu"), os.path.join(CSRC, "muon.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("kernels.cuh", "zero_opt_internal.h",
                                                      "host_util.h", "decide_core.h", "host_cast.h",
-                                                     "muon_kernels.cuh", "muon_products.cuh",
+                                                     "muon_kernels.cuh", "muon_products.cuh", "muon_resident.cuh",
                                                      "sm103.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("zero_opt.h", "zero_qk.h",
                                                                        "zero_muon.h")]

@@ -1,6 +1,6 @@
 // muon.cu -- host side of the orthogonalised update (zero_muon.h): checks,
 // the workspace and its layout, launches.
-#include "muon_products.cuh"
+#include "muon_resident.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -42,6 +42,11 @@ struct zero_muon_handle {
   int32_t triangles = 0, fulls = 0; // tiles of a product of the first two kinds, of the third
   int64_t launches = 0;
   uint32_t inject = 0;              // test hook, one call
+  // launches of a handle whose matrices all stay on the chip (muon_resident.cuh)
+  struct Launch {
+    int32_t first, n, unit0, units, span, cols;
+  };
+  std::vector<Launch> resident;
 };
 
 namespace {
@@ -98,33 +103,6 @@ const void* products_kernel(int pair) {
   return pair == 2 ? (const void*)zm::muon_products_kernel<2> : (const void*)zm::muon_products_kernel<1>;
 }
 
-// Estimated cycles of one step's products with tiles of 128 * pair: full waves of
-// tiles at what a stage of depth 128 takes (measured: 740 cycles for a single
-// CTA's 128 x 128, 1060 for a pair's 256 x 256, whose tensor work alone is 512
-// and 1024), and a fixed part a product (from a tile's needs being met to its
-// count: 5500 and 7500).  Measured, singles against pairs: 768x768 x 12 174 and
-// 186 us, 2048x2048 215 and 241, 1536x1536 x 4 305 and 267, 4096x4096 1164 and 922.
-double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
-  const int tile = 128 * pair, slots = std::max(1, sms / pair);
-  double tiles[2] = {0, 0}, work[3] = {0, 0, 0};
-  for (const zm::Entry& e : entries) {
-    const double nk = (e.k + tile - 1) / tile;
-    const double tri = e.batch * nk * (nk + 1) / 2;
-    const double full = (double)e.batch * ((e.rows + tile - 1) / tile) * ((e.cols + tile - 1) / tile);
-    tiles[0] += tri;
-    tiles[1] += full;
-    work[0] += tri * ((e.l + 127) / 128);
-    work[1] += tri * ((e.k + 127) / 128);
-    work[2] += full * ((e.k + 127) / 128);
-  }
-  double cycles = 0;
-  for (int which = 0; which < 3; ++which) {
-    const double n = tiles[which == 2];
-    cycles += std::ceil(n / slots) * (work[which] / n) * (pair == 2 ? 1060 : 740) + (pair == 2 ? 7500 : 5500);
-  }
-  return cycles;
-}
-
 // One cooperative launch (its CTAs wait for one another), in clusters of the pair.
 cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cudaStream_t s) {
   cudaLaunchConfig_t lc = {};
@@ -142,11 +120,151 @@ cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cud
   return lc;
 }
 
+// Estimated cycles of one step's products with tiles of 128 * pair: full waves of
+// tiles at what a stage of depth 128 takes (measured: 740 cycles for a single
+// CTA's 128 x 128, 1060 for a pair's 256 x 256, whose tensor work alone is 512
+// and 1024; a tile's epilogue at 3000 and 5500 where that is more), and a fixed
+// part a product (from a tile's needs being met to its count: 5500 and 7500).
+// Measured, singles against pairs: 768x768 x 12 174 and
+// 186 us, 2048x2048 215 and 241, 1536x1536 x 4 305 and 267, 4096x4096 1164 and 922.
+double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
+  const int tile = 128 * pair, slots = std::max(1, sms / pair);
+  double tiles[2] = {0, 0}, work[3] = {0, 0, 0};
+  for (const zm::Entry& e : entries) {
+    const double nk = (e.k + tile - 1) / tile;
+    const double tri = e.batch * nk * (nk + 1) / 2;
+    const double full = (double)e.batch * ((e.rows + tile - 1) / tile) * ((e.cols + tile - 1) / tile);
+    tiles[0] += tri;
+    tiles[1] += full;
+    work[0] += tri * ((e.l + 127) / 128);
+    work[1] += tri * ((e.k + 127) / 128);
+    work[2] += full * ((e.k + 127) / 128);
+  }
+  double cycles = 0;
+  for (int which = 0; which < 3; ++which) {
+    const double n = tiles[which == 2];
+    const double tile_cycles = pair == 2 ? std::max(5500.0, 1060 * work[which] / n) : std::max(3000.0, 740 * work[which] / n);
+    cycles += std::ceil(n / slots) * tile_cycles + (pair == 2 ? 7500 : 5500);
+  }
+  return cycles;
+}
+
+template <typename T, int N>
+const void* resident_kernel(int cols) {
+  return cols == 128 ? (const void*)zm::muon_resident_kernel<T, 128, N> : (const void*)zm::muon_resident_kernel<T, 256, N>;
+}
+
+int resident_bytes(int cols, int span) {
+  return cols == 128 ? zm::resident_bytes<128>(span) : zm::resident_bytes<256>(span);
+}
+
+template <typename T, int N>
+zero_status run_resident(zero_muon_t h, const zm::Start<N>& start, cudaStream_t s) {
+  zm::Resident r = {};
+  r.steps = h->cfg.steps;
+  for (int i = 0; i < r.steps; ++i)
+    for (int j = 0; j < 3; ++j) r.coef[i][j] = (float)h->cfg.coef[i][j];
+  r.head = 1;
+  r.inject = h->inject != 0;
+  h->inject = 0;
+  for (const auto& l : h->resident) {
+    r.first = l.first;
+    r.n = l.n;
+    r.unit0 = l.unit0;
+    r.span = l.span;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)l.span;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(l.units * l.span));
+    lc.blockDim = dim3(zm::kResidentThreads);
+    lc.dynamicSmemBytes = (size_t)resident_bytes(l.cols, l.span);
+    lc.stream = s;
+    lc.attrs = &attr;
+    lc.numAttrs = 1;
+    void* p[] = {&r, const_cast<zm::Start<N>*>(&start)};
+    const cudaError_t e = cudaLaunchKernelExC(&lc, resident_kernel<T, N>(l.cols), p);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
+    ++h->launches;
+    r.head = 0;
+  }
+  return ZERO_OK;
+}
+
+// Every kernel that a call of this handle may launch, readied for its shared memory.
+template <typename T, int N>
+cudaError_t ready_resident(const zero_muon_handle* h) {
+  for (const auto& l : h->resident) {
+    const cudaError_t e = cudaFuncSetAttribute(resident_kernel<T, N>(l.cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               resident_bytes(l.cols, zm::kResidentSpan));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+template <int N>
+cudaError_t ready_resident(const zero_muon_handle* h) {
+  cudaError_t e = ready_resident<__half, N>(h);
+  if (e == cudaSuccess) e = ready_resident<__nv_bfloat16, N>(h);
+  return e == cudaSuccess ? ready_resident<float, N>(h) : e;
+}
+
+// Decides whether the handle's matrices stay on the chip: if each of them can,
+// and that takes less time by estimate (with matrices too large among them they
+// all go through the workspace, where the small ones cost next to nothing).
+// A step of a wave of them takes 5 microseconds with 128 columns a CTA (two on
+// an SM), 6.6 with 256 and 11.5 with more CTAs a matrix, whose sums go through
+// distributed shared memory.  Measured, on the chip against the workspace:
+// 128x128 31 and 70 us, 128x1024 x 32 68 and 102, 64x64 x 1000 109 and 182, but
+// 100x1500 x 60 261 and 180.  Matrices that need fewer CTAs go in launches of
+// their own unless all fit on the device side by side.
+void choose_resident(zero_muon_t h) {
+  int most = 1;
+  int64_t units = 0;
+  const auto span_of = [](const zm::Entry& e) {
+    int span = 1;
+    while (span * 256 < e.l) span *= 2;
+    return span;
+  };
+  for (const zm::Entry& e : h->entries) {
+    if (e.k > zm::kResidentSide || e.l > 256 * zm::kResidentSpan) return;
+    most = std::max(most, span_of(e));
+    units += e.batch;
+  }
+  const bool together = units * most <= h->sms;
+  double here = 0;
+  for (const zm::Entry& e : h->entries) {
+    const int span = span_of(e);
+    const double at_once = e.l <= 128 ? 2 * h->sms : h->sms / span;
+    here += (together ? 1.0 / h->entries.size() : std::ceil(e.batch / at_once)) *
+            ((span > 1 || (together && most > 1) ? 11.5 : e.l <= 128 ? 5.0 : 6.6) * h->cfg.steps + 6);
+  }
+  const double there = 25 + products_cost(h->entries, 1, h->sms) * h->cfg.steps / 1900;
+  if (here > 1.1 * there) return;
+  // entries in order of span, so that a launch's are side by side
+  std::stable_sort(h->entries.begin(), h->entries.end(), [&](const zm::Entry& x, const zm::Entry& y) {
+    return span_of(x) != span_of(y) ? span_of(x) > span_of(y) : (x.l > 128) > (y.l > 128);
+  });
+  int32_t unit = 0;
+  for (int32_t i = 0; i < (int32_t)h->entries.size(); ++i) {
+    zm::Entry& e = h->entries[i];
+    e.unit0 = unit;
+    unit += e.batch;
+    const int span = together ? most : span_of(e);
+    const int cols = e.l <= 128 && span == 1 && !(together && h->resident.size()) ? 128 : 256;
+    if (h->resident.empty() || (!together && (h->resident.back().span != span || h->resident.back().cols != cols)))
+      h->resident.push_back({i, 0, e.unit0, 0, span, cols});
+    ++h->resident.back().n;
+    h->resident.back().units += e.batch;
+  }
+}
+
 template <typename T, int N>
 zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t s) {
   zm::Start<N> start;
   start.c = c;
   std::copy(io, io + c.n, start.io);
+  if (!h->resident.empty()) return run_resident<T, N>(h, start, s);
   void* p[] = {&start};
   zero_status st = launch(h, (const void*)zm::muon_stats_kernel<T, N>, h->chunks, p, s);
   if (st != ZERO_OK) return st;
@@ -217,6 +335,20 @@ bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t rows, int64_t l
 
 // Allocates the workspace, fills in the addresses and readies the products.
 cudaError_t place(zero_muon_t h) {
+  choose_resident(h);
+  if (!h->resident.empty()) {
+    const int64_t table = 256;
+    h->bytes = table + (int64_t)(h->entries.size() * sizeof(zm::Entry));
+    cudaError_t e = cudaMalloc(reinterpret_cast<void**>(&h->mem), (size_t)h->bytes);
+    if (e == cudaSuccess) e = cudaMemset(h->mem, 0, (size_t)table);
+    if (e == cudaSuccess)
+      e = cudaMemcpy(h->mem + table, h->entries.data(), h->entries.size() * sizeof(zm::Entry), cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+    h->call.ws = reinterpret_cast<zm::Workspace*>(h->mem);
+    h->call.entries = reinterpret_cast<const zm::Entry*>(h->mem + table);
+    if (e == cudaSuccess) e = h->entries.size() <= 8 ? ready_resident<8>(h) : ready_resident<zm::kMaxEntries>(h);
+    return e;
+  }
   Layout lay;
   const int64_t n = (int64_t)h->entries.size();
   h->pair = n > 0 && products_cost(h->entries, 1, h->sms) <= products_cost(h->entries, 2, h->sms) ? 1 : 2;
