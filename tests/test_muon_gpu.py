@@ -80,7 +80,8 @@ def close(got, ref, name, what=""):
 SHAPES = [(1, 1, 1), (1, 7, 3), (7, 1, 2), (2, 3, 5), (15, 17, 2), (17, 15, 1), (64, 64, 1),
           (63, 65, 4), (100, 300, 2), (300, 100, 1), (128, 128, 3), (129, 257, 1), (256, 256, 2),
           (257, 129, 2), (255, 511, 1), (511, 255, 1), (640, 130, 1), (384, 520, 1), (16, 2000, 2),
-          (2000, 16, 1), (1000, 777, 1), (520, 1300, 1)]
+          (2000, 16, 1), (1000, 777, 1), (520, 1300, 1), (80, 4200, 2), (5000, 300, 1),
+          (257, 6000, 1), (3000, 1, 2), (1025, 1025, 1)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)

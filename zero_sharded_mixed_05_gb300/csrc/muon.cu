@@ -34,12 +34,13 @@ struct zero_muon_handle {
   zm::Call call = {};               // the fields that no call changes
   const CUtensorMap* maps = nullptr;
   const int32_t* starts = nullptr;
+  float4* parts = nullptr;
   int64_t chunks = 0;               // CTAs of the first two stages
   bool second = false;              // some matrix needs the second
   int pair = 2;                     // CTAs a tile of the products
   int grid = 0;                     // CTAs of the products
   int smem = 0;
-  int32_t triangles = 0, fulls = 0; // tiles of a product of the first two kinds, of the third
+  int32_t count[3] = {0, 0, 0};     // tiles of a product of each kind
   int64_t launches = 0;
   uint32_t inject = 0;              // test hook, one call
   // launches of a handle whose matrices all stay on the chip (muon_resident.cuh)
@@ -120,6 +121,16 @@ cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cud
   return lc;
 }
 
+// Parts that the depth of X X^T (`stages` of 128) is cut into, so that `tiles`
+// tiles of it keep `slots` CTAs or pairs busy: each at least four stages deep,
+// below which the adding up costs what it saves.
+int32_t splits_of(int64_t tiles, int64_t slots, int32_t stages) {
+  const int64_t want = std::min<int64_t>({slots / std::max<int64_t>(tiles, 1), stages / 4, 16});
+  if (want < 2) return 1;
+  const int32_t deep = (int32_t)((stages + want - 1) / want);
+  return (stages + deep - 1) / deep;
+}
+
 // Estimated cycles of one step's products with tiles of 128 * pair: full waves of
 // tiles at what a stage of depth 128 takes (measured: 740 cycles for a single
 // CTA's 128 x 128, 1060 for a pair's 256 x 256, whose tensor work alone is 512
@@ -136,13 +147,21 @@ double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
     const double full = (double)e.batch * ((e.rows + tile - 1) / tile) * ((e.cols + tile - 1) / tile);
     tiles[0] += tri;
     tiles[1] += full;
-    work[0] += tri * ((e.l + 127) / 128);
+    work[0] += tri * ((e.l + 127) / 128);          // spread over parts below
     work[1] += tri * ((e.k + 127) / 128);
     work[2] += full * ((e.k + 127) / 128);
   }
   double cycles = 0;
   for (int which = 0; which < 3; ++which) {
     const double n = tiles[which == 2];
+    if (which == 0) {
+      const int32_t deep = (int32_t)(work[0] / n);
+      const int32_t parts = splits_of((int64_t)n, slots, deep);
+      if (parts > 1) {
+        cycles += deep / parts * (pair == 2 ? 1060 : 740) + (pair == 2 ? 7500 : 5500) + 2500;
+        continue;
+      }
+    }
     const double tile_cycles = pair == 2 ? std::max(5500.0, 1060 * work[which] / n) : std::max(3000.0, 740 * work[which] / n);
     cycles += std::ceil(n / slots) * tile_cycles + (pair == 2 ? 7500 : 5500);
   }
@@ -277,9 +296,9 @@ zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t
   pr.c = c;
   pr.maps = h->maps;
   pr.starts = h->starts;
-  pr.triangles = h->triangles;
-  pr.fulls = h->fulls;
-  pr.tiles = (2ll * h->triangles + h->fulls) * h->cfg.steps;
+  pr.parts = h->parts;
+  std::copy(h->count, h->count + 3, pr.count);
+  pr.tiles = ((int64_t)h->count[0] + h->count[1] + h->count[2]) * h->cfg.steps;
   pr.steps = h->cfg.steps;
   pr.inject = h->inject;
   h->inject = 0;
@@ -365,23 +384,41 @@ cudaError_t place(zero_muon_t h) {
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &lc);
   if (e != cudaSuccess) return e;
   const int tile = 128 * h->pair;
+  clusters = std::max(clusters, 1);
   std::vector<int32_t> starts;
+  int32_t cuts = 0, slots = 0, triangles = 0;
   for (const zm::Entry& en : h->entries) {
     const int32_t nk = (en.k + tile - 1) / tile;
-    starts.push_back(h->triangles);
-    h->triangles += en.batch * (nk * (nk + 1) / 2);
+    triangles += en.batch * (nk * (nk + 1) / 2);
+  }
+  for (zm::Entry& en : h->entries) {
+    const int32_t nk = (en.k + tile - 1) / tile, ntri = nk * (nk + 1) / 2;
+    en.splits = splits_of(triangles, clusters, (en.l + zm::kDepth - 1) / zm::kDepth);
+    en.cuts = en.splits > 1 ? ntri * h->pair : 0;
+    en.cut0 = cuts;
+    en.slot0 = slots;
+    cuts += en.batch * en.cuts;
+    slots += en.splits > 1 ? en.batch * ntri * en.splits : 0;
+    starts.push_back(h->count[0]);
+    h->count[0] += en.batch * ntri * en.splits;
   }
   for (const zm::Entry& en : h->entries) {
-    starts.push_back(h->fulls);
-    h->fulls += en.batch * ((en.rows + tile - 1) / tile) * ((en.cols + tile - 1) / tile);
+    const int32_t nk = (en.k + tile - 1) / tile;
+    starts.push_back(h->count[1]);
+    h->count[1] += en.batch * (nk * (nk + 1) / 2);
   }
-  h->grid = h->pair * std::min(std::max(clusters, 1), std::max(1, std::max(h->triangles, h->fulls)));
+  for (const zm::Entry& en : h->entries) {
+    starts.push_back(h->count[2]);
+    h->count[2] += en.batch * ((en.rows + tile - 1) / tile) * ((en.cols + tile - 1) / tile);
+  }
+  h->grid = h->pair * std::min(clusters, std::max({1, h->count[0], h->count[1], h->count[2]}));
   const int64_t ws = lay.take(sizeof(zm::Workspace)), table = lay.take(n * sizeof(zm::Entry));
   const int64_t maps = lay.take(4 * n * sizeof(CUtensorMap));
   const int64_t io = lay.take(n * sizeof(zm::Io)), first = lay.take(starts.size() * sizeof(int32_t));
   const int64_t part = lay.take(h->chunks * sizeof(double)), ticket = lay.take(units * 4),
-                inv = lay.take(units * 4), done = lay.take(units * 4);
+                inv = lay.take(units * 4), done = lay.take(units * 4), cut = lay.take(cuts * 4ll);
   const int64_t cleared = lay.size;
+  const int64_t parts = lay.take((int64_t)slots * h->pair * 128 * tile * 4);
   std::vector<int64_t> at;
   for (const zm::Entry& e : h->entries) {
     const int64_t x = e.batch * zm::block_size(e.rows, e.ldx) * 2, a = e.batch * zm::block_size(e.k, e.ldk) * 2;
@@ -428,6 +465,8 @@ cudaError_t place(zero_muon_t h) {
   h->call.ticket = reinterpret_cast<unsigned*>(h->mem + ticket);
   h->call.inv = reinterpret_cast<float*>(h->mem + inv);
   h->call.done = reinterpret_cast<uint32_t*>(h->mem + done);
+  h->call.cut = reinterpret_cast<uint32_t*>(h->mem + cut);
+  h->parts = reinterpret_cast<float4*>(h->mem + parts);
   h->maps = reinterpret_cast<const CUtensorMap*>(h->mem + maps);
   h->starts = reinterpret_cast<const int32_t*>(h->mem + first);
   return e;

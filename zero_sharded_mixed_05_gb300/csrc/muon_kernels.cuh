@@ -43,6 +43,8 @@ struct Entry {
   int32_t unit0;             // first matrix of the entry among all
   int32_t chunk0, chunks;    // first CTA, and CTAs a matrix, of the first two stages
   int32_t across;            // blocks of 32 columns
+  int32_t splits, cut0, cuts; // parts of the depth of X X^T; first counter, counters a matrix
+  int32_t slot0;             // first part's place among all
   int32_t item;              // the caller's index
   float s;                   // scale_rule's factor
 };
@@ -87,6 +89,7 @@ struct Call {
   int32_t nesterov, in_type, out_type;
   float decay, lr;           // 1 - lr * weight_decay; lr
   uint32_t* done;            // finished tiles of each matrix
+  uint32_t* cut;             // parts that have arrived, of each tile whose depth is cut
   Io* io;                    // by the caller's index; stage 1 fills it in
 };
 
@@ -210,6 +213,13 @@ __device__ __forceinline__ void put_x(const Entry& e, int b, int row, int col, c
 
 __device__ __forceinline__ float inverse(double squares, double eps) { return (float)(1.0 / (sqrt(squares) + eps)); }
 
+// Counters of a matrix, for the products (a call that ended in a fault leaves
+// them anywhere).
+__device__ __forceinline__ void clear(const Call& c, const Entry& e, int b) {
+  c.done[e.unit0 + b] = 0u;
+  for (int i = 0; i < e.cuts; ++i) c.cut[e.cut0 + b * e.cuts + i] = 0u;
+}
+
 // Stage 1.  Bound by memory: the step reads 2 + 4 bytes a number and writes 4.
 // Squares are added in binary32 within a thread's 64 numbers and in binary64
 // beyond; the last CTA of a matrix adds the CTAs' sums in index order.  Of a
@@ -266,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     d = 0.0;
     for (int i = 0; i < kThreads / 32; ++i) d += red[i];
     const float inv = inverse(d, c.eps);
-    if (threadIdx.x == 0) c.done[unit] = 0u;
+    if (threadIdx.x == 0) clear(c, e, b);
 #pragma unroll 2
     for (int i = 0; i < kPasses; ++i) {      // again from L1 or L2
       int row, col;
@@ -306,7 +316,7 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     for (int i = 1; i < kThreads / 32; ++i) d += red[i];
     c.inv[unit] = inverse(d, c.eps);
     c.ticket[unit] = 0u;
-    c.done[unit] = 0u;
+    clear(c, e, b);
   }
 }
 

@@ -24,6 +24,10 @@
 //   needs, dealt out in turn; a tile waits for its matrix's count of finished
 //   tiles.  With several matrices a wait finds another matrix's tiles done.
 //
+// A deep X X^T of few tiles (k x k of a matrix with l far above k) is cut along
+// its depth: each part leaves its binary32 sums in the workspace, and the one
+// that arrives last adds them up in order and goes on (8080x80 x 2: %CUT% us).
+//
 // The diagonals of A and of b A + c A A are near one where everything else is
 // small, so most of the rounding error would come from them.  A's is kept in
 // binary32 (`diag`, d) and left out of the stored A (A = S + diag d):
@@ -57,9 +61,10 @@ constexpr int kSlots = 16;                         // tiles a CTA has in work: 3
 struct Products {
   Call c;
   const CUtensorMap* maps;   // four an entry: x[0], x[1], a, b
-  const int32_t* starts;     // [2][n]: first tile of each entry in a product of the first two kinds, in the third
+  const int32_t* starts;     // [3][n]: first tile of each entry in a product of each kind
+  float4* parts;             // sums of the parts of cut tiles
   int64_t tiles;             // of all products
-  int32_t triangles, fulls;  // of a product of the first two kinds, of the third
+  int32_t count[3];          // of a product of each kind
   int32_t steps;
   uint32_t inject;           // test hook: added to what a tile waits for
   float coef[ZERO_MUON_MAX_STEPS][3];
@@ -67,7 +72,9 @@ struct Products {
 
 struct Tile {
   Entry e;
-  int entry, b, step, which, i, j, unit, depth;
+  int entry, b, step, which, i, j, unit;
+  int from, depth;           // the depth's part: from.. up to depth
+  int splits, part, cut, slot;   // parts of the tile, which this is, its counter, its first part's place
   uint32_t need;             // finished CTA tiles of the matrix that it waits for
 };
 
@@ -76,12 +83,12 @@ constexpr int kProductSmem = kStages * kStageBytes + kPatchBytes + kDiagBytes + 
 template <int kPair>
 __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int lane, Tile* out) {
   constexpr int kTile = 128 * kPair;
-  const int per = 2 * p.triangles + p.fulls;
+  const int per = p.count[0] + p.count[1] + p.count[2];
   const int step = (int)(index / per);
   int r = (int)(index - (int64_t)step * per);
-  const int which = r < p.triangles ? 0 : r < 2 * p.triangles ? 1 : 2;
-  r -= which * p.triangles;
-  const int32_t* at = p.starts + (which == 2 ? p.c.n : 0);
+  const int which = r < p.count[0] ? 0 : r < p.count[0] + p.count[1] ? 1 : 2;
+  r -= (which > 0 ? p.count[0] : 0) + (which > 1 ? p.count[1] : 0);
+  const int32_t* at = p.starts + which * p.c.n;
   int lo = 0, hi = p.c.n;                  // the last entry that starts at or before r
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -96,6 +103,8 @@ __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int la
   const Entry& e = out->e;
   const int nk = (e.k + kTile - 1) / kTile, nr = (e.rows + kTile - 1) / kTile, nc = (e.cols + kTile - 1) / kTile;
   const int ntri = nk * (nk + 1) / 2, nfull = nr * nc;
+  const int splits = which == 0 ? e.splits : 1, part = r % splits;
+  r /= splits;
   const int each = which == 2 ? nfull : ntri;
   const int b = r / each;
   r %= each;
@@ -118,7 +127,13 @@ __device__ __forceinline__ void tile_at(const Products& p, int64_t index, int la
     out->i = i;
     out->j = j;
     out->unit = e.unit0 + b;
-    out->depth = which == 0 ? e.l : e.k;
+    const int depth = which == 0 ? e.l : e.k, stages = ((depth + kDepth - 1) / kDepth + splits - 1) / splits;
+    out->from = part * stages * kDepth;
+    out->depth = min(depth, (part + 1) * stages * kDepth);
+    out->splits = splits;
+    out->part = part;
+    out->cut = e.cut0 + b * e.cuts + r * kPair;
+    out->slot = e.slot0 + (b * ntri + r) * splits;
     const uint32_t need = (uint32_t)kPair * ((uint32_t)step * (2 * ntri + nfull) +
                                    (which == 0 ? 0u : which == 1 ? (uint32_t)ntri : 2u * ntri));
     out->need = need ? need + p.inject : 0u;
@@ -192,12 +207,13 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // (`cols`), and the next columns' numbers are on their way while those before
 // are worked on.  The loops are kept short: a small matrix runs each of them
 // once a tile, and straight code of 64 columns waited on instruction fetches
-// longer than it ran (64x64: 91 us).  False: a wait ran out.
+// longer than it ran (64x64: 91 us).
+enum Outcome { kFailed, kDone, kPart };   // a wait ran out; the tile is done; a part of it is
 template <int kPair>
-__device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool ready, uint32_t told, uint32_t number,
+__device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bool ready, uint32_t told, uint32_t number,
                                          uint32_t acc, uint32_t full_bar,
                                          uint32_t phase, uint32_t empty_bar, int warp, int lane, uint32_t rank,
-                                         float* patch, float* cols) {
+                                         float* patch, float* cols, volatile int* arrived) {
   constexpr int kTile = 128 * kPair;
   const Entry& en = t.e;
   const int rows = en.rows, ncols = en.cols, k = en.k, tall = en.tall;
@@ -234,7 +250,8 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       fetch(part * 16);
       const int c = warp * 32 + lane;
       float d = 0.0f;
-      if (c < kTile && col0 + c < N) d = __ldcg(diag + col0 + c);
+      // the columns are A's, but those of a wide matrix's X
+      if (c < kTile && col0 + c < N && (t.which == 1 || tall)) d = __ldcg(diag + col0 + c);
       if (row < M && (t.which == 1 || !tall)) di = __ldcg(diag + row);
       // b A + c A A: c d_j; X: e_j of a tall matrix
       if (c < kTile) cols[c] = t.which == 1 ? __fmul_rn(cc, d) : __fmul_rn(d, __fmaf_rn(cc, d, cb));
@@ -249,21 +266,68 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       : "=r"(ok)
       : "r"(ok), "r"(32 * kEpiWarps)
       : "memory");
-  if (!ok) return false;
+  if (!ok) return kFailed;
   tc_fence_after();
 
   const uint32_t lanes = acc + ((uint32_t)(quarter * 32) << 16);
   // the row's share of b A + c A A's factor, or e_i of a wide matrix
   const float ei = t.which == 1 ? __fmaf_rn(cc, di, cb) : __fmul_rn(di, __fmaf_rn(cc, di, cb));
+  // the accumulator may be written again once both CTAs have read it
+  const auto release = [&] {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(kPair == 2 ? peer(empty_bar, 0) : empty_bar);
+  };
   float next[16];
   if (part * 16 < ncol) tmem_load16(lanes + part * 16, next);
+  const bool cut = t.splits > 1;
+  // four columns of the tile's 128 rows of this CTA side by side
+  const int slot_size = kTile / 4 * 128;
+  float4* sums = p.parts + ((int64_t)t.slot * kPair + rank) * slot_size + quarter * 32 + lane;
+  if (cut) {
+    float4* own = sums + (int64_t)t.part * kPair * slot_size;
+#pragma unroll 1
+    for (int c = part * 16; c < ncol; c += kNext) {
+      tmem_load_wait();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) __stcg(own + (c / 4 + q) * 128, reinterpret_cast<const float4*>(next)[q]);
+      if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
+    }
+    release();
+    asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
+    if (warp == 0 && lane == 0) {
+      __threadfence();
+      uint32_t* counter = p.c.cut + t.cut + rank;
+      const bool all = atomicAdd(counter, 1u) == (uint32_t)t.splits - 1;
+      if (all) *counter = 0u;
+      __threadfence();
+      *arrived = all;
+    }
+    asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
+    if (!*arrived) return kPart;
+  }
 #pragma unroll 1
   for (int c = part * 16; c < ncol; c += kNext) {
     float v[16];
-    tmem_load_wait();
+    if (cut) {
 #pragma unroll
-    for (int q = 0; q < 16; ++q) v[q] = next[q];
-    if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
+      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+#pragma unroll 2
+      for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 y = __ldcg(sums + (int64_t)s * kPair * slot_size + (c / 4 + q) * 128);
+          v[4 * q] = __fadd_rn(v[4 * q], y.x);
+          v[4 * q + 1] = __fadd_rn(v[4 * q + 1], y.y);
+          v[4 * q + 2] = __fadd_rn(v[4 * q + 2], y.z);
+          v[4 * q + 3] = __fadd_rn(v[4 * q + 3], y.w);
+        }
+    } else {
+      tmem_load_wait();
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = next[q];
+      if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
+    }
     float2* y = reinterpret_cast<float2*>(v);
     if (t.which == 0) {
       const int at = row - (col0 + c);         // the diagonal's place, if in these columns
@@ -316,11 +380,8 @@ __device__ __forceinline__ bool epilogue(const Products& p, const Tile& t, bool 
       to[c * 4 + q * 32] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
                                       pack(y[4 * q + 2].x, y[4 * q + 2].y), pack(y[4 * q + 3].x, y[4 * q + 3].y));
   }
-  // the accumulator may be written again once both CTAs have read it
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive_cluster(kPair == 2 ? peer(empty_bar, 0) : empty_bar);
-  return true;
+  if (!cut) release();
+  return kDone;
 }
 
 template <int kPair>
@@ -340,6 +401,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                  known = tmem_at + 4,      // tiles that are in the ring
                  told = known + 4,         // and whose needs are met
                  counted = told + 4;       // tiles whose writes the counting warp has seen
+  // [0] the epilogue gave up, [1] its tile's parts have all arrived, [2], [3] the tile is only a part
   volatile int* const stop = reinterpret_cast<volatile int*>(small + (counted - full) + 4);
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
   const uint32_t rank = kPair == 2 ? cluster_rank() : 0;
@@ -375,6 +437,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // together; one lane issues.
     const int side = warp == 3;
     uint32_t s = 0, phase = 1, issued = 0;
+    uint32_t fenced = 0;                   // maps of the first eight entries that have been
     bool ok = true;
     for (uint32_t n = 0; ok && n < mine; ++n) {
       Tile& t = slots[n % kSlots];
@@ -387,10 +450,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       const Side how = side_of(t.e, t.which, side), other = side_of(t.e, t.which, side ^ 1);
       const CUtensorMap* map = p.maps + 4 * t.entry + (how == kSymmetric ? 1 + t.which : t.step & 1);
+      const int which_map = (int)(map - p.maps);
+      if (which_map >= 32 || !(fenced >> which_map & 1)) {
+        tma_map_fence(map);
+        if (which_map < 32) fenced |= 1u << which_map;
+      }
       const int m0 = (side ? t.j : t.i) * kTile, at = uniform(m0 + (int)rank * 128);
       const int turn = uniform(across_from<kPair>(how, m0));
       const int other_turn = uniform(across_from<kPair>(other, (side ? t.i : t.j) * kTile));
-      const int depth = uniform(t.depth), b = uniform(t.b);
+      const int from = uniform(t.from), depth = uniform(t.depth), b = uniform(t.b);
       const uint32_t need = t.need;
       // each waits for the device's count itself: a shared word between them
       // would be one more step before the first load
@@ -399,7 +467,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (!ok) break;
         fence_proxy_async();
       }
-      for (int k0 = 0; k0 < depth; k0 += kDepth) {
+      for (int k0 = from; k0 < depth; k0 += kDepth) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));
         if (!ok) break;
         const uint32_t bar = kPair == 2 ? peer(full + 8 * s, 0) : full + 8 * s;
@@ -415,7 +483,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, 0, down, right + 8, b);
         }
         __syncwarp();
-        if (side == 0 && k0 == 0 && lane == 0) shared_set(told, n + 1);
+        if (side == 0 && k0 == from && lane == 0) shared_set(told, n + 1);
         ++issued;
         if (++s == kStages) { s = 0; phase ^= 1; }
       }
@@ -446,12 +514,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const Tile& t = slots[n % kSlots];
       const int ta = uniform(across_from<kPair>(side_of(t.e, t.which, 0), t.i * kTile));
       const int tb = uniform(across_from<kPair>(side_of(t.e, t.which, 1), t.j * kTile));
-      const int depth = uniform(t.depth);
+      const int from = uniform(t.from), depth = uniform(t.depth);
       ok = __all_sync(0xffffffffu, mbar_wait(acc_empty + 8 * acc, acc_phase, fault));
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + acc * kTile;
-      for (int k0 = 0; k0 < depth; k0 += kDepth) {
+      for (int k0 = from; k0 < depth; k0 += kDepth) {
         const bool xa = k0 >= ta, xb = k0 >= tb;
         const uint32_t idesc = instruction(kTile, kTile, xa, xb);
         const uint32_t at = stages + s * kStageBytes;
@@ -469,7 +537,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int q = q0; q < q0 + 4; ++q) {
               // 16 deep: two pieces, or sixteen rows
               const uint32_t along = q * 2 * kPieceBytes >> 4, down = q * 2 * 128 >> 4;
-              mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > 0 || q > 0);
+              mma_f16<kPair>(d, da + (xa ? down : along), db + (xb ? down : along), idesc, k0 > from || q > 0);
             }
           };
           four(0);
@@ -496,9 +564,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // the tile before the last is counted: its barrier is free again
       bool ok = shared_wait(known, n + 1, fault) && (n < 2 || shared_wait(counted, n - 1, fault));
       ok = __all_sync(0xffffffffu, ok);
-      ok = epilogue<kPair>(p, slots[n % kSlots], ok, told, n, tmem + acc * kTile, acc_full + 8 * acc, phase,
-                           acc_empty + 8 * acc, warp - 4, lane, rank, patch, cols + acc * 256);
+      const Outcome is = epilogue<kPair>(p, slots[n % kSlots], ok, told, n, tmem + acc * kTile, acc_full + 8 * acc, phase,
+                           acc_empty + 8 * acc, warp - 4, lane, rank, patch, cols + acc * 256, stop + 1);
+      ok = is != kFailed;
       if (!ok) *stop = 1;
+      if (warp == 4 && lane == 0) stop[2 + acc] = is == kPart;
       // the tile's writes are made: warp 2 counts it
       asm volatile("barrier.arrive %0, %1;" ::"r"(2 + acc), "r"(32 * kEpiWarps + 32) : "memory");
       if (!ok) break;
@@ -512,8 +582,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (*stop) break;
       if (lane == 0) {
         const uint32_t unit = (uint32_t)slots[n % kSlots].unit;
+        const bool whole = !stop[2 + n % 2];
         shared_set(counted, n + 1);
-        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + unit) : "memory");
+        if (whole) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.c.done + unit) : "memory");
       }
       __syncwarp();
     }

@@ -144,6 +144,13 @@ __device__ __forceinline__ void fence_proxy_async() {
 // ---- TMA: a box of an array of four dimensions.  x must be a multiple of 16
 // bytes.  With a pair the barrier may be the other CTA's.
 
+// A map in global memory that was written before the launch: what this SM may
+// hold of another map that lay there is not used for it.  Needed in every block
+// before the map's first use.
+__device__ __forceinline__ void tma_map_fence(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.sys [%0], 128;" ::"l"(map) : "memory");
+}
+
 template <int kPair>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                          int w) {
