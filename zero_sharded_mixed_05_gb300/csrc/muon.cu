@@ -340,14 +340,14 @@ typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, v
                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                 CUtensorMapFloatOOBfill);
 
-// Map of a matrix in blocks (muon_kernels.cuh), [batch] of them: runs of 32
-// rows of a piece, rows of blocks, pieces across, matrices.  A box is 128 rows
-// of eight pieces; what lies outside reads as zero.
+// Map of a matrix in pieces (muon_kernels.cuh), [batch] of them: a quarter of a
+// piece's 128 rows, the quarters, pieces across, rows of pieces, matrices.  A
+// box is 128 rows of eight pieces; what lies outside reads as zero.
 bool encode(EncodeTiled fn, CUtensorMap* map, __half* p, int64_t rows, int64_t ld, int64_t batch) {
-  const cuuint64_t dim[4] = {256, (cuuint64_t)(rows + 31) / 32, (cuuint64_t)ld / 8, (cuuint64_t)batch};
-  const cuuint64_t stride[3] = {(cuuint64_t)ld * 64, 512, (cuuint64_t)zm::block_size(rows, ld) * 2};
-  const cuuint32_t box[4] = {256, 4, 8, 1}, step[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, p, dim, stride, box, step,
+  const cuuint64_t dim[5] = {256, 4, (cuuint64_t)ld / 8, (cuuint64_t)(rows + 127) / 128, (cuuint64_t)batch};
+  const cuuint64_t stride[4] = {512, 2048, (cuuint64_t)ld * 256, (cuuint64_t)zm::block_size(rows, ld) * 2};
+  const cuuint32_t box[5] = {256, 4, 8, 1, 1}, step[5] = {1, 1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, p, dim, stride, box, step,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -417,7 +417,6 @@ cudaError_t place(zero_muon_t h) {
   const int64_t io = lay.take(n * sizeof(zm::Io)), first = lay.take(starts.size() * sizeof(int32_t));
   const int64_t part = lay.take(h->chunks * sizeof(double)), ticket = lay.take(units * 4),
                 inv = lay.take(units * 4), done = lay.take(units * 4), cut = lay.take(cuts * 4ll);
-  const int64_t cleared = lay.size;
   const int64_t parts = lay.take((int64_t)slots * h->pair * 128 * tile * 4);
   std::vector<int64_t> at;
   for (const zm::Entry& e : h->entries) {
@@ -449,7 +448,8 @@ cudaError_t place(zero_muon_t h) {
                     encode(fn, m + 2, en.a, en.k, en.ldk, en.batch) && encode(fn, m + 3, en.b, en.k, en.ldk, en.batch);
     if (!ok) return cudaErrorInvalidValue;
   }
-  e = cudaMemset(h->mem, 0, (size_t)cleared);
+  // counters, and what pads the matrices
+  e = cudaMemset(h->mem, 0, (size_t)h->bytes);
   const auto copy = [&](int64_t to, const void* from, size_t bytes) {
     if (e == cudaSuccess && bytes > 0)
       e = cudaMemcpy(h->mem + to, from, bytes, cudaMemcpyHostToDevice);

@@ -49,18 +49,18 @@ struct Entry {
   float s;                   // scale_rule's factor
 };
 
-// Every matrix of the workspace is in blocks of 32 x 32 binary16 numbers: eight
-// columns of a row are a piece of 16 bytes, the pieces of the block's 32 rows
-// lie side by side, then the next eight columns'.  One layout serves all: an
-// epilogue thread that holds a row reads and writes whole lines together with
-// its warp (by rows of a row-major array it would touch a line a thread); eight
-// pieces are the tensor core's 8 x 16-byte core matrix, for the depth along
-// the rows as well as down them; and TMA brings 512 bytes a run.  What pads a
-// matrix to whole blocks is zero.
+// Every matrix of the workspace is in pieces: eight columns of a row are 16
+// bytes, the pieces of 128 rows lie side by side, then the next eight columns'
+// of the same rows, then the next 128 rows.  One layout serves all: an
+// epilogue warp whose threads hold a row each reads and writes whole lines (by
+// rows of a row-major array it would touch a line a thread); eight rows of a
+// piece are the tensor core's 8 x 16-byte core matrix, for the depth along the
+// rows as well as down them; and TMA brings 2 KB a run.  What pads a matrix to
+// 128 rows and 32 columns is zero.
 __host__ __device__ inline int64_t block_at(int row, int col, int64_t ld) {
-  return (row / 32 * (ld / 32) + col / 32) * 1024 + col % 32 / 8 * 256 + row % 32 * 8;
+  return (row / 128 * (ld / 8) + col / 8) * 1024 + row % 128 * 8;
 }
-__host__ __device__ inline int64_t block_size(int64_t rows, int64_t ld) { return (rows + 31) / 32 * 32 * ld; }
+__host__ __device__ inline int64_t block_size(int64_t rows, int64_t ld) { return (rows + 127) / 128 * 128 * ld; }
 
 // What a call was given for one entry.
 struct Io {

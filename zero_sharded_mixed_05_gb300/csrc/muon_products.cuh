@@ -240,8 +240,8 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
     if (t.which == 0 || c >= ncol) return;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      hi[q] = __ldcg(from + c * 4 + q * 32);
-      if (t.which == 2) lo[q] = __ldcg(low + c * 4 + q * 32);
+      hi[q] = __ldcg(from + c * 16 + q * 128);
+      if (t.which == 2) lo[q] = __ldcg(low + c * 16 + q * 128);
     }
   };
   if (t.which != 0) {
@@ -370,14 +370,14 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
       for (int q = 0; q < 8; ++q) split(y[q], &first[q], &second[q]);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        to[c * 4 + q * 32] = reinterpret_cast<const uint4*>(first)[q];
-        low[c * 4 + q * 32] = reinterpret_cast<const uint4*>(second)[q];
+        to[c * 16 + q * 128] = reinterpret_cast<const uint4*>(first)[q];
+        low[c * 16 + q * 128] = reinterpret_cast<const uint4*>(second)[q];
       }
       continue;
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q)
-      to[c * 4 + q * 32] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
+      to[c * 16 + q * 128] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
                                       pack(y[4 * q + 2].x, y[4 * q + 2].y), pack(y[4 * q + 3].x, y[4 * q + 3].y));
   }
   if (!cut) release();
@@ -478,9 +478,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (elected()) {
           if (rank == 0 && side == 0)
             mbar_expect(full + 8 * s, kPair * kBoxBytes * (2 + (both || x) + (both || k0 >= other_turn)));
-          const int down = (x ? k0 : at) / 32, right = (x ? at : k0) / 8;   // rows of blocks, pieces
-          tma_load<kPair>(to, map, bar, 0, down, right, b);
-          if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, 0, down, right + 8, b);
+          const int down = (x ? k0 : at) / 128, right = (x ? at : k0) / 8;
+          tma_load<kPair>(to, map, bar, right, down, b);
+          if (both || x) tma_load<kPair>(to + kBoxBytes, map, bar, right + 8, down, b);
         }
         __syncwarp();
         if (side == 0 && k0 == from && lane == 0) shared_set(told, n + 1);
