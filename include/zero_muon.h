@@ -119,10 +119,11 @@ zero_status zero_muon_config_default(zero_muon_config* cfg);
 /* Make a handle for n shapes (n = 0..ZERO_MUON_MAX_SHAPES) and its workspace:
  * about 6 bytes per element of the matrices, their rows rounded up to 128, and
  * 4 per element of the k x k products (almost nothing where every matrix has a
- * side of at most 128 and the other of at most 2048 and stays on the chip).  Errors: EINVAL (NULL pointers, a field outside its range),
- * ERANGE (n or a shape beyond the limits above), ENOMEM, ECUDA.  *out is NULL
- * on failure.  Without a CUDA device the handle is created and every
- * launching call returns ZERO_ECUDA. */
+ * side of at most 128 and the other of at most 2048 and stays on the chip).
+ * Errors: EINVAL (NULL pointers, a field outside its range), ERANGE (n or a
+ * shape beyond the limits above), ENOMEM, ECUDA.  *out is NULL on failure.
+ * Without a CUDA device the handle is created and every launching call
+ * returns ZERO_ECUDA. */
 zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape* shapes,
                              int32_t n, zero_muon_t* out);
 zero_status zero_muon_destroy(zero_muon_t h);

@@ -122,11 +122,13 @@ cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cud
 }
 
 // Parts that the depth of X X^T (`stages` of 128) is cut into, so that `tiles`
-// tiles of it keep `slots` CTAs or pairs busy: each at least four stages deep,
-// below which the adding up costs what it saves.
+// tiles of it keep `slots` CTAs or pairs busy.  Each is at least eight stages
+// deep and there are three at least, or the adding up costs what it saves
+// (whole against cut: 8080x80 x 2 180 and 121 us, 300x5000 160 and 136; in two
+// 1024x4096 x 2 238 and 246, of four stages 400x1800 x 4 130 and 142).
 int32_t splits_of(int64_t tiles, int64_t slots, int32_t stages) {
-  const int64_t want = std::min<int64_t>({slots / std::max<int64_t>(tiles, 1), stages / 4, 16});
-  if (want < 2) return 1;
+  const int64_t want = std::min<int64_t>({slots / std::max<int64_t>(tiles, 1), stages / 8, 8});
+  if (want < 3) return 1;
   const int32_t deep = (int32_t)((stages + want - 1) / want);
   return (stages + deep - 1) / deep;
 }

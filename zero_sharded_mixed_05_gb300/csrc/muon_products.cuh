@@ -312,7 +312,7 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
     if (cut) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) v[q] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
       for (int s = 0; s < t.splits; ++s)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
