@@ -534,7 +534,6 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
       e.ldx = (s.cols + 31) / 32 * 32;
       e.ldk = (e.k + 31) / 32 * 32;
       e.across = (int32_t)(e.ldx / 32);
-      e.chunks = (int32_t)(((s.rows + 31) / 32 * e.across + zm::kChunk - 1) / zm::kChunk);
       e.s = (float)(cfg->scale_rule == ZERO_MUON_SCALE_RMS ? 0.2 * std::sqrt((double)e.l)
                     : cfg->scale_rule == ZERO_MUON_SCALE_ASPECT
                         ? std::sqrt(std::max(1.0, (double)s.rows / (double)s.cols))
@@ -545,8 +544,16 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
     std::stable_sort(h->entries.begin(), h->entries.end(), [](const zm::Entry& x, const zm::Entry& y) {
       return x.k != y.k ? x.k > y.k : x.l > y.l;
     });
+    // Blocks a warp of the first two stages: one wave of CTAs, three an SM, up
+    // to 8.  (Twelve of 2304x768: 378 us at one block and two waves, 362 at
+    // two and one; 14336x4096: 2646 at 16 blocks, 2607 at 8.)
+    int64_t blocks = 0;
+    for (const zm::Entry& e : h->entries) blocks += (int64_t)e.batch * ((e.rows + 31) / 32) * e.across;
+    h->call.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, (blocks + 8 * 152 * 3 - 1) / (8 * 152 * 3)));
+    const int64_t chunk = h->call.blocks * (zm::kThreads / 32);
     double tiles = 0;
     for (zm::Entry& e : h->entries) {
+      e.chunks = (int32_t)(((int64_t)(e.rows + 31) / 32 * e.across + chunk - 1) / chunk);
       e.unit0 = (int32_t)units;
       e.chunk0 = (int32_t)h->chunks;
       units += e.batch;

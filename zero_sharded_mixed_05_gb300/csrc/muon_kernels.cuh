@@ -22,8 +22,6 @@ namespace zm {
 constexpr int kThreads = 256;
 constexpr int kMaxEntries = ZERO_MUON_MAX_SHAPES;
 constexpr int kVec = 8;                        // numbers of a thread's vector in the first two stages
-constexpr int kPasses = 8;                     // vectors of a thread
-constexpr int kChunk = kThreads * kPasses * kVec / 1024;   // blocks of 32 x 32 numbers of a CTA
 
 // A and B are held times 4096 and X times 64, so that a product of X by itself
 // has A's scale (zero_muon.h).
@@ -78,7 +76,8 @@ struct Workspace {
 
 struct Call {
   const Entry* entries;
-  int32_t n, step;           // step: 1 zero_muon_step, 0 zero_muon_orthogonalize
+  int32_t n, blocks;         // entries; blocks of 32 x 32 a warp in the first two stages
+  int32_t step;              // step: 1 zero_muon_step, 0 zero_muon_orthogonalize
   Workspace* ws;
   double* part;              // sums of squares, one a CTA of the first stage
   unsigned* ticket;          // one a matrix, zero between calls
@@ -117,9 +116,11 @@ __device__ __forceinline__ float grad_factor(const Call& c) {
   return c.decision ? __fmul_rn(c.grad_scale, c.decision->coef) : c.grad_scale;
 }
 
-// What a CTA of the first two stages works on.  A warp's pass is 8 rows of a
-// block of 32 x 32: four threads a row, so that a row's 32 numbers are whole
-// sectors in every array, and so are the block's pieces of 8 rows.
+// What a CTA of the first two stages works on, call.blocks times 8192 numbers:
+// stage 1 in the order of the rows (blocks of rows 64 bytes wide read at half
+// the rate), stage 2 in blocks of 32 x 32 a warp, four threads a row, so that
+// X's pieces are written as whole sectors.  A thread's four vectors are on
+// their way at once.
 struct Part {
   int entry, b, chunk;       // matrix b of the entry, CTA `chunk` of the matrix
 };
@@ -135,43 +136,82 @@ __device__ __forceinline__ Part part_of(const Call& c, int cta) {
   const int at = cta - e.chunk0;
   return {found, at / e.chunks, at % e.chunks};
 }
-// Row and first column of a thread's vector of a pass; false: not in the blocks.
-__device__ __forceinline__ bool place(const Entry& e, int chunk, int pass, int* row, int* col) {
-  const int64_t blk = (int64_t)chunk * kChunk + pass / 4 * (kThreads / 32) + threadIdx.x / 32;
-  const int down = (int)(blk / e.across), right = (int)(blk - (int64_t)down * e.across);
-  *row = down * 32 + pass % 4 * 8 + threadIdx.x % 32 / 4;
-  *col = right * 32 + threadIdx.x % 4 * kVec;
-  return down * 32 < e.rows;
+
+// A thread's four vectors of eight columns: their rows, first columns, and how
+// many of the eight are in the matrix (0: the vector is padding).
+struct Place {
+  int row[4], col[4], n[4];
+};
+// In a block of 32 x 32 a warp: rows eight apart.  False: past the last block.
+__device__ __forceinline__ bool place_block(const Call& c, const Entry& e, int chunk, int i, Place* p) {
+  const uint32_t blk = (uint32_t)(chunk * c.blocks + i) * (kThreads / 32) + threadIdx.x / 32;
+  const uint32_t down = blk / (uint32_t)e.across, right = blk - down * e.across;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    p->row[q] = (int)down * 32 + 8 * q + threadIdx.x % 32 / 4;
+    p->col[q] = (int)right * 32 + threadIdx.x % 4 * kVec;
+    p->n[q] = p->row[q] < e.rows ? min(kVec, max(e.cols - p->col[q], 0)) : 0;
+  }
+  return (int)down * 32 < e.rows;
+}
+// In the order of the rows, kThreads vectors apart.
+__device__ __forceinline__ bool place_flat(const Call& c, const Entry& e, int chunk, int i, Place* p) {
+  const uint32_t vpr = (uint32_t)(e.cols + kVec - 1) / kVec;      // vectors a row
+  const uint32_t first = (uint32_t)(chunk * c.blocks + i) * (4 * kThreads);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t v = first + q * kThreads + threadIdx.x, row = v / vpr;
+    p->row[q] = (int)min(row, (uint32_t)e.rows);
+    p->col[q] = (int)(v - row * vpr) * kVec;
+    p->n[q] = p->row[q] < e.rows ? min(kVec, e.cols - p->col[q]) : 0;
+  }
+  return first < vpr * (uint32_t)e.rows;
 }
 
-// Eight numbers of a row (fewer at its end, the rest zero) from p.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float* x) {
-  if (vec && n == kVec) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const T* t = reinterpret_cast<const T*>(&u);
+// The numbers there of an array with its rows `ld` apart, p at the matrix's
+// first; zero where there are none.  kWhole: every vector is whole and aligned,
+// or padding.
+template <bool kWhole, typename T>
+__device__ __forceinline__ void load_at(const T* p, int64_t ld, const Place& at, float x[4][kVec]) {
+  if constexpr (kWhole) {
+    constexpr int kWords = kVec * (int)sizeof(T) / 16;
+    uint4 raw[4][kWords];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) x[i] = num<T>(t[i]);
-    } else {
-      const float4 u = reinterpret_cast<const float4*>(p)[0], v = reinterpret_cast<const float4*>(p)[1];
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-    }
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) {
+        raw[q][w] = make_uint4(0, 0, 0, 0);
+        if (at.n[q] > 0) raw[q][w] = reinterpret_cast<const uint4*>(p + at.row[q] * ld + at.col[q])[w];
+      }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) x[q][j] = num<T>(reinterpret_cast<const T*>(raw[q])[j]);
   } else {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) x[i] = i < n ? num<T>(p[i]) : 0.0f;
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        x[q][j] = 0.0f;
+        if (j < at.n[q]) x[q][j] = num<T>(p[at.row[q] * ld + at.col[q] + j]);
+      }
   }
 }
 
-__device__ __forceinline__ void store8(float* p, int n, bool vec, const float* x) {
-  if (vec && n == kVec) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-  } else {
+template <bool kWhole>
+__device__ __forceinline__ void store_at(float* p, int64_t ld, const Place& at, const float x[4][kVec]) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i)
-      if (i < n) p[i] = x[i];
+  for (int q = 0; q < 4; ++q) {
+    float* to = p + at.row[q] * ld + at.col[q];
+    if constexpr (kWhole) {
+      if (at.n[q] == 0) continue;
+      reinterpret_cast<float4*>(to)[0] = make_float4(x[q][0], x[q][1], x[q][2], x[q][3]);
+      reinterpret_cast<float4*>(to)[1] = make_float4(x[q][4], x[q][5], x[q][6], x[q][7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVec; ++j)
+        if (j < at.n[q]) to[j] = x[q][j];
+    }
   }
 }
 
@@ -180,17 +220,59 @@ __device__ __forceinline__ bool aligned(const void* p, int64_t row, int64_t batc
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && row % m == 0 && batch % m == 0;
 }
 
-// U of eight numbers for the step, from the gradient and the momentum; `mom`
-// holds the old momentum and gets the new one (kNew), or holds the new one.
-template <bool kNew>
-__device__ __forceinline__ void update_of(const Call& c, float f, const float* g, float* mom, float* u) {
+// What U of a matrix is made from.
+template <typename T>
+struct Source {
+  const T* in;
+  float* mom;                // the step's
+  int64_t in_row;
+  bool whole;                // all of their vectors are whole and aligned
+  float f;
+  __device__ __forceinline__ Source(const Call& c, const Entry& e, const Io& io, int b)
+      : in(static_cast<const T*>(io.in) + (int64_t)b * io.in_batch),
+        mom(c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr),
+        in_row(io.in_row),
+        whole(e.cols % kVec == 0 && aligned(io.in, io.in_row, io.in_batch, sizeof(T)) &&
+              (!c.step || aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4))),
+        f(grad_factor(c)) {}
+  // U of a thread's vectors.  kNew: `mom` holds the old momentum and gets the
+  // new one; else it holds the new one.
+  template <bool kNew, bool kWhole>
+  __device__ __forceinline__ void read(const Call& c, const Entry& e, const Place& at, float u[4][kVec]) const {
+    load_at<kWhole, T>(in, in_row, at, u);
+    if (!c.step) return;
+    float m[4][kVec];
+    load_at<kWhole, float>(mom, e.cols, at, m);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const float gi = __fmul_rn(g[i], f);
-    if (kNew) mom[i] = __fadd_rn(__fmul_rn(c.mu, mom[i]), gi);
-    u[i] = c.nesterov ? __fadd_rn(gi, __fmul_rn(c.mu, mom[i])) : mom[i];
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const float g = __fmul_rn(u[q][j], f);
+        if (kNew) m[q][j] = __fadd_rn(__fmul_rn(c.mu, m[q][j]), g);
+        u[q][j] = c.nesterov ? __fadd_rn(g, __fmul_rn(c.mu, m[q][j])) : m[q][j];
+      }
+    if (kNew) store_at<kWhole>(mom, e.cols, at, m);
   }
-}
+  // Walks a CTA's vectors.
+  template <bool kNew, typename Where, typename Work>
+  __device__ __forceinline__ void walk(const Call& c, const Entry& e, int chunk, Where where, Work work) const {
+    Place at;
+    float u[4][kVec];
+    if (whole) {
+#pragma unroll 1
+      for (int i = 0; i < c.blocks && where(c, e, chunk, i, &at); ++i) {
+        read<kNew, true>(c, e, at, u);
+        work(at, u);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < c.blocks && where(c, e, chunk, i, &at); ++i) {
+        read<kNew, false>(c, e, at, u);
+        work(at, u);
+      }
+    }
+  }
+};
 
 // x as the sum of two binary16 numbers, the second times kLoScale.
 __device__ __forceinline__ void split(float2 x, __half2* hi, __half2* lo) {
@@ -199,16 +281,20 @@ __device__ __forceinline__ void split(float2 x, __half2* hi, __half2* lo) {
   *lo = __floats2half2_rn(__fmul_rn(__fadd_rn(x.x, -h.x), kLoScale), __fmul_rn(__fadd_rn(x.y, -h.y), kLoScale));
 }
 
-// Writes a vector of X.
-__device__ __forceinline__ void put_x(const Entry& e, int b, int row, int col, const float* u, float inv) {
-  __align__(16) __half2 hi[kVec / 2], lo[kVec / 2];
+// Writes a thread's vectors of X, padding and all.
+__device__ __forceinline__ void put_x(const Entry& e, int b, const Place& p, const float u[4][kVec], float inv) {
+  const int64_t at = (int64_t)b * block_size(e.rows, e.ldx) + block_at(p.row[0], p.col[0], e.ldx);
 #pragma unroll
-  for (int j = 0; j < kVec / 2; ++j)
-    split(make_float2(__fmul_rn(__fmul_rn(u[2 * j], inv), kScaleX), __fmul_rn(__fmul_rn(u[2 * j + 1], inv), kScaleX)),
-          &hi[j], &lo[j]);
-  const int64_t at = (int64_t)b * block_size(e.rows, e.ldx) + block_at(row, col, e.ldx);
-  *reinterpret_cast<uint4*>(e.x[0] + at) = *reinterpret_cast<const uint4*>(hi);
-  *reinterpret_cast<uint4*>(e.lo + at) = *reinterpret_cast<const uint4*>(lo);
+  for (int q = 0; q < 4; ++q) {
+    __align__(16) __half2 hi[kVec / 2], lo[kVec / 2];
+#pragma unroll
+    for (int j = 0; j < kVec / 2; ++j)
+      split(make_float2(__fmul_rn(__fmul_rn(u[q][2 * j], inv), kScaleX), __fmul_rn(__fmul_rn(u[q][2 * j + 1], inv), kScaleX)),
+            &hi[j], &lo[j]);
+    // 32 rows from a multiple of 32 on are within a piece's 128
+    *reinterpret_cast<uint4*>(e.x[0] + at + q * 64) = *reinterpret_cast<const uint4*>(hi);
+    *reinterpret_cast<uint4*>(e.lo + at + q * 64) = *reinterpret_cast<const uint4*>(lo);
+  }
 }
 
 __device__ __forceinline__ float inverse(double squares, double eps) { return (float)(1.0 / (sqrt(squares) + eps)); }
@@ -225,10 +311,9 @@ __device__ __forceinline__ void clear(const Call& c, const Entry& e, int b) {
 // beyond; the last CTA of a matrix adds the CTAs' sums in index order.  Of a
 // matrix that one CTA holds the numbers are still there: it writes X at once.
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_constant__ Start<N> s) {
+__global__ void __launch_bounds__(kThreads, 3) muon_stats_kernel(const __grid_constant__ Start<N> s) {
   const Call& c = s.c;
   __shared__ double red[kThreads / 32];
-  __shared__ int last;
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     c.ws->fault = 0;
     c.ws->skipped = skipped(c);
@@ -238,35 +323,18 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     for (int i = threadIdx.x; i < c.n; i += kThreads) c.io[i] = s.io[i];
   const Part part = part_of(c, blockIdx.x);
   const Entry& e = c.entries[part.entry];
-  const Io& io = s.io[e.item];
   const int b = part.b;
-  const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
-  float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
-  const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
-  const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
-  const float f = grad_factor(c);
+  const Source<T> from(c, e, s.io[e.item], b);
   const bool alone = e.chunks == 1;
   float sq = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < kPasses; ++i) {
-    int row, col;
-    if (!place(e, part.chunk, i, &row, &col)) continue;
-    const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
-    float x[kVec], u[kVec];
-    load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
-    if (c.step) {
-      float m[kVec];
-      float* pm = mom + (int64_t)row * e.cols + col;
-      load8<float>(pm, n, vmom, m);
-      update_of<true>(c, f, x, m, u);
-      store8(pm, n, vmom, m);
-    } else {
+  from.template walk<true>(c, e, part.chunk, place_flat, [&](const Place&, const float(&u)[4][kVec]) {
+    float two[2] = {0.0f, 0.0f};
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) u[j] = x[j];
-    }
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) sq = __fmaf_rn(u[j], u[j], sq);
-  }
+      for (int j = 0; j < kVec; ++j) two[j % 2] = __fmaf_rn(u[q][j], u[q][j], two[j % 2]);
+    sq = __fadd_rn(sq, __fadd_rn(two[0], two[1]));
+  });
   double d = sq;
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
   if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
@@ -277,43 +345,28 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
     for (int i = 0; i < kThreads / 32; ++i) d += red[i];
     const float inv = inverse(d, c.eps);
     if (threadIdx.x == 0) clear(c, e, b);
-#pragma unroll 2
-    for (int i = 0; i < kPasses; ++i) {      // again from L1 or L2
-      int row, col;
-      if (!place(e, 0, i, &row, &col)) continue;
-      const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
-      float x[kVec], u[kVec];
-      load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
-      if (c.step) {
-        float m[kVec];
-        load8<float>(mom + (int64_t)row * e.cols + col, n, vmom, m);
-        update_of<false>(c, f, x, m, u);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) u[j] = x[j];
-      }
-      put_x(e, b, row, col, u, inv);
-    }
+    // again from L1 or L2
+    from.template walk<false>(c, e, 0, place_block,
+                              [&](const Place& at, const float(&u)[4][kVec]) { put_x(e, b, at, u, inv); });
     return;
   }
+  // the first warp alone ends the CTA's work: the others make room
+  if (threadIdx.x >= 32) return;
   double* sums = c.part + e.chunk0 + (int64_t)b * e.chunks;
+  int last = 0;
   if (threadIdx.x == 0) {
     for (int i = 1; i < kThreads / 32; ++i) d += red[i];
     sums[part.chunk] = d;
     __threadfence();
     last = atomicAdd(&c.ticket[unit], 1u) == (unsigned)e.chunks - 1;
+    __threadfence();
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
   d = 0.0;
-  for (int i = threadIdx.x; i < e.chunks; i += kThreads) d += __ldcg(&sums[i]);
+#pragma unroll 8
+  for (int i = threadIdx.x; i < e.chunks; i += 32) d += __ldcg(&sums[i]);
   for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = d;
-  __syncthreads();
   if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) d += red[i];
     c.inv[unit] = inverse(d, c.eps);
     c.ticket[unit] = 0u;
     clear(c, e, b);
@@ -324,36 +377,17 @@ __global__ void __launch_bounds__(kThreads) muon_stats_kernel(const __grid_const
 // to the first's: stage 1 ended with the last, which L2 still holds, and the
 // products begin with the first.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) muon_start_kernel(const __grid_constant__ Call c) {
+__global__ void __launch_bounds__(kThreads, 3) muon_start_kernel(const __grid_constant__ Call c) {
   cudaGridDependencySynchronize();           // launched while stage 1 still runs
   if (skipped(c)) return;
   const Part part = part_of(c, gridDim.x - 1 - blockIdx.x);
   const Entry& e = c.entries[part.entry];
   if (e.chunks == 1) return;                 // stage 1 wrote it
-  const Io& io = c.io[e.item];
   const int b = part.b;
-  const T* in = static_cast<const T*>(io.in) + (int64_t)b * io.in_batch;
-  const float* mom = c.step ? io.mom + (int64_t)b * e.rows * e.cols : nullptr;
-  const bool vin = aligned(io.in, io.in_row, io.in_batch, sizeof(T));
-  const bool vmom = c.step && aligned(io.mom, e.cols, (int64_t)e.rows * e.cols, 4);
-  const float f = grad_factor(c), inv = c.inv[e.unit0 + b];
-#pragma unroll 4
-  for (int i = 0; i < kPasses; ++i) {
-    int row, col;
-    if (!place(e, part.chunk, i, &row, &col)) continue;
-    const int n = row < e.rows ? min(kVec, max(e.cols - col, 0)) : 0;   // 0: padding
-    float x[kVec], u[kVec];
-    load8<T>(in + (int64_t)row * io.in_row + col, n, vin, x);
-    if (c.step) {
-      float m[kVec];
-      load8<float>(mom + (int64_t)row * e.cols + col, n, vmom, m);
-      update_of<false>(c, f, x, m, u);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) u[j] = x[j];
-    }
-    put_x(e, b, row, col, u, inv);
-  }
+  const Source<T> from(c, e, c.io[e.item], b);
+  const float inv = c.inv[e.unit0 + b];
+  from.template walk<false>(c, e, part.chunk, place_block,
+                            [&](const Place& at, const float(&u)[4][kVec]) { put_x(e, b, at, u, inv); });
 }
 
 // R numbers of the result, every S-th row from `row` on: O itself, o(0).., or the
