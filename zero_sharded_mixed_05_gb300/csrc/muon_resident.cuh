@@ -14,7 +14,10 @@
 //       distributed shared memory (each number once, so that every CTA has
 //       the same bits), its diagonal kept in binary32 (muon_products.cuh);
 //   B = b A + c A A, in every CTA alike;   X <- a X + B H.
-// Measured: 64x64 53 -> %RES64% us, 32 of 128x1024 102 -> %RES128% us.
+// Measured, a call through the workspace and here: 64x64 53 and 25 us, 32 of
+// 128x1024 102 and 67 us.  A step is a chain of three products and their
+// epilogues, 4 us, and with a cluster's sums and barriers 11 us, in which the
+// tensor cores work for 7 % of the cycles.
 #pragma once
 
 #include "muon_products.cuh"

