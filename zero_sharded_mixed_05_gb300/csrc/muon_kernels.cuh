@@ -390,39 +390,4 @@ __global__ void __launch_bounds__(kThreads, 3) muon_start_kernel(const __grid_co
                             [&](const Place& at, const float(&u)[4][kVec]) { put_x(e, b, at, u, inv); });
 }
 
-// R numbers of the result, every S-th row from `row` on: O itself, o(0).., or the
-// step with it.
-template <int R, int S, typename F>
-__device__ __forceinline__ void finish(const Call& c, const Entry& e, const Io& io, int b, int row, int col, F o) {
-  if (!c.step) {
-    const int64_t at = (int64_t)b * io.out_batch + (int64_t)row * io.out_row + col;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t i = at + r * S * io.out_row;
-      if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[i] = as<__half>(o(r));
-      else if (c.out_type == ZERO_BF16) static_cast<__nv_bfloat16*>(io.out)[i] = as<__nv_bfloat16>(o(r));
-      else static_cast<float*>(io.out)[i] = o(r);
-    }
-    return;
-  }
-  const int64_t at = ((int64_t)b * e.rows + row) * e.cols + col;
-  float w[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t i = at + (int64_t)r * S * e.cols;
-    if (io.master) w[r] = io.master[i];
-    else if (c.out_type == ZERO_FP16) w[r] = num<__half>(static_cast<__half*>(io.out)[i]);
-    else w[r] = num<__nv_bfloat16>(static_cast<__nv_bfloat16*>(io.out)[i]);
-  }
-  const float step = -__fmul_rn(c.lr, e.s);
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t i = at + (int64_t)r * S * e.cols;
-    w[r] = __fmaf_rn(step, o(r), __fmul_rn(w[r], c.decay));
-    if (io.master) io.master[i] = w[r];
-    if (c.out_type == ZERO_FP16) static_cast<__half*>(io.out)[i] = as<__half>(w[r]);
-    else static_cast<__nv_bfloat16*>(io.out)[i] = as<__nv_bfloat16>(w[r]);
-  }
-}
-
 }  // namespace zm

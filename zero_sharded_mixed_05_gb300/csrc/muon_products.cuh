@@ -181,25 +181,48 @@ __device__ __forceinline__ uint4* piece(float* patch, int row, int at) {
   return reinterpret_cast<uint4*>(patch) + row * 4 + (at ^ (row / 2 & 3));
 }
 
-// The result of 32 x 16 numbers of X, in the patch as 32 rows: a warp reads and
-// writes along rows, at any address.
-__device__ __forceinline__ void result(const Products& p, const Entry& e, const Io& io, int b, int row0, int col,
-                                       float* patch, int lane) {
-  __syncwarp();
-  const int at = lane % 16;
-  if (col + at < e.cols) {
-    const auto value = [&](int r) {
-      return __fmul_rn(reinterpret_cast<const float*>(piece(patch, r, at / 4))[at % 4], 1.0f / kScaleX);
-    };
-    const int n = min(32, e.rows - row0);
-    int r = lane / 16;
-#pragma unroll 1
-    for (; r + 14 < n; r += 16)
-      finish<8, 2>(p.c, e, io, b, row0 + r, col + at, [&](int k) { return value(r + 2 * k); });
-#pragma unroll 1
-    for (; r < n; r += 2) finish<1, 2>(p.c, e, io, b, row0 + r, col + at, [&](int) { return value(r); });
-  }
-  __syncwarp();
+// A warp's 32 x 16 numbers of the result: it reads and writes along rows, at any
+// address, a lane one column of every second row.
+constexpr int kLaneRows = 16;
+template <typename F>
+__device__ __forceinline__ void each_row(const Entry& e, int row0, int col0, int lane, F f) {
+  const int row = row0 + lane / 16, n = col0 + lane % 16 < e.cols ? e.rows - row : 0;
+#pragma unroll
+  for (int k = 0; k < kLaneRows; ++k)
+    if (2 * k < n) f(k);
+}
+// The masters there, which the step updates.
+__device__ __forceinline__ void fetch_masters(const Call& c, const Entry& e, const Io& io, int b, int row0, int col0,
+                                              int lane, float w[kLaneRows]) {
+  const int64_t at = ((int64_t)b * e.rows + row0 + lane / 16) * e.cols + col0 + lane % 16, down = 2 * (int64_t)e.cols;
+  if (io.master) each_row(e, row0, col0, lane, [&](int k) { w[k] = io.master[at + k * down]; });
+  else if (c.out_type == ZERO_FP16)
+    each_row(e, row0, col0, lane, [&](int k) { w[k] = num<__half>(static_cast<const __half*>(io.out)[at + k * down]); });
+  else
+    each_row(e, row0, col0, lane,
+             [&](int k) { w[k] = num<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(io.out)[at + k * down]); });
+}
+// The result from the patch, O itself or the step on the masters `w` with it.
+__device__ __forceinline__ void result(const Call& c, const Entry& e, const Io& io, int b, int row0, int col0,
+                                       float* patch, int lane, const float w[kLaneRows]) {
+  const int64_t ld = c.step ? e.cols : io.out_row;
+  const int64_t at = b * (c.step ? (int64_t)e.rows * e.cols : io.out_batch) + (row0 + lane / 16) * ld + col0 + lane % 16;
+  const float factor = c.step ? -__fmul_rn(c.lr, e.s) : 1.0f;
+  const auto value = [&](int k) {
+    const int col = lane % 16;
+    const float o = __fmul_rn(reinterpret_cast<const float*>(piece(patch, lane / 16 + 2 * k, col / 4))[col % 4], 1.0f / kScaleX);
+    if (!c.step) return o;
+    const float x = __fmaf_rn(factor, o, __fmul_rn(w[k], c.decay));
+    if (io.master) io.master[at + 2 * k * ld] = x;
+    return x;
+  };
+  if (c.out_type == ZERO_FP16)
+    each_row(e, row0, col0, lane, [&](int k) { static_cast<__half*>(io.out)[at + 2 * k * ld] = as<__half>(value(k)); });
+  else if (c.out_type == ZERO_BF16)
+    each_row(e, row0, col0, lane,
+             [&](int k) { static_cast<__nv_bfloat16*>(io.out)[at + 2 * k * ld] = as<__nv_bfloat16>(value(k)); });
+  else
+    each_row(e, row0, col0, lane, [&](int k) { static_cast<float*>(io.out)[at + 2 * k * ld] = value(k); });
 }
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
@@ -207,8 +230,8 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // One tile's epilogue: the warp's 32 rows of the accumulator, every third 16 of
 // its columns.  Whatever it reads besides is fetched while the products
 // still run: the diagonal's numbers of the tile's columns go to shared memory
-// (`cols`), and the next columns' numbers are on their way while those before
-// are worked on.  The loops are kept short: a small matrix runs each of them
+// (`cols`), and the numbers of the columns after the next are on their way while
+// those before are worked on.  The loops are kept short: a small matrix runs each of them
 // once a tile, and straight code of 64 columns waited on instruction fetches
 // longer than it ran (64x64 through this kernel: 91 us with it, 53 now).
 enum Outcome { kFailed, kDone, kPart };   // a wait ran out; the tile is done; a part of it is
@@ -237,20 +260,29 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
 
   int ok = ready;
   float di = 0.0f;
-  uint4 hi[2], lo[2];
   constexpr int kNext = 16 * (kEpiWarps / 4);  // to the warp's next 16 columns
-  const auto fetch = [&](int c) {
-    if (t.which == 0 || c >= ncol) return;
+  struct Pieces {
+    uint4 hi[2], lo[2];
+  } even, odd;
+  const auto fetch = [&](Pieces& y, int c) {
+    if (c >= ncol) return;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      hi[q] = __ldcg(from + c * 16 + q * 128);
-      if (t.which == 2) lo[q] = __ldcg(low + c * 16 + q * 128);
+      y.hi[q] = __ldcg(from + c * 16 + q * 128);
+      if (t.which == 2) y.lo[q] = __ldcg(low + c * 16 + q * 128);
     }
   };
+  const Io io = last && t.which == 2 ? p.c.io[en.item] : Io{};
+  float w[kLaneRows];
   if (t.which != 0) {
     ok = __all_sync(0xffffffffu, ok && shared_wait(told, number + 1, &p.c.ws->fault));
     if (ok) {
-      fetch(part * 16);
+      fetch(even, part * 16);
+      if (t.which == 2 && last) {
+        if (p.c.step && part * 16 < ncol) fetch_masters(p.c, en, io, t.b, row0, col0 + part * 16, lane, w);
+      } else {
+        fetch(odd, part * 16 + kNext);
+      }
       const int c = warp * 32 + lane;
       float d = 0.0f;
       // the columns are A's, but those of a wide matrix's X
@@ -281,9 +313,7 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(kPair == 2 ? peer(empty_bar, 0) : empty_bar);
   };
-  float next[16];
-  if (part * 16 < ncol) tmem_load16(lanes + part * 16, next);
-  const bool cut = t.splits > 1;
+  const bool cut = t.splits > 1;             // X X^T alone
   // four columns of the tile's 128 rows of this CTA side by side
   const int slot_size = kTile / 4 * 128;
   float4* sums = p.parts + ((int64_t)t.slot * kPair + rank) * slot_size + quarter * 32 + lane;
@@ -291,10 +321,11 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
     float4* own = sums + (int64_t)t.part * kPair * slot_size;
 #pragma unroll 1
     for (int c = part * 16; c < ncol; c += kNext) {
+      float v[16];
+      tmem_load16(lanes + c, v);
       tmem_load_wait();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) __stcg(own + (c / 4 + q) * 128, reinterpret_cast<const float4*>(next)[q]);
-      if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
+      for (int q = 0; q < 4; ++q) __stcg(own + (c / 4 + q) * 128, reinterpret_cast<const float4*>(v)[q]);
     }
     release();
     asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
@@ -309,30 +340,73 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
     asm volatile("barrier.sync 1, %0;" ::"r"(32 * kEpiWarps) : "memory");
     if (!*arrived) return kPart;
   }
-#pragma unroll 1
-  for (int c = part * 16; c < ncol; c += kNext) {
-    float v[16];
-    if (cut) {
+  const auto put = [&](int c, const float2* y) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) v[q] = 0.0f;
-#pragma unroll 4
-      for (int s = 0; s < t.splits; ++s)
+    for (int q = 0; q < 2; ++q)
+      to[c * 16 + q * 128] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
+                                        pack(y[4 * q + 2].x, y[4 * q + 2].y), pack(y[4 * q + 3].x, y[4 * q + 3].y));
+  };
+  // b A + c A A
+  const auto second = [&](int c, Pieces& x) {
+    float2 y[8];
+    tmem_load16(lanes + c, reinterpret_cast<float*>(y));
+    tmem_load_wait();
+    const float2 scale = both(__fmul_rn(cc, 1.0f / kScale)), e2 = both(ei);
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(x.hi);
+    const float2* d = reinterpret_cast<const float2*>(cols + c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 y = __ldcg(sums + (int64_t)s * kPair * slot_size + (c / 4 + q) * 128);
-          v[4 * q] = __fadd_rn(v[4 * q], y.x);
-          v[4 * q + 1] = __fadd_rn(v[4 * q + 1], y.y);
-          v[4 * q + 2] = __fadd_rn(v[4 * q + 2], y.z);
-          v[4 * q + 3] = __fadd_rn(v[4 * q + 3], y.w);
-        }
-    } else {
-      tmem_load_wait();
+    for (int q = 0; q < 8; ++q) y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
+    fetch(x, c + 2 * kNext);
+    put(c, y);
+  };
+  // a X + B X
+  const auto third = [&](int c, Pieces& x, float2* y, int ahead) {
+    tmem_load16(lanes + c, reinterpret_cast<float*>(y));
+    tmem_load_wait();
+    const uint32_t *h = reinterpret_cast<const uint32_t*>(x.hi), *l = reinterpret_cast<const uint32_t*>(x.lo);
+    const float2* d = reinterpret_cast<const float2*>(cols + c);
+    const float2 ca2 = both(ca), down = both(1.0f / kScale), e2 = both(ei), low2 = both(1.0f / kLoScale);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) v[q] = next[q];
-      if (c + kNext < ncol) tmem_load16(lanes + c + kNext, next);
+    for (int q = 0; q < 8; ++q) {
+      const float2 z = unpack(h[q]);
+      y[q] = __ffma2_rn(y[q], down,
+                        __ffma2_rn(ca2, __ffma2_rn(unpack(l[q]), low2, z), __fmul2_rn(tall ? d[q] : e2, z)));
     }
-    float2* y = reinterpret_cast<float2*>(v);
-    if (t.which == 0) {
+    fetch(x, c + ahead);
+  };
+  const auto next_x = [&](int c, Pieces& x) {
+    float2 y[8];
+    third(c, x, y, 2 * kNext);
+    __align__(16) __half2 first[8], rest[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) split(y[q], &first[q], &rest[q]);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      to[c * 16 + q * 128] = reinterpret_cast<const uint4*>(first)[q];
+      low[c * 16 + q * 128] = reinterpret_cast<const uint4*>(rest)[q];
+    }
+  };
+  if (t.which == 0) {
+#pragma unroll 1
+    for (int c = part * 16; c < ncol; c += kNext) {
+      float v[16];
+      if (cut) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) v[q] = 0.0f;
+#pragma unroll 4
+        for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 y = __ldcg(sums + (int64_t)s * kPair * slot_size + (c / 4 + q) * 128);
+            v[4 * q] = __fadd_rn(v[4 * q], y.x);
+            v[4 * q + 1] = __fadd_rn(v[4 * q + 1], y.y);
+            v[4 * q + 2] = __fadd_rn(v[4 * q + 2], y.z);
+            v[4 * q + 3] = __fadd_rn(v[4 * q + 3], y.w);
+          }
+      } else {
+        tmem_load16(lanes + c, v);
+        tmem_load_wait();
+      }
       const int at = row - (col0 + c);         // the diagonal's place, if in these columns
       if (row0 < col0 + c + 16 && row0 + 32 > col0 + c) {
         float d = 0.0f;
@@ -343,45 +417,32 @@ __device__ __forceinline__ Outcome epilogue(const Products& p, const Tile& t, bo
         }
         if (at >= 0 && at < 16 && row < M) __stcg(diag + row, __fmul_rn(d, 1.0f / kScale));
       }
-    } else if (t.which == 1) {
-      const float2 scale = both(__fmul_rn(cc, 1.0f / kScale)), e2 = both(ei);
-      const uint32_t* s = reinterpret_cast<const uint32_t*>(hi);
-      const float2* d = reinterpret_cast<const float2*>(cols + c);
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        y[q] = __ffma2_rn(__fadd2_rn(e2, d[q]), unpack(s[q]), __fmul2_rn(scale, y[q]));
-      fetch(c + kNext);
-    } else {
-      const uint32_t *h = reinterpret_cast<const uint32_t*>(hi), *l = reinterpret_cast<const uint32_t*>(lo);
-      const float2* d = reinterpret_cast<const float2*>(cols + c);
-      const float2 ca2 = both(ca), down = both(1.0f / kScale), e2 = both(ei), low2 = both(1.0f / kLoScale);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float2 x = unpack(h[q]);
-        y[q] = __ffma2_rn(y[q], down,
-                          __ffma2_rn(ca2, __ffma2_rn(unpack(l[q]), low2, x), __fmul2_rn(tall ? d[q] : e2, x)));
-      }
-      fetch(c + kNext);
-      if (last) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) *piece(patch, lane, q) = reinterpret_cast<const uint4*>(v)[q];
-        result(p, en, p.c.io[en.item], t.b, row0, col0 + c, patch, lane);
-        continue;
-      }
-      __align__(16) __half2 first[8], second[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) split(y[q], &first[q], &second[q]);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        to[c * 16 + q * 128] = reinterpret_cast<const uint4*>(first)[q];
-        low[c * 16 + q * 128] = reinterpret_cast<const uint4*>(second)[q];
-      }
-      continue;
+      put(c, reinterpret_cast<const float2*>(v));
     }
+  } else if (t.which == 1) {
+#pragma unroll 1
+    for (int c = part * 16; c < ncol; c += 2 * kNext) {
+      second(c, even);
+      if (c + kNext < ncol) second(c + kNext, odd);
+    }
+  } else if (!last) {
+#pragma unroll 1
+    for (int c = part * 16; c < ncol; c += 2 * kNext) {
+      next_x(c, even);
+      if (c + kNext < ncol) next_x(c + kNext, odd);
+    }
+  } else {
+#pragma unroll 1
+    for (int c = part * 16; c < ncol; c += kNext) {
+      float2 y[8];
+      third(c, even, y, kNext);
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      to[c * 16 + q * 128] = make_uint4(pack(y[4 * q].x, y[4 * q].y), pack(y[4 * q + 1].x, y[4 * q + 1].y),
-                                      pack(y[4 * q + 2].x, y[4 * q + 2].y), pack(y[4 * q + 3].x, y[4 * q + 3].y));
+      for (int q = 0; q < 4; ++q) *piece(patch, lane, q) = reinterpret_cast<const uint4*>(y)[q];
+      __syncwarp();
+      result(p.c, en, io, t.b, row0, col0 + c, patch, lane, w);
+      __syncwarp();
+      if (p.c.step && c + kNext < ncol) fetch_masters(p.c, en, io, t.b, row0, col0 + c + kNext, lane, w);
+    }
   }
   if (!cut) release();
   return kDone;
