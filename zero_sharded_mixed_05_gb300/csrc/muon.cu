@@ -171,8 +171,10 @@ double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
 }
 
 template <typename T, int N>
-const void* resident_kernel(int cols) {
-  return cols == 128 ? (const void*)zm::muon_resident_kernel<T, 128, N> : (const void*)zm::muon_resident_kernel<T, 256, N>;
+const void* resident_kernel(int cols, bool two) {
+  return cols == 256 ? (const void*)zm::muon_resident_kernel<T, 256, 1, N>
+         : two       ? (const void*)zm::muon_resident_kernel<T, 128, 2, N>
+                     : (const void*)zm::muon_resident_kernel<T, 128, 1, N>;
 }
 
 int resident_bytes(int cols, int span) {
@@ -205,7 +207,7 @@ zero_status run_resident(zero_muon_t h, const zm::Start<N>& start, cudaStream_t 
     lc.attrs = &attr;
     lc.numAttrs = 1;
     void* p[] = {&r, const_cast<zm::Start<N>*>(&start)};
-    const cudaError_t e = cudaLaunchKernelExC(&lc, resident_kernel<T, N>(l.cols), p);
+    const cudaError_t e = cudaLaunchKernelExC(&lc, resident_kernel<T, N>(l.cols, l.units > h->sms), p);
     if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
     ++h->launches;
     r.head = 0;
@@ -217,7 +219,7 @@ zero_status run_resident(zero_muon_t h, const zm::Start<N>& start, cudaStream_t 
 template <typename T, int N>
 cudaError_t ready_resident(const zero_muon_handle* h) {
   for (const auto& l : h->resident) {
-    const cudaError_t e = cudaFuncSetAttribute(resident_kernel<T, N>(l.cols), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(resident_kernel<T, N>(l.cols, l.units > h->sms), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                resident_bytes(l.cols, zm::kResidentSpan));
     if (e != cudaSuccess) return e;
   }
@@ -234,10 +236,10 @@ cudaError_t ready_resident(const zero_muon_handle* h) {
 // and that takes less time by estimate (with matrices too large among them they
 // all go through the workspace, where the small ones cost next to nothing).
 // A step of a wave of them takes 5 microseconds with 128 columns a CTA (two on
-// an SM), 6.6 with 256 and 11.5 with more CTAs a matrix, whose sums go through
-// distributed shared memory.  Measured, on the chip against the workspace:
-// 128x128 31 and 70 us, 128x1024 x 32 68 and 102, 64x64 x 1000 109 and 182, but
-// 100x1500 x 60 261 and 180.  Matrices that need fewer CTAs go in launches of
+// an SM), 6.6 with 256 and 10 with more CTAs a matrix, which add up their shares
+// of A.  Measured, on the chip against the workspace: 128x128 29 and 64 us,
+// 128x1024 x 32 61 and 95, 64x64 x 1000 109 and 204, but 100x1500 x 60 230 and
+// 178.  Matrices that need fewer CTAs go in launches of
 // their own unless all fit on the device side by side.
 void choose_resident(zero_muon_t h) {
   int most = 1;
@@ -258,7 +260,7 @@ void choose_resident(zero_muon_t h) {
     const int span = span_of(e);
     const double at_once = e.l <= 128 ? 2 * h->sms : h->sms / span;
     here += (together ? 1.0 / h->entries.size() : std::ceil(e.batch / at_once)) *
-            ((span > 1 || (together && most > 1) ? 11.5 : e.l <= 128 ? 5.0 : 6.6) * h->cfg.steps + 6);
+            ((span > 1 || (together && most > 1) ? 10.0 : e.l <= 128 ? 5.0 : 6.6) * h->cfg.steps + 6);
   }
   const double there = 25 + products_cost(h->entries, 1, h->sms) * h->cfg.steps / 1900;
   if (here > 1.1 * there) return;

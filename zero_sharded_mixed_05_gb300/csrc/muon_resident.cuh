@@ -10,13 +10,13 @@
 //           binary16 in shared memory as an operand (H)
 //   A, B    in shared memory as an operand, one over the other
 // A step is three products of the CTA's own operands, accumulated in TMEM:
-//   A = H H^T over the CTA's columns, added up over the cluster through
-//       distributed shared memory (each number once, so that every CTA has
-//       the same bits), its diagonal kept in binary32 (muon_products.cuh);
+//   A = H H^T over the CTA's columns, added up over the cluster by copies
+//       between the CTAs (each number once, so that every CTA has the same
+//       bits), its diagonal kept in binary32 (muon_products.cuh);
 //   B = b A + c A A, in every CTA alike;   X <- a X + B H.
-// Measured, a call through the workspace and here: 64x64 53 and 25 us, 32 of
-// 128x1024 102 and 67 us.  A step is a chain of three products and their
-// epilogues, 4 us, and with a cluster's sums and barriers 11 us, in which the
+// Measured, a call through the workspace and here: 64x64 49 and 24 us, 32 of
+// 128x1024 95 and 61 us.  A step is a chain of three products and their
+// epilogues, 4 us, or 6 with 256 columns a CTA, and 10 with a cluster's sums; the
 // tensor cores work for 7 % of the cycles.
 #pragma once
 
@@ -38,7 +38,7 @@ struct Resident {
 
 template <int kCols>
 constexpr int resident_bytes(int span) {
-  return 128 * kCols * 2 + 128 * 128 * 2 + 1024 + (span > 1 ? 128 * 128 * 4 : 0);
+  return 128 * kCols * 2 + 128 * 128 * 2 + 1024 + (span > 1 ? 2 * 128 * 128 * 4 : 0);
 }
 
 // Four numbers of a row (fewer at its end, the rest zero) from p, and back.
@@ -106,8 +106,23 @@ __device__ __forceinline__ void finish4(const Call& c, const Entry& e, const Io&
   else store4<float>(static_cast<float*>(io.out) + at, n, vout, o);
 }
 
-template <typename T, int kCols, int N>
-__global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
+// Takes A's diagonal, if it is there, out of columns `col`.. of row r.
+template <int N>
+__device__ __forceinline__ void take_diagonal(float* v, int r, int col, float* diag) {
+  float d = 0.0f;
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    d = q == r - col ? v[q] : d;
+    v[q] = q == r - col ? 0.0f : v[q];
+  }
+  if (r >= col && r < col + N) diag[r] = __fmul_rn(d, 1.0f / kScale);
+}
+
+// kPerSm: CTAs an SM, 2 with 128 columns for more matrices than SMs.  One has
+// twice the registers: 64x64 24 us against 27, a hundred 100x100 27 against 31,
+// but 400 of them 74 against 64.
+template <typename T, int kCols, int kPerSm, int N>
+__global__ void __launch_bounds__(kResidentThreads, kPerSm)
     muon_resident_kernel(const __grid_constant__ Resident p, const __grid_constant__ Start<N> s) {
   constexpr int kChunks = kCols / 128;            // 32 columns each, of a thread's
   constexpr uint32_t kTmem = kCols == 128 ? 256 : 512;
@@ -126,6 +141,7 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
   double* red = reinterpret_cast<double*>(small + 512);                 // 16 warps' sums, then the CTA's
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(small + 768);
   const uint32_t bar = smem_u32(small + 784);
+  const uint32_t shares = bar + 8, totals = bar + 16;                   // barriers of the cluster's sums
   float* sums = reinterpret_cast<float*>(small + 1024);                 // A's share, for the cluster
   float* patch = reinterpret_cast<float*>(base) + warp * 1024;          // over both operands, before and after
   const uint32_t x_at = smem_u32(base), a_at = x_at + 128 * kCols * 2;
@@ -140,6 +156,8 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(bar, 1);
+    mbar_init(shares, 1);
+    mbar_init(totals, 1);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc<1>(smem_u32(tmem_at), kTmem);
@@ -231,7 +249,8 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) put(base, (part + 4 * h) * 4 + q, x[h] + 8 * q);
   };
-  uint32_t phase = 0;
+  uint32_t phase = 0, sum_phase = 0;
+  bool ok = true;                      // no wait has run out
   // Issues products once every thread's operand is written, waits for them.
   const auto products = [&](auto issue) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -245,48 +264,77 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
       }
       __syncwarp();
     }
-    mbar_wait(bar, phase, fault);      // a wait that ran out is in *fault: the result is not written
+    ok = mbar_wait(bar, phase, fault) && ok;   // a wait that ran out is in *fault too: the result is not written
     phase ^= 1;
     tc_fence_after();
   };
 
-  // Adds up the CTAs' shares of A (32 columns of a row a thread): every CTA adds
-  // the share of all of one part of A, starting with its own so that no one
-  // CTA's memory is read by all at once, and hands the sums to all.
-  const auto add_up = [&](float* v) {
-    float4* own = reinterpret_cast<float4*>(sums);
+  // A from the CTAs' shares of it (32 columns of a row a thread).  Every CTA adds
+  // up some columns, whose shares the others send it in binary32, and sends them
+  // the operand and the diagonal that come of it.  Both ways are bulk copies, and
+  // what bounds them is the bytes between SMs (loads and stores of each other's
+  // memory by the threads, binary32 both ways: 32 of 128x1024 67 us; copies: 63;
+  // the operand back: 61).  What a copy overwrites has been read: a CTA sends
+  // its next share after its last product, and an operand after it has all shares.
+  const auto add_up = [&](const float* v) {
+    float4 *own = reinterpret_cast<float4*>(sums), *theirs = own + 4096;
+    const uint32_t pieces = 4096 / p.span, mine = 16 / p.span;   // of four columns, of eight
+    unsigned char* const a = base + 128 * kCols * 2;
+    const auto written = [&] {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncthreads();
+    };
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       own[(part * 8 + q) * 128 + row] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    cluster_sync();
-    const int pieces = 4096 / p.span;
-    for (int i = threadIdx.x; i < pieces; i += kResidentThreads) {
-      const uint32_t at = smem_u32(own + rank * pieces + i);
-      float4 y[kResidentSpan];
-#pragma unroll
-      for (int r = 0; r < kResidentSpan; ++r)
-        if (r < p.span)
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(y[r].x), "=f"(y[r].y), "=f"(y[r].z), "=f"(y[r].w)
-                       : "r"(peer(at, (rank + r) % p.span)) : "memory");
-      float4 t = y[0];
-#pragma unroll
-      for (int r = 1; r < kResidentSpan; ++r)
-        if (r < p.span) {
-          t.x = __fadd_rn(t.x, y[r].x);
-          t.y = __fadd_rn(t.y, y[r].y);
-          t.z = __fadd_rn(t.z, y[r].z);
-          t.w = __fadd_rn(t.w, y[r].w);
+    written();
+    if (warp == 0) {
+      if (elected() && ok) {
+        mbar_expect(shares, (p.span - 1) * pieces * 16);
+        mbar_expect(totals, (p.span - 1) * (mine * 2048 + mine * 32));
+        for (int r = 1; r < p.span; ++r) {
+          const uint32_t to = (rank + r) % p.span;
+          copy_to_peer(peer(smem_u32(theirs + rank * pieces), to), smem_u32(own + to * pieces), pieces * 16,
+                       peer(shares, to));
         }
-#pragma unroll
-      for (int r = 0; r < kResidentSpan; ++r)
-        if (r < p.span)
-          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(peer(at, (rank + r) % p.span)),
-                       "f"(t.x), "f"(t.y), "f"(t.z), "f"(t.w) : "memory");
+      }
+      __syncwarp();
     }
-    cluster_sync();
+    ok = mbar_wait(shares, sum_phase, fault) && ok;
+    for (int i = threadIdx.x; i < (int)mine * 128; i += kResidentThreads) {
+      const int at = i / 128, r = i % 128;       // a row of eight columns
+      float t[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) reinterpret_cast<float4*>(v)[q] = own[(part * 8 + q) * 128 + row];
+      for (int h = 0; h < 2; ++h)
+        reinterpret_cast<float4*>(t)[h] = own[rank * pieces + (2 * at + h) * 128 + r];
+#pragma unroll
+      for (int k = 1; k < kResidentSpan; ++k)
+        if (k < p.span) {
+          const float4* from = theirs + (rank + k) % p.span * pieces + 2 * at * 128 + r;
+          const float4 y = from[0], z = from[128];
+          const float u[8] = {y.x, y.y, y.z, y.w, z.x, z.y, z.z, z.w};
+#pragma unroll
+          for (int q = 0; q < 8; ++q) t[q] = __fadd_rn(t[q], u[q]);
+        }
+      const int piece = rank * mine + at;
+      take_diagonal<8>(t, r, piece * 8, diag);
+      *reinterpret_cast<uint4*>(a + piece * 2048 + r * 16) =
+          make_uint4(pack(t[0], t[1]), pack(t[2], t[3]), pack(t[4], t[5]), pack(t[6], t[7]));
+    }
+    written();
+    if (warp == 0) {
+      if (elected() && ok) {
+        const uint32_t from = smem_u32(a) + rank * mine * 2048, from_d = smem_u32(diag) + rank * mine * 32;
+        for (int r = 1; r < p.span; ++r) {
+          const uint32_t to = (rank + r) % p.span;
+          copy_to_peer(peer(from, to), from, mine * 2048, peer(totals, to));
+          copy_to_peer(peer(from_d, to), from_d, mine * 32, peer(totals, to));
+        }
+      }
+      __syncwarp();
+    }
+    ok = mbar_wait(totals, sum_phase, fault) && ok;
+    sum_phase ^= 1;
   };
 
   const int l0 = (int)rank * kCols;
@@ -308,19 +356,13 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
     tmem_load16(acc_a + lanes + part * 32, v);
     tmem_load16(acc_a + lanes + part * 32 + 16, v + 16);
     tmem_load_wait();
-    if constexpr (kCols == 256)
-      if (p.span > 1) add_up(v);
-    if (part == quarter) {            // the diagonal runs through these columns
-      float d = 0.0f;
+    if (kCols == 256 && p.span > 1) {
+      add_up(v);
+    } else {
+      if (part == quarter) take_diagonal<32>(v, row, part * 32, diag);
 #pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        d = q == lane ? v[q] : d;
-        v[q] = q == lane ? 0.0f : v[q];
-      }
-      diag[row] = __fmul_rn(d, 1.0f / kScale);
+      for (int q = 0; q < 4; ++q) put(base + 128 * kCols * 2, part * 4 + q, v + 8 * q);
     }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) put(base + 128 * kCols * 2, part * 4 + q, v + 8 * q);
     products([&] {
       const uint32_t idesc = instruction(128, 128, false, false);
       const uint64_t d = operand(a_at, kPieceBytes, 128);
@@ -373,6 +415,15 @@ __global__ void __launch_bounds__(kResidentThreads, kCols == 128 ? 2 : 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 0) tmem_free<1>(tmem, kTmem);
+  if (kCols == 256 && p.span > 1) {
+    // no CTA ends before all copies from and to it have: they have where every
+    // wait was met; else those in flight get a millisecond
+    if (!ok)
+      for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000;) {
+      }
+    __syncwarp();
+    cluster_sync();
+  }
   if (*(volatile int*)fault) return;
   const bool vout = fits4(io.out, io.out_row, io.out_batch, c.out_type == ZERO_FP32 ? 4 : 2);
   const bool vmaster = c.step && io.master && fits4(io.master, e.cols, (int64_t)e.rows * e.cols, 4);

@@ -141,6 +141,13 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// Copies a run of this CTA's shared memory to a CTA of the cluster, whose
+// barrier counts the bytes (addresses of it from peer(); all multiples of 16).
+__device__ __forceinline__ void copy_to_peer(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "r"(from), "r"(bytes), "r"(bar) : "memory");
+}
+
 // ---- TMA: the box at (0, 0, x, y, z) of an array of five dimensions.  With a
 // pair the barrier may be the other CTA's.
 
