@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
 #pragma unroll
     for (int k = 0; k < kRing - 1; ++k) fetch(first + k * slots < a.tokens, k);
     angles(p);
-    if (!a.gain_per_head) load_gain(0);
+    if (R == 1 || !a.gain_per_head) load_gain(0);
     int at = 0;
     for (int64_t t = first; t < a.tokens; t += slots) {
       fetch(t + (kRing - 1) * slots < a.tokens, at == 0 ? kRing - 1 : at - 1);
@@ -327,9 +327,10 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
 #pragma unroll
               for (int i = 0; i < V; ++i) dgain[kSum ? 0 : r][j][i] = both(f);
           }
+          if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(next);
           continue;
         }
-        if (a.gain_per_head) load_gain(r);
+        if (R > 1 && a.gain_per_head) load_gain(r);
         float2 x[C][V], g[C][V];
         float2 sq = both(0.0f), dot = both(0.0f);
 #pragma unroll
@@ -356,6 +357,9 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
             if (turned) turn<V, kInter>(x[j], cs[j], sn[j], false);
           }
         }
+        // forward the next token's angles come as soon as these are done with; the
+        // backward pass has no registers to wait for them in
+        if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(next);
         float sum = __fadd_rn(sq.x, sq.y), sum_dot = __fadd_rn(dot.x, dot.y);
         for (int o = lanes >> 1; o > 0; o >>= 1) {
           sum = __fadd_rn(sum, __shfl_xor_sync(mask, sum, o));
@@ -389,7 +393,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
       }
       out += out_t;
       p = next;
-      if (t + slots < a.tokens) angles(p);
+      if (kBackward && t + slots < a.tokens) angles(p);
       if (t + 2 * slots < a.tokens) next = position(a, t + 2 * slots);
       at = at == kRing - 1 ? 0 : at + 1;
     }
@@ -657,8 +661,9 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   while (2 * r <= most_r && c.q_heads % (2 * r) == 0 && c.k_heads % (2 * r) == 0 &&
          b->tokens * a.heads >= (int64_t)2 * r * groups * 2 * h->sms)
     r *= 2;
-  a.per = std::min(groups, a.heads / r);
-  a.head_blocks = (a.heads / r + a.per - 1) / a.per;
+  // the heads' groups spread evenly over as few CTAs as hold a token's
+  a.head_blocks = (a.heads / r + groups - 1) / groups;
+  a.per = (a.heads / r + a.head_blocks - 1) / a.head_blocks;
   a.reps = groups / a.per;
   a.part_rows = sum ? 2 : a.per * r;
   a.part = want ? h->part : nullptr;
