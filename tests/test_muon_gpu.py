@@ -107,6 +107,55 @@ def test_orthogonalize(z, shape, kind, src, dst):
         z.zero_muon_destroy(h)
 
 
+@pytest.mark.parametrize("shape", [(60, 500, 2), (128, 1000, 3), (513, 90, 2), (128, 2048, 2), (1801, 77, 20),
+                                   (100, 100, 200), (5, 128, 400)], ids=str)
+@pytest.mark.parametrize("kind,src,dst", [("signal", "bf16", "fp32"), ("decay", "fp32", "bf16")])
+def test_on_the_chip(z, shape, kind, src, dst):
+    """Clusters of two, four and eight CTAs, and more matrices than SMs; with
+    one CTA a matrix the same bits for it on its own and among others."""
+    import torch
+    m, n, b = shape
+    g = spectrum(kind, b, m, n, torch.Generator(device="cuda").manual_seed(m + n)).to(dt(src))
+    one, many = z.zero_muon_create(z.make_muon_config(), [(m, n)]), z.zero_muon_create(z.make_muon_config(), [shape])
+    try:
+        out = torch.full((b, m, n), float("nan"), device="cuda", dtype=dt(dst))
+        z.zero_muon_orthogonalize(many, [g], [out])
+        close(out, ortho64(g), dst)
+        alone = torch.empty_like(out[0])
+        z.zero_muon_orthogonalize(one, [g[b - 1]], [alone])
+        close(alone[None], ortho64(g[b - 1:]), dst)
+        if max(m, n) <= 128:
+            assert torch.equal(alone, out[b - 1])
+    finally:
+        z.zero_muon_destroy(one)
+        z.zero_muon_destroy(many)
+
+
+@pytest.mark.parametrize("shape", [(300, 1030, 2), (1030, 300, 1), (257, 257, 3), (90, 4300, 1)], ids=str)
+@pytest.mark.parametrize("param,master", [("bf16", True), ("fp16", False)])
+def test_step_through_the_workspace(z, shape, param, master):
+    """Result blocks that end inside a tile, with and without binary32 masters."""
+    import torch
+    mats = matrices([shape], "bf16", 21)
+    for x in mats:
+        x["param16"] = x["param16"].to(dt(param))
+        if not master:
+            x["master"] = None
+    h = z.zero_muon_create(z.make_muon_config(grad_dtype=z.BF16, param_dtype=code(z, param), lr=1e-2, momentum=0.9,
+                                              weight_decay=0.1, scale_rule=1), [shape])
+    try:
+        mom, tol_m, w, tol_w = expected(z, mats[0], 1.0, 1e-2, 0.9, 0.1, True, 1)
+        z.zero_muon_step(h, z.make_muon_list(mats))
+        got = mats[0]["param16"].double()
+        assert ((mats[0]["momentum"].double() - mom).abs() <= tol_m).all()
+        tol_w = tol_w + U[param] * w.flatten(-2).norm(dim=-1)      # one rounding to 16 bits
+        assert ((got - w).flatten(-2).norm(dim=-1) <= tol_w).all()
+        if master:
+            assert torch.equal(mats[0]["param16"], mats[0]["master"].to(dt(param)))
+    finally:
+        z.zero_muon_destroy(h)
+
+
 @pytest.mark.parametrize("scale", [1e-6, 1e-3, 1e4])
 def test_scale_of_the_input(z, scale):
     """|G| far from one, and against the eps that is added to it."""

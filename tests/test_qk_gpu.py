@@ -101,6 +101,8 @@ CASES = [
     (70, 3, 1, 128, 0, "bf16", False, False, "own"),
     (257, 8, 4, 128, 128, "bf16", False, True, "heads_first"),
     (600, 32, 8, 64, 64, "fp16", False, False, "fused"),
+    (300, 32, 8, 128, 128, "bf16", False, True, "fused"),     # heads spread over two CTAs
+    (90, 33, 0, 128, 64, "fp16", True, True, "own"),
 ]
 
 
