@@ -10,10 +10,12 @@
 // tensor core told that the operand's depth runs down the rows.
 //
 // What bounds it: the tensor cores, for matrices of a few thousand (14336x4096:
-// 2.35 ms, 83 % of the tensor cores' cycles; 4096x4096, whose 136 tiles of a
+// 2.39 ms, 83 % of the tensor cores' cycles; 4096x4096, whose 136 tiles of a
 // symmetric product make 1.8 waves of 76 pairs: 0.89 ms, 71 %); the latency of
-// fifteen dependent products for small ones (1000x777 x 3: 110 us of which the
-// tensor cores work 18).  Hence:
+// fifteen dependent products for small ones (1000x777 x 3: 104 us of which the
+// tensor cores work 18).  In between, shallow B X, the epilogue: 12 of 2304x768,
+// 0.30 ms, 45 %; a tile of depth 768 takes 4.0 us of products and 5.0 of epilogue,
+// 1.3 MB between L2 and its SMs, 19 TB/s in all.  Hence:
 // - one persistent CTA pair an SM pair, 256 x 256 tiles (cta_group::2: each CTA
 //   stages half of both operands, 64 KB a stage of depth 128, and holds half of
 //   the tile's accumulators), or single CTAs with 128 x 128 tiles where 256

@@ -6,8 +6,8 @@
 // pass reads the row and its output's gradient and writes the row's gradient.
 // Nothing else of size is moved: angles and gains are a few hundred bytes a
 // token and stay in L1.  Measured, 16,384 tokens of 40 heads of 128 in bf16:
-// forward 59 us a call (56 on the device: 5.2 TB/s of DRAM traffic, and 6.1 of
-// the bytes that have to move, as L2 keeps some of the result; 59 % of the issue
+// forward 57 us a call (55 on the device: 5.3 TB/s of DRAM traffic, and 6.3 of
+// the bytes that have to move, as L2 keeps some of the result; 60 % of the issue
 // slots), backward 100 us (94 and, for the sums of the gains' gradients, 5;
 // 5.1 TB/s; 50 % of the issue slots).  One token takes 4 us on the device, less
 // than the host's call of 8.
@@ -653,9 +653,10 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   // Heads a group: fewer reads of the angles and fewer bookkeeping
   // instructions a row, as long as both head counts divide and the tokens
   // still fill the device.  The most: what the ring and the registers leave two
-  // or three CTAs an SM for (16,384 tokens, 40 heads of 128: forward 59 us with
-  // four, 68 with two; backward 100 with two, 157 with one; with sums a head,
-  // 20 heads of 64, backward 46 with one, 52 with two).
+  // or three CTAs an SM for (16,384 tokens, 40 heads of 128: forward 58 us with
+  // four, 65 with two; backward 100 with two, 121 with one; with sums a head,
+  // 20 heads of 64, backward 46 with one, 52 with two when that was measured, 41
+  // now that one keeps its gain in registers).
   int r = 1;
   const int most_r = es_vec < 16 ? 1 : v == 8 ? (!backward ? 4 : sum ? 2 : 1) : (backward ? 1 : 2);
   while (2 * r <= most_r && c.q_heads % (2 * r) == 0 && c.k_heads % (2 * r) == 0 &&
