@@ -37,6 +37,7 @@ struct zero_muon_handle {
   float4* parts = nullptr;
   int64_t chunks = 0;               // CTAs of the first two stages
   bool second = false;              // some matrix needs the second
+  bool far = false;                 // X, both parts and twice the first, is more than L2 keeps
   int pair = 2;                     // CTAs a tile of the products
   int grid = 0;                     // CTAs of the products
   int smem = 0;
@@ -304,6 +305,7 @@ zero_status run(zero_muon_t h, const zm::Call& c, const zm::Io* io, cudaStream_t
   std::copy(h->count, h->count + 3, pr.count);
   pr.tiles = ((int64_t)h->count[0] + h->count[1] + h->count[2]) * h->cfg.steps;
   pr.steps = h->cfg.steps;
+  pr.far = h->far;
   pr.inject = h->inject;
   h->inject = 0;
   for (int i = 0; i < pr.steps; ++i)
@@ -427,6 +429,12 @@ cudaError_t place(zero_muon_t h) {
     const int64_t x = e.batch * zm::block_size(e.rows, e.ldx) * 2, a = e.batch * zm::block_size(e.k, e.ldk) * 2;
     for (int64_t bytes : {x, x, x, a, a, e.batch * e.ldk * 4}) at.push_back(lay.take(bytes));
   }
+  int l2 = 0;
+  e = cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, h->device);
+  if (e != cudaSuccess) return e;
+  int64_t x_bytes = 0;
+  for (const zm::Entry& en : h->entries) x_bytes += en.batch * zm::block_size(en.rows, en.ldx) * 6;
+  h->far = x_bytes > l2 / 8 * 7ll;
   h->bytes = lay.size;
   std::vector<CUtensorMap> map(4 * n);
   e = cudaMalloc(reinterpret_cast<void**>(&h->mem), (size_t)h->bytes);

@@ -71,6 +71,7 @@ struct Products {
   int64_t tiles;             // of all products
   int32_t count[3];          // of a product of each kind
   int32_t steps;
+  int32_t far;               // X does not stay in L2: its second part is asked for ahead
   uint32_t inject;           // test hook: added to what a tile waits for
   float coef[ZERO_MUON_MAX_STEPS][3];
 };
@@ -532,6 +533,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         ok = __all_sync(0xffffffffu, count_wait(p.c.done + t.unit, need, fault));
         if (!ok) break;
         fence_proxy_async();
+      }
+      // The epilogue's second part of X, which no operand brings: this CTA's 128
+      // rows of the tile are one run.  (36 of 11840x80: 600 us without, 536 with
+      // it; but 768x768 x 12, whose X stays in L2, 166 and 172.)
+      if (p.far && side && t.which == 2) {
+        const int row = t.i * kTile + (int)rank * 128, col = t.j * kTile;
+        if (row < t.e.rows && elected())
+          prefetch_l2(t.e.lo + b * block_size(t.e.rows, t.e.ldx) + block_at(row, col, t.e.ldx),
+                      min(kTile, (int)t.e.ldx - col) * 256);
+        __syncwarp();
       }
       for (int k0 = from; k0 < depth; k0 += kDepth) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + 8 * s, phase, fault));

@@ -141,6 +141,11 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 
+// Asks for a run of global memory (16-byte aligned, a multiple of 16) to be in L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // Copies a run of this CTA's shared memory to a CTA of the cluster, whose
 // barrier counts the bytes (addresses of it from peer(); all multiples of 16).
 __device__ __forceinline__ void copy_to_peer(uint32_t to, uint32_t from, uint32_t bytes, uint32_t bar) {
