@@ -11,10 +11,10 @@
 //
 // What bounds it: the tensor cores, for matrices of a few thousand (14336x4096:
 // 2.39 ms, 83 % of the tensor cores' cycles; 4096x4096, whose 136 tiles of a
-// symmetric product make 1.8 waves of 76 pairs: 0.89 ms, 71 %); the latency of
+// symmetric product make 1.8 waves of 76 pairs: 0.88 ms, 72 %); the latency of
 // fifteen dependent products for small ones (1000x777 x 3: 104 us of which the
 // tensor cores work 18).  In between, shallow B X, the epilogue: 12 of 2304x768,
-// 0.30 ms, 45 %; a tile of depth 768 takes 4.0 us of products and 5.0 of epilogue,
+// 0.29 ms, 46 %; a tile of depth 768 takes 4.0 us of products and 5.0 of epilogue,
 // 1.3 MB between L2 and its SMs, 19 TB/s in all.  Hence:
 // - one persistent CTA pair an SM pair, 256 x 256 tiles (cta_group::2: each CTA
 //   stages half of both operands, 64 KB a stage of depth 128, and holds half of
@@ -535,9 +535,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         fence_proxy_async();
       }
       // The epilogue's second part of X, which no operand brings: this CTA's 128
-      // rows of the tile are one run.  (36 of 11840x80: 600 us without, 536 with
-      // it; but 768x768 x 12, whose X stays in L2, 166 and 172.)
-      if (p.far && side && t.which == 2) {
+      // rows of the tile are one run.  For products that are over before it has
+      // come.  (36 of 11840x80: 600 us without, 536 with it; 2304x768 x 12 336 and
+      // 328; but 768x768 x 12, whose X stays in L2, 166 and 172, and the step on
+      // seven matrices 4096 deep 11.40 and 11.54 ms.)
+      if (p.far && side && t.which == 2 && depth <= 1024) {
         const int row = t.i * kTile + (int)rank * 128, col = t.j * kTile;
         if (row < t.e.rows && elected())
           prefetch_l2(t.e.lo + b * block_size(t.e.rows, t.e.ldx) + block_at(row, col, t.e.ldx),
