@@ -443,9 +443,10 @@ def test_binding_refuses(z):
         z.zero_muon_destroy(h)
 
 
-@pytest.mark.parametrize("shape", [(100, 60, 1), (1536, 1536, 4)], ids=str)
+@pytest.mark.parametrize("shape", [(100, 60, 1), (128, 1000, 2), (257, 300, 1), (1536, 1536, 4)], ids=str)
 def test_a_wait_that_runs_out_is_a_reported_fault(z, shape):
-    """With single CTAs' tiles and with pairs': the call ends by itself, says
+    """On the chip, with a CTA and a cluster a matrix, and through the workspace,
+    with single CTAs' tiles and with pairs': the call ends by itself, says
     so, writes no result, and the next one is whole."""
     import torch
     m, n, b = shape
