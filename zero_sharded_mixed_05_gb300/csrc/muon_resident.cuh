@@ -8,7 +8,7 @@
 // matrix is held transposed):
 //   X       binary32 in registers, a thread a row and kCols / 4 columns;
 //           binary16 in shared memory as an operand (H)
-//   A, B    in shared memory as an operand, one over the other
+//   A, B    in shared memory as an operand, one over the other in a single CTA
 // A step is three products of the CTA's own operands, accumulated in TMEM:
 //   A = H H^T over the CTA's columns, added up over the cluster by copies
 //       between the CTAs (each number once, so that every CTA has the same
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(small + 768);
   const uint32_t bar = smem_u32(small + 784);
   const uint32_t shares = bar + 8, totals = bar + 16;                   // barriers of the cluster's sums
-  float* sums = reinterpret_cast<float*>(small + 1024);                 // A's share, for the cluster
+  float* sums = reinterpret_cast<float*>(small + 1024);                 // A's share, for the cluster; then B
   float* patch = reinterpret_cast<float*>(base) + warp * 1024;          // over both operands, before and after
   const uint32_t x_at = smem_u32(base), a_at = x_at + 128 * kCols * 2;
   int* fault = &c.ws->fault;
@@ -276,6 +276,11 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   // memory by the threads, binary32 both ways: 32 of 128x1024 67 us; copies: 63;
   // the operand back: 61).  What a copy overwrites has been read: a CTA sends
   // its next share after its last product, and an operand after it has all shares.
+  // What a copy reads stays until it has read it.  The shares: every CTA sends its
+  // totals after it has all shares, so when the totals are here nobody reads `own`.
+  // The operand and the diagonal: that a CTA has the others' totals says nothing of
+  // its own on their way out; those have arrived when the next shares have, and
+  // until then neither is written.  So B goes over `own`, not over A.
   const auto add_up = [&](const float* v) {
     float4 *own = reinterpret_cast<float4*>(sums), *theirs = own + 4096;
     const uint32_t pieces = 4096 / p.span, mine = 16 / p.span;   // of four columns, of eight
@@ -337,6 +342,8 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     sum_phase ^= 1;
   };
 
+  // where B goes: over A, or over this CTA's share of it
+  unsigned char* const b_to = kCols == 256 && p.span > 1 ? small + 1024 : base + 128 * kCols * 2;
   const int l0 = (int)rank * kCols;
   const int mine = max(0, min(kCols, e.l - l0));               // the CTA's columns
   const int deep_x = (mine + 15) / 16, deep_k = (e.k + 15) / 16, wide = max(16, deep_x * 16);
@@ -386,11 +393,11 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
           y[4 * q + k] = __ffma2_rn(__ffma2_rn(c2, d[k], ri), unpack(o[k]), __fmul2_rn(scale, y[4 * q + k]));
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) put(base + 128 * kCols * 2, part * 4 + q, v + 8 * q);
+      for (int q = 0; q < 4; ++q) put(b_to, part * 4 + q, v + 8 * q);
     }
     products([&] {
       const uint32_t idesc = instruction(128, wide, false, true);
-      const uint64_t da = operand(a_at, kPieceBytes, 128), db = operand(x_at, 128, kPieceBytes);
+      const uint64_t da = operand(smem_u32(b_to), kPieceBytes, 128), db = operand(x_at, 128, kPieceBytes);
       for (int q = 0; q < deep_k; ++q)
         mma_f16<1>(tmem, da + q * (2 * kPieceBytes >> 4), db + q * (2 * 128 >> 4), idesc, q > 0);
     });
