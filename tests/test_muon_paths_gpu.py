@@ -29,3 +29,31 @@ def test_a_clusters_ctas_agree_call_after_call(z, m, n, b):  # noqa: F811
         assert z.zero_muon_last_step(h).fault == 0
     finally:
         z.zero_muon_destroy(h)
+
+
+@pytest.mark.parametrize("shape", [(200, 60, 3), (90, 128, 400), (128, 400, 90), (1500, 100, 30), (40, 2000, 1)], ids=str)
+def test_a_wait_that_runs_out_on_the_chip(z, shape):  # noqa: F811
+    """One CTA a matrix with 256 columns and two CTAs an SM; clusters of two and
+    eight, more than run at once: the call leaves its steps at the first wait
+    that runs out (two seconds, not two a product), writes nothing, says so, and
+    TMEM, barriers and clusters are as the next calls need them."""
+    import time
+
+    import torch
+    m, n, b = shape
+    g = torch.randn(b, m, n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(8))
+    h = z.zero_muon_create(z.make_muon_config(), [shape])
+    try:
+        want, out = torch.empty_like(g), torch.full_like(g, 7.0)
+        z.zero_muon_orthogonalize(h, [g], [want])
+        close(want, ortho64(g), "fp32")
+        z.zero_muon_inject_wait_fault(h)
+        t0 = time.time()
+        z.zero_muon_orthogonalize(h, [g], [out])
+        assert z.zero_muon_last_step(h).fault == 1 and (out == 7).all()
+        assert time.time() - t0 < 5.0
+        for _ in range(3):
+            z.zero_muon_orthogonalize(h, [g], [out])
+            assert z.zero_muon_last_step(h).fault == 0 and torch.equal(out, want)
+    finally:
+        z.zero_muon_destroy(h)

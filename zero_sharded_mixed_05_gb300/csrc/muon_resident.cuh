@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(small + 768);
   const uint32_t bar = smem_u32(small + 784);
   const uint32_t shares = bar + 8, totals = bar + 16;                   // barriers of the cluster's sums
+  const uint32_t drain = bar + 24;
   float* sums = reinterpret_cast<float*>(small + 1024);                 // A's share, for the cluster; then B
   float* patch = reinterpret_cast<float*>(base) + warp * 1024;          // over both operands, before and after
   const uint32_t x_at = smem_u32(base), a_at = x_at + 128 * kCols * 2;
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     mbar_init(bar, 1);
     mbar_init(shares, 1);
     mbar_init(totals, 1);
+    mbar_init(drain, 1);
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc<1>(smem_u32(tmem_at), kTmem);
@@ -250,21 +252,30 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       for (int q = 0; q < 4; ++q) put(base, (part + 4 * h) * 4 + q, x[h] + 8 * q);
   };
   uint32_t phase = 0, sum_phase = 0;
-  bool ok = true;                      // no wait has run out
-  // Issues products once every thread's operand is written, waits for them.
-  const auto products = [&](auto issue) {
+  bool ok = true;                      // no wait of this thread's has run out
+  // What threads wrote to shared memory is there for products and copies.
+  const auto written = [&] {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
     __syncthreads();
+  };
+  // Issues products once every thread's operand is written, waits for them.  The
+  // issuing thread goes by its own waits: where they were met, what it issued
+  // before is over.  After one that ran out it issues nothing more, and no thread
+  // waits again once it has given up: the steps that are left pass in no time, on
+  // numbers that nobody uses (leaving them by a vote at each barrier cost 64x64
+  // a microsecond).
+  const auto products = [&](auto issue) {
+    written();
     if (warp == 0) {
       tc_fence_after();
-      if (elected()) {
+      if (elected() && ok) {
         issue();
         if (!p.inject) mma_commit<1>(bar);
       }
       __syncwarp();
     }
-    ok = mbar_wait(bar, phase, fault) && ok;   // a wait that ran out is in *fault too: the result is not written
+    ok = ok && mbar_wait(bar, phase, fault);
     phase ^= 1;
     tc_fence_after();
   };
@@ -285,10 +296,6 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     float4 *own = reinterpret_cast<float4*>(sums), *theirs = own + 4096;
     const uint32_t pieces = 4096 / p.span, mine = 16 / p.span;   // of four columns, of eight
     unsigned char* const a = base + 128 * kCols * 2;
-    const auto written = [&] {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncthreads();
-    };
 #pragma unroll
     for (int q = 0; q < 8; ++q)
       own[(part * 8 + q) * 128 + row] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       }
       __syncwarp();
     }
-    ok = mbar_wait(shares, sum_phase, fault) && ok;
+    ok = ok && mbar_wait(shares, sum_phase, fault);
     for (int i = threadIdx.x; i < (int)mine * 128; i += kResidentThreads) {
       const int at = i / 128, r = i % 128;       // a row of eight columns
       float t[8];
@@ -338,7 +345,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       }
       __syncwarp();
     }
-    ok = mbar_wait(totals, sum_phase, fault) && ok;
+    ok = ok && mbar_wait(totals, sum_phase, fault);
     sum_phase ^= 1;
   };
 
@@ -417,21 +424,32 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     if (step + 1 < p.steps) put_x();
   }
 
-  // ---- result: back through the patches, which lie over the operands
+  // ---- the end of all products, in flight or not
   tc_fence_before();
-  __syncthreads();
+  ok = __syncthreads_and(ok);
   tc_fence_after();
+  if (!ok) {   // products in flight still read shared memory and write TMEM: they get a second
+    if (warp == 0 && elected()) mma_commit<1>(drain);
+    __syncwarp();
+    for (const uint64_t t0 = now_ns(); !mbar_try(drain, 0) && now_ns() - t0 < 1000000000ull;) {
+    }
+    __syncthreads();
+  }
   if (warp == 0) tmem_free<1>(tmem, kTmem);
   if (kCols == 256 && p.span > 1) {
-    // no CTA ends before all copies from and to it have: they have where every
-    // wait was met; else those in flight get a millisecond
-    if (!ok)
-      for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000;) {
-      }
     __syncwarp();
     cluster_sync();
   }
-  if (*(volatile int*)fault) return;
+  if (*(volatile int*)fault) {
+    // No CTA of a cluster ends before all copies from and to it have.  They have
+    // where every wait of the cluster's was met; else, as no more are issued once
+    // all its CTAs have been here, those in flight get a millisecond.
+    if (p.span > 1)
+      for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000;) {
+      }
+    return;
+  }
+  // ---- result: back through the patches, which lie over the operands
   const bool vout = fits4(io.out, io.out_row, io.out_batch, c.out_type == ZERO_FP32 ? 4 : 2);
   const bool vmaster = c.step && io.master && fits4(io.master, e.cols, (int64_t)e.rows * e.cols, 4);
 #pragma unroll
