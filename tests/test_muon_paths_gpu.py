@@ -57,3 +57,31 @@ def test_a_wait_that_runs_out_on_the_chip(z, shape):  # noqa: F811
             assert z.zero_muon_last_step(h).fault == 0 and torch.equal(out, want)
     finally:
         z.zero_muon_destroy(h)
+
+
+@pytest.mark.parametrize("shapes", [[(100, 100, 400)], [(128, 1000, 40)], [(60, 60, 300), (90, 700, 50)]], ids=str)
+def test_a_call_after_a_faulted_one_is_whole(z, shapes):  # noqa: F811
+    """Queued behind it, with more CTAs than run at once and in several launches:
+    it starts without the fault, gives what it always gives, and reports none;
+    the faulted call reports its own, whichever of its launches ends last."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    g = [torch.randn(b, m, n, device="cuda", generator=gen) for m, n, b in shapes]
+    h = z.zero_muon_create(z.make_muon_config(), shapes)
+    try:
+        want, out = ([torch.empty_like(t) for t in g] for _ in range(2))
+        z.zero_muon_orthogonalize(h, g, want)
+        for w, t in zip(want, g):
+            close(w, ortho64(t), "fp32")
+        for _ in range(2):
+            z.zero_muon_inject_wait_fault(h)
+            z.zero_muon_orthogonalize(h, g, out)
+            assert z.zero_muon_last_step(h).fault == 1
+            z.zero_muon_inject_wait_fault(h)
+            z.zero_muon_orthogonalize(h, g, out)
+            z.zero_muon_orthogonalize(h, g, out)
+            assert z.zero_muon_last_step(h).fault == 0
+            for w, t in zip(want, out):
+                assert torch.equal(w, t)
+    finally:
+        z.zero_muon_destroy(h)

@@ -712,7 +712,7 @@ zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "zero_muon_last_step");
   out->skipped = w.skipped;
-  out->fault = w.fault;
+  out->fault = h->resident.empty() ? w.fault : w.last;
   return ZERO_OK;
 }
 

@@ -70,8 +70,12 @@ struct Io {
 };
 
 struct Workspace {
-  int32_t fault;
+  int32_t fault;             // a wait has run out in the call that is running, or in the last
   int32_t skipped;
+  // On the chip `fault` is a launch's own: zero when it starts, as the last of
+  // its CTAs to end takes it from there.
+  int32_t last;              // what the last call ended with
+  unsigned long long ended;  // CTAs of the launch that have ended; times 2^32, without a result
 };
 
 struct Call {

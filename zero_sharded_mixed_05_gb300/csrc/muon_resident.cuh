@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   extern __shared__ __align__(1024) unsigned char base[];
   const Call& c = s.c;
   if (p.head && blockIdx.x == 0 && threadIdx.x == 0) {
-    c.ws->fault = 0;
     c.ws->skipped = skipped(c);
+    if (skipped(c)) c.ws->last = 0;
   }
   if (skipped(c)) return;
   const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(small + 768);
   const uint32_t bar = smem_u32(small + 784);
   const uint32_t shares = bar + 8, totals = bar + 16;                   // barriers of the cluster's sums
-  const uint32_t drain = bar + 24;
+  const uint32_t drain = bar + 24, failed = bar + 32;                   // failed: a wait of the cluster's has run out
   float* sums = reinterpret_cast<float*>(small + 1024);                 // A's share, for the cluster; then B
   float* patch = reinterpret_cast<float*>(base) + warp * 1024;          // over both operands, before and after
   const uint32_t x_at = smem_u32(base), a_at = x_at + 128 * kCols * 2;
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     mbar_init(shares, 1);
     mbar_init(totals, 1);
     mbar_init(drain, 1);
+    *(volatile int*)(small + 816) = 0;
     mbar_init_fence();
   }
   if (warp == 0) tmem_alloc<1>(smem_u32(tmem_at), kTmem);
@@ -425,28 +426,49 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   }
 
   // ---- the end of all products, in flight or not
+  const bool several = kCols == 256 && p.span > 1;
+  if (several) {
+    if (!ok)             // all of the cluster's CTAs know by the barrier
+      for (int r = 0; r < p.span; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer(failed, r)), "r"(1) : "memory");
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_before();
-  ok = __syncthreads_and(ok);
+  ok = __syncthreads_and(ok && (!several || *(volatile int*)(small + 816) == 0));
   tc_fence_after();
-  if (!ok) {   // products in flight still read shared memory and write TMEM: they get a second
+  if (!ok) {
+    // Products in flight still read shared memory and write TMEM: they get a
+    // second.  No CTA of a cluster ends before all copies from and to it have.
+    // They have where every wait of the cluster's was met; else, as no more are
+    // issued once all its CTAs have been here, those in flight get a millisecond.
     if (warp == 0 && elected()) mma_commit<1>(drain);
     __syncwarp();
     for (const uint64_t t0 = now_ns(); !mbar_try(drain, 0) && now_ns() - t0 < 1000000000ull;) {
     }
+    if (several)
+      for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000;) {
+      }
     __syncthreads();
   }
   if (warp == 0) tmem_free<1>(tmem, kTmem);
-  if (kCols == 256 && p.span > 1) {
-    __syncwarp();
-    cluster_sync();
+  // This CTA's threads are done with `fault`.  Whether it is the last to be, and
+  // whether any had no result, is asked now and looked at once this result is
+  // written (asked with fences and a look at `fault`, 64x64 took 24.7 us for 22.7).
+  unsigned long long ended = 0;
+  if (threadIdx.x == 0) {
+    if (!ok) __threadfence();
+    ended = atomicAdd(&c.ws->ended, ok ? 1ull : 1ull + (1ull << 32)) + (ok ? 1ull : 1ull + (1ull << 32));
   }
-  if (*(volatile int*)fault) {
-    // No CTA of a cluster ends before all copies from and to it have.  They have
-    // where every wait of the cluster's was met; else, as no more are issued once
-    // all its CTAs have been here, those in flight get a millisecond.
-    if (p.span > 1)
-      for (const uint64_t t0 = now_ns(); now_ns() - t0 < 1000000;) {
-      }
+  const auto end = [&] {
+    if (threadIdx.x != 0 || (uint32_t)ended != gridDim.x) return;
+    const bool failed = ended >> 32;
+    if (failed) c.ws->fault = 0;
+    if (failed || p.head) c.ws->last = failed;
+    c.ws->ended = 0;
+  };
+  if (!ok) {
+    end();
     return;
   }
   // ---- result: back through the patches, which lie over the operands
@@ -475,6 +497,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     }
     __syncwarp();
   }
+  end();
 }
 
 }  // namespace zm
