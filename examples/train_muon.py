@@ -147,7 +147,11 @@ def train(steps=60, width=256, layers=2, lr=4e-3, quiet=False):
             z.zero_opt_step_folded(opt, 0, bufs, records, 2)
             z.zero_muon_step(muon, items, decision=decision)
             losses.append(float(loss.detach()))
-            if not quiet and (step % 10 == 0 or step == steps - 1):
+            if step % 10 and step != steps - 1:
+                continue
+            if z.zero_muon_fault_count(muon):
+                raise RuntimeError("a step of the matrices ended in a fault")
+            if not quiet:
                 info = z.zero_opt_last_step(opt)
                 print(f"step {step:3d}  loss {losses[-1]:.4f}  gradient norm {info.norm:.3f}  "
                       f"loss scale {info.scale_used:g}{'  skipped' if info.skipped else ''}")

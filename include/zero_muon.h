@@ -109,7 +109,8 @@ typedef struct zero_muon_info {
   int32_t skipped;          /* 1: the decision said skip, nothing changed    */
   int32_t fault;            /* 1: a bounded wait ran out inside the kernels:
                                outputs (master, param16, O) are not to be
-                               used; the momentum has been updated           */
+                               used; the momentum has been updated.  The next
+                               call starts anew (zero_muon_fault_count)      */
 } zero_muon_info;
 
 /* lr 2e-2, momentum 0.95, Nesterov, weight decay 0, eps 1e-7, five steps of
@@ -151,6 +152,11 @@ zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double 
 
 /* What the last call did.  Synchronizes `stream`.  Errors: EINVAL, ECUDA. */
 zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out);
+
+/* Calls of the handle that have ended in a fault since its creation, the last
+ * one included: what a loop that does not ask after every step looks at now and
+ * then.  Synchronizes `stream`.  Errors: EINVAL, ECUDA. */
+zero_status zero_muon_fault_count(zero_muon_t h, void* stream, int64_t* faults);
 
 /* Failure-detection test hook.  In the next call of this handle the tiles of
  * every product but the first wait for counts that are never reached.  Their

@@ -85,3 +85,26 @@ def test_a_call_after_a_faulted_one_is_whole(z, shapes):  # noqa: F811
                 assert torch.equal(w, t)
     finally:
         z.zero_muon_destroy(h)
+
+
+@pytest.mark.parametrize("shapes", [[(64, 64, 2)], [(60, 60, 300), (90, 700, 50)], [(257, 300, 1)]], ids=str)
+def test_a_fault_that_nobody_asked_about_is_counted(z, shapes):  # noqa: F811
+    """Once a faulted call, on the chip (one launch and several) and through the
+    workspace, whatever calls come after it."""
+    import torch
+    g = [torch.randn(b, m, n, device="cuda") for m, n, b in shapes]
+    out = [torch.empty_like(t) for t in g]
+    h = z.zero_muon_create(z.make_muon_config(), shapes)
+    try:
+        for count in range(3):
+            assert z.zero_muon_fault_count(h) == count
+            z.zero_muon_orthogonalize(h, g, out)
+            assert z.zero_muon_fault_count(h) == count and z.zero_muon_last_step(h).fault == 0
+            z.zero_muon_inject_wait_fault(h)
+            z.zero_muon_orthogonalize(h, g, out)
+            if count == 1:
+                assert z.zero_muon_fault_count(h) == 2 and z.zero_muon_last_step(h).fault == 1
+            z.zero_muon_orthogonalize(h, g, out)
+            z.zero_muon_orthogonalize(h, g, out)
+    finally:
+        z.zero_muon_destroy(h)

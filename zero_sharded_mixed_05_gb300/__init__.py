@@ -199,6 +199,7 @@ SIGNATURES = [
     ("zero_muon_orthogonalize", _i32, [_vp, _P(zero_muon_operand), _i32, _i32, _vp]),
     ("zero_muon_step", _i32, [_vp, _P(zero_muon_matrix), _f64, _vp, _vp]),
     ("zero_muon_last_step", _i32, [_vp, _vp, _P(zero_muon_info)]),
+    ("zero_muon_fault_count", _i32, [_vp, _vp, _P(_i64)]),
     ("zero_muon_inject_wait_fault", _i32, [_vp]),
     ("zero_muon_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_qk_create", _i32, [_P(zero_qk_config), _P(_vp)]),
@@ -791,6 +792,14 @@ def zero_muon_last_step(h, stream=None) -> zero_muon_info:
     _check(lib().zero_muon_last_step(h, _stream(stream), ctypes.byref(out)),
            "zero_muon_last_step")
     return out
+
+
+def zero_muon_fault_count(h, stream=None) -> int:
+    """Calls of the handle that have ended in a fault since its creation."""
+    out = _i64()
+    _check(lib().zero_muon_fault_count(h, _stream(stream), ctypes.byref(out)),
+           "zero_muon_fault_count")
+    return out.value
 
 
 def zero_muon_inject_wait_fault(h) -> None:

@@ -341,6 +341,15 @@ zero_status check_device(zero_muon_t h) {
   return ZERO_OK;
 }
 
+zero_status read_workspace(zero_muon_t h, void* stream, zm::Workspace* w, const char* what) {
+  const zero_status st = check_device(h);
+  if (st != ZERO_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(w, h->call.ws, sizeof(*w), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  return e == cudaSuccess ? ZERO_OK : cuda_fail(e, what);
+}
+
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                 CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
@@ -704,15 +713,20 @@ zero_status zero_muon_step(zero_muon_t h, const zero_muon_matrix* items, double 
 
 zero_status zero_muon_last_step(zero_muon_t h, void* stream, zero_muon_info* out) {
   if (!h || !out) return fail(ZERO_EINVAL, "NULL argument");
-  const zero_status st = check_device(h);
-  if (st != ZERO_OK) return st;
   zm::Workspace w;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemcpyAsync(&w, h->call.ws, sizeof(w), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return cuda_fail(e, "zero_muon_last_step");
+  const zero_status st = read_workspace(h, stream, &w, "zero_muon_last_step");
+  if (st != ZERO_OK) return st;
   out->skipped = w.skipped;
   out->fault = h->resident.empty() ? w.fault : w.last;
+  return ZERO_OK;
+}
+
+zero_status zero_muon_fault_count(zero_muon_t h, void* stream, int64_t* faults) {
+  if (!h || !faults) return fail(ZERO_EINVAL, "NULL argument");
+  zm::Workspace w;
+  const zero_status st = read_workspace(h, stream, &w, "zero_muon_fault_count");
+  if (st != ZERO_OK) return st;
+  *faults = (int64_t)w.faults + (h->resident.empty() ? w.fault : 0);
   return ZERO_OK;
 }
 

@@ -75,6 +75,7 @@ struct Workspace {
   // On the chip `fault` is a launch's own: zero when it starts, as the last of
   // its CTAs to end takes it from there.
   int32_t last;              // what the last call ended with
+  int32_t faults;            // faulted calls; through the workspace, before the last
   unsigned long long ended;  // CTAs of the launch that have ended; times 2^32, without a result
 };
 
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 3) muon_stats_kernel(const __grid_co
   const Call& c = s.c;
   __shared__ double red[kThreads / 32];
   if (blockIdx.x == 0 && threadIdx.x == 0) {
+    c.ws->faults += c.ws->fault;
     c.ws->fault = 0;
     c.ws->skipped = skipped(c);
   }

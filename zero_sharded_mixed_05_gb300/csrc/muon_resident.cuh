@@ -463,7 +463,10 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
   const auto end = [&] {
     if (threadIdx.x != 0 || (uint32_t)ended != gridDim.x) return;
     const bool failed = ended >> 32;
-    if (failed) c.ws->fault = 0;
+    if (failed) {
+      c.ws->fault = 0;
+      if (p.head || !c.ws->last) ++c.ws->faults;     // once a call
+    }
     if (failed || p.head) c.ws->last = failed;
     c.ws->ended = 0;
   };
