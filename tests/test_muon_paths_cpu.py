@@ -15,3 +15,46 @@ def test_fault_count_refuses(z, handle):  # noqa: F811
         with pytest.raises(z.ZeroOptError) as e:
             z.zero_muon_fault_count(handle)
         assert e.value.status == z.ZERO_ECUDA
+
+
+WAITS = r"""
+#include <cstdio>
+#include "sm103.cuh"
+using sm103::Patience;
+constexpr uint64_t kMs = 1000 * 1000;
+// looks `each` ns apart from `from` on, `pause` ns once after `at` of them: the
+// time until the wait is given up
+uint64_t given_up(uint64_t from, uint64_t each, int at, uint64_t pause) {
+  Patience p;
+  uint64_t now = from;
+  for (int n = 0; n < 100000000; ++n) {
+    if (p.out(now)) return now - from;
+    now += each + (n == at ? pause : 0);
+  }
+  return 0;
+}
+int main() {
+  std::printf("%.3f %.3f %.3f %.3f\n", given_up(5, kMs / 100, -1, 0) / 1e6,
+              given_up(5, kMs / 100, 0, 3600000 * kMs) / 1e6, given_up(5, kMs / 100, 1000, 3600000 * kMs) / 1e6,
+              given_up(5, 500 * kMs, -1, 0) / 1e6);
+}
+"""
+
+
+def test_a_wait_does_not_count_what_the_gpu_did_meanwhile(tmp_path):
+    """Two seconds of looking on; an hour between two looks counts as a
+    twentieth of them; and every wait ends, however seldom it looks."""
+    import subprocess
+
+    from zero_sharded_mixed_05_gb300 import _build
+    src, exe = tmp_path / "waits.cu", tmp_path / "waits"
+    src.write_text(WAITS)
+    subprocess.run([_build.nvcc(), *_build.ARCH, "-std=c++17", "-I", _build.CSRC, "-o", str(exe), str(src)],
+                   check=True)
+    steady, early, late, seldom = map(float, subprocess.run([str(exe)], check=True, capture_output=True,
+                                                            text=True).stdout.split())
+    hour = 3600e3
+    assert 2000 <= steady < 2001
+    for paused in (early, late):
+        assert hour + 1900 <= paused < hour + 1902
+    assert 10000 <= seldom <= 11000

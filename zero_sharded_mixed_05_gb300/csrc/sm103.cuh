@@ -79,20 +79,32 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 
 constexpr uint64_t kWaitNs = 2ull * 1000 * 1000 * 1000;
+constexpr uint64_t kLookNs = kWaitNs / 20;
 
-// Waits until the phase of `parity` has completed: true.  After two seconds (a
-// tile takes milliseconds at most), or when another thread has given up, sets
-// *fault and gives up: false.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* fault) {
-  if (mbar_try(bar, parity)) return true;
-  uint64_t t0 = 0;
+// How long a wait has lasted, by its looks at the clock.  What lies between two
+// of them counts as a twentieth of the bound at most: in a longer time the GPU
+// was doing something else, and so was what is waited for.
+struct Patience {
+  uint64_t last = 0, spent = 0;
+  __host__ __device__ __forceinline__ bool out(uint64_t now) {
+    const uint64_t past = last == 0 ? 0 : now - last;
+    last = now;
+    spent += past < kLookNs ? past : kLookNs;
+    return spent > kWaitNs;
+  }
+};
+
+// Waits until load() is true: true.  After two seconds (a tile takes
+// milliseconds at most), or when another thread has given up, sets *fault and
+// gives up: false.
+template <typename Load>
+__device__ __forceinline__ bool bounded(Load load, int* fault) {
+  Patience patience;
   for (uint32_t n = 1;; ++n) {
-    if (mbar_try(bar, parity)) return true;
+    if (load()) return true;
     if (n % 64 == 0) {
       if (*(volatile int*)fault) return false;
-      const uint64_t t = now_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitNs) {
+      if (patience.out(now_ns())) {
         *(volatile int*)fault = 1;
         return false;
       }
@@ -100,23 +112,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* fa
   }
 }
 
-// The same for a counter in global memory to reach `need`, and for one in this
-// CTA's shared memory.
+// For the phase of `parity` to complete.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* fault) {
+  return mbar_try(bar, parity) || bounded([=] { return mbar_try(bar, parity); }, fault);
+}
+
+// For a counter in global memory, or in this CTA's shared memory, to reach `need`.
 template <typename Load>
 __device__ __forceinline__ bool reach(Load load, uint32_t need, int* fault) {
-  uint64_t t0 = 0;
-  for (uint32_t n = 1;; ++n) {
-    if (load() >= need) return true;
-    if (n % 64 == 0) {
-      if (*(volatile int*)fault) return false;
-      const uint64_t t = now_ns();
-      if (t0 == 0) t0 = t;
-      if (t - t0 > kWaitNs) {
-        *(volatile int*)fault = 1;
-        return false;
-      }
-    }
-  }
+  return bounded([=] { return load() >= need; }, fault);
 }
 __device__ __forceinline__ bool count_wait(const uint32_t* counter, uint32_t need, int* fault) {
   return reach([=] {
