@@ -1,5 +1,6 @@
 """The query/key norm with rotation for torch programs: a callable that keeps
-the handle and takes part in autograd.
+the handle and takes part in autograd (first derivatives; a second one is an
+error).
 
     norm = QkNormRope(make_qk_config(q_heads=8, k_heads=2, head_dim=64))
     q, k = norm(q, k, q_gain, k_gain, cos, sin, positions)
@@ -7,6 +8,7 @@ the handle and takes part in autograd.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (make_qk_config, zero_qk_create, zero_qk_destroy, zero_qk_norm_rope,
                zero_qk_norm_rope_backward)
@@ -34,6 +36,7 @@ class _Apply(torch.autograd.Function):
         return q_out, k_out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, cos, sin, positions = ctx.saved_tensors
         dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
