@@ -1,5 +1,7 @@
 """The autograd wrapper of the query/key norm, with the formula in binary64 in
 the kernels' place and the checks of the binding in front of it."""
+import gc
+
 import pytest
 import torch
 
@@ -69,7 +71,10 @@ def calls(monkeypatch):
     for name, fn in (("zero_qk_create", c.create), ("zero_qk_destroy", c.destroy), ("zero_qk_norm_rope", c.forward),
                      ("zero_qk_norm_rope_backward", c.backward)):
         monkeypatch.setattr(qk, name, fn)
-    return c
+    yield c
+    for o in gc.get_objects():             # a failed test's: no handle of the library's
+        if type(o) is qk.QkNormRope:
+            o._handle = None
 
 
 T, HQ, HK, D = 9, 4, 4, 8
@@ -98,3 +103,26 @@ def test_second_derivatives_are_refused(calls):
     dq, = torch.autograd.grad((qo * ko).sum(), q, create_graph=True)
     with pytest.raises(RuntimeError):
         (dq.square().sum() + q.sum()).backward()
+
+
+@pytest.mark.parametrize("how", ["einsum", "matmul", "expanded", "sliced"])
+def test_gradients_in_any_order(calls, how):
+    """What attention and reductions send back: permuted, broadcast and cut
+    gradients, against autograd on the formula."""
+    ins = inputs(2)
+    ref = [t.detach().double().requires_grad_() for t in ins[:4]]
+
+    def loss(q, k):
+        if how == "einsum":
+            return torch.einsum("qhd,khd->hqk", q, k).softmax(-1).square().sum()
+        if how == "matmul":
+            return (q.transpose(0, 1) @ k.permute(1, 2, 0)).tanh().sum()
+        if how == "expanded":
+            return q.sum() * k.mean()
+        return (q[1:, :2] * k[:-1, 2:]).sum()
+    norm = norm_of()
+    loss(*norm(*ins)).backward()
+    loss(*(plain(x, gain, *ins[4:]) for x, gain in ((ref[0], ref[2]), (ref[1], ref[3])))).backward()
+    for a, b in zip(ins[:4], ref):
+        # binary32 results of sums of T * heads * D terms of size one
+        assert ((a.grad.double() - b.grad).abs() <= T * HQ * D * 2.0 ** -22).all()

@@ -39,7 +39,7 @@ class _Apply(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, cos, sin, positions = ctx.saved_tensors
-        dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
         dqg, dkg = torch.empty_like(q_gain), torch.empty_like(k_gain)
         zero_qk_norm_rope_backward(ctx.handle, dq_out.contiguous(), dk_out.contiguous(), q, k, dq, dk,
                                    dqg, dkg, q_gain, k_gain, cos, sin, positions)
