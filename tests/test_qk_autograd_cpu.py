@@ -126,3 +126,28 @@ def test_gradients_in_any_order(calls, how):
     for a, b in zip(ins[:4], ref):
         # binary32 results of sums of T * heads * D terms of size one
         assert ((a.grad.double() - b.grad).abs() <= T * HQ * D * 2.0 ** -22).all()
+
+
+def test_gains_of_ones_and_gains_that_do_not_learn(calls):
+    """A gain may be None, as in the call itself; sums are made for those that
+    take a gradient alone."""
+    q, k, qg, kg, *rest = inputs(3)
+    norm = norm_of()
+    for gains, summed in (((None, None), (False, False)), ((qg.detach(), kg), (False, True)),
+                          ((qg, None), (True, False)), ((qg, kg), (True, True))):
+        ins = [t.detach().clone().requires_grad_() for t in (q, k)]
+        ref = [t.detach().double().requires_grad_() for t in (q, k)]
+        for t in (qg, kg):
+            t.grad = None
+        qo, ko = norm(*ins, *gains, *rest)
+        (qo * ko).sum().backward()
+        assert calls.summed[-1] == summed
+        wide = [None if t is None else t.detach().double().requires_grad_() for t in gains]
+        (plain(ref[0], wide[0], *rest) * plain(ref[1], wide[1], *rest)).sum().backward()
+        for a, b in zip(ins, ref):
+            assert ((a.grad.double() - b.grad).abs() <= D * 2.0 ** -20).all()
+        for t, w, s in zip(gains, wide, summed):
+            if s:
+                assert ((t.grad.double() - w.grad).abs() <= T * HQ * D * 2.0 ** -22).all()
+            elif t is not None:
+                assert t.grad is None

@@ -40,7 +40,8 @@ class _Apply(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, cos, sin, positions = ctx.saved_tensors
         dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
-        dqg, dkg = torch.empty_like(q_gain), torch.empty_like(k_gain)
+        dqg, dkg = (torch.empty_like(gain) if wanted else None
+                    for gain, wanted in zip((q_gain, k_gain), ctx.needs_input_grad[3:5]))
         zero_qk_norm_rope_backward(ctx.handle, dq_out.contiguous(), dk_out.contiguous(), q, k, dq, dk,
                                    dqg, dkg, q_gain, k_gain, cos, sin, positions)
         return None, dq, dk, dqg, dkg, None, None, None
@@ -57,7 +58,8 @@ class QkNormRope:
 
     def __call__(self, q, k, q_gain, k_gain, cos, sin, positions):
         """q [tokens, q_heads, D] and k [tokens, k_heads, D] (heads contiguous),
-        binary32 gains, tables and positions as `zero_qk_norm_rope` takes them."""
+        binary32 gains (None: ones), tables and positions as `zero_qk_norm_rope`
+        takes them.  A gain that requires no gradient costs no sums."""
         return _Apply.apply(self._handle, q, k, q_gain, k_gain, cos, sin, positions)
 
     def close(self):
