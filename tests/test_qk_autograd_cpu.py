@@ -151,3 +151,26 @@ def test_gains_of_ones_and_gains_that_do_not_learn(calls):
                 assert ((t.grad.double() - w.grad).abs() <= T * HQ * D * 2.0 ** -22).all()
             elif t is not None:
                 assert t.grad is None
+
+
+def test_the_handle_lives_as_long_as_a_graph_needs_it(calls):
+    """The callable may be gone before the backward pass; its handle is
+    destroyed once, after it."""
+    *ins, cos, sin, pos = inputs(4)
+    norm = norm_of()
+    qo, ko = norm(*ins, cos, sin, pos)
+    del norm
+    gc.collect()
+    assert len(calls.live) == 1
+    (qo * ko).sum().backward()
+    assert ins[0].grad is not None and ins[2].grad is not None
+    del qo, ko
+    gc.collect()
+    assert not calls.live
+    # closed by hand is closed
+    norm = norm_of()
+    qo, ko = norm(*ins, cos, sin, pos)
+    norm.close()
+    assert not calls.live
+    with pytest.raises(ValueError):
+        (qo * ko).sum().backward()

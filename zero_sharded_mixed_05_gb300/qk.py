@@ -27,11 +27,11 @@ def rotation_tables(n_pos: int, rotary_dim: int, base: float = 10000.0, device="
 
 class _Apply(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, handle, q, k, q_gain, k_gain, cos, sin, positions):
+    def forward(ctx, owner, q, k, q_gain, k_gain, cos, sin, positions):
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        zero_qk_norm_rope(handle, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions)
-        ctx.handle = handle
+        zero_qk_norm_rope(owner._handle, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions)
+        ctx.owner = owner          # the handle is there for the backward pass
         ctx.save_for_backward(q, k, q_gain, k_gain, cos, sin, positions)
         return q_out, k_out
 
@@ -42,14 +42,16 @@ class _Apply(torch.autograd.Function):
         dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
         dqg, dkg = (torch.empty_like(gain) if wanted else None
                     for gain, wanted in zip((q_gain, k_gain), ctx.needs_input_grad[3:5]))
-        zero_qk_norm_rope_backward(ctx.handle, dq_out.contiguous(), dk_out.contiguous(), q, k, dq, dk,
-                                   dqg, dkg, q_gain, k_gain, cos, sin, positions)
+        zero_qk_norm_rope_backward(ctx.owner._handle, dq_out.contiguous(), dk_out.contiguous(), q, k, dq,
+                                   dk, dqg, dkg, q_gain, k_gain, cos, sin, positions)
         return None, dq, dk, dqg, dkg, None, None, None
 
 
 class QkNormRope:
     """Owns a handle of `cfg` (with at least one key head); calls are ordered as
-    the handle's are: on one stream, or synchronized by the caller."""
+    the handle's are: on one stream, or synchronized by the caller.  The handle
+    lives until `close()`, or until neither this object nor a graph that came
+    from it is left."""
 
     def __init__(self, cfg):
         if cfg.k_heads < 1:
@@ -60,7 +62,7 @@ class QkNormRope:
         """q [tokens, q_heads, D] and k [tokens, k_heads, D] (heads contiguous),
         binary32 gains (None: ones), tables and positions as `zero_qk_norm_rope`
         takes them.  A gain that requires no gradient costs no sums."""
-        return _Apply.apply(self._handle, q, k, q_gain, k_gain, cos, sin, positions)
+        return _Apply.apply(self, q, k, q_gain, k_gain, cos, sin, positions)
 
     def close(self):
         if self._handle is not None:
