@@ -58,3 +58,25 @@ def test_a_wait_does_not_count_what_the_gpu_did_meanwhile(tmp_path):
     for paused in (early, late):
         assert hour + 1900 <= paused < hour + 1902
     assert 10000 <= seldom <= 11000
+
+
+def test_step_refuses_tensors_that_are_not_the_handles(z, handle):  # noqa: F811
+    """Before any launch: the call itself would say that there is no device."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("a CUDA device is present")
+
+    def items(**change):
+        shapes, half = [(8, 16), (2, 5, 3)], torch.float16
+        return [dict(grad=torch.zeros(s, dtype=half), momentum=torch.zeros(s), master=torch.zeros(s),
+                     param16=torch.zeros(s, dtype=half)) | change for s in shapes]
+    with pytest.raises(ValueError, match="item 0: grad"):
+        z.zero_muon_step(handle, z.make_muon_list(items()))              # tensors of the host
+    with pytest.raises(ValueError, match="2"):
+        z.zero_muon_step(handle, z.make_muon_list(items()[:1]))
+    with pytest.raises(ValueError):
+        z.zero_muon_step(handle + 8, z.make_muon_list(items()))
+    addresses = z.make_muon_list([dict(grad=16, momentum=32, master=None, param16=64)] * 2)
+    with pytest.raises(z.ZeroOptError) as e:
+        z.zero_muon_step(handle, addresses)
+    assert e.value.status == z.ZERO_ECUDA and addresses.fits is z._muon_handles[handle]

@@ -108,3 +108,45 @@ def test_a_fault_that_nobody_asked_about_is_counted(z, shapes):  # noqa: F811
             z.zero_muon_orthogonalize(h, g, out)
     finally:
         z.zero_muon_destroy(h)
+
+
+def test_step_refuses_tensors_that_are_not_the_handles(z):  # noqa: F811
+    """Another order, type, size, shape or device than the handle's: an error on
+    the host, before any launch; and the list is checked against every handle
+    that it is given to."""
+    import torch
+    shapes = [(8, 16, 1), (16, 8, 1), (4, 4, 3)]
+
+    def items(types=(torch.float16, torch.float32, torch.float32, torch.bfloat16)):
+        return [{name: torch.zeros(b, m, n, device="cuda", dtype=t)
+                 for name, t in zip(("grad", "momentum", "master", "param16"), types)} for m, n, b in shapes]
+    cfg = z.make_muon_config(grad_dtype=z.FP16, param_dtype=z.BF16)
+    h = z.zero_muon_create(cfg, shapes)
+    try:
+        good = items()
+        good[0] = {k: t[0] for k, t in good[0].items()}            # one matrix without its batch
+        good[1] = {k: t.flatten() for k, t in good[1].items()}     # a slice of a flat buffer
+        lst = z.make_muon_list(good)
+        z.zero_muon_step(h, lst)
+        launches = z.zero_muon_launch_count(h)
+        x = items()
+        bad = [x[::-1], [x[1], x[0], x[2]], x[:2], x + x[:1]]
+        for i, name, t in [(0, "grad", x[0]["grad"].bfloat16()), (1, "param16", x[1]["grad"]),
+                           (0, "momentum", x[0]["momentum"].half()), (2, "master", x[2]["param16"]),
+                           (2, "grad", x[2]["grad"][:2]), (0, "master", x[1]["master"]),
+                           (1, "momentum", x[1]["momentum"].cpu()), (2, "grad", x[2]["grad"].view(12, 4)),
+                           (0, "grad", x[0]["grad"].flatten()[:64])]:
+            bad.append([m | ({name: t} if j == i else {}) for j, m in enumerate(x)])
+        for b in bad:
+            with pytest.raises(ValueError):
+                z.zero_muon_step(h, z.make_muon_list(b))
+        other = z.zero_muon_create(z.make_muon_config(grad_dtype=z.BF16), shapes)
+        with pytest.raises(ValueError):
+            z.zero_muon_step(other, lst)
+        z.zero_muon_destroy(other)
+        with pytest.raises(ValueError):
+            z.zero_muon_step(other, lst)                           # a handle that is gone
+        assert z.zero_muon_launch_count(h) == launches
+        z.zero_muon_step(h, lst)
+    finally:
+        z.zero_muon_destroy(h)

@@ -680,8 +680,9 @@ def zero_opt_decision(h) -> int:
 
 # ---------------------------------------------------------------- orthogonalised updates
 
-# Shapes a handle was made for, so that the binding can check tensors against them.
-_muon_shapes = {}
+# What a handle was made for, so that the binding can check tensors against it:
+# (shapes, grad_dtype, param_dtype, device), an object of the handle's own.
+_muon_handles = {}
 
 
 def make_muon_config(grad_dtype=FP16, param_dtype=None, lr=2e-2, momentum=0.95, nesterov=True,
@@ -710,12 +711,21 @@ def zero_muon_create(cfg: zero_muon_config, shapes) -> int:
     h = _vp()
     _check(lib().zero_muon_create(ctypes.byref(cfg), arr, len(full), ctypes.byref(h)),
            "zero_muon_create")
-    _muon_shapes[h.value] = full
+    import torch
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    _muon_handles[h.value] = (full, cfg.grad_dtype, cfg.param_dtype, dev)
     return h.value
 
 
+def _muon_handle(h):
+    made = _muon_handles.get(h)
+    if made is None:
+        raise ValueError("not a handle of zero_muon_create")
+    return made
+
+
 def zero_muon_destroy(h) -> None:
-    _muon_shapes.pop(h, None)
+    _muon_handles.pop(h, None)
     _check(lib().zero_muon_destroy(h), "zero_muon_destroy")
 
 
@@ -735,9 +745,7 @@ def zero_muon_orthogonalize(h, ins, outs, stream=None) -> None:
     contiguous rows; all inputs of one dtype (float16, bfloat16 or float32),
     all outputs of one."""
     import torch
-    shapes = _muon_shapes.get(h)
-    if shapes is None:
-        raise ValueError("not a handle of zero_muon_create")
+    shapes = _muon_handle(h)[0]
     if len(ins) != len(shapes) or len(outs) != len(shapes):
         raise ValueError(f"{len(shapes)} inputs and outputs are wanted")
     codes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
@@ -762,28 +770,58 @@ def zero_muon_orthogonalize(h, ins, outs, stream=None) -> None:
            "zero_muon_orthogonalize")
 
 
+_MUON_ARRAYS = ("grad", "momentum", "master", "param16")
+
+
+class _MuonList(tuple):
+    """(array of zero_muon_matrix, items, their dicts), and the handle's entry
+    in `_muon_handles` that the tensors have been checked against."""
+    fits = None
+
+
 def make_muon_list(mats):
     """Per-matrix list for `zero_muon_step`; each item is a dict with grad,
-    momentum, master (or None: param16 is the master) and param16, contiguous."""
+    momentum, master (or None: param16 is the master) and param16, contiguous:
+    [batch, rows, cols], [rows, cols] of one matrix, or the same numbers in one
+    dimension (a slice of a flat buffer).  An address (int) is taken as it is."""
     arr = (zero_muon_matrix * max(len(mats), 1))()
     for i, m in enumerate(mats):
-        for name in ("grad", "momentum", "master", "param16"):
+        for name in _MUON_ARRAYS:
             t = m[name]
             if hasattr(t, "is_contiguous") and not t.is_contiguous():
                 raise ValueError(f"item {i}: {name} must be contiguous")
-        arr[i] = zero_muon_matrix(_ptr(m["grad"]), _ptr(m["momentum"]), _ptr(m["master"]),
-                                  _ptr(m["param16"]))
-    return arr, len(mats), list(mats)
+        arr[i] = zero_muon_matrix(*(_ptr(m[name]) for name in _MUON_ARRAYS))
+    return _MuonList((arr, len(mats), [dict(m) for m in mats]))
+
+
+def _muon_check(made, mats):
+    """Compare every tensor of a list with what the handle was made for."""
+    import torch
+    shapes, grad, param, dev = made
+    if mats[1] != len(shapes):
+        raise ValueError(f"the list has {mats[1]} matrices, the handle {len(shapes)}")
+    half = (torch.float16, torch.bfloat16)
+    dtypes = dict(grad=half[grad], momentum=torch.float32, master=torch.float32, param16=half[param])
+    for i, ((rows, cols, batch), m) in enumerate(zip(shapes, mats[2])):
+        for name in _MUON_ARRAYS:
+            t = m[name]
+            if t is None or isinstance(t, int):
+                continue
+            if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_cuda \
+                    or t.dtype is not dtypes[name] or t.numel() != batch * rows * cols \
+                    or not (t.dim() == 1 or t.shape[-2:] == (rows, cols)):
+                raise ValueError(f"item {i}: {name} must be a {dtypes[name]} tensor of "
+                                 f"{(batch, rows, cols)} on cuda:{dev}")
+    mats.fits = made
 
 
 def zero_muon_step(h, mats, grad_scale=1.0, decision=None, stream=None) -> None:
     """Step of every matrix (`mats` from `make_muon_list`, one item per shape of
     the handle).  `decision`: None, or the address from `zero_opt_decision`."""
-    arr, n, _ = mats
-    if n != len(_muon_shapes.get(h, ())):
-        raise ValueError(f"the list has {n} matrices, the handle "
-                         f"{len(_muon_shapes.get(h, ()))}")
-    _check(lib().zero_muon_step(h, arr, grad_scale, _ptr(decision), _stream(stream)),
+    made = _muon_handle(h)
+    if mats.fits is not made:
+        _muon_check(made, mats)
+    _check(lib().zero_muon_step(h, mats[0], grad_scale, _ptr(decision), _stream(stream)),
            "zero_muon_step")
 
 
