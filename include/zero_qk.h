@@ -12,14 +12,15 @@
  *
  * Backward, with dy the gradient of `out` rotated back:
  *   dgain = sum over tokens (and heads, for a shared gain) of dy * x * r
- *   dx    = r * dy * gain - x * r^3 * mean(dy * gain * x)
+ *   dx    = r * (dy * gain - x * r * mean(dy * gain * x * r))
  *
  * A token whose position is negative is padding: what its inputs hold (NaN
  * and infinity included) is ignored, its outputs and gradients are zero and it adds nothing to the gains' gradients.
  * A position of n_pos or more has no angle: its rows come out as NaN.
  *
- * Arithmetic is binary32 throughout; results are rounded once, to the data's
- * type.  The gains' gradients are binary32, summed in an order fixed by the
+ * Arithmetic is binary32 throughout (a row's squares have to be within its
+ * range: numbers from about 1e-18 to 1e18); results are rounded once, to the
+ * data's type.  The gains' gradients are binary32, summed in an order fixed by the
  * shapes and the device, so equal inputs give equal bits.
  *
  * Conventions are those of zero_opt.h: a zero_status from every call,

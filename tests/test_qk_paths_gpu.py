@@ -46,3 +46,52 @@ def test_gains_and_tables_at_any_address(z, numbers, per_head, name):  # noqa: F
             assert ((dg.double() - terms.sum(dims)).abs() <= tol).all()
     finally:
         z.zero_qk_destroy(h)
+
+
+@pytest.mark.parametrize("name", ["bf16", "fp32"])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_gradients_of_rows_of_any_size(z, name, per_head, monkeypatch):  # noqa: F811
+    """With eps 0 the rows' root mean square may be anything whose square
+    binary32 holds: dx is of the size of its inverse, whose cube is not held."""
+    import test_qk_gpu
+    import torch
+    monkeypatch.setattr(test_qk_gpu, "EPS", 0.0)
+    case = (11, 4, 2, 64, 64, name, False, per_head, "own")
+    q, k, qg, kg, cos, sin, pos = make(case, 31)
+    gq, gk = make(case, 32)[:2]
+    pos = pos.clamp(min=0)
+    size = 10.0 ** torch.arange(-15, 18, 3, device="cuda").double()
+    q, k = ((t.double() * size[:, None, None]).to(t.dtype) for t in (q, k))
+    h = handle(z, case)
+    try:
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        dqg, dkg = torch.empty_like(qg), torch.empty_like(kg)
+        z.zero_qk_norm_rope_backward(h, gq, gk, q, k, dq, dk, dqg, dkg, qg, kg, cos, sin, pos)
+        for d, dg, x, go, gain in ((dq, dqg, q, gq, qg), (dk, dkg, k, gk, kg)):
+            ref, mag, terms = backward64(go, x, gain, pos, cos, sin, 64, False)
+            near(d, ref, mag, name, 64)
+            dims = 0 if per_head else (0, 1)
+            scale = terms.abs().amax(-1, keepdim=True).expand_as(terms)
+            tol = (11 * x.shape[1] + 64 + 16) * 2.0 ** -24 * scale.sum(dims)
+            assert ((dg.double() - terms.sum(dims)).abs() <= tol).all()
+    finally:
+        z.zero_qk_destroy(h)
+
+
+def test_gradient_of_a_zero_row_with_a_small_eps(z, monkeypatch):  # noqa: F811
+    import test_qk_gpu
+    import torch
+    monkeypatch.setattr(test_qk_gpu, "EPS", 1e-30)
+    case = (3, 2, 1, 64, 64, "fp32", False, False, "own")
+    q, k, qg, kg, cos, sin, pos = make(case, 33)
+    gq, gk = make(case, 34)[:2]
+    q[1] = 0
+    pos[:] = torch.tensor([4, 5, 6], device="cuda")
+    h = handle(z, case)
+    try:
+        dq, dk = torch.empty_like(q), torch.empty_like(k)
+        z.zero_qk_norm_rope_backward(h, gq, gk, q, k, dq, dk, None, None, qg, kg, cos, sin, pos)
+        ref, mag, _ = backward64(gq, q, qg, pos, cos, sin, 64, False)
+        near(dq, ref, mag, "fp32", 64)
+    finally:
+        z.zero_qk_destroy(h)

@@ -369,7 +369,9 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
         }
         const float inv = rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps));
         const float2 inv2 = both(inv);
-        const float2 back = both(__fmul_rn(-__fmul_rn(inv, __fmul_rn(inv, inv)), __fmul_rn(sum_dot, a.inv_dim)));
+        // dx = inv (dn - xhat mean(dn xhat)), dn = dy gain: no power of inv but the
+        // first, so that it holds for rows of any size
+        const float2 back = both(__fmul_rn(-inv, __fmul_rn(__fmul_rn(inv, sum_dot), a.inv_dim)));
 #pragma unroll
         for (int j = 0; j < C; ++j) {
           if (!live(j)) continue;
@@ -377,8 +379,9 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3) qk_kernel(const
           for (int i = 0; i < V; ++i) {
             if constexpr (kBackward) {
               float2& d = dgain[kSum ? 0 : r][j][i];
-              d = __ffma2_rn(g[j][i], __fmul2_rn(x[j][i], inv2), d);
-              x[j][i] = __ffma2_rn(__fmul2_rn(g[j][i], gain[j][i]), inv2, __fmul2_rn(x[j][i], back));
+              const float2 xhat = __fmul2_rn(x[j][i], inv2);
+              d = __ffma2_rn(g[j][i], xhat, d);
+              x[j][i] = __ffma2_rn(__fmul2_rn(g[j][i], gain[j][i]), inv2, __fmul2_rn(xhat, back));
             } else {
               x[j][i] = __fmul2_rn(x[j][i], inv2);
             }
