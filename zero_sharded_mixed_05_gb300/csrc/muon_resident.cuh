@@ -260,6 +260,11 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
     tc_fence_before();
     __syncthreads();
   };
+  // Its threads come out of a wait one by one, and what follows is for whole warps.
+  const auto wait = [&](uint32_t at, uint32_t parity) {
+    ok = ok && mbar_wait(at, parity, fault);
+    __syncwarp();
+  };
   // Issues products once every thread's operand is written, waits for them.  The
   // issuing thread goes by its own waits: where they were met, what it issued
   // before is over.  After one that ran out it issues nothing more, and no thread
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       }
       __syncwarp();
     }
-    ok = ok && mbar_wait(bar, phase, fault);
+    wait(bar, phase);
     phase ^= 1;
     tc_fence_after();
   };
@@ -313,7 +318,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       }
       __syncwarp();
     }
-    ok = ok && mbar_wait(shares, sum_phase, fault);
+    wait(shares, sum_phase);
     for (int i = threadIdx.x; i < (int)mine * 128; i += kResidentThreads) {
       const int at = i / 128, r = i % 128;       // a row of eight columns
       float t[8];
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(kResidentThreads, kPerSm)
       }
       __syncwarp();
     }
-    ok = ok && mbar_wait(totals, sum_phase, fault);
+    wait(totals, sum_phase);
     sum_phase ^= 1;
   };
 
