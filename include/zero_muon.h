@@ -139,7 +139,8 @@ zero_status zero_muon_set_lr(zero_muon_t h, double lr);
  * ZERO_BF16 or ZERO_FP32; out_dtype likewise (binary32 results carry the
  * accuracy stated above).
  * Errors: EINVAL (NULL handle, items or pointer, a bad dtype, a row stride
- * below cols with rows > 1, a negative stride), ECUDA. */
+ * below cols with rows > 1, an out_batch below cols with batch > 1, a negative
+ * stride), ECUDA. */
 zero_status zero_muon_orthogonalize(zero_muon_t h, const zero_muon_operand* items,
                                     int32_t in_dtype, int32_t out_dtype, void* stream);
 

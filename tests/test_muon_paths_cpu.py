@@ -80,3 +80,24 @@ def test_step_refuses_tensors_that_are_not_the_handles(z, handle):  # noqa: F811
     with pytest.raises(z.ZeroOptError) as e:
         z.zero_muon_step(handle, addresses)
     assert e.value.status == z.ZERO_ECUDA and addresses.fits is z._muon_handles[handle]
+
+
+def test_results_that_lie_on_one_another_are_refused(z):  # noqa: F811
+    """As a broadcast tensor's do: they would be written by several matrices at
+    once.  Rows' strides are looked at as before."""
+    h = z.zero_muon_create(z.make_muon_config(), [(8, 16, 3)])
+    one = z.zero_muon_create(z.make_muon_config(), [(8, 16, 1)])
+    try:
+        for stride in (0, 1, 15):
+            item = (z.zero_muon_operand * 1)((0x1000, 0x2000, 16, 128, 16, stride))
+            assert z.lib().zero_muon_orthogonalize(h, item, 0, 0, None) == z.ZERO_EINVAL
+        import torch
+        if not torch.cuda.is_available():
+            for handle_, item in [(h, (0x1000, 0x2000, 16, 0, 16, 128)),      # a broadcast input
+                                  (h, (0x1000, 0x2000, 16, 128, 48, 16)),     # matrices side by side
+                                  (one, (0x1000, 0x2000, 16, 0, 16, 0))]:
+                arr = (z.zero_muon_operand * 1)(item)
+                assert z.lib().zero_muon_orthogonalize(handle_, arr, 0, 0, None) == z.ZERO_ECUDA
+    finally:
+        z.zero_muon_destroy(h)
+        z.zero_muon_destroy(one)

@@ -664,6 +664,8 @@ zero_status zero_muon_orthogonalize(zero_muon_t h, const zero_muon_operand* item
     if (e.rows > 1 && (t.in_row < e.cols || t.out_row < e.cols))
       return fail(ZERO_EINVAL, "item %d: a row stride is below its %lld columns", i,
                   (long long)e.cols);
+    if (e.batch > 1 && t.out_batch < e.cols)
+      return fail(ZERO_EINVAL, "item %d: its matrices' results lie on one another", i);
     io[i].in = t.in;
     io[i].out = t.out;
     io[i].in_row = t.in_row;

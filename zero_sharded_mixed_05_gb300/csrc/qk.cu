@@ -30,6 +30,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 #include <mutex>
 #include <new>
 
@@ -578,6 +579,10 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     for (int w = 0; w < (c.k_heads > 0 ? 2 : 1); ++w)
       if (!in[w]->data || !out[w]->data || (backward && !go[w]->data))
         return fail(ZERO_EINVAL, "a %s tensor is NULL", w ? "key" : "query");
+    for (int w = 0; w < (c.k_heads > 0 ? 2 : 1); ++w)
+      if ((b->tokens > 1 && std::abs(out[w]->token_stride) < c.head_dim) ||
+          ((w ? c.k_heads : c.q_heads) > 1 && std::abs(out[w]->head_stride) < c.head_dim))
+        return fail(ZERO_EINVAL, "rows of a %s result lie on one another", w ? "key" : "query");
     if (!b->positions) return fail(ZERO_EINVAL, "positions are NULL");
     if (c.rotary_dim > 0 && b->n_pos > 0 && (!b->cos || !b->sin))
       return fail(ZERO_EINVAL, "cos and sin must be non-NULL");
