@@ -243,6 +243,7 @@ cudaError_t ready_resident(const zero_muon_handle* h) {
 // 178.  Matrices that need fewer CTAs go in launches of
 // their own unless all fit on the device side by side.
 void choose_resident(zero_muon_t h) {
+  if (h->entries.empty()) return;
   int most = 1;
   int64_t units = 0;
   const auto span_of = [](const zm::Entry& e) {
