@@ -538,6 +538,15 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
   zero_muon_handle* h = new (std::nothrow) zero_muon_handle;
   if (!h) return fail(ZERO_ENOMEM, "handle allocation failed");
   h->cfg = *cfg;
+  int count = 0;
+  const bool device = cudaGetDeviceCount(&count) == cudaSuccess && count > 0;
+  cudaError_t e = cudaSuccess;
+  if (device) {
+    e = cudaGetDevice(&h->device);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
+  } else {
+    cudaGetLastError();  // clear the sticky "no device" error
+  }
   int64_t units = 0;
   try {
     h->shapes.assign(shapes, shapes + n);
@@ -569,7 +578,8 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
     // two and one; 14336x4096: 2646 at 16 blocks, 2607 at 8.)
     int64_t blocks = 0;
     for (const zm::Entry& e : h->entries) blocks += (int64_t)e.batch * ((e.rows + 31) / 32) * e.across;
-    h->call.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, (blocks + 8 * 152 * 3 - 1) / (8 * 152 * 3)));
+    const int64_t wave = (int64_t)(zm::kThreads / 32) * 3 * std::max(h->sms, 1);
+    h->call.blocks = (int32_t)std::max<int64_t>(1, std::min<int64_t>(8, (blocks + wave - 1) / wave));
     const int64_t chunk = h->call.blocks * (zm::kThreads / 32);
     double tiles = 0;
     for (zm::Entry& e : h->entries) {
@@ -593,15 +603,10 @@ zero_status zero_muon_create(const zero_muon_config* cfg, const zero_muon_shape*
   h->call.eps = cfg->eps;
   h->call.mu = (float)cfg->momentum;
   h->call.nesterov = cfg->nesterov;
-  int count = 0;
-  if (cudaGetDeviceCount(&count) != cudaSuccess || count < 1) {
-    cudaGetLastError();  // clear the sticky "no device" error
+  if (!device) {
     *out = h;            // host-only handle
     return ZERO_OK;
   }
-  cudaError_t e = cudaGetDevice(&h->device);
-  if (e == cudaSuccess)
-    e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   try {
     if (e == cudaSuccess) e = place(h);
   } catch (const std::bad_alloc&) {
