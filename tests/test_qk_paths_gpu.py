@@ -95,3 +95,50 @@ def test_gradient_of_a_zero_row_with_a_small_eps(z, monkeypatch):  # noqa: F811
         near(dq, ref, mag, "fp32", 64)
     finally:
         z.zero_qk_destroy(h)
+
+
+# More tokens than a wave of groups: each walks several, through both places of
+# its ring and the next token's angles; two and four heads a group where head
+# counts divide and rows are enough (19,456 and 38,912 of 128 numbers in 16 bits).
+MANY = [
+    (4500, 32, 8, 128, 128, "bf16", False, False, "fused"),     # four heads a group; backward two, summed together
+    (4501, 32, 8, 128, 128, "fp16", True, True, "fused"),       # a gain a head
+    (3500, 6, 2, 128, 64, "bf16", False, False, "own"),         # two heads, half of each turned
+    (4200, 32, 8, 64, 64, "bf16", False, False, "heads_first"),
+    (2300, 16, 16, 128, 128, "fp32", False, False, "own"),      # two heads of binary32
+    (2100, 16, 4, 256, 256, "fp32", True, True, "fused"),
+    (4300, 12, 12, 80, 40, "fp16", True, False, "fused"),       # 8-byte vectors
+    (4300, 12, 4, 96, 48, "bf16", False, True, "fused"),
+    (2500, 20, 4, 128, 128, "bf16", False, False, "odd"),       # single numbers
+    (2500, 5, 3, 66, 34, "fp32", False, True, "odd"),
+    (15000, 4, 0, 128, 128, "bf16", False, False, "own"),       # queries alone
+    (12001, 1, 1, 128, 128, "bf16", False, False, "fused"),     # heads that do not divide
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_many_tokens(z, case):  # noqa: F811
+    import test_qk_gpu
+    import torch
+    test_qk_gpu.test_forward(z, case, False)
+    if case[2] > 0:
+        return test_qk_gpu.test_backward(z, case)
+    # queries alone: what belongs to keys is not looked at
+    T, hq, _, D, rot, name, inter, per_head, _ = case
+    q, _, qg, _, cos, sin, pos = make(case, 2)
+    go = make(case, 3)[0]
+    h = handle(z, case)
+    try:
+        runs = []
+        for _ in range(2):
+            dq, dqg = torch.full_like(q, float("nan")), torch.full_like(qg, float("nan"))
+            z.zero_qk_norm_rope_backward(h, go, None, q, None, dq, None, dqg, None, qg, None, cos, sin, pos)
+            runs.append((dq, dqg))
+        ref, mag, terms = backward64(go, q, qg, pos, cos, sin, rot, inter)
+        near(dq, ref, mag, name, D)
+        scale = terms.abs().amax(-1, keepdim=True).expand_as(terms)
+        tol = (T * hq + D + 16) * 2.0 ** -24 * scale.sum((0, 1))
+        assert ((dqg.double() - terms.sum((0, 1))).abs() <= tol).all()
+        assert all(torch.equal(a, b) for a, b in zip(*runs))
+    finally:
+        z.zero_qk_destroy(h)
