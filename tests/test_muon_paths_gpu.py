@@ -327,3 +327,28 @@ def test_odd_addresses_through_the_workspace(z):  # noqa: F811
             assert got[name]._base[0] == 5 and got[name]._base[-1] == 5
     finally:
         z.zero_muon_destroy(h)
+
+
+@pytest.mark.parametrize("m,n", [(100, 60), (70, 900), (300, 200)])
+def test_strides_past_32_bits(z, m, n):  # noqa: F811
+    """Rows and matrices that lie more than 2^32 bytes and 2^31 numbers apart,
+    one CTA, a cluster and the workspace."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    g = torch.randn(2, m, n, device="cuda", generator=gen).bfloat16()
+    want = torch.empty_like(g)
+    store = torch.empty(5_000_000_000, device="cuda", dtype=torch.bfloat16)
+    h = z.zero_muon_create(z.make_muon_config(), [(m, n, 2)])
+    try:
+        z.zero_muon_orthogonalize(h, [g], [want])
+        close(want, ortho64(g), "bf16")
+        row = 4_700_000_000 // m
+        for strides in ((2_400_000_000, n, 1), (n, row, 1)):     # matrices, then rows far apart
+            far = store.as_strided((2, m, n), strides, 8)
+            far.copy_(g)
+            z.zero_muon_orthogonalize(h, [far], [far])
+            close(far, ortho64(g), "bf16")
+    finally:
+        z.zero_muon_destroy(h)
+        del store, far
+        torch.cuda.empty_cache()

@@ -142,3 +142,32 @@ def test_many_tokens(z, case):  # noqa: F811
         assert all(torch.equal(a, b) for a, b in zip(*runs))
     finally:
         z.zero_qk_destroy(h)
+
+
+@pytest.mark.parametrize("head,token", [(64, 110_000_000), (1_100_000_000, 64)])
+def test_strides_past_32_bits(z, head, token):  # noqa: F811
+    """Tokens or heads more than 2^31 numbers from the first."""
+    import torch
+    case = (40, 4, 1, 64, 64, "bf16", False, False, "own")
+    q, k, qg, kg, cos, sin, pos = make(case, 41)
+    gq, gk = make(case, 42)[:2]
+    store = torch.empty(4_500_000_000, device="cuda", dtype=torch.bfloat16)
+    h = handle(z, case)
+    try:
+        def spread(t):
+            far = store.as_strided(t.shape, (token, head, 1), 8)
+            far.copy_(t)
+            return far
+        qo, ko, q1, k1 = (torch.empty_like(t) for t in (q, k, q, k))
+        z.zero_qk_norm_rope(h, q, k, qo, ko, qg, kg, cos, sin, pos)
+        far = spread(q)
+        z.zero_qk_norm_rope(h, far, k, far, k1, qg, kg, cos, sin, pos)
+        assert torch.equal(far, qo) and torch.equal(k1, ko)
+        z.zero_qk_norm_rope_backward(h, gq, gk, q, k, q1, k1, None, None, qg, kg, cos, sin, pos)
+        far = spread(gq)
+        z.zero_qk_norm_rope_backward(h, far, gk, q, k, far, ko, None, None, qg, kg, cos, sin, pos)
+        assert torch.equal(far, q1) and torch.equal(ko, k1)
+    finally:
+        z.zero_qk_destroy(h)
+        del store, far
+        torch.cuda.empty_cache()
