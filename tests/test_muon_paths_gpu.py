@@ -352,3 +352,27 @@ def test_strides_past_32_bits(z, m, n):  # noqa: F811
         z.zero_muon_destroy(h)
         del store, far
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["gauss", "signal", "rank1", "decay"])
+@pytest.mark.parametrize("k,l", [(1, 3), (2, 2), (3, 12), (5, 6), (8, 8), (13, 40), (16, 17), (31, 31), (32, 40),
+                                 (64, 64), (128, 130), (2, 3000), (130, 160)])
+def test_accuracy_by_size(z, k, l, kind):  # noqa: F811
+    """What zero_muon.h states.  With a shorter side of 32 or more the bound that
+    test_muon_gpu.py derives from roundings that average out, for each matrix.
+    Below, of few numbers, each of the fifteen roundings (2^-12 at most) may go
+    the same way, times the same |b| + 2 |c|: 15 * 2^-12 * 8.84 = 3.2e-2; over
+    many matrices they average out again, and the mean square has the first bound."""
+    import torch
+    b = max(4, min(500, 2_000_000 // (k * l)))
+    g = spectrum(kind, b, k, l, torch.Generator(device="cuda").manual_seed(7 * k + l))
+    h = z.zero_muon_create(z.make_muon_config(), [(k, l, b)])
+    try:
+        out = torch.empty_like(g)
+        z.zero_muon_orthogonalize(h, [g], [out])
+        ref = ortho64(g)
+        off = (out.double() - ref).flatten(-2).norm(dim=-1) / ref.flatten(-2).norm(dim=-1)
+        assert off.max() <= (4.8e-3 if k >= 32 else 3.2e-2), off.max()
+        assert off.square().mean().sqrt() <= 4.8e-3
+    finally:
+        z.zero_muon_destroy(h)
