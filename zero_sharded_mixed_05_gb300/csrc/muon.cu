@@ -125,7 +125,8 @@ cudaLaunchConfig_t products_config(zero_muon_t h, cudaLaunchAttribute* attr, cud
 // Parts that the depth of X X^T (`stages` of 128) is cut into, so that `tiles`
 // tiles of it keep `slots` CTAs or pairs busy.  Each is at least eight stages
 // deep and there are three at least, or the adding up costs what it saves
-// (whole against cut: 8080x80 x 2 180 and 121 us, 300x5000 160 and 136; in two
+// (whole against cut: 8080x80 x 2 176 and 116 us, 300x5000 152 and 133, 11840x80
+// x 24 483 and 368, 700x3000 in three of eight stages 140 and 140; in two
 // 1024x4096 x 2 238 and 246, of four stages 400x1800 x 4 130 and 142).
 int32_t splits_of(int64_t tiles, int64_t slots, int32_t stages) {
   const int64_t want = std::min<int64_t>({slots / std::max<int64_t>(tiles, 1), stages / 8, 8});
@@ -139,8 +140,14 @@ int32_t splits_of(int64_t tiles, int64_t slots, int32_t stages) {
 // CTA's 128 x 128, 1060 for a pair's 256 x 256, whose tensor work alone is 512
 // and 1024; a tile's epilogue at 3000 and 5500 where that is more), and a fixed
 // part a product (from a tile's needs being met to its count: 5500 and 7500).
+// A part of a cut tile writes its sums and the last reads them all: 2500 and
+// 5000 a part, by which twenty shapes of 150x4000 to 1536x12000 choose the
+// faster, or one within 2 %, with 4000 to 6000 as well; cuts at 2500 in all took
+// pairs of 1024x4096 x 2, 1536x4000 and 768x4000 x 3 (257, 307 and 251 us).
 // Measured, singles against pairs: 768x768 x 12 174 and
-// 186 us, 2048x2048 215 and 241, 1536x1536 x 4 305 and 267, 4096x4096 1164 and 922.
+// 186 us, 2048x2048 215 and 241, 1536x1536 x 4 305 and 267, 4096x4096 1164 and
+// 922; 1024x4096 x 2 235 and 257, 1536x4000 256 and 307, 768x4000 x 3 232 and 251;
+// 1000x8000 x 2 405 and 364, 768x8000 x 4 516 and 426, 1536x12000 590 and 496.
 double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
   const int tile = 128 * pair, slots = std::max(1, sms / pair);
   double tiles[2] = {0, 0}, work[3] = {0, 0, 0};
@@ -161,7 +168,7 @@ double products_cost(const std::vector<zm::Entry>& entries, int pair, int sms) {
       const int32_t deep = (int32_t)(work[0] / n);
       const int32_t parts = splits_of((int64_t)n, slots, deep);
       if (parts > 1) {
-        cycles += deep / parts * (pair == 2 ? 1060 : 740) + (pair == 2 ? 7500 : 5500) + 2500;
+        cycles += deep / parts * (pair == 2 ? 1060 : 740) + (pair == 2 ? 7500 : 5500) + parts * (pair == 2 ? 5000 : 2500);
         continue;
       }
     }

@@ -31,7 +31,7 @@
 //
 // A deep X X^T of few tiles (k x k of a matrix with l far above k) is cut along
 // its depth: each part leaves its binary32 sums in the workspace, and the one
-// that arrives last adds them up in order and goes on (8080x80 x 2: 180 -> 116 us).
+// that arrives last adds them up in order and goes on (8080x80 x 2: 176 -> 116 us).
 //
 // The diagonals of A and of b A + c A A are near one where everything else is
 // small, so most of the rounding error would come from them.  A's is kept in
