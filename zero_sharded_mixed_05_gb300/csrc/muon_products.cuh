@@ -536,10 +536,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       // The epilogue's second part of X, which no operand brings: this CTA's 128
       // rows of the tile are one run.  For products that are over before it has
-      // come.  (36 of 11840x80: 600 us without, 536 with it; 2304x768 x 12 336 and
-      // 328; but 768x768 x 12, whose X stays in L2, 166 and 172, and the step on
-      // seven matrices 4096 deep 11.40 and 11.54 ms.)
-      if (p.far && side && t.which == 2 && depth <= 1024) {
+      // come.  (36 of 11840x80: 603 us without, 540 with it; 2304x768 x 12 340 and
+      // 335, 768x2304 x 24 618 and 616; but 3000x1000 x 12 623 and 632, 4096x2048 x 4
+      // 940 and 957, the step on seven matrices 4096 deep 11.40 and 11.54 ms, and
+      // 768x768 x 12, whose X stays in L2, 166 and 172.)
+      if (p.far && side && t.which == 2 && depth <= 768) {
         const int row = t.i * kTile + (int)rank * 128, col = t.j * kTile;
         if (row < t.e.rows && elected())
           prefetch_l2(t.e.lo + b * block_size(t.e.rows, t.e.ldx) + block_at(row, col, t.e.ldx),
