@@ -312,9 +312,10 @@ __device__ __forceinline__ void clear(const Call& c, const Entry& e, int b) {
 }
 
 // Stage 1.  Bound by memory: the step reads 2 + 4 bytes a number and writes 4.
-// Squares are added in binary32 within a thread's 64 numbers and in binary64
-// beyond; the last CTA of a matrix adds the CTAs' sums in index order.  Of a
-// matrix that one CTA holds the numbers are still there: it writes X at once.
+// Squares are added in binary32 within a thread's 32 numbers of a block and its
+// blocks (256 numbers at most) and in binary64 beyond; the last CTA of a matrix
+// adds the CTAs' sums in index order.  Of a matrix that one CTA holds the
+// numbers are still there: it writes X at once.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads, 3) muon_stats_kernel(const __grid_constant__ Start<N> s) {
   const Call& c = s.c;

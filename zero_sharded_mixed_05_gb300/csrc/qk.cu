@@ -664,9 +664,9 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   // instructions a row, as long as both head counts divide and the tokens
   // still fill the device.  The most: what the ring and the registers leave two
   // or three CTAs an SM for (16,384 tokens, 40 heads of 128: forward 58 us with
-  // four, 65 with two; backward 100 with two, 121 with one; with sums a head,
-  // 20 heads of 64, backward 46 with one, 52 with two when that was measured, 41
-  // now that one keeps its gain in registers).
+  // four, 64 with two, 81 with one; backward 100 with two, 122 with one; with sums
+  // a head, which keep one head's gain in registers, 8,192 tokens of 40 heads of
+  // 128 67 with one, 75 with two, 16,384 of 20 heads of 64 39 and 43).
   int r = 1;
   const int most_r = es_vec < 16 ? 1 : v == 8 ? (!backward ? 4 : sum ? 2 : 1) : (backward ? 1 : 2);
   while (2 * r <= most_r && c.q_heads % (2 * r) == 0 && c.k_heads % (2 * r) == 0 &&
