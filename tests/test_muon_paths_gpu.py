@@ -126,6 +126,7 @@ def test_step_refuses_tensors_that_are_not_the_handles(z):  # noqa: F811
         good = items()
         good[0] = {k: t[0] for k, t in good[0].items()}            # one matrix without its batch
         good[1] = {k: t.flatten() for k, t in good[1].items()}     # a slice of a flat buffer
+        good[2] = {k: t.view(12, 4) for k, t in good[2].items()}   # all matrices' rows
         lst = z.make_muon_list(good)
         z.zero_muon_step(h, lst)
         launches = z.zero_muon_launch_count(h)
@@ -134,7 +135,7 @@ def test_step_refuses_tensors_that_are_not_the_handles(z):  # noqa: F811
         for i, name, t in [(0, "grad", x[0]["grad"].bfloat16()), (1, "param16", x[1]["grad"]),
                            (0, "momentum", x[0]["momentum"].half()), (2, "master", x[2]["param16"]),
                            (2, "grad", x[2]["grad"][:2]), (0, "master", x[1]["master"]),
-                           (1, "momentum", x[1]["momentum"].cpu()), (2, "grad", x[2]["grad"].view(12, 4)),
+                           (1, "momentum", x[1]["momentum"].cpu()), (2, "grad", x[2]["grad"].view(6, 8)),
                            (0, "grad", x[0]["grad"].flatten()[:64])]:
             bad.append([m | ({name: t} if j == i else {}) for j, m in enumerate(x)])
         for b in bad:

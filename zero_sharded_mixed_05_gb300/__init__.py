@@ -782,7 +782,7 @@ class _MuonList(tuple):
 def make_muon_list(mats):
     """Per-matrix list for `zero_muon_step`; each item is a dict with grad,
     momentum, master (or None: param16 is the master) and param16, contiguous:
-    [batch, rows, cols], [rows, cols] of one matrix, or the same numbers in one
+    [batch, rows, cols], [batch * rows, cols], or the same numbers in one
     dimension (a slice of a flat buffer).  An address (int) is taken as it is."""
     arr = (zero_muon_matrix * max(len(mats), 1))()
     for i, m in enumerate(mats):
@@ -809,7 +809,8 @@ def _muon_check(made, mats):
                 continue
             if not isinstance(t, torch.Tensor) or t.get_device() != dev or not t.is_cuda \
                     or t.dtype is not dtypes[name] or t.numel() != batch * rows * cols \
-                    or not (t.dim() == 1 or t.shape[-2:] == (rows, cols)):
+                    or not (t.dim() == 1 or t.shape[-2:] == (rows, cols)
+                            or t.shape == (batch * rows, cols)):
                 raise ValueError(f"item {i}: {name} must be a {dtypes[name]} tensor of "
                                  f"{(batch, rows, cols)} on cuda:{dev}")
     mats.fits = made
