@@ -137,6 +137,37 @@ class zero_qk_buffers(ctypes.Structure):
                 ("positions64", _i32), ("reserved", _i32)]
 
 
+GATE_NONE, GATE_PLAIN, GATE_SIGMOID = range(3)
+
+
+class zero_rng(ctypes.Structure):
+    _fields_ = [("seed", ctypes.c_uint64), ("step", _i64), ("step_dev", _vp),
+                ("call", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class zero_block_config(ctypes.Structure):
+    _fields_ = [("dim", _i32), ("dtype", _i32), ("stream_dtype", _i32), ("norm_branch", _i32),
+                ("norm_out", _i32), ("gate", _i32), ("reserved", _i32 * 2), ("eps", _f64),
+                ("alpha", _f64), ("beta", _f64), ("dropout", _f64)]
+
+
+class zero_block_rows(ctypes.Structure):
+    _fields_ = [("data", _vp), ("stride", _i64)]
+
+
+class zero_block_buffers(ctypes.Structure):
+    _fields_ = [("tokens", _i64)] + [(n, zero_block_rows) for n in (
+        "x", "y", "gate", "x_out", "h", "dx_out", "dh", "dx", "dy", "dgate")] + [
+        ("y_gain", _vp), ("gain", _vp), ("dy_gain", _vp), ("dgain", _vp), ("mask", _vp),
+        ("rng", zero_rng)]
+
+
+class zero_drop_buffers(ctypes.Structure):
+    _fields_ = [("in_", _vp), ("out", _vp), ("rows", _i64), ("cols", _i64), ("in_stride", _i64),
+                ("out_stride", _i64), ("dtype", _i32), ("reserved", _i32), ("p", _f64),
+                ("rng", zero_rng)]
+
+
 class ZeroOptError(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         super().__init__(f"{where}: status {status}: {message}")
@@ -207,6 +238,12 @@ SIGNATURES = [
     ("zero_qk_norm_rope", _i32, [_vp, _vp, _vp]),
     ("zero_qk_norm_rope_backward", _i32, [_vp, _vp, _vp]),
     ("zero_qk_launch_count", _i32, [_vp, _P(_i64)]),
+    ("zero_block_create", _i32, [_P(zero_block_config), _P(_vp)]),
+    ("zero_block_destroy", _i32, [_vp]),
+    ("zero_block_join", _i32, [_vp, _vp, _vp]),
+    ("zero_block_join_backward", _i32, [_vp, _vp, _vp]),
+    ("zero_block_launch_count", _i32, [_vp, _P(_i64)]),
+    ("zero_dropout", _i32, [_vp, _vp]),
     ("zero_opt_status_string", ctypes.c_char_p, [_i32]),
     ("zero_opt_last_error", ctypes.c_char_p, []),
 ]
@@ -976,3 +1013,181 @@ def zero_qk_launch_count(h) -> int:
     out = _i64()
     _check(lib().zero_qk_launch_count(h, ctypes.byref(out)), "zero_qk_launch_count")
     return out.value
+
+
+# ---------------------------------------------------------------- join of a block with the stream, dropout
+
+# What a handle was made for (dim, dtype, stream dtype, norm_out, gated, dropout,
+# device), and memory for one call's zero_block_buffers (calls on one handle are
+# ordered).
+_block_handles = {}
+_block_pack = struct.Struct("=26qQqqII").pack_into
+_drop_pack = struct.Struct("=6qiidQqqII").pack_into
+
+
+def make_block_config(dim, dtype=BF16, stream_dtype=None, norm_branch=False, norm_out=True,
+                      gate=GATE_NONE, eps=1e-6, alpha=1.0, beta=1.0, dropout=0.0) -> zero_block_config:
+    """`stream_dtype` None: as `dtype`; otherwise FP32 beside it."""
+    return zero_block_config(dim, dtype, dtype if stream_dtype is None else stream_dtype,
+                             int(norm_branch), int(norm_out), gate, (_i32 * 2)(), eps, alpha, beta,
+                             dropout)
+
+
+def zero_block_create(cfg: zero_block_config) -> int:
+    h = _vp()
+    _check(lib().zero_block_create(ctypes.byref(cfg), ctypes.byref(h)), "zero_block_create")
+    import torch
+    types = (torch.float16, torch.bfloat16, torch.float32)
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
+    b = zero_block_buffers()
+    _block_handles[h.value] = (cfg.dim, types[cfg.dtype], types[cfg.stream_dtype], bool(cfg.norm_out),
+                               cfg.gate != GATE_NONE, dev, b, ctypes.addressof(b))
+    return h.value
+
+
+def zero_block_destroy(h) -> None:
+    _block_handles.pop(h, None)
+    _check(lib().zero_block_destroy(h), "zero_block_destroy")
+
+
+def _rows(t, name, n, dim, dtype, dev):
+    """(address, row stride) of a [tokens, dim] tensor."""
+    st, sd = t.stride() if t.dim() == 2 else (0, 0)
+    if t.dtype is not dtype or t.shape != (n, dim) or t.get_device() != dev or (sd != 1 and dim > 1):
+        _qk_refuse(name, f"a {dtype} tensor of {(n, dim)} with contiguous rows on cuda:{dev}")
+    return t.data_ptr(), st
+
+
+def _rng(seed, call, step, dev):
+    """The last fields of a call: (seed, step, address of a step on the device, call, 0)."""
+    if not 0 <= seed < 2 ** 64 or not 0 <= call < 2 ** 32:
+        raise ValueError("seed must be in 0..2^64-1 and call in 0..2^32-1")
+    if type(step) is int:
+        if not -2 ** 63 <= step < 2 ** 63:
+            raise ValueError("step must be a 64-bit integer")
+        return seed, step, 0, call, 0
+    import torch
+    if step.dtype is not torch.int64 or step.numel() != 1 or step.get_device() != dev:
+        _qk_refuse("step", f"an integer or a torch.int64 tensor of one number on cuda:{dev}")
+    return seed, 0, step.data_ptr(), call, 0
+
+
+def _own_stream(stream, dev):
+    if stream is None and dev >= 0:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+_NO_ROWS = (0, 0)
+
+
+def _block_small(y_gain, gain, dy_gain, dgain, mask, n, dim, dev):
+    import torch
+    f32, shape = torch.float32, (dim,)
+    out = [0 if g is None else _qk_flat(g, name, shape, f32, dev)
+           for name, g in (("y_gain", y_gain), ("gain", gain), ("dy_gain", dy_gain), ("dgain", dgain))]
+    if mask is None:
+        return (*out, 0)
+    return (*out, _qk_flat(mask, "mask", (n,), torch.uint8 if mask.dtype is torch.uint8 else torch.bool, dev))
+
+
+def _block_handle(h):
+    if h not in _block_handles:
+        raise ValueError("not a handle of zero_block_create")
+    return _block_handles[h]
+
+
+def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, seed=0, call=0, step=0,
+                    stream=None) -> None:
+    """Join a block's output `y` [tokens, D] to the stream `x` into `x_out`
+    (None: not wanted), and normalise that into `h_out` (None without norm_out).
+    `y` None: `x` is only normalised.  Gains are float32 [D] or None (ones);
+    `mask` is bool [tokens], False for padding, whose results are zero.  `seed`,
+    `call` and `step` (an integer, or an int64 tensor on the device) choose the
+    dropped numbers."""
+    dim, dtype, sdtype, norm, gated, dev, b, at = _block_handle(h)
+    n = x.shape[0]
+    px = _rows(x, "x", n, dim, sdtype, dev)
+    py = pg = pxo = ph = _NO_ROWS
+    if y is not None:
+        py = _rows(y, "y", n, dim, dtype, dev)
+        if gated and gate is not None:
+            pg = _rows(gate, "gate", n, dim, dtype, dev)
+        if x_out is not None:
+            pxo = _rows(x_out, "x_out", n, dim, sdtype, dev)
+    if norm and h_out is not None:
+        ph = _rows(h_out, "h_out", n, dim, dtype, dev)
+    _block_pack(b, 0, n, *px, *py, *pg, *pxo, *ph, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+                *_block_small(y_gain, gain, None, None, mask, n, dim, dev), *_rng(seed, call, step, dev))
+    status = lib().zero_block_join(h, at, _own_stream(stream, dev))
+    if status:
+        _check(status, "zero_block_join")
+
+
+def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_gain, gain, gate=None,
+                             dgate=None, mask=None, seed=0, call=0, step=0, stream=None) -> None:
+    """Gradients of `zero_block_join`: from `dx_out` and `dh` (either may be
+    None: zero), the forward call's `x_out` (without `y`: its `x`), `y` and
+    `gate` into `dx`, `dy`, `dgate` and the gains' float32 gradients (None: not
+    wanted).  The rng is the forward call's."""
+    dim, dtype, sdtype, norm, gated, dev, b, at = _block_handle(h)
+    n = x_out.shape[0]
+    px = _rows(x_out, "x_out", n, dim, sdtype, dev)
+    py = pg = pdxo = pdh = pdx = pdy = pdg = _NO_ROWS
+    if dx_out is not None:
+        pdxo = _rows(dx_out, "dx_out", n, dim, sdtype, dev)
+    if norm and dh is not None:
+        pdh = _rows(dh, "dh", n, dim, dtype, dev)
+    if dx is not None:
+        pdx = _rows(dx, "dx", n, dim, sdtype, dev)
+    if y is not None:
+        py = _rows(y, "y", n, dim, dtype, dev)
+        if dy is not None:
+            pdy = _rows(dy, "dy", n, dim, dtype, dev)
+        if gated and gate is not None:
+            pg = _rows(gate, "gate", n, dim, dtype, dev)
+        if gated and dgate is not None:
+            pdg = _rows(dgate, "dgate", n, dim, dtype, dev)
+    _block_pack(b, 0, n, 0, 0, *py, *pg, *px, 0, 0, *pdxo, *pdh, *pdx, *pdy, *pdg,
+                *_block_small(y_gain, gain, dy_gain, dgain, mask, n, dim, dev),
+                *_rng(seed, call, step, dev))
+    status = lib().zero_block_join_backward(h, at, _own_stream(stream, dev))
+    if status:
+        _check(status, "zero_block_join_backward")
+
+
+def zero_block_launch_count(h) -> int:
+    out = _i64()
+    _check(lib().zero_block_launch_count(h, ctypes.byref(out)), "zero_block_launch_count")
+    return out.value
+
+
+def zero_dropout(x, out, p, seed=0, call=0, step=0, stream=None) -> None:
+    """Dropout of `x` into `out` (which may be `x`); of a gradient the same call
+    with the same `seed`, `call` and `step`.  The last dimension is the row's;
+    two dimensions may have any row stride, others are contiguous."""
+    import torch
+    dev = x.get_device()
+    if x.dim() == 2 and out.dim() == 2:
+        rows, cols = x.shape
+        (si, ui), (so, uo) = x.stride(), out.stride()
+        rowwise = cols <= 1 or (ui == 1 and uo == 1)
+    else:
+        cols = x.shape[-1] if x.dim() else 1
+        rows = x.numel() // cols if cols else 0
+        si = so = cols
+        rowwise = x.is_contiguous() and out.is_contiguous()
+    dtypes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
+    if x.dtype not in dtypes or dev < 0 or not rowwise:
+        _qk_refuse("x", "a 16-bit or float32 tensor with contiguous rows on a CUDA device")
+    if out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
+        _qk_refuse("out", f"a {x.dtype} tensor of {tuple(x.shape)} on cuda:{dev}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"x is on cuda:{dev}, which is not the current device")
+    b = zero_drop_buffers()
+    _drop_pack(b, 0, x.data_ptr(), out.data_ptr(), rows, cols, si, so, dtypes[x.dtype], 0, p,
+               *_rng(seed, call, step, dev))
+    status = lib().zero_dropout(ctypes.addressof(b), _own_stream(stream, dev))
+    if status:
+        _check(status, "zero_dropout")

@@ -1,0 +1,441 @@
+// block.cu -- the host side of the join of a block with the residual stream
+// (zero_block.h): checks, choice of kernel and launch shape; the sums of the
+// gains' gradients over CTAs; and dropout by itself.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdlib>
+#include <mutex>
+#include <new>
+
+#include "block_host.h"
+#include "block_kernels.cuh"
+#include "host_util.h"
+
+namespace {
+
+using zo::Drop;
+using zo::fail;
+using zo::JoinArgs;
+using zo::JoinRow;
+using zo::Num;
+using zo::Vec;
+
+constexpr int kMaxDim = 16384;
+constexpr int kMaxDim32 = 8192;          // of binary32 blocks: a row of each tensor fits shared memory
+constexpr int kMaxSmem = 227 * 1024 - 1024;
+constexpr int kMaxPerSm = 4;             // CTAs an SM
+
+struct FoldArgs {
+  const float* part;
+  float* out[2];
+  int32_t grid, dim;
+};
+
+// Sums the CTAs' partial gradients in index order: 32 columns a CTA, 8 threads a
+// column, each over every eighth partial.
+__global__ void __launch_bounds__(256) join_fold_kernel(const __grid_constant__ FoldArgs a) {
+  __shared__ float s[8][33];
+  cudaGridDependencySynchronize();   // launched while the partials are still written
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32, cols = 2 * a.dim;
+  float sum = 0.0f;
+  if (col < cols) {
+    const float* at = a.part + col;
+    int c = part;
+    for (; c + 56 < a.grid; c += 64) {
+      float v[8];                    // eight loads on their way at once
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = at[(int64_t)(c + 8 * k) * cols];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum = __fadd_rn(sum, v[k]);
+    }
+#pragma unroll 4
+    for (; c < a.grid; c += 8) sum = __fadd_rn(sum, at[(int64_t)c * cols]);
+  }
+  s[part][threadIdx.x % 32] = sum;
+  __syncthreads();
+  if (part == 0 && col < cols) {
+    for (int k = 1; k < 8; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
+    float* out = a.out[col >= a.dim];
+    if (out) out[col >= a.dim ? col - a.dim : col] = sum;
+  }
+}
+
+struct DropArgs {
+  const char* in;
+  char* out;
+  int64_t rows, blocks;        // blocks of eight a row
+  int64_t cols, in_stride, out_stride;   // strides in bytes
+  Drop drop;
+};
+
+// A block of eight a thread and step; kWide: rows on 16-byte boundaries.
+// Otherwise a warp takes 256 numbers of a row, which pass through shared memory
+// so that global memory is read and written 32 numbers next to one another.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropArgs a) {
+  constexpr int kE = 16 / (int)sizeof(T), kV = 8 / kE;
+  const uint32_t step = zo::step_of(a.drop);
+  const auto apply = [&](Vec<T, kE>* p, int64_t block) {
+    const uint32_t bits = zo::kept(a.drop, step, block);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      float2 x = Num<T>::get2(p[i / kE].v + i % kE);
+      x = make_float2(bits >> i & 1 ? __fmul_rn(x.x, a.drop.factor) : 0.0f,
+                      bits >> i & 2 ? __fmul_rn(x.y, a.drop.factor) : 0.0f);
+      Num<T>::put2(p[i / kE].v + i % kE, x);
+    }
+  };
+  if constexpr (kWide) {
+    const int64_t n = a.rows * a.blocks, stride = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < n; b += stride) {
+      const int64_t row = a.rows == 1 ? 0 : b / a.blocks, c = b - row * a.blocks;
+      const T* from = reinterpret_cast<const T*>(a.in + row * a.in_stride) + c * 8;
+      T* to = reinterpret_cast<T*>(a.out + row * a.out_stride) + c * 8;
+      const int64_t left = a.cols - c * 8;
+      Vec<T, kE> p[kV];
+      if (left >= 8) {
+#pragma unroll
+        for (int v = 0; v < kV; ++v) p[v] = reinterpret_cast<const Vec<T, kE>*>(from)[v];
+        apply(p, b);
+#pragma unroll
+        for (int v = 0; v < kV; ++v) reinterpret_cast<Vec<T, kE>*>(to)[v] = p[v];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i / kE].v[i % kE] = i < left ? from[i] : Num<T>::put(0.0f);
+        apply(p, b);
+#pragma unroll
+        for (int i = 0; i < 7; ++i)
+          if (i < left) to[i] = p[i / kE].v[i % kE];
+      }
+    }
+  } else {
+    __shared__ alignas(16) T s_tile[8][256];
+    T* tile = s_tile[threadIdx.x / 32];
+    const int l = threadIdx.x % 32;
+    const int64_t per = (a.cols + 255) / 256, n = a.rows * per;
+    for (int64_t w = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; w < n; w += (int64_t)gridDim.x * 8) {
+      const int64_t row = w / per, begin = (w - row * per) * 256;
+      const T* from = reinterpret_cast<const T*>(a.in + row * a.in_stride);
+      T* to = reinterpret_cast<T*>(a.out + row * a.out_stride);
+      T x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t e = begin + k * 32 + l;
+        x[k] = e < a.cols ? from[e] : Num<T>::put(0.0f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) tile[k * 32 + l] = x[k];
+      __syncwarp();
+      apply(reinterpret_cast<Vec<T, kE>*>(tile + 8 * l), row * a.blocks + begin / 8 + l);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t e = begin + k * 32 + l;
+        if (e < a.cols) to[e] = tile[k * 32 + l];
+      }
+      __syncwarp();
+    }
+  }
+}
+
+zero_status cuda_fail(cudaError_t e, const char* what) {
+  return fail(ZERO_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+int elem_size(int32_t dtype) { return dtype == ZERO_FP32 ? 4 : 2; }
+
+bool known(int32_t dtype) { return dtype == ZERO_FP16 || dtype == ZERO_BF16 || dtype == ZERO_FP32; }
+
+bool on16(const void* p, int64_t stride_bytes, int64_t rows) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || stride_bytes % 16 == 0);
+}
+
+}  // namespace
+
+struct zero_block_handle {
+  zero_block_config cfg;
+  bool has_device = false;
+  int device = -1;
+  int sms = 0;
+  float* part = nullptr;
+  int64_t max_grid = 0;      // CTAs that `part` has room for
+  int64_t launches = 0;
+  std::mutex mu;
+  struct {
+    const void* fn;
+    int threads, smem, ctas;
+  } occ[32] = {};            // launch shapes seen, oldest overwritten
+  int seen = 0;
+
+  // CTAs of a kernel that an SM holds at once, at most kMaxPerSm.
+  int resident(const void* fn, int threads, int smem) {
+    std::lock_guard<std::mutex> lock(mu);
+    for (const auto& o : occ)
+      if (o.fn == fn && o.threads == threads && o.smem == smem) return o.ctas;
+    int n = 0;
+    cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) n = 1;
+    n = std::max(1, std::min(n, kMaxPerSm));
+    occ[seen++ % 32] = {fn, threads, smem, n};
+    return n;
+  }
+};
+
+namespace {
+
+// A row tensor of the call, or none where `p` is NULL.
+JoinRow row_of(const zero_block_rows& r, int es) {
+  return {static_cast<char*>(r.data), r.data ? r.stride * es : 0};
+}
+
+zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool backward) {
+  if (!h) return fail(ZERO_EINVAL, "handle is NULL");
+  if (!b) return fail(ZERO_EINVAL, "buffers are NULL");
+  const zero_block_config& c = h->cfg;
+  if (b->tokens < 0) return fail(ZERO_EINVAL, "tokens must be >= 0");
+  const int es = elem_size(c.dtype), ss = elem_size(c.stream_dtype);
+  const bool with_y = b->y.data != nullptr, with_gate = with_y && c.gate != ZERO_GATE_NONE;
+  JoinArgs a = {};
+  if (with_y) a.y = row_of(b->y, es);
+  if (with_gate) a.gate = row_of(b->gate, es);
+  if (backward) {
+    a.x = row_of(b->x_out, ss);
+    a.dxo = row_of(b->dx_out, ss);
+    if (c.norm_out) a.dh = row_of(b->dh, es);
+    a.dx = row_of(b->dx, ss);
+    if (with_y) a.dy = row_of(b->dy, es);
+    if (with_gate) a.dgate = row_of(b->dgate, es);
+  } else {
+    a.x = row_of(b->x, ss);
+    if (with_y) a.x_out = row_of(b->x_out, ss);
+    if (c.norm_out) a.h = row_of(b->h, es);
+  }
+  const struct {
+    const JoinRow* r;
+    const char* name;
+    bool result;
+    int size;
+  } rows[] = {{&a.x, backward ? "x_out" : "x", false, ss}, {&a.y, "y", false, es},
+              {&a.gate, "gate", false, es},                {&a.dxo, "dx_out", false, ss},
+              {&a.dh, "dh", false, es},                    {&a.x_out, "x_out", true, ss},
+              {&a.h, "h", true, es},                       {&a.dx, "dx", true, ss},
+              {&a.dy, "dy", true, es},                     {&a.dgate, "dgate", true, es}};
+  if (b->tokens > 0) {
+    if (!a.x.data) return fail(ZERO_EINVAL, "%s is NULL", backward ? "x_out" : "x");
+    if (with_gate && !a.gate.data) return fail(ZERO_EINVAL, "gate is NULL");
+    if (!backward && c.norm_out && !a.h.data) return fail(ZERO_EINVAL, "h is NULL");
+    if (!backward && !a.h.data && !a.x_out.data) return fail(ZERO_EINVAL, "no result is wanted");
+    if (backward && !a.dxo.data && !a.dh.data) return fail(ZERO_EINVAL, "no gradient is given");
+    for (const auto& r : rows) {
+      if (!r.r->data) continue;
+      if (reinterpret_cast<uintptr_t>(r.r->data) % r.size) return fail(ZERO_EINVAL, "%s is misaligned", r.name);
+      if (r.result && b->tokens > 1 && std::abs(r.r->stride) < (int64_t)c.dim * r.size)
+        return fail(ZERO_EINVAL, "rows of %s lie on one another", r.name);
+    }
+    for (const void* p : {(const void*)b->y_gain, (const void*)b->gain, (const void*)b->dy_gain, (const void*)b->dgain})
+      if (reinterpret_cast<uintptr_t>(p) % 4) return fail(ZERO_EINVAL, "a gain is misaligned");
+    if (reinterpret_cast<uintptr_t>(b->rng.step_dev) % 8) return fail(ZERO_EINVAL, "step_dev is misaligned");
+  }
+  if (!h->has_device) return fail(ZERO_ECUDA, "no CUDA device for this handle");
+  int cur = -1;
+  cudaError_t e = cudaGetDevice(&cur);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (cur != h->device)
+    return fail(ZERO_ECUDA, "current device %d is not the handle's device %d", cur, h->device);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  float* dgain[2] = {backward ? b->dy_gain : nullptr, backward ? b->dgain : nullptr};
+  const bool want = dgain[0] || dgain[1];
+  if (b->tokens == 0) {
+    for (float* g : dgain)
+      if (g) {
+        e = cudaMemsetAsync(g, 0, c.dim * sizeof(float), s);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+      }
+    return ZERO_OK;
+  }
+
+  a.y_gain = b->y_gain;
+  a.gain = b->gain;
+  a.mask = b->mask;
+  a.tokens = b->tokens;
+  a.drop = zo::drop_of(b->rng, with_y ? c.dropout : 0.0);
+  a.dim = c.dim;
+  a.chunks = (c.dim + 7) / 8;
+  a.gate_kind = c.gate;
+  a.post = c.norm_branch;
+  a.pre = c.norm_out;
+  a.eps = (float)c.eps;
+  a.inv_dim = 1.0f / (float)c.dim;
+  a.alpha = (float)c.alpha;
+  a.beta = (float)c.beta;
+  a.part = want ? h->part : nullptr;
+  bool wide = true;
+  for (const auto& r : rows) wide = wide && on16(r.r->data, r.r->stride, b->tokens);
+  // Chunks a thread, warps a team, teams a CTA.
+  const int few = a.chunks <= 32 || (b->tokens <= 2 * h->sms && a.chunks <= 512);
+  const int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= 1024 ? 2 : 4;
+  a.warps = (a.chunks + 32 * cs - 1) / (32 * cs);
+  a.teams = std::max(1, 8 / a.warps);
+  a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
+  const int threads = a.teams * a.warps * 32;
+  const int vt = es / 2, vs = ss / 2;
+  a.vecs = cs * (backward ? 2 * vs + 2 * vt : vs + vt) + (with_gate ? cs * vt : 0);
+  const int row = a.vecs * threads * 16;
+  a.ring = wide ? std::max(1, std::min(3, kMaxSmem / 2 / row)) : 1;
+  size_t smem = (size_t)a.ring * row;
+  if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
+  const void* fn = backward ? zo::join_backward(c.dtype, c.stream_dtype, cs, wide)
+                            : zo::join_forward(c.dtype, c.stream_dtype, cs, wide);
+  int64_t grid = (b->tokens + a.teams - 1) / a.teams;
+  grid = std::min(grid, (int64_t)h->resident(fn, threads, (int)smem) * h->sms);
+  if (want) grid = std::min(grid, h->max_grid);
+  void* params[] = {&a};
+  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), params, smem, s);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+  ++h->launches;
+  if (want) {
+    FoldArgs f = {h->part, {dgain[0], dgain[1]}, (int)grid, c.dim};
+    void* fp[] = {&f};
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)((2 * c.dim + 31) / 32));
+    lc.blockDim = dim3(256);
+    lc.stream = s;
+    lc.attrs = &early;
+    lc.numAttrs = 1;
+    e = cudaLaunchKernelExC(&lc, (const void*)join_fold_kernel, fp);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
+    ++h->launches;
+  }
+  return ZERO_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
+  if (!out) return fail(ZERO_EINVAL, "out is NULL");
+  *out = nullptr;
+  if (!cfg) return fail(ZERO_EINVAL, "cfg is NULL");
+  if (!known(cfg->dtype)) return fail(ZERO_EINVAL, "dtype must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
+  if (cfg->stream_dtype != cfg->dtype && cfg->stream_dtype != ZERO_FP32)
+    return fail(ZERO_EINVAL, "stream_dtype must be dtype or ZERO_FP32");
+  const int most = cfg->dtype == ZERO_FP32 ? kMaxDim32 : kMaxDim;
+  if (cfg->dim < 1 || cfg->dim > most) return fail(ZERO_EINVAL, "dim must be in 1..%d", most);
+  if ((cfg->norm_branch | 1) != 1 || (cfg->norm_out | 1) != 1)
+    return fail(ZERO_EINVAL, "norm_branch and norm_out must be 0 or 1");
+  if (cfg->gate < ZERO_GATE_NONE || cfg->gate > ZERO_GATE_SIGMOID)
+    return fail(ZERO_EINVAL, "gate must be a ZERO_GATE_*");
+  if (!(cfg->eps >= 0.0) || !std::isfinite(cfg->eps)) return fail(ZERO_EINVAL, "eps must be >= 0");
+  if (!std::isfinite(cfg->alpha) || !std::isfinite(cfg->beta))
+    return fail(ZERO_EINVAL, "alpha and beta must be finite");
+  if (!(cfg->dropout >= 0.0 && cfg->dropout <= 1.0)) return fail(ZERO_EINVAL, "dropout must be in 0..1");
+  zero_block_handle* h = new (std::nothrow) zero_block_handle;
+  if (!h) return fail(ZERO_ENOMEM, "handle allocation failed");
+  h->cfg = *cfg;
+  int count = 0;
+  if (cudaGetDeviceCount(&count) != cudaSuccess || count < 1) {
+    cudaGetLastError();
+    *out = h;
+    return ZERO_OK;
+  }
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
+  // Partial gradients of every CTA of the largest grid.
+  h->max_grid = (int64_t)kMaxPerSm * h->sms;
+  if (e == cudaSuccess)
+    e = cudaMalloc(reinterpret_cast<void**>(&h->part), (size_t)h->max_grid * 2 * cfg->dim * sizeof(float));
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    delete h;
+    return e == cudaErrorMemoryAllocation ? fail(ZERO_ENOMEM, "workspace allocation failed")
+                                          : cuda_fail(e, "zero_block_create");
+  }
+  h->has_device = true;
+  *out = h;
+  return ZERO_OK;
+}
+
+zero_status zero_block_destroy(zero_block_t h) {
+  if (!h) return ZERO_OK;
+  if (h->has_device) {
+    int prev = -1;
+    cudaGetDevice(&prev);
+    cudaSetDevice(h->device);
+    cudaDeviceSynchronize();
+    cudaFree(h->part);
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+  delete h;
+  return ZERO_OK;
+}
+
+zero_status zero_block_join(zero_block_t h, const zero_block_buffers* b, void* stream) {
+  return run(h, b, stream, false);
+}
+
+zero_status zero_block_join_backward(zero_block_t h, const zero_block_buffers* b, void* stream) {
+  return run(h, b, stream, true);
+}
+
+zero_status zero_block_launch_count(zero_block_t h, int64_t* launches) {
+  if (!h || !launches) return fail(ZERO_EINVAL, "NULL argument");
+  *launches = h->launches;
+  return ZERO_OK;
+}
+
+zero_status zero_dropout(const zero_drop_buffers* b, void* stream) {
+  if (!b) return fail(ZERO_EINVAL, "buffers are NULL");
+  if (b->rows < 0 || b->cols < 0) return fail(ZERO_EINVAL, "rows and cols must be >= 0");
+  if (!known(b->dtype)) return fail(ZERO_EINVAL, "dtype must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
+  if (!(b->p >= 0.0 && b->p <= 1.0)) return fail(ZERO_EINVAL, "p must be in 0..1");
+  const int es = elem_size(b->dtype);
+  const bool any = b->rows > 0 && b->cols > 0;
+  if (any) {
+    if (!b->in || !b->out) return fail(ZERO_EINVAL, "in or out is NULL");
+    if (reinterpret_cast<uintptr_t>(b->in) % es || reinterpret_cast<uintptr_t>(b->out) % es)
+      return fail(ZERO_EINVAL, "in or out is misaligned");
+    if (b->rows > 1 && std::abs(b->out_stride) < b->cols) return fail(ZERO_EINVAL, "rows of the result lie on one another");
+    if (reinterpret_cast<uintptr_t>(b->rng.step_dev) % 8) return fail(ZERO_EINVAL, "step_dev is misaligned");
+  }
+  int device = -1, sms = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return cuda_fail(e, "no CUDA device");
+  }
+  if (!any) return ZERO_OK;
+  DropArgs a = {};
+  a.in = static_cast<const char*>(b->in);
+  a.out = static_cast<char*>(b->out);
+  a.rows = b->rows;
+  a.cols = b->cols;
+  a.in_stride = b->in_stride * es;
+  a.out_stride = b->out_stride * es;
+  a.blocks = (b->cols + 7) / 8;
+  a.drop = zo::drop_of(b->rng, b->p);
+  // rows that follow one another and are whole blocks: one long row
+  if (b->cols % 8 == 0 && b->in_stride == b->cols && b->out_stride == b->cols) {
+    a.blocks *= a.rows;
+    a.cols *= a.rows;
+    a.rows = 1;
+  }
+  const bool wide = on16(a.in, a.in_stride, a.rows) && on16(a.out, a.out_stride, a.rows);
+  const int64_t work = wide ? (a.rows * a.blocks + 255) / 256 : (a.rows * ((a.cols + 255) / 256) + 7) / 8;
+  const int64_t grid = std::min<int64_t>(work, (int64_t)sms * 8);
+  const void* fn = b->dtype == ZERO_FP16   ? (wide ? (const void*)drop_kernel<__half, true> : (const void*)drop_kernel<__half, false>)
+                   : b->dtype == ZERO_BF16 ? (wide ? (const void*)drop_kernel<__nv_bfloat16, true> : (const void*)drop_kernel<__nv_bfloat16, false>)
+                                           : (wide ? (const void*)drop_kernel<float, true> : (const void*)drop_kernel<float, false>);
+  void* params[] = {&a};
+  e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3(256), params, 0, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
+  return ZERO_OK;
+}
+
+}  // extern "C"

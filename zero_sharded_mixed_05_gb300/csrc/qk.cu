@@ -25,8 +25,6 @@
 // in which every thread reads only what it copied itself, so that bytes in
 // flight cost no registers and no barrier; narrower ones are loaded directly.
 // The angles of the next token are fetched while the rows are still on their way.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,11 +33,16 @@
 #include <new>
 
 #include "host_util.h"
+#include "numbers.cuh"
 #include "zero_qk.h"
 
 namespace {
 
+using zo::both;
+using zo::copy16;
 using zo::fail;
+using zo::Num;
+using zo::Vec;
 
 constexpr int kQkThreads = 256;
 constexpr int kMaxDim = 512;
@@ -70,38 +73,6 @@ struct QkArgs {
   int32_t part_rows;   // rows of a CTA's partial: 2 (shared gains) or its heads
   float eps, inv_dim;
 };
-
-// Two numbers of the data's type as binary32, and back with one rounding each.
-template <typename T> struct Num;
-template <> struct Num<__half> {
-  static __device__ float get(__half x) { return __half2float(x); }
-  static __device__ float2 get2(const __half* p) { return __half22float2(*reinterpret_cast<const __half2*>(p)); }
-  static __device__ __half put(float x) { return __float2half_rn(x); }
-  static __device__ void put2(__half* p, float2 x) { *reinterpret_cast<__half2*>(p) = __float22half2_rn(x); }
-};
-template <> struct Num<__nv_bfloat16> {
-  static __device__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-  static __device__ float2 get2(const __nv_bfloat16* p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-  }
-  static __device__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-  static __device__ void put2(__nv_bfloat16* p, float2 x) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __float22bfloat162_rn(x);
-  }
-};
-template <> struct Num<float> {
-  static __device__ float get(float x) { return x; }
-  static __device__ float2 get2(const float* p) { return make_float2(p[0], p[1]); }
-  static __device__ float put(float x) { return x; }
-  static __device__ void put2(float* p, float2 x) { p[0] = x.x; p[1] = x.y; }
-};
-
-// V numbers at an address that is a multiple of their size, of 16 bytes at most:
-// that is what run() asks of every address (eight gains are 32 bytes).
-template <typename T, int V> struct alignas(sizeof(T) * V < 16 ? sizeof(T) * V : 16) Vec { T v[V]; };
-
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A chunk: the lane's two vectors one after the other, as V pairs of numbers
 // for the two-wide binary32 instructions.
@@ -139,13 +110,6 @@ __device__ __forceinline__ Vec<T, V> load(const char* p, int e) {
 template <typename T, int V>
 __device__ __forceinline__ void store(char* p, int e, const Vec<T, V>& x) {
   *reinterpret_cast<Vec<T, V>*>(reinterpret_cast<T*>(p) + e) = x;
-}
-
-// 16 bytes from global to shared memory, in the background.
-__device__ __forceinline__ void copy16(void* to, const char* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-               "l"(from)
-               : "memory");
 }
 
 // Where the two vectors of chunk c start.
