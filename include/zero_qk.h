@@ -14,9 +14,13 @@
  *   dgain = sum over tokens (and heads, for a shared gain) of dy * x * r
  *   dx    = r * (dy * gain - x * r * mean(dy * gain * x * r))
  *
- * A token whose position is negative is padding: what its inputs hold (NaN
+ * A handle of zero_qk_create_axes turns each pair by the position that the token
+ * has on that pair's axis (time, height, width of a video's patch, ...), and may
+ * leave the norm out (y = x), so that rows are only rotated.
+ *
+ * A token whose position (any of them) is negative is padding: what its inputs hold (NaN
  * and infinity included) is ignored, its outputs and gradients are zero and it adds nothing to the gains' gradients.
- * A position of n_pos or more has no angle: its rows come out as NaN.
+ * A position (any) of n_pos or more has no angle: the token's rows come out as NaN.
  *
  * Arithmetic is binary32 throughout (a row's squares have to be within its
  * range: numbers from about 1e-18 to 1e18); results are rounded once, to the
@@ -74,7 +78,7 @@ typedef struct zero_qk_buffers {
   float* dk_gain;           /*   gains; NULL: not wanted                     */
   const float* cos;         /* device fp32 [n_pos][rotary_dim/2]             */
   const float* sin;         /* device fp32 [n_pos][rotary_dim/2]             */
-  const void* positions;    /* device int32 or int64 [T]                     */
+  const void* positions;    /* device int32 or int64 [T]; with axes [axes][T] */
   int32_t positions64;      /* 1: int64                                      */
   int32_t reserved;
 } zero_qk_buffers;
@@ -84,12 +88,26 @@ typedef struct zero_qk_buffers {
  * failure.  Without a CUDA device the handle is created and every launching
  * call returns ZERO_ECUDA. */
 zero_status zero_qk_create(const zero_qk_config* cfg, zero_qk_t* out);
+
+/* Positions on several axes.  Pair j < rotary_dim/2 turns by
+ * cos[p[axis[j]]][j], sin[p[axis[j]]][j], p the token's positions; each axis
+ * below n_pos, and n_pos below 2^31.  Without the norm (normalise 0) there are no
+ * gains (their pointers, and their gradients', are NULL), eps is not used, and the
+ * backward call looks at neither q nor k.
+ * Errors: those of zero_qk_create; EINVAL (NULL axes, a field out of range). */
+typedef struct zero_qk_axes {
+  int32_t axes;             /* 1..4                                          */
+  int32_t normalise;        /* 1: as zero_qk_create; 0: rotation alone       */
+  uint8_t axis[256];        /* of each pair: 0..axes-1                       */
+} zero_qk_axes;
+zero_status zero_qk_create_axes(const zero_qk_config* cfg, const zero_qk_axes* axes, zero_qk_t* out);
+
 zero_status zero_qk_destroy(zero_qk_t h);
 
 /* Errors of both: EINVAL (NULL handle or buffers; a NULL tensor with
  * T > 0; tokens or n_pos < 0; NULL tables with rotary_dim and n_pos > 0 or
  * NULL positions, T > 0; a result's token or head stride that lays rows on one
- * another), ECUDA (no device, another device current, a launch
+ * another; gains without the norm, n_pos of 2^31 or more with axes), ECUDA (no device, another device current, a launch
  * failure).  T = 0 launches nothing, except that the backward call sets the
  * gains' gradients to zero. */
 zero_status zero_qk_norm_rope(zero_qk_t h, const zero_qk_buffers* b, void* stream);

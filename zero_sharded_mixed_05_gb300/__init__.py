@@ -125,6 +125,10 @@ class zero_qk_config(ctypes.Structure):
                 ("reserved", _i32), ("eps", _f64)]
 
 
+class zero_qk_axes(ctypes.Structure):
+    _fields_ = [("axes", _i32), ("normalise", _i32), ("axis", ctypes.c_uint8 * 256)]
+
+
 class zero_qk_tensor(ctypes.Structure):
     _fields_ = [("data", _vp), ("token_stride", _i64), ("head_stride", _i64)]
 
@@ -234,6 +238,7 @@ SIGNATURES = [
     ("zero_muon_inject_wait_fault", _i32, [_vp]),
     ("zero_muon_launch_count", _i32, [_vp, _P(_i64)]),
     ("zero_qk_create", _i32, [_P(zero_qk_config), _P(_vp)]),
+    ("zero_qk_create_axes", _i32, [_P(zero_qk_config), _P(zero_qk_axes), _P(_vp)]),
     ("zero_qk_destroy", _i32, [_vp]),
     ("zero_qk_norm_rope", _i32, [_vp, _vp, _vp]),
     ("zero_qk_norm_rope_backward", _i32, [_vp, _vp, _vp]),
@@ -892,8 +897,8 @@ def zero_muon_launch_count(h) -> int:
 # ---------------------------------------------------------------- query/key norm and rotation
 
 # What a handle was made for, so that the binding can check tensors against it
-# (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, device), and
-# memory for one call's zero_qk_buffers (calls on one handle are ordered).
+# (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, axes or 0,
+# device), and memory for one call's zero_qk_buffers (calls on one handle are ordered).
 _qk_handles = {}
 _qk_pack = struct.Struct("=27qii").pack_into
 
@@ -906,15 +911,31 @@ def make_qk_config(q_heads, k_heads, head_dim, rotary_dim=None, dtype=BF16, inte
                           int(interleaved), int(gain_per_head), 0, eps)
 
 
-def zero_qk_create(cfg: zero_qk_config) -> int:
+def make_qk_axes(axis, axes=None, normalise=True) -> zero_qk_axes:
+    """`axis`: of each pair, in 0..`axes` - 1 (None: as many as `axis` names).
+    `normalise` False: rows are only rotated."""
+    axis = list(axis)
+    if len(axis) > 256 or any(not 0 <= a < 256 for a in axis):
+        raise ValueError("axis must be at most 256 numbers in 0..3")
+    return zero_qk_axes(max(axis, default=0) + 1 if axes is None else axes, int(normalise),
+                        (ctypes.c_uint8 * 256)(*axis))
+
+
+def zero_qk_create(cfg: zero_qk_config, axes: zero_qk_axes = None) -> int:
+    """`axes` of make_qk_axes: tokens have a position on each axis."""
     h = _vp()
-    _check(lib().zero_qk_create(ctypes.byref(cfg), ctypes.byref(h)), "zero_qk_create")
+    if axes is None:
+        _check(lib().zero_qk_create(ctypes.byref(cfg), ctypes.byref(h)), "zero_qk_create")
+    else:
+        _check(lib().zero_qk_create_axes(ctypes.byref(cfg), ctypes.byref(axes), ctypes.byref(h)),
+               "zero_qk_create_axes")
     import torch
     dtype = (torch.float16, torch.bfloat16, torch.float32)[cfg.dtype]
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_qk_buffers()
     _qk_handles[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
-                            bool(cfg.gain_per_head), dev, b, ctypes.addressof(b))
+                            bool(cfg.gain_per_head), axes.axes if axes else 0, dev, b,
+                            ctypes.addressof(b))
     return h.value
 
 
@@ -952,7 +973,7 @@ def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gai
     import torch
     if h not in _qk_handles:
         raise ValueError("not a handle of zero_qk_create")
-    hq, hk, dim, half, dtype, per_head, dev, b, at = _qk_handles[h]
+    hq, hk, dim, half, dtype, per_head, axes, dev, b, at = _qk_handles[h]
     n = q.shape[0]
     f32 = torch.float32
     tq = _qk_heads(q, "q", n, hq, dim, dtype, dev)
@@ -981,7 +1002,7 @@ def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gai
         pc = _qk_flat(cos, "cos", table, f32, dev)
         ps = _qk_flat(sin, "sin", table, f32, dev)
     wide = positions.dtype is torch.int64
-    pp = _qk_flat(positions, "positions", (n,), torch.int64 if wide else torch.int32, dev)
+    pp = _qk_flat(positions, "positions", (axes, n) if axes else (n,), torch.int64 if wide else torch.int32, dev)
     _qk_pack(b, 0, n, n_pos, *tq, *tk, *tqo, *tko, *tdq, *tdk, gq, gk, dgq, dgk, pc, ps, pp, wide, 0)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
@@ -994,8 +1015,9 @@ def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions
                       stream=None) -> None:
     """Normalise and rotate every head of `q` [tokens, q_heads, D] and `k` into
     `q_out` and `k_out` (which may be `q` and `k`).  `k`, `k_out` are not looked
-    at by a handle with k_heads 0; a gain may be None (ones).  A token of
-    position -1 is padding and gets zeros."""
+    at by a handle with k_heads 0; a gain may be None (ones).  `positions` is
+    [tokens], or [axes, tokens] of a handle with axes; a token of position -1 (on
+    any axis) is padding and gets zeros."""
     _qk_call(lib().zero_qk_norm_rope, h, ("q_out", "k_out"), q, k, q_out, k_out, None, None, q_gain,
              k_gain, None, None, cos, sin, positions, stream)
 
