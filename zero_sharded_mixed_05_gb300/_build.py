@@ -12,11 +12,12 @@ INCLUDE = os.path.join(ROOT, "include")
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "zero_opt.cu", "ckpt.cpp", "noalloc.cu", "host_step.cpp", "qk.cu", "qk_one.cu", "qk_axes.cu",
-    "muon.cu", "block.cu", "join_forward.cu", "join_backward.cu")]
+    "muon.cu", "block.cu", "join_half.cu", "join_half_float.cu", "join_bf16.cu", "join_bf16_float.cu",
+    "join_float.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in (
     "kernels.cuh", "zero_opt_internal.h", "host_util.h", "decide_core.h", "host_cast.h", "muon_kernels.cuh",
     "muon_products.cuh", "muon_resident.cuh", "sm103.cuh", "numbers.cuh", "philox.cuh", "block_host.h",
-    "block_kernels.cuh", "qk_host.h", "qk_kernels.cuh")] + [
+    "block_kernels.cuh", "join_pick.cuh", "qk_host.h", "qk_kernels.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("zero_opt.h", "zero_qk.h", "zero_muon.h", "zero_block.h")]
 LIB = os.path.join(PKG, "libzero_opt.so")
 

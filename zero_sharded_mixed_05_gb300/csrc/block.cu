@@ -20,7 +20,6 @@ using zo::fail;
 using zo::JoinArgs;
 using zo::JoinRow;
 using zo::Num;
-using zo::Vec;
 
 constexpr int kMaxDim = 16384;
 constexpr int kMaxDim32 = 8192;          // of binary32 blocks: a row of each tensor fits shared memory
@@ -77,15 +76,16 @@ template <typename T, bool kWide>
 __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropArgs a) {
   constexpr int kE = 16 / (int)sizeof(T), kV = 8 / kE;
   const uint32_t step = zo::step_of(a.drop);
-  const auto apply = [&](Vec<T, kE>* p, int64_t block) {
+  const auto apply = [&](uint4* p, int64_t block) {
     const uint32_t bits = zo::kept(a.drop, step, block);
+    float2 x[4];
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      float2 x = Num<T>::get2(p[i / kE].v + i % kE);
-      x = make_float2(bits >> i & 1 ? __fmul_rn(x.x, a.drop.factor) : 0.0f,
-                      bits >> i & 2 ? __fmul_rn(x.y, a.drop.factor) : 0.0f);
-      Num<T>::put2(p[i / kE].v + i % kE, x);
-    }
+    for (int v = 0; v < kV; ++v) zo::unpack<T>(p[v], x + v * (kE / 2));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], zo::both(a.drop.factor));
+    zo::drop8(x, bits);
+#pragma unroll
+    for (int v = 0; v < kV; ++v) p[v] = zo::pack<T>(x + v * (kE / 2));
   };
   if constexpr (kWide) {
     const int64_t n = a.rows * a.blocks, stride = (int64_t)gridDim.x * blockDim.x;
@@ -94,20 +94,17 @@ __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropA
       const T* from = reinterpret_cast<const T*>(a.in + row * a.in_stride) + c * 8;
       T* to = reinterpret_cast<T*>(a.out + row * a.out_stride) + c * 8;
       const int64_t left = a.cols - c * 8;
-      Vec<T, kE> p[kV];
       if (left >= 8) {
+        uint4 p[kV];
 #pragma unroll
-        for (int v = 0; v < kV; ++v) p[v] = reinterpret_cast<const Vec<T, kE>*>(from)[v];
+        for (int v = 0; v < kV; ++v) p[v] = reinterpret_cast<const uint4*>(from)[v];
         apply(p, b);
 #pragma unroll
-        for (int v = 0; v < kV; ++v) reinterpret_cast<Vec<T, kE>*>(to)[v] = p[v];
+        for (int v = 0; v < kV; ++v) reinterpret_cast<uint4*>(to)[v] = p[v];
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i / kE].v[i % kE] = i < left ? from[i] : Num<T>::put(0.0f);
-        apply(p, b);
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i < left) to[i] = p[i / kE].v[i % kE];
+        const uint32_t bits = zo::kept(a.drop, step, b);
+        for (int i = 0; i < left; ++i)
+          to[i] = Num<T>::put(bits >> i & 1 ? __fmul_rn(Num<T>::get(from[i]), a.drop.factor) : 0.0f);
       }
     }
   } else {
@@ -128,7 +125,7 @@ __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropA
 #pragma unroll
       for (int k = 0; k < 8; ++k) tile[k * 32 + l] = x[k];
       __syncwarp();
-      apply(reinterpret_cast<Vec<T, kE>*>(tile + 8 * l), row * a.blocks + begin / 8 + l);
+      apply(reinterpret_cast<uint4*>(tile + 8 * l), row * a.blocks + begin / 8 + l);
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -159,7 +156,8 @@ struct zero_block_handle {
   bool has_device = false;
   int device = -1;
   int sms = 0;
-  float* part = nullptr;
+  float* part = nullptr;     // and, behind it, the row of zeros
+  float* zeros = nullptr;
   int64_t max_grid = 0;      // CTAs that `part` has room for
   int64_t launches = 0;
   std::mutex mu;
@@ -264,18 +262,25 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.dim = c.dim;
   a.chunks = (c.dim + 7) / 8;
   a.gate_kind = c.gate;
-  a.post = c.norm_branch;
-  a.pre = c.norm_out;
-  a.eps = (float)c.eps;
+  a.eps = a.eps_y = (float)c.eps;
   a.inv_dim = 1.0f / (float)c.dim;
-  a.alpha = (float)c.alpha;
+  a.alpha = with_y ? (float)c.alpha : 1.0f;
   a.beta = (float)c.beta;
+  // absent inputs are zeros; without dh the stream is not read, and its norm, which
+  // then counts for nothing, stays finite
+  const JoinRow none = {reinterpret_cast<char*>(h->zeros), 0};
+  if (!a.y.data) a.y = none;
+  if (backward && !a.dxo.data) a.dxo = none;
+  if (backward && !a.dh.data) {
+    a.dh = a.x = none;
+    a.eps = 1.0f;
+  }
   a.part = want ? h->part : nullptr;
-  bool wide = true;
+  bool wide = c.dim % 8 == 0;
   for (const auto& r : rows) wide = wide && on16(r.r->data, r.r->stride, b->tokens);
   // Chunks a thread, warps a team, teams a CTA.
   const int few = a.chunks <= 32 || (b->tokens <= 2 * h->sms && a.chunks <= 512);
-  const int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= 1024 ? 2 : 4;
+  int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= 1024 ? 2 : 4;
   a.warps = (a.chunks + 32 * cs - 1) / (32 * cs);
   a.teams = std::max(1, 8 / a.warps);
   a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
@@ -286,8 +291,11 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.ring = wide ? std::max(1, std::min(3, kMaxSmem / 2 / row)) : 1;
   size_t smem = (size_t)a.ring * row;
   if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
-  const void* fn = backward ? zo::join_backward(c.dtype, c.stream_dtype, cs, wide)
-                            : zo::join_forward(c.dtype, c.stream_dtype, cs, wide);
+  const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate || a.drop.cut > 0, cs};
+  const bool mixed = c.stream_dtype != c.dtype;
+  const void* fn = c.dtype == ZERO_FP32   ? zo::join_float(pick)
+                   : c.dtype == ZERO_FP16 ? (mixed ? zo::join_half_float(pick) : zo::join_half(pick))
+                                          : (mixed ? zo::join_bf16_float(pick) : zo::join_bf16(pick));
   int64_t grid = (b->tokens + a.teams - 1) / a.teams;
   grid = std::min(grid, (int64_t)h->resident(fn, threads, (int)smem) * h->sms);
   if (want) grid = std::min(grid, h->max_grid);
@@ -348,9 +356,15 @@ zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   // Partial gradients of every CTA of the largest grid.
   h->max_grid = (int64_t)kMaxPerSm * h->sms;
+  const size_t numbers = (size_t)h->max_grid * 2 * ((cfg->dim + 7) / 8 * 8), dim = (cfg->dim + 7) / 8 * 8;
   if (e == cudaSuccess)
-    e = cudaMalloc(reinterpret_cast<void**>(&h->part), (size_t)h->max_grid * 2 * cfg->dim * sizeof(float));
+    e = cudaMalloc(reinterpret_cast<void**>(&h->part), (numbers + dim) * sizeof(float));
+  if (e == cudaSuccess) {
+    h->zeros = h->part + numbers;
+    e = cudaMemset(h->zeros, 0, dim * sizeof(float));
+  }
   if (e != cudaSuccess) {
+    cudaFree(h->part);
     cudaGetLastError();
     delete h;
     return e == cudaErrorMemoryAllocation ? fail(ZERO_ENOMEM, "workspace allocation failed")

@@ -5,8 +5,18 @@
 
 namespace zo {
 
-// Kernels that take a JoinArgs; c: 1, 2 (wide only) or 4 chunks a thread.
-const void* join_forward(int32_t dtype, int32_t stream, int c, bool wide);
-const void* join_backward(int32_t dtype, int32_t stream, int c, bool wide);
+struct JoinPick {
+  bool backward, wide;
+  bool post;       // the branch is normalised
+  bool extra;      // it has a gate or a dropout
+  int chunks;      // a thread: 1, 2 (wide only) or 4
+};
+
+// Kernels that take a JoinArgs, by the types of the block and of the stream.
+const void* join_half(const JoinPick& p);
+const void* join_half_float(const JoinPick& p);
+const void* join_bf16(const JoinPick& p);
+const void* join_bf16_float(const JoinPick& p);
+const void* join_float(const JoinPick& p);
 
 }  // namespace zo

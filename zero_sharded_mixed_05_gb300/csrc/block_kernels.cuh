@@ -31,7 +31,8 @@ struct JoinRow {
 
 struct JoinArgs {
   // forward: x, y, gate in; x_out, h out.  backward: x (the x' of the forward
-  // pass), y, gate, dxo, dh in; dx, dy, dgate out.  NULL where absent.
+  // pass), y, gate, dxo, dh in; dx, dy, dgate out.  An input that is absent is a
+  // row of zeros for every token (the gate: NULL); a result that is: NULL.
   JoinRow x, y, gate, x_out, h, dxo, dh, dx, dy, dgate;
   const float* y_gain;
   const float* gain;
@@ -42,8 +43,8 @@ struct JoinArgs {
   int32_t dim, chunks;
   int32_t warps, teams; // of a team; of a CTA
   int32_t ring, vecs;   // rows of the ring; 16-byte vectors of a thread in one
-  int32_t gate_kind, post, pre;
-  float eps, inv_dim, alpha, beta;
+  int32_t gate_kind;
+  float eps, eps_y, inv_dim, alpha, beta;
 };
 
 template <typename E> constexpr int kVecs = (int)sizeof(E) / 2;   // 16-byte vectors of a chunk
@@ -56,47 +57,40 @@ __device__ __forceinline__ void copies_left(int n) {
 }
 
 // The place of a thread in its team and in shared memory, and the moves between
-// there and the rows.
+// there and the rows.  A warp's vectors of a row lie one after another, 512
+// bytes each, so that a vector is a fixed distance from the row's first.
 template <int kC, bool kWide>
 struct Lane {
-  const JoinArgs& a;
-  unsigned char* smem;    // the CTA's ring
-  int threads;            // of the CTA
-  int team, lane, lanes;  // this thread's team, its place in it, threads of a team
+  int dim, chunks, warps;           // as in JoinArgs
+  unsigned char* smem;    // the warp's ring
+  int team, warp;         // this thread's team, and its warp's place in it
 
-  __device__ __forceinline__ int chunk(int j) const { return lane + j * lanes; }
-  __device__ __forceinline__ bool live(int j) const { return chunk(j) < a.chunks; }
-  // numbers of the chunk
-  __device__ __forceinline__ int count(int j) const { return min(8, a.dim - chunk(j) * 8); }
-  // vector n of the thread in the ring's row `at`
+  __device__ __forceinline__ int lanes() const { return warps * 32; }
+  __device__ __forceinline__ int chunk(int j) const { return (j * warps + warp) * 32 + threadIdx.x % 32; }
+  __device__ __forceinline__ bool live(int j) const { return chunk(j) < chunks; }
+  // vector n of the thread in the row of the ring that begins at `at`
   __device__ __forceinline__ unsigned char* vec(int at, int n) const {
-    return smem + ((at * a.vecs + n) * threads + threadIdx.x) * 16;
+    return smem + at + n * 512 + threadIdx.x % 32 * 16;
   }
 
   // A row's chunks into vectors from `first` on.
   template <typename E>
-  __device__ __forceinline__ void fetch(const JoinRow& r, int64_t t, int at, int first) const {
-    const char* row = r.data + t * r.stride;
+  __device__ __forceinline__ void fetch(const char* row, int at, int first) const {
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       if constexpr (kWide) {
         if (!live(j)) continue;
-        const char* from = row + (int64_t)chunk(j) * (8 * (int)sizeof(E));
-        const int bytes = count(j) * (int)sizeof(E);
+        const char* from = row + (uint32_t)chunk(j) * (8 * (uint32_t)sizeof(E));
 #pragma unroll
-        for (int v = 0; v < kVecs<E>; ++v) {
-          unsigned char* to = vec(at, first + j * kVecs<E> + v);
-          if (bytes == 8 * (int)sizeof(E)) copy16(to, from + 16 * v);
-          else copy16(to, bytes > 16 * v ? from + 16 * v : row, max(0, min(16, bytes - 16 * v)));
-        }
+        for (int v = 0; v < kVecs<E>; ++v) copy16(vec(at, first + j * kVecs<E> + v), from + 16 * v);
       } else {
-        const int l = threadIdx.x % 32, begin = (chunk(j) - l) * 8;
-        if (begin >= a.dim) continue;
+        const int l = threadIdx.x % 32, begin = (j * warps + warp) * 256;
+        if (begin >= dim) continue;
         E x[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int e = begin + k * 32 + l;
-          x[k] = e < a.dim ? reinterpret_cast<const E*>(row)[e] : Num<E>::put(0.0f);
+          x[k] = e < dim ? reinterpret_cast<const E*>(row)[e] : Num<E>::put(0.0f);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) *place<E>(at, first + j * kVecs<E>, k * 32 + l) = x[k];
@@ -106,57 +100,41 @@ struct Lane {
   // Number e of the 256 that the warp holds in a chunk whose vectors start at n.
   template <typename E>
   __device__ __forceinline__ E* place(int at, int n, int e) const {
-    const int l = threadIdx.x % 32;
-    unsigned char* v = vec(at, n) - l * 16;                 // lane 0's
+    unsigned char* v = smem + at + n * 512;
     if constexpr (sizeof(E) == 2) return reinterpret_cast<E*>(v) + e;
-    else return reinterpret_cast<E*>(v + (e % 8 / 4 * threads + e / 8) * 16) + e % 4;
+    else return reinterpret_cast<E*>(v + e % 8 / 4 * 512 + e / 8 * 16) + e % 4;
   }
 
   template <typename E>
   __device__ __forceinline__ void get(int at, int n, float2* x) const {
-    constexpr int kE = 16 / (int)sizeof(E);
 #pragma unroll
-    for (int v = 0; v < kVecs<E>; ++v) {
-      const Vec<E, kE> p = *reinterpret_cast<const Vec<E, kE>*>(vec(at, n + v));
-#pragma unroll
-      for (int k = 0; k < kE / 2; ++k) x[v * (kE / 2) + k] = Num<E>::get2(p.v + 2 * k);
-    }
+    for (int v = 0; v < kVecs<E>; ++v)
+      unpack<E>(*reinterpret_cast<const uint4*>(vec(at, n + v)), x + v * (8 / (int)sizeof(E)));
   }
 
   // A chunk of a result.  Narrow rows pass through the vectors from n on, which
   // are done with.
   template <typename E>
-  __device__ __forceinline__ void put(const JoinRow& r, int64_t t, int j, const float2* x, int at,
-                                      int n) const {
-    constexpr int kE = 16 / (int)sizeof(E);
-    E* row = reinterpret_cast<E*>(r.data + t * r.stride);
-    Vec<E, kE> p[kVecs<E>];
+  __device__ __forceinline__ void put(char* data, int j, const float2* x, int at, int n) const {
+    uint4 p[kVecs<E>];
 #pragma unroll
-    for (int v = 0; v < kVecs<E>; ++v)
-#pragma unroll
-      for (int k = 0; k < kE / 2; ++k) Num<E>::put2(p[v].v + 2 * k, x[v * (kE / 2) + k]);
+    for (int v = 0; v < kVecs<E>; ++v) p[v] = pack<E>(x + v * (8 / (int)sizeof(E)));
     if constexpr (kWide) {
       if (!live(j)) return;
-      E* to = row + chunk(j) * 8;
-      const int left = count(j);
-      if (left == 8) {
+      uint4* to = reinterpret_cast<uint4*>(data + (uint32_t)chunk(j) * (8 * (uint32_t)sizeof(E)));
 #pragma unroll
-        for (int v = 0; v < kVecs<E>; ++v) reinterpret_cast<Vec<E, kE>*>(to)[v] = p[v];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 7; ++k)
-          if (k < left) to[k] = p[k / kE].v[k % kE];
-      }
+      for (int v = 0; v < kVecs<E>; ++v) to[v] = p[v];
     } else {
-      const int l = threadIdx.x % 32, begin = (chunk(j) - l) * 8;
-      if (begin >= a.dim) return;
+      E* row = reinterpret_cast<E*>(data);
+      const int l = threadIdx.x % 32, begin = (j * warps + warp) * 256;
+      if (begin >= dim) return;
 #pragma unroll
-      for (int v = 0; v < kVecs<E>; ++v) *reinterpret_cast<Vec<E, kE>*>(vec(at, n + v)) = p[v];
+      for (int v = 0; v < kVecs<E>; ++v) *reinterpret_cast<uint4*>(vec(at, n + v)) = p[v];
       __syncwarp();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int e = begin + k * 32 + l;
-        if (e < a.dim) row[e] = *place<E>(at, n, k * 32 + l);
+        if (e < dim) row[e] = *place<E>(at, n, k * 32 + l);
       }
       __syncwarp();
     }
@@ -164,7 +142,7 @@ struct Lane {
 
   // A chunk of a gain (NULL: ones).
   __device__ __forceinline__ void gain(const float* g, int j, float2* x) const {
-    const int left = live(j) ? count(j) : 0;
+    const int left = min(8, dim - chunk(j) * 8);
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = both(g ? 0.0f : 1.0f);
     if (!g) return;
@@ -185,31 +163,43 @@ struct Lane {
     }
   }
 
-  // Sums over the team's threads, in an order fixed by its size; every thread
-  // gets them.  `turn` alternates between two pieces of shared memory, so that
-  // one barrier a sum is enough: who writes a piece again has passed the
-  // barrier of the sum between, which everyone reaches after reading the first.
+  // Sums of kN numbers over the team's threads, in an order fixed by its size;
+  // every thread gets them.  In a warp the numbers are spread over the lanes as
+  // they are added, so that after log2(kP) steps each lane has one of them; the
+  // warps' sums meet in shared memory.  `turn` alternates between two pieces of
+  // it, so that one barrier a sum is enough: who writes a piece again has passed
+  // the barrier of the sum between, which everyone reaches after reading the first.
   template <int kN>
-  __device__ __forceinline__ void sum(float (&x)[kN], float4 (*red)[kJoinThreads / 32], int& turn) const {
+  __device__ __forceinline__ void sum(float* x, float (*red)[kJoinThreads / 32 * 8], int& turn) const {
+    constexpr int kP = kN <= 1 ? 1 : kN <= 2 ? 2 : 8, kGroup = 32 / kP;   // lanes of one number
+    const int l = threadIdx.x % 32;
+    float v[kP];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int i = 0; i < kP; ++i) v[i] = i < kN ? x[i] : 0.0f;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) x[i] = __fadd_rn(x[i], __shfl_xor_sync(0xffffffffu, x[i], o));
-    if (a.warps == 1) return;
-    float4* mine = red[turn] + team * a.warps;
-    if (threadIdx.x % 32 == 0) mine[lane / 32] = make_float4(x[0], kN > 1 ? x[kN > 1] : 0.0f, kN > 2 ? x[kN - 1] : 0.0f, 0.0f);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(lanes) : "memory");
-    float4 s = mine[0];
-    for (int w = 1; w < a.warps; ++w) {
-      const float4 y = mine[w];
-      s.x = __fadd_rn(s.x, y.x);
-      if (kN > 1) s.y = __fadd_rn(s.y, y.y);
-      if (kN > 2) s.z = __fadd_rn(s.z, y.z);
+    for (int n = kP / 2, o = 16; n > 0; n /= 2, o /= 2) {
+      const bool upper = l & o;
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float send = upper ? v[i] : v[i + n];
+        v[i] = __fadd_rn(upper ? v[i + n] : v[i], __shfl_xor_sync(0xffffffffu, send, o));
+      }
     }
-    x[0] = s.x;
-    if (kN > 1) x[kN > 1] = s.y;
-    if (kN > 2) x[kN - 1] = s.z;
-    turn ^= 1;
+#pragma unroll
+    for (int o = kGroup / 2; o > 0; o /= 2) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    if (warps > 1) {
+      float* mine = red[turn] + team * warps * kP;
+      if (l % kGroup == 0) mine[warp * kP + l / kGroup] = v[0];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(lanes()) : "memory");
+      float s = 0.0f;
+      for (int w = l % kGroup; w < warps; w += kGroup) s = __fadd_rn(s, mine[w * kP + l / kGroup]);
+#pragma unroll
+      for (int o = kGroup / 2; o > 0; o /= 2) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      v[0] = s;
+      turn ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kN; ++i) x[i] = kP == 1 ? v[0] : __shfl_sync(0xffffffffu, v[0], i * kGroup);
   }
 };
 
@@ -243,30 +233,48 @@ __device__ __forceinline__ void act8(int kind, float2* g, float2* slope) {
 
 __device__ __forceinline__ float add2(float2 x) { return __fadd_rn(x.x, x.y); }
 
-template <typename T, typename S, int kC, bool kWide>
+// kPost: the branch is normalised.  kExtra: it may have a gate, a dropout.
+template <typename T, typename S, int kC, bool kWide, bool kPost, bool kExtra>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
-  __shared__ float4 s_red[2][kJoinThreads / 32];
-  const int lanes = a.warps * 32;
-  const Lane<kC, kWide> me{a, s_ring, (int)blockDim.x, (int)threadIdx.x / lanes, (int)threadIdx.x % lanes, lanes};
+  __shared__ float s_red[2][kJoinThreads / 32 * 8];
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
+  const int row = a.vecs * 512;                                            // of the ring, a warp's
+  const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   constexpr int kY = kC * kVecs<S>, kGate = kY + kC * kVecs<T>;   // vectors: x, y, gate
-  const bool with_y = a.y.data, with_gate = a.gate.data;
+  const bool gated = kExtra && a.gate.data, drops = kExtra && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
-  const uint32_t rng_step = a.drop.cut ? step_of(a.drop) : 0;
+  const int rows = first < a.tokens ? (int)((a.tokens - first + step - 1) / step) : 0;   // of this team
+  const uint32_t rng_step = drops ? step_of(a.drop) : 0;
   const float scale = __fmul_rn(a.beta, a.drop.factor);
 
-  const auto fetch = [&](int64_t t, int at) {
-    if (t < a.tokens) {
-      me.template fetch<S>(a.x, t, at, 0);
-      if (with_y) me.template fetch<T>(a.y, t, at, kY);
-      if (with_gate) me.template fetch<T>(a.gate, t, at, kGate);
+  // where the team's next rows are to be read, and its present ones written
+  const char* x = a.x.data + first * a.x.stride;
+  const char* y = a.y.data + first * a.y.stride;
+  const char* gate = gated ? a.gate.data + first * a.gate.stride : nullptr;
+  char* x_out = a.x_out.data + first * a.x_out.stride;
+  char* h = a.h.data + first * a.h.stride;
+  const uint8_t* mask = a.mask + first;
+  int64_t block = first * a.chunks;         // of the generator
+  const auto fetch = [&](bool on, int at) {
+    if (on) {
+      me.template fetch<S>(x, at, 0);
+      me.template fetch<T>(y, at, kY);
+      x += step * a.x.stride;
+      y += step * a.y.stride;
+      if (gated) {
+        me.template fetch<T>(gate, at, kGate);
+        gate += step * a.gate.stride;
+      }
     }
     if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   // the gains stay in registers where there is room for them
   constexpr bool kKeep = kC <= 2;
   float2 yg_[kKeep ? kC : 1][4], g_[kKeep ? kC : 1][4];
+  const int ahead = a.ring - 1;
+  for (int k = 0; k < ahead; ++k) fetch(k < rows, k * row);
   if constexpr (kKeep)
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
@@ -274,79 +282,76 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       me.gain(a.gain, j, g_[j]);
     }
 
-  const int ahead = a.ring - 1;
-  for (int k = 0; k < ahead; ++k) fetch(first + k * step, k);
   int at = 0, turn = 0;
-  bool there = first < a.tokens && (!a.mask || __ldg(a.mask + first));
-  for (int64_t t = first; t < a.tokens; t += step) {
+  bool there = rows > 0 && (!a.mask || __ldg(mask));
+  for (int i = 0; i < rows; ++i) {
     if (!kWide) __syncwarp();
-    fetch(t + ahead * step, at + ahead >= a.ring ? at + ahead - a.ring : at + ahead);
-    const bool next = t + step < a.tokens && (!a.mask || __ldg(a.mask + t + step));
+    fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
+    bool next = true;
+    if (a.mask && i + 1 < rows) next = __ldg(mask += step);
     uint32_t bits[kC];
-    if (a.drop.cut && there)
+    if (drops && there)
 #pragma unroll
-      for (int j = 0; j < kC; ++j)
-        if (me.live(j)) bits[j] = kept(a.drop, rng_step, t * a.chunks + me.chunk(j));
+      for (int j = 0; j < kC; ++j) bits[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
     else __syncwarp();
     float2 v[kC][4];
     if (there) {
       float ry = scale;
-      if (with_y && a.post) {
+      if constexpr (kPost) {
         float2 sq = both(0.0f);
 #pragma unroll
         for (int j = 0; j < kC; ++j)
           if (me.live(j)) {
-            float2 y[4];
-            me.template get<T>(at, kY + j * kVecs<T>, y);
+            float2 b[4];
+            me.template get<T>(at, kY + j * kVecs<T>, b);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sq = __ffma2_rn(y[k], y[k], sq);
+            for (int k = 0; k < 4; ++k) sq = __ffma2_rn(b[k], b[k], sq);
           }
-        float s[1] = {add2(sq)};
-        me.sum(s, s_red, turn);
-        ry = __fmul_rn(rsqrtf(__fmaf_rn(s[0], a.inv_dim, a.eps)), scale);
+        float s = add2(sq);
+        me.template sum<1>(&s, s_red, turn);
+        ry = __fmul_rn(rsqrtf(__fmaf_rn(s, a.inv_dim, a.eps_y)), scale);
       }
       float2 sq = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         if (!me.live(j)) continue;
+        float2 b[4], w[4];
         me.template get<S>(at, j * kVecs<S>, v[j]);
-        if (with_y) {
-          float2 b[4], w[4];
-          me.template get<T>(at, kY + j * kVecs<T>, b);
-          if constexpr (!kKeep) me.gain(a.y_gain, j, w);
+        me.template get<T>(at, kY + j * kVecs<T>, b);
+        if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(__fmul2_rn(b[k], both(ry)), kKeep ? yg_[j][k] : w[k]);
-          if (with_gate) {
-            float2 g[4], slope[4];
-            me.template get<T>(at, kGate + j * kVecs<T>, g);
-            act8(a.gate_kind, g, slope);
+        for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(__fmul2_rn(b[k], both(ry)), kKeep ? yg_[j][k] : w[k]);
+        if (gated) {
+          float2 g[4], slope[4];
+          me.template get<T>(at, kGate + j * kVecs<T>, g);
+          act8(a.gate_kind, g, slope);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(b[k], g[k]);
-          }
-          if (a.drop.cut) drop8(b, bits[j]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[j][k] = __ffma2_rn(v[j][k], both(a.alpha), b[k]);
+          for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(b[k], g[k]);
         }
+        if (drops) drop8(b, bits[j]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sq = __ffma2_rn(v[j][k], v[j][k], sq);
+        for (int k = 0; k < 4; ++k) {
+          v[j][k] = __ffma2_rn(v[j][k], both(a.alpha), b[k]);
+          sq = __ffma2_rn(v[j][k], v[j][k], sq);
+        }
       }
       // a narrow result goes out through the places of what was read
       if (a.x_out.data) {
 #pragma unroll
-        for (int j = 0; j < kC; ++j) me.template put<S>(a.x_out, t, j, v[j], at, j * kVecs<S>);
+        for (int j = 0; j < kC; ++j) me.template put<S>(x_out, j, v[j], at, j * kVecs<S>);
       }
-      if (a.pre) {
-        float s[1] = {add2(sq)};
-        me.sum(s, s_red, turn);
-        const float2 r = both(rsqrtf(__fmaf_rn(s[0], a.inv_dim, a.eps)));
+      if (a.h.data) {
+        float s = add2(sq);
+        me.template sum<1>(&s, s_red, turn);
+        const float2 r = both(rsqrtf(__fmaf_rn(s, a.inv_dim, a.eps)));
 #pragma unroll
         for (int j = 0; j < kC; ++j) {
           float2 w[4];
           if constexpr (!kKeep) me.gain(a.gain, j, w);
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[j][k] = __fmul2_rn(__fmul2_rn(v[j][k], r), kKeep ? g_[j][k] : w[k]);
-          me.template put<T>(a.h, t, j, v[j], at, kY + j * kVecs<T>);
+          me.template put<T>(h, j, v[j], at, kY + j * kVecs<T>);
         }
       }
     } else {
@@ -354,43 +359,65 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       for (int j = 0; j < kC; ++j) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[j][k] = both(0.0f);
-        if (a.x_out.data) me.template put<S>(a.x_out, t, j, v[j], at, j * kVecs<S>);
-        if (a.pre) me.template put<T>(a.h, t, j, v[j], at, kY + j * kVecs<T>);
+        if (a.x_out.data) me.template put<S>(x_out, j, v[j], at, j * kVecs<S>);
+        if (a.h.data) me.template put<T>(h, j, v[j], at, kY + j * kVecs<T>);
       }
     }
+    x_out += step * a.x_out.stride;
+    h += step * a.h.stride;
+    block += step * a.chunks;
     there = next;
-    at = at + 1 == a.ring ? 0 : at + 1;
+    at = at + row == a.ring * row ? 0 : at + row;
   }
 }
 
-template <typename T, typename S, int kC, bool kWide>
+template <typename T, typename S, int kC, bool kWide, bool kPost, bool kExtra>
 __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
-  __shared__ float4 s_red[2][kJoinThreads / 32];
-  const int lanes = a.warps * 32;
-  const Lane<kC, kWide> me{a, s_ring, (int)blockDim.x, (int)threadIdx.x / lanes, (int)threadIdx.x % lanes, lanes};
+  __shared__ float s_red[2][kJoinThreads / 32 * 8];
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
+  const int row = a.vecs * 512;                                            // of the ring, a warp's
+  const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   // vectors: x', dx', dh, y, gate
   constexpr int kDxo = kC * kVecs<S>, kDh = 2 * kDxo, kY = kDh + kC * kVecs<T>, kGate = kY + kC * kVecs<T>;
-  const bool with_y = a.y.data, with_gate = a.gate.data;
+  const bool gated = kExtra && a.gate.data, drops = kExtra && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
-  const uint32_t rng_step = a.drop.cut ? step_of(a.drop) : 0;
+  const int rows = first < a.tokens ? (int)((a.tokens - first + step - 1) / step) : 0;
+  const uint32_t rng_step = drops ? step_of(a.drop) : 0;
   const float scale = __fmul_rn(a.beta, a.drop.factor);
 
-  const auto fetch = [&](int64_t t, int at) {
-    if (t < a.tokens) {
-      if (a.dh.data) {
-        me.template fetch<S>(a.x, t, at, 0);
-        me.template fetch<T>(a.dh, t, at, kDh);
+  const char* x = a.x.data + first * a.x.stride;
+  const char* dxo = a.dxo.data + first * a.dxo.stride;
+  const char* dh = a.dh.data + first * a.dh.stride;
+  const char* y = a.y.data + first * a.y.stride;
+  const char* gate = gated ? a.gate.data + first * a.gate.stride : nullptr;
+  char* dx = a.dx.data + first * a.dx.stride;
+  char* dy = a.dy.data + first * a.dy.stride;
+  char* dgate = gated ? a.dgate.data + first * a.dgate.stride : nullptr;
+  const uint8_t* mask = a.mask + first;
+  int64_t block = first * a.chunks;
+  const auto fetch = [&](bool on, int at) {
+    if (on) {
+      me.template fetch<S>(x, at, 0);
+      me.template fetch<S>(dxo, at, kDxo);
+      me.template fetch<T>(dh, at, kDh);
+      me.template fetch<T>(y, at, kY);
+      x += step * a.x.stride;
+      dxo += step * a.dxo.stride;
+      dh += step * a.dh.stride;
+      y += step * a.y.stride;
+      if (gated) {
+        me.template fetch<T>(gate, at, kGate);
+        gate += step * a.gate.stride;
       }
-      if (a.dxo.data) me.template fetch<S>(a.dxo, t, at, kDxo);
-      if (with_y) me.template fetch<T>(a.y, t, at, kY);
-      if (with_gate) me.template fetch<T>(a.gate, t, at, kGate);
     }
     if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   constexpr bool kKeep = kC <= 2;
   float2 yg_[kKeep ? kC : 1][4], g_[kKeep ? kC : 1][4];
+  const int ahead = a.ring - 1;
+  for (int k = 0; k < ahead; ++k) fetch(k < rows, k * row);
   if constexpr (kKeep)
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
@@ -403,156 +430,157 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 4; ++k) dyg[j][k] = dg[j][k] = both(0.0f);
 
-  const int ahead = a.ring - 1;
-  for (int k = 0; k < ahead; ++k) fetch(first + k * step, k);
   int at = 0, turn = 0;
-  bool there = first < a.tokens && (!a.mask || __ldg(a.mask + first));
-  for (int64_t t = first; t < a.tokens; t += step) {
+  bool there = rows > 0 && (!a.mask || __ldg(mask));
+  for (int i = 0; i < rows; ++i) {
     if (!kWide) __syncwarp();
-    fetch(t + ahead * step, at + ahead >= a.ring ? at + ahead - a.ring : at + ahead);
-    const bool next = t + step < a.tokens && (!a.mask || __ldg(a.mask + t + step));
+    fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
+    bool next = true;
+    if (a.mask && i + 1 < rows) next = __ldg(mask += step);
     uint32_t bits[kC];
-    if (a.drop.cut && there && with_y)
+    if (drops && there)
 #pragma unroll
-      for (int j = 0; j < kC; ++j)
-        if (me.live(j)) bits[j] = kept(a.drop, rng_step, t * a.chunks + me.chunk(j));
+      for (int j = 0; j < kC; ++j) bits[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
     else __syncwarp();
-    float2 G[kC][4];
     if (there) {
-      float2 sx = both(0.0f), sd = both(0.0f), sy = both(0.0f);
+      // With q = act y_gain y where the branch is kept, the branch's own dot product
+      // sum G q is linear in G, so that its parts are summed before r is known: one
+      // sum over the team a row.
+      float2 s2[kPost ? 6 : 2];
+#pragma unroll
+      for (int k = 0; k < (kPost ? 6 : 2); ++k) s2[k] = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         if (!me.live(j)) continue;
-        if (a.dh.data) {
-          float2 x[4], d[4], w[4];
-          me.template get<S>(at, j * kVecs<S>, x);
-          me.template get<T>(at, kDh + j * kVecs<T>, d);
-          if constexpr (!kKeep) me.gain(a.gain, j, w);
+        float2 xv[4], d[4], w[4];
+        me.template get<S>(at, j * kVecs<S>, xv);
+        me.template get<T>(at, kDh + j * kVecs<T>, d);
+        if constexpr (!kKeep) me.gain(a.gain, j, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          d[k] = __fmul2_rn(d[k], kKeep ? g_[j][k] : w[k]);
+          s2[0] = __ffma2_rn(xv[k], xv[k], s2[0]);
+          s2[1] = __ffma2_rn(d[k], xv[k], s2[1]);
+        }
+        if constexpr (kPost) {
+          float2 q[4], o[4];
+          me.template get<T>(at, kY + j * kVecs<T>, q);
+          me.template get<S>(at, kDxo + j * kVecs<S>, o);
+          if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            sx = __ffma2_rn(x[k], x[k], sx);
-            sd = __ffma2_rn(__fmul2_rn(d[k], kKeep ? g_[j][k] : w[k]), x[k], sd);
+            s2[2] = __ffma2_rn(q[k], q[k], s2[2]);
+            q[k] = __fmul2_rn(q[k], kKeep ? yg_[j][k] : w[k]);
+          }
+          if (gated) {
+            float2 g[4], slope[4];
+            me.template get<T>(at, kGate + j * kVecs<T>, g);
+            act8(a.gate_kind, g, slope);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], g[k]);
+          }
+          // What is dropped may be anything.  (Of x' and dh not: one of their numbers
+          // that is not finite is in every number of G, by the norm's mean.)
+          if (drops) {
+            drop8(q, bits[j]);
+            drop8(o, bits[j]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s2[3] = __ffma2_rn(o[k], q[k], s2[3]);
+            s2[4] = __ffma2_rn(d[k], q[k], s2[4]);
+            s2[5] = __ffma2_rn(xv[k], q[k], s2[5]);
           }
         }
-        if (with_y && a.post) {
-          float2 y[4];
-          me.template get<T>(at, kY + j * kVecs<T>, y);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) sy = __ffma2_rn(y[k], y[k], sy);
-        }
       }
-      float s[3] = {add2(sx), add2(sd), add2(sy)};
-      me.sum(s, s_red, turn);
+      float s[kPost ? 6 : 2];
+#pragma unroll
+      for (int k = 0; k < (kPost ? 6 : 2); ++k) s[k] = add2(s2[k]);
+      me.template sum<kPost ? 6 : 2>(s, s_red, turn);
       // G = dx' + r (dn - xhat mean(dn xhat)), dn = dh gain: no power of r but the
       // first, so that it holds for rows of any size
       const float r = rsqrtf(__fmaf_rn(s[0], a.inv_dim, a.eps));
       const float back = __fmul_rn(-r, __fmul_rn(__fmul_rn(r, s[1]), a.inv_dim));
-      const float ry = a.post ? rsqrtf(__fmaf_rn(s[2], a.inv_dim, a.eps)) : 1.0f;
-      float2 dot = both(0.0f);
+      float ry = 1.0f, back_y = 0.0f;
+      if constexpr (kPost) {
+        ry = rsqrtf(__fmaf_rn(s[2], a.inv_dim, a.eps_y));
+        const float dot = __fmul_rn(scale, __fmaf_rn(back, __fmul_rn(r, s[5]), __fmaf_rn(r, s[4], s[3])));
+        back_y = __fmul_rn(-ry, __fmul_rn(__fmul_rn(ry, dot), a.inv_dim));
+      }
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
+        float2 G[4], o[4], slope[4];
         if (me.live(j)) {
+          float2 xv[4], d[4], w[4];
+          me.template get<S>(at, j * kVecs<S>, xv);
+          me.template get<T>(at, kDh + j * kVecs<T>, d);
+          me.template get<S>(at, kDxo + j * kVecs<S>, G);
+          if constexpr (!kKeep) me.gain(a.gain, j, w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) G[j][k] = both(0.0f);
-          if (a.dxo.data) me.template get<S>(at, kDxo + j * kVecs<S>, G[j]);
-          if (a.dh.data) {
-            float2 x[4], d[4], w[4];
-            me.template get<S>(at, j * kVecs<S>, x);
-            me.template get<T>(at, kDh + j * kVecs<T>, d);
-            if constexpr (!kKeep) me.gain(a.gain, j, w);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 xhat = __fmul2_rn(x[k], both(r));
-              dg[j][k] = __ffma2_rn(d[k], xhat, dg[j][k]);
-              const float2 dn = __fmul2_rn(d[k], kKeep ? g_[j][k] : w[k]);
-              G[j][k] = __fadd2_rn(G[j][k], __ffma2_rn(dn, both(r), __fmul2_rn(xhat, both(back))));
-            }
+          for (int k = 0; k < 4; ++k) {
+            const float2 xhat = __fmul2_rn(xv[k], both(r));
+            dg[j][k] = __ffma2_rn(d[k], xhat, dg[j][k]);
+            const float2 dn = __fmul2_rn(d[k], kKeep ? g_[j][k] : w[k]);
+            G[k] = __fadd2_rn(G[k], __ffma2_rn(dn, both(r), __fmul2_rn(xhat, both(back))));
+            o[k] = __fmul2_rn(G[k], both(a.alpha));
           }
         }
-        if (a.dx.data) {
-          float2 o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) o[k] = with_y ? __fmul2_rn(G[j][k], both(a.alpha)) : G[j][k];
-          me.template put<S>(a.dx, t, j, o, at, j * kVecs<S>);
-        }
-        if (!with_y || !me.live(j)) continue;
-        // G becomes db, and the dot product of dz y_gain and y is taken
-#pragma unroll
-        for (int k = 0; k < 4; ++k) G[j][k] = __fmul2_rn(G[j][k], both(scale));
-        if (a.drop.cut) drop8(G[j], bits[j]);
-        if (a.post) {
-          float2 y[4], g[4], w[4], slope[4];
-          me.template get<T>(at, kY + j * kVecs<T>, y);
-          if (with_gate) {
+        if (a.dx.data) me.template put<S>(dx, j, o, at, j * kVecs<S>);
+        if (me.live(j)) {
+          float2 yv[4], g[4], w[4];
+          me.template get<T>(at, kY + j * kVecs<T>, yv);
+          if (gated) {
             me.template get<T>(at, kGate + j * kVecs<T>, g);
             act8(a.gate_kind, g, slope);
-            if (a.drop.cut) drop8(g, bits[j]);
           }
           if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 dz = with_gate ? __fmul2_rn(G[j][k], g[k]) : G[j][k];
-            dot = __ffma2_rn(__fmul2_rn(dz, kKeep ? yg_[j][k] : w[k]), y[k], dot);
+            G[k] = __fmul2_rn(G[k], both(scale));       // db
+            if constexpr (kPost) {
+              yv[k] = __fmul2_rn(yv[k], both(ry));
+              o[k] = __fmul2_rn(yv[k], both(back_y));
+            }
+          }
+          if (drops) {
+            drop8(G, bits[j]);
+            drop8(yv, bits[j]);
+            if (gated) {
+              drop8(g, bits[j]);
+              drop8(slope, bits[j]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 yg = kKeep ? yg_[j][k] : w[k];
+            if (gated) {
+              slope[k] = __fmul2_rn(__fmul2_rn(__fmul2_rn(G[k], slope[k]), yv[k]), yg);
+              G[k] = __fmul2_rn(G[k], g[k]);
+            }
+            dyg[j][k] = __ffma2_rn(G[k], yv[k], dyg[j][k]);
+            G[k] = __fmul2_rn(G[k], yg);
+            o[k] = kPost ? __ffma2_rn(G[k], both(ry), o[k]) : G[k];
           }
         }
-      }
-      if (with_y) {
-        float backy = 0.0f;
-        if (a.post) {
-          float s2[1] = {add2(dot)};
-          me.sum(s2, s_red, turn);
-          backy = __fmul_rn(-ry, __fmul_rn(__fmul_rn(ry, s2[0]), a.inv_dim));
-        }
-#pragma unroll
-        for (int j = 0; j < kC; ++j) {
-          float2 slope[4];
-          float2 o[4];
-          if (me.live(j)) {
-            float2 y[4], g[4], w[4];
-            me.template get<T>(at, kY + j * kVecs<T>, y);
-            if (with_gate) {
-              me.template get<T>(at, kGate + j * kVecs<T>, g);
-              act8(a.gate_kind, g, slope);
-            }
-            if constexpr (!kKeep) me.gain(a.y_gain, j, w);
-            float2 rest[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              y[k] = __fmul2_rn(y[k], both(ry));
-              rest[k] = __fmul2_rn(y[k], both(backy));
-            }
-            if (a.drop.cut) {            // a dropped number's factors may be anything
-              drop8(y, bits[j]);
-              if (with_gate) drop8(g, bits[j]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 yg = kKeep ? yg_[j][k] : w[k];
-              const float2 dz = with_gate ? __fmul2_rn(G[j][k], g[k]) : G[j][k];
-              if (with_gate) slope[k] = __fmul2_rn(__fmul2_rn(__fmul2_rn(G[j][k], slope[k]), y[k]), yg);
-              dyg[j][k] = __ffma2_rn(dz, y[k], dyg[j][k]);
-              o[k] = __fmul2_rn(dz, yg);
-              if (a.post) o[k] = __ffma2_rn(o[k], both(ry), rest[k]);
-            }
-            if (a.drop.cut && with_gate) drop8(slope, bits[j]);
-          }
-          if (a.dy.data) me.template put<T>(a.dy, t, j, o, at, kY + j * kVecs<T>);
-          if (a.dgate.data) me.template put<T>(a.dgate, t, j, slope, at, kY + j * kVecs<T>);
-        }
+        if (a.dy.data) me.template put<T>(dy, j, o, at, kY + j * kVecs<T>);
+        if (gated && a.dgate.data) me.template put<T>(dgate, j, slope, at, kY + j * kVecs<T>);
       }
     } else {
+      const float2 zero[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) G[j][k] = both(0.0f);
-        if (a.dx.data) me.template put<S>(a.dx, t, j, G[j], at, j * kVecs<S>);
-        if (a.dy.data) me.template put<T>(a.dy, t, j, G[j], at, kY + j * kVecs<T>);
-        if (a.dgate.data) me.template put<T>(a.dgate, t, j, G[j], at, kY + j * kVecs<T>);
+        if (a.dx.data) me.template put<S>(dx, j, zero, at, j * kVecs<S>);
+        if (a.dy.data) me.template put<T>(dy, j, zero, at, kY + j * kVecs<T>);
+        if (gated && a.dgate.data) me.template put<T>(dgate, j, zero, at, kY + j * kVecs<T>);
       }
     }
+    dx += step * a.dx.stride;
+    dy += step * a.dy.stride;
+    if (gated) dgate += step * a.dgate.stride;
+    block += step * a.chunks;
     there = next;
-    at = at + 1 == a.ring ? 0 : at + 1;
+    at = at + row == a.ring * row ? 0 : at + row;
   }
 
   // The CTA's share of the gains' gradients: its teams' one after the other.
@@ -566,7 +594,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
     const bool last = team == a.teams - 1;
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
-      const int left = me.live(j) ? me.count(j) : 0;
+      const int left = min(8, a.dim - me.chunk(j) * 8);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         if (k >= left) continue;
