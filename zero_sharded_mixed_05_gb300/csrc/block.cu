@@ -77,15 +77,16 @@ __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropA
   constexpr int kE = 16 / (int)sizeof(T), kV = 8 / kE;
   const uint32_t step = zo::step_of(a.drop);
   const auto apply = [&](uint4* p, int64_t block) {
-    const uint32_t bits = zo::kept(a.drop, step, block);
+    const uint4 m = zo::kept(a.drop, step, block);
     float2 x[4];
 #pragma unroll
     for (int v = 0; v < kV; ++v) zo::unpack<T>(p[v], x + v * (kE / 2));
 #pragma unroll
     for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], zo::both(a.drop.factor));
-    zo::drop8(x, bits);
+    if constexpr (sizeof(T) == 4) zo::mask8(x, m);
 #pragma unroll
     for (int v = 0; v < kV; ++v) p[v] = zo::pack<T>(x + v * (kE / 2));
+    if constexpr (sizeof(T) == 2) p[0] = make_uint4(p[0].x & m.x, p[0].y & m.y, p[0].z & m.z, p[0].w & m.w);
   };
   if constexpr (kWide) {
     const int64_t n = a.rows * a.blocks, stride = (int64_t)gridDim.x * blockDim.x;
@@ -102,9 +103,10 @@ __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropA
 #pragma unroll
         for (int v = 0; v < kV; ++v) reinterpret_cast<uint4*>(to)[v] = p[v];
       } else {
-        const uint32_t bits = zo::kept(a.drop, step, b);
+        const uint4 m = zo::kept(a.drop, step, b);
         for (int i = 0; i < left; ++i)
-          to[i] = Num<T>::put(bits >> i & 1 ? __fmul_rn(Num<T>::get(from[i]), a.drop.factor) : 0.0f);
+          to[i] = Num<T>::put(zo::word_of(m, i / 2) >> i % 2 * 16 & 1
+                                  ? __fmul_rn(Num<T>::get(from[i]), a.drop.factor) : 0.0f);
       }
     }
   } else {
@@ -280,7 +282,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   for (const auto& r : rows) wide = wide && on16(r.r->data, r.r->stride, b->tokens);
   // Chunks a thread, warps a team, teams a CTA.
   const int few = a.chunks <= 32 || (b->tokens <= 2 * h->sms && a.chunks <= 512);
-  int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= 1024 ? 2 : 4;
+  int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= (backward ? 1024 : 512) ? 2 : 4;
   a.warps = (a.chunks + 32 * cs - 1) / (32 * cs);
   a.teams = std::max(1, 8 / a.warps);
   a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
@@ -291,7 +293,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.ring = wide ? std::max(1, std::min(3, kMaxSmem / 2 / row)) : 1;
   size_t smem = (size_t)a.ring * row;
   if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
-  const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate || a.drop.cut > 0, cs};
+  const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate ? 2 : a.drop.cut > 0 ? 1 : 0, cs};
   const bool mixed = c.stream_dtype != c.dtype;
   const void* fn = c.dtype == ZERO_FP32   ? zo::join_float(pick)
                    : c.dtype == ZERO_FP16 ? (mixed ? zo::join_half_float(pick) : zo::join_half(pick))

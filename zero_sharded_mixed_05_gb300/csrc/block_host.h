@@ -8,7 +8,7 @@ namespace zo {
 struct JoinPick {
   bool backward, wide;
   bool post;       // the branch is normalised
-  bool extra;      // it has a gate or a dropout
+  int has;         // 0; 1: a dropout; 2: a gate and maybe a dropout
   int chunks;      // a thread: 1, 2 (wide only) or 4
 };
 

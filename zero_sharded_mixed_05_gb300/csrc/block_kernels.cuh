@@ -112,6 +112,19 @@ struct Lane {
       unpack<E>(*reinterpret_cast<const uint4*>(vec(at, n + v)), x + v * (8 / (int)sizeof(E)));
   }
 
+  // The same with the dropped numbers zero.
+  template <typename E>
+  __device__ __forceinline__ void get(int at, int n, float2* x, const uint4& m) const {
+    if constexpr (sizeof(E) == 2) {
+      uint4 w = *reinterpret_cast<const uint4*>(vec(at, n));
+      w = make_uint4(w.x & m.x, w.y & m.y, w.z & m.z, w.w & m.w);
+      unpack<E>(w, x);
+    } else {
+      get<E>(at, n, x);
+      mask8(x, m);
+    }
+  }
+
   // A chunk of a result.  Narrow rows pass through the vectors from n on, which
   // are done with.
   template <typename E>
@@ -203,15 +216,6 @@ struct Lane {
   }
 };
 
-// Eight numbers of which the dropped ones become zero.
-__device__ __forceinline__ void drop8(float2* x, uint32_t bits) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (!(bits >> 2 * k & 1)) x[k].x = 0.0f;
-    if (!(bits >> 2 * k & 2)) x[k].y = 0.0f;
-  }
-}
-
 // The gate's factor, in place, and the factor's derivative.  The sigmoid by
 // e = exp(-|g|), so that neither it nor its derivative e / (1 + e)^2 is a
 // difference of nearly equal numbers.
@@ -233,16 +237,19 @@ __device__ __forceinline__ void act8(int kind, float2* g, float2* slope) {
 
 __device__ __forceinline__ float add2(float2 x) { return __fadd_rn(x.x, x.y); }
 
-// kPost: the branch is normalised.  kExtra: it may have a gate, a dropout.
-template <typename T, typename S, int kC, bool kWide, bool kPost, bool kExtra>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ JoinArgs a) {
+// What the branch has, besides a norm (kPost).
+enum { kBare = 0, kDrop = 1, kGated = 2 };   // nothing; a dropout; either or both
+
+template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas>
+__global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
+    join_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ float s_red[2][kJoinThreads / 32 * 8];
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
   const int row = a.vecs * 512;                                            // of the ring, a warp's
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   constexpr int kY = kC * kVecs<S>, kGate = kY + kC * kVecs<T>;   // vectors: x, y, gate
-  const bool gated = kExtra && a.gate.data, drops = kExtra && a.drop.cut;
+  const bool gated = kHas == kGated && a.gate.data, drops = kHas != kBare && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
   const int rows = first < a.tokens ? (int)((a.tokens - first + step - 1) / step) : 0;   // of this team
@@ -289,10 +296,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
     bool next = true;
     if (a.mask && i + 1 < rows) next = __ldg(mask += step);
-    uint32_t bits[kC];
+    uint4 keep[kHas == kBare ? 1 : kC];
     if (drops && there)
 #pragma unroll
-      for (int j = 0; j < kC; ++j) bits[j] = kept(a.drop, rng_step, block + me.chunk(j));
+      for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
     else __syncwarp();
     float2 v[kC][4];
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
           for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(b[k], g[k]);
         }
-        if (drops) drop8(b, bits[j]);
+        if (drops) mask8(b, keep[kHas == kBare ? 0 : j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           v[j][k] = __ffma2_rn(v[j][k], both(a.alpha), b[k]);
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
 }
 
-template <typename T, typename S, int kC, bool kWide, bool kPost, bool kExtra>
+template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas>
 __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ float s_red[2][kJoinThreads / 32 * 8];
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   // vectors: x', dx', dh, y, gate
   constexpr int kDxo = kC * kVecs<S>, kDh = 2 * kDxo, kY = kDh + kC * kVecs<T>, kGate = kY + kC * kVecs<T>;
-  const bool gated = kExtra && a.gate.data, drops = kExtra && a.drop.cut;
+  const bool gated = kHas == kGated && a.gate.data, drops = kHas != kBare && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
   const int rows = first < a.tokens ? (int)((a.tokens - first + step - 1) / step) : 0;
@@ -437,10 +444,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
     fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
     bool next = true;
     if (a.mask && i + 1 < rows) next = __ldg(mask += step);
-    uint32_t bits[kC];
+    uint4 keep[kHas == kBare ? 1 : kC];
     if (drops && there)
 #pragma unroll
-      for (int j = 0; j < kC; ++j) bits[j] = kept(a.drop, rng_step, block + me.chunk(j));
+      for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
     else __syncwarp();
     if (there) {
@@ -483,8 +490,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           // What is dropped may be anything.  (Of x' and dh not: one of their numbers
           // that is not finite is in every number of G, by the norm's mean.)
           if (drops) {
-            drop8(q, bits[j]);
-            drop8(o, bits[j]);
+            mask8(q, keep[kHas == kBare ? 0 : j]);
+            mask8(o, keep[kHas == kBare ? 0 : j]);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -544,11 +551,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
             }
           }
           if (drops) {
-            drop8(G, bits[j]);
-            drop8(yv, bits[j]);
+            const uint4& m = keep[kHas == kBare ? 0 : j];
+            mask8(G, m);
+            mask8(yv, m);
             if (gated) {
-              drop8(g, bits[j]);
-              drop8(slope, bits[j]);
+              mask8(g, m);
+              mask8(slope, m);
             }
           }
 #pragma unroll

@@ -6,22 +6,30 @@
 
 namespace zo {
 
-template <typename T, typename S, int kC, bool kWide, bool kExtra>
+template <typename T, typename S, int kC, bool kWide, int kHas>
 const void* join_of(bool backward, bool post) {
   if (backward)
-    return post ? (const void*)join_backward_kernel<T, S, kC, kWide, true, kExtra>
-                : (const void*)join_backward_kernel<T, S, kC, kWide, false, kExtra>;
-  return post ? (const void*)join_kernel<T, S, kC, kWide, true, kExtra>
-              : (const void*)join_kernel<T, S, kC, kWide, false, kExtra>;
+    return post ? (const void*)join_backward_kernel<T, S, kC, kWide, true, kHas>
+                : (const void*)join_backward_kernel<T, S, kC, kWide, false, kHas>;
+  return post ? (const void*)join_kernel<T, S, kC, kWide, true, kHas>
+              : (const void*)join_kernel<T, S, kC, kWide, false, kHas>;
 }
 
+template <typename T, typename S, int kC>
+const void* join_of(const JoinPick& p) {
+  return p.has == kBare   ? join_of<T, S, kC, true, kBare>(p.backward, p.post)
+         : p.has == kDrop ? join_of<T, S, kC, true, kDrop>(p.backward, p.post)
+                          : join_of<T, S, kC, true, kGated>(p.backward, p.post);
+}
+
+// Long rows and narrow ones have one kernel for all that a branch may have.
 template <typename T, typename S>
 const void* join_of(const JoinPick& p) {
-  if (!p.wide) return p.chunks == 1 ? join_of<T, S, 1, false, true>(p.backward, p.post) : join_of<T, S, 4, false, true>(p.backward, p.post);
-  if (p.chunks == 4) return join_of<T, S, 4, true, true>(p.backward, p.post);
-  if (p.chunks == 2)
-    return p.extra ? join_of<T, S, 2, true, true>(p.backward, p.post) : join_of<T, S, 2, true, false>(p.backward, p.post);
-  return p.extra ? join_of<T, S, 1, true, true>(p.backward, p.post) : join_of<T, S, 1, true, false>(p.backward, p.post);
+  if (!p.wide)
+    return p.chunks == 1 ? join_of<T, S, 1, false, kGated>(p.backward, p.post)
+                         : join_of<T, S, 4, false, kGated>(p.backward, p.post);
+  if (p.chunks == 4) return join_of<T, S, 4, true, kGated>(p.backward, p.post);
+  return p.chunks == 2 ? join_of<T, S, 2>(p) : join_of<T, S, 1>(p);
 }
 
 }  // namespace zo
