@@ -187,7 +187,7 @@ namespace {
 
 // A row tensor of the call, or none where `p` is NULL.
 JoinRow row_of(const zero_block_rows& r, int es) {
-  return {static_cast<char*>(r.data), r.data ? r.stride * es : 0};
+  return {static_cast<char*>(r.data), r.data ? r.stride * es : 0, 0};
 }
 
 zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool backward) {
@@ -196,6 +196,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   const zero_block_config& c = h->cfg;
   if (b->tokens < 0) return fail(ZERO_EINVAL, "tokens must be >= 0");
   const int es = elem_size(c.dtype), ss = elem_size(c.stream_dtype);
+  const bool mixed = c.stream_dtype != c.dtype;
   const bool with_y = b->y.data != nullptr, with_gate = with_y && c.gate != ZERO_GATE_NONE;
   JoinArgs a = {};
   if (with_y) a.y = row_of(b->y, es);
@@ -213,7 +214,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     if (c.norm_out) a.h = row_of(b->h, es);
   }
   const struct {
-    const JoinRow* r;
+    JoinRow* r;
     const char* name;
     bool result;
     int size;
@@ -270,7 +271,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.beta = (float)c.beta;
   // absent inputs are zeros; without dh the stream is not read, and its norm, which
   // then counts for nothing, stays finite
-  const JoinRow none = {reinterpret_cast<char*>(h->zeros), 0};
+  const JoinRow none = {reinterpret_cast<char*>(h->zeros), 0, 0};
   if (!a.y.data) a.y = none;
   if (backward && !a.dxo.data) a.dxo = none;
   if (backward && !a.dh.data) {
@@ -280,27 +281,38 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.part = want ? h->part : nullptr;
   bool wide = c.dim % 8 == 0;
   for (const auto& r : rows) wide = wide && on16(r.r->data, r.r->stride, b->tokens);
-  // Chunks a thread, warps a team, teams a CTA.
-  const int few = a.chunks <= 32 || (b->tokens <= 2 * h->sms && a.chunks <= 512);
-  int cs = few ? 1 : !wide ? (a.chunks <= 512 ? 1 : 4) : a.chunks <= (backward ? 1024 : 512) ? 2 : 4;
+  // Chunks a thread.  One where there are few, or few rows (a row is done sooner by
+  // more threads); two otherwise forward, which leaves room for three CTAs an SM, and
+  // backward unless the gate's registers or a binary32 stream's ring are too many for
+  // it; four of long rows.
+  const bool one = a.chunks <= 32 || (a.chunks <= 512 && (b->tokens <= 2 * h->sms || !wide));
+  int cs = one ? 1 : wide && a.chunks <= 1024 ? 2 : 4;
+  if (cs == 2 && backward && a.chunks <= 512 && (with_gate || mixed)) cs = 1;
   a.warps = (a.chunks + 32 * cs - 1) / (32 * cs);
   a.teams = std::max(1, 8 / a.warps);
   a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
   const int threads = a.teams * a.warps * 32;
-  const int vt = es / 2, vs = ss / 2;
-  a.vecs = cs * (backward ? 2 * vs + 2 * vt : vs + vt) + (with_gate ? cs * vt : 0);
-  const int row = a.vecs * threads * 16;
-  a.ring = wide ? std::max(1, std::min(3, kMaxSmem / 2 / row)) : 1;
-  size_t smem = (size_t)a.ring * row;
-  if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
-  const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate ? 2 : a.drop.cut > 0 ? 1 : 0, cs};
-  const bool mixed = c.stream_dtype != c.dtype;
+  const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate ? 2 : a.drop.cut > 0 ? 1 : 0, cs,
+                             threads > 256};
   const void* fn = c.dtype == ZERO_FP32   ? zo::join_float(pick)
                    : c.dtype == ZERO_FP16 ? (mixed ? zo::join_half_float(pick) : zo::join_half(pick))
                                           : (mixed ? zo::join_bf16_float(pick) : zo::join_bf16(pick));
+  const int vt = es / 2, vs = ss / 2;
+  a.vecs = cs * (backward ? 2 * vs + 2 * vt : vs + vt) + (with_gate ? cs * vt : 0);
+  const int row = a.vecs * threads * 16;
+  // Rows of the ring: what leaves the SM as many CTAs as its registers hold, two at
+  // least where one has the room.
+  const int ctas = h->resident(fn, threads, row);
+  int most = backward && !mixed ? 2 : 3;
+  a.ring = !wide ? 1 : std::max(std::min(2, kMaxSmem / row), std::min(most, kMaxSmem / (ctas * row)));
+  a.ring = std::max(1, a.ring);
+  size_t smem = (size_t)a.ring * row;
+  if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
   int64_t grid = (b->tokens + a.teams - 1) / a.teams;
-  grid = std::min(grid, (int64_t)h->resident(fn, threads, (int)smem) * h->sms);
+  const int resident = h->resident(fn, threads, (int)smem);
+  grid = std::min(grid, (int64_t)(pick.post || pick.has ? resident : std::min(resident, 2)) * h->sms);
   if (want) grid = std::min(grid, h->max_grid);
+  for (const auto& r : rows) r.r->step = r.r->stride * grid * a.teams;
   void* params[] = {&a};
   e = cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), params, smem, s);
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");

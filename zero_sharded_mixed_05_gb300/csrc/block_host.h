@@ -10,6 +10,7 @@ struct JoinPick {
   bool post;       // the branch is normalised
   int has;         // 0; 1: a dropout; 2: a gate and maybe a dropout
   int chunks;      // a thread: 1, 2 (wide only) or 4
+  bool large;      // more than 256 threads a CTA
 };
 
 // Kernels that take a JoinArgs, by the types of the block and of the stream.

@@ -27,6 +27,7 @@ constexpr int kJoinThreads = 512;   // of a CTA, at most
 struct JoinRow {
   char* data;
   int64_t stride;       // in bytes
+  int64_t step;         // from a team's row to its next one, in bytes
 };
 
 struct JoinArgs {
@@ -73,16 +74,28 @@ struct Lane {
     return smem + at + n * 512 + threadIdx.x % 32 * 16;
   }
 
+  // Zeros in the warp's `bytes` of the ring, if some of its lanes have no chunk: what
+  // is never copied to counts for nothing, and needs no check where it is read.
+  __device__ __forceinline__ void clear(int bytes) const {
+    if (((kC - 1) * warps + warp + 1) * 32 <= chunks) return;
+    for (int at = 0; at < bytes; at += 512) *reinterpret_cast<uint4*>(vec(at, 0)) = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+  }
+
   // A row's chunks into vectors from `first` on.
   template <typename E>
   __device__ __forceinline__ void fetch(const char* row, int at, int first) const {
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
-      if constexpr (kWide) {
-        if (!live(j)) continue;
-        const char* from = row + (uint32_t)chunk(j) * (8 * (uint32_t)sizeof(E));
+      if constexpr (kWide && sizeof(E) == 2) {
+        if (live(j)) copy16(vec(at, first + j), row + (uint32_t)chunk(j) * 16);
+      } else if constexpr (kWide) {
+        // a lane's 32 bytes are two vectors; the warp's 64 are copied in their order,
+        // 32 next to one another at a time
+        const uint32_t begin = (j * warps + warp) * 64, l = threadIdx.x % 32;
 #pragma unroll
-        for (int v = 0; v < kVecs<E>; ++v) copy16(vec(at, first + j * kVecs<E> + v), from + 16 * v);
+        for (uint32_t u = l; u < 64; u += 32)
+          if ((begin + u) * 4 < (uint32_t)dim) copy16(pair(at, first + 2 * j, u), row + (begin + u) * 16);
       } else {
         const int l = threadIdx.x % 32, begin = (j * warps + warp) * 256;
         if (begin >= dim) continue;
@@ -97,19 +110,29 @@ struct Lane {
       }
     }
   }
+  // Vector u of the 64 of a warp's chunks of binary32, the lane's at 2 l and 2 l + 1:
+  // every other group of eight swaps neighbours, so that eight lanes that read (or
+  // write) their first vectors, or their second, meet in no bank.
+  __device__ __forceinline__ unsigned char* pair(int at, int n, uint32_t u) const {
+    return smem + at + n * 512 + (u ^ (u >> 3 & 1)) * 16;
+  }
   // Number e of the 256 that the warp holds in a chunk whose vectors start at n.
   template <typename E>
   __device__ __forceinline__ E* place(int at, int n, int e) const {
     unsigned char* v = smem + at + n * 512;
     if constexpr (sizeof(E) == 2) return reinterpret_cast<E*>(v) + e;
-    else return reinterpret_cast<E*>(v + e % 8 / 4 * 512 + e / 8 * 16) + e % 4;
+    else return reinterpret_cast<E*>(pair(at, n, e / 4)) + e % 4;
   }
 
   template <typename E>
   __device__ __forceinline__ void get(int at, int n, float2* x) const {
-#pragma unroll
-    for (int v = 0; v < kVecs<E>; ++v)
-      unpack<E>(*reinterpret_cast<const uint4*>(vec(at, n + v)), x + v * (8 / (int)sizeof(E)));
+    if constexpr (sizeof(E) == 2) {
+      unpack<E>(*reinterpret_cast<const uint4*>(vec(at, n)), x);
+    } else {
+      const uint32_t u = threadIdx.x % 32 * 2;
+      unpack<E>(*reinterpret_cast<const uint4*>(pair(at, n, u)), x);
+      unpack<E>(*reinterpret_cast<const uint4*>(pair(at, n, u + 1)), x + 2);
+    }
   }
 
   // The same with the dropped numbers zero.
@@ -125,32 +148,40 @@ struct Lane {
     }
   }
 
-  // A chunk of a result.  Narrow rows pass through the vectors from n on, which
-  // are done with.
+  // A chunk of a result.  What a lane does not write as it holds it passes through
+  // the vectors from n on, which are done with, to be written in its order.
   template <typename E>
   __device__ __forceinline__ void put(char* data, int j, const float2* x, int at, int n) const {
-    uint4 p[kVecs<E>];
-#pragma unroll
-    for (int v = 0; v < kVecs<E>; ++v) p[v] = pack<E>(x + v * (8 / (int)sizeof(E)));
+    const uint32_t l = threadIdx.x % 32;
+    if constexpr (kWide && sizeof(E) == 2) {
+      if (live(j)) *reinterpret_cast<uint4*>(data + (uint32_t)chunk(j) * 16) = pack<E>(x);
+      return;
+    }
+    const int begin = (j * warps + warp) * 256;
+    if (begin >= dim) return;
+    if (live(j)) {                 // what no number comes to stays zero
+      if constexpr (sizeof(E) == 2) {
+        *reinterpret_cast<uint4*>(vec(at, n)) = pack<E>(x);
+      } else {
+        *reinterpret_cast<uint4*>(pair(at, n, 2 * l)) = pack<E>(x);
+        *reinterpret_cast<uint4*>(pair(at, n, 2 * l + 1)) = pack<E>(x + 2);
+      }
+    }
+    __syncwarp();
     if constexpr (kWide) {
-      if (!live(j)) return;
-      uint4* to = reinterpret_cast<uint4*>(data + (uint32_t)chunk(j) * (8 * (uint32_t)sizeof(E)));
 #pragma unroll
-      for (int v = 0; v < kVecs<E>; ++v) to[v] = p[v];
+      for (uint32_t u = l; u < 64; u += 32)
+        if (begin + u * 4 < (uint32_t)dim)
+          *reinterpret_cast<uint4*>(data + (begin / 4 + u) * 16) = *reinterpret_cast<const uint4*>(pair(at, n, u));
     } else {
       E* row = reinterpret_cast<E*>(data);
-      const int l = threadIdx.x % 32, begin = (j * warps + warp) * 256;
-      if (begin >= dim) return;
-#pragma unroll
-      for (int v = 0; v < kVecs<E>; ++v) *reinterpret_cast<uint4*>(vec(at, n + v)) = p[v];
-      __syncwarp();
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int e = begin + k * 32 + l;
         if (e < dim) row[e] = *place<E>(at, n, k * 32 + l);
       }
-      __syncwarp();
     }
+    __syncwarp();
   }
 
   // A chunk of a gain (NULL: ones).
@@ -185,6 +216,7 @@ struct Lane {
   template <int kN>
   __device__ __forceinline__ void sum(float* x, float (*red)[kJoinThreads / 32 * 8], int& turn) const {
     constexpr int kP = kN <= 1 ? 1 : kN <= 2 ? 2 : 8, kGroup = 32 / kP;   // lanes of one number
+    static_assert(kJoinThreads / 32 <= 16, "16 lanes take the warps' sums");
     const int l = threadIdx.x % 32;
     float v[kP];
 #pragma unroll
@@ -204,10 +236,15 @@ struct Lane {
       float* mine = red[turn] + team * warps * kP;
       if (l % kGroup == 0) mine[warp * kP + l / kGroup] = v[0];
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(lanes()) : "memory");
+      constexpr int kTake = kGroup < 16 ? kGroup : 16;
       float s = 0.0f;
-      for (int w = l % kGroup; w < warps; w += kGroup) s = __fadd_rn(s, mine[w * kP + l / kGroup]);
 #pragma unroll
-      for (int o = kGroup / 2; o > 0; o /= 2) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+      for (int k = 0; k < 16; k += kTake) {
+        const int w = k + l % kTake;
+        if (w < warps) s = __fadd_rn(s, mine[w * kP + (kP == 1 ? 0 : l / kGroup)]);
+      }
+#pragma unroll
+      for (int o = kTake / 2; o > 0; o /= 2) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
       v[0] = s;
       turn ^= 1;
     }
@@ -218,18 +255,24 @@ struct Lane {
 
 // The gate's factor, in place, and the factor's derivative.  The sigmoid by
 // e = exp(-|g|), so that neither it nor its derivative e / (1 + e)^2 is a
-// difference of nearly equal numbers.
+// difference of nearly equal numbers.  For 16-bit data e is the quick exponential,
+// 2 + 1.2 |g| units in the last place of binary32 off at most, which is far below
+// those types' steps wherever e counts beside 1.
+template <typename T>
 __device__ __forceinline__ float sigmoid(float g, float* slope) {
-  const float e = expf(-fabsf(g)), inv = __frcp_rn(__fadd_rn(1.0f, e)), low = __fmul_rn(e, inv);
+  const float e = sizeof(T) == 2 ? __expf(-fabsf(g)) : expf(-fabsf(g));
+  const float inv = sizeof(T) == 2 ? __fdividef(1.0f, __fadd_rn(1.0f, e)) : __frcp_rn(__fadd_rn(1.0f, e));
+  const float low = __fmul_rn(e, inv);
   *slope = __fmul_rn(low, inv);
   return g >= 0.0f ? inv : low;
 }
 
+template <typename T>
 __device__ __forceinline__ void act8(int kind, float2* g, float2* slope) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (kind == ZERO_GATE_SIGMOID)
-      g[k] = make_float2(sigmoid(g[k].x, &slope[k].x), sigmoid(g[k].y, &slope[k].y));
+      g[k] = make_float2(sigmoid<T>(g[k].x, &slope[k].x), sigmoid<T>(g[k].y, &slope[k].y));
     else
       slope[k] = both(1.0f);
   }
@@ -240,15 +283,16 @@ __device__ __forceinline__ float add2(float2 x) { return __fadd_rn(x.x, x.y); }
 // What the branch has, besides a norm (kPost).
 enum { kBare = 0, kDrop = 1, kGated = 2 };   // nothing; a dropout; either or both
 
-template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas>
-__global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
-    join_kernel(const __grid_constant__ JoinArgs a) {
+// kMost: threads of a CTA at most; of 256 there are three an SM.
+template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas, int kMost>
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) join_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ float s_red[2][kJoinThreads / 32 * 8];
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
   const int row = a.vecs * 512;                                            // of the ring, a warp's
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   constexpr int kY = kC * kVecs<S>, kGate = kY + kC * kVecs<T>;   // vectors: x, y, gate
+  constexpr bool kShared = !kWide || sizeof(S) == 4;   // lanes read what others of their warp copied
   const bool gated = kHas == kGated && a.gate.data, drops = kHas != kBare && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
@@ -268,18 +312,20 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
     if (on) {
       me.template fetch<S>(x, at, 0);
       me.template fetch<T>(y, at, kY);
-      x += step * a.x.stride;
-      y += step * a.y.stride;
+      x += a.x.step;
+      y += a.y.step;
       if (gated) {
         me.template fetch<T>(gate, at, kGate);
-        gate += step * a.gate.stride;
+        gate += a.gate.step;
       }
     }
     if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  // the gains stay in registers where there is room for them
+  // the gains stay in registers where there is room for them; columns that no lane
+  // has are zeros from here on, which change no sum
   constexpr bool kKeep = kC <= 2;
   float2 yg_[kKeep ? kC : 1][4], g_[kKeep ? kC : 1][4];
+  me.clear(a.ring * row);
   const int ahead = a.ring - 1;
   for (int k = 0; k < ahead; ++k) fetch(k < rows, k * row);
   if constexpr (kKeep)
@@ -289,11 +335,11 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
       me.gain(a.gain, j, g_[j]);
     }
 
-  int at = 0, turn = 0;
+  int at = 0, to = ahead * row, turn = 0;     // the rings' rows that are read, and copied to
   bool there = rows > 0 && (!a.mask || __ldg(mask));
   for (int i = 0; i < rows; ++i) {
-    if (!kWide) __syncwarp();
-    fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
+    if (kShared) __syncwarp();     // all have read what is fetched over
+    fetch(i + ahead < rows, to);
     bool next = true;
     if (a.mask && i + 1 < rows) next = __ldg(mask += step);
     uint4 keep[kHas == kBare ? 1 : kC];
@@ -301,20 +347,19 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
 #pragma unroll
       for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
-    else __syncwarp();
+    if (kShared) __syncwarp();
     float2 v[kC][4];
     if (there) {
       float ry = scale;
       if constexpr (kPost) {
         float2 sq = both(0.0f);
 #pragma unroll
-        for (int j = 0; j < kC; ++j)
-          if (me.live(j)) {
-            float2 b[4];
-            me.template get<T>(at, kY + j * kVecs<T>, b);
+        for (int j = 0; j < kC; ++j) {
+          float2 b[4];
+          me.template get<T>(at, kY + j * kVecs<T>, b);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) sq = __ffma2_rn(b[k], b[k], sq);
-          }
+          for (int k = 0; k < 4; ++k) sq = __ffma2_rn(b[k], b[k], sq);
+        }
         float s = add2(sq);
         me.template sum<1>(&s, s_red, turn);
         ry = __fmul_rn(rsqrtf(__fmaf_rn(s, a.inv_dim, a.eps_y)), scale);
@@ -322,7 +367,6 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
       float2 sq = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        if (!me.live(j)) continue;
         float2 b[4], w[4];
         me.template get<S>(at, j * kVecs<S>, v[j]);
         me.template get<T>(at, kY + j * kVecs<T>, b);
@@ -332,7 +376,7 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
         if (gated) {
           float2 g[4], slope[4];
           me.template get<T>(at, kGate + j * kVecs<T>, g);
-          act8(a.gate_kind, g, slope);
+          act8<T>(a.gate_kind, g, slope);
 #pragma unroll
           for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(b[k], g[k]);
         }
@@ -340,8 +384,11 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           v[j][k] = __ffma2_rn(v[j][k], both(a.alpha), b[k]);
-          sq = __ffma2_rn(v[j][k], v[j][k], sq);
         }
+        // (a factor that is infinite makes NaN of a zero that is no number of the row)
+        if (me.live(j))
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sq = __ffma2_rn(v[j][k], v[j][k], sq);
       }
       // a narrow result goes out through the places of what was read
       if (a.x_out.data) {
@@ -370,11 +417,12 @@ __global__ void __launch_bounds__(kC == 2 ? 256 : kJoinThreads, kC == 2 ? 3 : 1)
         if (a.h.data) me.template put<T>(h, j, v[j], at, kY + j * kVecs<T>);
       }
     }
-    x_out += step * a.x_out.stride;
-    h += step * a.h.stride;
+    x_out += a.x_out.step;
+    h += a.h.step;
     block += step * a.chunks;
     there = next;
     at = at + row == a.ring * row ? 0 : at + row;
+    to = to + row == a.ring * row ? 0 : to + row;
   }
 }
 
@@ -382,11 +430,14 @@ template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas>
 __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ float s_red[2][kJoinThreads / 32 * 8];
+  // the kernel that sums the partial gradients may be set up now; it waits for the end
+  if (a.part) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
   const int row = a.vecs * 512;                                            // of the ring, a warp's
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   // vectors: x', dx', dh, y, gate
   constexpr int kDxo = kC * kVecs<S>, kDh = 2 * kDxo, kY = kDh + kC * kVecs<T>, kGate = kY + kC * kVecs<T>;
+  constexpr bool kShared = !kWide || sizeof(S) == 4;   // lanes read what others of their warp copied
   const bool gated = kHas == kGated && a.gate.data, drops = kHas != kBare && a.drop.cut;
   const int64_t step = (int64_t)gridDim.x * a.teams;
   const int64_t first = (int64_t)blockIdx.x * a.teams + me.team;
@@ -410,19 +461,20 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
       me.template fetch<S>(dxo, at, kDxo);
       me.template fetch<T>(dh, at, kDh);
       me.template fetch<T>(y, at, kY);
-      x += step * a.x.stride;
-      dxo += step * a.dxo.stride;
-      dh += step * a.dh.stride;
-      y += step * a.y.stride;
+      x += a.x.step;
+      dxo += a.dxo.step;
+      dh += a.dh.step;
+      y += a.y.step;
       if (gated) {
         me.template fetch<T>(gate, at, kGate);
-        gate += step * a.gate.stride;
+        gate += a.gate.step;
       }
     }
     if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   constexpr bool kKeep = kC <= 2;
   float2 yg_[kKeep ? kC : 1][4], g_[kKeep ? kC : 1][4];
+  me.clear(a.ring * row);
   const int ahead = a.ring - 1;
   for (int k = 0; k < ahead; ++k) fetch(k < rows, k * row);
   if constexpr (kKeep)
@@ -437,11 +489,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
 #pragma unroll
     for (int k = 0; k < 4; ++k) dyg[j][k] = dg[j][k] = both(0.0f);
 
-  int at = 0, turn = 0;
+  int at = 0, to = ahead * row, turn = 0;     // the rings' rows that are read, and copied to
   bool there = rows > 0 && (!a.mask || __ldg(mask));
   for (int i = 0; i < rows; ++i) {
-    if (!kWide) __syncwarp();
-    fetch(i + ahead < rows, at + ahead * row >= a.ring * row ? at + (ahead - a.ring) * row : at + ahead * row);
+    if (kShared) __syncwarp();     // all have read what is fetched over
+    fetch(i + ahead < rows, to);
     bool next = true;
     if (a.mask && i + 1 < rows) next = __ldg(mask += step);
     uint4 keep[kHas == kBare ? 1 : kC];
@@ -449,7 +501,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
     if constexpr (kWide) copies_left(ahead);
-    else __syncwarp();
+    if (kShared) __syncwarp();
     if (there) {
       // With q = act y_gain y where the branch is kept, the branch's own dot product
       // sum G q is linear in G, so that its parts are summed before r is known: one
@@ -459,7 +511,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
       for (int k = 0; k < (kPost ? 6 : 2); ++k) s2[k] = both(0.0f);
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
-        if (!me.live(j)) continue;
         float2 xv[4], d[4], w[4];
         me.template get<S>(at, j * kVecs<S>, xv);
         me.template get<T>(at, kDh + j * kVecs<T>, d);
@@ -483,7 +534,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           if (gated) {
             float2 g[4], slope[4];
             me.template get<T>(at, kGate + j * kVecs<T>, g);
-            act8(a.gate_kind, g, slope);
+            act8<T>(a.gate_kind, g, slope);
 #pragma unroll
             for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], g[k]);
           }
@@ -518,7 +569,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
         float2 G[4], o[4], slope[4];
-        if (me.live(j)) {
+        {
           float2 xv[4], d[4], w[4];
           me.template get<S>(at, j * kVecs<S>, xv);
           me.template get<T>(at, kDh + j * kVecs<T>, d);
@@ -534,12 +585,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           }
         }
         if (a.dx.data) me.template put<S>(dx, j, o, at, j * kVecs<S>);
-        if (me.live(j)) {
+        {
           float2 yv[4], g[4], w[4];
           me.template get<T>(at, kY + j * kVecs<T>, yv);
           if (gated) {
             me.template get<T>(at, kGate + j * kVecs<T>, g);
-            act8(a.gate_kind, g, slope);
+            act8<T>(a.gate_kind, g, slope);
           }
           if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
@@ -583,17 +634,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
         if (gated && a.dgate.data) me.template put<T>(dgate, j, zero, at, kY + j * kVecs<T>);
       }
     }
-    dx += step * a.dx.stride;
-    dy += step * a.dy.stride;
-    if (gated) dgate += step * a.dgate.stride;
+    dx += a.dx.step;
+    dy += a.dy.step;
+    if (gated) dgate += a.dgate.step;
     block += step * a.chunks;
     there = next;
     at = at + row == a.ring * row ? 0 : at + row;
+    to = to + row == a.ring * row ? 0 : to + row;
   }
 
   // The CTA's share of the gains' gradients: its teams' one after the other.
   if (!a.part) return;
-  float* to = a.part + (int64_t)blockIdx.x * 2 * a.dim;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.dim;
   float* s_sum = reinterpret_cast<float*>(s_ring);
   if constexpr (kWide) asm volatile("cp.async.wait_all;" ::: "memory");
   for (int team = 0; team < a.teams; ++team) {
@@ -612,9 +664,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           y = __fadd_rn(s_sum[e], y);
           g = __fadd_rn(s_sum[a.dim + e], g);
         }
-        float* at_ = last ? to : s_sum;
-        at_[e] = y;
-        at_[a.dim + e] = g;
+        float* out = last ? part : s_sum;
+        out[e] = y;
+        out[a.dim + e] = g;
       }
     }
   }

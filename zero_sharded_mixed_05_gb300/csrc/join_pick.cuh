@@ -6,17 +6,21 @@
 
 namespace zo {
 
-template <typename T, typename S, int kC, bool kWide, int kHas>
+template <typename T, typename S, int kC, bool kWide, int kHas, int kMost = kJoinThreads>
 const void* join_of(bool backward, bool post) {
   if (backward)
     return post ? (const void*)join_backward_kernel<T, S, kC, kWide, true, kHas>
                 : (const void*)join_backward_kernel<T, S, kC, kWide, false, kHas>;
-  return post ? (const void*)join_kernel<T, S, kC, kWide, true, kHas>
-              : (const void*)join_kernel<T, S, kC, kWide, false, kHas>;
+  return post ? (const void*)join_kernel<T, S, kC, kWide, true, kHas, kMost>
+              : (const void*)join_kernel<T, S, kC, kWide, false, kHas, kMost>;
 }
 
 template <typename T, typename S, int kC>
 const void* join_of(const JoinPick& p) {
+  if (!p.backward && kC == 2 && !p.large)
+    return p.has == kBare   ? join_of<T, S, kC, true, kBare, 256>(false, p.post)
+           : p.has == kDrop ? join_of<T, S, kC, true, kDrop, 256>(false, p.post)
+                            : join_of<T, S, kC, true, kGated, 256>(false, p.post);
   return p.has == kBare   ? join_of<T, S, kC, true, kBare>(p.backward, p.post)
          : p.has == kDrop ? join_of<T, S, kC, true, kDrop>(p.backward, p.post)
                           : join_of<T, S, kC, true, kGated>(p.backward, p.post);
