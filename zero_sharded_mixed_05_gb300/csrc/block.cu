@@ -300,17 +300,23 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   const int vt = es / 2, vs = ss / 2;
   a.vecs = cs * (backward ? 2 * vs + 2 * vt : vs + vt) + (with_gate ? cs * vt : 0);
   const int row = a.vecs * threads * 16;
-  // Rows of the ring: what leaves the SM as many CTAs as its registers hold, two at
-  // least where one has the room.
-  const int ctas = h->resident(fn, threads, row);
-  int most = backward && !mixed ? 2 : 3;
-  a.ring = !wide ? 1 : std::max(std::min(2, kMaxSmem / row), std::min(most, kMaxSmem / (ctas * row)));
-  a.ring = std::max(1, a.ring);
+  // CTAs an SM and rows of their rings.  Memory is quickest with some 16,384 numbers
+  // of each tensor on their way to an SM: with fewer it is waited for, with more reads
+  // and writes get into one another's way (16,384 rows of 4096 in bf16, two CTAs: two
+  // rows each 81 us, three 92; with both norms 84, 91, three CTAs of two rows 92;
+  // backward 131 and 143, and without the branch's norm, whose rows are done sooner,
+  // one CTA of three rows 125, two of two 142).  A dropout's integer work wants more
+  // CTAs (95 us with three, 104 with two).
+  const int numbers = backward ? (pick.post || pick.has ? 16384 : 12288) : pick.has ? 24576 : 18432;
+  int slots = std::max(1, numbers / (a.teams * c.dim));
+  int ctas = std::max(1, std::min(h->resident(fn, threads, wide ? 2 * row : row), slots / 2));
+  a.ring = !wide ? 1 : ctas == 1 ? 3 : std::max(2, std::min(3, slots / ctas));
+  if (!wide) ctas = kMaxPerSm;
+  a.ring = std::max(1, std::min(a.ring, kMaxSmem / row));
   size_t smem = (size_t)a.ring * row;
   if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
-  int64_t grid = (b->tokens + a.teams - 1) / a.teams;
-  const int resident = h->resident(fn, threads, (int)smem);
-  grid = std::min(grid, (int64_t)(pick.post || pick.has ? resident : std::min(resident, 2)) * h->sms);
+  ctas = std::min(ctas, h->resident(fn, threads, (int)smem));
+  int64_t grid = std::min((b->tokens + a.teams - 1) / a.teams, (int64_t)ctas * h->sms);
   if (want) grid = std::min(grid, h->max_grid);
   for (const auto& r : rows) r.r->step = r.r->stride * grid * a.teams;
   void* params[] = {&a};

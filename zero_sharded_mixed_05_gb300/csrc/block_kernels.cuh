@@ -524,25 +524,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
         if constexpr (kPost) {
           float2 q[4], o[4];
           me.template get<T>(at, kY + j * kVecs<T>, q);
-          me.template get<S>(at, kDxo + j * kVecs<S>, o);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s2[2] = __ffma2_rn(q[k], q[k], s2[2]);
+          // What is dropped may be anything.  (Of x' and dh not: one of their numbers
+          // that is not finite is in every number of G, by the norm's mean; one of y's
+          // makes its own place of the norm's gradient NaN.)
+          if (drops) {
+            me.template get<T>(at, kY + j * kVecs<T>, q, keep[kHas == kBare ? 0 : j]);
+            me.template get<S>(at, kDxo + j * kVecs<S>, o, keep[kHas == kBare ? 0 : j]);
+          } else {
+            me.template get<S>(at, kDxo + j * kVecs<S>, o);
+          }
           if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s2[2] = __ffma2_rn(q[k], q[k], s2[2]);
-            q[k] = __fmul2_rn(q[k], kKeep ? yg_[j][k] : w[k]);
-          }
+          for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], kKeep ? yg_[j][k] : w[k]);
           if (gated) {
             float2 g[4], slope[4];
             me.template get<T>(at, kGate + j * kVecs<T>, g);
             act8<T>(a.gate_kind, g, slope);
 #pragma unroll
             for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], g[k]);
-          }
-          // What is dropped may be anything.  (Of x' and dh not: one of their numbers
-          // that is not finite is in every number of G, by the norm's mean.)
-          if (drops) {
-            mask8(q, keep[kHas == kBare ? 0 : j]);
-            mask8(o, keep[kHas == kBare ? 0 : j]);
+            if (drops) mask8(q, keep[kHas == kBare ? 0 : j]);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -587,7 +589,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
         if (a.dx.data) me.template put<S>(dx, j, o, at, j * kVecs<S>);
         {
           float2 yv[4], g[4], w[4];
-          me.template get<T>(at, kY + j * kVecs<T>, yv);
+          if (!kPost && drops) me.template get<T>(at, kY + j * kVecs<T>, yv, keep[kHas == kBare ? 0 : j]);
+          else me.template get<T>(at, kY + j * kVecs<T>, yv);
           if (gated) {
             me.template get<T>(at, kGate + j * kVecs<T>, g);
             act8<T>(a.gate_kind, g, slope);
@@ -604,7 +607,6 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           if (drops) {
             const uint4& m = keep[kHas == kBare ? 0 : j];
             mask8(G, m);
-            mask8(yv, m);
             if (gated) {
               mask8(g, m);
               mask8(slope, m);
