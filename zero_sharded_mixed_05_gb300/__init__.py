@@ -1039,9 +1039,9 @@ def zero_qk_launch_count(h) -> int:
 
 # ---------------------------------------------------------------- join of a block with the stream, dropout
 
-# What a handle was made for (dim, dtype, stream dtype, norm_out, gated, dropout,
-# device), and memory for one call's zero_block_buffers (calls on one handle are
-# ordered).
+# What a handle was made for (dim, dtype, stream dtype, norm_out, gated, device),
+# the dtypes and the calls that its checks need, and memory for one call's
+# zero_block_buffers (calls on one handle are ordered).
 _block_handles = {}
 _block_pack = struct.Struct("=26qQqqII").pack_into
 _drop_pack = struct.Struct("=6qiidQqqII").pack_into
@@ -1062,8 +1062,9 @@ def zero_block_create(cfg: zero_block_config) -> int:
     types = (torch.float16, torch.bfloat16, torch.float32)
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_block_buffers()
+    small = ((cfg.dim,), torch.float32, torch.bool, torch.uint8)
     _block_handles[h.value] = (cfg.dim, types[cfg.dtype], types[cfg.stream_dtype], bool(cfg.norm_out),
-                               cfg.gate != GATE_NONE, dev, b, ctypes.addressof(b))
+                               cfg.gate != GATE_NONE, dev, small, b, ctypes.addressof(b))
     return h.value
 
 
@@ -1072,12 +1073,13 @@ def zero_block_destroy(h) -> None:
     _check(lib().zero_block_destroy(h), "zero_block_destroy")
 
 
-def _rows(t, name, n, dim, dtype, dev):
+def _rows(t, name, shape, dtype, dev):
     """(address, row stride) of a [tokens, dim] tensor."""
-    st, sd = t.stride() if t.dim() == 2 else (0, 0)
-    if t.dtype is not dtype or t.shape != (n, dim) or t.get_device() != dev or (sd != 1 and dim > 1):
-        _qk_refuse(name, f"a {dtype} tensor of {(n, dim)} with contiguous rows on cuda:{dev}")
-    return t.data_ptr(), st
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        st, sd = t.stride()
+        if sd == 1 or shape[1] == 1:
+            return t.data_ptr(), st
+    _qk_refuse(name, f"a {dtype} tensor of {shape} with contiguous rows on cuda:{dev}")
 
 
 def _rng(seed, call, step, dev):
@@ -1104,14 +1106,8 @@ def _own_stream(stream, dev):
 _NO_ROWS = (0, 0)
 
 
-def _block_small(y_gain, gain, dy_gain, dgain, mask, n, dim, dev):
-    import torch
-    f32, shape = torch.float32, (dim,)
-    out = [0 if g is None else _qk_flat(g, name, shape, f32, dev)
-           for name, g in (("y_gain", y_gain), ("gain", gain), ("dy_gain", dy_gain), ("dgain", dgain))]
-    if mask is None:
-        return (*out, 0)
-    return (*out, _qk_flat(mask, "mask", (n,), torch.uint8 if mask.dtype is torch.uint8 else torch.bool, dev))
+def _block_mask(mask, n, small, dev):
+    return _qk_flat(mask, "mask", (n,), small[3] if mask.dtype is small[3] else small[2], dev)
 
 
 def _block_handle(h):
@@ -1128,20 +1124,23 @@ def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, s
     `mask` is bool [tokens], False for padding, whose results are zero.  `seed`,
     `call` and `step` (an integer, or an int64 tensor on the device) choose the
     dropped numbers."""
-    dim, dtype, sdtype, norm, gated, dev, b, at = _block_handle(h)
+    dim, dtype, sdtype, norm, gated, dev, small, b, at = _block_handle(h)
     n = x.shape[0]
-    px = _rows(x, "x", n, dim, sdtype, dev)
+    shape = (n, dim)
+    px = _rows(x, "x", shape, sdtype, dev)
     py = pg = pxo = ph = _NO_ROWS
     if y is not None:
-        py = _rows(y, "y", n, dim, dtype, dev)
+        py = _rows(y, "y", shape, dtype, dev)
         if gated and gate is not None:
-            pg = _rows(gate, "gate", n, dim, dtype, dev)
+            pg = _rows(gate, "gate", shape, dtype, dev)
         if x_out is not None:
-            pxo = _rows(x_out, "x_out", n, dim, sdtype, dev)
+            pxo = _rows(x_out, "x_out", shape, sdtype, dev)
     if norm and h_out is not None:
-        ph = _rows(h_out, "h_out", n, dim, dtype, dev)
+        ph = _rows(h_out, "h_out", shape, dtype, dev)
     _block_pack(b, 0, n, *px, *py, *pg, *pxo, *ph, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
-                *_block_small(y_gain, gain, None, None, mask, n, dim, dev), *_rng(seed, call, step, dev))
+                0 if y_gain is None else _qk_flat(y_gain, "y_gain", small[0], small[1], dev),
+                0 if gain is None else _qk_flat(gain, "gain", small[0], small[1], dev), 0, 0,
+                0 if mask is None else _block_mask(mask, n, small, dev), *_rng(seed, call, step, dev))
     status = lib().zero_block_join(h, at, _own_stream(stream, dev))
     if status:
         _check(status, "zero_block_join")
@@ -1153,27 +1152,32 @@ def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_
     None: zero), the forward call's `x_out` (without `y`: its `x`), `y` and
     `gate` into `dx`, `dy`, `dgate` and the gains' float32 gradients (None: not
     wanted).  The rng is the forward call's."""
-    dim, dtype, sdtype, norm, gated, dev, b, at = _block_handle(h)
+    dim, dtype, sdtype, norm, gated, dev, small, b, at = _block_handle(h)
     n = x_out.shape[0]
-    px = _rows(x_out, "x_out", n, dim, sdtype, dev)
+    shape = (n, dim)
+    px = _rows(x_out, "x_out", shape, sdtype, dev)
     py = pg = pdxo = pdh = pdx = pdy = pdg = _NO_ROWS
     if dx_out is not None:
-        pdxo = _rows(dx_out, "dx_out", n, dim, sdtype, dev)
+        pdxo = _rows(dx_out, "dx_out", shape, sdtype, dev)
     if norm and dh is not None:
-        pdh = _rows(dh, "dh", n, dim, dtype, dev)
+        pdh = _rows(dh, "dh", shape, dtype, dev)
     if dx is not None:
-        pdx = _rows(dx, "dx", n, dim, sdtype, dev)
+        pdx = _rows(dx, "dx", shape, sdtype, dev)
     if y is not None:
-        py = _rows(y, "y", n, dim, dtype, dev)
+        py = _rows(y, "y", shape, dtype, dev)
         if dy is not None:
-            pdy = _rows(dy, "dy", n, dim, dtype, dev)
+            pdy = _rows(dy, "dy", shape, dtype, dev)
         if gated and gate is not None:
-            pg = _rows(gate, "gate", n, dim, dtype, dev)
-        if gated and dgate is not None:
-            pdg = _rows(dgate, "dgate", n, dim, dtype, dev)
+            pg = _rows(gate, "gate", shape, dtype, dev)
+            if dgate is not None:
+                pdg = _rows(dgate, "dgate", shape, dtype, dev)
+    cols, f32 = small[0], small[1]
     _block_pack(b, 0, n, 0, 0, *py, *pg, *px, 0, 0, *pdxo, *pdh, *pdx, *pdy, *pdg,
-                *_block_small(y_gain, gain, dy_gain, dgain, mask, n, dim, dev),
-                *_rng(seed, call, step, dev))
+                0 if y_gain is None else _qk_flat(y_gain, "y_gain", cols, f32, dev),
+                0 if gain is None else _qk_flat(gain, "gain", cols, f32, dev),
+                0 if dy_gain is None else _qk_flat(dy_gain, "dy_gain", cols, f32, dev),
+                0 if dgain is None else _qk_flat(dgain, "dgain", cols, f32, dev),
+                0 if mask is None else _block_mask(mask, n, small, dev), *_rng(seed, call, step, dev))
     status = lib().zero_block_join_backward(h, at, _own_stream(stream, dev))
     if status:
         _check(status, "zero_block_join_backward")

@@ -32,30 +32,31 @@ struct FoldArgs {
   int32_t grid, dim;
 };
 
-// Sums the CTAs' partial gradients in index order: 32 columns a CTA, 8 threads a
-// column, each over every eighth partial.
-__global__ void __launch_bounds__(256) join_fold_kernel(const __grid_constant__ FoldArgs a) {
-  __shared__ float s[8][33];
+// Sums the CTAs' partial gradients in index order: 32 columns a CTA, kParts threads
+// a column, each over every kParts-th partial.  Eight fill the device for long rows
+// (the gradient of 16,384 rows of 4096 131 us, with 32 136), for short ones 32 are
+// sooner done (of 768: 34.6 us, with 32 32.6).
+template <int kParts>
+__global__ void __launch_bounds__(32 * kParts) join_fold_kernel(const __grid_constant__ FoldArgs a) {
+  __shared__ float s[kParts][33];
   cudaGridDependencySynchronize();   // launched while the partials are still written
   const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32, cols = 2 * a.dim;
   float sum = 0.0f;
   if (col < cols) {
     const float* at = a.part + col;
-    int c = part;
-    for (; c + 56 < a.grid; c += 64) {
-      float v[8];                    // eight loads on their way at once
+    for (int c = part; c < a.grid; c += 10 * kParts) {
+      float v[10];                   // ten loads on their way at once
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = at[(int64_t)(c + 8 * k) * cols];
+      for (int k = 0; k < 10; ++k) v[k] = c + kParts * k < a.grid ? at[(int64_t)(c + kParts * k) * cols] : 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = __fadd_rn(sum, v[k]);
+      for (int k = 0; k < 10; ++k) sum = __fadd_rn(sum, v[k]);
     }
-#pragma unroll 4
-    for (; c < a.grid; c += 8) sum = __fadd_rn(sum, at[(int64_t)c * cols]);
   }
   s[part][threadIdx.x % 32] = sum;
   __syncthreads();
   if (part == 0 && col < cols) {
-    for (int k = 1; k < 8; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
+#pragma unroll
+    for (int k = 1; k < kParts; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
     float* out = a.out[col >= a.dim];
     if (out) out[col >= a.dim ? col - a.dim : col] = sum;
   }
@@ -331,11 +332,12 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)((2 * c.dim + 31) / 32));
-    lc.blockDim = dim3(256);
+    const bool few = c.dim <= 2048;
+    lc.blockDim = dim3(few ? 1024 : 256);
     lc.stream = s;
     lc.attrs = &early;
     lc.numAttrs = 1;
-    e = cudaLaunchKernelExC(&lc, (const void*)join_fold_kernel, fp);
+    e = cudaLaunchKernelExC(&lc, few ? (const void*)join_fold_kernel<32> : (const void*)join_fold_kernel<8>, fp);
     if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
     ++h->launches;
   }

@@ -253,6 +253,7 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   const auto pick = ax.axes > 0 ? zo::qk_kernel_axes : zo::qk_kernel_one;
   const void* fn = pick(c.dtype, c.interleaved, backward, sum, v, r);
   size_t smem = es_vec == 16 ? (size_t)ring_bytes(threads, chunks_lane, r, backward) : 0;
+  if (ax.axes > 0) smem += (size_t)(threads / a.lanes) * zo::kPosSlots * zo::kPosBytes;
   if (want) smem = std::max(smem, (size_t)a.per * a.reps * c.head_dim * sizeof(float));
   const int64_t slots = (b->tokens + a.reps - 1) / a.reps;
   int64_t grid = slots * a.head_blocks;

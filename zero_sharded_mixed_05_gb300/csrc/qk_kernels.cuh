@@ -114,41 +114,35 @@ __device__ __forceinline__ void places(const QkArgs& a, int c, int* p0, int* p1)
   }
 }
 
-__device__ __forceinline__ int64_t position_at(const QkArgs& a, int64_t i) {
+__device__ __forceinline__ int64_t position(const QkArgs& a, int64_t i) {
   return a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + i)
                  : (int64_t)__ldg(static_cast<const int*>(a.pos) + i);
 }
 
-// A token's position, or its positions: `first` is negative for padding and
-// n_pos or more where an axis has no angle.
+// A token's position, or its positions: `first` is negative for padding and n_pos
+// or more where an axis has no angle.
 struct Position {
   int64_t first;
-  __device__ __forceinline__ int64_t of(int) const { return first; }
 };
+// Several lie in shared memory (kPosSlots tokens' for each group of lanes), where
+// they come with the rows, a token ahead of them: in registers, with their checks,
+// they left too few for the rows (16,384 tokens over three axes 74 us, 65 so, with two CTAs an SM).
+constexpr int kPosSlots = 4, kPosBytes = kMaxAxes * 8;
 struct Positions {
-  int first, rest[kMaxAxes - 1];
-  __device__ __forceinline__ int of(int axis) const {
-    const int lo = axis & 1 ? rest[0] : first, hi = axis & 1 ? rest[2] : rest[1];
-    return axis & 2 ? hi : lo;
-  }
+  int first;
+  const unsigned char* at;
+  __device__ __forceinline__ int of(int axis) const { return *reinterpret_cast<const int*>(at + axis * 8); }
 };
 
-__device__ __forceinline__ Position position(const QkArgs& a, int64_t t) { return {position_at(a, t)}; }
-
-__device__ __forceinline__ Positions position(const QkAxesArgs& a, int64_t t) {
-  Positions p;
+__device__ __forceinline__ Positions positions(const QkAxesArgs& a, const unsigned char* at) {
   bool low = false, high = false;
-#pragma unroll
-  for (int k = 0; k < kMaxAxes; ++k) {
-    int64_t v = 0;
-    if (k < a.axes) v = position_at(a, k * a.tokens + t);
+  for (int k = 0; k < a.axes; ++k) {
+    const int64_t v = a.pos64 ? *reinterpret_cast<const int64_t*>(at + k * 8) : (int64_t)*reinterpret_cast<const int*>(at + k * 8);
     low |= v < 0;
-    high |= v >= a.n_pos && k < a.axes;
-    (k == 0 ? p.first : p.rest[k - 1]) = (int)v;
+    high |= v >= a.n_pos;
   }
-  if (high) p.first = 0x7fffffff;      // n_pos is less
-  if (low) p.first = -1;
-  return p;
+  // n_pos is at most the second
+  return {low ? -1 : high ? 0x7fffffff : 0, at};
 }
 
 // The rotation of one chunk, or with -sin its inverse.
@@ -194,7 +188,7 @@ constexpr int ring_bytes(int threads, int c, int r, bool backward) {
 // keys).  kSum: one sum of gain gradients a group (a shared gain) instead of
 // one a head.
 template <typename T, int V, int C, int R, bool kInter, bool kBackward, bool kSum, bool kAxes>
-__global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
+__global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
     qk_kernel(const __grid_constant__ std::conditional_t<kAxes, QkAxesArgs, QkArgs> a) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   constexpr bool kAsync = sizeof(T) * V == 16;
@@ -277,6 +271,29 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
   };
   float cs[C][V], sn[C][V];
   using At = std::conditional_t<kAxes, Positions, Position>;
+  // Positions of the group's token number n, or of the token n slots behind its
+  // first (one position: loaded a token ahead into `next`, which is not looked at
+  // until it is used, so that it is not waited for).
+  unsigned char* const pos = s_raw + (kAsync ? kRing * (R * C * kEach) * step : 0) + group * (kPosSlots * kPosBytes);
+  const auto fetch_positions = [&](int n, int64_t t) {
+    if constexpr (kAxes) {
+      if (t >= a.tokens) return;
+      for (int k = lane; k < a.axes; k += lanes) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(pos + n % kPosSlots * kPosBytes + k * 8);
+        if (a.pos64)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to),
+                       "l"(static_cast<const int64_t*>(a.pos) + k * a.tokens + t) : "memory");
+        else
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to),
+                       "l"(static_cast<const int*>(a.pos) + k * a.tokens + t) : "memory");
+      }
+    }
+  };
+  int64_t next = 0;
+  const auto look = [&](int n) -> At {
+    if constexpr (kAxes) return positions(a, pos + n % kPosSlots * kPosBytes);
+    else return {next};
+  };
   // the axes of a chunk's pairs, two bits each
   uint32_t axis[kAxes ? C : 1];
   if constexpr (kAxes)
@@ -320,16 +337,32 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
   };
 
   if (on && first < a.tokens) {
-    At p = position(a, first), next = p;
-    if (first + slots < a.tokens) next = position(a, first + slots);
+    At p;
+    if constexpr (kAxes) {
+      fetch_positions(0, first);
+      fetch_positions(1, first + slots);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      p.first = position(a, first);
+      next = first + slots < a.tokens ? position(a, first + slots) : 0;
+    }
 #pragma unroll
     for (int k = 0; k < kRing - 1; ++k) fetch(first + k * slots < a.tokens, k);
+    if constexpr (kAxes) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kAsync ? kRing - 1 : 0) : "memory");
+      __syncwarp(mask);
+      p = look(0);
+    }
     angles(p);
     if (R == 1 || !a.gain_per_head) load_gain(0);
+    int n = 0;                 // the token's number among the group's
     int at = 0;
     for (int64_t t = first; t < a.tokens; t += slots) {
+      fetch_positions(n + 2, t + 2 * slots);  // over those of token n - 2, which all lanes have looked at
       fetch(t + (kRing - 1) * slots < a.tokens, at == 0 ? kRing - 1 : at - 1);
-      if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      if constexpr (kAxes && !kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+      if constexpr (kAsync || kAxes) asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+      if constexpr (kAxes) __syncwarp(mask);
       // padding, or no angle for this position: a fill of the rows
       const bool skip = p.first < 0 || (p.first >= a.n_pos && a.rot > 0);
 #pragma unroll
@@ -348,7 +381,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
 #pragma unroll
               for (int i = 0; i < V; ++i) dgain[kSum ? 0 : r][j][i] = both(f);
           }
-          if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(next);
+          if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(n + 1));
           continue;
         }
         if (R > 1 && a.gain_per_head) load_gain(r);
@@ -384,7 +417,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
         }
         // forward the next token's angles come as soon as these are done with; the
         // backward pass has no registers to wait for them in
-        if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(next);
+        if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(n + 1));
         float sum = __fadd_rn(sq.x, sq.y), sum_dot = __fadd_rn(dot.x, dot.y);
         for (int o = lanes >> 1; o > 0; o >>= 1) {
           sum = __fadd_rn(sum, __shfl_xor_sync(mask, sum, o));
@@ -422,9 +455,14 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 3)
         if (kBackward) go += go_t;
       }
       out += out_t;
-      p = next;
+      if constexpr (kAxes) {
+        if (t + slots < a.tokens) p = look(n + 1);
+        ++n;
+      } else {
+        p.first = next;
+      }
       if (kBackward && t + slots < a.tokens) angles(p);
-      if (t + 2 * slots < a.tokens) next = position(a, t + 2 * slots);
+      if (!kAxes && t + 2 * slots < a.tokens) next = position(a, t + 2 * slots);
       at = at == kRing - 1 ? 0 : at + 1;
     }
   }
