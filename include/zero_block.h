@@ -76,7 +76,8 @@ typedef struct zero_rng {
 } zero_rng;
 
 typedef struct zero_block_config {
-  int32_t dim;              /* D: 1..16384                                    */
+  int32_t dim;              /* D: 1..16384; 8192 at most with dtype FP32, 12288 with
+                               a gate and a binary32 stream beside 16-bit blocks */
   int32_t dtype;            /* y, gate, h and their gradients: ZERO_FP16/BF16/FP32 */
   int32_t stream_dtype;     /* x, x' and their gradients: `dtype` or ZERO_FP32 */
   int32_t norm_branch;      /* 1: y is normalised                             */

@@ -47,8 +47,11 @@ def test_create_refuses(z, field, value):
 
 
 def test_the_widest_rows(z):
-    for dim, dtype, ok in [(16384, z.BF16, True), (8192, z.FP32, True), (8193, z.FP32, False)]:
-        cfg, h = z.make_block_config(dim, dtype=dtype), ctypes.c_void_p()
+    for dim, dtype, kw, ok in [(16384, z.BF16, {}, True), (8192, z.FP32, {}, True), (8193, z.FP32, {}, False),
+                               (16384, z.BF16, dict(gate=1), True), (16384, z.BF16, dict(stream_dtype=z.FP32), True),
+                               (12288, z.BF16, dict(stream_dtype=z.FP32, gate=1), True),
+                               (12289, z.FP16, dict(stream_dtype=z.FP32, gate=2), False)]:
+        cfg, h = z.make_block_config(dim, dtype=dtype, **kw), ctypes.c_void_p()
         status = z.lib().zero_block_create(ctypes.byref(cfg), ctypes.byref(h))
         assert status == (z.ZERO_OK if ok else z.ZERO_EINVAL)
         z.lib().zero_block_destroy(h)

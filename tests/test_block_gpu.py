@@ -43,7 +43,13 @@ CASES = [
     (700, 4097, "bf16", "fp32", True, True, "none", 0.0, 0.0, "own", 1.0, 1.0, True),
     (900, 5000, "fp16", "fp16", True, True, "plain", 0.1, 0.1, "padded", 1.0, 1.0, True),
     (400, 8192, "fp32", "fp32", True, True, "sigmoid", 0.1, 0.0, "own", 1.0, 1.0, True),
-    (333, 16384, "bf16", "fp32", True, True, "plain", 0.1, 0.0, "own", 1.0, 1.0, True),
+    (333, 12288, "bf16", "fp32", True, True, "plain", 0.1, 0.0, "own", 1.0, 1.0, True),
+    (310, 12287, "bf16", "fp32", True, True, "sigmoid", 0.1, 0.1, "own", 1.0, 1.0, True),
+    (320, 16384, "bf16", "fp32", True, True, "none", 0.1, 0.0, "own", 1.0, 1.0, True),
+    (315, 8191, "fp32", "fp32", True, True, "plain", 0.1, 0.0, "odd", 1.0, 1.0, True),
+    (700, 2050, "fp32", "fp32", False, True, "sigmoid", 0.0, 0.1, "odd", 1.0, 1.0, True),
+    (2500, 100, "bf16", "fp32", True, True, "none", 0.1, 0.1, "own", 1.0, 1.0, True),
+    (3000, 12, "fp16", "fp16", True, True, "plain", 0.1, 0.1, "odd", 1.0, 1.0, True),
     (320, 16383, "fp16", "fp16", True, True, "plain", 0.1, 0.0, "odd", 1.0, 1.0, True),
     (3, 12345, "bf16", "bf16", False, True, "none", 0.1, 0.0, "own", 1.0, 1.0, True),
     (300, 1024, "bf16", "bf16", False, True, "none", 0.0, 0.2, "own", 1.0, 1.0, False),

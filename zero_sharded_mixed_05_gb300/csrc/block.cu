@@ -22,7 +22,9 @@ using zo::JoinRow;
 using zo::Num;
 
 constexpr int kMaxDim = 16384;
-constexpr int kMaxDim32 = 8192;          // of binary32 blocks: a row of each tensor fits shared memory
+// so that a row of each tensor fits shared memory:
+constexpr int kMaxDim32 = 8192;          // of binary32 blocks
+constexpr int kMaxDimGated = 12288;      // of gated 16-bit blocks on a binary32 stream
 constexpr int kMaxSmem = 227 * 1024 - 1024;
 constexpr int kMaxPerSm = 4;             // CTAs an SM
 
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(256) drop_kernel(const __grid_constant__ DropA
 }
 
 zero_status cuda_fail(cudaError_t e, const char* what) {
+  cudaGetLastError();
   return fail(ZERO_ECUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -177,7 +180,7 @@ struct zero_block_handle {
       if (o.fn == fn && o.threads == threads && o.smem == smem) return o.ctas;
     int n = 0;
     cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) n = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, threads, smem) != cudaSuccess) cudaGetLastError();
     n = std::max(1, std::min(n, kMaxPerSm));
     occ[seen++ % 32] = {fn, threads, smem, n};
     return n;
@@ -287,20 +290,20 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   // backward unless the gate's registers or a binary32 stream's ring are too many for
   // it; four of long rows.
   const bool one = a.chunks <= 32 || (a.chunks <= 512 && (b->tokens <= 2 * h->sms || !wide));
-  int cs = one ? 1 : wide && a.chunks <= 1024 ? 2 : 4;
+  int cs = one ? 1 : a.chunks <= 1024 ? 2 : 4;
   if (cs == 2 && backward && a.chunks <= 512 && (with_gate || mixed)) cs = 1;
   a.warps = (a.chunks + 32 * cs - 1) / (32 * cs);
   a.teams = std::max(1, 8 / a.warps);
   a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
   const int threads = a.teams * a.warps * 32;
   const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate ? 2 : a.drop.cut > 0 ? 1 : 0, cs,
-                             threads > 256};
+                             threads > (wide ? 256 : 320)};
   const void* fn = c.dtype == ZERO_FP32   ? zo::join_float(pick)
                    : c.dtype == ZERO_FP16 ? (mixed ? zo::join_half_float(pick) : zo::join_half(pick))
                                           : (mixed ? zo::join_bf16_float(pick) : zo::join_bf16(pick));
   const int vt = es / 2, vs = ss / 2;
   a.vecs = cs * (backward ? 2 * vs + 2 * vt : vs + vt) + (with_gate ? cs * vt : 0);
-  const int row = a.vecs * threads * 16;
+  const int row = a.vecs * threads / 32 * (wide ? zo::kVecBytesOf<true> : zo::kVecBytesOf<false>);
   // CTAs an SM and rows of their rings.  Memory is quickest with some 16,384 numbers
   // of each tensor on their way to an SM: with fewer it is waited for, with more reads
   // and writes get into one another's way (16,384 rows of 4096 in bf16, two CTAs: two
@@ -310,9 +313,8 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   // CTAs (95 us with three, 104 with two).
   const int numbers = backward ? (pick.post || pick.has ? 16384 : 12288) : pick.has ? 24576 : 18432;
   int slots = std::max(1, numbers / (a.teams * c.dim));
-  int ctas = std::max(1, std::min(h->resident(fn, threads, wide ? 2 * row : row), slots / 2));
-  a.ring = !wide ? 1 : ctas == 1 ? 3 : std::max(2, std::min(3, slots / ctas));
-  if (!wide) ctas = kMaxPerSm;
+  int ctas = std::max(1, std::min(h->resident(fn, threads, 2 * row), slots / 2));
+  a.ring = ctas == 1 ? 3 : std::max(2, std::min(3, slots / ctas));
   a.ring = std::max(1, std::min(a.ring, kMaxSmem / row));
   size_t smem = (size_t)a.ring * row;
   if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
@@ -355,7 +357,9 @@ zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
   if (!known(cfg->dtype)) return fail(ZERO_EINVAL, "dtype must be ZERO_FP16, ZERO_BF16 or ZERO_FP32");
   if (cfg->stream_dtype != cfg->dtype && cfg->stream_dtype != ZERO_FP32)
     return fail(ZERO_EINVAL, "stream_dtype must be dtype or ZERO_FP32");
-  const int most = cfg->dtype == ZERO_FP32 ? kMaxDim32 : kMaxDim;
+  const int most = cfg->dtype == ZERO_FP32                                                    ? kMaxDim32
+                   : cfg->gate != ZERO_GATE_NONE && cfg->stream_dtype != cfg->dtype ? kMaxDimGated
+                                                                                    : kMaxDim;
   if (cfg->dim < 1 || cfg->dim > most) return fail(ZERO_EINVAL, "dim must be in 1..%d", most);
   if ((cfg->norm_branch | 1) != 1 || (cfg->norm_out | 1) != 1)
     return fail(ZERO_EINVAL, "norm_branch and norm_out must be 0 or 1");
@@ -443,7 +447,6 @@ zero_status zero_dropout(const zero_drop_buffers* b, void* stream) {
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) {
-    cudaGetLastError();
     return cuda_fail(e, "no CUDA device");
   }
   if (!any) return ZERO_OK;

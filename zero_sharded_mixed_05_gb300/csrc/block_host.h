@@ -9,8 +9,8 @@ struct JoinPick {
   bool backward, wide;
   bool post;       // the branch is normalised
   int has;         // 0; 1: a dropout; 2: a gate and maybe a dropout
-  int chunks;      // a thread: 1, 2 (wide only) or 4
-  bool large;      // more than 256 threads a CTA
+  int chunks;      // a thread: 1, 2 or 4
+  bool large;      // more than 256 threads a CTA, or 320 where not wide
 };
 
 // Kernels that take a JoinArgs, by the types of the block and of the stream.

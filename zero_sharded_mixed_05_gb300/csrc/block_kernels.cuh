@@ -11,10 +11,12 @@
 // chunk is one block of the dropout's generator.  The teams walk the tokens.
 //
 // Rows come by cp.async into a ring in shared memory in which every thread reads
-// only what it copied itself (kWide: all rows on 16-byte boundaries), so bytes
-// in flight cost no registers and no barrier.  Other rows are read number by
-// number, a warp's 32 next to one another, through the same shared memory, which
-// brings each thread its eight, and written the same way.
+// only what it copied itself, so that bytes in flight cost no registers and no
+// barrier (kWide: rows of whole chunks on 16-byte boundaries; those of binary32
+// are copied in the warp's order).  Of other rows the 16-byte granules that they
+// lie in are copied, and a warp's lanes shift what they hold to where it belongs
+// once it is there; results are shifted the other way, so that all but the ends of
+// a warp's 256 numbers are written 16 bytes at a time.
 #pragma once
 
 #include "numbers.cuh"
@@ -48,6 +50,10 @@ struct JoinArgs {
   float eps, eps_y, inv_dim, alpha, beta;
 };
 
+// A warp's bytes of a vector: 32 lanes' and, of rows that are shifted, one granule
+// more (of two vectors' worth for the pair).
+template <bool kWide> constexpr int kVecBytesOf = kWide ? 512 : 528;
+
 template <typename E> constexpr int kVecs = (int)sizeof(E) / 2;   // 16-byte vectors of a chunk
 
 // Waits until at most n of the thread's groups of copies are on their way.
@@ -58,81 +64,114 @@ __device__ __forceinline__ void copies_left(int n) {
 }
 
 // The place of a thread in its team and in shared memory, and the moves between
-// there and the rows.  A warp's vectors of a row lie one after another, 512
-// bytes each, so that a vector is a fixed distance from the row's first.
+// there and the rows.  A warp's vectors of a row lie one after another, so that
+// each is a fixed distance from the row's first.
 template <int kC, bool kWide>
 struct Lane {
   int dim, chunks, warps;           // as in JoinArgs
   unsigned char* smem;    // the warp's ring
   int team, warp;         // this thread's team, and its warp's place in it
+  static constexpr int kVecBytes = kVecBytesOf<kWide>;
 
   __device__ __forceinline__ int lanes() const { return warps * 32; }
   __device__ __forceinline__ int chunk(int j) const { return (j * warps + warp) * 32 + threadIdx.x % 32; }
   __device__ __forceinline__ bool live(int j) const { return chunk(j) < chunks; }
   // vector n of the thread in the row of the ring that begins at `at`
   __device__ __forceinline__ unsigned char* vec(int at, int n) const {
-    return smem + at + n * 512 + threadIdx.x % 32 * 16;
+    return smem + at + n * kVecBytes + threadIdx.x % 32 * 16;
+  }
+  // Vector u of a warp's chunks of E whose vectors start at n.  Of binary32 a lane's
+  // are 2 l and 2 l + 1: every other group of eight swaps neighbours, so that eight
+  // lanes that read (or write) their first vectors, or their second, meet in no bank.
+  template <typename E>
+  __device__ __forceinline__ unsigned char* slot(int at, int n, uint32_t u) const {
+    return smem + at + n * kVecBytes + (sizeof(E) == 2 ? u : u ^ (u >> 3 & 1)) * 16;
   }
 
   // Zeros in the warp's `bytes` of the ring, if some of its lanes have no chunk: what
   // is never copied to counts for nothing, and needs no check where it is read.
   __device__ __forceinline__ void clear(int bytes) const {
     if (((kC - 1) * warps + warp + 1) * 32 <= chunks) return;
-    for (int at = 0; at < bytes; at += 512) *reinterpret_cast<uint4*>(vec(at, 0)) = make_uint4(0, 0, 0, 0);
+    for (int at = threadIdx.x % 32 * 16; at < bytes; at += 512)
+      *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
     __syncwarp();
   }
 
   // A row's chunks into vectors from `first` on.
   template <typename E>
   __device__ __forceinline__ void fetch(const char* row, int at, int first) const {
+    constexpr uint32_t kV = kVecs<E>;
+    const uint32_t l = threadIdx.x % 32;
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
-      if constexpr (kWide && sizeof(E) == 2) {
+      if constexpr (kWide && kV == 1) {
         if (live(j)) copy16(vec(at, first + j), row + (uint32_t)chunk(j) * 16);
       } else if constexpr (kWide) {
-        // a lane's 32 bytes are two vectors; the warp's 64 are copied in their order,
-        // 32 next to one another at a time
-        const uint32_t begin = (j * warps + warp) * 64, l = threadIdx.x % 32;
+        const uint32_t begin = (j * warps + warp) * 64;
 #pragma unroll
         for (uint32_t u = l; u < 64; u += 32)
-          if ((begin + u) * 4 < (uint32_t)dim) copy16(pair(at, first + 2 * j, u), row + (begin + u) * 16);
+          if ((begin + u) * 4 < (uint32_t)dim) copy16(slot<E>(at, first + 2 * j, u), row + (begin + u) * 16);
       } else {
-        const int l = threadIdx.x % 32, begin = (j * warps + warp) * 256;
-        if (begin >= dim) continue;
-        E x[8];
+        // the granules that the warp's numbers lie in, as far as the row goes
+        const uint32_t shift = reinterpret_cast<uintptr_t>(row) % 16, begin = (j * warps + warp) * (512 * kV);
+        const int left = (int)(shift + dim * (uint32_t)sizeof(E) - begin);
+        if (left <= (int)shift) continue;
+        const char* from = row - shift + begin;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int e = begin + k * 32 + l;
-          x[k] = e < dim ? reinterpret_cast<const E*>(row)[e] : Num<E>::put(0.0f);
+        for (uint32_t u = l; u <= 32 * kV; u += 32) {
+          const int bytes = left - 16 * (int)u;
+          copy16(slot<E>(at, first + j * kV, u), bytes > 0 ? from + 16 * u : from, max(0, min(16, bytes)));
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) *place<E>(at, first + j * kVecs<E>, k * 32 + l) = x[k];
       }
     }
   }
-  // Vector u of the 64 of a warp's chunks of binary32, the lane's at 2 l and 2 l + 1:
-  // every other group of eight swaps neighbours, so that eight lanes that read (or
-  // write) their first vectors, or their second, meet in no bank.
-  __device__ __forceinline__ unsigned char* pair(int at, int n, uint32_t u) const {
-    return smem + at + n * 512 + (u ^ (u >> 3 & 1)) * 16;
+
+  // Words a, of which the first is `shift` bytes (a multiple of E's size, below 16)
+  // before what is wanted, moved down by that.
+  template <typename E, int kN>
+  static __device__ __forceinline__ void move_down(uint32_t (&a)[kN], uint32_t shift) {
+#pragma unroll
+    for (int k = 0; k < kN - 2; ++k) a[k] = shift & 8 ? a[k + 2] : a[k];
+#pragma unroll
+    for (int k = 0; k < kN - 3; ++k) a[k] = shift & 4 ? a[k + 1] : a[k];
+    if constexpr (sizeof(E) == 2)
+#pragma unroll
+      for (int k = 0; k < kN - 4; ++k) a[k] = __funnelshift_r(a[k], a[k + 1], shift % 4 * 8);
   }
-  // Number e of the 256 that the warp holds in a chunk whose vectors start at n.
+
+  // Brings what was fetched from an address `shift` above a granule's to its lanes.
   template <typename E>
-  __device__ __forceinline__ E* place(int at, int n, int e) const {
-    unsigned char* v = smem + at + n * 512;
-    if constexpr (sizeof(E) == 2) return reinterpret_cast<E*>(v) + e;
-    else return reinterpret_cast<E*>(pair(at, n, e / 4)) + e % 4;
+  __device__ __forceinline__ void settle(int at, int first, uint32_t shift) const {
+    constexpr int kV = kVecs<E>;
+    if (kWide || shift == 0) return;
+    const uint32_t l = threadIdx.x % 32;
+#pragma unroll
+    for (int j = 0; j < kC; ++j) {
+      if ((j * warps + warp) * 256 >= dim) continue;
+      uint32_t a[4 * kV + 4];
+#pragma unroll
+      for (int v = 0; v <= kV; ++v) {
+        const uint4 w = *reinterpret_cast<const uint4*>(slot<E>(at, first + j * kV, l * kV + v));
+        a[4 * v] = w.x;
+        a[4 * v + 1] = w.y;
+        a[4 * v + 2] = w.z;
+        a[4 * v + 3] = w.w;
+      }
+      move_down<E>(a, shift);
+      __syncwarp();
+#pragma unroll
+      for (int v = 0; v < kV; ++v)
+        *reinterpret_cast<uint4*>(slot<E>(at, first + j * kV, l * kV + v)) =
+            make_uint4(a[4 * v], a[4 * v + 1], a[4 * v + 2], a[4 * v + 3]);
+    }
   }
 
   template <typename E>
   __device__ __forceinline__ void get(int at, int n, float2* x) const {
-    if constexpr (sizeof(E) == 2) {
-      unpack<E>(*reinterpret_cast<const uint4*>(vec(at, n)), x);
-    } else {
-      const uint32_t u = threadIdx.x % 32 * 2;
-      unpack<E>(*reinterpret_cast<const uint4*>(pair(at, n, u)), x);
-      unpack<E>(*reinterpret_cast<const uint4*>(pair(at, n, u + 1)), x + 2);
-    }
+#pragma unroll
+    for (int v = 0; v < kVecs<E>; ++v)
+      unpack<E>(*reinterpret_cast<const uint4*>(slot<E>(at, n, threadIdx.x % 32 * kVecs<E> + v)),
+                x + v * (8 / (int)sizeof(E)));
   }
 
   // The same with the dropped numbers zero.
@@ -149,37 +188,45 @@ struct Lane {
   }
 
   // A chunk of a result.  What a lane does not write as it holds it passes through
-  // the vectors from n on, which are done with, to be written in its order.
+  // the vectors from n on, which are done with, to be written in the warp's order.
   template <typename E>
-  __device__ __forceinline__ void put(char* data, int j, const float2* x, int at, int n) const {
+  __device__ __forceinline__ void put(char* row, int j, const float2* x, int at, int n) const {
+    constexpr uint32_t kV = kVecs<E>, kS = sizeof(E);
     const uint32_t l = threadIdx.x % 32;
-    if constexpr (kWide && sizeof(E) == 2) {
-      if (live(j)) *reinterpret_cast<uint4*>(data + (uint32_t)chunk(j) * 16) = pack<E>(x);
+    if constexpr (kWide && kV == 1) {
+      if (live(j)) *reinterpret_cast<uint4*>(row + (uint32_t)chunk(j) * 16) = pack<E>(x);
       return;
     }
     const int begin = (j * warps + warp) * 256;
     if (begin >= dim) return;
-    if (live(j)) {                 // what no number comes to stays zero
-      if constexpr (sizeof(E) == 2) {
-        *reinterpret_cast<uint4*>(vec(at, n)) = pack<E>(x);
-      } else {
-        *reinterpret_cast<uint4*>(pair(at, n, 2 * l)) = pack<E>(x);
-        *reinterpret_cast<uint4*>(pair(at, n, 2 * l + 1)) = pack<E>(x + 2);
-      }
-    }
+    if (live(j))                   // what no number comes to stays zero
+#pragma unroll
+      for (uint32_t v = 0; v < kV; ++v)
+        *reinterpret_cast<uint4*>(slot<E>(at, n, l * kV + v)) = pack<E>(x + v * (8 / kS));
     __syncwarp();
-    if constexpr (kWide) {
+    char* to = row + (uint32_t)begin * kS;
+    const uint32_t bytes = min(256, dim - begin) * kS;
+    const uint32_t shift = kWide ? 0 : reinterpret_cast<uintptr_t>(to) % 16;
+    // whole granules [16 u - shift, 16 u - shift + 16) of these bytes
+    const uint32_t lo = shift ? 1 : 0, hi = (bytes + shift) / 16;
 #pragma unroll
-      for (uint32_t u = l; u < 64; u += 32)
-        if (begin + u * 4 < (uint32_t)dim)
-          *reinterpret_cast<uint4*>(data + (begin / 4 + u) * 16) = *reinterpret_cast<const uint4*>(pair(at, n, u));
-    } else {
-      E* row = reinterpret_cast<E*>(data);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int e = begin + k * 32 + l;
-        if (e < dim) row[e] = *place<E>(at, n, k * 32 + l);
+    for (uint32_t u = l; u < 32 * kV; u += 32) {
+      if (u < lo || u >= hi) continue;
+      uint4 w = *reinterpret_cast<const uint4*>(slot<E>(at, n, u));
+      if (!kWide && shift) {
+        const uint4 p = *reinterpret_cast<const uint4*>(slot<E>(at, n, u - 1));
+        uint32_t a[8] = {p.x, p.y, p.z, p.w, w.x, w.y, w.z, w.w};
+        move_down<E>(a, 16 - shift);
+        w = make_uint4(a[0], a[1], a[2], a[3]);
       }
+      *reinterpret_cast<uint4*>(to + 16 * u - shift) = w;
+    }
+    if constexpr (!kWide) {
+      // the ends, number by number: those before the first whole granule, and behind the last
+      const uint32_t number = l % 8 * kS, head = min(bytes, (16 - shift) % 16), rest = max(head, 16 * hi - min(16 * hi, shift));
+      const uint32_t e = l < 8 ? number : rest + number;
+      if (l < 16 && number < 16 && e < (l < 8 ? head : bytes))
+        *reinterpret_cast<E*>(to + e) = *reinterpret_cast<const E*>(slot<E>(at, n, e / 16) + e % 16);
     }
     __syncwarp();
   }
@@ -283,13 +330,15 @@ __device__ __forceinline__ float add2(float2 x) { return __fadd_rn(x.x, x.y); }
 // What the branch has, besides a norm (kPost).
 enum { kBare = 0, kDrop = 1, kGated = 2 };   // nothing; a dropout; either or both
 
-// kMost: threads of a CTA at most; of 256 there are three an SM.
+// kMost: threads of a CTA at most.  Forward three CTAs of 256 threads are to fit an
+// SM, or two of more where the rows are shifted.
 template <typename T, typename S, int kC, bool kWide, bool kPost, int kHas, int kMost>
-__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) join_kernel(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : kWide || (kC > 1 && kMost == 512) ? 1 : 2)
+    join_kernel(const __grid_constant__ JoinArgs a) {
   extern __shared__ __align__(16) unsigned char s_ring[];
   __shared__ float s_red[2][kJoinThreads / 32 * 8];
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
-  const int row = a.vecs * 512;                                            // of the ring, a warp's
+  const int row = a.vecs * kVecBytesOf<kWide>;                             // of the ring, a warp's
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   constexpr int kY = kC * kVecs<S>, kGate = kY + kC * kVecs<T>;   // vectors: x, y, gate
   constexpr bool kShared = !kWide || sizeof(S) == 4;   // lanes read what others of their warp copied
@@ -319,7 +368,19 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) join_kernel(const
         gate += a.gate.step;
       }
     }
-    if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // how far the present rows begin above a granule
+  uint32_t ux = (uintptr_t)x % 16, uy = (uintptr_t)y % 16, ug = (uintptr_t)gate % 16;
+  const auto settle = [&](int at) {
+    if constexpr (!kWide) {
+      me.template settle<S>(at, 0, ux);
+      me.template settle<T>(at, kY, uy);
+      if (gated) me.template settle<T>(at, kGate, ug);
+      ux = (ux + (uint32_t)a.x.step) % 16;
+      uy = (uy + (uint32_t)a.y.step) % 16;
+      ug = (ug + (uint32_t)a.gate.step) % 16;
+    }
   };
   // the gains stay in registers where there is room for them; columns that no lane
   // has are zeros from here on, which change no sum
@@ -346,8 +407,9 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : 1) join_kernel(const
     if (drops && there)
 #pragma unroll
       for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
-    if constexpr (kWide) copies_left(ahead);
+    copies_left(ahead);
     if (kShared) __syncwarp();
+    settle(at);
     float2 v[kC][4];
     if (there) {
       float ry = scale;
@@ -433,7 +495,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
   // the kernel that sums the partial gradients may be set up now; it waits for the end
   if (a.part) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0);     // known to be the warp's
-  const int row = a.vecs * 512;                                            // of the ring, a warp's
+  const int row = a.vecs * kVecBytesOf<kWide>;                             // of the ring, a warp's
   const Lane<kC, kWide> me{a.dim, a.chunks, a.warps, s_ring + warp * a.ring * row, warp / a.warps, warp % a.warps};
   // vectors: x', dx', dh, y, gate
   constexpr int kDxo = kC * kVecs<S>, kDh = 2 * kDxo, kY = kDh + kC * kVecs<T>, kGate = kY + kC * kVecs<T>;
@@ -470,7 +532,23 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
         gate += a.gate.step;
       }
     }
-    if constexpr (kWide) asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  uint32_t ux = (uintptr_t)x % 16, uo = (uintptr_t)dxo % 16, uh = (uintptr_t)dh % 16, uy = (uintptr_t)y % 16,
+           ug = (uintptr_t)gate % 16;
+  const auto settle = [&](int at) {
+    if constexpr (!kWide) {
+      me.template settle<S>(at, 0, ux);
+      me.template settle<S>(at, kDxo, uo);
+      me.template settle<T>(at, kDh, uh);
+      me.template settle<T>(at, kY, uy);
+      if (gated) me.template settle<T>(at, kGate, ug);
+      ux = (ux + (uint32_t)a.x.step) % 16;
+      uo = (uo + (uint32_t)a.dxo.step) % 16;
+      uh = (uh + (uint32_t)a.dh.step) % 16;
+      uy = (uy + (uint32_t)a.y.step) % 16;
+      ug = (ug + (uint32_t)a.gate.step) % 16;
+    }
   };
   constexpr bool kKeep = kC <= 2;
   float2 yg_[kKeep ? kC : 1][4], g_[kKeep ? kC : 1][4];
@@ -500,8 +578,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
     if (drops && there)
 #pragma unroll
       for (int j = 0; j < kC; ++j) keep[j] = kept(a.drop, rng_step, block + me.chunk(j));
-    if constexpr (kWide) copies_left(ahead);
+    copies_left(ahead);
     if (kShared) __syncwarp();
+    settle(at);
     if (there) {
       // With q = act y_gain y where the branch is kept, the branch's own dot product
       // sum G q is linear in G, so that its parts are summed before r is known: one
@@ -649,7 +728,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
   if (!a.part) return;
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.dim;
   float* s_sum = reinterpret_cast<float*>(s_ring);
-  if constexpr (kWide) asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
   for (int team = 0; team < a.teams; ++team) {
     __syncthreads();
     if (me.team != team) continue;

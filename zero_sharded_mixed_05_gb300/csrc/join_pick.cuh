@@ -26,13 +26,21 @@ const void* join_of(const JoinPick& p) {
                           : join_of<T, S, kC, true, kGated>(p.backward, p.post);
 }
 
-// Long rows and narrow ones have one kernel for all that a branch may have.
+template <typename T, typename S, int kC, int kMost>
+const void* shifted_join_of(const JoinPick& p) {
+  return p.has == kBare ? join_of<T, S, kC, false, kBare, kMost>(p.backward, p.post)
+                        : join_of<T, S, kC, false, kGated, kMost>(p.backward, p.post);
+}
+
+// Long rows have one kernel for all that a branch may have.
 template <typename T, typename S>
 const void* join_of(const JoinPick& p) {
+  if (p.chunks == 4)
+    return p.wide ? join_of<T, S, 4, true, kGated>(p.backward, p.post) : join_of<T, S, 4, false, kGated>(p.backward, p.post);
   if (!p.wide)
-    return p.chunks == 1 ? join_of<T, S, 1, false, kGated>(p.backward, p.post)
-                         : join_of<T, S, 4, false, kGated>(p.backward, p.post);
-  if (p.chunks == 4) return join_of<T, S, 4, true, kGated>(p.backward, p.post);
+    return p.chunks == 1           ? shifted_join_of<T, S, 1, kJoinThreads>(p)
+           : p.large || p.backward ? shifted_join_of<T, S, 2, kJoinThreads>(p)
+                                   : shifted_join_of<T, S, 2, 320>(p);
   return p.chunks == 2 ? join_of<T, S, 2>(p) : join_of<T, S, 1>(p);
 }
 
