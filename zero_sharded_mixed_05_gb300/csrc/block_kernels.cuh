@@ -63,6 +63,19 @@ __device__ __forceinline__ void copies_left(int n) {
   else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// Words a, of which the first is `shift` bytes (a multiple of E's size, below 16)
+// before what is wanted, moved down by that.
+template <typename E, int kN>
+__device__ __forceinline__ void move_down(uint32_t (&a)[kN], uint32_t shift) {
+#pragma unroll
+  for (int k = 0; k < kN - 2; ++k) a[k] = shift & 8 ? a[k + 2] : a[k];
+#pragma unroll
+  for (int k = 0; k < kN - 3; ++k) a[k] = shift & 4 ? a[k + 1] : a[k];
+  if constexpr (sizeof(E) == 2)
+#pragma unroll
+    for (int k = 0; k < kN - 4; ++k) a[k] = __funnelshift_r(a[k], a[k + 1], shift % 4 * 8);
+}
+
 // The place of a thread in its team and in shared memory, and the moves between
 // there and the rows.  A warp's vectors of a row lie one after another, so that
 // each is a fixed distance from the row's first.
@@ -124,19 +137,6 @@ struct Lane {
         }
       }
     }
-  }
-
-  // Words a, of which the first is `shift` bytes (a multiple of E's size, below 16)
-  // before what is wanted, moved down by that.
-  template <typename E, int kN>
-  static __device__ __forceinline__ void move_down(uint32_t (&a)[kN], uint32_t shift) {
-#pragma unroll
-    for (int k = 0; k < kN - 2; ++k) a[k] = shift & 8 ? a[k + 2] : a[k];
-#pragma unroll
-    for (int k = 0; k < kN - 3; ++k) a[k] = shift & 4 ? a[k + 1] : a[k];
-    if constexpr (sizeof(E) == 2)
-#pragma unroll
-      for (int k = 0; k < kN - 4; ++k) a[k] = __funnelshift_r(a[k], a[k + 1], shift % 4 * 8);
   }
 
   // Brings what was fetched from an address `shift` above a granule's to its lanes.
