@@ -2,7 +2,7 @@
 orthogonalised updates, everything else by AdamW, its queries and keys
 normalised and rotated in one pass.
 
-    python examples/train_muon.py [--steps 60] [--width 256] [--layers 2]
+    python examples/train_muon.py [--steps 60] [--width 256] [--layers 2] [--dropout 0.1]
 
 The optimizer's state is as the library's: flat 16-bit parameters and
 gradients (the module's tensors are views of them), fp32 masters.  One step:
@@ -12,6 +12,9 @@ gradients (the module's tensors are views of them), fp32 masters.  One step:
     zero_opt_step_folded   folds both, decides (skip, clip, loss scale) on the
                            device and updates the others
     zero_muon_step         updates the matrices by that decision
+
+With --dropout the blocks' outputs are dropped out, added to the stream and
+normalised for the next block in one pass (BlockJoin).
 
 Only the loss scale and the printed loss are read back.  The data are sequences whose next token is
 a fixed function of the two before, so the loss falls from log(vocabulary).
@@ -27,9 +30,10 @@ import torch.nn.functional as F
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import zero_sharded_mixed_05_gb300 as z  # noqa: E402
+from zero_sharded_mixed_05_gb300.block import BlockJoin  # noqa: E402
 from zero_sharded_mixed_05_gb300.qk import QkNormRope, rotation_tables  # noqa: E402
 
-VOCAB, HEAD = 64, 64
+VOCAB, HEAD, SEED = 64, 64, 3
 
 
 class Flat:
@@ -56,9 +60,10 @@ class Flat:
 
 
 class Decoder:
-    """Pre-norm decoder blocks; matrices [outputs, inputs]."""
+    """Pre-norm decoder blocks; matrices [outputs, inputs].  `dropout` None: norms
+    and additions are torch's."""
 
-    def __init__(self, width, layers, dev):
+    def __init__(self, width, layers, dev, dropout=None):
         g = torch.Generator(device=dev).manual_seed(1)
         self.q_heads, self.k_heads = width // HEAD, max(1, width // HEAD // 2)
         kv = self.k_heads * HEAD
@@ -77,6 +82,13 @@ class Decoder:
         self.head = (torch.randn(VOCAB, width, generator=g, device=dev) * width ** -0.5).requires_grad_()
         self.final = vec(width)
         self.norm = QkNormRope(z.make_qk_config(self.q_heads, self.k_heads, HEAD, dtype=z.FP16))
+        self.join = None if dropout is None else BlockJoin(
+            z.make_block_config(width, dtype=z.FP16, eps=torch.finfo(torch.float16).eps, dropout=dropout))
+
+    def close(self):
+        self.norm.close()
+        if self.join is not None:
+            self.join.close()
 
     def matrices(self):
         return [b[n] for b in self.blocks for n in ("qkv", "out", "up", "down")]
@@ -85,12 +97,26 @@ class Decoder:
         return [self.embed, self.head, self.final] + \
             [b[n] for b in self.blocks for n in ("norm1", "norm2", "q_gain", "k_gain")]
 
-    def loss(self, tokens, cos, sin):
+    def loss(self, tokens, cos, sin, step=0):
         batch, length = tokens.shape[0], tokens.shape[1] - 1
         pos = torch.arange(length, device=tokens.device).repeat(batch)
         x = F.embedding(tokens[:, :-1].reshape(-1), self.embed)
-        for b in self.blocks:
-            h = F.rms_norm(x, (x.shape[-1],), b["norm1"])
+        gains = [b[n] for b in self.blocks for n in ("norm1", "norm2")] + [self.final]
+
+        def normed(x, i):
+            """The stream's i-th norm."""
+            if self.join is None:
+                return F.rms_norm(x, (x.shape[-1],), gains[i])
+            return self.join.norm(x, gains[i].float())
+
+        def joined(x, y, i):
+            """The stream with the i-th output, and the norm behind it."""
+            if self.join is None:
+                x = x + y
+                return x, normed(x, i + 1)
+            return self.join(x, y, gain=gains[i + 1].float(), seed=SEED, call=i, step=step)
+        h = normed(x, 0)
+        for i, b in enumerate(self.blocks):
             qkv = (h @ b["qkv"].T).view(batch * length, -1, HEAD)
             q, k, v = qkv.split([self.q_heads, self.k_heads, self.k_heads], 1)
             q, k = self.norm(q, k, b["q_gain"].float(), b["k_gain"].float(), cos, sin, pos)
@@ -99,10 +125,9 @@ class Decoder:
                 t = t.view(batch, length, -1, HEAD).transpose(1, 2)
                 return t.repeat_interleave(self.q_heads // t.shape[1], 1)
             a = F.scaled_dot_product_attention(heads(q), heads(k), heads(v), is_causal=True)
-            x = x + a.transpose(1, 2).reshape(batch * length, -1) @ b["out"].T
-            h = F.rms_norm(x, (x.shape[-1],), b["norm2"])
-            x = x + F.gelu(h @ b["up"].T) @ b["down"].T
-        logits = F.rms_norm(x, (x.shape[-1],), self.final) @ self.head.T
+            x, h = joined(x, a.transpose(1, 2).reshape(batch * length, -1) @ b["out"].T, 2 * i)
+            x, h = joined(x, F.gelu(h @ b["up"].T) @ b["down"].T, 2 * i + 1)
+        logits = h @ self.head.T
         return F.cross_entropy(logits.float(), tokens[:, 1:].reshape(-1))
 
 
@@ -113,10 +138,10 @@ def batch_of(gen, batch, length, dev):
     return t
 
 
-def train(steps=60, width=256, layers=2, lr=4e-3, quiet=False):
+def train(steps=60, width=256, layers=2, lr=4e-3, quiet=False, dropout=None):
     """Losses of every step."""
     dev = torch.device("cuda", torch.cuda.current_device())
-    model = Decoder(width, layers, dev)
+    model = Decoder(width, layers, dev, dropout)
     mats, rest = Flat(model.matrices()), Flat(model.others())
     n = rest.master.numel()
     opt = z.zero_opt_create(z.make_config(numel=n, grad_dtype=z.FP16, lr=lr, weight_decay=0.0,
@@ -140,7 +165,7 @@ def train(steps=60, width=256, layers=2, lr=4e-3, quiet=False):
             scale = z.zero_opt_loss_scale(opt, 0).scale
             mats.grad.zero_()
             rest.grad.zero_()
-            loss = model.loss(batch_of(gen, 16, 96, dev), cos, sin)
+            loss = model.loss(batch_of(gen, 16, 96, dev), cos, sin, step)
             (loss * scale).backward()
             z.zero_opt_grad_stats_noalloc([mats.grad], z.FP16, mats.grad.numel(), records[:2])
             z.zero_opt_grad_stats_async(opt, 0, bufs, records[2:])
@@ -158,7 +183,7 @@ def train(steps=60, width=256, layers=2, lr=4e-3, quiet=False):
     finally:
         z.zero_muon_destroy(muon)
         z.zero_opt_destroy(opt)
-        model.norm.close()
+        model.close()
     return losses
 
 
@@ -168,5 +193,6 @@ if __name__ == "__main__":
     ap.add_argument("--width", type=int, default=256)
     ap.add_argument("--layers", type=int, default=2)
     ap.add_argument("--lr", type=float, default=4e-3)
+    ap.add_argument("--dropout", type=float, help="join blocks to the stream in one pass, with this dropout")
     a = ap.parse_args()
-    train(a.steps, a.width, a.layers, a.lr)
+    train(a.steps, a.width, a.layers, a.lr, dropout=a.dropout)

@@ -107,7 +107,8 @@ zero_status zero_qk_destroy(zero_qk_t h);
 /* Errors of both: EINVAL (NULL handle or buffers; a NULL tensor with
  * T > 0; tokens or n_pos < 0; NULL tables with rotary_dim and n_pos > 0 or
  * NULL positions, T > 0; a result's token or head stride that lays rows on one
- * another; gains without the norm, n_pos of 2^31 or more with axes), ECUDA (no device, another device current, a launch
+ * another; with axes n_pos of 2^31 or more, gains without the norm, positions off
+ * their size's boundary), ECUDA (no device, another device current, a launch
  * failure).  T = 0 launches nothing, except that the backward call sets the
  * gains' gradients to zero. */
 zero_status zero_qk_norm_rope(zero_qk_t h, const zero_qk_buffers* b, void* stream);

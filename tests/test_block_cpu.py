@@ -179,7 +179,7 @@ def test_the_binding_refuses(z):
     import torch
     if torch.cuda.is_available():
         pytest.skip("a CUDA device is present")
-    h = z.zero_block_create(z.make_block_config(64, dtype=z.FP32))
+    h = z.zero_block_create(z.make_block_config(64, dtype=z.FP32, dropout=0.1))
     try:
         good = torch.zeros(3, 64)
         for bad in (torch.zeros(3, 65), torch.zeros(3, 64).half(), torch.zeros(3, 64, 1),

@@ -41,7 +41,7 @@ def test_create_checks_the_rest_as_ever(z):  # noqa: F811
 
 
 @pytest.mark.parametrize("backward", [False, True])
-@pytest.mark.parametrize("broken", ["n_pos", "q_gain", "k_gain", "dq_gain", "q", "q_out", "dq", "none"])
+@pytest.mark.parametrize("broken", ["n_pos", "positions", "q_gain", "k_gain", "dq_gain", "q", "q_out", "dq", "none"])
 def test_calls_refuse(z, backward, broken):  # noqa: F811
     """Without the norm there are no gains, and the backward call needs no rows."""
     import torch
@@ -51,6 +51,8 @@ def test_calls_refuse(z, backward, broken):  # noqa: F811
         ok = broken == "none"
         if broken == "n_pos":
             b.n_pos = 2 ** 31
+        elif broken == "positions":
+            b.positions, b.positions64 = 0x30004, 1
         elif broken in ("q_gain", "k_gain", "dq_gain"):
             setattr(b, broken, 0x9000)
             ok = broken == "dq_gain" and not backward

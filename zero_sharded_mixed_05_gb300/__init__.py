@@ -1039,9 +1039,9 @@ def zero_qk_launch_count(h) -> int:
 
 # ---------------------------------------------------------------- join of a block with the stream, dropout
 
-# What a handle was made for (dim, dtype, stream dtype, norm_out, gated, device),
-# the dtypes and the calls that its checks need, and memory for one call's
-# zero_block_buffers (calls on one handle are ordered).
+# What a handle was made for (dim, dtype, stream dtype, norm_out, gated, drops,
+# device), what its checks compare with, the current stream's getter, and memory for
+# one call's zero_block_buffers (calls on one handle are ordered).
 _block_handles = {}
 _block_pack = struct.Struct("=26qQqqII").pack_into
 _drop_pack = struct.Struct("=6qiidQqqII").pack_into
@@ -1063,8 +1063,10 @@ def zero_block_create(cfg: zero_block_config) -> int:
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_block_buffers()
     small = ((cfg.dim,), torch.float32, torch.bool, torch.uint8)
+    current = torch._C._cuda_getCurrentRawStream if dev >= 0 else lambda dev: None
     _block_handles[h.value] = (cfg.dim, types[cfg.dtype], types[cfg.stream_dtype], bool(cfg.norm_out),
-                               cfg.gate != GATE_NONE, dev, small, b, ctypes.addressof(b))
+                               cfg.gate != GATE_NONE, cfg.dropout > 0, dev, small, current, b,
+                               ctypes.addressof(b))
     return h.value
 
 
@@ -1096,24 +1098,12 @@ def _rng(seed, call, step, dev):
     return seed, 0, step.data_ptr(), call, 0
 
 
-def _own_stream(stream, dev):
-    if stream is None and dev >= 0:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
-
-
 _NO_ROWS = (0, 0)
+_NO_RNG = (0, 0, 0, 0, 0)
 
 
 def _block_mask(mask, n, small, dev):
     return _qk_flat(mask, "mask", (n,), small[3] if mask.dtype is small[3] else small[2], dev)
-
-
-def _block_handle(h):
-    if h not in _block_handles:
-        raise ValueError("not a handle of zero_block_create")
-    return _block_handles[h]
 
 
 def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, seed=0, call=0, step=0,
@@ -1123,8 +1113,10 @@ def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, s
     `y` None: `x` is only normalised.  Gains are float32 [D] or None (ones);
     `mask` is bool [tokens], False for padding, whose results are zero.  `seed`,
     `call` and `step` (an integer, or an int64 tensor on the device) choose the
-    dropped numbers."""
-    dim, dtype, sdtype, norm, gated, dev, small, b, at = _block_handle(h)
+    dropped numbers of a handle with a dropout."""
+    if h not in _block_handles:
+        raise ValueError("not a handle of zero_block_create")
+    dim, dtype, sdtype, norm, gated, drops, dev, small, current, b, at = _block_handles[h]
     n = x.shape[0]
     shape = (n, dim)
     px = _rows(x, "x", shape, sdtype, dev)
@@ -1140,8 +1132,9 @@ def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, s
     _block_pack(b, 0, n, *px, *py, *pg, *pxo, *ph, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
                 0 if y_gain is None else _qk_flat(y_gain, "y_gain", small[0], small[1], dev),
                 0 if gain is None else _qk_flat(gain, "gain", small[0], small[1], dev), 0, 0,
-                0 if mask is None else _block_mask(mask, n, small, dev), *_rng(seed, call, step, dev))
-    status = lib().zero_block_join(h, at, _own_stream(stream, dev))
+                0 if mask is None else _block_mask(mask, n, small, dev),
+                *(_rng(seed, call, step, dev) if drops else _NO_RNG))
+    status = lib().zero_block_join(h, at, current(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "zero_block_join")
 
@@ -1152,7 +1145,9 @@ def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_
     None: zero), the forward call's `x_out` (without `y`: its `x`), `y` and
     `gate` into `dx`, `dy`, `dgate` and the gains' float32 gradients (None: not
     wanted).  The rng is the forward call's."""
-    dim, dtype, sdtype, norm, gated, dev, small, b, at = _block_handle(h)
+    if h not in _block_handles:
+        raise ValueError("not a handle of zero_block_create")
+    dim, dtype, sdtype, norm, gated, drops, dev, small, current, b, at = _block_handles[h]
     n = x_out.shape[0]
     shape = (n, dim)
     px = _rows(x_out, "x_out", shape, sdtype, dev)
@@ -1177,8 +1172,9 @@ def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_
                 0 if gain is None else _qk_flat(gain, "gain", cols, f32, dev),
                 0 if dy_gain is None else _qk_flat(dy_gain, "dy_gain", cols, f32, dev),
                 0 if dgain is None else _qk_flat(dgain, "dgain", cols, f32, dev),
-                0 if mask is None else _block_mask(mask, n, small, dev), *_rng(seed, call, step, dev))
-    status = lib().zero_block_join_backward(h, at, _own_stream(stream, dev))
+                0 if mask is None else _block_mask(mask, n, small, dev),
+                *(_rng(seed, call, step, dev) if drops else _NO_RNG))
+    status = lib().zero_block_join_backward(h, at, current(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "zero_block_join_backward")
 
@@ -1214,6 +1210,7 @@ def zero_dropout(x, out, p, seed=0, call=0, step=0, stream=None) -> None:
     b = zero_drop_buffers()
     _drop_pack(b, 0, x.data_ptr(), out.data_ptr(), rows, cols, si, so, dtypes[x.dtype], 0, p,
                *_rng(seed, call, step, dev))
-    status = lib().zero_dropout(ctypes.addressof(b), _own_stream(stream, dev))
+    status = lib().zero_dropout(ctypes.addressof(b), torch._C._cuda_getCurrentRawStream(dev)
+                                if stream is None else _stream(stream))
     if status:
         _check(status, "zero_dropout")

@@ -422,8 +422,9 @@ zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
   }
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
-  // Partial gradients of every CTA of the largest grid.
-  h->max_grid = (int64_t)kMaxPerSm * h->sms;
+  // Partial gradients of every CTA of the largest grid (the backward pass has two rows
+  // a CTA or more on their way to an SM, of 16,384 numbers together).
+  h->max_grid = (int64_t)h->sms * std::max(1, std::min(kMaxPerSm, 8192 / cfg->dim));
   const size_t numbers = (size_t)h->max_grid * 2 * ((cfg->dim + 7) / 8 * 8), dim = (cfg->dim + 7) / 8 * 8;
   if (e == cudaSuccess)
     e = cudaMalloc(reinterpret_cast<void**>(&h->part), (numbers + dim) * sizeof(float));
@@ -482,7 +483,8 @@ zero_status zero_dropout(const zero_drop_buffers* b, void* stream) {
     if (!b->in || !b->out) return fail(ZERO_EINVAL, "in or out is NULL");
     if (reinterpret_cast<uintptr_t>(b->in) % es || reinterpret_cast<uintptr_t>(b->out) % es)
       return fail(ZERO_EINVAL, "in or out is misaligned");
-    if (b->rows > 1 && std::abs(b->out_stride) < b->cols) return fail(ZERO_EINVAL, "rows of the result lie on one another");
+    if (b->rows > 1 && std::abs(b->out_stride) < b->cols)
+      return fail(ZERO_EINVAL, "rows of the result lie on one another");
     if (reinterpret_cast<uintptr_t>(b->rng.step_dev) % 8) return fail(ZERO_EINVAL, "step_dev is misaligned");
   }
   int device = -1, sms = 0;

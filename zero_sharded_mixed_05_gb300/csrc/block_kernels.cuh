@@ -223,7 +223,8 @@ struct Lane {
     }
     if constexpr (!kWide) {
       // the ends, number by number: those before the first whole granule, and behind the last
-      const uint32_t number = l % 8 * kS, head = min(bytes, (16 - shift) % 16), rest = max(head, 16 * hi - min(16 * hi, shift));
+      const uint32_t number = l % 8 * kS, head = min(bytes, (16 - shift) % 16);
+      const uint32_t rest = max(head, 16 * hi - min(16 * hi, shift));
       const uint32_t e = l < 8 ? number : rest + number;
       if (l < 16 && number < 16 && e < (l < 8 ? head : bytes))
         *reinterpret_cast<E*>(to + e) = *reinterpret_cast<const E*>(slot<E>(at, n, e / 16) + e % 16);

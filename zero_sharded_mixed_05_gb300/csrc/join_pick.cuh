@@ -36,7 +36,8 @@ const void* shifted_join_of(const JoinPick& p) {
 template <typename T, typename S>
 const void* join_of(const JoinPick& p) {
   if (p.chunks == 4)
-    return p.wide ? join_of<T, S, 4, true, kGated>(p.backward, p.post) : join_of<T, S, 4, false, kGated>(p.backward, p.post);
+    return p.wide ? join_of<T, S, 4, true, kGated>(p.backward, p.post)
+                  : join_of<T, S, 4, false, kGated>(p.backward, p.post);
   if (!p.wide)
     return p.chunks == 1           ? shifted_join_of<T, S, 1, kJoinThreads>(p)
            : p.large || p.backward ? shifted_join_of<T, S, 2, kJoinThreads>(p)

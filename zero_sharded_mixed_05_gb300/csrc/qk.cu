@@ -150,6 +150,8 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
           ((w ? c.k_heads : c.q_heads) > 1 && std::abs(out[w]->head_stride) < c.head_dim))
         return fail(ZERO_EINVAL, "rows of a %s result lie on one another", w ? "key" : "query");
     if (!b->positions) return fail(ZERO_EINVAL, "positions are NULL");
+    if (ax.axes > 0 && reinterpret_cast<uintptr_t>(b->positions) % (b->positions64 ? 8 : 4))
+      return fail(ZERO_EINVAL, "positions are misaligned");
     if (c.rotary_dim > 0 && b->n_pos > 0 && (!b->cos || !b->sin))
       return fail(ZERO_EINVAL, "cos and sin must be non-NULL");
   }

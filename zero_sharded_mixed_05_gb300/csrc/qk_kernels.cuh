@@ -137,7 +137,8 @@ struct Positions {
 __device__ __forceinline__ Positions positions(const QkAxesArgs& a, const unsigned char* at) {
   bool low = false, high = false;
   for (int k = 0; k < a.axes; ++k) {
-    const int64_t v = a.pos64 ? *reinterpret_cast<const int64_t*>(at + k * 8) : (int64_t)*reinterpret_cast<const int*>(at + k * 8);
+    const int64_t v = a.pos64 ? *reinterpret_cast<const int64_t*>(at + k * 8)
+                              : (int64_t)*reinterpret_cast<const int*>(at + k * 8);
     low |= v < 0;
     high |= v >= a.n_pos;
   }
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
     // The CTA's share of the gains' gradients: a group's sums to shared memory
     // (over the ring, which is done with), each column then added over the
     // groups in order.
-    if constexpr (kAsync) asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (kAsync || kAxes) asm volatile("cp.async.wait_all;" ::: "memory");
     float* s_part = reinterpret_cast<float*>(s_raw);
     float* to = a.part + (int64_t)blockIdx.x * a.part_rows * a.dim;
     // groups of queries among the CTA's
