@@ -56,11 +56,14 @@ __global__ void __launch_bounds__(32 * kParts) join_fold_kernel(const __grid_con
   }
   s[part][threadIdx.x % 32] = sum;
   __syncthreads();
-  if (part == 0 && col < cols) {
+  // kParts lanes a column, of which each has one thread's sum
+  const int mine = threadIdx.x / kParts, lane = threadIdx.x % kParts, at = blockIdx.x * 32 + mine;
+  sum = s[lane][mine];
 #pragma unroll
-    for (int k = 1; k < kParts; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
-    float* out = a.out[col >= a.dim];
-    if (out) out[col >= a.dim ? col - a.dim : col] = sum;
+  for (int o = kParts / 2; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
+  if (lane == 0 && at < cols) {
+    float* out = a.out[at >= a.dim];
+    if (out) out[at >= a.dim ? at - a.dim : at] = sum;
   }
 }
 

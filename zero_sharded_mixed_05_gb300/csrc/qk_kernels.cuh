@@ -196,14 +196,18 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
   constexpr int kEach = kBackward ? 4 : 2;                 // vectors of a chunk
   constexpr int kSums = !kBackward ? 1 : kSum ? 1 : R;
   const int lanes = a.lanes;
-  const int group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  // (rows that are only rotated need no power of two lanes: the rest of a warp idles)
+  const int in_warp = 32 / lanes;
+  const int group = kAxes ? threadIdx.x / 32 * in_warp + threadIdx.x % 32 / lanes : threadIdx.x / lanes;
+  const int lane = kAxes ? threadIdx.x % 32 % lanes : threadIdx.x % lanes;
+  const bool idle = kAxes && threadIdx.x % 32 >= in_warp * lanes;
   // the group's lanes of its warp: groups of one warp walk on by themselves
   const unsigned mask = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u)
                         << (threadIdx.x % 32 / lanes * lanes);
   const int block = blockIdx.x % a.head_blocks;
   const int rep = group / a.per;
   const int head0 = (block * a.per + group % a.per) * R;
-  const bool on = rep < a.reps && head0 < a.heads;
+  const bool on = rep < a.reps && head0 < a.heads && !idle;
   const int64_t slots = (int64_t)(gridDim.x / a.head_blocks) * a.reps;
   const int64_t first = (int64_t)(blockIdx.x / a.head_blocks) * a.reps + rep;
   const Rows& w = a.r[on && head0 >= a.r[0].heads ? 1 : 0];
@@ -420,13 +424,13 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
         // backward pass has no registers to wait for them in
         if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(n + 1));
         float sum = __fadd_rn(sq.x, sq.y), sum_dot = __fadd_rn(dot.x, dot.y);
-        for (int o = lanes >> 1; o > 0; o >>= 1) {
+        bool norm = true;
+        if constexpr (kAxes && !kBackward) norm = a.norm;
+        for (int o = norm ? lanes >> 1 : 0; o > 0; o >>= 1) {
           sum = __fadd_rn(sum, __shfl_xor_sync(mask, sum, o));
           if (kBackward) sum_dot = __fadd_rn(sum_dot, __shfl_xor_sync(mask, sum_dot, o));
         }
-        float inv = rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps));
-        if constexpr (kAxes && !kBackward)
-          if (!a.norm) inv = 1.0f;
+        const float inv = norm ? rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps)) : 1.0f;
         const float2 inv2 = both(inv);
         // dx = inv (dn - xhat mean(dn xhat)), dn = dy gain: no power of inv but the
         // first, so that it holds for rows of any size
