@@ -370,6 +370,69 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
       if constexpr (kAxes) __syncwarp(mask);
       // padding, or no angle for this position: a fill of the rows
       const bool skip = p.first < 0 || (p.first >= a.n_pos && a.rot > 0);
+      if constexpr (kAxes && !kBackward) {
+        // Two rows at a time, so that their sums over the lanes do not wait for one
+        // another (16,384 tokens over three axes 66 us a row at a time, 62 so, four
+        // at a time, whose registers spill, 81).
+        constexpr int kPair = R < 2 ? R : 2;
+#pragma unroll
+        for (int r0 = 0; r0 < R; r0 += kPair) {
+          float2 x[kPair][C][V];
+          float sum[kPair];
+          if (!skip) {
+#pragma unroll
+            for (int q = 0; q < kPair; ++q) {
+              const int r = r0 + q;
+              if (R > 1 && a.gain_per_head) load_gain(r);
+              float2 sq = both(0.0f);
+#pragma unroll
+              for (int j = 0; j < C; ++j) {
+                if (!live(j)) continue;
+                const unsigned char* from = mine + (at * (R * C * kEach) + (r * C + j) * kEach) * step;
+                const auto vec = [&](int k, int e) {
+                  if constexpr (kAsync) return *reinterpret_cast<const Vec<T, V>*>(from + k * step);
+                  else return load<T, V>(in + r * in_h, e);
+                };
+                widen<T, V>(vec(0, p0[j]), vec(1, p1[j]), x[q][j]);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                  sq = __ffma2_rn(x[q][j][i], x[q][j][i], sq);
+                  x[q][j][i] = __fmul2_rn(x[q][j][i], gain[j][i]);
+                }
+                if ((lane + j * lanes) * 2 * V < a.rot) turn<V, kInter>(x[q][j], cs[j], sn[j], a.inverse);
+              }
+              sum[q] = __fadd_rn(sq.x, sq.y);
+            }
+          }
+          if (r0 + kPair >= R && t + slots < a.tokens) angles(look(n + 1));
+          if (!skip && a.norm) {
+            for (int o = lanes >> 1; o > 0; o >>= 1)
+#pragma unroll
+              for (int q = 0; q < kPair; ++q) sum[q] = __fadd_rn(sum[q], __shfl_xor_sync(mask, sum[q], o));
+#pragma unroll
+            for (int q = 0; q < kPair; ++q) {
+              const float2 inv = both(rsqrtf(__fmaf_rn(sum[q], a.inv_dim, a.eps)));
+#pragma unroll
+              for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[q][j][i] = __fmul2_rn(x[q][j][i], inv);
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kPair; ++q)
+#pragma unroll
+            for (int j = 0; j < C; ++j) {
+              if (!live(j)) continue;
+              if (skip)
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[q][j][i] = both(p.first < 0 ? 0.0f : __int_as_float(0x7fffffff));
+              Vec<T, V> u, v;
+              narrow<T, V>(x[q][j], u, v);
+              store<T, V>(out + (r0 + q) * out_h, p0[j], u);
+              store<T, V>(out + (r0 + q) * out_h, p1[j], v);
+            }
+        }
+      } else {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (skip) {
@@ -386,7 +449,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
 #pragma unroll
               for (int i = 0; i < V; ++i) dgain[kSum ? 0 : r][j][i] = both(f);
           }
-          if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(n + 1));
+          if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(0));
           continue;
         }
         if (R > 1 && a.gain_per_head) load_gain(r);
@@ -413,24 +476,18 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
             // the rotation does not wait for the norm, which scales it as a whole
 #pragma unroll
             for (int i = 0; i < V; ++i) x[j][i] = __fmul2_rn(x[j][i], gain[j][i]);
-            if (turned) {
-              bool inverse = false;
-              if constexpr (kAxes) inverse = a.inverse;
-              turn<V, kInter>(x[j], cs[j], sn[j], inverse);
-            }
+            if (turned) turn<V, kInter>(x[j], cs[j], sn[j], false);
           }
         }
         // forward the next token's angles come as soon as these are done with; the
         // backward pass has no registers to wait for them in
-        if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(n + 1));
+        if (!kBackward && r == R - 1 && t + slots < a.tokens) angles(look(0));
         float sum = __fadd_rn(sq.x, sq.y), sum_dot = __fadd_rn(dot.x, dot.y);
-        bool norm = true;
-        if constexpr (kAxes && !kBackward) norm = a.norm;
-        for (int o = norm ? lanes >> 1 : 0; o > 0; o >>= 1) {
+        for (int o = lanes >> 1; o > 0; o >>= 1) {
           sum = __fadd_rn(sum, __shfl_xor_sync(mask, sum, o));
           if (kBackward) sum_dot = __fadd_rn(sum_dot, __shfl_xor_sync(mask, sum_dot, o));
         }
-        const float inv = norm ? rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps)) : 1.0f;
+        const float inv = rsqrtf(__fmaf_rn(sum, a.inv_dim, a.eps));
         const float2 inv2 = both(inv);
         // dx = inv (dn - xhat mean(dn xhat)), dn = dy gain: no power of inv but the
         // first, so that it holds for rows of any size
@@ -454,6 +511,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
           store<T, V>(out + r * out_h, p0[j], u);
           store<T, V>(out + r * out_h, p1[j], v);
         }
+      }
       }
       if (!kAsync) {
         in += in_t;
