@@ -29,41 +29,45 @@ constexpr int kMaxSmem = 227 * 1024 - 1024;
 constexpr int kMaxPerSm = 4;             // CTAs an SM
 
 struct FoldArgs {
-  const float* part;
+  const float* part;    // as JoinArgs::part
   float* out[2];
-  int32_t grid, dim;
+  int32_t grid, dim, chunks;
 };
 
-// Sums the CTAs' partial gradients in index order: 32 columns a CTA, kParts threads
-// a column, each over every kParts-th partial.  Eight fill the device for long rows
-// (the gradient of 16,384 rows of 4096 131 us, with 32 136), for short ones 32 are
-// sooner done (of 768: 34.6 us, with 32 32.6).
-template <int kParts>
-__global__ void __launch_bounds__(32 * kParts) join_fold_kernel(const __grid_constant__ FoldArgs a) {
-  __shared__ float s[kParts][33];
+// Sums the CTAs' partial gradients in index order: 64 columns a CTA, 32 threads a
+// pair of columns, each over every 32nd partial.
+__global__ void __launch_bounds__(1024) join_fold_kernel(const __grid_constant__ FoldArgs a) {
+  __shared__ float s[32][65];
   cudaGridDependencySynchronize();   // launched while the partials are still written
-  const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32, cols = 2 * a.dim;
-  float sum = 0.0f;
+  const int lane = threadIdx.x % 32, part = threadIdx.x / 32, cols = 16 * a.chunks;
+  const int col = blockIdx.x * 64 + 2 * lane;
+  float2 sum = make_float2(0.0f, 0.0f);
   if (col < cols) {
     const float* at = a.part + col;
-    for (int c = part; c < a.grid; c += 10 * kParts) {
-      float v[10];                   // ten loads on their way at once
+    for (int c = part; c < a.grid; c += 320) {
+      float2 v[10];                  // ten loads on their way at once
 #pragma unroll
-      for (int k = 0; k < 10; ++k) v[k] = c + kParts * k < a.grid ? at[(int64_t)(c + kParts * k) * cols] : 0.0f;
+      for (int k = 0; k < 10; ++k)
+        v[k] = c + 32 * k < a.grid ? *reinterpret_cast<const float2*>(at + (int64_t)(c + 32 * k) * cols)
+                                   : make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int k = 0; k < 10; ++k) sum = __fadd_rn(sum, v[k]);
+      for (int k = 0; k < 10; ++k) sum = __fadd2_rn(sum, v[k]);
     }
   }
-  s[part][threadIdx.x % 32] = sum;
+  s[part][2 * lane] = sum.x;
+  s[part][2 * lane + 1] = sum.y;
   __syncthreads();
-  // kParts lanes a column, of which each has one thread's sum
-  const int mine = threadIdx.x / kParts, lane = threadIdx.x % kParts, at = blockIdx.x * 32 + mine;
-  sum = s[lane][mine];
+  // a warp a pair of columns: each lane has one thread's sums
 #pragma unroll
-  for (int o = kParts / 2; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, o));
-  if (lane == 0 && at < cols) {
-    float* out = a.out[at >= a.dim];
-    if (out) out[at >= a.dim ? at - a.dim : at] = sum;
+  for (int k = 0; k < 2; ++k) {
+    float v = s[lane][2 * part + k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, o));
+    // number col % 4 of the first or the last half of a chunk, of the first gain or the second
+    const int at = blockIdx.x * 64 + 2 * part + k, quarter = at / (4 * a.chunks), rest = at - quarter * 4 * a.chunks;
+    const int e = rest / 4 * 8 + quarter % 2 * 4 + rest % 4;
+    float* out = at < cols ? a.out[quarter / 2] : nullptr;
+    if (lane == 0 && out && e < a.dim) out[e] = v;
   }
 }
 
@@ -327,7 +331,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     a.dh = a.x = none;
     a.eps = 1.0f;
   }
-  a.part = want ? h->part : nullptr;
+  a.part = want ? reinterpret_cast<float4*>(h->part) : nullptr;
   bool wide = c.dim % 8 == 0;
   for (const auto& r : rows) wide = wide && on16(r.r->data, r.r->stride, b->tokens);
   // Chunks a thread.  One where there are few, or few rows (a row is done sooner by
@@ -362,7 +366,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.ring = ctas == 1 ? 3 : std::max(2, std::min(3, slots / ctas));
   a.ring = std::max(1, std::min(a.ring, kMaxSmem / row));
   size_t smem = (size_t)a.ring * row;
-  if (want && a.teams > 1) smem = std::max(smem, (size_t)c.dim * 2 * sizeof(float));
+  if (want && a.teams > 1) smem = std::max(smem, (size_t)a.chunks * 16 * sizeof(float));
   ctas = std::min(ctas, h->resident(fn, threads, (int)smem));
   int64_t grid = std::min((b->tokens + a.teams - 1) / a.teams, (int64_t)ctas * h->sms);
   if (want) grid = std::min(grid, h->max_grid);
@@ -372,19 +376,18 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernel");
   ++h->launches;
   if (want) {
-    FoldArgs f = {h->part, {dgain[0], dgain[1]}, (int)grid, c.dim};
+    FoldArgs f = {h->part, {dgain[0], dgain[1]}, (int)grid, c.dim, a.chunks};
     void* fp[] = {&f};
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)((2 * c.dim + 31) / 32));
-    const bool few = c.dim <= 2048;
-    lc.blockDim = dim3(few ? 1024 : 256);
+    lc.gridDim = dim3((unsigned)((16 * a.chunks + 63) / 64));
+    lc.blockDim = dim3(1024);
     lc.stream = s;
     lc.attrs = &early;
     lc.numAttrs = 1;
-    e = cudaLaunchKernelExC(&lc, few ? (const void*)join_fold_kernel<32> : (const void*)join_fold_kernel<8>, fp);
+    e = cudaLaunchKernelExC(&lc, (const void*)join_fold_kernel, fp);
     if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
     ++h->launches;
   }

@@ -40,7 +40,8 @@ struct JoinArgs {
   const float* y_gain;
   const float* gain;
   const uint8_t* mask;
-  float* part;          // backward: [grid][2][D] partial gradients of y_gain and gain, or NULL
+  float4* part;         // backward: [grid][2][2][chunks] partial gradients of y_gain and gain, the
+                        // first and the last four numbers of every chunk, or NULL
   int64_t tokens;
   Drop drop;
   int32_t dim, chunks;
@@ -208,10 +209,10 @@ struct Lane {
     const uint32_t bytes = min(256, dim - begin) * kS;
     const uint32_t shift = kWide ? 0 : reinterpret_cast<uintptr_t>(to) % 16;
     // whole granules [16 u - shift, 16 u - shift + 16) of these bytes
-    const uint32_t lo = shift ? 1 : 0, hi = (bytes + shift) / 16;
+    const int lo = shift ? 1 : 0, hi = (bytes + shift) / 16;
 #pragma unroll
     for (uint32_t u = l; u < 32 * kV; u += 32) {
-      if (u < lo || u >= hi) continue;
+      if ((int)u < lo || (int)u >= hi) continue;
       uint4 w = *reinterpret_cast<const uint4*>(slot<E>(at, n, u));
       if (!kWide && shift) {
         const uint4 p = *reinterpret_cast<const uint4*>(slot<E>(at, n, u - 1));
@@ -224,7 +225,7 @@ struct Lane {
     if constexpr (!kWide) {
       // the ends, number by number: those before the first whole granule, and behind the last
       const uint32_t number = l % 8 * kS, head = min(bytes, (16 - shift) % 16);
-      const uint32_t rest = max(head, 16 * hi - min(16 * hi, shift));
+      const uint32_t rest = max(head, 16u * hi - min(16u * hi, shift));
       const uint32_t e = l < 8 ? number : rest + number;
       if (l < 16 && number < 16 && e < (l < 8 ? head : bytes))
         *reinterpret_cast<E*>(to + e) = *reinterpret_cast<const E*>(slot<E>(at, n, e / 16) + e % 16);
@@ -725,30 +726,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
     to = to + row == a.ring * row ? 0 : to + row;
   }
 
-  // The CTA's share of the gains' gradients: its teams' one after the other.
+  // The CTA's share of the gains' gradients: its teams' one after the other, in
+  // shared memory as in `part`, where the lanes of a warp are next to one another.
   if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * 2 * a.dim;
-  float* s_sum = reinterpret_cast<float*>(s_ring);
+  float4* const part = a.part + (int64_t)blockIdx.x * 4 * a.chunks;
+  float4* const s_sum = reinterpret_cast<float4*>(s_ring);
   asm volatile("cp.async.wait_all;" ::: "memory");
   for (int team = 0; team < a.teams; ++team) {
     __syncthreads();
     if (me.team != team) continue;
-    const bool last = team == a.teams - 1;
+    float4* const out = team == a.teams - 1 ? part : s_sum;
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
-      const int left = min(8, a.dim - me.chunk(j) * 8);
+      if (!me.live(j)) continue;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k >= left) continue;
-        const int e = me.chunk(j) * 8 + k;
-        float y = k % 2 ? dyg[j][k / 2].y : dyg[j][k / 2].x, g = k % 2 ? dg[j][k / 2].y : dg[j][k / 2].x;
+      for (int k = 0; k < 4; ++k) {
+        const float2* d = (k < 2 ? dyg[j] : dg[j]) + k % 2 * 2;
+        const int at = k * a.chunks + me.chunk(j);
+        float4 v = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
         if (team > 0) {
-          y = __fadd_rn(s_sum[e], y);
-          g = __fadd_rn(s_sum[a.dim + e], g);
+          const float4 o = s_sum[at];
+          v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
         }
-        float* out = last ? part : s_sum;
-        out[e] = y;
-        out[a.dim + e] = g;
+        out[at] = v;
       }
     }
   }
