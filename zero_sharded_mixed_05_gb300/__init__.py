@@ -898,9 +898,16 @@ def zero_muon_launch_count(h) -> int:
 
 # What a handle was made for, so that the binding can check tensors against it
 # (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, axes or 0,
-# device), and memory for one call's zero_qk_buffers (calls on one handle are ordered).
+# device), the other dtypes, the current stream's getter, and memory for one
+# call's zero_qk_buffers (calls on one handle are ordered).
 _qk_handles = {}
 _qk_pack = struct.Struct("=27qii").pack_into
+
+
+def _stream_getter(dev):
+    """What gives the current stream of a device (-1: none) as an integer."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream if dev >= 0 else lambda dev: None
 
 
 def make_qk_config(q_heads, k_heads, head_dim, rotary_dim=None, dtype=BF16, interleaved=False,
@@ -934,7 +941,8 @@ def zero_qk_create(cfg: zero_qk_config, axes: zero_qk_axes = None) -> int:
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_qk_buffers()
     _qk_handles[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
-                            bool(cfg.gain_per_head), axes.axes if axes else 0, dev, b,
+                            bool(cfg.gain_per_head), axes.axes if axes else 0, dev,
+                            (torch.float32, torch.int64, torch.int32), _stream_getter(dev), b,
                             ctypes.addressof(b))
     return h.value
 
@@ -948,13 +956,13 @@ def _qk_refuse(name, what):
     raise ValueError(f"{name} must be {what}")
 
 
-def _qk_heads(t, name, n, heads, dim, dtype, dev):
+def _qk_heads(t, name, shape, dtype, dev):
     """(address, token stride, head stride) of a [tokens, heads, D] tensor."""
-    st, sh, sd = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if t.dtype is not dtype or t.shape != (n, heads, dim) or t.get_device() != dev or sd != 1:
-        _qk_refuse(name, f"a {dtype} tensor of {(n, heads, dim)} with contiguous heads on "
-                   f"cuda:{dev}")
-    return t.data_ptr(), st, sh
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        st, sh, sd = t.stride()
+        if sd == 1:
+            return t.data_ptr(), st, sh
+    _qk_refuse(name, f"a {dtype} tensor of {shape} with contiguous heads on cuda:{dev}")
 
 
 def _qk_flat(t, name, shape, dtype, dev):
@@ -970,27 +978,26 @@ _NO_HEADS = (0, 0, 0)
 def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gain, cos, sin,
              positions, stream):
     """Check the tensors against the handle and make the call."""
-    import torch
     if h not in _qk_handles:
         raise ValueError("not a handle of zero_qk_create")
-    hq, hk, dim, half, dtype, per_head, axes, dev, b, at = _qk_handles[h]
+    hq, hk, dim, half, dtype, per_head, axes, dev, (f32, i64, i32), current, b, at = _qk_handles[h]
     n = q.shape[0]
-    f32 = torch.float32
-    tq = _qk_heads(q, "q", n, hq, dim, dtype, dev)
-    tqo = _qk_heads(qo, names[0], n, hq, dim, dtype, dev)
-    tdq = _NO_HEADS if dq is None else _qk_heads(dq, "dq", n, hq, dim, dtype, dev)
+    shape = (n, hq, dim)
+    tq = _qk_heads(q, "q", shape, dtype, dev)
+    tqo = _qk_heads(qo, names[0], shape, dtype, dev)
+    tdq = _NO_HEADS if dq is None else _qk_heads(dq, "dq", shape, dtype, dev)
     shape = (hq, dim) if per_head else (dim,)
     gq = 0 if q_gain is None else _qk_flat(q_gain, "q_gain", shape, f32, dev)
     dgq = 0 if dq_gain is None else _qk_flat(dq_gain, "dq_gain", shape, f32, dev)
     tk = tko = tdk = _NO_HEADS
     gk = dgk = 0
     if hk:
-        tk = _qk_heads(k, "k", n, hk, dim, dtype, dev)
-        tko = _qk_heads(ko, names[1], n, hk, dim, dtype, dev)
+        shape = (n, hk, dim)
+        tk = _qk_heads(k, "k", shape, dtype, dev)
+        tko = _qk_heads(ko, names[1], shape, dtype, dev)
         if dk is not None:
-            tdk = _qk_heads(dk, "dk", n, hk, dim, dtype, dev)
-        if per_head:
-            shape = (hk, dim)
+            tdk = _qk_heads(dk, "dk", shape, dtype, dev)
+        shape = (hk, dim) if per_head else (dim,)
         if k_gain is not None:
             gk = _qk_flat(k_gain, "k_gain", shape, f32, dev)
         if dk_gain is not None:
@@ -1001,12 +1008,10 @@ def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gai
         table = (n_pos, half)
         pc = _qk_flat(cos, "cos", table, f32, dev)
         ps = _qk_flat(sin, "sin", table, f32, dev)
-    wide = positions.dtype is torch.int64
-    pp = _qk_flat(positions, "positions", (axes, n) if axes else (n,), torch.int64 if wide else torch.int32, dev)
+    wide = positions.dtype is i64
+    pp = _qk_flat(positions, "positions", (axes, n) if axes else (n,), i64 if wide else i32, dev)
     _qk_pack(b, 0, n, n_pos, *tq, *tk, *tqo, *tko, *tdq, *tdk, gq, gk, dgq, dgk, pc, ps, pp, wide, 0)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
-    status = fn(h, at, _stream(stream))
+    status = fn(h, at, current(dev) if stream is None else _stream(stream))
     if status:
         _check(status, fn.__name__)
 
@@ -1063,9 +1068,8 @@ def zero_block_create(cfg: zero_block_config) -> int:
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_block_buffers()
     small = ((cfg.dim,), torch.float32, torch.bool, torch.uint8)
-    current = torch._C._cuda_getCurrentRawStream if dev >= 0 else lambda dev: None
     _block_handles[h.value] = (cfg.dim, types[cfg.dtype], types[cfg.stream_dtype], bool(cfg.norm_out),
-                               cfg.gate != GATE_NONE, cfg.dropout > 0, dev, small, current, b,
+                               cfg.gate != GATE_NONE, cfg.dropout > 0, dev, small, _stream_getter(dev), b,
                                ctypes.addressof(b))
     return h.value
 

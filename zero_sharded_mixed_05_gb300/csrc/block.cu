@@ -35,7 +35,9 @@ struct FoldArgs {
 };
 
 // Sums the CTAs' partial gradients in index order: 64 columns a CTA, 32 threads a
-// pair of columns, each over every 32nd partial.
+// pair of columns, each over every 32nd partial.  Bound by its launch and one or two
+// round trips: with the writing of the partials it adds 2.2 us to a small gradient and
+// 4.2 to one of 4096 columns.
 __global__ void __launch_bounds__(1024) join_fold_kernel(const __grid_constant__ FoldArgs a) {
   __shared__ float s[32][65];
   cudaGridDependencySynchronize();   // launched while the partials are still written
