@@ -273,6 +273,41 @@ def test_what_is_dropped_does_not_count(z):
         c.close()
 
 
+@pytest.mark.parametrize("D", [1, 3, 8, 13])
+def test_a_row_of_which_all_is_dropped(z, D):
+    """It is the stream's, though the branch's norm be NaN; also of rows that are not
+    whole chunks."""
+    import torch
+    c = Case(z, (4000, D, "fp32", "fp32", True, True, "none", 0.6, 0.0, "own", 1.0, 1.0, True), 14)
+    keep = torch.from_numpy(R.kept(4000, D, 0.6, *c.rng)).cuda()
+    gone = ~keep.any(-1)
+    assert gone.any()
+    c.y[:, 0] = float("nan")
+    xo, h = c.forward()
+    assert torch.equal(xo[gone], c.x[gone]) and h[gone].isfinite().all()
+    c.y.zero_()
+    c.y[:, 0] = 1.0
+    want = c.forward()
+    assert torch.equal(want[1][gone], h[gone])
+    c.close()
+
+
+@pytest.mark.parametrize("D", [520, 521])
+def test_in_place_on_a_binary32_stream(z, D):
+    """As test_in_place, with results that change places with other inputs."""
+    import torch
+    c = Case(z, (333, D, "bf16", "fp32", True, True, "plain", 0.1, 0.1, "own", 1.0, 1.0, True), 15)
+    xo, h = c.forward()
+    want = c.backward(xo)
+    x, gate = c.x.clone(), c.gate.clone()
+    z.zero_block_join(c.h, x, c.y, x, gate, c.y_gain, c.gain, **dict(c.kw, gate=gate))
+    assert torch.equal(x, xo) and torch.equal(gate, h)
+    y, dh, xo2 = c.y.clone(), c.dh.clone(), xo.clone()       # dgate over dh, dy over y, dx over x'
+    z.zero_block_join_backward(c.h, c.dxo, dh, xo2, y, xo2, y, None, None, c.y_gain, c.gain, dgate=dh, **c.kw)
+    assert torch.equal(xo2, want["dx"]) and torch.equal(y, want["dy"]) and torch.equal(dh, want["dgate"])
+    c.close()
+
+
 def test_rows_of_zeros_and_of_extreme_sizes(z):
     """1e-17 to 1e17 in binary32 with eps 0 is exact in its scale; zero rows are
     normalised to zero."""

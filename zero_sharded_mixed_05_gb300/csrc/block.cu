@@ -440,6 +440,8 @@ zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
     h->zeros = h->part + numbers;
     e = cudaMemset(h->zeros, 0, dim * sizeof(float));
   }
+  // (a call's stream need not wait for the default stream)
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);
   if (e != cudaSuccess) {
     cudaFree(h->part);
     cudaGetLastError();

@@ -457,7 +457,14 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : kWide || (kC > 1 && 
         for (int k = 0; k < 4; ++k) {
           v[j][k] = __ffma2_rn(v[j][k], both(a.alpha), b[k]);
         }
-        // (a factor that is infinite makes NaN of a zero that is no number of the row)
+        // (a factor that is no number makes NaN of a zero that is no number of the row)
+        if constexpr (!kWide) {
+          const int left = a.dim - me.chunk(j) * 8;
+          if (left < 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              v[j][k] = make_float2(2 * k < left ? v[j][k].x : 0.0f, 2 * k + 1 < left ? v[j][k].y : 0.0f);
+        }
         if (me.live(j))
 #pragma unroll
           for (int k = 0; k < 4; ++k) sq = __ffma2_rn(v[j][k], v[j][k], sq);
