@@ -24,7 +24,7 @@
 // once it is there; results are shifted the other way, so that all but the ends of
 // a warp's 256 numbers are written 16 bytes at a time (4,000 rows of 4097 in bf16 with
 // both norms: 48 us forward, 105 backward, 40 and 28 % of the copy rate; number by
-// number 78 and 207.  The shifts' selects bound them).
+// number 76 and 171.  The shifts' selects bound them).
 #pragma once
 
 #include "numbers.cuh"
