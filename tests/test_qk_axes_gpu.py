@@ -2,8 +2,8 @@
 
 It is the rotation by one position whose tables were gathered for each token
 (row t of cos: cos[p[axis[j]][t]][j]), which the one-position kernels, tested
-against 64 bits by themselves, give bit for bit; and both against 64 bits with
-test_qk_gpu.py's tolerances.  Rotation alone rounds twice in binary32 (a product
+against 64 bits by themselves, give bit for bit (the gains' gradients are summed in
+another order); and all against 64 bits with test_qk_gpu.py's tolerances.  Rotation alone rounds twice in binary32 (a product
 and a fused sum of two terms): 2 2^-24 of the terms' magnitudes, and once to the
 type.
 """
@@ -109,14 +109,21 @@ def test_against_gathered_tables_and_64_bits(z, case):  # noqa: F811
         want = run(c.one, c.cos1, c.sin1, c.pos1)
         for pos in (c.pos, c.pos.int()):
             got = run(c.many, *c.many_at(pos))
-            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            assert all(torch.equal(a, b) for a, b in zip(got[:2], want))
+            if c.hk:
+                assert all(torch.equal(a, b) for a, b in zip(got, run(c.many, *c.many_at(pos))))
     fw, bw = c.forward(c.many, *c.many_at()), c.backward(c.many, *c.many_at())
     for i, (x, go, gain) in enumerate(((c.q, c.gq, c.qg), (c.k, c.gk, c.kg))):
         if x.shape[1]:
             ref = forward64(x, gain, c.pos1, c.cos1, c.sin1, c.rot, c.inter)
             near(fw[i], ref, ref.abs().amax(-1, keepdim=True), c.name, c.D)
-            ref, mag, _ = backward64(go, x, gain, c.pos1, c.cos1, c.sin1, c.rot, c.inter)
+            ref, mag, terms = backward64(go, x, gain, c.pos1, c.cos1, c.sin1, c.rot, c.inter)
             near(bw[i], ref, mag, c.name, c.D)
+            dims = 0 if c.per_head else (0, 1)
+            n = c.T if c.per_head else c.T * x.shape[1]
+            scale = terms.abs().amax(-1, keepdim=True) if c.rot else terms.abs()
+            tol = (n + c.D + 16) * 2.0 ** -24 * scale.expand_as(terms).sum(dims)
+            assert ((bw[2 + i].double() - terms.sum(dims)).abs() <= tol).all()
     c.close()
 
 

@@ -41,10 +41,13 @@ struct FoldArgs {
   int32_t grid, head_blocks, part_rows, per, dim, q_heads, heads, gain_per_head;
 };
 
-// Sums the CTAs' partial gain gradients in index order: 32 columns a CTA, 8
-// threads a column, each over every eighth partial.
-__global__ void __launch_bounds__(256) qk_fold_kernel(const __grid_constant__ FoldArgs a) {
-  __shared__ float s[8][33];
+// Sums the CTAs' partial gain gradients in index order: 32 columns a CTA, kParts
+// threads a column, each over every kParts-th partial: eight, or 32 for handles with
+// axes, whose sums are done sooner (3,001 tokens of 16 heads of 64: 15.2 us with
+// eight, 13.6 with 32).
+template <int kParts>
+__global__ void __launch_bounds__(32 * kParts) qk_fold_kernel(const __grid_constant__ FoldArgs a) {
+  __shared__ float s[kParts][33];
   cudaGridDependencySynchronize();   // launched while the partials are still written
   const int col = blockIdx.x * 32 + threadIdx.x % 32, part = threadIdx.x / 32;
   const int rows = a.gain_per_head ? a.heads : 2;
@@ -57,20 +60,21 @@ __global__ void __launch_bounds__(256) qk_fold_kernel(const __grid_constant__ Fo
     const int64_t one = (int64_t)a.part_rows * a.dim;
     const float* at = a.part + (int64_t)local * a.dim + d;
     int c = first + part * step;
-    for (; c + 56 * step < a.grid; c += 64 * step) {
+    for (; c + 7 * kParts * step < a.grid; c += 8 * kParts * step) {
       float v[8];                // eight loads on their way at once
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = at[(c + 8 * k * step) * one];
+      for (int k = 0; k < 8; ++k) v[k] = at[(c + kParts * k * step) * one];
 #pragma unroll
       for (int k = 0; k < 8; ++k) sum = __fadd_rn(sum, v[k]);
     }
 #pragma unroll 4
-    for (; c < a.grid; c += 8 * step) sum = __fadd_rn(sum, at[c * one]);
+    for (; c < a.grid; c += kParts * step) sum = __fadd_rn(sum, at[c * one]);
   }
   s[part][threadIdx.x % 32] = sum;
   __syncthreads();
   if (part == 0 && row < rows) {
-    for (int k = 1; k < 8; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
+#pragma unroll
+    for (int k = 1; k < kParts; ++k) sum = __fadd_rn(sum, s[k][threadIdx.x]);
     const int which = a.gain_per_head ? (row >= a.q_heads) : row;
     const int at = a.gain_per_head ? row - (which ? a.q_heads : 0) : 0;
     if (a.out[which]) a.out[which][(int64_t)at * a.dim + d] = sum;
@@ -290,11 +294,11 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)((cols + 31) / 32));
-    lc.blockDim = dim3(256);
+    lc.blockDim = dim3(ax.axes > 0 ? 1024 : 256);
     lc.stream = s;
     lc.attrs = &early;
     lc.numAttrs = 1;
-    e = cudaLaunchKernelExC(&lc, (const void*)qk_fold_kernel, fp);
+    e = cudaLaunchKernelExC(&lc, ax.axes > 0 ? (const void*)qk_fold_kernel<32> : (const void*)qk_fold_kernel<8>, fp);
     if (e != cudaSuccess) return cuda_fail(e, "cudaLaunchKernelExC");
     ++h->launches;
   }

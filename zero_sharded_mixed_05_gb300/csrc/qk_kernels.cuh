@@ -569,6 +569,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward || kAxes ? 2 : 3)
         const int lo = !kSum ? row : row ? nq : 0, hi = !kSum ? row + 1 : row ? a.per : nq;
         float s = 0.0f;
         for (int q = 0; q < a.reps; ++q)
+#pragma unroll 8
           for (int k = lo; k < hi; ++k) s = __fadd_rn(s, s_part[(q * a.per + k) * a.dim + d]);
         to[kSum ? e : (row * R + r) * a.dim + d] = s;
       }
