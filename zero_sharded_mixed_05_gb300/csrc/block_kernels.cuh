@@ -23,7 +23,7 @@
 // lie in are copied, and a warp's lanes shift what they hold to where it belongs
 // once it is there; results are shifted the other way, so that all but the ends of
 // a warp's 256 numbers are written 16 bytes at a time (4,000 rows of 4097 in bf16 with
-// both norms: 48 us forward, 105 backward, 40 and 28 % of the copy rate; number by
+// both norms: 45 us forward, 95 backward, 43 and 30 % of the copy rate; number by
 // number 76 and 171.  The shifts' selects bound them).
 #pragma once
 
@@ -139,13 +139,35 @@ struct Lane {
         const int left = (int)(shift + dim * (uint32_t)sizeof(E) - begin);
         if (left <= (int)shift) continue;
         const char* from = row - shift + begin;
+        if (left >= (int)(512 * kV + 16)) {      // not the row's last numbers
 #pragma unroll
-        for (uint32_t u = l; u <= 32 * kV; u += 32) {
-          const int bytes = left - 16 * (int)u;
-          copy16(slot<E>(at, first + j * kV, u), bytes > 0 ? from + 16 * u : from, max(0, min(16, bytes)));
+          for (uint32_t u = l; u < 32 * kV; u += 32) copy16(slot<E>(at, first + j * kV, u), from + 16 * u);
+          if (l == 0 && shift) copy16(slot<E>(at, first + j * kV, 32 * kV), from + 512 * kV);
+        } else {
+#pragma unroll
+          for (uint32_t u = l; u <= 32 * kV; u += 32) {
+            const int bytes = left - 16 * (int)u;
+            copy16(slot<E>(at, first + j * kV, u), bytes > 0 ? from + 16 * u : from, max(0, min(16, bytes)));
+          }
         }
       }
     }
+  }
+
+  // The 16 bytes `shift` (even, below 16) behind an address on a 16-byte boundary.
+  static __device__ __forceinline__ uint4 moved(const unsigned char* from, uint32_t shift) {
+    uint32_t a[6];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint2 w = *reinterpret_cast<const uint2*>(from + (shift & 8) + 8 * k);
+      a[2 * k] = w.x;
+      a[2 * k + 1] = w.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 5; ++k) a[k] = shift & 4 ? a[k + 1] : a[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = __funnelshift_r(a[k], a[k + 1], shift % 4 * 8);
+    return make_uint4(a[0], a[1], a[2], a[3]);
   }
 
   // Brings what was fetched from an address `shift` above a granule's to its lanes.
@@ -157,6 +179,13 @@ struct Lane {
 #pragma unroll
     for (int j = 0; j < kC; ++j) {
       if ((j * warps + warp) * 256 >= dim) continue;
+      if constexpr (kV == 1) {
+        unsigned char* const to = slot<E>(at, first + j, l);
+        const uint4 w = moved(to, shift);
+        __syncwarp();
+        *reinterpret_cast<uint4*>(to) = w;
+        continue;
+      }
       uint32_t a[4 * kV + 4];
 #pragma unroll
       for (int v = 0; v <= kV; ++v) {
@@ -221,8 +250,11 @@ struct Lane {
 #pragma unroll
     for (uint32_t u = l; u < 32 * kV; u += 32) {
       if ((int)u < lo || (int)u >= hi) continue;
-      uint4 w = *reinterpret_cast<const uint4*>(slot<E>(at, n, u));
-      if (!kWide && shift) {
+      uint4 w;
+      if (kV == 1 && shift) w = moved(slot<E>(at, n, u - 1), 16 - shift);
+      else if (kV == 1) w = pack<E>(x);
+      else w = *reinterpret_cast<const uint4*>(slot<E>(at, n, u));
+      if (!kWide && kV == 2 && shift) {
         const uint4 p = *reinterpret_cast<const uint4*>(slot<E>(at, n, u - 1));
         uint32_t a[8] = {p.x, p.y, p.z, p.w, w.x, w.y, w.z, w.w};
         move_down<E>(a, 16 - shift);
