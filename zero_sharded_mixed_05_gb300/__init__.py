@@ -1045,11 +1045,10 @@ def zero_qk_launch_count(h) -> int:
 # ---------------------------------------------------------------- join of a block with the stream, dropout
 
 # What a handle was made for (dim, dtype, stream dtype, norm_out, gated, drops,
-# device), what its checks compare with, the current stream's getter, and memory for
-# one call's zero_block_buffers (calls on one handle are ordered).
+# device), what its checks compare with, and the current stream's getter.
 _block_handles = {}
-_block_pack = struct.Struct("=26qQqqII").pack_into
-_drop_pack = struct.Struct("=6qiidQqqII").pack_into
+_block_pack = struct.Struct("=26qQqqII").pack     # a zero_block_buffers
+_drop_pack = struct.Struct("=6qiidQqqII").pack    # a zero_drop_buffers
 
 
 def make_block_config(dim, dtype=BF16, stream_dtype=None, norm_branch=False, norm_out=True,
@@ -1066,11 +1065,9 @@ def zero_block_create(cfg: zero_block_config) -> int:
     import torch
     types = (torch.float16, torch.bfloat16, torch.float32)
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
-    b = zero_block_buffers()
     small = ((cfg.dim,), torch.float32, torch.bool, torch.uint8)
     _block_handles[h.value] = (cfg.dim, types[cfg.dtype], types[cfg.stream_dtype], bool(cfg.norm_out),
-                               cfg.gate != GATE_NONE, cfg.dropout > 0, dev, small, _stream_getter(dev), b,
-                               ctypes.addressof(b))
+                               cfg.gate != GATE_NONE, cfg.dropout > 0, dev, small, _stream_getter(dev))
     return h.value
 
 
@@ -1120,7 +1117,7 @@ def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, s
     dropped numbers of a handle with a dropout."""
     if h not in _block_handles:
         raise ValueError("not a handle of zero_block_create")
-    dim, dtype, sdtype, norm, gated, drops, dev, small, current, b, at = _block_handles[h]
+    dim, dtype, sdtype, norm, gated, drops, dev, small, current = _block_handles[h]
     n = x.shape[0]
     shape = (n, dim)
     px = _rows(x, "x", shape, sdtype, dev)
@@ -1133,11 +1130,12 @@ def zero_block_join(h, x, y, x_out, h_out, y_gain, gain, gate=None, mask=None, s
             pxo = _rows(x_out, "x_out", shape, sdtype, dev)
     if norm and h_out is not None:
         ph = _rows(h_out, "h_out", shape, dtype, dev)
-    _block_pack(b, 0, n, *px, *py, *pg, *pxo, *ph, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
-                0 if y_gain is None else _qk_flat(y_gain, "y_gain", small[0], small[1], dev),
-                0 if gain is None else _qk_flat(gain, "gain", small[0], small[1], dev), 0, 0,
-                0 if mask is None else _block_mask(mask, n, small, dev),
-                *(_rng(seed, call, step, dev) if drops else _NO_RNG))
+    at = _block_pack(
+        n, *px, *py, *pg, *pxo, *ph, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+        0 if y_gain is None else _qk_flat(y_gain, "y_gain", small[0], small[1], dev),
+        0 if gain is None else _qk_flat(gain, "gain", small[0], small[1], dev), 0, 0,
+        0 if mask is None else _block_mask(mask, n, small, dev),
+        *(_rng(seed, call, step, dev) if drops else _NO_RNG))
     status = lib().zero_block_join(h, at, current(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "zero_block_join")
@@ -1151,7 +1149,7 @@ def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_
     wanted).  The rng is the forward call's."""
     if h not in _block_handles:
         raise ValueError("not a handle of zero_block_create")
-    dim, dtype, sdtype, norm, gated, drops, dev, small, current, b, at = _block_handles[h]
+    dim, dtype, sdtype, norm, gated, drops, dev, small, current = _block_handles[h]
     n = x_out.shape[0]
     shape = (n, dim)
     px = _rows(x_out, "x_out", shape, sdtype, dev)
@@ -1171,13 +1169,14 @@ def zero_block_join_backward(h, dx_out, dh, x_out, y, dx, dy, dy_gain, dgain, y_
             if dgate is not None:
                 pdg = _rows(dgate, "dgate", shape, dtype, dev)
     cols, f32 = small[0], small[1]
-    _block_pack(b, 0, n, 0, 0, *py, *pg, *px, 0, 0, *pdxo, *pdh, *pdx, *pdy, *pdg,
-                0 if y_gain is None else _qk_flat(y_gain, "y_gain", cols, f32, dev),
-                0 if gain is None else _qk_flat(gain, "gain", cols, f32, dev),
-                0 if dy_gain is None else _qk_flat(dy_gain, "dy_gain", cols, f32, dev),
-                0 if dgain is None else _qk_flat(dgain, "dgain", cols, f32, dev),
-                0 if mask is None else _block_mask(mask, n, small, dev),
-                *(_rng(seed, call, step, dev) if drops else _NO_RNG))
+    at = _block_pack(
+        n, 0, 0, *py, *pg, *px, 0, 0, *pdxo, *pdh, *pdx, *pdy, *pdg,
+        0 if y_gain is None else _qk_flat(y_gain, "y_gain", cols, f32, dev),
+        0 if gain is None else _qk_flat(gain, "gain", cols, f32, dev),
+        0 if dy_gain is None else _qk_flat(dy_gain, "dy_gain", cols, f32, dev),
+        0 if dgain is None else _qk_flat(dgain, "dgain", cols, f32, dev),
+        0 if mask is None else _block_mask(mask, n, small, dev),
+        *(_rng(seed, call, step, dev) if drops else _NO_RNG))
     status = lib().zero_block_join_backward(h, at, current(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "zero_block_join_backward")
@@ -1189,11 +1188,17 @@ def zero_block_launch_count(h) -> int:
     return out.value
 
 
+_drop_dtypes = None
+
+
 def zero_dropout(x, out, p, seed=0, call=0, step=0, stream=None) -> None:
     """Dropout of `x` into `out` (which may be `x`); of a gradient the same call
     with the same `seed`, `call` and `step`.  The last dimension is the row's;
     two dimensions may have any row stride, others are contiguous."""
     import torch
+    global _drop_dtypes
+    if _drop_dtypes is None:
+        _drop_dtypes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
     dev = x.get_device()
     if x.dim() == 2 and out.dim() == 2:
         rows, cols = x.shape
@@ -1204,17 +1209,15 @@ def zero_dropout(x, out, p, seed=0, call=0, step=0, stream=None) -> None:
         rows = x.numel() // cols if cols else 0
         si = so = cols
         rowwise = x.is_contiguous() and out.is_contiguous()
-    dtypes = {torch.float16: FP16, torch.bfloat16: BF16, torch.float32: FP32}
-    if x.dtype not in dtypes or dev < 0 or not rowwise:
+    code = _drop_dtypes.get(x.dtype)
+    if code is None or dev < 0 or not rowwise:
         _qk_refuse("x", "a 16-bit or float32 tensor with contiguous rows on a CUDA device")
     if out.dtype is not x.dtype or out.shape != x.shape or out.get_device() != dev:
         _qk_refuse("out", f"a {x.dtype} tensor of {tuple(x.shape)} on cuda:{dev}")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"x is on cuda:{dev}, which is not the current device")
-    b = zero_drop_buffers()
-    _drop_pack(b, 0, x.data_ptr(), out.data_ptr(), rows, cols, si, so, dtypes[x.dtype], 0, p,
-               *_rng(seed, call, step, dev))
-    status = lib().zero_dropout(ctypes.addressof(b), torch._C._cuda_getCurrentRawStream(dev)
-                                if stream is None else _stream(stream))
+    status = lib().zero_dropout(
+        _drop_pack(x.data_ptr(), out.data_ptr(), rows, cols, si, so, code, 0, p, *_rng(seed, call, step, dev)),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
     if status:
         _check(status, "zero_dropout")
