@@ -312,7 +312,7 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     return ZERO_OK;
   }
 
-  a.y_gain = b->y_gain;
+  a.y_gain = with_y ? b->y_gain : nullptr;   // of zeros a gain would make NaN where it is no number
   a.gain = b->gain;
   a.mask = b->mask;
   a.tokens = b->tokens;
