@@ -38,8 +38,10 @@
  * infinity included) is ignored, its results and gradients are zero and it adds
  * nothing to the gains' gradients.
  *
- * Arithmetic is binary32 throughout (a row's squares have to be within its
- * range: numbers from about 1e-18 to 1e18); results are rounded once, to their
+ * Arithmetic is binary32 throughout.  Of every row the squares have to be within
+ * its range, numbers from about 1e-18 to 1e18: of x', y, dx', dh * gain, and of the
+ * branch behind its norm, z * act(gate), where it has one (products of one with
+ * another then are, whatever each one's size).  Results are rounded once, to their
  * tensor's type; h comes from x' before its rounding.  The gains' gradients are
  * binary32, summed in an order fixed by the shapes and the device, so equal
  * inputs give equal bits.

@@ -20,3 +20,35 @@ def test_the_norm_alone_does_not_see_the_branch_s_gain(z, D, fill):  # noqa: F81
     got = (c.forward()[1], *c.backward(c.x).values())
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     c.close()
+
+
+@pytest.mark.parametrize("D,dtype,layout", [(640, "fp32", "own"), (517, "fp32", "own"), (640, "bf16", "own"),
+                                            (333, "bf16", "odd"), (4104, "bf16", "own"), (4103, "fp32", "own"),
+                                            (8200, "bf16", "own"), (8201, "bf16", "odd")])
+@pytest.mark.parametrize("p", [0.0, 0.1])
+def test_a_gradient_of_rows_of_extreme_sizes(z, monkeypatch, D, dtype, layout, p):  # noqa: F811
+    """x' and y of 2^-56, 1 and 2^56 together, the branch scaled by 2^-10 to 2^10
+    behind its norm: squares are within binary32's range, products of x', dx' and y
+    are not.  dy goes down to 2^-56 2^-56 2^-10 of numbers below one: into bf16's
+    subnormals (below 2^-126), whose half step is 2^-134 whatever the number."""
+    import torch
+    monkeypatch.setattr(R, "EPS", 0.0)
+    sizes = [(a, b, e) for a in (-56, 0, 56) for b in (-56, 0, 56) for e in (-10, 0, 10)]
+    T = len(sizes)
+    c = Case(z, (T, D, dtype, "fp32", True, True, "plain", p, 0.0, layout, 1.0, 1.0, True), 21)
+    z.zero_block_destroy(c.h)
+    cfg = z.make_block_config(D, dtype=z.FP32 if dtype == "fp32" else z.BF16, stream_dtype=z.FP32, norm_branch=True,
+                              gate=z.GATE_PLAIN, eps=0.0, dropout=p)
+    c.h = z.zero_block_create(cfg)
+    sx, sy, sg = (2.0 ** torch.tensor(s, device="cuda", dtype=torch.float32)[:, None] for s in zip(*sizes))
+    c.x.mul_(sx)                   # powers of two: nothing is rounded
+    c.y.mul_(sy.to(c.y.dtype))
+    c.gate.mul_(sg.to(c.gate.dtype))
+    c.dxo.div_(sx)
+    got = c.backward(c.x)
+    out, tol = c.ref().backward(c.x, c.dxo, c.dh)
+    assert all(v.isfinite().all() for v in out.values())
+    if dtype == "bf16":
+        tol["dy"] = tol["dy"] + 2.0 ** -134
+    c.check(got, out, tol)
+    c.close()

@@ -694,7 +694,47 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
       if constexpr (kPost) {
         ry = rsqrtf(__fmaf_rn(s[2], a.inv_dim, a.eps_y));
         const float dot = __fmul_rn(scale, __fmaf_rn(back, __fmul_rn(r, s[5]), __fmaf_rn(r, s[4], s[3])));
-        back_y = __fmul_rn(-ry, __fmul_rn(__fmul_rn(ry, dot), a.inv_dim));
+        float hat = __fmul_rn(ry, dot);
+        // Products of x', dx' and q, which no norm has scaled, may leave binary32's range
+        // though each row's squares do not.  Of rows far from order one the sums are taken
+        // again, of xhat and yhat (all threads of the team see the same r and ry).  Four
+        // chunks in a loop, with the bits made again, which leaves their other registers as
+        // they were.
+        if (!(fminf(r, ry) > 0x1p-20f && fmaxf(r, ry) < 0x1p20f)) {
+          float2 t[3] = {both(0.0f), both(0.0f), both(0.0f)};
+          constexpr int kUnroll = kKeep ? kC : 1;
+#pragma unroll kUnroll
+          for (int j = 0; j < kC; ++j) {
+            float2 v[4], q[4], w[4];
+            uint4 m = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (drops) m = kKeep ? keep[kHas == kBare ? 0 : j] : kept(a.drop, rng_step, block + me.chunk(j));
+            me.template get<T>(at, kY + j * kVecs<T>, q, m);
+            if constexpr (!kKeep) me.gain(a.y_gain, j, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(__fmul2_rn(q[k], both(ry)), kKeep ? yg_[j][k] : w[k]);
+            if (gated) {
+              me.template get<T>(at, kGate + j * kVecs<T>, v);
+              act8<T>(a.gate_kind, v, w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], v[k]);
+              mask8(q, m);
+            }
+            me.template get<S>(at, kDxo + j * kVecs<S>, v, m);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[0] = __ffma2_rn(v[k], q[k], t[0]);
+            me.template get<T>(at, kDh + j * kVecs<T>, v);
+            if constexpr (!kKeep) me.gain(a.gain, j, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[1] = __ffma2_rn(__fmul2_rn(v[k], kKeep ? g_[j][k] : w[k]), q[k], t[1]);
+            me.template get<S>(at, j * kVecs<S>, v);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) t[2] = __ffma2_rn(__fmul2_rn(v[k], both(r)), q[k], t[2]);
+          }
+          float u[3] = {add2(t[0]), add2(t[1]), add2(t[2])};
+          me.template sum<3>(u, s_red, turn);
+          hat = __fmul_rn(scale, __fmaf_rn(back, u[2], __fmaf_rn(r, u[1], u[0])));
+        }
+        back_y = __fmul_rn(-ry, __fmul_rn(hat, a.inv_dim));
       }
 #pragma unroll
       for (int j = 0; j < kC; ++j) {
