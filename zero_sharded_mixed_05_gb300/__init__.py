@@ -898,7 +898,7 @@ def zero_muon_launch_count(h) -> int:
 
 # What a handle was made for, so that the binding can check tensors against it
 # (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, axes or 0,
-# device), the other dtypes, the current stream's getter, and memory for one
+# whether rows are only rotated, device), the other dtypes, the current stream's getter, and memory for one
 # call's zero_qk_buffers (calls on one handle are ordered).
 _qk_handles = {}
 _qk_pack = struct.Struct("=27qii").pack_into
@@ -941,7 +941,8 @@ def zero_qk_create(cfg: zero_qk_config, axes: zero_qk_axes = None) -> int:
     dev = torch.cuda.current_device() if torch.cuda.is_available() else -1
     b = zero_qk_buffers()
     _qk_handles[h.value] = (cfg.q_heads, cfg.k_heads, cfg.head_dim, cfg.rotary_dim // 2, dtype,
-                            bool(cfg.gain_per_head), axes.axes if axes else 0, dev,
+                            bool(cfg.gain_per_head), axes.axes if axes else 0,
+                            axes is not None and not axes.normalise, dev,
                             (torch.float32, torch.int64, torch.int32), _stream_getter(dev), b,
                             ctypes.addressof(b))
     return h.value
@@ -973,6 +974,7 @@ def _qk_flat(t, name, shape, dtype, dev):
 
 
 _NO_HEADS = (0, 0, 0)
+_QK_RESULTS, _QK_GRADIENTS = ("q_out", "k_out"), ("dq_out", "dk_out")
 
 
 def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gain, cos, sin,
@@ -980,10 +982,13 @@ def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gai
     """Check the tensors against the handle and make the call."""
     if h not in _qk_handles:
         raise ValueError("not a handle of zero_qk_create")
-    hq, hk, dim, half, dtype, per_head, axes, dev, (f32, i64, i32), current, b, at = _qk_handles[h]
-    n = q.shape[0]
+    hq, hk, dim, half, dtype, per_head, axes, alone, dev, (f32, i64, i32), current, b, at = _qk_handles[h]
+    alone = alone and names is _QK_GRADIENTS       # a rotation back looks at neither q nor k
+    if not alone and (q is None or (hk and k is None)):
+        _qk_refuse("q" if q is None else "k", "given")
+    n = (qo if alone else q).shape[0]
     shape = (n, hq, dim)
-    tq = _qk_heads(q, "q", shape, dtype, dev)
+    tq = _NO_HEADS if alone else _qk_heads(q, "q", shape, dtype, dev)
     tqo = _qk_heads(qo, names[0], shape, dtype, dev)
     tdq = _NO_HEADS if dq is None else _qk_heads(dq, "dq", shape, dtype, dev)
     shape = (hq, dim) if per_head else (dim,)
@@ -993,7 +998,8 @@ def _qk_call(fn, h, names, q, k, qo, ko, dq, dk, q_gain, k_gain, dq_gain, dk_gai
     gk = dgk = 0
     if hk:
         shape = (n, hk, dim)
-        tk = _qk_heads(k, "k", shape, dtype, dev)
+        if not alone:
+            tk = _qk_heads(k, "k", shape, dtype, dev)
         tko = _qk_heads(ko, names[1], shape, dtype, dev)
         if dk is not None:
             tdk = _qk_heads(dk, "dk", shape, dtype, dev)
@@ -1023,7 +1029,7 @@ def zero_qk_norm_rope(h, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions
     at by a handle with k_heads 0; a gain may be None (ones).  `positions` is
     [tokens], or [axes, tokens] of a handle with axes; a token of position -1 (on
     any axis) is padding and gets zeros."""
-    _qk_call(lib().zero_qk_norm_rope, h, ("q_out", "k_out"), q, k, q_out, k_out, None, None, q_gain,
+    _qk_call(lib().zero_qk_norm_rope, h, _QK_RESULTS, q, k, q_out, k_out, None, None, q_gain,
              k_gain, None, None, cos, sin, positions, stream)
 
 
@@ -1031,8 +1037,9 @@ def zero_qk_norm_rope_backward(h, dq_out, dk_out, q, k, dq, dk, dq_gain, dk_gain
                                cos, sin, positions, stream=None) -> None:
     """Gradients of `zero_qk_norm_rope`: from `dq_out`, `dk_out` and the
     forward call's inputs into `dq`, `dk` (which may be `dq_out`, `dk_out`) and
-    the gains' float32 gradients (None: not wanted)."""
-    _qk_call(lib().zero_qk_norm_rope_backward, h, ("dq_out", "dk_out"), q, k, dq_out, dk_out, dq, dk,
+    the gains' float32 gradients (None: not wanted).  A handle without the norm
+    does not look at `q` and `k`, which may be None."""
+    _qk_call(lib().zero_qk_norm_rope_backward, h, _QK_GRADIENTS, q, k, dq_out, dk_out, dq, dk,
              q_gain, k_gain, dq_gain, dk_gain, cos, sin, positions, stream)
 
 

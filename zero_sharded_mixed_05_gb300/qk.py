@@ -59,14 +59,16 @@ class _Apply(torch.autograd.Function):
         k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
         zero_qk_norm_rope(owner._handle, q, k, q_out, k_out, q_gain, k_gain, cos, sin, positions)
         ctx.owner = owner          # the handle is there for the backward pass
-        ctx.save_for_backward(q, k, q_gain, k_gain, cos, sin, positions)
+        # a rotation back needs neither queries nor keys
+        rows = (q, k) if owner._normalise else (None, None)
+        ctx.save_for_backward(*rows, q_gain, k_gain, cos, sin, positions)
         return q_out, k_out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, cos, sin, positions = ctx.saved_tensors
-        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k))
+        dq, dk = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (dq_out, dk_out))
         dqg, dkg = (torch.empty_like(gain) if wanted else None
                     for gain, wanted in zip((q_gain, k_gain), ctx.needs_input_grad[3:5]))
         zero_qk_norm_rope_backward(ctx.owner._handle, dq_out.contiguous(), dk_out.contiguous(), q, k, dq,
@@ -84,12 +86,14 @@ class QkNormRope:
     def __init__(self, cfg, axes=None):
         if cfg.k_heads < 1:
             raise ValueError("QkNormRope takes queries and keys")
+        self._normalise = axes is None or bool(axes.normalise)
         self._handle = zero_qk_create(cfg) if axes is None else zero_qk_create(cfg, axes)
 
     def __call__(self, q, k, q_gain, k_gain, cos, sin, positions):
         """q [tokens, q_heads, D] and k [tokens, k_heads, D] (heads contiguous),
         binary32 gains (None: ones), tables and positions as `zero_qk_norm_rope`
-        takes them.  A gain that requires no gradient costs no sums."""
+        takes them.  A gain that requires no gradient costs no sums.  Without the
+        norm the backward pass keeps neither q nor k, which may be overwritten."""
         return _Apply.apply(self, q, k, q_gain, k_gain, cos, sin, positions)
 
     def close(self):
