@@ -42,7 +42,9 @@
  * its range, numbers from about 1e-18 to 1e18: of x', y, dx', dh * gain, and of the
  * branch behind its norm, z * act(gate), where it has one (products of one with
  * another then are, whatever each one's size).  Results are rounded once, to their
- * tensor's type; h comes from x' before its rounding.  The gains' gradients are
+ * tensor's type; h comes from x' before its rounding.  A sigmoid is within 10 2^-24 of
+ * itself, but where only 16-bit numbers and the gains' gradients come of it: there up
+ * to (10 + 2.4 |gate|) 2^-24.  The gains' gradients are
  * binary32, summed in an order fixed by the shapes and the device, so equal
  * inputs give equal bits.
  *

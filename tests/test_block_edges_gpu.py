@@ -52,3 +52,21 @@ def test_a_gradient_of_rows_of_extreme_sizes(z, monkeypatch, D, dtype, layout, p
         tol["dy"] = tol["dy"] + 2.0 ** -134
     c.check(got, out, tol)
     c.close()
+
+
+@pytest.mark.parametrize("D,layout", [(64, "own"), (61, "odd"), (4104, "own")])
+def test_a_gate_beside_a_binary32_stream(z, D, layout):  # noqa: F811
+    """The branch alone (x = 0) as the stream has it.  With e = exp(-|g|), in halves of
+    a unit in the last place (2^-24): e within four, 1 + e one, its reciprocal four, the
+    product of both one; the product with y y_gain one and that one itself one: 12 2^-24
+    of the branch, to first order."""
+    import torch
+    T = 500
+    c = Case(z, (T, D, "fp16", "fp32", False, True, "sigmoid", 0.0, 0.0, layout, 1.0, 1.0, True), 22)
+    c.x.zero_()
+    g = torch.Generator(device="cuda").manual_seed(22)
+    c.gate.copy_(14 * (2 * torch.rand(T, D, device="cuda", generator=g) - 1))
+    xo, _ = c.forward()
+    ref = c.y.double() * c.y_gain.double() * torch.sigmoid(c.gate.double())
+    assert ((xo.double() - ref).abs() <= 12.1 * R.E32 * ref.abs()).all()
+    c.close()

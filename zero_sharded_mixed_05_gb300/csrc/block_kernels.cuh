@@ -344,24 +344,29 @@ struct Lane {
 
 // The gate's factor, in place, and the factor's derivative.  The sigmoid by
 // e = exp(-|g|), so that neither it nor its derivative e / (1 + e)^2 is a
-// difference of nearly equal numbers.  For 16-bit data e is the quick exponential,
-// 2 + 1.2 |g| units in the last place of binary32 off at most, which is far below
-// those types' steps wherever e counts beside 1.
-template <typename T>
+// difference of nearly equal numbers.  W is the widest type that the factor counts
+// in: forward the stream's, backward the block's.  Where that has 16 bits e is the quick
+// exponential, 2 + 1.2 |g| units in the last place of binary32 off at most, which is
+// far below those types' steps wherever e counts beside 1 (and, in y_gain's gradient,
+// below the errors of its sum over the tokens, but for gates far below zero).  16-bit
+// blocks on a binary32 stream have the exact one and the quick reciprocal, two units off
+// at most (8,192 rows of 4096 in bf16 on a binary32 stream, forward: 79 us with both
+// quick, 81 so, 93 with the rounded reciprocal).
+template <typename T, typename W>
 __device__ __forceinline__ float sigmoid(float g, float* slope) {
-  const float e = sizeof(T) == 2 ? __expf(-fabsf(g)) : expf(-fabsf(g));
+  const float e = sizeof(W) == 2 ? __expf(-fabsf(g)) : expf(-fabsf(g));
   const float inv = sizeof(T) == 2 ? __fdividef(1.0f, __fadd_rn(1.0f, e)) : __frcp_rn(__fadd_rn(1.0f, e));
   const float low = __fmul_rn(e, inv);
   *slope = __fmul_rn(low, inv);
   return g >= 0.0f ? inv : low;
 }
 
-template <typename T>
+template <typename T, typename W>
 __device__ __forceinline__ void act8(int kind, float2* g, float2* slope) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (kind == ZERO_GATE_SIGMOID)
-      g[k] = make_float2(sigmoid<T>(g[k].x, &slope[k].x), sigmoid<T>(g[k].y, &slope[k].y));
+      g[k] = make_float2(sigmoid<T, W>(g[k].x, &slope[k].x), sigmoid<T, W>(g[k].y, &slope[k].y));
     else
       slope[k] = both(1.0f);
   }
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kMost, kMost == 256 ? 3 : kWide || (kC > 1 && 
         if (gated) {
           float2 g[4], slope[4];
           me.template get<T>(at, kGate + j * kVecs<T>, g);
-          act8<T>(a.gate_kind, g, slope);
+          act8<T, S>(a.gate_kind, g, slope);
 #pragma unroll
           for (int k = 0; k < 4; ++k) b[k] = __fmul2_rn(b[k], g[k]);
         }
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           if (gated) {
             float2 g[4], slope[4];
             me.template get<T>(at, kGate + j * kVecs<T>, g);
-            act8<T>(a.gate_kind, g, slope);
+            act8<T, T>(a.gate_kind, g, slope);
 #pragma unroll
             for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], g[k]);
             if (drops) mask8(q, keep[kHas == kBare ? 0 : j]);
@@ -714,7 +719,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
             for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(__fmul2_rn(q[k], both(ry)), kKeep ? yg_[j][k] : w[k]);
             if (gated) {
               me.template get<T>(at, kGate + j * kVecs<T>, v);
-              act8<T>(a.gate_kind, v, w);
+              act8<T, T>(a.gate_kind, v, w);
 #pragma unroll
               for (int k = 0; k < 4; ++k) q[k] = __fmul2_rn(q[k], v[k]);
               mask8(q, m);
@@ -761,7 +766,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_backward_kernel(const __gri
           else me.template get<T>(at, kY + j * kVecs<T>, yv);
           if (gated) {
             me.template get<T>(at, kGate + j * kVecs<T>, g);
-            act8<T>(a.gate_kind, g, slope);
+            act8<T, T>(a.gate_kind, g, slope);
           }
           if constexpr (!kKeep) me.gain(a.y_gain, j, w);
 #pragma unroll
