@@ -70,3 +70,21 @@ def test_a_gate_beside_a_binary32_stream(z, D, layout):  # noqa: F811
     ref = c.y.double() * c.y_gain.double() * torch.sigmoid(c.gate.double())
     assert ((xo.double() - ref).abs() <= 12.1 * R.E32 * ref.abs()).all()
     c.close()
+
+
+@pytest.mark.parametrize("eps", [1e-12, 1e-30, 1e-44, 1e-50, 1e-300])
+@pytest.mark.parametrize("D", [64, 61])
+def test_rows_of_zeros_by_any_eps(z, D, eps):  # noqa: F811
+    """Zero over the root of any eps that is not zero is zero, of both norms; and
+    the gradient of such rows is dx' for the stream, as no term of the norm's is
+    with dh = 0."""
+    import torch
+    h = z.zero_block_create(z.make_block_config(D, dtype=z.FP32, norm_branch=True, eps=eps))
+    x = torch.zeros(9, D, device="cuda")
+    xo, ho = torch.ones_like(x), torch.ones_like(x)
+    z.zero_block_join(h, x, x, xo, ho, None, None)
+    assert not xo.any() and not ho.any()
+    dx, dxo, dh = torch.zeros_like(x), torch.randn_like(x), torch.zeros_like(x)
+    z.zero_block_join_backward(h, dxo, dh, xo, x, dx, None, None, None, None, None)
+    assert torch.equal(dx, dxo)
+    z.zero_block_destroy(h)

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
+#include <limits>
 #include <mutex>
 #include <new>
 
@@ -320,7 +321,8 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.dim = c.dim;
   a.chunks = (c.dim + 7) / 8;
   a.gate_kind = c.gate;
-  a.eps = a.eps_y = (float)c.eps;
+  // (an eps below binary32's smallest number still makes zero of a row of zeros)
+  a.eps = a.eps_y = c.eps > 0.0 ? std::max((float)c.eps, std::numeric_limits<float>::denorm_min()) : 0.0f;
   a.inv_dim = 1.0f / (float)c.dim;
   a.alpha = with_y ? (float)c.alpha : 1.0f;
   a.beta = (float)c.beta;

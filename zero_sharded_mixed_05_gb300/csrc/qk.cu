@@ -15,6 +15,7 @@
 
 #include <algorithm>
 #include <cstdlib>
+#include <limits>
 #include <mutex>
 #include <new>
 
@@ -192,7 +193,8 @@ zero_status run(zero_qk_t h, const zero_qk_buffers* b, void* stream, bool backwa
   a.rot = c.rotary_dim;
   a.gain_per_head = c.gain_per_head;
   a.heads = c.q_heads + c.k_heads;
-  a.eps = (float)c.eps;
+  // (an eps below binary32's smallest number still makes zero of a row of zeros)
+  a.eps = c.eps > 0.0 ? std::max((float)c.eps, std::numeric_limits<float>::denorm_min()) : 0.0f;
   a.inv_dim = 1.0f / (float)c.head_dim;
   const int es = elem_size(c.dtype);
   // The widest vector that the head's halves, every address and every stride
