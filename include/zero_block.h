@@ -114,7 +114,7 @@ typedef struct zero_block_buffers {
   zero_block_rows dh;       /* backward: gradient of h (NULL: zero)           */
   zero_block_rows dx, dy, dgate; /* backward: results (NULL: not wanted)      */
   const float* y_gain;      /* device fp32 [D]; NULL: ones.  Ignored without y */
-  const float* gain;        /* device fp32 [D]; NULL: ones                    */
+  const float* gain;        /* device fp32 [D]; NULL: ones.  Ignored without h or dh */
   float* dy_gain;           /* backward: device fp32 [D]; NULL: not wanted    */
   float* dgain;             /* backward: device fp32 [D]; NULL: not wanted    */
   const uint8_t* mask;      /* device [T]; NULL: every token counts           */

@@ -88,3 +88,20 @@ def test_rows_of_zeros_by_any_eps(z, D, eps):  # noqa: F811
     z.zero_block_join_backward(h, dxo, dh, xo, x, dx, None, None, None, None, None)
     assert torch.equal(dx, dxo)
     z.zero_block_destroy(h)
+
+
+@pytest.mark.parametrize("D", [512, 517])
+@pytest.mark.parametrize("norm_out", [False, True])
+def test_a_gain_that_nothing_is_scaled_by_is_not_seen(z, D, norm_out):  # noqa: F811
+    """Without norm_out there is no h for it, and without a gradient of h it has no
+    part in those of x and y."""
+    import torch
+    c = Case(z, (300, D, "bf16", "bf16", True, norm_out, "none", 0.1, 0.2, "own", 1.5, 1.0, True), 23)
+    results = []
+    for c.gain in (None, torch.full((D,), float("nan"), device="cuda")):
+        xo = c.like("bf16")
+        if not norm_out:
+            z.zero_block_join(c.h, c.x, c.y, xo, None, c.y_gain, c.gain, **c.kw)
+        results.append((xo, *c.backward(c.x, dh=None).values()))
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    c.close()

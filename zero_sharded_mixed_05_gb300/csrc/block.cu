@@ -313,8 +313,9 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     return ZERO_OK;
   }
 
-  a.y_gain = with_y ? b->y_gain : nullptr;   // of zeros a gain would make NaN where it is no number
-  a.gain = b->gain;
+  // (of zeros a gain would make NaN where it is no number)
+  a.y_gain = with_y ? b->y_gain : nullptr;
+  a.gain = (backward ? a.dh.data : a.h.data) ? b->gain : nullptr;
   a.mask = b->mask;
   a.tokens = b->tokens;
   a.drop = zo::drop_of(b->rng, with_y ? c.dropout : 0.0);
