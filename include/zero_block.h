@@ -118,7 +118,7 @@ typedef struct zero_block_buffers {
   float* dy_gain;           /* backward: device fp32 [D]; NULL: not wanted    */
   float* dgain;             /* backward: device fp32 [D]; NULL: not wanted    */
   const uint8_t* mask;      /* device [T]; NULL: every token counts           */
-  zero_rng rng;             /* looked at with dropout > 0                     */
+  zero_rng rng;             /* looked at with dropout > 0 and y               */
 } zero_block_buffers;
 
 /* Errors: EINVAL (NULL pointers, a field outside the ranges above); ENOMEM;

@@ -269,6 +269,11 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     if (with_y) a.x_out = row_of(b->x_out, ss);
     if (c.norm_out) a.h = row_of(b->h, es);
   }
+  // (of zeros a gain would make NaN where it is no number)
+  a.y_gain = with_y ? b->y_gain : nullptr;
+  a.gain = (backward ? a.dh.data : a.h.data) ? b->gain : nullptr;
+  float* const dgain[2] = {backward ? b->dy_gain : nullptr, backward ? b->dgain : nullptr};
+  const bool want = dgain[0] || dgain[1], drops = with_y && c.dropout > 0.0;
   const struct {
     JoinRow* r;
     const char* name;
@@ -291,9 +296,10 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
       if (r.result && b->tokens > 1 && std::abs(r.r->stride) < (int64_t)c.dim * r.size)
         return fail(ZERO_EINVAL, "rows of %s lie on one another", r.name);
     }
-    for (const void* p : {(const void*)b->y_gain, (const void*)b->gain, (const void*)b->dy_gain, (const void*)b->dgain})
+    for (const void* p : {(const void*)a.y_gain, (const void*)a.gain, (const void*)dgain[0], (const void*)dgain[1]})
       if (reinterpret_cast<uintptr_t>(p) % 4) return fail(ZERO_EINVAL, "a gain is misaligned");
-    if (reinterpret_cast<uintptr_t>(b->rng.step_dev) % 8) return fail(ZERO_EINVAL, "step_dev is misaligned");
+    if (drops && reinterpret_cast<uintptr_t>(b->rng.step_dev) % 8)
+      return fail(ZERO_EINVAL, "step_dev is misaligned");
   }
   if (!h->has_device) return fail(ZERO_ECUDA, "no CUDA device for this handle");
   int cur = -1;
@@ -302,8 +308,6 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   if (cur != h->device)
     return fail(ZERO_ECUDA, "current device %d is not the handle's device %d", cur, h->device);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  float* dgain[2] = {backward ? b->dy_gain : nullptr, backward ? b->dgain : nullptr};
-  const bool want = dgain[0] || dgain[1];
   if (b->tokens == 0) {
     for (float* g : dgain)
       if (g) {
@@ -313,12 +317,9 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
     return ZERO_OK;
   }
 
-  // (of zeros a gain would make NaN where it is no number)
-  a.y_gain = with_y ? b->y_gain : nullptr;
-  a.gain = (backward ? a.dh.data : a.h.data) ? b->gain : nullptr;
   a.mask = b->mask;
   a.tokens = b->tokens;
-  a.drop = zo::drop_of(b->rng, with_y ? c.dropout : 0.0);
+  a.drop = zo::drop_of(b->rng, drops ? c.dropout : 0.0);
   a.dim = c.dim;
   a.chunks = (c.dim + 7) / 8;
   a.gate_kind = c.gate;
