@@ -30,3 +30,23 @@ def test_what_a_call_does_not_use_is_not_checked(z, backward, name, over, drop_y
         setattr(b, name, 0x100002)
     assert _calls(z, backward)(h, ctypes.byref(b), None) == z.ZERO_ECUDA
     z.zero_block_destroy(h)
+
+
+def test_integers_of_any_kind_choose_the_numbers(z):  # noqa: F811
+    """numpy's and others that index: what is refused is what is no integer, and by
+    the binding's own error."""
+    import numpy as np
+    import torch
+    h = z.zero_block_create(z.make_block_config(64, dtype=z.FP32, dropout=0.1))
+    t = torch.zeros(3, 64)
+    try:
+        for seed, call, step in ((np.int64(5), np.uint32(7), np.int64(9)), (True, False, True),
+                                 (torch.tensor(3), torch.tensor(4), 5), (2 ** 64 - 1, 2 ** 32 - 1, -2 ** 63)):
+            with pytest.raises(z.ZeroOptError):       # nothing wrong but the missing device
+                z.zero_block_join(h, t, t, t, t, None, None, seed=seed, call=call, step=step)
+        for bad in (dict(seed=1.0), dict(call=1.5), dict(step=2.0), dict(step="1"), dict(seed=None), dict(step=None),
+                    dict(call=np.float32(1)), dict(step=np.int64(3) + 0.5)):
+            with pytest.raises(ValueError):
+                z.zero_block_join(h, t, t, t, t, None, None, **bad)
+    finally:
+        z.zero_block_destroy(h)

@@ -13,6 +13,7 @@ Build the library with ``zero_sharded_mixed_05_gb300._build.build()`` (or
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import struct
 
@@ -1092,18 +1093,29 @@ def _rows(t, name, shape, dtype, dev):
     _qk_refuse(name, f"a {dtype} tensor of {shape} with contiguous rows on cuda:{dev}")
 
 
+def _integer(v, name):
+    try:
+        return operator.index(v)
+    except TypeError:
+        raise ValueError(f"{name} must be an integer") from None
+
+
 def _rng(seed, call, step, dev):
     """The last fields of a call: (seed, step, address of a step on the device, call, 0)."""
+    if type(seed) is not int or type(call) is not int:
+        seed, call = _integer(seed, "seed"), _integer(call, "call")
     if not 0 <= seed < 2 ** 64 or not 0 <= call < 2 ** 32:
         raise ValueError("seed must be in 0..2^64-1 and call in 0..2^32-1")
-    if type(step) is int:
-        if not -2 ** 63 <= step < 2 ** 63:
-            raise ValueError("step must be a 64-bit integer")
-        return seed, step, 0, call, 0
-    import torch
-    if step.dtype is not torch.int64 or step.numel() != 1 or step.get_device() != dev:
-        _qk_refuse("step", f"an integer or a torch.int64 tensor of one number on cuda:{dev}")
-    return seed, 0, step.data_ptr(), call, 0
+    if type(step) is not int:
+        import torch
+        if isinstance(step, torch.Tensor):
+            if step.dtype is not torch.int64 or step.numel() != 1 or step.get_device() != dev:
+                _qk_refuse("step", f"an integer or a torch.int64 tensor of one number on cuda:{dev}")
+            return seed, 0, step.data_ptr(), call, 0
+        step = _integer(step, "step")
+    if not -2 ** 63 <= step < 2 ** 63:
+        raise ValueError("step must be a 64-bit integer")
+    return seed, step, 0, call, 0
 
 
 _NO_ROWS = (0, 0)
