@@ -89,7 +89,7 @@ typedef struct zero_block_config {
   int32_t gate;             /* ZERO_GATE_*                                    */
   int32_t reserved[2];
   double eps;               /* >= 0, added to the mean squares                */
-  double alpha, beta;       /* finite; of the stream and of the branch        */
+  double alpha, beta;       /* finite in binary32; of the stream and of the branch */
   double dropout;           /* p: 0..1                                        */
 } zero_block_config;
 

@@ -50,3 +50,15 @@ def test_integers_of_any_kind_choose_the_numbers(z):  # noqa: F811
                 z.zero_block_join(h, t, t, t, t, None, None, **bad)
     finally:
         z.zero_block_destroy(h)
+
+
+@pytest.mark.parametrize("field,value", [("alpha", 1e39), ("beta", -1e39), ("alpha", 1e308), ("beta", 3.5e38)])
+def test_factors_that_binary32_does_not_hold_are_refused(z, field, value):  # noqa: F811
+    """They would be infinities in the kernels."""
+    cfg = z.make_block_config(**GOOD)
+    setattr(cfg, field, value)
+    h = ctypes.c_void_p(123)
+    assert z.lib().zero_block_create(ctypes.byref(cfg), ctypes.byref(h)) == z.ZERO_EINVAL and h.value is None
+    setattr(cfg, field, 3.4e38)
+    assert z.lib().zero_block_create(ctypes.byref(cfg), ctypes.byref(h)) == z.ZERO_OK
+    z.lib().zero_block_destroy(h)

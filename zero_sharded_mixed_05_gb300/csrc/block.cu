@@ -420,8 +420,9 @@ zero_status zero_block_create(const zero_block_config* cfg, zero_block_t* out) {
   if (cfg->gate < ZERO_GATE_NONE || cfg->gate > ZERO_GATE_SIGMOID)
     return fail(ZERO_EINVAL, "gate must be a ZERO_GATE_*");
   if (!(cfg->eps >= 0.0) || !std::isfinite(cfg->eps)) return fail(ZERO_EINVAL, "eps must be >= 0");
-  if (!std::isfinite(cfg->alpha) || !std::isfinite(cfg->beta))
-    return fail(ZERO_EINVAL, "alpha and beta must be finite");
+  constexpr double kLargest = std::numeric_limits<float>::max();
+  if (!(std::fabs(cfg->alpha) <= kLargest && std::fabs(cfg->beta) <= kLargest))
+    return fail(ZERO_EINVAL, "alpha and beta must be finite in binary32");
   if (!(cfg->dropout >= 0.0 && cfg->dropout <= 1.0)) return fail(ZERO_EINVAL, "dropout must be in 0..1");
   zero_block_handle* h = new (std::nothrow) zero_block_handle;
   if (!h) return fail(ZERO_ENOMEM, "handle allocation failed");
