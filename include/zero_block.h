@@ -44,9 +44,11 @@
  * another then are, whatever each one's size).  Results are rounded once, to their
  * tensor's type; h comes from x' before its rounding.  A sigmoid is within 10 2^-24 of
  * itself, but where only 16-bit numbers and the gains' gradients come of it: there up
- * to (10 + 2.4 |gate|) 2^-24.  The gains' gradients are
- * binary32, summed in an order fixed by the shapes and the device, so equal
- * inputs give equal bits.
+ * to (10 + 2.4 |gate|) 2^-24.  The gains' gradients are binary32.  Sums, over a row's
+ * numbers and over tokens, are taken in an order fixed by the shapes, the device, which
+ * tensors are given, and whether all their rows begin on 16-byte boundaries; so equal
+ * inputs in an equal layout give equal bits, and in another layout results within the
+ * arithmetic's errors of them.
  *
  * Conventions are those of zero_opt.h: a zero_status from every call,
  * arguments checked before any CUDA work, device buffers owned by the caller,

@@ -24,8 +24,11 @@
  *
  * Arithmetic is binary32 throughout (a row's squares have to be within its
  * range: numbers from about 1e-18 to 1e18); results are rounded once, to the
- * data's type.  The gains' gradients are binary32, summed in an order fixed by the
- * shapes and the device, so equal inputs give equal bits.
+ * data's type.  The gains' gradients are binary32.  Sums, over a row's numbers and over
+ * tokens, are taken in an order fixed by the shapes, the device and the widest vector
+ * (16 bytes down to one number) that all addresses and strides are multiples of; so
+ * equal inputs in an equal layout give equal bits, and in another layout results within
+ * the arithmetic's errors of them.
  *
  * Conventions are those of zero_opt.h: a zero_status from every call,
  * arguments checked before any CUDA work, device buffers owned by the caller,
