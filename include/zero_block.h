@@ -32,7 +32,10 @@
  * 65536 / (65536 - c), and is zero otherwise, whatever it held (p is taken to
  * the nearest 65536th; at 1 everything is zero).  No mask is stored: the backward
  * pass makes the same bits from the same zero_rng, so a program gives each
- * dropout of a step its own `call`, and each step its own `step`.
+ * dropout of a step its own `call`, and each step its own `step`.  Every call's rows
+ * are counted from 0: the micro-batches of a step, and the shards that ranks have of a
+ * batch or of a sequence, drop the same places unless each has a `seed` or `call` of its
+ * own, and no call makes the bits that a part of a larger tensor's rows would get.
  *
  * A token whose mask byte is zero is padding: what its inputs hold (NaN and
  * infinity included) is ignored, its results and gradients are zero and it adds

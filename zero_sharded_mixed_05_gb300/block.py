@@ -9,6 +9,9 @@ error).
 A program gives each dropout of a step its own `call`, and each step its own
 `step`: an integer, or, for a captured step, an int64 tensor on the device that
 every replay reads (and that stays as it is until the backward pass is done).
+A call counts its rows from 0: micro-batches of one step, and ranks that have a
+shard of the batch or of the sequence, drop the same places unless each is given
+a `seed` (or `call`) of its own, as seed + rank.
 
 For a step captured in a CUDA graph hold to what torch asks of any captured
 backward pass: no autograd graph of the same leaves, made outside the capture,
