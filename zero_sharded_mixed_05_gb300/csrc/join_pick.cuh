@@ -17,10 +17,11 @@ const void* join_of(bool backward, bool post) {
 
 template <typename T, typename S, int kC>
 const void* join_of(const JoinPick& p) {
-  if (!p.backward && kC == 2 && !p.large)
-    return p.has == kBare   ? join_of<T, S, kC, true, kBare, 256>(false, p.post)
-           : p.has == kDrop ? join_of<T, S, kC, true, kDrop, 256>(false, p.post)
-                            : join_of<T, S, kC, true, kGated, 256>(false, p.post);
+  if constexpr (kC == 2)
+    if (!p.backward && !p.large)
+      return p.has == kBare   ? join_of<T, S, kC, true, kBare, 256>(false, p.post)
+             : p.has == kDrop ? join_of<T, S, kC, true, kDrop, 256>(false, p.post)
+                              : join_of<T, S, kC, true, kGated, 256>(false, p.post);
   return p.has == kBare   ? join_of<T, S, kC, true, kBare>(p.backward, p.post)
          : p.has == kDrop ? join_of<T, S, kC, true, kDrop>(p.backward, p.post)
                           : join_of<T, S, kC, true, kGated>(p.backward, p.post);
@@ -32,12 +33,14 @@ const void* shifted_join_of(const JoinPick& p) {
                         : join_of<T, S, kC, false, kGated, kMost>(p.backward, p.post);
 }
 
-// Long rows have one kernel for all that a branch may have.
+// Long rows, which binary32 blocks have not, have one kernel for all that a branch may
+// have.
 template <typename T, typename S>
 const void* join_of(const JoinPick& p) {
-  if (p.chunks == 4)
-    return p.wide ? join_of<T, S, 4, true, kGated>(p.backward, p.post)
-                  : join_of<T, S, 4, false, kGated>(p.backward, p.post);
+  if constexpr (sizeof(T) == 2)
+    if (p.chunks == 4)
+      return p.wide ? join_of<T, S, 4, true, kGated>(p.backward, p.post)
+                    : join_of<T, S, 4, false, kGated>(p.backward, p.post);
   if (!p.wide)
     return p.chunks == 1           ? shifted_join_of<T, S, 1, kJoinThreads>(p)
            : p.large || p.backward ? shifted_join_of<T, S, 2, kJoinThreads>(p)
