@@ -351,6 +351,11 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   a.teams = std::max(1, 8 / a.warps);
   a.teams = (int)std::min<int64_t>(a.teams, (b->tokens + h->sms - 1) / h->sms);
   const int threads = a.teams * a.warps * 32;
+  // Shifted rows in CTAs of up to 320 threads (4097 to 5120 numbers forward) have a kernel
+  // of fewer registers, two CTAs of which fit an SM: 4,000 rows of 4097 in bf16 45 us
+  // against 63 with the other's one, of 5119 with a dropout 61 against 82.  From 4609
+  // numbers without a dropout the rule below leaves one CTA in any case, and it loses: 70
+  // against 66, at 5119 73 against 68.
   const zo::JoinPick pick = {backward, wide, with_y && c.norm_branch, with_gate ? 2 : a.drop.cut > 0 ? 1 : 0, cs,
                              threads > (wide ? 256 : 320)};
   const void* fn = c.dtype == ZERO_FP32   ? zo::join_float(pick)
@@ -365,7 +370,11 @@ zero_status run(zero_block_t h, const zero_block_buffers* b, void* stream, bool 
   // rows each 81 us, three 92; with both norms 84, 91, three CTAs of two rows 92;
   // backward 131 and 143, and without the branch's norm, whose rows are done sooner,
   // one CTA of three rows 125, two of two 142).  A dropout's integer work wants more
-  // CTAs (95 us with three, 104 with two).
+  // CTAs (95 us with three, 104 with two).  The constants were found at 4096 and count
+  // whole rows: from 4097 numbers on (4609 forward) the room is for three rows, which is
+  // one CTA with three.  What that gives of the copy rate, forward and backward, with
+  // both norms: 4096 93 and 94 %, 5120 85 and 84, 6144 93 and 94, 7168 96 and 92, 8192 94
+  // and 89; without the branch's norm 97 and 99, at 5120 94 and 92, at 7168 87 and 85.
   const int numbers = backward ? (pick.post || pick.has ? 16384 : 12288) : pick.has ? 24576 : 18432;
   int slots = std::max(1, numbers / (a.teams * c.dim));
   int ctas = std::max(1, std::min(h->resident(fn, threads, 2 * row), slots / 2));

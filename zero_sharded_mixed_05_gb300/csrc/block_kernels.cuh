@@ -3,12 +3,15 @@
 //
 // What bounds it: memory.  Each row is read once and each result written once;
 // sums over a row are taken by the threads that hold it.  Measured on the device,
-// 16,384 rows of 4096 in bf16: forward 81 us (98 % of the copy rate), with a norm of
-// the branch 84 (94 %: two sums over the team a row, one after the other), backward 120
-// and 129 (99 and 92 %, with the sums of the gains' gradients).  A dropout costs some
-// 15 integer instructions a number (95 us forward, 152 backward with both norms, at two
-// thirds of the issue slots), a gate's sigmoid and its derivative about as much (8,192
-// rows backward 120 us, 66 %).  One row takes 2.8 us, backward 5.9 with its second kernel.
+// 16,384 rows of 4096 in bf16: forward 82 us (97 % of the copy rate), with a norm of
+// the branch 85 (93 %: two sums over the team a row, one after the other), backward 120
+// and 126 (99 and 94 %, with the sums of the gains' gradients).  A dropout costs some
+// 13 integer instructions a number (95 us forward, 152 backward with both norms, at two
+// thirds of the issue slots).  A gate's sigmoid and its derivative cost less forward
+// (8,192 rows 56 us, 89 %) than backward, where both are made twice (120 us, 66 %).
+// Binary32, 8,192 rows: 93 us (86 %) and 139 (86 %).  Long rows have one CTA of sixteen
+// warps an SM, and backward their registers spill: 2,048 rows of 16,384 in bf16 67 us
+// (60 %) and 137 (43 %).  One row takes 2.8 us, backward 5.9 with its second kernel.
 //
 // Layout: a row of D numbers is cut into chunks of eight, and a team of whole
 // warps takes a row at a time: thread i of n holds chunks i, i + n, ... (kC at
@@ -23,8 +26,10 @@
 // lie in are copied, and a warp's lanes shift what they hold to where it belongs
 // once it is there; results are shifted the other way, so that all but the ends of
 // a warp's 256 numbers are written 16 bytes at a time (4,000 rows of 4097 in bf16 with
-// both norms: 45 us forward, 95 backward, 43 and 30 % of the copy rate; number by
-// number 76 and 171.  The shifts' selects bound them).
+// both norms: 45 us forward, 96 backward, 43 and 30 % of the copy rate; number by
+// number 76 and 171.  They take 56 and 86 thread instructions a number where aligned rows
+// take 25 and 40, and have 17 and 9 warps an SM to run them: issue slots are 58 and 44 %
+// used and no pipe more than that, so that it is work and latency together).
 #pragma once
 
 #include "numbers.cuh"

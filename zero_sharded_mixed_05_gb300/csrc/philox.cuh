@@ -2,9 +2,10 @@
 // Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3", 2011), a
 // function of a counter and a key that keeps nothing.  Eight numbers take one
 // call's 128 bits, 16 each: half the integer work of 32 bits a number, and p to
-// 1.5e-5.  That work is 12 instructions a number (20 wide products, 20 exclusive ors
-// and 16 instructions for the comparisons a block), which at full rate is 33 us for
-// 67 million numbers in the integer pipe: next to dropout's 40 us of memory traffic.
+// 1.5e-5.  A call is 20 wide products, 20 exclusive ors of three words and 16 instructions
+// for the comparisons: 56, or 7 a number.  Dropout alone measures 10.8 integer
+// instructions a number, its addresses and masks among them, which keep the integer pipe
+// 69 % busy for the 47.6 us of 67 million numbers: 33 us, next to 40 us of memory traffic.
 #pragma once
 
 #include <cuda_runtime.h>

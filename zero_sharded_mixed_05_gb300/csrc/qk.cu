@@ -43,9 +43,10 @@ struct FoldArgs {
 };
 
 // Sums the CTAs' partial gain gradients in index order: 32 columns a CTA, kParts
-// threads a column, each over every kParts-th partial: eight, or 32 for handles with
-// axes, whose sums are done sooner (3,001 tokens of 16 heads of 64: 15.2 us with
-// eight, 13.6 with 32).
+// threads a column, each over every kParts-th partial: 32 for handles with axes, whose
+// sums are done sooner so (3,001 tokens of 16 heads of 64: 15.2 us with eight, 13.6
+// with 32); eight with one position, whose gradients have been summed in that order
+// before and keep their bits.
 template <int kParts>
 __global__ void __launch_bounds__(32 * kParts) qk_fold_kernel(const __grid_constant__ FoldArgs a) {
   __shared__ float s[kParts][33];
