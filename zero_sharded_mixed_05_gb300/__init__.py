@@ -899,8 +899,9 @@ def zero_muon_launch_count(h) -> int:
 
 # What a handle was made for, so that the binding can check tensors against it
 # (head counts, head_dim, rotary_dim / 2, dtype, gain_per_head, axes or 0,
-# whether rows are only rotated, device), the other dtypes, the current stream's getter, and memory for one
-# call's zero_qk_buffers (calls on one handle are ordered).
+# whether rows are only rotated, device), the other dtypes, the current stream's
+# getter, and memory for one call's zero_qk_buffers (calls on one handle are
+# ordered).
 _qk_handles = {}
 _qk_pack = struct.Struct("=27qii").pack_into
 
